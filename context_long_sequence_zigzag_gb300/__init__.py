@@ -13,7 +13,10 @@ Functions carry the C names: ``cp_shard_permute``, ``cp_attn_block_fwd``,
 ``cp_lse_merge``, ``cp_attn_fwd``, ``cp_attn_bwd``, ``cp_workspace_size``,
 ``cp_shard_offsets``, ``cp_rank_block_counts``, ``cp_rank_fwd_key_tiles``, ``cp_device_status``,
 ``cp_check_bounded_wait``, ``cp_status_string``, ``cp_validate``, ``cp_ulysses_a2a``,
-``cp_ulysses_attn_fwd``, ``cp_ulysses_attn_bwd``, ``cp_ring_attn_fwd``, ``cp_lin_attn_fwd``.
+``cp_ulysses_attn_fwd``, ``cp_ulysses_attn_bwd``, ``cp_ring_attn_fwd``, ``cp_lin_attn_fwd``,
+``cp_attn_key_weights``, and for decoding over a 4-bit key/value cache (``Kv4Cache``) ``cp_kv4_append``,
+``cp_kv4_read``, ``cp_kv4_attn``, ``cp_kv4_evict``, ``cp_kv4_block_bytes``, ``cp_kv4_validate``,
+``cp_kv4_workspace_size``.
 """
 
 from __future__ import annotations
@@ -41,6 +44,8 @@ CP_DT_F32, CP_DT_BF16 = 0, 1
 CP_GQA_BLOCKED, CP_GQA_INTERLEAVED = 0, 1
 CP_OP_FWD, CP_OP_BWD, CP_OP_BLOCK_FWD, CP_OP_PERMUTE, CP_OP_BWD_DKDV, CP_OP_BWD_DQ = 0, 1, 2, 3, 4, 5
 CP_OP_ULYSSES_A2A, CP_OP_ULYSSES_FWD, CP_OP_ULYSSES_BWD, CP_OP_LIN_FWD, CP_OP_RING_FWD = 6, 7, 8, 9, 10
+CP_OP_KEY_WEIGHTS = 11
+CP_KV4_PAGE, CP_KV4_GROUP, CP_KV4_MAX_QUERIES = 64, 64, 16
 
 EXPORTED = [
     "cp_status_string", "cp_validate", "cp_workspace_size", "cp_shard_offsets",
@@ -48,7 +53,9 @@ EXPORTED = [
     "cp_attn_fwd", "cp_attn_bwd", "cp_device_status", "cp_check_bounded_wait",
     "cp_attn_fwd_noalloc", "cp_attn_bwd_prep", "cp_attn_bwd_dkdv", "cp_attn_bwd_dq",
     "cp_ulysses_a2a", "cp_ulysses_attn_fwd", "cp_ulysses_attn_bwd", "cp_lin_attn_fwd", "cp_ring_attn_fwd",
-    "cp_set_debug_checks",
+    "cp_set_debug_checks", "cp_attn_key_weights",
+    "cp_kv4_block_bytes", "cp_kv4_validate", "cp_kv4_workspace_size", "cp_kv4_append", "cp_kv4_read", "cp_kv4_attn",
+    "cp_kv4_evict",
 ]
 
 
@@ -70,8 +77,27 @@ class cp_desc_t(ctypes.Structure):
     ]
 
 
+class cp_kv4_t(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int32),
+        ("hq", ctypes.c_int32),
+        ("hkv", ctypes.c_int32),
+        ("d_qk", ctypes.c_int32),
+        ("d_v", ctypes.c_int32),
+        ("gqa", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("num_pages", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("pages", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.c_void_p
 _DP = ctypes.POINTER(cp_desc_t)
+_KP = ctypes.POINTER(cp_kv4_t)
 _sigs = {
     "cp_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "cp_validate": (ctypes.c_int, [_DP]),
@@ -98,6 +124,15 @@ _sigs = {
     "cp_ulysses_attn_bwd": (ctypes.c_int, [_DP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "cp_ring_attn_fwd": (ctypes.c_int, [_DP, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
     "cp_set_debug_checks": (ctypes.c_int, [ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)]),
+    "cp_attn_key_weights": (ctypes.c_int, [_DP, ctypes.c_int64, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "cp_kv4_block_bytes": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
+    "cp_kv4_validate": (ctypes.c_int, [_KP]),
+    "cp_kv4_workspace_size": (ctypes.c_int, [_KP, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
+    "cp_kv4_append": (ctypes.c_int, [_KP, _P, _P, _P, ctypes.c_int64, _P, _P, _P, ctypes.c_int64, _P]),
+    "cp_kv4_read": (ctypes.c_int, [_KP, _P, _P, ctypes.c_int64, _P, _P, _P]),
+    "cp_kv4_attn": (ctypes.c_int, [_KP, ctypes.c_int32, _P, _P, _P, ctypes.c_int32, _P, ctypes.c_int32, _P,
+                                   ctypes.c_size_t, _P]),
+    "cp_kv4_evict": (ctypes.c_int, [_KP, _P, ctypes.c_int32, ctypes.c_int32, _KP, _P, _P, _P]),
 }
 for _name, (_res, _args) in _sigs.items():
     _f = getattr(_lib, _name)
@@ -411,6 +446,208 @@ def cp_attn_fwd_noalloc(prob: Problem, q, k, v, o, lse, stream=None):
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
+def _launch(t: torch.Tensor, stream, temps, name: str, *args) -> None:
+    """Calls a library function with the stream appended, on t's device.
+    ``temps`` (buffers allocated here) are kept until that stream is done."""
+    dev = t.device
+    current = torch.cuda.current_stream(dev)
+    if stream is not None:
+        handle = _stream(stream)
+        if handle != current.cuda_stream:
+            on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=dev)
+            for x in temps:
+                x.record_stream(on)
+    else:
+        handle = current.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        status = getattr(_lib, name)(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(_lib, name)(*args, handle)
+    if status != CP_OK:
+        raise CpError(status, name)
+
+
+def _need(t, name: str, dtype, shape, device=None) -> int:
+    """Data pointer of a contiguous CUDA tensor of this type and shape (None
+    in the shape: any size); ValueError otherwise."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name}: a tensor on {device or 'a CUDA device'} is needed")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} is needed, got {t.dtype}")
+    if t.shape != shape and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        raise ValueError(f"{name}: shape {tuple(shape)} is needed, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors must be contiguous")
+    return t.data_ptr()
+
+
+def cp_attn_key_weights(prob: Problem, q, k, lse, last: Optional[int] = None, w=None, ws=None, stream=None):
+    """Accumulated attention weight of every key, float32 [hkv, T] in sharded
+    order: the attention probabilities summed over the query heads of the
+    key's head and over the queries, or over the last ``last`` of every
+    sequence.  lse: the forward's."""
+    d = prob.desc
+    T, dev = d.total_tokens, q.device
+    if last is not None and last < 1:
+        raise ValueError("last: a positive number of queries, or None for all")
+    pq = _need(q, "q", prob.torch_dtype, (T, d.hq, d.d_qk))
+    pk = _need(k, "k", prob.torch_dtype, (T, d.hkv, d.d_qk), dev)
+    pl = _need(lse, "lse", torch.float32, (d.hq, T), dev)
+    temps = []
+    if w is None:
+        w = torch.empty(d.hkv, T, dtype=torch.float32, device=dev)
+        temps.append(w)
+    pw = _need(w, "w", torch.float32, (d.hkv, T), dev)
+    if ws is None:
+        ws = workspace(prob, CP_OP_KEY_WEIGHTS, dev)
+        temps.append(ws)
+    _launch(q, stream, temps, "cp_attn_key_weights", prob.ptr, last or 0, pq, pk, pl, pw, ws.data_ptr(), ws.numel())
+    return w
+
+
+def cp_kv4_block_bytes(d_qk: int, d_v: int) -> int:
+    """Bytes of one page (64 tokens) of one key/value head."""
+    n = ctypes.c_size_t(0)
+    _check(_lib.cp_kv4_block_bytes(d_qk, d_v, ctypes.byref(n)), "cp_kv4_block_bytes")
+    return int(n.value)
+
+
+class Kv4Cache:
+    """A paged key/value cache in 4 bits, or the part of it that a call deals
+    with: the pool and the page table of the sequences in the batch.
+
+    pages      : uint8 [num_pages, hkv, cp_kv4_block_bytes(d_qk, d_v)]
+    page_table : int32 [num_seqs, max_pages], a page of 64 tokens an entry
+    weights    : float32 [num_pages, hkv, 64], the tokens' accumulated attention weights, or None
+    dtype      : of keys, values, queries and outputs (float32 or bfloat16)
+
+    Holds the tensors; lengths stay with the caller.
+    """
+
+    def __init__(self, pages: torch.Tensor, page_table: torch.Tensor, hq: int, hkv: int, d_qk: int, d_v: int,
+                 weights: Optional[torch.Tensor] = None, scale: Optional[float] = None, gqa: str = "blocked",
+                 dtype=torch.bfloat16):
+        block = cp_kv4_block_bytes(d_qk, d_v)
+        p = _need(pages, "pages", torch.uint8, (None, hkv, block))
+        t = _need(page_table, "page_table", torch.int32, (None, None), pages.device)
+        w = None
+        if weights is not None:
+            w = _need(weights, "weights", torch.float32, (pages.shape[0], hkv, CP_KV4_PAGE), pages.device)
+        self.pages, self.page_table, self.weights = pages, page_table, weights
+        self.torch_dtype, self.device = dtype, pages.device
+        self.desc = cp_kv4_t(
+            num_seqs=page_table.shape[0], hq=hq, hkv=hkv, d_qk=d_qk, d_v=d_v,
+            gqa={"blocked": CP_GQA_BLOCKED, "interleaved": CP_GQA_INTERLEAVED}[gqa],
+            dtype={torch.float32: CP_DT_F32, torch.bfloat16: CP_DT_BF16}[dtype],
+            scale=float(scale if scale is not None else 1.0 / math.sqrt(d_qk)),
+            num_pages=pages.shape[0], max_pages=page_table.shape[1], pages=p, weights=w, page_table=t)
+        self.ptr = ctypes.byref(self.desc)
+        self._ws_bytes = {}
+        _check(_lib.cp_kv4_validate(self.ptr), "cp_kv4_validate")
+
+    def workspace_bytes(self, n_q: int, accumulate: bool) -> int:
+        key = (n_q, accumulate)
+        if key not in self._ws_bytes:
+            self._ws_bytes[key] = cp_kv4_workspace_size(self, n_q, accumulate)
+        return self._ws_bytes[key]
+
+
+def cp_kv4_validate(cache: Kv4Cache) -> int:
+    return _lib.cp_kv4_validate(cache.ptr)
+
+
+def cp_kv4_workspace_size(cache: Kv4Cache, n_q: int = 1, accumulate: bool = False) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.cp_kv4_workspace_size(cache.ptr, n_q, int(bool(accumulate)), ctypes.byref(n)), "cp_kv4_workspace_size")
+    return int(n.value)
+
+
+def cp_kv4_append(cache: Kv4Cache, k, v, cu, start, w=None, rows=None, stream=None) -> None:
+    """Quantises tokens into the cache: token t, cu[b] <= t < cu[b + 1], becomes
+    slot start[b] + t - cu[b] of sequence b, from row rows[t] (or t) of k
+    [n, hkv, d_qk], v [n, hkv, d_v] and w [hkv, n] (their first weights; None: 0).
+    cu int32 [B + 1], start int32 [B], rows int32 [tokens], on the device."""
+    d, dev = cache.desc, cache.device
+    pk = _need(k, "k", cache.torch_dtype, (None, d.hkv, d.d_qk), dev)
+    n = k.shape[0]
+    pv = _need(v, "v", cache.torch_dtype, (n, d.hkv, d.d_v), dev)
+    pw = None if w is None else _need(w, "w", torch.float32, (d.hkv, n), dev)
+    pr = None if rows is None else _need(rows, "rows", torch.int32, (None,), dev)
+    tokens = n if rows is None else rows.shape[0]
+    _launch(k, stream, (), "cp_kv4_append", cache.ptr, pk, pv, pw, n, pr,
+            _need(cu, "cu", torch.int32, (d.num_seqs + 1,), dev), _need(start, "start", torch.int32, (d.num_seqs,), dev),
+            tokens)
+
+
+def cp_kv4_read(cache: Kv4Cache, cu, start, tokens: int, k=None, v=None, stream=None):
+    """Slots start[b], start[b] + 1, ... of every sequence b as rows cu[b] .. cu[b + 1] - 1 of
+    k [tokens, hkv, d_qk] and v [tokens, hkv, d_v]."""
+    d, dev = cache.desc, cache.device
+    temps = []
+    if k is None:
+        k = torch.empty(tokens, d.hkv, d.d_qk, dtype=cache.torch_dtype, device=dev)
+        temps.append(k)
+    if v is None:
+        v = torch.empty(tokens, d.hkv, d.d_v, dtype=cache.torch_dtype, device=dev)
+        temps.append(v)
+    _launch(cache.pages, stream, temps, "cp_kv4_read", cache.ptr,
+            _need(cu, "cu", torch.int32, (d.num_seqs + 1,), dev), _need(start, "start", torch.int32, (d.num_seqs,), dev),
+            tokens, _need(k, "k", cache.torch_dtype, (tokens, d.hkv, d.d_qk), dev),
+            _need(v, "v", cache.torch_dtype, (tokens, d.hkv, d.d_v), dev))
+    return k, v
+
+
+def cp_kv4_attn(cache: Kv4Cache, q, lengths, accumulate: bool = False, part: bool = False, o=None, lse=None, ws=None,
+                stream=None):
+    """Attention of q [B, n_q, hq, d_qk], the newest n_q tokens of every sequence, over the cache
+    (lengths int32 [B]: tokens held, the new ones among them).  Returns o [B, n_q, hq, d_v] and
+    lse [hq, B * n_q].  accumulate: the attention probabilities are added to cache.weights.
+    part: o in float32, for cp_lse_merge."""
+    d, dev = cache.desc, cache.device
+    pq = _need(q, "q", cache.torch_dtype, (d.num_seqs, None, d.hq, d.d_qk), dev)
+    n_q = q.shape[1]
+    o_dtype = torch.float32 if part else cache.torch_dtype
+    temps = []
+    if o is None:
+        o = torch.empty(d.num_seqs, n_q, d.hq, d.d_v, dtype=o_dtype, device=dev)
+        temps.append(o)
+    if lse is None:
+        lse = torch.empty(d.hq, d.num_seqs * n_q, dtype=torch.float32, device=dev)
+        temps.append(lse)
+    accumulate = bool(accumulate)
+    if ws is None:
+        ws = torch.empty(max(cache.workspace_bytes(n_q, accumulate), 1), dtype=torch.uint8, device=dev)
+        temps.append(ws)
+    _launch(q, stream, temps, "cp_kv4_attn", cache.ptr, n_q, pq,
+            _need(lengths, "lengths", torch.int32, (d.num_seqs,), dev),
+            _need(o, "o", o_dtype, (d.num_seqs, n_q, d.hq, d.d_v), dev), int(part),
+            _need(lse, "lse", torch.float32, (d.hq, d.num_seqs * n_q), dev), int(accumulate), ws.data_ptr(), ws.numel())
+    return o, lse
+
+
+def cp_kv4_evict(cache: Kv4Cache, lengths, budget: int, recent: int, to: Kv4Cache, new_lengths=None, kept=None,
+                 stream=None):
+    """Keeps, for every sequence and head, the last ``recent`` slots and the budget - recent others of
+    largest weight, copied in slot order into the pages of ``to`` (no page may be read and written).
+    Returns new_lengths int32 [B] and kept int32 [B, hkv, budget], the slots kept (-1 behind the last)."""
+    d, dev = cache.desc, cache.device
+    temps = []
+    if new_lengths is None:
+        new_lengths = torch.empty(d.num_seqs, dtype=torch.int32, device=dev)
+        temps.append(new_lengths)
+    if kept is None:
+        kept = torch.empty(d.num_seqs, d.hkv, max(budget, 0), dtype=torch.int32, device=dev)
+        temps.append(kept)
+    if to.device != dev:
+        raise ValueError(f"to: a cache on {dev} is needed")
+    _launch(cache.pages, stream, temps, "cp_kv4_evict", cache.ptr,
+            _need(lengths, "lengths", torch.int32, (d.num_seqs,), dev), budget, recent, to.ptr,
+            _need(new_lengths, "new_lengths", torch.int32, (d.num_seqs,), dev),
+            _need(kept, "kept", torch.int32, (d.num_seqs, d.hkv, max(budget, 0)), dev))
+    return new_lengths, kept
+
+
 def cp_set_debug_checks(on: bool) -> bool:
     """Turns the plan checks on or off for later calls; returns the former setting."""
     prev = ctypes.c_int32(0)
@@ -433,4 +670,4 @@ def cp_check_bounded_wait(timeout_ns: int = 20_000_000, stream=None) -> int:
     return int(code.value)
 
 
-__all__ = ["Problem", "CpError", "workspace", "LIB_PATH", "EXPORTED"] + EXPORTED
+__all__ = ["Problem", "Kv4Cache", "CpError", "workspace", "LIB_PATH", "EXPORTED"] + EXPORTED

@@ -32,6 +32,10 @@ SOURCES = [
     "attn_bwd_sm103.cu",
     "linear_attn.cu",
     "linear_attn_tc.cu",
+    "key_weights_sm103.cu",
+    "kv4_host.cu",
+    "kv4_cache.cu",
+    "kv4_attn.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -328,11 +328,21 @@ Plan build_fwd_plan(const cp_desc_t* d, const ShardMap& m, int q_rank, int kv_ra
   return p;
 }
 
+// Tokens of chunk A before the last `last` positions of its sequence (of
+// length len, first global row seq_row0); last = 0: none, all count.
+int32_t tokens_before_window(const Chunk& A, int64_t seq_row0, int64_t len, int64_t last) {
+  if (last <= 0 || last >= len) return 0;
+  const int64_t first = len - last - (A.grow0 - seq_row0);  // positions left out from A's first token on
+  return int32_t(std::min<int64_t>(A.len, std::max<int64_t>(0, (first + A.stride - 1) / A.stride)));
+}
+
 // Key-major plan for the backward: every key tile with the query runs that
 // see it, visiting ranks r, r+1, ... (the direction dK/dV travel in a ring).
-Plan build_bwd_plan(const cp_desc_t* d, const ShardMap& m, bool pack = false) {
+// last > 0 keeps only the last `last` queries of every sequence.
+Plan build_bwd_plan(const cp_desc_t* d, const ShardMap& m, bool pack = false, int64_t last = 0) {
   Plan p;
   const bool causal = d->causal != 0;
+  const std::vector<int32_t> cu = seqlens_of(d);
   for (const Chunk& B : m.chunks) {
     for (int32_t t0 = 0; t0 < B.len; t0 += kTile) {
       TileDesc t{};
@@ -353,17 +363,19 @@ Plan build_bwd_plan(const cp_desc_t* d, const ShardMap& m, bool pack = false) {
           if (A.len == 0) continue;
           RangeDesc r{};
           const int32_t apos = query_pos0(m, A, B);
+          int32_t skip = tokens_before_window(A, cu[B.seq], int64_t(cu[B.seq + 1]) - cu[B.seq], last);
+          if (skip == A.len) continue;
           if (causal) {
             if (apos + A.len - 1 < kmin) continue;  // every query precedes the keys
-            const int32_t skip = std::max(0, kmin - apos);
+            skip = std::max(skip, kmin - apos);
             r.row0 = int32_t(A.srow0 + skip);
             r.nrows = A.len - skip;
             r.pos0 = apos + skip;
             r.flags = (r.pos0 < kmax) ? kRangeMasked : 0;
           } else {
-            r.row0 = int32_t(A.srow0);
-            r.nrows = A.len;
-            r.pos0 = apos;
+            r.row0 = int32_t(A.srow0 + skip);
+            r.nrows = A.len - skip;
+            r.pos0 = apos + skip;
             r.flags = 0;
           }
           whole[p.ranges.size() - first] = r.flags == 0 && r.nrows == A.len;
@@ -448,14 +460,15 @@ size_t plan_bytes(const Plan& p) {
 // the query runs that see a whole key tile gathered into shared query tiles
 // (the tensor-core dK/dV kernel with 128-row query steps).
 enum PlanKind : int64_t { kPlanQueryMajor = 0, kPlanKeyMajor = 1, kPlanQueryMajorPacked = 2, kPlanKeyMajorPacked = 3 };
+// last: the observation window of a key-major plan (build_bwd_plan).
 std::shared_ptr<const Plan> get_plan(const cp_desc_t* d, const ShardMap& m, PlanKind kind, int q_rank = -1,
-                                     int kv_rank = -1, int ring_step = -1, int64_t slot_rows = 0) {
+                                     int kv_rank = -1, int ring_step = -1, int64_t slot_rows = 0, int64_t last = 0) {
   static std::mutex mu;
   static std::list<std::pair<std::vector<int64_t>, std::shared_ptr<const Plan>>> cache;  // most recent first
   static size_t cached_bytes = 0;
   // a ring of C steps uses C plans; bounded by count and by host bytes
   constexpr size_t kMaxPlans = 80, kMaxBytes = size_t(256) << 20;
-  std::vector<int64_t> key = {kind, q_rank, kv_rank, ring_step, slot_rows, d->total_tokens, d->cp_size, d->layout,
+  std::vector<int64_t> key = {kind, q_rank, kv_rank, ring_step, slot_rows, last, d->total_tokens, d->cp_size, d->layout,
                               d->causal, d->num_seqs};
   if (d->cu_seqlens) key.insert(key.end(), d->cu_seqlens, d->cu_seqlens + d->num_seqs + 1);
   {
@@ -467,7 +480,7 @@ std::shared_ptr<const Plan> get_plan(const cp_desc_t* d, const ShardMap& m, Plan
       }
   }
   const bool key_major = kind == kPlanKeyMajor || kind == kPlanKeyMajorPacked;
-  auto plan = std::make_shared<Plan>(key_major ? build_bwd_plan(d, m, kind == kPlanKeyMajorPacked)
+  auto plan = std::make_shared<Plan>(key_major ? build_bwd_plan(d, m, kind == kPlanKeyMajorPacked, last)
                                                : build_fwd_plan(d, m, q_rank, kv_rank, ring_step, slot_rows,
                                                                 kind == kPlanQueryMajorPacked));
   order_by_work(*plan);
@@ -652,6 +665,9 @@ bool use_tc_fwd(const cp_desc_t* d) {
 bool use_tc_bwd(const cp_desc_t* d) {
   return d->dtype == CP_DT_BF16 && tc_bwd_supported(d->d_qk, d->d_v);
 }
+bool use_tc_key_weights(const cp_desc_t* d) {
+  return d->dtype == CP_DT_BF16 && tc_key_weights_supported(d->d_qk);
+}
 // The whole forward's plan and the dQ kernel's: the tensor-core kernels read
 // gathered key tiles.
 PlanKind fwd_plan_kind(const cp_desc_t* d) { return use_tc_fwd(d) ? kPlanQueryMajorPacked : kPlanQueryMajor; }
@@ -659,6 +675,28 @@ PlanKind dq_plan_kind(const cp_desc_t* d) { return use_tc_bwd(d) ? kPlanQueryMaj
 // The dK/dV kernel's: gathered query tiles where its query steps are 128 rows.
 PlanKind dkdv_plan_kind(const cp_desc_t* d) {
   return use_tc_bwd(d) && d->d_qk == 128 ? kPlanKeyMajorPacked : kPlanKeyMajor;
+}
+
+// The key-weight kernel's: 128-row query steps for both of its head dims.
+PlanKind key_weights_plan_kind(const cp_desc_t* d) { return use_tc_key_weights(d) ? kPlanKeyMajorPacked : kPlanKeyMajor; }
+
+// Bytes that hold the key-major plan of any observation window: a window only
+// takes query runs away or shortens them, runs that are not merged are at
+// most the (key tile, query chunk) pairs, and gathering turns a run into at
+// most a whole-step run and two pieces.
+size_t key_weights_bytes(const cp_desc_t* d, const ShardMap& m) {
+  int64_t tiles = 0, runs = 0;
+  for (const Chunk& B : m.chunks)
+    for (int32_t t0 = 0; t0 < B.len; t0 += kTile) {
+      ++tiles;
+      for (int r = 0; r < m.C; ++r)
+        for (int k = 0; k < m.per; ++k) {
+          const Chunk& A = m.at(r, B.seq, k);
+          runs += A.len > 0 && (d->causal == 0 || query_pos0(m, A, B) + A.len - 1 >= B.pos0 + t0);
+        }
+    }
+  return align256(size_t(tiles) * sizeof(TileDesc)) + align256(size_t(runs) * 2 * sizeof(RangeDesc)) +
+         align256(size_t(runs) * sizeof(PackMask)) + align256(size_t(runs) * 2 * sizeof(PackPiece));
 }
 
 AttnArgs base_args(const cp_desc_t* d) {
@@ -1011,6 +1049,8 @@ cp_status_t cp_workspace_size(const cp_desc_t* d, int32_t op, size_t* bytes) {
     *bytes = plan_bytes(*get_plan(d, m, dkdv_plan_kind(d)));
   } else if (op == CP_OP_BWD_DQ) {
     *bytes = plan_bytes(*get_plan(d, m, dq_plan_kind(d)));
+  } else if (op == CP_OP_KEY_WEIGHTS) {
+    *bytes = key_weights_bytes(d, m);
   } else if (op == CP_OP_RING_FWD) {
     *bytes = ring_layout(d, m).total;
   } else if (op == CP_OP_ULYSSES_FWD || op == CP_OP_ULYSSES_BWD) {
@@ -1504,6 +1544,33 @@ cp_status_t cp_lin_attn_fwd(const cp_desc_t* d, const void* q, const void* k, co
                          reinterpret_cast<float*>(base + L.init), o, cs) == cudaSuccess
              ? CP_OK
              : CP_ERR_CUDA;
+}
+
+cp_status_t cp_attn_key_weights(const cp_desc_t* d, int64_t last, const void* q, const void* k, const float* lse,
+                                float* w, void* ws, size_t ws_bytes, cp_stream_t stream) {
+  CallRange range_("cp_attn_key_weights");
+  cp_status_t st = check_attn_fields(d);
+  if (st != CP_OK) return st;
+  if (last < 0) return CP_ERR_INVALID_ARG;
+  if (d->total_tokens == 0) return CP_OK;
+  const void* ptrs[] = {q, k, lse, w};
+  for (const void* p : ptrs)
+    if (p == nullptr || !aligned16(p)) return CP_ERR_INVALID_ARG;
+  if (last >= d->total_tokens) last = 0;
+  const ShardMap m = build_map(d);
+  const auto pp = get_plan(d, m, key_weights_plan_kind(d), -1, -1, -1, 0, last);
+  const Plan& p = *pp;
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < plan_bytes(p)) return CP_ERR_WORKSPACE;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  AttnArgs a = base_args(d);
+  a.q = q;
+  a.k = k;
+  a.lse_in = lse;
+  a.out = w;
+  st = stage_plan(p, static_cast<char*>(ws), cs, a, d->total_tokens, d->total_tokens);
+  if (st != CP_OK) return st;
+  const cudaError_t e = use_tc_key_weights(d) ? launch_tc_key_weights(a, cs) : launch_simt_key_weights(a, d->dtype, cs);
+  return e == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 
 cp_status_t cp_set_debug_checks(int32_t on, int32_t* previous) {

@@ -166,6 +166,10 @@ cudaError_t launch_tc_fwd(const AttnArgs& a, cudaStream_t st);
 // tensor-core backward: dK/dV over the key-major plan, dQ over the query-major plan
 cudaError_t launch_tc_bwd_dkdv(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_tc_bwd_dq(const AttnArgs& a, cudaStream_t st);
+// accumulated attention weight of every key (out: float w [hkv, T]) over the key-major plan
+cudaError_t launch_simt_key_weights(const AttnArgs& a, int32_t dtype, cudaStream_t st);
+cudaError_t launch_tc_key_weights(const AttnArgs& a, cudaStream_t st);
+bool tc_key_weights_supported(int32_t d_qk);
 bool tc_fwd_supported(int32_t d_qk, int32_t d_v);
 bool tc_bwd_supported(int32_t d_qk, int32_t d_v);
 cudaError_t read_and_clear_device_status(int32_t* code, cudaStream_t st);

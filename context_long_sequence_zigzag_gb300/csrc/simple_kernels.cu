@@ -452,6 +452,50 @@ __global__ void __launch_bounds__(256) simt_bwd_dkdv_kernel(const AttnArgs a) {
   }
 }
 
+// w for one key row per warp (key-major plan), summed over the query heads of
+// the key's GQA group and the plan's queries.
+template <typename E>
+__global__ void __launch_bounds__(256) simt_key_weights_kernel(const AttnArgs a) {
+  const int tile_idx = blockIdx.x / a.hkv;
+  const int kvh = blockIdx.x - tile_idx * a.hkv;
+  const int G = a.hq / a.hkv;
+  if (a.debug && !debug_plan_ok(a, tile_idx, kvh, kvh, true, a.err)) return;
+  const TileDesc t = a.tiles[tile_idx];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const E* q = static_cast<const E*>(a.q);
+  const E* k = static_cast<const E*>(a.k);
+  for (int r = warp; r < t.nrows; r += (blockDim.x >> 5)) {
+    const int64_t krow = int64_t(t.row0) + r;
+    const int kpos = t.pos0 + r;
+    float kv_[kMaxPerLane];
+#pragma unroll
+    for (int e = 0; e < kMaxPerLane; ++e) {
+      const int c = lane + 32 * e;
+      kv_[e] = c < a.d_qk ? ldf(k + (krow * a.hkv + kvh) * a.d_qk + c) : 0.f;
+    }
+    float w = 0.f;
+    for (int g = 0; g < G; ++g) {
+      const int h = a.gqa_interleaved ? g * a.hkv + kvh : kvh * G + g;
+      for (int ri = 0; ri < t.range_count; ++ri) {
+        const RangeDesc R = a.ranges[t.range_begin + ri];
+        float part = 0.f;  // a run's sum on its own: the roundings of a long sum stay small
+        for (int i = a.causal ? max(0, kpos - R.pos0) : 0; i < R.nrows; ++i) {
+          const int64_t qrow = int64_t(R.row0) + i;
+          float s = 0.f;
+#pragma unroll
+          for (int e = 0; e < kMaxPerLane; ++e) {
+            const int c = lane + 32 * e;
+            s += c < a.d_qk ? ldf(q + (qrow * a.hq + h) * a.d_qk + c) * kv_[e] : 0.f;
+          }
+          part += expf(warp_sum(s) * a.scale - a.lse_in[int64_t(h) * a.T + qrow]);
+        }
+        w += part;
+      }
+    }
+    if (lane == 0) static_cast<float*>(a.out)[int64_t(kvh) * a.T + krow] = w;
+  }
+}
+
 int64_t grid_for(int64_t work_items, int per_block) {
   int64_t g = (work_items + per_block - 1) / per_block;
   const int64_t cap = int64_t(sm_count()) * 16;
@@ -568,6 +612,18 @@ cudaError_t launch_simt_bwd_dkdv(const AttnArgs& args, int32_t dtype, cudaStream
     simt_bwd_dkdv_kernel<float><<<unsigned(grid), 256, 0, st>>>(a);
   else
     simt_bwd_dkdv_kernel<__nv_bfloat16><<<unsigned(grid), 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_simt_key_weights(const AttnArgs& args, int32_t dtype, cudaStream_t st) {
+  AttnArgs a = args;
+  a.err = device_error_word();
+  const int64_t grid = int64_t(a.num_tiles) * a.hkv;
+  if (grid == 0) return cudaSuccess;
+  if (dtype == CP_DT_F32)
+    simt_key_weights_kernel<float><<<unsigned(grid), 256, 0, st>>>(a);
+  else
+    simt_key_weights_kernel<__nv_bfloat16><<<unsigned(grid), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -98,7 +98,8 @@ typedef enum { CP_DT_F32 = 0, CP_DT_BF16 = 1 } cp_dtype_t;
 typedef enum { CP_GQA_BLOCKED = 0, CP_GQA_INTERLEAVED = 1 } cp_gqa_t;
 typedef enum {
   CP_OP_FWD = 0, CP_OP_BWD = 1, CP_OP_BLOCK_FWD = 2, CP_OP_PERMUTE = 3, CP_OP_BWD_DKDV = 4, CP_OP_BWD_DQ = 5,
-  CP_OP_ULYSSES_A2A = 6, CP_OP_ULYSSES_FWD = 7, CP_OP_ULYSSES_BWD = 8, CP_OP_LIN_FWD = 9, CP_OP_RING_FWD = 10
+  CP_OP_ULYSSES_A2A = 6, CP_OP_ULYSSES_FWD = 7, CP_OP_ULYSSES_BWD = 8, CP_OP_LIN_FWD = 9, CP_OP_RING_FWD = 10,
+  CP_OP_KEY_WEIGHTS = 11
 } cp_op_t;
 
 /* Problem descriptor.  Read on the host during each call; not retained. */
@@ -334,6 +335,151 @@ cp_status_t cp_ulysses_attn_bwd(const cp_desc_t* desc, const void* q, const void
 cp_status_t cp_lin_attn_fwd(const cp_desc_t* desc, const void* q, const void* k, const void* v,
                             const float* g, void* o,
                             void* workspace, size_t workspace_bytes, cp_stream_t stream);
+
+/* Accumulated attention weight of every key of a prompt, the score by which
+ * cp_kv4_evict ranks cached tokens: for kv head c and key j
+ *   w[c, j] = sum over the heads h of c's GQA group and the queries i that
+ *             see j of exp(scale * q_i[h].k_j[c] - lse[h, i]),
+ * i.e. column sums of the attention probabilities, recomputed from the
+ * forward's lse as the backward does ("Ulysses与Ring-Attention详解" §4.3).
+ *   last      : > 0: only the last `last` queries of every sequence count
+ *               (an observation window at the prompt's end); 0: all of them
+ *   q, k      : device, sharded order, as cp_attn_fwd
+ *   lse       : device float32 [hq, T], output of cp_attn_fwd (read at the
+ *               counted queries only); +inf leaves a query out
+ *   w         : device float32 [hkv, T], sharded order; keys that no counted
+ *               query sees get 0
+ *   workspace : cp_workspace_size(desc, CP_OP_KEY_WEIGHTS) bytes, for any `last`
+ * BF16 with d_qk in {128, 192} runs on the tensor cores; other head dims and
+ * FP32 run on the CUDA cores.  d_v is not used. */
+cp_status_t cp_attn_key_weights(const cp_desc_t* desc, int64_t last, const void* q, const void* k, const float* lse,
+                                float* w, void* workspace, size_t workspace_bytes, cp_stream_t stream);
+
+/* ------------------------------------------------- key/value cache in 4 bits
+ * Decoding against the keys and values of a long prompt: a paged cache of
+ * 4-bit codes, the attention that reads it, and eviction by accumulated
+ * attention weight.  The source pages stop at training; these calls take up
+ * where their long-context forward ends, in its conventions: head layouts and
+ * GQA maps as above, o and lse as the forward's.  With o in fp32 a call's
+ * (o, lse) is a partial result that cp_lse_merge joins with others (a cache
+ * split over context-parallel ranks).
+ *
+ * Values.  A group is 64 channels of one token's head.  It is held as a low
+ * (bf16, the group's minimum, rounded down), a scale (bf16, of (max - low) /
+ * 15) and 64 codes n = the integer nearest to (x - low) / scale, in 0 .. 15
+ * (halves to even; scale 0: n = 0).  It reads back as scale * n + low.  A
+ * group that holds a NaN or an infinity reads back as NaN.
+ *
+ * Pages.  A page holds CP_KV4_PAGE = 64 tokens.  `pages` is
+ * [num_pages][hkv][cp_kv4_block_bytes]; a block is two sub-blocks of 32
+ * tokens, each
+ *   K codes [32][d_qk / 2 bytes]   V codes [32][d_v / 2 bytes]
+ *   K parameters bf16 [32][2][d_qk / 64] (a token's scales, then its lows)
+ *   V scales bf16 [32][d_v / 64]   V lows bf16 [d_v / 64][32]
+ * Channels 8w .. 8w + 7 share a little-endian 32-bit word, channel 8w + i in
+ * bits 4i .. 4i + 3; word w of a K row lies at word (w % 4) * (d / 32) + w / 4,
+ * of a V row at (w % 8) * (d / 64) + w / 8.
+ * Token (slot) j of sequence b is in page page_table[b][j / 64], row j % 64.
+ * Several sequences may share pages (a common prefix) as long as no call
+ * writes them.  Table entries past a sequence's last page are not read.
+ *
+ * Lengths, offsets and tables are device arrays, read by the kernels: a
+ * captured graph can be replayed with new ones.  A length outside 0 ..
+ * max_pages * 64 is clamped; a page outside 0 .. num_pages - 1, or a row
+ * outside its tensor, is skipped (attention: its keys count as absent).  Both
+ * put 0x300 | site into the device error word (cp_device_status). */
+#define CP_KV4_PAGE 64
+#define CP_KV4_GROUP 64
+#define CP_KV4_MAX_QUERIES 16
+#define CP_KV4_MAX_SEQS 65536
+
+/* A cache, or the part of it that a call deals with.  Read on the host during
+ * each call; not retained. */
+typedef struct {
+  int32_t num_seqs;          /* B >= 0 sequences (rows of page_table), at most CP_KV4_MAX_SEQS */
+  int32_t hq, hkv;           /* query heads, key/value heads (hq % hkv == 0)     */
+  int32_t d_qk, d_v;         /* d_qk in {64, 128, 192}, d_v in {64, 128}         */
+  int32_t gqa;               /* cp_gqa_t                                         */
+  int32_t dtype;             /* cp_dtype_t of k, v, q and o outside the cache    */
+  float scale;               /* softmax scale applied to q.k (> 0, finite)       */
+  int32_t num_pages;         /* pages of the pool                                */
+  int32_t max_pages;         /* columns of page_table                            */
+  void* pages;               /* device, 16-byte aligned                          */
+  float* weights;            /* device [num_pages][hkv][64], the tokens' accumulated
+                                attention weights, or NULL                       */
+  const int32_t* page_table; /* device [B][max_pages]                            */
+} cp_kv4_t;
+
+/* Bytes of one page of one kv head.  Host only. */
+cp_status_t cp_kv4_block_bytes(int32_t d_qk, int32_t d_v, size_t* bytes);
+
+/* Check a cache descriptor on the host (no GPU work). */
+cp_status_t cp_kv4_validate(const cp_kv4_t* cache);
+
+/* Workspace bytes of cp_kv4_attn with n_q queries a sequence, without or with
+ * weights.  Grows with num_seqs * max_pages in the second case.  Host only.
+ * The rules of cp_workspace_size apply. */
+cp_status_t cp_kv4_workspace_size(const cp_kv4_t* cache, int32_t n_q, int32_t accumulate, size_t* bytes);
+
+/* Quantise tokens into the cache: token t, cu[b] <= t < cu[b+1], becomes slot
+ * start[b] + t - cu[b] of sequence b.  The caller keeps the lengths.
+ *   k, v   : device [src_rows, hkv, d_qk] and [src_rows, hkv, d_v] (cache.dtype)
+ *   w      : device float32 [hkv, src_rows], the tokens' first weights
+ *            (cp_attn_key_weights), or NULL: 0.  Not read without cache.weights
+ *   rows   : device int32 [tokens], the row of k, v and w that token t is in
+ *            (e.g. its sharded row), or NULL: row t
+ *   cu     : device int32 [B + 1], cu[0] = 0, non-decreasing; tokens from
+ *            cu[B] on (padding) are left out
+ *   start  : device int32 [B]
+ *   tokens : tokens given, >= cu[B]
+ * Two tokens must not go to the same slot. */
+cp_status_t cp_kv4_append(const cp_kv4_t* cache, const void* k, const void* v, const float* w, int64_t src_rows,
+                          const int32_t* rows, const int32_t* cu, const int32_t* start, int64_t tokens,
+                          cp_stream_t stream);
+
+/* Read slots back: rows cu[b] .. cu[b+1] - 1 of k and v get slots start[b],
+ * start[b] + 1, ... of sequence b, rounded to cache.dtype.  Rows from cu[B]
+ * on, and rows whose slot is outside the cache, are left as they were.
+ *   k, v : device [tokens, hkv, d_qk] and [tokens, hkv, d_v] */
+cp_status_t cp_kv4_read(const cp_kv4_t* cache, const int32_t* cu, const int32_t* start, int64_t tokens, void* k,
+                        void* v, cp_stream_t stream);
+
+/* Attention of the newest n_q tokens of every sequence over its cache (their
+ * own keys and values appended before).  Query t of sequence b sees slots j <
+ * lengths[b] - (n_q - 1 - t); one that sees none gets o = 0, lse = -inf.
+ *   q          : device [B, n_q, hq, d_qk] (cache.dtype), 1 <= n_q <=
+ *                CP_KV4_MAX_QUERIES
+ *   lengths    : device int32 [B], tokens held, the new ones among them
+ *   o          : device [B, n_q, hq, d_v], cache.dtype, or float32 with
+ *                o_f32 = 1
+ *   lse        : device float32 [hq, B * n_q]
+ *   accumulate : 1: every visible slot's attention probabilities, summed over
+ *                the query heads of its kv head and the n_q queries, are added
+ *                to cache.weights; 0: not
+ *   workspace  : cp_kv4_workspace_size bytes
+ * Queries, keys and probabilities meet on the tensor cores with FP32
+ * accumulation: exactly unpacked codes, the softmax and the scales in FP32;
+ * for BF16 caches the scaled probabilities are rounded to BF16 as operands,
+ * for FP32 ones queries and probabilities are split into three BF16 terms. */
+cp_status_t cp_kv4_attn(const cp_kv4_t* cache, int32_t n_q, const void* q, const int32_t* lengths, void* o,
+                        int32_t o_f32, float* lse, int32_t accumulate, void* workspace, size_t workspace_bytes,
+                        cp_stream_t stream);
+
+/* Eviction: for every sequence and kv head, keeps the last `recent` slots and,
+ * of the others, the budget - recent of largest weight (equal weights: the
+ * lowest slots first; NaN ranks above every number), and copies them in slot
+ * order, codes and weights as they are, to slots 0, 1, ... of the same
+ * sequence in `to`.  A sequence of at most `budget` tokens is copied whole.
+ *   lengths     : device int32 [B], tokens held
+ *   budget      : >= 1, at most to->max_pages * 64;  0 <= recent <= budget
+ *   to          : the same shape as cache (num_seqs, hkv, d_qk, d_v), weights
+ *                 not NULL, pages of its own (another table of the same pool,
+ *                 or another pool): no page may be read and written
+ *   new_lengths : device int32 [B], min(length, budget); not `lengths` itself
+ *   kept        : device int32 [B, hkv, budget], the slots kept, -1 behind the
+ *                 last */
+cp_status_t cp_kv4_evict(const cp_kv4_t* cache, const int32_t* lengths, int32_t budget, int32_t recent,
+                         const cp_kv4_t* to, int32_t* new_lengths, int32_t* kept, cp_stream_t stream);
 
 /* Forward without a workspace, for callers that cannot allocate device
  * memory.  The source pages have no counterpart to this entry point.

@@ -31,6 +31,8 @@ Contents and the passage each follows:
   "Ulysses与Ring-Attention详解" §4.2 (lse_new = log(exp(lse_prev) +
   exp(lse_cur))); "LLM context parallel production guide" "核心原理" (partials
   are merged through the softmax statistics, not averaged).
+* ``kv4``        — the 4-bit key/value cache, attention over it, eviction and a
+  prompt's key weights.
 
 Parity pins for every function live in ``tests/test_oracle_*.py``.
 """
@@ -66,4 +68,17 @@ from .linear_attention import (  # noqa: F401
     linear_attn_recurrent,
     linear_attn_cp,
     local_state,
+)
+from .kv4 import (  # noqa: F401
+    attn_key_weights,
+    bf16_bits,
+    bf16_values,
+    kv4_attention,
+    kv4_block_bytes,
+    kv4_codes,
+    kv4_keep,
+    kv4_pack,
+    kv4_quantise,
+    kv4_unpack,
+    kv4_values,
 )
