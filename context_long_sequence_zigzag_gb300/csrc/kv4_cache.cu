@@ -120,7 +120,8 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Cache c, 
     }
     __nv_bfloat16 low = __float2bfloat16_rd(lo);
     const float lowf = __bfloat162float(low);
-    __nv_bfloat16 scale = __float2bfloat16_rn(__fdiv_rn(0.5f * hi - 0.5f * lowf, 7.5f));
+    // (max - low) / 15; halved first, so that no finite range overflows
+    __nv_bfloat16 scale = __float2bfloat16_rn((0.5f * hi - 0.5f * lowf) * (1.f / 7.5f));
     const float s = __bfloat162float(scale);
     uint32_t codes = 0;
     if (bad != 0.f || isinf(lowf)) {  // bad is 0 or NaN
