@@ -97,6 +97,9 @@ cudaError_t launch_kv4_evict(const Kv4Cache& c, int dqk, int dv, const int32_t* 
                              int32_t recent, const Kv4Cache& to, int32_t* new_lengths, int32_t* kept,
                              cudaStream_t st);
 size_t kv4_attn_workspace(const cp_kv4_t* c, int32_t n_q, int32_t accumulate);
-cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, int dqk, int dv, int dtype, cudaStream_t st);
+// units of work of the longest sequences that the table can hold
+int64_t kv4_attn_units(const cp_kv4_t* c, int32_t n_q);
+// fills in rows and row_tiles
+cudaError_t launch_kv4_attn(Kv4AttnArgs a, int dqk, int dv, int dtype, cudaStream_t st);
 
 }  // namespace cpattn

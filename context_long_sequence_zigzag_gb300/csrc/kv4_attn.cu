@@ -2,144 +2,826 @@
 //
 // Row (b, t, h) sees slots j < lengths[b] - (n_q - 1 - t):
 //   S_j = scale q.K_j,  lse = log sum_j exp(S_j),  o = sum_j exp(S_j - lse) V_j.
-// One CTA per row; its warps take the slots in turn, each with a running
-// maximum and sum, and are joined at the end.
+// The cache is read once (144 bytes a token's head of 128 channels) and every
+// byte of it meets G * n_q rows, so the kernel is bound by HBM as long as
+// unpacking keeps up: at 6.7 TB/s an SM gets about 23 bytes a cycle, 46 codes.
+//
+// Warp-level MMAs, not tcgen05: with 1 to 16 rows a tcgen05 tile would be
+// nearly empty, and its operands would have to be unpacked into shared or
+// tensor memory first; here a lane's packed words are unpacked in registers
+// straight into the fragments of mma.m16n8k16 (keys or channels on the 16
+// side, rows on the 8 side), which the format's word order was chosen for.
+//
+// * A code n becomes bf16(16 + n) with one shift and one LOP3 per pair: 16 is
+//   1.0000000b * 2^4, so a code in mantissa bits 3-6 adds n exactly.  The 16s
+//   are taken out again in fp32: of S by starting the accumulators at -16
+//   sum(q), of O by one MMA a group with a constant -16.
+// * Scales and lows act in fp32: on S per (key, group); on P per (token, group)
+//   before P is rounded to the bf16 operand.
+// * S^T comes out with keys as rows and goes back in as P^T with tokens as
+//   the contracted index: movmatrix transposes the 8 x 8 quarters.
+// * The softmax keeps a reference per row instead of a running maximum: P =
+//   2^(S - ref), and only when an element exceeds the reference by more than
+//   2^10 does the warp reduce a new maximum and rescale.
+// * fp32 caches split q and P s into three bf16 terms (24 bits), more MMAs on
+//   the same unpacked codes.
+//
+// Work: every (sequence, kv head, row tile) is a run of sub-blocks of 32
+// tokens; all runs laid end to end are cut evenly over the CTAs (one an SM),
+// whatever the lengths, on the device: a graph replays with other lengths.
+// Inside its share a CTA's warps take sub-blocks in turn, each through its own
+// ring of bulk copies, so nothing but the end of a run is synchronised.  Runs
+// that lie in one CTA are finished there; the others leave partials, which a
+// second kernel joins.  Weights need the final lse, so the raw scores wait in
+// the workspace (they stay in L2) and the second kernel adds them up.
+#include <algorithm>
+
 #include "kv4.cuh"
 #include "sm103_ptx.cuh"
 
 namespace cpattn {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNoRef = -1e30f;   // a row that has seen nothing
+constexpr float kSlack = 10.f;     // how far (log2) an element may exceed the reference
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
-__device__ __forceinline__ float ldf(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float ldf(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+template <int DQK_, int DV_, int NT_, int TERMS_>
+struct Cfg {
+  static constexpr int DQK = DQK_, DV = DV_, NT = NT_, TERMS = TERMS_;
+  static constexpr int GK = DQK / 64, GV = DV / 64;
+  static constexpr int KW = DQK / 32;  // words of a K row a lane unpacks
+  static constexpr int COLS = 8 * NT;
+  static constexpr int NW = NT == 1 && TERMS == 1 && DQK < 192 ? 16 : 8;
+  static constexpr int THREADS = 32 * NW;
+  static constexpr uint32_t kFragBytes = DQK / 16 * TERMS * NT * 32 * 8;
+};
 
-__device__ __forceinline__ float warp_sum(float x) {
+// The shares: sub-blocks ("units") of all runs end to end, cut over n CTAs.  n
+// is at most the number of units, so that no share is empty.
+__host__ __device__ __forceinline__ int64_t share_begin(int64_t units, int n, int c) { return int64_t(c) * units / n; }
+__device__ __forceinline__ int share_of(int64_t units, int n, int64_t u) { return int(((u + 1) * n - 1) / units); }
+
+// Partial result of a run in a CTA's share: [m][l] of COLS rows, then o.
+__host__ __device__ constexpr int part_floats(int cols, int dv) { return 2 * cols + cols * dv; }
+
+struct Grid {
+  int ctas;          // shares
+  int rows_per_tile;  // rows of a row tile (at most COLS)
+  int stages;
+  uint32_t off_base, off_frag, off_sum, off_stat, off_merge, off_ring;
+  float* part;   // [ctas][2][part_floats]
+  float* score;  // [units][rows_per_tile][32], log2 units
+};
+
+// First unit of every sequence (base[b], base[num_seqs] = all): the CTA's
+// threads fill it.  per: runs a sequence has (hkv * row tiles).
+template <int THREADS>
+__device__ void scan_lengths(const Kv4AttnArgs& a, int per, int32_t* base, int32_t* scratch) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int carry = 0;
+  for (int b0 = 0; b0 < a.c.num_seqs; b0 += THREADS) {
+    const int b = b0 + tid;
+    int x = b < a.c.num_seqs ? (kv4_length(a.c, a.lengths, b) + kKv4Sub - 1) / kKv4Sub * per : 0;
+    const int own = x;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-
-template <typename E>
-__global__ void __launch_bounds__(kWarps * 32) kv4_attn_kernel(const Kv4AttnArgs a, const Kv4Format f) {
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][128];
-  const Kv4Cache& c = a.c;
-  const int G = c.hq / c.hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = blockIdx.x;  // (b, t, h)
-  const int h = int(row % c.hq);
-  const int64_t bt = row / c.hq;
-  const int t = int(bt % a.n_q), b = int(bt / a.n_q);
-  const int kvh = c.inter ? h % c.hkv : h / G;
-  const int n = kv4_length(c, a.lengths, b) - (a.n_q - 1 - t);
-  const E* q = static_cast<const E*>(a.q) + row * f.dqk;
-  // lane: channels 8w .. 8w + 7 of word w = lane, lane < d / 8
-  float qv[8] = {}, o[8] = {};
-  if (lane < f.dqk / 8)
-    for (int i = 0; i < 8; ++i) qv[i] = ldf(q + 8 * lane + i);
-  auto block_of = [&](int j, int* r) -> const uint8_t* {
-    const int page = kv4_page(c, b, j / CP_KV4_PAGE);
-    *r = j % kKv4Sub;
-    return page < 0 ? nullptr
-                    : c.pages + (int64_t(page) * c.hkv + kvh) * f.block() + (j % CP_KV4_PAGE) / kKv4Sub * f.sub();
-  };
-  auto score = [&](const uint8_t* sub, int r) {
-    float x = 0.f;
-    if (lane < f.dqk / 8) {
-      const uint32_t w = reinterpret_cast<const uint32_t*>(sub + f.kc() + r * (f.dqk / 2))[f.kword(lane)];
-      const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(sub + f.kp()) + r * 2 * f.gk() + lane / 8;
-      const float s = __bfloat162float(p[0]), lo = __bfloat162float(p[f.gk()]);
-      for (int i = 0; i < 8; ++i) x += fmaf(s, float((w >> (4 * i)) & 15u), lo) * qv[i];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
-    return warp_sum(x) * c.scale;
-  };
-  float m = -INFINITY, l = 0.f;
-  for (int j = warp; j < n; j += kWarps) {
-    int r;
-    const uint8_t* sub = block_of(j, &r);
-    if (!sub) continue;
-    const float x = score(sub, r);
-    const float top = fmaxf(m, x);
-    const float keep = m == -INFINITY ? 0.f : expf(m - top), p = x == -INFINITY ? 0.f : expf(x - top);
-    m = top;
-    l = l * keep + p;
-    if (lane < f.dv / 8) {
-      const uint32_t w = reinterpret_cast<const uint32_t*>(sub + f.vc() + r * (f.dv / 2))[f.vword(lane)];
-      const float s = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sub + f.vs())[r * f.gv() + lane / 8]);
-      const float lo = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sub + f.vl())[lane / 8 * kKv4Sub + r]);
-      for (int i = 0; i < 8; ++i) o[i] = o[i] * keep + p * fmaf(s, float((w >> (4 * i)) & 15u), lo);
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    int before = carry, all = carry;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) before += scratch[w];
+      all += scratch[w];
     }
+    if (b < a.c.num_seqs) base[b] = before + x - own;
+    carry = all;
+    __syncthreads();
   }
-  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
-  if (lane < f.dv / 8)
-    for (int i = 0; i < 8; ++i) s_o[warp][8 * lane + i] = o[i];
+  if (tid == 0) base[a.c.num_seqs] = carry;
   __syncthreads();
-  float top = -INFINITY, total = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-  for (int w = 0; w < kWarps; ++w) total += s_m[w] == -INFINITY ? 0.f : s_l[w] * expf(s_m[w] - top);
-  const float lse = top == -INFINITY ? -INFINITY : top + logf(total);
-  if (threadIdx.x == 0) a.lse[int64_t(h) * c.num_seqs * a.n_q + bt] = lse;
-  for (int e = threadIdx.x; e < f.dv; e += kWarps * 32) {
-    float x = 0.f;
-    for (int w = 0; w < kWarps; ++w) x += s_m[w] == -INFINITY ? 0.f : s_o[w][e] * expf(s_m[w] - top);
-    x = top == -INFINITY ? 0.f : x / total;
-    if (a.o_f32) static_cast<float*>(a.o)[row * f.dv + e] = x;
-    else static_cast<__nv_bfloat16*>(a.o)[row * f.dv + e] = __float2bfloat16_rn(x);
+}
+
+// The sequence that holds unit u, searched from b on (base[b] <= u < base[num_seqs]).
+__device__ __forceinline__ int seq_of_unit(const int32_t* base, int n, int b, int u) {
+  if (u < base[b + 1]) return b;
+  int lo = b + 1, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (u < base[mid + 1]) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+// 16 + n of nibbles i and i + 4 as a bf16 pair
+template <int I>
+__device__ __forceinline__ uint32_t nibbles(uint32_t w) {
+  constexpr uint32_t kMask = 0x00780078u, kSixteen = 0x41804180u;
+  const uint32_t x = I == 0 ? w << 3 : w >> (4 * I - 3);
+  return (x & kMask) | kSixteen;
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// bf16 number i of packed words
+template <int N>
+__device__ __forceinline__ float half_at(const uint32_t (&w)[N], int i) {
+  return (i & 1) ? bf_hi(w[i >> 1]) : bf_lo(w[i >> 1]);
+}
+
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                   : "r"(addr + 4 * i));
+  } else if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[i]), "=r"(w[i + 1]) : "r"(addr + 4 * i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i]) : "r"(addr + 4 * i));
+  }
+}
+__device__ __forceinline__ float lds_bf16(uint32_t addr) {
+  uint16_t x;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(addr));
+  return __uint_as_float(uint32_t(x) << 16);
+}
+
+// x as TERMS bf16 terms, the first the nearest
+template <int TERMS>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&t)[TERMS]) {
+#pragma unroll
+  for (int i = 0; i < TERMS; ++i) {
+    t[i] = ptx::pack_bf16(x, y);
+    if (i + 1 < TERMS) {
+      x -= bf_lo(t[i]);
+      y -= bf_hi(t[i]);
+    }
   }
 }
 
-// Every visible slot's probabilities, summed over its head's rows in one
-// order and added once.  A warp per slot.
-template <typename E>
-__global__ void __launch_bounds__(kWarps * 32) kv4_weights_kernel(const Kv4AttnArgs a, const Kv4Format f) {
-  const Kv4Cache& c = a.c;
-  const int G = c.hq / c.hkv, lane = threadIdx.x & 31;
-  const int b = blockIdx.x / c.hkv, kvh = blockIdx.x - b * c.hkv;
-  const int n = kv4_length(c, a.lengths, b);
-  for (int j = blockIdx.y * kWarps + (threadIdx.x >> 5); j < n; j += gridDim.y * kWarps) {
-    const int page = kv4_page(c, b, j / CP_KV4_PAGE);
-    if (page < 0) continue;
-    const int64_t block = int64_t(page) * c.hkv + kvh;
-    const uint8_t* sub = c.pages + block * f.block() + (j % CP_KV4_PAGE) / kKv4Sub * f.sub();
-    const int r = j % kKv4Sub;
-    float kv[8] = {};
-    if (lane < f.dqk / 8) {
-      const uint32_t w = reinterpret_cast<const uint32_t*>(sub + f.kc() + r * (f.dqk / 2))[f.kword(lane)];
-      const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(sub + f.kp()) + r * 2 * f.gk() + lane / 8;
-      const float s = __bfloat162float(p[0]), lo = __bfloat162float(p[f.gk()]);
-      for (int i = 0; i < 8; ++i) kv[i] = fmaf(s, float((w >> (4 * i)) & 15u), lo);
-    }
-    float sum = 0.f;
-    for (int t = 0; t < a.n_q; ++t) {
-      if (j >= n - (a.n_q - 1 - t)) continue;
-      for (int g = 0; g < G; ++g) {
-        const int h = c.inter ? g * c.hkv + kvh : kvh * G + g;
-        const int64_t bt = int64_t(b) * a.n_q + t;
-        float x = 0.f;
-        if (lane < f.dqk / 8)
-          for (int i = 0; i < 8; ++i) x += kv[i] * ldf(static_cast<const E*>(a.q) + (bt * c.hq + h) * f.dqk + 8 * lane + i);
-        sum += expf(warp_sum(x) * c.scale - a.lse[int64_t(h) * c.num_seqs * a.n_q + bt]);
+__device__ __forceinline__ float q_at(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float q_at(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+__device__ __forceinline__ void store_o(const Kv4AttnArgs& a, int64_t i, float x) {
+  if (a.o_f32) static_cast<float*>(a.o)[i] = x;
+  else static_cast<__nv_bfloat16*>(a.o)[i] = __float2bfloat16_rn(x);
+}
+
+// Row n of a row tile of kv head h of sequence b: its (b, t, head) row of q and o, and t
+__device__ __forceinline__ int64_t row_index(const Kv4AttnArgs& a, int b, int h, int n, int* t, int* head) {
+  const int G = a.c.hq / a.c.hkv;
+  *t = n / G;
+  const int g = n - *t * G;
+  *head = a.c.inter ? g * a.c.hkv + h : h * G + g;
+  return (int64_t(b) * a.n_q + *t) * a.c.hq + *head;
+}
+
+template <typename C, typename E>
+__global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnArgs a, const Grid gr) {
+  constexpr int NT = C::NT, GK = C::GK, GV = C::GV, NW = C::NW, DQK = C::DQK, DV = C::DV, TERMS = C::TERMS;
+  constexpr Kv4Format f(DQK, DV);
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[NW * 4];
+  __shared__ int s_abort;
+  __shared__ int32_t s_scan[NW];
+  const uint32_t sbase = ptx::smem_u32(smem);
+  int32_t* base = reinterpret_cast<int32_t*>(smem + gr.off_base);
+  float* qsum_s = reinterpret_cast<float*>(smem + gr.off_sum);      // [GK][COLS]
+  float* stat_s = reinterpret_cast<float*>(smem + gr.off_stat);     // [2][NW][COLS]: references, sums
+  float* merge_s = reinterpret_cast<float*>(smem + gr.off_merge);   // [NW][rows_per_tile][DV]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = lane >> 2, c = lane & 3;
+  const int row_tiles = a.row_tiles, per = a.c.hkv * row_tiles;
+  const uint32_t ring = sbase + gr.off_ring + uint32_t(warp * gr.stages) * f.sub();
+  const uint32_t bar0 = ptx::smem_u32(&bars[warp * 4]);
+  if (lane == 0) {
+    for (int s = 0; s < gr.stages; ++s) ptx::mbar_init(bar0 + 8 * s, 1);
+    ptx::fence_barrier_init();
+  }
+  if (tid == 0) s_abort = 0;
+  scan_lengths<C::THREADS>(a, per, base, s_scan);
+  const int units = base[a.c.num_seqs];
+  const int shares = min(gr.ctas, units);
+  if (int(blockIdx.x) >= shares) return;
+  const int u0 = int(share_begin(units, shares, blockIdx.x)), u1 = int(share_begin(units, shares, blockIdx.x + 1));
+  const ptx::WaitCtx wctx{&s_abort, a.c.err, kWaitLimitNs};
+
+  // ---- this warp's copies: unit u0 + warp, then every NW-th, `stages` ahead
+  int load_unit = u0 + warp, load_seq = 0, loaded = 0;
+  uint32_t absent = 0;  // bit s: the page of stage s's unit is not in the pool
+  auto load_next = [&]() {
+    if (load_unit >= u1) return;
+    load_seq = seq_of_unit(base, a.c.num_seqs, load_seq, load_unit);
+    const int at = load_unit - base[load_seq];
+    const int per_run = (base[load_seq + 1] - base[load_seq]) / per;
+    const int run = at / per_run, i = at - run * per_run;
+    const int page = kv4_page(a.c, load_seq, i / (CP_KV4_PAGE / kKv4Sub));
+    const int s = loaded % gr.stages;
+    absent = page < 0 ? absent | (1u << s) : absent & ~(1u << s);
+    if (lane == 0) {
+      if (page >= 0) {
+        ptx::mbar_arrive_expect_tx(bar0 + 8 * s, uint32_t(f.sub()));
+        ptx::bulk_load(ring + uint32_t(s) * f.sub(),
+                       a.c.pages + (int64_t(page) * a.c.hkv + run / row_tiles) * f.block() +
+                           i % (CP_KV4_PAGE / kKv4Sub) * f.sub(),
+                       uint32_t(f.sub()), bar0 + 8 * s);
+      } else {
+        ptx::mbar_arrive(bar0 + 8 * s);
       }
     }
-    if (lane == 0) atomicAdd(c.weights + block * CP_KV4_PAGE + j % CP_KV4_PAGE, sum);
+    ++loaded;
+    load_unit += NW;
+  };
+  for (int s = 0; s < gr.stages; ++s) load_next();
+
+  const float sl2 = a.c.scale * kLog2e;
+  int done = 0, b = 0;
+  bool ok = true;
+  for (int seg0 = u0; seg0 < u1;) {
+    // ---- the run that holds unit seg0, as far as this share goes
+    b = seq_of_unit(base, a.c.num_seqs, b, seg0);
+    const int per_run = (base[b + 1] - base[b]) / per;
+    const int run = (seg0 - base[b]) / per_run, run0 = base[b] + run * per_run;
+    const int seg1 = min(u1, run0 + per_run);
+    const int h = run / row_tiles, n0 = (run - h * row_tiles) * gr.rows_per_tile;
+    const int rows = min(gr.rows_per_tile, a.rows - n0);
+    const int len = min(kv4_length(a.c, a.lengths, b), per_run * kKv4Sub);
+    // ---- its queries as B fragments (kstep 2j + p: channels 8w + 2p, 8w + 2p + 4 and the next two, w = 4j + lane % 4)
+    for (int e = tid; e < DQK / 16 * NT * 32; e += C::THREADS) {
+      const int ln = e & 31, nt = (e >> 5) % NT, ks = (e >> 5) / NT;
+      const int n = nt * 8 + (ln >> 2), ch = 8 * (4 * (ks >> 1) + (ln & 3)) + 2 * (ks & 1);
+      float x[4] = {};
+      if (n < rows) {
+        int t, head;
+        const E* q = static_cast<const E*>(a.q) + row_index(a, b, h, n0 + n, &t, &head) * DQK + ch;
+        x[0] = q_at(q), x[1] = q_at(q + 4), x[2] = q_at(q + 1), x[3] = q_at(q + 5);
+      }
+      uint32_t f0[TERMS], f1[TERMS];
+      split_pair<TERMS>(x[0], x[1], f0);
+      split_pair<TERMS>(x[2], x[3], f1);
+#pragma unroll
+      for (int m = 0; m < TERMS; ++m)
+        reinterpret_cast<uint2*>(smem + gr.off_frag)[((ks * TERMS + m) * NT + nt) * 32 + ln] = make_uint2(f0[m], f1[m]);
+    }
+    for (int e = tid; e < C::COLS * GK * 8; e += C::THREADS) {  // sums of 64 channels, 8 lanes each
+      const int part = e & 7, n = (e >> 3) % C::COLS, g = (e >> 3) / C::COLS;
+      float x = 0.f;
+      if (n < rows) {
+        int t, head;
+        const E* q = static_cast<const E*>(a.q) + row_index(a, b, h, n0 + n, &t, &head) * DQK + 64 * g + 8 * part;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x += q_at(q + i);
+      }
+      const uint32_t lanes = 0xffu << (lane & 24);
+      x += __shfl_xor_sync(lanes, x, 1);
+      x += __shfl_xor_sync(lanes, x, 2);
+      x += __shfl_xor_sync(lanes, x, 4);
+      if (part == 0) qsum_s[g * C::COLS + n] = x;
+    }
+    __syncthreads();
+    float qsum[GK][NT][2];
+    int lim[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int n = nt * 8 + 2 * c + e;
+#pragma unroll
+        for (int g = 0; g < GK; ++g) qsum[g][nt][e] = qsum_s[g * C::COLS + n];
+        int t, head;
+        row_index(a, b, h, n0 + min(n, rows - 1), &t, &head);
+        lim[nt][e] = len - (a.n_q - 1 - t);
+      }
+    int t_first, head_;
+    row_index(a, b, h, n0, &t_first, &head_);
+    const int lim_min = len - (a.n_q - 1 - t_first);
+
+    float O[GV][4][NT][4], osix[GV][NT][4], ooff[GV][NT][2], ref[NT][2], sum[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int g = 0; g < GV; ++g) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) O[g][i][nt][e] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) osix[g][nt][e] = 0.f;
+        ooff[g][nt][0] = ooff[g][nt][1] = 0.f;
+      }
+      ref[nt][0] = ref[nt][1] = kNoRef;
+      sum[nt][0] = sum[nt][1] = 0.f;
+    }
+
+    bool worked = false;
+    for (int u = u0 + warp + done * NW; u < seg1; u += NW) {
+      const int s = done % gr.stages;
+      if (ok) ok = ptx::mbar_wait_w(bar0 + 8 * s, (done / gr.stages) & 1, kKv4Wait, wctx);
+      if (!ok) break;
+      worked = true;
+      const uint32_t st = ring + uint32_t(s) * f.sub();
+      const bool gone = (absent >> s) & 1;
+      const int j0 = (u - run0) * kKv4Sub;
+
+      // ---- S^T = K Q^T
+      float S[2][NT][4];
+      {
+        uint32_t kw[2][2][C::KW], kp[2][2][GK];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t tok = mt * 16 + x * 8 + r;
+            lds_words<C::KW>(st + f.kc() + tok * (DQK / 2) + c * (C::KW * 4), kw[mt][x]);
+            lds_words<GK>(st + f.kp() + tok * (GK * 4), kp[mt][x]);
+          }
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[mt][nt][e] = 0.f;
+#pragma unroll
+        for (int g = 0; g < GK; ++g) {
+          float acc[2][NT][4];
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[mt][nt][e] = -16.f * qsum[g][nt][e & 1];
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            const int j = 2 * g + jj;
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              uint32_t A[2][4];
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  A[mt][x] = p == 0 ? nibbles<0>(kw[mt][x][j]) : nibbles<2>(kw[mt][x][j]);
+                  A[mt][2 + x] = p == 0 ? nibbles<1>(kw[mt][x][j]) : nibbles<3>(kw[mt][x][j]);
+                }
+#pragma unroll
+              for (int m = 0; m < TERMS; ++m)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  uint32_t q2[2];
+                  lds_words<2>(sbase + gr.off_frag + ((((2 * j + p) * TERMS + m) * NT + nt) * 32 + lane) * 8, q2);
+#pragma unroll
+                  for (int mt = 0; mt < 2; ++mt) ptx::mma_16816(acc[mt][nt], A[mt], q2[0], q2[1]);
+                }
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float ks = half_at(kp[mt][x], g), kl = half_at(kp[mt][x], GK + g);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  S[mt][nt][2 * x + e] += fmaf(ks, acc[mt][nt][2 * x + e], kl * qsum[g][nt][e]);
+            }
+        }
+      }
+      // ---- P = 2^(S - ref)
+      const bool masked = gone || j0 + kKv4Sub > lim_min;  // the same for the whole warp
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[mt][nt][e] *= sl2;
+      uint32_t vis = 0xffffffffu;  // bit (mt * NT + nt) * 4 + e: the element is visible
+      if (masked) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (gone || j0 + mt * 16 + (e >> 1) * 8 + r >= lim[nt][e & 1]) {
+                S[mt][nt][e] = -INFINITY;
+                vis &= ~(1u << ((mt * NT + nt) * 4 + e));
+              }
+      }
+      if (a.accumulate) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int n = nt * 8 + 2 * c + (e & 1);
+            if (n < rows) {
+              float* to = gr.score + (int64_t(u) * gr.rows_per_tile + n) * kKv4Sub + (e >> 1) * 8 + r;
+              to[0] = S[0][nt][e];
+              to[16] = S[1][nt][e];
+            }
+          }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, S[mt][nt][e] - ref[nt][e & 1]);
+      if (__any_sync(0xffffffffu, top > kSlack)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float m = fmaxf(fmaxf(S[0][nt][e], S[0][nt][e + 2]), fmaxf(S[1][nt][e], S[1][nt][e + 2]));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            m = fmaxf(m, ref[nt][e]);
+            const float keep = ptx::ex2(ref[nt][e] - m);
+            ref[nt][e] = m;
+            sum[nt][e] *= keep;
+#pragma unroll
+            for (int g = 0; g < GV; ++g) {
+              ooff[g][nt][e] *= keep;
+              osix[g][nt][e] *= keep;
+              osix[g][nt][e + 2] *= keep;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                O[g][i][nt][e] *= keep;
+                O[g][i][nt][e + 2] *= keep;
+              }
+            }
+          }
+      }
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            S[mt][nt][e] = ptx::ex2(S[mt][nt][e] - ref[nt][e & 1]);
+            sum[nt][e & 1] += S[mt][nt][e];
+          }
+      // ---- O^T += V^T P^T, 16 tokens at a time
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t vw[4][GV], vs[2][(GV + 1) / 2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t tok = mt * 16 + 2 * c + (i & 1) + (i >> 1) * 8;
+          lds_words<GV>(st + f.vc() + tok * (DV / 2) + r * (GV * 4), vw[i]);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t tok = mt * 16 + x * 8 + r;
+          if constexpr (GV == 2) {
+            lds_words<1>(st + f.vs() + tok * 4, vs[x]);
+          } else {
+            vs[x][0] = __float_as_uint(lds_bf16(st + f.vs() + tok * 2)) >> 16;
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < GV; ++g) {
+          // P s of this group as B fragments, and P low on the side
+          uint32_t B0[NT][TERMS], B1[NT][TERMS];
+          const float s0 = half_at(vs[0], g), s1 = half_at(vs[1], g);
+          const float l0 = lds_bf16(st + f.vl() + (g * kKv4Sub + mt * 16 + r) * 2);
+          const float l1 = lds_bf16(st + f.vl() + (g * kKv4Sub + mt * 16 + 8 + r) * 2);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float* p = S[mt][nt];
+            float ps[4] = {p[0] * s0, p[1] * s0, p[2] * s1, p[3] * s1};
+            float pl[4] = {p[0] * l0, p[1] * l0, p[2] * l1, p[3] * l1};
+            if (masked) {  // what an unseen slot holds (NaN, in the worst case) reaches nothing
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (!((vis >> ((mt * NT + nt) * 4 + e)) & 1)) ps[e] = pl[e] = 0.f;
+            }
+            ooff[g][nt][0] += pl[0] + pl[2];
+            ooff[g][nt][1] += pl[1] + pl[3];
+            split_pair<TERMS>(ps[0], ps[1], B0[nt]);
+            split_pair<TERMS>(ps[2], ps[3], B1[nt]);
+#pragma unroll
+            for (int m = 0; m < TERMS; ++m) {
+              B0[nt][m] = ptx::movm_trans(B0[nt][m]);
+              B1[nt][m] = ptx::movm_trans(B1[nt][m]);
+            }
+          }
+          const uint32_t lo0 = __byte_perm(vw[0][g], vw[1][g], 0x5410), hi0 = __byte_perm(vw[0][g], vw[1][g], 0x7632);
+          const uint32_t lo1 = __byte_perm(vw[2][g], vw[3][g], 0x5410), hi1 = __byte_perm(vw[2][g], vw[3][g], 0x7632);
+          const uint32_t A[5][4] = {{nibbles<0>(lo0), nibbles<0>(hi0), nibbles<0>(lo1), nibbles<0>(hi1)},
+                                    {nibbles<1>(lo0), nibbles<1>(hi0), nibbles<1>(lo1), nibbles<1>(hi1)},
+                                    {nibbles<2>(lo0), nibbles<2>(hi0), nibbles<2>(lo1), nibbles<2>(hi1)},
+                                    {nibbles<3>(lo0), nibbles<3>(hi0), nibbles<3>(lo1), nibbles<3>(hi1)},
+                                    {0xC180C180u, 0xC180C180u, 0xC180C180u, 0xC180C180u}};  // -16
+#pragma unroll
+          for (int m = 0; m < TERMS; ++m)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) ptx::mma_16816(O[g][i][nt], A[i], B0[nt][m], B1[nt][m]);
+              ptx::mma_16816(osix[g][nt], A[4], B0[nt][m], B1[nt][m]);
+            }
+        }
+      }
+      __syncwarp();  // the stage has been read
+      ++done;
+      load_next();
+    }
+
+    // ---- end of the run in this share: the warps' results joined in shared memory
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], o);
+#pragma unroll
+          for (int g = 0; g < GV; ++g) ooff[g][nt][e] += __shfl_xor_sync(0xffffffffu, ooff[g][nt][e], o);
+        }
+        const int n = nt * 8 + 2 * c + e;
+        if (r == 0) {
+          stat_s[warp * C::COLS + n] = ref[nt][e];
+          stat_s[(NW + warp) * C::COLS + n] = sum[nt][e];
+        }
+        if (worked && n < rows) {
+          float* to = merge_s + (warp * gr.rows_per_tile + n) * DV + 8 * r;
+#pragma unroll
+          for (int g = 0; g < GV; ++g) {
+            const float add = osix[g][nt][e] + ooff[g][nt][e];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              *reinterpret_cast<float4*>(to + 64 * g + 4 * x) =
+                  make_float4(O[g][0][nt][e + 2 * x] + add, O[g][1][nt][e + 2 * x] + add, O[g][2][nt][e + 2 * x] + add,
+                              O[g][3][nt][e + 2 * x] + add);
+          }
+        }
+      }
+    __syncthreads();
+    const bool whole = seg0 == run0 && seg1 == run0 + per_run;
+    float* part = gr.part + (int64_t(blockIdx.x) * 2 + (seg0 == run0)) * part_floats(C::COLS, DV);
+    for (int e = tid; e < rows * DV; e += C::THREADS) {
+      const int n = e / DV, d = e - n * DV;
+      float m = kNoRef, l = 0.f, x = 0.f;
+      for (int w = 0; w < NW; ++w) m = fmaxf(m, stat_s[w * C::COLS + n]);
+      for (int w = 0; w < NW; ++w) {
+        const float mw = stat_s[w * C::COLS + n], lw = stat_s[(NW + w) * C::COLS + n];
+        if (lw == 0.f) continue;  // saw nothing (or has no unit here)
+        const float k = ptx::ex2(mw - m);
+        l += k * lw;
+        x += k * merge_s[(w * gr.rows_per_tile + n) * DV + d];
+      }
+      if (whole) {
+        int t, head;
+        const int64_t row = row_index(a, b, h, n0 + n, &t, &head);
+        store_o(a, row * DV + d, l == 0.f ? 0.f : x / l);
+        if (d == 0)
+          a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] =
+              l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      } else {
+        part[2 * C::COLS + e] = x;
+        if (d == 0) {
+          part[n] = m;
+          part[C::COLS + n] = l;
+        }
+      }
+    }
+    __syncthreads();
+    seg0 = seg1;
+  }
+  if (!ok) {  // copies still in flight land before the CTA goes
+    volatile int no_abort = 0;
+    const ptx::WaitCtx drain{&no_abort, nullptr, kWaitLimitNs};
+    for (int i = max(done, loaded - gr.stages); i < loaded; ++i)
+      ptx::mbar_wait_w(bar0 + 8 * (i % gr.stages), (i / gr.stages) & 1, kKv4Wait, drain);
   }
 }
 
-template <typename E>
-cudaError_t launch(const Kv4AttnArgs& a, Kv4Format f, cudaStream_t st) {
-  kv4_attn_kernel<E><<<unsigned(a.c.num_seqs) * unsigned(a.n_q) * unsigned(a.c.hq), kWarps * 32, 0, st>>>(a, f);
-  if (a.accumulate)
-    kv4_weights_kernel<E><<<dim3(unsigned(a.c.num_seqs) * unsigned(a.c.hkv), 64), kWarps * 32, 0, st>>>(a, f);
+// Joins the runs that were cut (one CTA each; whole ones are done, empty ones
+// get o = 0, lse = -inf), and adds up the weights: the other CTAs' warps take
+// sub-blocks, a lane a token.
+constexpr int kJoinThreads = 256;
+
+template <int COLS, int DV>
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnArgs a, const Grid gr, int runs) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int32_t s_scan[kJoinThreads / 32];
+  int32_t* base = reinterpret_cast<int32_t*>(smem);
+  const int row_tiles = a.row_tiles, per = a.c.hkv * row_tiles;
+  scan_lengths<kJoinThreads>(a, per, base, s_scan);
+  const int units = base[a.c.num_seqs], shares = min(gr.ctas, units);
+  ptx::grid_wait_previous();
+  constexpr int kPart = part_floats(COLS, DV);
+  // partials of the run that starts at unit run0: shares c0 .. c1, slot 0 in all but its first
+  auto part_of = [&](int sh, int run0) {
+    return gr.part + (int64_t(sh) * 2 + (share_begin(units, shares, sh) <= run0)) * kPart;
+  };
+  if (int(blockIdx.x) < runs) {
+    const int b = int(blockIdx.x) / per, run = int(blockIdx.x) - b * per;
+    const int per_run = (base[b + 1] - base[b]) / per, run0 = base[b] + run * per_run;
+    const int h = run / row_tiles, n0 = (run - h * row_tiles) * gr.rows_per_tile;
+    const int rows = min(gr.rows_per_tile, a.rows - n0);
+    int c0 = 0, c1 = 0;
+    if (per_run > 0) {
+      c0 = share_of(units, shares, run0);
+      c1 = share_of(units, shares, run0 + per_run - 1);
+      if (c0 == c1) return;
+    }
+    for (int e = threadIdx.x; e < rows * DV; e += kJoinThreads) {
+      const int n = e / DV, d = e - n * DV;
+      float m = kNoRef, l = 0.f, x = 0.f;
+      if (per_run > 0) {
+        for (int sh = c0; sh <= c1; ++sh) m = fmaxf(m, part_of(sh, run0)[n]);
+        for (int sh = c0; sh <= c1; ++sh) {
+          const float* p = part_of(sh, run0);
+          if (p[COLS + n] == 0.f) continue;
+          const float k = ptx::ex2(p[n] - m);
+          l += k * p[COLS + n];
+          x += k * p[2 * COLS + e];
+        }
+      }
+      int t, head;
+      const int64_t row = row_index(a, b, h, n0 + n, &t, &head);
+      store_o(a, row * DV + d, l == 0.f ? 0.f : x / l);
+      if (d == 0)
+        a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] =
+            l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+    return;
+  }
+  // ---- weights
+  const int lane = threadIdx.x & 31;
+  const int warps = (int(gridDim.x) - runs) * (kJoinThreads / 32);
+  const int w = (int(blockIdx.x) - runs) * (kJoinThreads / 32) + int(threadIdx.x >> 5);
+  const int64_t all = units / row_tiles;  // sub-blocks of the cache
+  const int64_t v0 = all * w / warps, v1 = all * (w + 1) / warps;
+  int b = 0, last_h = -1, last_b = -1;
+  float lse2[8];  // row lane of row tile i (at most 8 tiles are kept)
+  for (int64_t v = v0; v < v1; ++v) {
+    b = seq_of_unit(base, a.c.num_seqs, b, int(v * row_tiles));
+    const int per_run = (base[b + 1] - base[b]) / per;
+    const int at = int(v) - base[b] / row_tiles, h = at / per_run, i = at - h * per_run;
+    float add = 0.f;
+    for (int rt = 0; rt < row_tiles; ++rt) {
+      const int run0 = base[b] + (h * row_tiles + rt) * per_run, n0 = rt * gr.rows_per_tile;
+      const int rows = min(gr.rows_per_tile, a.rows - n0);
+      float ls;
+      if (b == last_b && h == last_h && rt < 8) {
+        ls = lse2[0];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) ls = rt == k ? lse2[k] : ls;
+      } else {
+        ls = INFINITY;
+        if (lane < rows) {
+          const int c0 = share_of(units, shares, run0), c1 = share_of(units, shares, run0 + per_run - 1);
+          if (c0 == c1) {
+            int t, head;
+            row_index(a, b, h, n0 + lane, &t, &head);
+            ls = a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] * kLog2e;
+          } else {
+            float m = kNoRef, l = 0.f;
+            for (int sh = c0; sh <= c1; ++sh) m = fmaxf(m, part_of(sh, run0)[lane]);
+            for (int sh = c0; sh <= c1; ++sh) {
+              const float* p = part_of(sh, run0);
+              l += ptx::ex2(p[lane] - m) * p[COLS + lane];
+            }
+            ls = l == 0.f ? -INFINITY : m + log2f(l);
+          }
+          if (ls == -INFINITY) ls = INFINITY;  // a row that sees nothing gives nothing
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) lse2[k] = rt == k ? ls : lse2[k];
+      }
+      const float* sc = gr.score + int64_t(run0 + i) * gr.rows_per_tile * kKv4Sub + lane;
+      for (int n = 0; n < rows; ++n) add += ptx::ex2(sc[n * kKv4Sub] - __shfl_sync(0xffffffffu, ls, n));
+    }
+    last_b = b;
+    last_h = h;
+    const int page = kv4_page(a.c, b, i / (CP_KV4_PAGE / kKv4Sub));
+    const int slot = i * kKv4Sub + lane;
+    if (page >= 0 && slot < kv4_length(a.c, a.lengths, b))
+      atomicAdd(a.c.weights + (int64_t(page) * a.c.hkv + h) * CP_KV4_PAGE + slot % CP_KV4_PAGE, add);
+  }
+}
+
+int sm_count() {
+  static int n = 0;
+  if (n == 0) {
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess &&
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0)
+      n = v;
+    else
+      return 152;
+  }
+  return n;
+}
+
+// Rows of one pass: up to 8 in one column tile of the MMAs, else up to 16 in
+// two (fp32 caches: 8, their three terms take the registers).
+int cols_of(int rows, int dtype) { return dtype == CP_DT_BF16 && rows > 8 ? 16 : 8; }
+
+uint32_t up(uint32_t x, uint32_t n) { return (x + n - 1) / n * n; }
+
+template <typename C, typename E>
+cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
+  constexpr Kv4Format f(C::DQK, C::DV);
+  uint32_t off = 0;
+  gr.off_base = off;
+  off = up(off + 4 * (a.c.num_seqs + 1), 128);
+  gr.off_frag = off;
+  off += C::kFragBytes;
+  gr.off_sum = off;
+  off += C::GK * C::COLS * 4;
+  gr.off_stat = off;
+  off += 2 * C::NW * C::COLS * 4;
+  gr.off_merge = off;
+  off = up(off + C::NW * gr.rows_per_tile * C::DV * 4, 128);
+  gr.off_ring = off;
+  constexpr uint32_t kMost = 231000;
+  gr.stages = int(std::min<uint32_t>(4, (kMost - off) / (C::NW * f.sub())));
+  if (off > kMost || gr.stages < 1) return cudaErrorInvalidValue;
+  off += gr.stages * C::NW * f.sub();
+  auto kernel = kv4_attn_kernel<C, E>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(off));
+  if (e != cudaSuccess) return e;
+  kernel<<<unsigned(gr.ctas), C::THREADS, off, st>>>(a, gr);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int runs = a.c.num_seqs * a.c.hkv * a.row_tiles;
+  kv4_join_kernel<C::COLS, C::DV><<<unsigned(runs + (a.accumulate ? 2 * gr.ctas : 0)), kJoinThreads,
+                                    4 * (a.c.num_seqs + 1), st>>>(a, gr, runs);
   return cudaGetLastError();
+}
+
+template <int DQK, int DV>
+cudaError_t launch_dims(const Kv4AttnArgs& a, const Grid& gr, int dtype, cudaStream_t st) {
+  if (dtype == CP_DT_F32) return launch<Cfg<DQK, DV, 1, 3>, float>(a, gr, st);
+  return cols_of(a.rows, dtype) == 8 ? launch<Cfg<DQK, DV, 1, 1>, __nv_bfloat16>(a, gr, st)
+                                     : launch<Cfg<DQK, DV, 2, 1>, __nv_bfloat16>(a, gr, st);
+}
+
+struct Layout {
+  int rows, cols, row_tiles, rows_per_tile;
+  size_t part, score, total;
+};
+Layout layout_of(int num_seqs, int hq, int hkv, int dv, int max_pages, int dtype, int n_q, int accumulate) {
+  Layout L;
+  L.rows = hq / hkv * n_q;
+  L.cols = cols_of(L.rows, dtype);
+  L.row_tiles = (L.rows + L.cols - 1) / L.cols;
+  L.rows_per_tile = (L.rows + L.row_tiles - 1) / L.row_tiles;
+  L.row_tiles = (L.rows + L.rows_per_tile - 1) / L.rows_per_tile;
+  L.part = 0;
+  L.score = (size_t(sm_count()) * 2 * part_floats(L.cols, dv) * 4 + 255) / 256 * 256;
+  const size_t units = size_t(num_seqs) * hkv * L.row_tiles * max_pages * (CP_KV4_PAGE / kKv4Sub);
+  L.total = L.score + (accumulate ? units * L.rows_per_tile * kKv4Sub * 4 : 0);
+  L.total = (L.total + 255) / 256 * 256;
+  return L;
 }
 
 }  // namespace
 
-size_t kv4_attn_workspace(const cp_kv4_t*, int32_t, int32_t) { return 256; }
+size_t kv4_attn_workspace(const cp_kv4_t* c, int32_t n_q, int32_t accumulate) {
+  return layout_of(c->num_seqs, c->hq, c->hkv, c->d_v, c->max_pages, c->dtype, n_q, accumulate).total;
+}
 
-cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, int dqk, int dv, int dtype, cudaStream_t st) {
-  return dtype == CP_DT_BF16 ? launch<__nv_bfloat16>(a, Kv4Format(dqk, dv), st) : launch<float>(a, Kv4Format(dqk, dv), st);
+int64_t kv4_attn_units(const cp_kv4_t* c, int32_t n_q) {
+  return int64_t(c->num_seqs) * c->hkv * c->max_pages * (CP_KV4_PAGE / kKv4Sub) *
+         layout_of(c->num_seqs, c->hq, c->hkv, c->d_v, c->max_pages, c->dtype, n_q, 0).row_tiles;
+}
+
+cudaError_t launch_kv4_attn(Kv4AttnArgs a, int dqk, int dv, int dtype, cudaStream_t st) {
+  const Layout L = layout_of(a.c.num_seqs, a.c.hq, a.c.hkv, dv, a.c.max_pages, dtype, a.n_q, a.accumulate);
+  a.rows = L.rows;
+  a.row_tiles = L.row_tiles;
+  Grid gr{};
+  gr.ctas = sm_count();
+  gr.rows_per_tile = L.rows_per_tile;
+  gr.part = reinterpret_cast<float*>(a.ws + L.part);
+  gr.score = reinterpret_cast<float*>(a.ws + L.score);
+  switch (dqk * 1000 + dv) {
+    case 64064: return launch_dims<64, 64>(a, gr, dtype, st);
+    case 64128: return launch_dims<64, 128>(a, gr, dtype, st);
+    case 128064: return launch_dims<128, 64>(a, gr, dtype, st);
+    case 128128: return launch_dims<128, 128>(a, gr, dtype, st);
+    case 192064: return launch_dims<192, 64>(a, gr, dtype, st);
+    case 192128: return launch_dims<192, 128>(a, gr, dtype, st);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace cpattn

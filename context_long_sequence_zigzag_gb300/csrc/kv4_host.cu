@@ -65,8 +65,7 @@ Kv4Cache device_cache(const cp_kv4_t* c) {
 cp_status_t check_queries(const cp_kv4_t* c, int32_t n_q) {
   if (n_q < 1) return CP_ERR_INVALID_ARG;
   if (n_q > CP_KV4_MAX_QUERIES) return CP_ERR_UNSUPPORTED;
-  const int64_t rows = int64_t(c->hq / c->hkv) * n_q;
-  if (int64_t(c->num_seqs) * c->hkv * c->max_pages * rows > (int64_t(1) << 34)) return CP_ERR_UNSUPPORTED;
+  if (kv4_attn_units(c, n_q) > INT32_MAX) return CP_ERR_UNSUPPORTED;
   return CP_OK;
 }
 
@@ -137,7 +136,6 @@ cp_status_t cp_kv4_attn(const cp_kv4_t* c, int32_t n_q, const void* q, const int
   Kv4AttnArgs a{};
   a.c = device_cache(c);
   a.n_q = n_q;
-  a.rows = c->hq / c->hkv * n_q;
   a.q = q;
   a.lengths = lengths;
   a.o = o;

@@ -391,7 +391,7 @@ cp_status_t cp_attn_key_weights(const cp_desc_t* desc, int64_t last, const void*
 #define CP_KV4_PAGE 64
 #define CP_KV4_GROUP 64
 #define CP_KV4_MAX_QUERIES 16
-#define CP_KV4_MAX_SEQS 65536
+#define CP_KV4_MAX_SEQS 4096
 
 /* A cache, or the part of it that a call deals with.  Read on the host during
  * each call; not retained. */

@@ -219,6 +219,16 @@ def test_attn_nan_behind_the_end_and_in_unseen_slots(dtype):
     assert nan_lse.sum() == 2 and bool(nan_lse[:2, 0, 2].all())
 
 
+def test_attn_nothing_but_nan():
+    """A sequence whose only visible keys are NaN gives NaN, not the empty result."""
+    c = Filled([1, 40], 2, 1, 64, 64, seed=18)
+    c.k[1][c.table[0, 0]] = math.nan
+    c.k[1][c.table[1, 0]] = math.nan
+    c.pages.copy_(torch.from_numpy(oracle.kv4_pack(c.k, c.v)))
+    o, lse = cpa.cp_kv4_attn(c.cache, torch.ones(2, 1, 2, 64, device="cuda").bfloat16(), ints(c.lengths))
+    assert torch.isnan(o).all() and torch.isnan(lse).all()
+
+
 def test_attn_partials_join_to_the_whole():
     """A sequence cut over two caches (context-parallel ranks): the partial results join in cp_lse_merge."""
     c = Filled([128 + 71], 8, 2, 128, 128, seed=13)

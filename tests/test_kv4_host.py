@@ -73,7 +73,7 @@ def _desc(**kw):
     ({"weights": 8196}, cpa.CP_ERR_INVALID_ARG),
     ({"num_pages": -1}, cpa.CP_ERR_INVALID_ARG),
     ({"max_pages": 1 << 25}, cpa.CP_ERR_UNSUPPORTED),
-    ({"num_seqs": 65537}, cpa.CP_ERR_UNSUPPORTED),
+    ({"num_seqs": 4097}, cpa.CP_ERR_UNSUPPORTED),
     ({"num_seqs": 0, "pages": None, "page_table": None}, cpa.CP_OK),
     ({"weights": None}, cpa.CP_OK),
 ])
