@@ -1,6 +1,334 @@
-// placeholder
+// key_weights_sm103.cu — accumulated attention weight of every key of a
+// prompt, on the sm_103a tensor cores (tcgen05 + TMEM + TMA).
+//
+//   w[c, j] = sum over c's query heads h and the queries i that see key j of
+//             exp(scale q_i.k_j - lse_i)
+// which is a column sum of the attention probabilities, rebuilt from the
+// forward's lse as the backward rebuilds them ("Ulysses与Ring-Attention详解"
+// §4.3).  The key-major walk is the dK/dV kernel's: one CTA owns a 128-key
+// tile of one kv head and visits, for every query head of the group, the
+// query runs that see it.  With S^T = K Q^T a thread holds a whole key row
+// (TMEM lane = key), so its column sum is a sum over its own registers: no
+// exchange between threads, nothing written but one float a key.
+//
+// Per 128 x 128 step the tensor cores need 512 cycles (128-wide heads), the
+// exponentials 1024 at 16 a cycle.  S^T has four TMEM buffers; two groups of
+// four warps take the steps in turn, so that one group's loads and waits
+// overlap the other's exponentials.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
 #include "internal.h"
+#include "plan_check.cuh"
+#include "query_steps.cuh"
+#include "sm103_ptx.cuh"
+
 namespace cpattn {
-bool tc_key_weights_supported(int32_t) { return false; }
-cudaError_t launch_tc_key_weights(const AttnArgs&, cudaStream_t) { return cudaErrorInvalidValue; }
+
+bool make_map_3d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elt, int64_t dim, int64_t heads,
+                 int64_t T, int box_inner, int box_rows, CUtensorMapSwizzle swz);
+
+namespace {
+
+constexpr int BT = 128;                 // keys of a tile, queries of a step
+constexpr uint32_t kPanel = 128 * 128;  // 128 rows x 64 bf16 columns, 128-byte swizzled: 16 KiB
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr int kGroupThreads = 128;
+constexpr int kThreads = 2 * kGroupThreads + 64;
+constexpr int kBufs = 4;        // S^T buffers
+constexpr int kPieceMaps = 15;  // boxes of 8, 16, ..., 120 rows for the pieces of gathered tiles
+
+enum WaitSite : int { kSiteK = 0x61, kSiteQEmpty, kSiteQFull, kSiteSFull, kSiteSFree, kSiteDrain, kSiteAlign };
+
+struct Params {
+  CUtensorMap tq, tk;
+  CUtensorMap tqp[kPieceMaps];  // plans with gathered query tiles only
+  AttnArgs a;
+  int32_t* err;
+};
+
+template <int DQK>
+struct Cfg {
+  static constexpr int kPanels = DQK / 64;
+  static constexpr int NS = DQK == 128 ? 5 : 3;  // stages of Q
+  static constexpr uint32_t kTileBytes = kPanels * kPanel;
+  static constexpr uint32_t offK = 0;
+  static constexpr uint32_t offQ = kTileBytes;
+  static constexpr uint32_t offStat = offQ + NS * kTileBytes;  // [group][2][BT] floats
+  static constexpr uint32_t offBar = offStat + 2 * 2 * BT * 4;
+  static constexpr int kNumBars = 1 + 2 * NS + 2 * kBufs;
+  static constexpr uint32_t kSmem = offBar + kNumBars * 8 + 16;
+  static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+// -lse * log2e of query column `col` of the step the cursor points at, -inf
+// where a gathered tile holds no query.
+template <bool PACKED>
+__device__ __forceinline__ float load_stat(const AttnArgs& a, const StepCursor<BT>& c, int col) {
+  int64_t row = -1;
+  if (PACKED && c.packed()) {
+    const int count = c.cur.flags >> kPackCountShift;
+    for (int i = 0; i < count; ++i) {
+      const PackPiece pc = a.pieces[c.cur.row0 + i];
+      if (col >= pc.dst && col < pc.dst + pc.keys) row = int64_t(pc.src) + (col - pc.dst);
+    }
+  } else if (col < c.n()) {
+    row = c.row() + col;
+  }
+  return row < 0 ? -INFINITY : -(a.lse_in[int64_t(c.head()) * a.T + row] * kLog2e);
+}
+
+template <int DQK, bool PACKED>
+__global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<DQK>;
+  constexpr int NS = C::NS;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = ptx::smem_u32(smem);
+  const AttnArgs& a = p.a;
+  if (sbase & 1023u) {  // the swizzled operand panels need 1024-byte alignment
+    if (threadIdx.x == 0 && p.err) atomicCAS(p.err, 0, 0x100 | kSiteAlign);
+    return;
+  }
+  // kv heads outermost, then the tiles (heaviest first): the CTAs resident at
+  // one time read one head's Q
+  const int kvh = int(blockIdx.x / unsigned(a.num_tiles));
+  const int tile_idx = int(blockIdx.x - unsigned(kvh) * unsigned(a.num_tiles));
+  if (a.debug && !debug_plan_ok(a, tile_idx, kvh, kvh, true, p.err)) return;
+  const TileDesc tile = a.tiles[tile_idx];
+  const int G = a.hq / a.hkv;
+  const int n_steps = tile.work * G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const uint32_t bar_k = sbase + C::offBar;
+  auto bar_q_full = [&](int s) { return bar_k + 8u * (1 + s); };
+  auto bar_q_empty = [&](int s) { return bar_k + 8u * (1 + NS + s); };
+  auto bar_s_full = [&](int b) { return bar_k + 8u * (1 + 2 * NS + b); };           // S^T of buffer b computed
+  auto bar_s_free = [&](int b) { return bar_k + 8u * (1 + 2 * NS + kBufs + b); };   // and read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::offBar + C::kNumBars * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::offBar + C::kNumBars * 8 + 4);
+
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(bar_k, 1);
+    for (int s = 0; s < NS; ++s) {
+      ptx::mbar_init(bar_q_full(s), 2);
+      ptx::mbar_init(bar_q_empty(s), 1);
+    }
+    for (int b = 0; b < kBufs; ++b) {
+      ptx::mbar_init(bar_s_full(b), 1);
+      ptx::mbar_init(bar_s_free(b), 4);
+    }
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    ptx::prefetch_tmap(&p.tq);
+    ptx::prefetch_tmap(&p.tk);
+  }
+  if (PACKED && warp == 8 && lane >= 1 && lane <= kPieceMaps) ptx::prefetch_tmap(&p.tqp[lane - 1]);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const ptx::WaitCtx wctx{abort_flag, p.err, kWaitLimitNs};
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ producers: lanes 0 and 1 split the panels
+    if (lane < 2 && n_steps > 0) {
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(bar_k, C::kTileBytes);
+        for (int c = 0; c < C::kPanels; ++c)
+          ptx::tma_load_3d(sbase + C::offK + c * kPanel, &p.tk, bar_k, c * 64, kvh, tile.row0);
+      }
+      const uint32_t bytes = uint32_t((C::kPanels + 1 - lane) / 2) * kPanel;  // panels lane, lane + 2, ...
+      StepCursor<BT> cur;
+      cur.init(a.ranges, tile.range_begin, tile.range_count, G, kvh, a.hkv, a.gqa_interleaved);
+      int issued = 0;
+      for (int i = 0; i < n_steps; ++i, cur.next()) {
+        const int st = i % NS;
+        if (i >= NS && !ptx::mbar_wait(bar_q_empty(st), ((i / NS) - 1) & 1, kSiteQEmpty, wctx)) break;
+        const int h = cur.head();
+        const uint32_t dst = sbase + C::offQ + st * C::kTileBytes;
+        ptx::mbar_arrive_expect_tx(bar_q_full(st), bytes);
+        if (!PACKED || !cur.packed()) {
+          for (int c = lane; c < C::kPanels; c += 2)
+            ptx::tma_load_3d(dst + c * kPanel, &p.tq, bar_q_full(st), c * 64, h, cur.row());
+        } else {
+          // one box per piece; the pieces cover the rows of the step from 8-row (1 KiB) boundaries
+          const int count = cur.cur.flags >> kPackCountShift;
+          for (int k = 0; k < count; ++k) {
+            const PackPiece pc = a.pieces[cur.cur.row0 + k];
+            const CUtensorMap* m = pc.rows >= BT ? &p.tq : p.tqp + (max(pc.rows, 8) >> 3) - 1;
+            for (int c = lane; c < C::kPanels; c += 2)
+              ptx::tma_load_3d(dst + c * kPanel + uint32_t(pc.dst) * 128, m, bar_q_full(st), c * 64, h, pc.src);
+          }
+        }
+        ++issued;
+      }
+      if (*abort_flag) {
+        volatile int no_abort = 0;
+        const ptx::WaitCtx drain{&no_abort, nullptr, kWaitLimitNs};
+        if (lane == 0) ptx::mbar_wait(bar_k, 0, kSiteDrain, drain);
+        for (int i = max(0, issued - NS); i < issued; ++i)
+          ptx::mbar_wait(bar_q_full(i % NS), (i / NS) & 1, kSiteDrain, drain);
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issuer (whole warp)
+    if (n_steps > 0) {
+      constexpr uint32_t idS = ptx::idesc_bf16_f32(BT, BT, false, false);
+      const uint64_t dk = ptx::sdesc_sw128(sbase + C::offK, 16, 1024);
+      bool ok = ptx::mbar_wait_w(bar_k, 0, kSiteK, wctx);
+      int i = 0;
+      for (; ok && i < n_steps; ++i) {
+        const int st = i % NS, b = i % kBufs;
+        ok = ptx::mbar_wait_w(bar_q_full(st), (i / NS) & 1, kSiteQFull, wctx) &&
+             (i < kBufs || ptx::mbar_wait_w(bar_s_free(b), ((i / kBufs) - 1) & 1, kSiteSFree, wctx));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint64_t dq = ptx::sdesc_sw128(sbase + C::offQ + st * C::kTileBytes, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < DQK / 16; ++kk) {
+          const uint32_t o = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
+          ptx::mma_ss_w(tmem + b * BT, dk + o, dq + o, idS, kk > 0);
+        }
+        ptx::mma_commit_w(bar_s_full(b));
+        ptx::mma_commit_w(bar_q_empty(st));
+      }
+      if (!ok && i > 0) {  // the MMAs issued so far end before the CTA frees its TMEM
+        volatile int no_abort = 0;
+        const ptx::WaitCtx drain{&no_abort, nullptr, kWaitLimitNs};
+        ptx::mbar_wait_w(bar_s_full((i - 1) % kBufs), ((i - 1) / kBufs) & 1, kSiteDrain, drain);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ column sums: group g takes steps g, g + 2, ...
+    const int grp = warp >> 2;
+    const int t = threadIdx.x & (kGroupThreads - 1);  // key row = TMEM lane; column whose statistic it loads
+    const uint32_t tS = tmem + (uint32_t((warp & 3) * 32) << 16);
+    float* stat = reinterpret_cast<float*>(smem + C::offStat) + grp * 2 * BT;
+    const float sl2 = a.scale * kLog2e;
+    const uint64_t sl2x2 = ptx::f32x2(sl2, sl2);
+    const int kpos = tile.pos0 + t, nk = tile.nrows;
+    StepCursor<BT> cur;
+    cur.init(a.ranges, tile.range_begin, tile.range_count, G, kvh, a.hkv, a.gqa_interleaved);
+    if (grp == 1 && n_steps > 1) cur.next();
+    float next = grp < n_steps ? load_stat<PACKED>(a, cur, t) : 0.f;
+    float w = 0.f;
+    bool ok = true;
+    for (int i = grp, k = 0; i < n_steps; i += 2, ++k) {
+      const int nq = cur.n(), qpos0 = cur.pos(), b = i % kBufs;
+      const bool packed = PACKED && cur.packed();
+      float* st = stat + (k & 1) * BT;
+      // (the buffer was last read two of this group's steps ago, before the barrier of the step between)
+      st[t] = next;
+      ptx::named_barrier(1 + grp, kGroupThreads);
+      cur.next();
+      if (i + 2 < n_steps) {
+        cur.next();
+        next = load_stat<PACKED>(a, cur, t);
+      }
+      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_poll(bar_s_full(b), (i / kBufs) & 1, kSiteSFull, wctx));
+      if (!ok) continue;  // keep to the group's barriers
+      ptx::tc_fence_after();
+      const bool causal = a.causal && !packed;
+      // columns [cmin, cmax) are visible; columns without a query have the statistic -inf
+      const bool need_mask = packed || nq < BT || (causal && qpos0 < tile.pos0 + BT - 1);
+      const int cmin = causal ? kpos - qpos0 : 0;
+      uint64_t s0 = 0, s1 = 0;  // a step's own sums: a long sum's roundings stay small
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t x[2][32];
+        ptx::tmem_ld32(tS + b * BT + 64 * half, x[0]);
+        ptx::tmem_ld32(tS + b * BT + 64 * half + 32, x[1]);
+        ptx::tmem_ld_wait();
+        ptx::reg_fence32(x[0]);
+        ptx::reg_fence32(x[1]);
+        if (half == 1) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar_s_free(b));
+        }
+#pragma unroll
+        for (int j = 0; j < 64; j += 4) {
+          const int col = 64 * half + j;
+          const float4 nl = *reinterpret_cast<const float4*>(st + col);
+          const uint32_t* xs = &x[j >> 5][j & 31];
+          float y[4];
+          ptx::f32x2_split(ptx::fma_f32x2(ptx::f32x2(__uint_as_float(xs[0]), __uint_as_float(xs[1])), sl2x2,
+                                          ptx::f32x2(nl.x, nl.y)), y[0], y[1]);
+          ptx::f32x2_split(ptx::fma_f32x2(ptx::f32x2(__uint_as_float(xs[2]), __uint_as_float(xs[3])), sl2x2,
+                                          ptx::f32x2(nl.z, nl.w)), y[2], y[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = ptx::ex2(y[e]);
+          if (need_mask) {
+            const float n4[4] = {nl.x, nl.y, nl.z, nl.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (col + e < cmin || n4[e] == -INFINITY) y[e] = 0.f;
+          }
+          s0 = ptx::add_f32x2(s0, ptx::f32x2(y[0], y[1]));
+          s1 = ptx::add_f32x2(s1, ptx::f32x2(y[2], y[3]));
+        }
+      }
+      float e0, e1;
+      ptx::f32x2_split(ptx::add_f32x2(s0, s1), e0, e1);
+      w += e0 + e1;
+    }
+    // the second group's sums through shared memory, in its statistics' place once all its threads have read them
+    if (grp == 1) {
+      ptx::named_barrier(2, kGroupThreads);
+      stat[t] = w;
+    }
+    ptx::named_barrier(3, 2 * kGroupThreads);
+    if (grp == 0 && t < nk)
+      static_cast<float*>(a.out)[int64_t(kvh) * a.T + tile.row0 + t] = w + stat[2 * BT + t];
+  }
+
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int DQK>
+cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
+  using C = Cfg<DQK>;
+  Params p;
+  p.a = a;
+  p.err = device_error_word();
+  if (!make_map_3d(&p.tq, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, DQK, a.hq, a.T, 64, BT, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map_3d(&p.tk, a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, DQK, a.hkv, a.T, 64, BT, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  if (a.num_packs > 0)
+    for (int m = 0; m < kPieceMaps; ++m)
+      if (!make_map_3d(&p.tqp[m], a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, DQK, a.hq, a.T, 64, 8 * (m + 1),
+                       CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+  auto kernel = a.num_packs > 0 ? key_weights_kernel<DQK, true> : key_weights_kernel<DQK, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
+  if (e != cudaSuccess) return e;
+  const int64_t grid = int64_t(a.num_tiles) * a.hkv;
+  if (grid == 0) return cudaSuccess;
+  kernel<<<unsigned(grid), kThreads, C::kSmem, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool tc_key_weights_supported(int32_t d_qk) { return d_qk == 128 || d_qk == 192; }
+
+cudaError_t launch_tc_key_weights(const AttnArgs& a, cudaStream_t st) {
+  if (a.d_qk == 128) return launch<128>(a, st);
+  if (a.d_qk == 192) return launch<192>(a, st);
+  return cudaErrorInvalidValue;
+}
+
 }  // namespace cpattn
