@@ -11,12 +11,18 @@
 // (TMEM lane = key), so its column sum is a sum over its own registers: no
 // exchange between threads, nothing written but one float a key.
 //
-// Per 128 x 128 step the tensor cores need 512 cycles (128-wide heads), the
-// exponentials 1024 at 16 a cycle.  S^T has four TMEM buffers; two groups of
-// four warps take the steps in turn, so that one group's loads and waits
-// overlap the other's exponentials.
+// Per 128 x 128 step the tensor cores need 512 cycles (128-wide heads), and
+// as much at 32 exponentials a cycle.  K lives in TMEM (a TS MMA): as an SS MMA
+// both operands and the Q copies together asked shared memory for 96 KB a
+// step, 768 cycles (16K tokens, 32 heads: 1.64 ms, against 0.98 ms).  S^T has
+// three TMEM buffers; three groups of four warps take the steps in turn, so
+// that one group's loads and waits overlap the others' exponentials (two
+// groups: 1.10 ms; a part of the exponentials as polynomials on the FMA pipes
+// instead: 1.09 ms and up, the issue slots are needed elsewhere).
 #include <cuda.h>
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "plan_check.cuh"
@@ -35,14 +41,16 @@ constexpr uint32_t kPanel = 128 * 128;  // 128 rows x 64 bf16 columns, 128-byte 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr int kGroupThreads = 128;
-constexpr int kThreads = 2 * kGroupThreads + 64;
-constexpr int kBufs = 4;        // S^T buffers
+constexpr int kGroups = 3;      // group g takes steps g, g + kGroups, ...
+constexpr int kThreads = kGroups * kGroupThreads + 64;
+constexpr int kProducer = 4 * kGroups, kIssuer = kProducer + 1;  // warps
+constexpr int kBufs = 3;        // S^T buffers of 128 TMEM columns; K behind them
 constexpr int kPieceMaps = 15;  // boxes of 8, 16, ..., 120 rows for the pieces of gathered tiles
 
 enum WaitSite : int { kSiteK = 0x61, kSiteQEmpty, kSiteQFull, kSiteSFull, kSiteSFree, kSiteDrain, kSiteAlign };
 
 struct Params {
-  CUtensorMap tq, tk;
+  CUtensorMap tq;
   CUtensorMap tqp[kPieceMaps];  // plans with gathered query tiles only
   AttnArgs a;
   int32_t* err;
@@ -51,15 +59,16 @@ struct Params {
 template <int DQK>
 struct Cfg {
   static constexpr int kPanels = DQK / 64;
-  static constexpr int NS = DQK == 128 ? 5 : 3;  // stages of Q
+  static constexpr int NS = DQK == 128 ? 6 : 4;  // stages of Q
   static constexpr uint32_t kTileBytes = kPanels * kPanel;
-  static constexpr uint32_t offK = 0;
-  static constexpr uint32_t offQ = kTileBytes;
+  static constexpr uint32_t offQ = 0;
   static constexpr uint32_t offStat = offQ + NS * kTileBytes;  // [group][2][BT] floats
-  static constexpr uint32_t offBar = offStat + 2 * 2 * BT * 4;
+  static constexpr uint32_t offBar = offStat + kGroups * 2 * BT * 4;
   static constexpr int kNumBars = 1 + 2 * NS + 2 * kBufs;
   static constexpr uint32_t kSmem = offBar + kNumBars * 8 + 16;
   static_assert(kSmem <= 232448, "shared memory budget");
+  static constexpr uint32_t tK = kBufs * BT;  // TMEM column of K (packed bf16 pairs)
+  static_assert(tK + DQK / 2 <= 512, "TMEM budget");
 };
 
 // -lse * log2e of query column `col` of the step the cursor points at, -inf
@@ -77,6 +86,12 @@ __device__ __forceinline__ float load_stat(const AttnArgs& a, const StepCursor<B
     row = c.row() + col;
   }
   return row < 0 ? -INFINITY : -(a.lse_in[int64_t(c.head()) * a.T + row] * kLog2e);
+}
+
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t y) {
+  float a, b;
+  ptx::f32x2_split(y, a, b);
+  return ptx::f32x2(ptx::ex2(a), ptx::ex2(b));
 }
 
 template <int DQK, bool PACKED>
@@ -109,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::offBar + C::kNumBars * 8 + 4);
 
   if (threadIdx.x == 0) {
-    ptx::mbar_init(bar_k, 1);
+    ptx::mbar_init(bar_k, 4);
     for (int s = 0; s < NS; ++s) {
       ptx::mbar_init(bar_q_full(s), 2);
       ptx::mbar_init(bar_q_empty(s), 1);
@@ -121,29 +136,23 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
     *abort_flag = 0;
     ptx::fence_barrier_init();
   }
-  if (warp == 9) {
+  if (warp == kIssuer) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
     ptx::tmem_relinquish();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == kProducer && lane == 0) {
     ptx::prefetch_tmap(&p.tq);
-    ptx::prefetch_tmap(&p.tk);
   }
-  if (PACKED && warp == 8 && lane >= 1 && lane <= kPieceMaps) ptx::prefetch_tmap(&p.tqp[lane - 1]);
+  if (PACKED && warp == kProducer && lane >= 1 && lane <= kPieceMaps) ptx::prefetch_tmap(&p.tqp[lane - 1]);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const ptx::WaitCtx wctx{abort_flag, p.err, kWaitLimitNs};
 
-  if (warp == 8) {
+  if (warp == kProducer) {
     // ------------------------------------------------------------ producers: lanes 0 and 1 split the panels
     if (lane < 2 && n_steps > 0) {
-      if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(bar_k, C::kTileBytes);
-        for (int c = 0; c < C::kPanels; ++c)
-          ptx::tma_load_3d(sbase + C::offK + c * kPanel, &p.tk, bar_k, c * 64, kvh, tile.row0);
-      }
       const uint32_t bytes = uint32_t((C::kPanels + 1 - lane) / 2) * kPanel;  // panels lane, lane + 2, ...
       StepCursor<BT> cur;
       cur.init(a.ranges, tile.range_begin, tile.range_count, G, kvh, a.hkv, a.gqa_interleaved);
@@ -172,16 +181,14 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
       if (*abort_flag) {
         volatile int no_abort = 0;
         const ptx::WaitCtx drain{&no_abort, nullptr, kWaitLimitNs};
-        if (lane == 0) ptx::mbar_wait(bar_k, 0, kSiteDrain, drain);
         for (int i = max(0, issued - NS); i < issued; ++i)
           ptx::mbar_wait(bar_q_full(i % NS), (i / NS) & 1, kSiteDrain, drain);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == kIssuer) {
     // ------------------------------------------------------------ MMA issuer (whole warp)
     if (n_steps > 0) {
       constexpr uint32_t idS = ptx::idesc_bf16_f32(BT, BT, false, false);
-      const uint64_t dk = ptx::sdesc_sw128(sbase + C::offK, 16, 1024);
       bool ok = ptx::mbar_wait_w(bar_k, 0, kSiteK, wctx);
       int i = 0;
       for (; ok && i < n_steps; ++i) {
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
 #pragma unroll
         for (int kk = 0; kk < DQK / 16; ++kk) {
           const uint32_t o = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
-          ptx::mma_ss_w(tmem + b * BT, dk + o, dq + o, idS, kk > 0);
+          ptx::mma_ts_w(tmem + b * BT, tmem + C::tK + kk * 8, dq + o, idS, kk > 0);
         }
         ptx::mma_commit_w(bar_s_full(b));
         ptx::mma_commit_w(bar_q_empty(st));
@@ -206,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
       }
     }
   } else {
-    // ------------------------------------------------------------ column sums: group g takes steps g, g + 2, ...
+    // ------------------------------------------------------------ column sums
     const int grp = warp >> 2;
     const int t = threadIdx.x & (kGroupThreads - 1);  // key row = TMEM lane; column whose statistic it loads
     const uint32_t tS = tmem + (uint32_t((warp & 3) * 32) << 16);
@@ -214,85 +221,113 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
     const float sl2 = a.scale * kLog2e;
     const uint64_t sl2x2 = ptx::f32x2(sl2, sl2);
     const int kpos = tile.pos0 + t, nk = tile.nrows;
+    if (grp == 0 && n_steps > 0) {
+      // K row -> TMEM (bf16 pairs are the A-operand packing).  Rows past the
+      // tile are the following ones, or zeros past the end: not written out.
+      const int64_t krow = int64_t(tile.row0) + t;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k) + (krow * a.hkv + kvh) * DQK);
+#pragma unroll
+      for (int c = 0; c < DQK / 64; ++c) {
+        uint32_t kr[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 v = krow < a.T ? __ldg(src + 8 * c + i) : make_uint4(0, 0, 0, 0);
+          kr[4 * i] = v.x, kr[4 * i + 1] = v.y, kr[4 * i + 2] = v.z, kr[4 * i + 3] = v.w;
+        }
+        ptx::tmem_st32(tS + C::tK + 32 * c, kr);
+      }
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar_k);
+    }
     StepCursor<BT> cur;
     cur.init(a.ranges, tile.range_begin, tile.range_count, G, kvh, a.hkv, a.gqa_interleaved);
-    if (grp == 1 && n_steps > 1) cur.next();
+    for (int i = 0; i < grp && i < n_steps; ++i) cur.next();
     float next = grp < n_steps ? load_stat<PACKED>(a, cur, t) : 0.f;
     float w = 0.f;
     bool ok = true;
-    for (int i = grp, k = 0; i < n_steps; i += 2, ++k) {
+    for (int i = grp, k = 0; i < n_steps; i += kGroups, ++k) {
       const int nq = cur.n(), qpos0 = cur.pos(), b = i % kBufs;
       const bool packed = PACKED && cur.packed();
       float* st = stat + (k & 1) * BT;
       // (the buffer was last read two of this group's steps ago, before the barrier of the step between)
       st[t] = next;
       ptx::named_barrier(1 + grp, kGroupThreads);
-      cur.next();
-      if (i + 2 < n_steps) {
-        cur.next();
-        next = load_stat<PACKED>(a, cur, t);
-      }
+      for (int x = 0; x < kGroups && i + x + 1 < n_steps; ++x) cur.next();
+      if (i + kGroups < n_steps) next = load_stat<PACKED>(a, cur, t);
       if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_poll(bar_s_full(b), (i / kBufs) & 1, kSiteSFull, wctx));
       if (!ok) continue;  // keep to the group's barriers
       ptx::tc_fence_after();
       const bool causal = a.causal && !packed;
-      // columns [cmin, cmax) are visible; columns without a query have the statistic -inf
+      // columns from cmin on are visible; columns without a query have the statistic -inf
       const bool need_mask = packed || nq < BT || (causal && qpos0 < tile.pos0 + BT - 1);
       const int cmin = causal ? kpos - qpos0 : 0;
       uint64_t s0 = 0, s1 = 0;  // a step's own sums: a long sum's roundings stay small
+      auto sums = [&](auto mask_) {
+        constexpr bool MASK = decltype(mask_)::value;
+        uint32_t x[2][32];  // 32 columns at hand, the next 32 on their way
+        ptx::tmem_ld32(tS + b * BT, x[0]);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t x[2][32];
-        ptx::tmem_ld32(tS + b * BT + 64 * half, x[0]);
-        ptx::tmem_ld32(tS + b * BT + 64 * half + 32, x[1]);
-        ptx::tmem_ld_wait();
-        ptx::reg_fence32(x[0]);
-        ptx::reg_fence32(x[1]);
-        if (half == 1) {
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bar_s_free(b));
-        }
-#pragma unroll
-        for (int j = 0; j < 64; j += 4) {
-          const int col = 64 * half + j;
-          const float4 nl = *reinterpret_cast<const float4*>(st + col);
-          const uint32_t* xs = &x[j >> 5][j & 31];
-          float y[4];
-          ptx::f32x2_split(ptx::fma_f32x2(ptx::f32x2(__uint_as_float(xs[0]), __uint_as_float(xs[1])), sl2x2,
-                                          ptx::f32x2(nl.x, nl.y)), y[0], y[1]);
-          ptx::f32x2_split(ptx::fma_f32x2(ptx::f32x2(__uint_as_float(xs[2]), __uint_as_float(xs[3])), sl2x2,
-                                          ptx::f32x2(nl.z, nl.w)), y[2], y[3]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] = ptx::ex2(y[e]);
-          if (need_mask) {
-            const float n4[4] = {nl.x, nl.y, nl.z, nl.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (col + e < cmin || n4[e] == -INFINITY) y[e] = 0.f;
+        for (int q = 0; q < 4; ++q) {
+          ptx::tmem_ld_wait();
+          ptx::reg_fence32(x[q & 1]);
+          if (q < 3) {
+            ptx::tmem_ld32(tS + b * BT + 32 * (q + 1), x[(q + 1) & 1]);
+          } else {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar_s_free(b));
           }
-          s0 = ptx::add_f32x2(s0, ptx::f32x2(y[0], y[1]));
-          s1 = ptx::add_f32x2(s1, ptx::f32x2(y[2], y[3]));
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const int col = 32 * q + j;
+            const float4 nl = *reinterpret_cast<const float4*>(st + col);
+            const uint32_t* xs = &x[q & 1][j];
+            const uint64_t y0 = ptx::fma_f32x2(ptx::f32x2(__uint_as_float(xs[0]), __uint_as_float(xs[1])), sl2x2,
+                                               ptx::f32x2(nl.x, nl.y));
+            const uint64_t y1 = ptx::fma_f32x2(ptx::f32x2(__uint_as_float(xs[2]), __uint_as_float(xs[3])), sl2x2,
+                                               ptx::f32x2(nl.z, nl.w));
+            uint64_t e0 = exp2_pair(y0);
+            uint64_t e1 = exp2_pair(y1);
+            if (MASK) {
+              float v[4];
+              ptx::f32x2_split(e0, v[0], v[1]);
+              ptx::f32x2_split(e1, v[2], v[3]);
+              const float n4[4] = {nl.x, nl.y, nl.z, nl.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (col + e < cmin || n4[e] == -INFINITY) v[e] = 0.f;
+              e0 = ptx::f32x2(v[0], v[1]);
+              e1 = ptx::f32x2(v[2], v[3]);
+            }
+            s0 = ptx::add_f32x2(s0, e0);
+            s1 = ptx::add_f32x2(s1, e1);
+          }
         }
-      }
-      float e0, e1;
-      ptx::f32x2_split(ptx::add_f32x2(s0, s1), e0, e1);
-      w += e0 + e1;
+      };
+      // warp-uniform: only tiles on the diagonal, at a ragged edge or gathered pay for the tests
+      if (need_mask) sums(std::true_type{});
+      else sums(std::false_type{});
+      float a0, a1;
+      ptx::f32x2_split(ptx::add_f32x2(s0, s1), a0, a1);
+      w += a0 + a1;
     }
-    // the second group's sums through shared memory, in its statistics' place once all its threads have read them
-    if (grp == 1) {
-      ptx::named_barrier(2, kGroupThreads);
-      stat[t] = w;
+    // the other groups' sums through shared memory, in their statistics' places once all of a group's threads have read them
+    ptx::named_barrier(1 + grp, kGroupThreads);
+    if (grp > 0) stat[t] = w;
+    ptx::named_barrier(1 + kGroups, kGroups * kGroupThreads);
+    if (grp == 0 && t < nk) {
+#pragma unroll
+      for (int g = 1; g < kGroups; ++g) w += stat[g * 2 * BT + t];
+      static_cast<float*>(a.out)[int64_t(kvh) * a.T + tile.row0 + t] = w;
     }
-    ptx::named_barrier(3, 2 * kGroupThreads);
-    if (grp == 0 && t < nk)
-      static_cast<float*>(a.out)[int64_t(kvh) * a.T + tile.row0 + t] = w + stat[2 * BT + t];
   }
 
   __syncwarp();
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kIssuer) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
   }
@@ -304,8 +339,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   Params p;
   p.a = a;
   p.err = device_error_word();
-  if (!make_map_3d(&p.tq, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, DQK, a.hq, a.T, 64, BT, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map_3d(&p.tk, a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, DQK, a.hkv, a.T, 64, BT, CU_TENSOR_MAP_SWIZZLE_128B))
+  if (!make_map_3d(&p.tq, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, DQK, a.hq, a.T, 64, BT, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   if (a.num_packs > 0)
     for (int m = 0; m < kPieceMaps; ++m)
