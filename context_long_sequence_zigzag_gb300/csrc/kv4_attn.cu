@@ -59,8 +59,10 @@ struct Cfg {
   static constexpr uint32_t kFragBytes = DQK / 16 * TERMS * NT * 32 * 8;
 };
 
-// The shares: sub-blocks ("units") of all runs end to end, cut over n CTAs.  n
-// is at most the number of units, so that no share is empty.
+// The shares: sub-blocks ("units") of all runs end to end, cut over n CTAs, a
+// unit a warp at least (a CTA with fewer takes as long, and every CTA that a
+// run is cut over leaves a partial to join).  No share is empty.
+__device__ __forceinline__ int share_count(int units, int ctas, int warps) { return min(ctas, (units + warps - 1) / warps); }
 __host__ __device__ __forceinline__ int64_t share_begin(int64_t units, int n, int c) { return int64_t(c) * units / n; }
 __device__ __forceinline__ int share_of(int64_t units, int n, int64_t u) { return int(((u + 1) * n - 1) / units); }
 
@@ -68,9 +70,11 @@ __device__ __forceinline__ int share_of(int64_t units, int n, int64_t u) { retur
 __host__ __device__ constexpr int part_floats(int cols, int dv) { return 2 * cols + cols * dv; }
 
 struct Grid {
-  int ctas;          // shares
+  int ctas;          // shares at most
+  int warps;         // of a CTA of the first kernel
   int rows_per_tile;  // rows of a row tile (at most COLS)
   int stages;
+  uint32_t off_join;  // the join's weights behind its scan
   uint32_t off_base, off_frag, off_sum, off_stat, off_merge, off_ring;
   float* part;   // [ctas][2][part_floats]
   float* score;  // [units][rows_per_tile][32], log2 units
@@ -198,7 +202,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
   const uint32_t sbase = ptx::smem_u32(smem);
   int32_t* base = reinterpret_cast<int32_t*>(smem + gr.off_base);
   float* qsum_s = reinterpret_cast<float*>(smem + gr.off_sum);      // [GK][COLS]
-  float* stat_s = reinterpret_cast<float*>(smem + gr.off_stat);     // [2][NW][COLS]: references, sums
+  // [NW][COLS] of references, of sums and of weights, [COLS] of largest references
+  float* stat_s = reinterpret_cast<float*>(smem + gr.off_stat);
   float* merge_s = reinterpret_cast<float*>(smem + gr.off_merge);   // [NW][rows_per_tile][DV]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
@@ -212,7 +217,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
   if (tid == 0) s_abort = 0;
   scan_lengths<C::THREADS>(a, per, base, s_scan);
   const int units = base[a.c.num_seqs];
-  const int shares = min(gr.ctas, units);
+  const int shares = share_count(units, gr.ctas, NW);
   if (int(blockIdx.x) >= shares) return;
   const int u0 = int(share_begin(units, shares, blockIdx.x)), u1 = int(share_begin(units, shares, blockIdx.x + 1));
   const ptx::WaitCtx wctx{&s_abort, a.c.err, kWaitLimitNs};
@@ -244,6 +249,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
     load_unit += NW;
   };
   for (int s = 0; s < gr.stages; ++s) load_next();
+  ptx::grid_launch_dependents();
 
   const float sl2 = a.c.scale * kLog2e;
   int done = 0, b = 0;
@@ -571,19 +577,31 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
         }
       }
     __syncthreads();
+    // what every warp's part weighs: 2^(its reference - the largest), 0 where it saw nothing (or has no unit here)
+    if (tid < NW * C::COLS) {
+      const int n = tid % C::COLS;
+      float m = kNoRef;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) m = fmaxf(m, stat_s[w * C::COLS + n]);
+      const float l = stat_s[NW * C::COLS + tid];
+      const float k = l == 0.f ? 0.f : ptx::ex2(stat_s[tid] - m);
+      stat_s[2 * NW * C::COLS + tid] = k;
+      stat_s[NW * C::COLS + tid] = l == 0.f ? 0.f : k * l;
+      if (tid < C::COLS) stat_s[3 * NW * C::COLS + n] = m;
+    }
+    __syncthreads();
     const bool whole = seg0 == run0 && seg1 == run0 + per_run;
     float* part = gr.part + (int64_t(blockIdx.x) * 2 + (seg0 == run0)) * part_floats(C::COLS, DV);
     for (int e = tid; e < rows * DV; e += C::THREADS) {
       const int n = e / DV, d = e - n * DV;
-      float m = kNoRef, l = 0.f, x = 0.f;
-      for (int w = 0; w < NW; ++w) m = fmaxf(m, stat_s[w * C::COLS + n]);
+      float l = 0.f, x = 0.f;
+#pragma unroll
       for (int w = 0; w < NW; ++w) {
-        const float mw = stat_s[w * C::COLS + n], lw = stat_s[(NW + w) * C::COLS + n];
-        if (lw == 0.f) continue;  // saw nothing (or has no unit here)
-        const float k = ptx::ex2(mw - m);
-        l += k * lw;
-        x += k * merge_s[(w * gr.rows_per_tile + n) * DV + d];
+        const float k = stat_s[(2 * NW + w) * C::COLS + n];
+        l += stat_s[(NW + w) * C::COLS + n];
+        if (k != 0.f) x += k * merge_s[(w * gr.rows_per_tile + n) * DV + d];
       }
+      const float m = stat_s[3 * NW * C::COLS + n];
       if (whole) {
         int t, head;
         const int64_t row = row_index(a, b, h, n0 + n, &t, &head);
@@ -622,13 +640,11 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnArg
   int32_t* base = reinterpret_cast<int32_t*>(smem);
   const int row_tiles = a.row_tiles, per = a.c.hkv * row_tiles;
   scan_lengths<kJoinThreads>(a, per, base, s_scan);
-  const int units = base[a.c.num_seqs], shares = min(gr.ctas, units);
+  const int units = base[a.c.num_seqs], shares = share_count(units, gr.ctas, gr.warps);
   ptx::grid_wait_previous();
   constexpr int kPart = part_floats(COLS, DV);
-  // partials of the run that starts at unit run0: shares c0 .. c1, slot 0 in all but its first
-  auto part_of = [&](int sh, int run0) {
-    return gr.part + (int64_t(sh) * 2 + (share_begin(units, shares, sh) <= run0)) * kPart;
-  };
+  // partial i of a run cut over shares c0, c0 + 1, ...: slot 1 of the share it starts in, slot 0 of the others
+  auto part_of = [&](int c0, int i) { return gr.part + (int64_t(c0 + i) * 2 + (i == 0)) * kPart; };
   if (int(blockIdx.x) < runs) {
     const int b = int(blockIdx.x) / per, run = int(blockIdx.x) - b * per;
     const int per_run = (base[b + 1] - base[b]) / per, run0 = base[b] + run * per_run;
@@ -640,25 +656,44 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnArg
       c1 = share_of(units, shares, run0 + per_run - 1);
       if (c0 == c1) return;
     }
+    // what every partial weighs, as in the first kernel
+    const int parts = per_run > 0 ? c1 - c0 + 1 : 0;
+    float* k_s = reinterpret_cast<float*>(smem + gr.off_join);  // [parts][rows]: references, then weights
+    float* l_s = k_s + gr.ctas * gr.rows_per_tile;              // [parts][rows]: sums
+    for (int e = threadIdx.x; e < parts * rows; e += kJoinThreads) {
+      const float* p = part_of(c0, e / rows) + e % rows;
+      k_s[e] = p[0];
+      l_s[e] = p[COLS];
+    }
+    __syncthreads();
+    float* m_s = l_s + gr.ctas * gr.rows_per_tile;  // [rows]
+    if (threadIdx.x < rows) {
+      float m = kNoRef;
+      for (int i = 0; i < parts; ++i) m = fmaxf(m, k_s[i * rows + threadIdx.x]);
+      m_s[threadIdx.x] = m;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < parts * rows; e += kJoinThreads) {
+      const float k = l_s[e] == 0.f ? 0.f : ptx::ex2(k_s[e] - m_s[e % rows]);
+      k_s[e] = k;
+      l_s[e] = l_s[e] == 0.f ? 0.f : k * l_s[e];
+    }
+    __syncthreads();
     for (int e = threadIdx.x; e < rows * DV; e += kJoinThreads) {
       const int n = e / DV, d = e - n * DV;
-      float m = kNoRef, l = 0.f, x = 0.f;
-      if (per_run > 0) {
-        for (int sh = c0; sh <= c1; ++sh) m = fmaxf(m, part_of(sh, run0)[n]);
-        for (int sh = c0; sh <= c1; ++sh) {
-          const float* p = part_of(sh, run0);
-          if (p[COLS + n] == 0.f) continue;
-          const float k = ptx::ex2(p[n] - m);
-          l += k * p[COLS + n];
-          x += k * p[2 * COLS + e];
-        }
+      float l = 0.f, x = 0.f;
+#pragma unroll 8
+      for (int i = 0; i < parts; ++i) {
+        // (a partial that saw nothing is all zeros)
+        l += l_s[i * rows + n];
+        x += k_s[i * rows + n] * part_of(c0, i)[2 * COLS + e];
       }
       int t, head;
       const int64_t row = row_index(a, b, h, n0 + n, &t, &head);
       store_o(a, row * DV + d, l == 0.f ? 0.f : x / l);
       if (d == 0)
         a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] =
-            l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            l == 0.f ? -INFINITY : (m_s[n] + log2f(l)) * kLn2;
     }
     return;
   }
@@ -693,9 +728,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnArg
             ls = a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] * kLog2e;
           } else {
             float m = kNoRef, l = 0.f;
-            for (int sh = c0; sh <= c1; ++sh) m = fmaxf(m, part_of(sh, run0)[lane]);
-            for (int sh = c0; sh <= c1; ++sh) {
-              const float* p = part_of(sh, run0);
+            for (int k = 0; k <= c1 - c0; ++k) m = fmaxf(m, part_of(c0, k)[lane]);
+            for (int k = 0; k <= c1 - c0; ++k) {
+              const float* p = part_of(c0, k);
               l += ptx::ex2(p[lane] - m) * p[COLS + lane];
             }
             ls = l == 0.f ? -INFINITY : m + log2f(l);
@@ -747,7 +782,7 @@ cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
   gr.off_sum = off;
   off += C::GK * C::COLS * 4;
   gr.off_stat = off;
-  off += 2 * C::NW * C::COLS * 4;
+  off += (3 * C::NW + 1) * C::COLS * 4;
   gr.off_merge = off;
   off = up(off + C::NW * gr.rows_per_tile * C::DV * 4, 128);
   gr.off_ring = off;
@@ -755,6 +790,7 @@ cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
   gr.stages = int(std::min<uint32_t>(4, (kMost - off) / (C::NW * f.sub())));
   if (off > kMost || gr.stages < 1) return cudaErrorInvalidValue;
   off += gr.stages * C::NW * f.sub();
+  gr.warps = C::NW;
   auto kernel = kv4_attn_kernel<C, E>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(off));
   if (e != cudaSuccess) return e;
@@ -762,8 +798,21 @@ cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int runs = a.c.num_seqs * a.c.hkv * a.row_tiles;
-  kv4_join_kernel<C::COLS, C::DV><<<unsigned(runs + (a.accumulate ? 2 * gr.ctas : 0)), kJoinThreads,
-                                    4 * (a.c.num_seqs + 1), st>>>(a, gr, runs);
+  gr.off_join = up(4 * (a.c.num_seqs + 1), 16);
+  const uint32_t join_smem = gr.off_join + (2 * gr.ctas + 1) * gr.rows_per_tile * 4;  // at most 36 KB
+  // the second kernel's launch overlaps the first: it waits on the device
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(runs + (a.accumulate ? 2 * gr.ctas : 0)));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = join_smem;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kv4_join_kernel<C::COLS, C::DV>, a, gr, runs);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
