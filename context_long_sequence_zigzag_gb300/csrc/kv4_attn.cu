@@ -48,15 +48,13 @@ constexpr float kNoRef = -1e30f;   // a row that has seen nothing
 constexpr float kSlack = 10.f;     // how far (log2) an element may exceed the reference
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
-template <int DQK_, int DV_, int NT_, int TERMS_>
+template <int DQK_, int DV_, int NT_, int TERMS_, int NW_>
 struct Cfg {
-  static constexpr int DQK = DQK_, DV = DV_, NT = NT_, TERMS = TERMS_;
+  static constexpr int DQK = DQK_, DV = DV_, NT = NT_, TERMS = TERMS_, NW = NW_;
   static constexpr int GK = DQK / 64, GV = DV / 64;
   static constexpr int KW = DQK / 32;  // words of a K row a lane unpacks
   static constexpr int COLS = 8 * NT;
-  static constexpr int NW = NT == 1 && TERMS == 1 && DQK < 192 ? 16 : 8;
   static constexpr int THREADS = 32 * NW;
-  static constexpr uint32_t kFragBytes = DQK / 16 * TERMS * NT * 32 * 8;
 };
 
 // The shares: sub-blocks ("units") of all runs end to end, cut over n CTAs, a
@@ -70,12 +68,12 @@ __device__ __forceinline__ int share_of(int64_t units, int n, int64_t u) { retur
 __host__ __device__ constexpr int part_floats(int cols, int dv) { return 2 * cols + cols * dv; }
 
 struct Grid {
-  int ctas;          // shares at most
-  int warps;         // of a CTA of the first kernel
+  int ctas;           // shares at most
+  int warps;          // of a CTA of the first kernel
   int rows_per_tile;  // rows of a row tile (at most COLS)
   int stages;
+  uint32_t off_base, off_frag, off_stat, off_stash, off_ring;
   uint32_t off_join;  // the join's weights behind its scan
-  uint32_t off_base, off_frag, off_sum, off_stat, off_merge, off_ring;
   float* part;   // [ctas][2][part_floats]
   float* score;  // [units][rows_per_tile][32], log2 units
 };
@@ -174,9 +172,22 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t (&t)[TERMS
   }
 }
 
-__device__ __forceinline__ float q_at(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float q_at(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void load_q8(const float* p, float (&x)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load_q8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  x[0] = bf_lo(a.x), x[1] = bf_hi(a.x), x[2] = bf_lo(a.y), x[3] = bf_hi(a.y);
+  x[4] = bf_lo(a.z), x[5] = bf_hi(a.z), x[6] = bf_lo(a.w), x[7] = bf_hi(a.w);
+}
 
+__device__ __forceinline__ void store_o4(const Kv4AttnArgs& a, int64_t i, float4 x) {
+  if (a.o_f32) *reinterpret_cast<float4*>(static_cast<float*>(a.o) + i) = x;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + i) =
+        make_uint2(ptx::pack_bf16(x.x, x.y), ptx::pack_bf16(x.z, x.w));
+}
 __device__ __forceinline__ void store_o(const Kv4AttnArgs& a, int64_t i, float x) {
   if (a.o_f32) static_cast<float*>(a.o)[i] = x;
   else static_cast<__nv_bfloat16*>(a.o)[i] = __float2bfloat16_rn(x);
@@ -191,6 +202,26 @@ __device__ __forceinline__ int64_t row_index(const Kv4AttnArgs& a, int b, int h,
   return (int64_t(b) * a.n_q + *t) * a.c.hq + *head;
 }
 
+// Walks units: sub-block i of run `run` of sequence b.
+struct UnitCursor {
+  int b, run, i, per_run;
+  __device__ void seek(const int32_t* base, int n, int per, int u) {
+    b = seq_of_unit(base, n, 0, u);
+    per_run = (base[b + 1] - base[b]) / per;
+    run = (u - base[b]) / per_run;
+    i = u - base[b] - run * per_run;
+  }
+  __device__ void next(const int32_t* base, int n, int per) {
+    if (++i < per_run) return;
+    i = 0;
+    if (++run < per) return;
+    run = 0;
+    do ++b;
+    while (b < n && base[b + 1] == base[b]);
+    per_run = b < n ? (base[b + 1] - base[b]) / per : 1;
+  }
+};
+
 template <typename C, typename E>
 __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnArgs a, const Grid gr) {
   constexpr int NT = C::NT, GK = C::GK, GV = C::GV, NW = C::NW, DQK = C::DQK, DV = C::DV, TERMS = C::TERMS;
@@ -199,12 +230,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
   __shared__ __align__(8) uint64_t bars[NW * 4];
   __shared__ int s_abort;
   __shared__ int32_t s_scan[NW];
+  __shared__ int32_t s_run[2 * NW];  // run of warp w's first partial (2w) and of its last (2w + 1), or -1
   const uint32_t sbase = ptx::smem_u32(smem);
   int32_t* base = reinterpret_cast<int32_t*>(smem + gr.off_base);
-  float* qsum_s = reinterpret_cast<float*>(smem + gr.off_sum);      // [GK][COLS]
-  // [NW][COLS] of references, of sums and of weights, [COLS] of largest references
-  float* stat_s = reinterpret_cast<float*>(smem + gr.off_stat);
-  float* merge_s = reinterpret_cast<float*>(smem + gr.off_merge);   // [NW][rows_per_tile][DV]
+  float* stat_s = reinterpret_cast<float*>(smem + gr.off_stat);    // [2 NW][2][COLS]: the partials' references and sums
+  float* stash_s = reinterpret_cast<float*>(smem + gr.off_stash);  // [NW][rows_per_tile][DV]: the first partials
+  float* last_s = reinterpret_cast<float*>(smem + gr.off_ring);    // the last ones, once no warp uses its ring
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
   const int row_tiles = a.row_tiles, per = a.c.hkv * row_tiles;
@@ -213,6 +244,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
   if (lane == 0) {
     for (int s = 0; s < gr.stages; ++s) ptx::mbar_init(bar0 + 8 * s, 1);
     ptx::fence_barrier_init();
+    s_run[2 * warp] = s_run[2 * warp + 1] = -1;
   }
   if (tid == 0) s_abort = 0;
   scan_lengths<C::THREADS>(a, per, base, s_scan);
@@ -220,100 +252,108 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
   const int shares = share_count(units, gr.ctas, NW);
   if (int(blockIdx.x) >= shares) return;
   const int u0 = int(share_begin(units, shares, blockIdx.x)), u1 = int(share_begin(units, shares, blockIdx.x + 1));
+  // this warp's units
+  const int w0 = u0 + (u1 - u0) * warp / NW, w1 = u0 + (u1 - u0) * (warp + 1) / NW;
   const ptx::WaitCtx wctx{&s_abort, a.c.err, kWaitLimitNs};
 
-  // ---- this warp's copies: unit u0 + warp, then every NW-th, `stages` ahead
-  int load_unit = u0 + warp, load_seq = 0, loaded = 0;
+  // ---- its copies, `stages` ahead
+  UnitCursor cur, ahead;
+  int loaded = 0;
   uint32_t absent = 0;  // bit s: the page of stage s's unit is not in the pool
+  int next_page = 0;
+  auto look_up = [&]() {
+    if (w0 + loaded >= w1) return;
+    const int page = __ldg(a.c.table + int64_t(ahead.b) * a.c.max_pages + ahead.i / (CP_KV4_PAGE / kKv4Sub));
+    next_page = page < a.c.num_pages ? page : -1;
+  };
   auto load_next = [&]() {
-    if (load_unit >= u1) return;
-    load_seq = seq_of_unit(base, a.c.num_seqs, load_seq, load_unit);
-    const int at = load_unit - base[load_seq];
-    const int per_run = (base[load_seq + 1] - base[load_seq]) / per;
-    const int run = at / per_run, i = at - run * per_run;
-    const int page = kv4_page(a.c, load_seq, i / (CP_KV4_PAGE / kKv4Sub));
+    if (w0 + loaded >= w1) return;
+    const int page = next_page;  // looked up while the unit before was on its way
+    if (page < 0) kv4_error(a.c, kKv4Page);
     const int s = loaded % gr.stages;
     absent = page < 0 ? absent | (1u << s) : absent & ~(1u << s);
     if (lane == 0) {
       if (page >= 0) {
         ptx::mbar_arrive_expect_tx(bar0 + 8 * s, uint32_t(f.sub()));
         ptx::bulk_load(ring + uint32_t(s) * f.sub(),
-                       a.c.pages + (int64_t(page) * a.c.hkv + run / row_tiles) * f.block() +
-                           i % (CP_KV4_PAGE / kKv4Sub) * f.sub(),
+                       a.c.pages + (int64_t(page) * a.c.hkv + ahead.run / row_tiles) * f.block() +
+                           ahead.i % (CP_KV4_PAGE / kKv4Sub) * f.sub(),
                        uint32_t(f.sub()), bar0 + 8 * s);
       } else {
         ptx::mbar_arrive(bar0 + 8 * s);
       }
     }
     ++loaded;
-    load_unit += NW;
+    ahead.next(base, a.c.num_seqs, per);
+    look_up();
   };
-  for (int s = 0; s < gr.stages; ++s) load_next();
+  if (w0 < w1) {
+    cur.seek(base, a.c.num_seqs, per, w0);
+    ahead = cur;
+    look_up();
+    for (int s = 0; s < gr.stages; ++s) load_next();
+  }
   ptx::grid_launch_dependents();
 
   const float sl2 = a.c.scale * kLog2e;
-  int done = 0, b = 0;
-  bool ok = true;
-  for (int seg0 = u0; seg0 < u1;) {
-    // ---- the run that holds unit seg0, as far as this share goes
-    b = seq_of_unit(base, a.c.num_seqs, b, seg0);
-    const int per_run = (base[b + 1] - base[b]) / per;
-    const int run = (seg0 - base[b]) / per_run, run0 = base[b] + run * per_run;
-    const int seg1 = min(u1, run0 + per_run);
+  const int frag_rows = gr.rows_per_tile;
+  const uint32_t frag0 = sbase + gr.off_frag + uint32_t(warp) * (DQK / 16 * TERMS * 32) * frag_rows;
+  float O[GV][4][NT][4], osix[GV][NT][4], ooff[GV][NT][2], ref[NT][2], sum[NT][2];
+  int done = 0;
+  bool ok = true, last = false;  // last: the registers hold a partial that the next warp's units continue
+  for (int u = w0; u < w1 && ok && !last;) {
+    // ---- a run, as far as this warp's units go
+    const int b = cur.b, run = cur.run, run0 = u - cur.i, per_run = cur.per_run;
+    const int seg1 = min(w1, run0 + per_run);
     const int h = run / row_tiles, n0 = (run - h * row_tiles) * gr.rows_per_tile;
     const int rows = min(gr.rows_per_tile, a.rows - n0);
     const int len = min(kv4_length(a.c, a.lengths, b), per_run * kKv4Sub);
-    // ---- its queries as B fragments (kstep 2j + p: channels 8w + 2p, 8w + 2p + 4 and the next two, w = 4j + lane % 4)
-    for (int e = tid; e < DQK / 16 * NT * 32; e += C::THREADS) {
-      const int ln = e & 31, nt = (e >> 5) % NT, ks = (e >> 5) / NT;
-      const int n = nt * 8 + (ln >> 2), ch = 8 * (4 * (ks >> 1) + (ln & 3)) + 2 * (ks & 1);
-      float x[4] = {};
-      if (n < rows) {
-        int t, head;
-        const E* q = static_cast<const E*>(a.q) + row_index(a, b, h, n0 + n, &t, &head) * DQK + ch;
-        x[0] = q_at(q), x[1] = q_at(q + 4), x[2] = q_at(q + 1), x[3] = q_at(q + 5);
-      }
-      uint32_t f0[TERMS], f1[TERMS];
-      split_pair<TERMS>(x[0], x[1], f0);
-      split_pair<TERMS>(x[2], x[3], f1);
-#pragma unroll
-      for (int m = 0; m < TERMS; ++m)
-        reinterpret_cast<uint2*>(smem + gr.off_frag)[((ks * TERMS + m) * NT + nt) * 32 + ln] = make_uint2(f0[m], f1[m]);
-    }
-    for (int e = tid; e < C::COLS * GK * 8; e += C::THREADS) {  // sums of 64 channels, 8 lanes each
-      const int part = e & 7, n = (e >> 3) % C::COLS, g = (e >> 3) / C::COLS;
-      float x = 0.f;
-      if (n < rows) {
-        int t, head;
-        const E* q = static_cast<const E*>(a.q) + row_index(a, b, h, n0 + n, &t, &head) * DQK + 64 * g + 8 * part;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x += q_at(q + i);
-      }
-      const uint32_t lanes = 0xffu << (lane & 24);
-      x += __shfl_xor_sync(lanes, x, 1);
-      x += __shfl_xor_sync(lanes, x, 2);
-      x += __shfl_xor_sync(lanes, x, 4);
-      if (part == 0) qsum_s[g * C::COLS + n] = x;
-    }
-    __syncthreads();
+    // ---- its queries as B fragments (kstep 2j + p: channels 8w + 2p, 8w + 2p + 4 and the next two, w = 4j + c), and
+    // the sums of their groups.  Columns past the rows repeat rows; nothing of them is written out.
     float qsum[GK][NT][2];
     int lim[NT][2];
+    uint32_t frag[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      const int n = (nt * 8 + r) % rows;
+      frag[nt] = frag0 + uint32_t(n * 4 + c) * 8;
+      int t, head;
+      const E* q = static_cast<const E*>(a.q) + row_index(a, b, h, n0 + n, &t, &head) * DQK + 8 * c;
+      float gs[GK];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int n = nt * 8 + 2 * c + e;
+      for (int j = 0; j < DQK / 32; ++j) {
+        float x[8];
+        load_q8(q + 32 * j, x);
+        if (j % 2 == 0) gs[j / 2] = 0.f;
+        gs[j / 2] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+        uint32_t f0[2][TERMS], f1[2][TERMS];
 #pragma unroll
-        for (int g = 0; g < GK; ++g) qsum[g][nt][e] = qsum_s[g * C::COLS + n];
-        int t, head;
-        row_index(a, b, h, n0 + min(n, rows - 1), &t, &head);
-        lim[nt][e] = len - (a.n_q - 1 - t);
+        for (int p = 0; p < 2; ++p) {
+          split_pair<TERMS>(x[2 * p], x[2 * p + 4], f0[p]);
+          split_pair<TERMS>(x[2 * p + 1], x[2 * p + 5], f1[p]);
+#pragma unroll
+          for (int m = 0; m < TERMS; ++m)
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(frag[nt] + ((2 * j + p) * TERMS + m) * (frag_rows * 32)),
+                         "r"(f0[p][m]), "r"(f1[p][m])
+                         : "memory");
+        }
       }
+#pragma unroll
+      for (int g = 0; g < GK; ++g) {
+        gs[g] += __shfl_xor_sync(0xffffffffu, gs[g], 1);
+        gs[g] += __shfl_xor_sync(0xffffffffu, gs[g], 2);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) qsum[g][nt][e] = __shfl_sync(0xffffffffu, gs[g], (2 * c + e) * 4);
+      }
+      const int own = len - (a.n_q - 1 - t);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) lim[nt][e] = __shfl_sync(0xffffffffu, own, (2 * c + e) * 4);
+    }
     int t_first, head_;
     row_index(a, b, h, n0, &t_first, &head_);
     const int lim_min = len - (a.n_q - 1 - t_first);
+    __syncwarp();
 
-    float O[GV][4][NT][4], osix[GV][NT][4], ooff[GV][NT][2], ref[NT][2], sum[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -330,12 +370,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
       sum[nt][0] = sum[nt][1] = 0.f;
     }
 
-    bool worked = false;
-    for (int u = u0 + warp + done * NW; u < seg1; u += NW) {
+    for (; u < seg1; ++u) {
       const int s = done % gr.stages;
       if (ok) ok = ptx::mbar_wait_w(bar0 + 8 * s, (done / gr.stages) & 1, kKv4Wait, wctx);
       if (!ok) break;
-      worked = true;
       const uint32_t st = ring + uint32_t(s) * f.sub();
       const bool gone = (absent >> s) & 1;
       const int j0 = (u - run0) * kKv4Sub;
@@ -385,7 +423,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                   uint32_t q2[2];
-                  lds_words<2>(sbase + gr.off_frag + ((((2 * j + p) * TERMS + m) * NT + nt) * 32 + lane) * 8, q2);
+                  lds_words<2>(frag[nt] + ((2 * j + p) * TERMS + m) * (frag_rows * 32), q2);
 #pragma unroll
                   for (int mt = 0; mt < 2; ++mt) ptx::mma_16816(acc[mt][nt], A[mt], q2[0], q2[1]);
                 }
@@ -545,86 +583,125 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
       __syncwarp();  // the stage has been read
       ++done;
       load_next();
+      cur.next(base, a.c.num_seqs, per);
     }
 
-    // ---- end of the run in this share: the warps' results joined in shared memory
+    // ---- the warp's sums
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], o);
 #pragma unroll
           for (int g = 0; g < GV; ++g) ooff[g][nt][e] += __shfl_xor_sync(0xffffffffu, ooff[g][nt][e], o);
         }
-        const int n = nt * 8 + 2 * c + e;
-        if (r == 0) {
-          stat_s[warp * C::COLS + n] = ref[nt][e];
-          stat_s[(NW + warp) * C::COLS + n] = sum[nt][e];
-        }
-        if (worked && n < rows) {
-          float* to = merge_s + (warp * gr.rows_per_tile + n) * DV + 8 * r;
+    const bool starts = run0 >= w0, ends = run0 + per_run <= w1;
+    if (starts && ends) {  // whole: done
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int n = nt * 8 + 2 * c + e;
+          if (n >= rows) continue;
+          int t, head;
+          const int64_t row = row_index(a, b, h, n0 + n, &t, &head);
+          const float l = sum[nt][e], inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
           for (int g = 0; g < GV; ++g) {
             const float add = osix[g][nt][e] + ooff[g][nt][e];
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-              *reinterpret_cast<float4*>(to + 64 * g + 4 * x) =
+              store_o4(a, row * DV + 64 * g + 8 * r + 4 * x,
+                       make_float4((O[g][0][nt][e + 2 * x] + add) * inv, (O[g][1][nt][e + 2 * x] + add) * inv,
+                                   (O[g][2][nt][e + 2 * x] + add) * inv, (O[g][3][nt][e + 2 * x] + add) * inv));
+          }
+          if (r == 0)
+            a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] =
+                l == 0.f ? -INFINITY : (ref[nt][e] + log2f(l)) * kLn2;
+        }
+    } else {
+      last = !ends;
+      if (last) __syncthreads();  // no ring is used any more (the other warps: below)
+      float* part = (last ? last_s : stash_s) + warp * gr.rows_per_tile * DV;
+      float* stat = stat_s + (2 * warp + last) * 2 * C::COLS;
+      if (lane == 0) s_run[2 * warp + last] = b * per + run;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int n = nt * 8 + 2 * c + e;
+          if (n >= rows) continue;
+          if (r == 0) {
+            stat[n] = ref[nt][e];
+            stat[C::COLS + n] = sum[nt][e];
+          }
+#pragma unroll
+          for (int g = 0; g < GV; ++g) {
+            const float add = osix[g][nt][e] + ooff[g][nt][e];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              *reinterpret_cast<float4*>(part + n * DV + 64 * g + 8 * r + 4 * x) =
                   make_float4(O[g][0][nt][e + 2 * x] + add, O[g][1][nt][e + 2 * x] + add, O[g][2][nt][e + 2 * x] + add,
                               O[g][3][nt][e + 2 * x] + add);
           }
         }
-      }
-    __syncthreads();
-    // what every warp's part weighs: 2^(its reference - the largest), 0 where it saw nothing (or has no unit here)
-    if (tid < NW * C::COLS) {
-      const int n = tid % C::COLS;
-      float m = kNoRef;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) m = fmaxf(m, stat_s[w * C::COLS + n]);
-      const float l = stat_s[NW * C::COLS + tid];
-      const float k = l == 0.f ? 0.f : ptx::ex2(stat_s[tid] - m);
-      stat_s[2 * NW * C::COLS + tid] = k;
-      stat_s[NW * C::COLS + tid] = l == 0.f ? 0.f : k * l;
-      if (tid < C::COLS) stat_s[3 * NW * C::COLS + n] = m;
     }
-    __syncthreads();
-    const bool whole = seg0 == run0 && seg1 == run0 + per_run;
-    float* part = gr.part + (int64_t(blockIdx.x) * 2 + (seg0 == run0)) * part_floats(C::COLS, DV);
-    for (int e = tid; e < rows * DV; e += C::THREADS) {
-      const int n = e / DV, d = e - n * DV;
-      float l = 0.f, x = 0.f;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const float k = stat_s[(2 * NW + w) * C::COLS + n];
-        l += stat_s[(NW + w) * C::COLS + n];
-        if (k != 0.f) x += k * merge_s[(w * gr.rows_per_tile + n) * DV + d];
-      }
-      const float m = stat_s[3 * NW * C::COLS + n];
-      if (whole) {
-        int t, head;
-        const int64_t row = row_index(a, b, h, n0 + n, &t, &head);
-        store_o(a, row * DV + d, l == 0.f ? 0.f : x / l);
-        if (d == 0)
-          a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] =
-              l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-      } else {
-        part[2 * C::COLS + e] = x;
-        if (d == 0) {
-          part[n] = m;
-          part[C::COLS + n] = l;
-        }
-      }
-    }
-    __syncthreads();
-    seg0 = seg1;
   }
-  if (!ok) {  // copies still in flight land before the CTA goes
+  if (!ok) {  // copies still in flight land before the rings are used for anything else
     volatile int no_abort = 0;
     const ptx::WaitCtx drain{&no_abort, nullptr, kWaitLimitNs};
     for (int i = max(done, loaded - gr.stages); i < loaded; ++i)
       ptx::mbar_wait_w(bar0 + 8 * (i % gr.stages), (i / gr.stages) & 1, kKv4Wait, drain);
+  }
+  if (!last) __syncthreads();
+  __syncthreads();
+
+  // ---- runs cut over warps: their partials, in order, joined by the whole CTA
+  constexpr int kSlots = 2 * NW;
+  for (int s0 = 0; s0 < kSlots;) {
+    const int id = s_run[s0];
+    int s1 = s0 + 1;
+    if (id >= 0)
+      while (s1 < kSlots && (s_run[s1] < 0 || s_run[s1] == id)) ++s1;
+    if (id >= 0) {
+      const int b = id / per, run = id - b * per;
+      const int per_run = (base[b + 1] - base[b]) / per, run0 = base[b] + run * per_run;
+      const int h = run / row_tiles, n0 = (run - h * row_tiles) * gr.rows_per_tile;
+      const int rows = min(gr.rows_per_tile, a.rows - n0);
+      const bool whole = run0 >= u0 && run0 + per_run <= u1;
+      float* part = gr.part + (int64_t(blockIdx.x) * 2 + (run0 >= u0)) * part_floats(C::COLS, DV);
+      for (int e = tid; e < rows * DV; e += C::THREADS) {
+        const int n = e / DV, d = e - n * DV;
+        float m = kNoRef, l = 0.f, x = 0.f;
+        for (int s = s0; s < s1; ++s)
+          if (s_run[s] >= 0) m = fmaxf(m, stat_s[s * 2 * C::COLS + n]);
+        for (int s = s0; s < s1; ++s) {
+          if (s_run[s] < 0) continue;
+          const float* st = stat_s + s * 2 * C::COLS;
+          if (st[C::COLS + n] == 0.f) continue;  // saw nothing
+          const float k = ptx::ex2(st[n] - m);
+          l += k * st[C::COLS + n];
+          x += k * ((s & 1) ? last_s : stash_s)[(s >> 1) * gr.rows_per_tile * DV + e];
+        }
+        if (whole) {
+          int t, head;
+          const int64_t row = row_index(a, b, h, n0 + n, &t, &head);
+          store_o(a, row * DV + d, l == 0.f ? 0.f : x / l);
+          if (d == 0)
+            a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] =
+                l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        } else {
+          part[2 * C::COLS + e] = x;
+          if (d == 0) {
+            part[n] = m;
+            part[C::COLS + n] = l;
+          }
+        }
+      }
+    }
+    s0 = s1;
   }
 }
 
@@ -778,18 +855,19 @@ cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
   gr.off_base = off;
   off = up(off + 4 * (a.c.num_seqs + 1), 128);
   gr.off_frag = off;
-  off += C::kFragBytes;
-  gr.off_sum = off;
-  off += C::GK * C::COLS * 4;
+  off += C::NW * (C::DQK / 16 * C::TERMS * 32) * gr.rows_per_tile;
   gr.off_stat = off;
-  off += (3 * C::NW + 1) * C::COLS * 4;
-  gr.off_merge = off;
-  off = up(off + C::NW * gr.rows_per_tile * C::DV * 4, 128);
+  off += 2 * C::NW * 2 * C::COLS * 4;
+  gr.off_stash = off;
+  const uint32_t partials = C::NW * gr.rows_per_tile * C::DV * 4;
+  off = up(off + partials, 128);
   gr.off_ring = off;
-  constexpr uint32_t kMost = 231000;
+  constexpr uint32_t kMost = 230000;  // 227 KB less the static arrays
+  if (off > kMost) return cudaErrorInvalidValue;
   gr.stages = int(std::min<uint32_t>(4, (kMost - off) / (C::NW * f.sub())));
-  if (off > kMost || gr.stages < 1) return cudaErrorInvalidValue;
   off += gr.stages * C::NW * f.sub();
+  // the rings hold the last partials in the end
+  if (gr.stages < 1 || gr.stages * C::NW * f.sub() < partials) return cudaErrorInvalidValue;
   gr.warps = C::NW;
   auto kernel = kv4_attn_kernel<C, E>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(off));
@@ -818,9 +896,11 @@ cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
 
 template <int DQK, int DV>
 cudaError_t launch_dims(const Kv4AttnArgs& a, const Grid& gr, int dtype, cudaStream_t st) {
-  if (dtype == CP_DT_F32) return launch<Cfg<DQK, DV, 1, 3>, float>(a, gr, st);
-  return cols_of(a.rows, dtype) == 8 ? launch<Cfg<DQK, DV, 1, 1>, __nv_bfloat16>(a, gr, st)
-                                     : launch<Cfg<DQK, DV, 2, 1>, __nv_bfloat16>(a, gr, st);
+  if (dtype == CP_DT_F32) return launch<Cfg<DQK, DV, 1, 3, 8>, float>(a, gr, st);
+  if (cols_of(a.rows, dtype) == 16) return launch<Cfg<DQK, DV, 2, 1, 8>, __nv_bfloat16>(a, gr, st);
+  // sixteen warps where registers and shared memory (partials of few rows) allow
+  if (DQK < 192 && gr.rows_per_tile <= 4) return launch<Cfg<DQK, DV, 1, 1, DQK < 192 ? 16 : 12>, __nv_bfloat16>(a, gr, st);
+  return launch<Cfg<DQK, DV, 1, 1, 12>, __nv_bfloat16>(a, gr, st);
 }
 
 struct Layout {
