@@ -36,6 +36,8 @@
 // the workspace (they stay in L2) and the second kernel adds them up.
 #include <algorithm>
 
+#include <cuda_fp8.h>
+
 #include "kv4.cuh"
 #include "sm103_ptx.cuh"
 
@@ -128,6 +130,13 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t w) {
   return (x & kMask) | kSixteen;
 }
 
+// Nibbles 0 and 4 of V words: of bf16 caches as 128 + n, which takes no shift
+// (the eightfold of the other channels' offset is taken out in the end)
+template <int TERMS>
+__device__ __forceinline__ uint32_t nibble0(uint32_t w) {
+  return TERMS == 1 ? (w & 0x000f000fu) | 0x43004300u : nibbles<0>(w);
+}
+
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 // bf16 number i of packed words
@@ -170,6 +179,17 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t (&t)[TERMS
       y -= bf_hi(t[i]);
     }
   }
+}
+
+// x and y, times `unit`, as two e4m3 bytes (x low); x and y become what is left over
+__device__ __forceinline__ uint32_t e4m3_pair(float& x, float& y, float unit) {
+  x *= unit;
+  y *= unit;
+  const __nv_fp8x2_storage_t t = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+  const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(t, __NV_E4M3)));
+  x -= back.x;
+  y -= back.y;
+  return t;
 }
 
 __device__ __forceinline__ void load_q8(const float* p, float (&x)[8]) {
@@ -234,6 +254,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
   const uint32_t sbase = ptx::smem_u32(smem);
   int32_t* base = reinterpret_cast<int32_t*>(smem + gr.off_base);
   float* stat_s = reinterpret_cast<float*>(smem + gr.off_stat);    // [2 NW][2][COLS]: the partials' references and sums
+  float* top_s = stat_s + 2 * NW * 2 * C::COLS;                    // [2 NW][COLS]: the largest of a run's references
   float* stash_s = reinterpret_cast<float*>(smem + gr.off_stash);  // [NW][rows_per_tile][DV]: the first partials
   float* last_s = reinterpret_cast<float*>(smem + gr.off_ring);    // the last ones, once no warp uses its ring
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -258,7 +279,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
 
   // ---- its copies, `stages` ahead
   UnitCursor cur, ahead;
-  int loaded = 0;
+  int loaded = 0, load_stage = 0;
   uint32_t absent = 0;  // bit s: the page of stage s's unit is not in the pool
   int next_page = 0;
   auto look_up = [&]() {
@@ -270,7 +291,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
     if (w0 + loaded >= w1) return;
     const int page = next_page;  // looked up while the unit before was on its way
     if (page < 0) kv4_error(a.c, kKv4Page);
-    const int s = loaded % gr.stages;
+    const int s = load_stage;
+    if (++load_stage == gr.stages) load_stage = 0;
     absent = page < 0 ? absent | (1u << s) : absent & ~(1u << s);
     if (lane == 0) {
       if (page >= 0) {
@@ -295,11 +317,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
   }
   ptx::grid_launch_dependents();
 
-  const float sl2 = a.c.scale * kLog2e;
   const int frag_rows = gr.rows_per_tile;
   const uint32_t frag0 = sbase + gr.off_frag + uint32_t(warp) * (DQK / 16 * TERMS * 32) * frag_rows;
   float O[GV][4][NT][4], osix[GV][NT][4], ooff[GV][NT][2], ref[NT][2], sum[NT][2];
-  int done = 0;
+  int done = 0, stage = 0;
+  uint32_t phase = 0;
   bool ok = true, last = false;  // last: the registers hold a partial that the next warp's units continue
   for (int u = w0; u < w1 && ok && !last;) {
     // ---- a run, as far as this warp's units go
@@ -310,7 +332,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
     const int len = min(kv4_length(a.c, a.lengths, b), per_run * kKv4Sub);
     // ---- its queries as B fragments (kstep 2j + p: channels 8w + 2p, 8w + 2p + 4 and the next two, w = 4j + c), and
     // the sums of their groups.  Columns past the rows repeat rows; nothing of them is written out.
-    float qsum[GK][NT][2];
+    float qsum[GK][NT][2], sl2[NT][2];
     int lim[NT][2];
     uint32_t frag[NT];
 #pragma unroll
@@ -319,32 +341,69 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
       frag[nt] = frag0 + uint32_t(n * 4 + c) * 8;
       int t, head;
       const E* q = static_cast<const E*>(a.q) + row_index(a, b, h, n0 + n, &t, &head) * DQK + 8 * c;
-      float gs[GK];
+      float gs[GK], x[DQK / 32][8];
 #pragma unroll
       for (int j = 0; j < DQK / 32; ++j) {
-        float x[8];
-        load_q8(q + 32 * j, x);
+        load_q8(q + 32 * j, x[j]);
         if (j % 2 == 0) gs[j / 2] = 0.f;
-        gs[j / 2] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-        uint32_t f0[2][TERMS], f1[2][TERMS];
+        gs[j / 2] += ((x[j][0] + x[j][1]) + (x[j][2] + x[j][3])) + ((x[j][4] + x[j][5]) + (x[j][6] + x[j][7]));
+      }
+      float unit = 1.f, factor = a.c.scale * kLog2e;
+      if constexpr (TERMS == 1) {
+        // the row times a power of two that brings its largest channel to 128 .. 256
+        uint32_t big = 0;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          split_pair<TERMS>(x[2 * p], x[2 * p + 4], f0[p]);
-          split_pair<TERMS>(x[2 * p + 1], x[2 * p + 5], f1[p]);
+        for (int j = 0; j < DQK / 32; ++j)
 #pragma unroll
-          for (int m = 0; m < TERMS; ++m)
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(frag[nt] + ((2 * j + p) * TERMS + m) * (frag_rows * 32)),
-                         "r"(f0[p][m]), "r"(f1[p][m])
+          for (int i = 0; i < 8; ++i) big = max(big, __float_as_uint(x[j][i]) & 0x7fffffffu);
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        const int k = big < 0x00800000u ? 0 : 134 - int(min(big, 0x7f800000u) >> 23);  // 7 - exponent
+        unit = __uint_as_float(uint32_t(127 + max(min(k, 126), -126)) << 23);
+        // codes are n 2^-9 as e4m3 bytes: scores come out times unit / 512
+        factor = big >= 0x7f800000u ? NAN : factor * (512.f / unit);
+#pragma unroll
+        for (int j = 0; j < DQK / 32; ++j)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            // bytes: channels 8w, 8w + 2, .. and 8w + 1, 8w + 3, ..
+            uint32_t f0 = 0, f1 = 0;
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {
+              const uint32_t even = e4m3_pair(x[j][i], x[j][i + 2], m == 0 ? unit : 1.f);
+              const uint32_t odd = e4m3_pair(x[j][i + 1], x[j][i + 3], m == 0 ? unit : 1.f);
+              f0 |= even << (4 * i);
+              f1 |= odd << (4 * i);
+            }
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(frag[nt] + (2 * j + m) * (frag_rows * 32)), "r"(f0), "r"(f1)
                          : "memory");
+          }
+      } else {
+#pragma unroll
+        for (int j = 0; j < DQK / 32; ++j) {
+          uint32_t f0[2][TERMS], f1[2][TERMS];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            split_pair<TERMS>(x[j][2 * p], x[j][2 * p + 4], f0[p]);
+            split_pair<TERMS>(x[j][2 * p + 1], x[j][2 * p + 5], f1[p]);
+#pragma unroll
+            for (int m = 0; m < TERMS; ++m)
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(frag[nt] + ((2 * j + p) * TERMS + m) * (frag_rows * 32)),
+                           "r"(f0[p][m]), "r"(f1[p][m])
+                           : "memory");
+          }
         }
       }
 #pragma unroll
       for (int g = 0; g < GK; ++g) {
         gs[g] += __shfl_xor_sync(0xffffffffu, gs[g], 1);
         gs[g] += __shfl_xor_sync(0xffffffffu, gs[g], 2);
+        if (TERMS == 1) gs[g] *= unit * (1.f / 512.f);
 #pragma unroll
         for (int e = 0; e < 2; ++e) qsum[g][nt][e] = __shfl_sync(0xffffffffu, gs[g], (2 * c + e) * 4);
       }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) sl2[nt][e] = __shfl_sync(0xffffffffu, factor, (2 * c + e) * 4);
       const int own = len - (a.n_q - 1 - t);
 #pragma unroll
       for (int e = 0; e < 2; ++e) lim[nt][e] = __shfl_sync(0xffffffffu, own, (2 * c + e) * 4);
@@ -371,8 +430,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
     }
 
     for (; u < seg1; ++u) {
-      const int s = done % gr.stages;
-      if (ok) ok = ptx::mbar_wait_w(bar0 + 8 * s, (done / gr.stages) & 1, kKv4Wait, wctx);
+      const int s = stage;
+      ok = ptx::mbar_wait_w(bar0 + 8 * s, phase, kKv4Wait, wctx);
       if (!ok) break;
       const uint32_t st = ring + uint32_t(s) * f.sub();
       const bool gone = (absent >> s) & 1;
@@ -391,12 +450,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
             lds_words<GK>(st + f.kp() + tok * (GK * 4), kp[mt][x]);
           }
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[mt][nt][e] = 0.f;
-#pragma unroll
         for (int g = 0; g < GK; ++g) {
           float acc[2][NT][4];
 #pragma unroll
@@ -404,29 +457,49 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[mt][nt][e] = -16.f * qsum[g][nt][e & 1];
+              for (int e = 0; e < 4; ++e) acc[mt][nt][e] = TERMS == 1 ? 0.f : -16.f * qsum[g][nt][e & 1];
 #pragma unroll
           for (int jj = 0; jj < 2; ++jj) {
             const int j = 2 * g + jj;
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
+            if constexpr (TERMS == 1) {
               uint32_t A[2][4];
 #pragma unroll
               for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                  A[mt][x] = p == 0 ? nibbles<0>(kw[mt][x][j]) : nibbles<2>(kw[mt][x][j]);
-                  A[mt][2 + x] = p == 0 ? nibbles<1>(kw[mt][x][j]) : nibbles<3>(kw[mt][x][j]);
+                  A[mt][x] = kw[mt][x][j] & 0x0f0f0f0fu;
+                  A[mt][2 + x] = (kw[mt][x][j] >> 4) & 0x0f0f0f0fu;
                 }
 #pragma unroll
-              for (int m = 0; m < TERMS; ++m)
+              for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                   uint32_t q2[2];
-                  lds_words<2>(frag[nt] + ((2 * j + p) * TERMS + m) * (frag_rows * 32), q2);
+                  lds_words<2>(frag[nt] + (2 * j + m) * (frag_rows * 32), q2);
 #pragma unroll
-                  for (int mt = 0; mt < 2; ++mt) ptx::mma_16816(acc[mt][nt], A[mt], q2[0], q2[1]);
+                  for (int mt = 0; mt < 2; ++mt) ptx::mma_16832(acc[mt][nt], A[mt], q2[0], q2[1]);
                 }
+            } else {
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                uint32_t A[2][4];
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    A[mt][x] = p == 0 ? nibbles<0>(kw[mt][x][j]) : nibbles<2>(kw[mt][x][j]);
+                    A[mt][2 + x] = p == 0 ? nibbles<1>(kw[mt][x][j]) : nibbles<3>(kw[mt][x][j]);
+                  }
+#pragma unroll
+                for (int m = 0; m < TERMS; ++m)
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    uint32_t q2[2];
+                    lds_words<2>(frag[nt] + ((2 * j + p) * TERMS + m) * (frag_rows * 32), q2);
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) ptx::mma_16816(acc[mt][nt], A[mt], q2[0], q2[1]);
+                  }
+              }
             }
           }
 #pragma unroll
@@ -437,19 +510,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  S[mt][nt][2 * x + e] += fmaf(ks, acc[mt][nt][2 * x + e], kl * qsum[g][nt][e]);
+                for (int e = 0; e < 2; ++e) {
+                  float& sc = S[mt][nt][2 * x + e];
+                  sc = g == 0 ? kl * qsum[0][nt][e] : fmaf(kl, qsum[g][nt][e], sc);
+                  sc = fmaf(ks, acc[mt][nt][2 * x + e], sc);
+                }
             }
         }
       }
       // ---- P = 2^(S - ref)
       const bool masked = gone || j0 + kKv4Sub > lim_min;  // the same for the whole warp
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) S[mt][nt][e] *= sl2;
       uint32_t vis = 0xffffffffu;  // bit (mt * NT + nt) * 4 + e: the element is visible
       if (masked) {
 #pragma unroll
@@ -471,24 +541,28 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
             const int n = nt * 8 + 2 * c + (e & 1);
             if (n < rows) {
               float* to = gr.score + (int64_t(u) * gr.rows_per_tile + n) * kKv4Sub + (e >> 1) * 8 + r;
-              to[0] = S[0][nt][e];
-              to[16] = S[1][nt][e];
+              to[0] = S[0][nt][e] * sl2[nt][e & 1];
+              to[16] = S[1][nt][e] * sl2[nt][e & 1];
             }
           }
       }
+      float P[2][NT][4];
       float top = -INFINITY;
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top = fmaxf(top, S[mt][nt][e] - ref[nt][e & 1]);
+          for (int e = 0; e < 4; ++e) {
+            P[mt][nt][e] = fmaf(S[mt][nt][e], sl2[nt][e & 1], -ref[nt][e & 1]);
+            top = fmaxf(top, P[mt][nt][e]);
+          }
       if (__any_sync(0xffffffffu, top > kSlack)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float m = fmaxf(fmaxf(S[0][nt][e], S[0][nt][e + 2]), fmaxf(S[1][nt][e], S[1][nt][e + 2]));
+            float m = fmaxf(fmaxf(S[0][nt][e], S[0][nt][e + 2]), fmaxf(S[1][nt][e], S[1][nt][e + 2])) * sl2[nt][e];
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -507,6 +581,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
                 O[g][i][nt][e + 2] *= keep;
               }
             }
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int x = 0; x < 4; x += 2) P[mt][nt][e + x] = fmaf(S[mt][nt][e + x], sl2[nt][e], -m);
           }
       }
 #pragma unroll
@@ -515,8 +593,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            S[mt][nt][e] = ptx::ex2(S[mt][nt][e] - ref[nt][e & 1]);
-            sum[nt][e & 1] += S[mt][nt][e];
+            P[mt][nt][e] = ptx::ex2(P[mt][nt][e]);
+            sum[nt][e & 1] += P[mt][nt][e];
           }
       // ---- O^T += V^T P^T, 16 tokens at a time
 #pragma unroll
@@ -545,16 +623,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
           const float l1 = lds_bf16(st + f.vl() + (g * kKv4Sub + mt * 16 + 8 + r) * 2);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const float* p = S[mt][nt];
+            const float* p = P[mt][nt];
             float ps[4] = {p[0] * s0, p[1] * s0, p[2] * s1, p[3] * s1};
-            float pl[4] = {p[0] * l0, p[1] * l0, p[2] * l1, p[3] * l1};
             if (masked) {  // what an unseen slot holds (NaN, in the worst case) reaches nothing
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (!((vis >> ((mt * NT + nt) * 4 + e)) & 1)) ps[e] = pl[e] = 0.f;
+              for (int e = 0; e < 4; ++e) {
+                const bool see = (vis >> ((mt * NT + nt) * 4 + e)) & 1;
+                if (!see) ps[e] = 0.f;
+                if (see) ooff[g][nt][e & 1] = fmaf(p[e], e < 2 ? l0 : l1, ooff[g][nt][e & 1]);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) ooff[g][nt][e & 1] = fmaf(p[e], e < 2 ? l0 : l1, ooff[g][nt][e & 1]);
             }
-            ooff[g][nt][0] += pl[0] + pl[2];
-            ooff[g][nt][1] += pl[1] + pl[3];
             split_pair<TERMS>(ps[0], ps[1], B0[nt]);
             split_pair<TERMS>(ps[2], ps[3], B1[nt]);
 #pragma unroll
@@ -565,7 +646,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
           }
           const uint32_t lo0 = __byte_perm(vw[0][g], vw[1][g], 0x5410), hi0 = __byte_perm(vw[0][g], vw[1][g], 0x7632);
           const uint32_t lo1 = __byte_perm(vw[2][g], vw[3][g], 0x5410), hi1 = __byte_perm(vw[2][g], vw[3][g], 0x7632);
-          const uint32_t A[5][4] = {{nibbles<0>(lo0), nibbles<0>(hi0), nibbles<0>(lo1), nibbles<0>(hi1)},
+          const uint32_t A[5][4] = {{nibble0<TERMS>(lo0), nibble0<TERMS>(hi0), nibble0<TERMS>(lo1), nibble0<TERMS>(hi1)},
                                     {nibbles<1>(lo0), nibbles<1>(hi0), nibbles<1>(lo1), nibbles<1>(hi1)},
                                     {nibbles<2>(lo0), nibbles<2>(hi0), nibbles<2>(lo1), nibbles<2>(hi1)},
                                     {nibbles<3>(lo0), nibbles<3>(hi0), nibbles<3>(lo1), nibbles<3>(hi1)},
@@ -582,6 +663,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
       }
       __syncwarp();  // the stage has been read
       ++done;
+      if (++stage == gr.stages) stage = 0, phase ^= 1;
       load_next();
       cur.next(base, a.c.num_seqs, per);
     }
@@ -611,10 +693,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
 #pragma unroll
           for (int g = 0; g < GV; ++g) {
             const float add = osix[g][nt][e] + ooff[g][nt][e];
+            const float add0 = TERMS == 1 ? fmaf(8.f, osix[g][nt][e], ooff[g][nt][e]) : add;
 #pragma unroll
             for (int x = 0; x < 2; ++x)
               store_o4(a, row * DV + 64 * g + 8 * r + 4 * x,
-                       make_float4((O[g][0][nt][e + 2 * x] + add) * inv, (O[g][1][nt][e + 2 * x] + add) * inv,
+                       make_float4((O[g][0][nt][e + 2 * x] + add0) * inv, (O[g][1][nt][e + 2 * x] + add) * inv,
                                    (O[g][2][nt][e + 2 * x] + add) * inv, (O[g][3][nt][e + 2 * x] + add) * inv));
           }
           if (r == 0)
@@ -640,10 +723,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
 #pragma unroll
           for (int g = 0; g < GV; ++g) {
             const float add = osix[g][nt][e] + ooff[g][nt][e];
+            const float add0 = TERMS == 1 ? fmaf(8.f, osix[g][nt][e], ooff[g][nt][e]) : add;
 #pragma unroll
             for (int x = 0; x < 2; ++x)
               *reinterpret_cast<float4*>(part + n * DV + 64 * g + 8 * r + 4 * x) =
-                  make_float4(O[g][0][nt][e + 2 * x] + add, O[g][1][nt][e + 2 * x] + add, O[g][2][nt][e + 2 * x] + add,
+                  make_float4(O[g][0][nt][e + 2 * x] + add0, O[g][1][nt][e + 2 * x] + add, O[g][2][nt][e + 2 * x] + add,
                               O[g][3][nt][e + 2 * x] + add);
           }
         }
@@ -658,14 +742,32 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
   if (!last) __syncthreads();
   __syncthreads();
 
-  // ---- runs cut over warps: their partials, in order, joined by the whole CTA
+  // ---- runs cut over warps: their partials, in order, joined by the whole CTA.  First what every partial weighs:
+  // lane = partial, a warp a row; partials of one run find their largest reference among them.
   constexpr int kSlots = 2 * NW;
+  for (int n = warp; n < gr.rows_per_tile; n += NW) {
+    const int id = lane < kSlots ? s_run[lane] : -1;
+    float* st = stat_s + (lane < kSlots ? lane : 0) * 2 * C::COLS + n;
+    const float m = id < 0 ? kNoRef : st[0], l = id < 0 ? 0.f : st[C::COLS];
+    const uint32_t mask = __match_any_sync(0xffffffffu, id);
+    // floats as integers of the same order
+    const int order = __float_as_int(m) ^ ((__float_as_int(m) >> 31) & 0x7fffffff);
+    const int top = __reduce_max_sync(mask, order);
+    const float mm = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
+    const float k = l == 0.f ? 0.f : ptx::ex2(m - mm);  // 0: saw nothing
+    __syncwarp();
+    if (lane < kSlots) {
+      st[0] = k;
+      st[C::COLS] = l == 0.f ? 0.f : k * l;
+      top_s[lane * C::COLS + n] = mm;
+    }
+  }
+  __syncthreads();
   for (int s0 = 0; s0 < kSlots;) {
     const int id = s_run[s0];
     int s1 = s0 + 1;
-    if (id >= 0)
-      while (s1 < kSlots && (s_run[s1] < 0 || s_run[s1] == id)) ++s1;
     if (id >= 0) {
+      while (s1 < kSlots && (s_run[s1] < 0 || s_run[s1] == id)) ++s1;
       const int b = id / per, run = id - b * per;
       const int per_run = (base[b + 1] - base[b]) / per, run0 = base[b] + run * per_run;
       const int h = run / row_tiles, n0 = (run - h * row_tiles) * gr.rows_per_tile;
@@ -674,17 +776,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
       float* part = gr.part + (int64_t(blockIdx.x) * 2 + (run0 >= u0)) * part_floats(C::COLS, DV);
       for (int e = tid; e < rows * DV; e += C::THREADS) {
         const int n = e / DV, d = e - n * DV;
-        float m = kNoRef, l = 0.f, x = 0.f;
-        for (int s = s0; s < s1; ++s)
-          if (s_run[s] >= 0) m = fmaxf(m, stat_s[s * 2 * C::COLS + n]);
+        float l = 0.f, x = 0.f;
+#pragma unroll 4
         for (int s = s0; s < s1; ++s) {
-          if (s_run[s] < 0) continue;
-          const float* st = stat_s + s * 2 * C::COLS;
-          if (st[C::COLS + n] == 0.f) continue;  // saw nothing
-          const float k = ptx::ex2(st[n] - m);
-          l += k * st[C::COLS + n];
-          x += k * ((s & 1) ? last_s : stash_s)[(s >> 1) * gr.rows_per_tile * DV + e];
+          const float* st = stat_s + s * 2 * C::COLS + n;
+          const float k = s_run[s] < 0 ? 0.f : st[0];
+          if (k != 0.f) {
+            l += st[C::COLS];
+            x += k * ((s & 1) ? last_s : stash_s)[(s >> 1) * gr.rows_per_tile * DV + e];
+          }
         }
+        const float m = top_s[s0 * C::COLS + n];
         if (whole) {
           int t, head;
           const int64_t row = row_index(a, b, h, n0 + n, &t, &head);
@@ -705,7 +807,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
   }
 }
 
-// Joins the runs that were cut (one CTA each; whole ones are done, empty ones
+// Joins the runs that were cut (a CTA a row; whole ones are done, empty ones
 // get o = 0, lse = -inf), and adds up the weights: the other CTAs' warps take
 // sub-blocks, a lane a token.
 constexpr int kJoinThreads = 256;
@@ -722,62 +824,62 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnArg
   constexpr int kPart = part_floats(COLS, DV);
   // partial i of a run cut over shares c0, c0 + 1, ...: slot 1 of the share it starts in, slot 0 of the others
   auto part_of = [&](int c0, int i) { return gr.part + (int64_t(c0 + i) * 2 + (i == 0)) * kPart; };
-  if (int(blockIdx.x) < runs) {
-    const int b = int(blockIdx.x) / per, run = int(blockIdx.x) - b * per;
+  const int joins = runs * gr.rows_per_tile;
+  if (int(blockIdx.x) < joins) {
+    const int id = int(blockIdx.x) / gr.rows_per_tile, n = int(blockIdx.x) - id * gr.rows_per_tile;
+    const int b = id / per, run = id - b * per;
     const int per_run = (base[b + 1] - base[b]) / per, run0 = base[b] + run * per_run;
     const int h = run / row_tiles, n0 = (run - h * row_tiles) * gr.rows_per_tile;
-    const int rows = min(gr.rows_per_tile, a.rows - n0);
-    int c0 = 0, c1 = 0;
+    if (n0 + n >= a.rows) return;
+    int c0 = 0, parts = 0;
     if (per_run > 0) {
       c0 = share_of(units, shares, run0);
-      c1 = share_of(units, shares, run0 + per_run - 1);
-      if (c0 == c1) return;
+      parts = share_of(units, shares, run0 + per_run - 1) - c0 + 1;
+      if (parts == 1) return;
     }
-    // what every partial weighs, as in the first kernel
-    const int parts = per_run > 0 ? c1 - c0 + 1 : 0;
-    float* k_s = reinterpret_cast<float*>(smem + gr.off_join);  // [parts][rows]: references, then weights
-    float* l_s = k_s + gr.ctas * gr.rows_per_tile;              // [parts][rows]: sums
-    for (int e = threadIdx.x; e < parts * rows; e += kJoinThreads) {
-      const float* p = part_of(c0, e / rows) + e % rows;
-      k_s[e] = p[0];
-      l_s[e] = p[COLS];
+    float* k_s = reinterpret_cast<float*>(smem + gr.off_join);  // [parts]: references, then weights
+    float* l_s = k_s + gr.ctas;                                 // [parts]: sums
+    for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
+      const float* p = part_of(c0, i) + n;
+      k_s[i] = p[0];
+      l_s[i] = p[COLS];
     }
     __syncthreads();
-    float* m_s = l_s + gr.ctas * gr.rows_per_tile;  // [rows]
-    if (threadIdx.x < rows) {
-      float m = kNoRef;
-      for (int i = 0; i < parts; ++i) m = fmaxf(m, k_s[i * rows + threadIdx.x]);
-      m_s[threadIdx.x] = m;
+    float m = kNoRef;
+    for (int i = threadIdx.x & 31; i < parts; i += 32) m = fmaxf(m, k_s[i]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    __syncthreads();
+    for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
+      const float k = l_s[i] == 0.f ? 0.f : ptx::ex2(k_s[i] - m);  // 0: saw nothing
+      k_s[i] = k;
+      l_s[i] = l_s[i] == 0.f ? 0.f : k * l_s[i];
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < parts * rows; e += kJoinThreads) {
-      const float k = l_s[e] == 0.f ? 0.f : ptx::ex2(k_s[e] - m_s[e % rows]);
-      k_s[e] = k;
-      l_s[e] = l_s[e] == 0.f ? 0.f : k * l_s[e];
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < rows * DV; e += kJoinThreads) {
-      const int n = e / DV, d = e - n * DV;
-      float l = 0.f, x = 0.f;
+    constexpr int kSplit = kJoinThreads / DV;
+    float* x_s = l_s + gr.ctas;  // [kSplit][DV]
+    const int d = threadIdx.x % DV, first = threadIdx.x / DV;
+    float l = 0.f, x = 0.f;
 #pragma unroll 8
-      for (int i = 0; i < parts; ++i) {
-        // (a partial that saw nothing is all zeros)
-        l += l_s[i * rows + n];
-        x += k_s[i * rows + n] * part_of(c0, i)[2 * COLS + e];
-      }
-      int t, head;
-      const int64_t row = row_index(a, b, h, n0 + n, &t, &head);
-      store_o(a, row * DV + d, l == 0.f ? 0.f : x / l);
-      if (d == 0)
-        a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] =
-            l == 0.f ? -INFINITY : (m_s[n] + log2f(l)) * kLn2;
-    }
+    for (int i = first; i < parts; i += kSplit) x += k_s[i] * part_of(c0, i)[2 * COLS + n * DV + d];
+    x_s[first * DV + d] = x;
+    for (int i = 0; i < parts; ++i) l += l_s[i];
+    __syncthreads();
+    if (first > 0) return;
+#pragma unroll
+    for (int i = 1; i < kSplit; ++i) x += x_s[i * DV + d];
+    int t, head;
+    const int64_t row = row_index(a, b, h, n0 + n, &t, &head);
+    store_o(a, row * DV + d, l == 0.f ? 0.f : x / l);
+    if (d == 0)
+      a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] =
+          l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     return;
   }
   // ---- weights
   const int lane = threadIdx.x & 31;
-  const int warps = (int(gridDim.x) - runs) * (kJoinThreads / 32);
-  const int w = (int(blockIdx.x) - runs) * (kJoinThreads / 32) + int(threadIdx.x >> 5);
+  const int warps = (int(gridDim.x) - joins) * (kJoinThreads / 32);
+  const int w = (int(blockIdx.x) - joins) * (kJoinThreads / 32) + int(threadIdx.x >> 5);
   const int64_t all = units / row_tiles;  // sub-blocks of the cache
   const int64_t v0 = all * w / warps, v1 = all * (w + 1) / warps;
   int b = 0, last_h = -1, last_b = -1;
@@ -857,7 +959,7 @@ cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
   gr.off_frag = off;
   off += C::NW * (C::DQK / 16 * C::TERMS * 32) * gr.rows_per_tile;
   gr.off_stat = off;
-  off += 2 * C::NW * 2 * C::COLS * 4;
+  off += 2 * C::NW * 3 * C::COLS * 4;
   gr.off_stash = off;
   const uint32_t partials = C::NW * gr.rows_per_tile * C::DV * 4;
   off = up(off + partials, 128);
@@ -877,13 +979,13 @@ cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int runs = a.c.num_seqs * a.c.hkv * a.row_tiles;
   gr.off_join = up(4 * (a.c.num_seqs + 1), 16);
-  const uint32_t join_smem = gr.off_join + (2 * gr.ctas + 1) * gr.rows_per_tile * 4;  // at most 36 KB
+  const uint32_t join_smem = gr.off_join + (2 * gr.ctas + kJoinThreads) * 4;
   // the second kernel's launch overlaps the first: it waits on the device
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(runs + (a.accumulate ? 2 * gr.ctas : 0)));
+  cfg.gridDim = dim3(unsigned(runs * gr.rows_per_tile + (a.accumulate ? 4 * gr.ctas : 0)));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = join_smem;
   cfg.stream = st;
