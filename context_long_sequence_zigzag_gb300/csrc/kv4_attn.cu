@@ -122,19 +122,33 @@ __device__ __forceinline__ int seq_of_unit(const int32_t* base, int n, int b, in
   return lo;
 }
 
+// Masks of the unpacking in registers (a LOP3 has room for one immediate, and
+// the compiler, seeing two, makes two instructions of each).
+struct Masks {
+  uint32_t nib, sixteen, low, big;
+  __device__ Masks() {
+    asm("mov.u32 %0, 0x00780078;" : "=r"(nib));
+    asm("mov.u32 %0, 0x41804180;" : "=r"(sixteen));
+    asm("mov.u32 %0, 0x000f000f;" : "=r"(low));
+    asm("mov.u32 %0, 0x43004300;" : "=r"(big));
+  }
+};
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t a, uint32_t o) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(a), "r"(o));
+  return y;
+}
 // 16 + n of nibbles i and i + 4 as a bf16 pair
 template <int I>
-__device__ __forceinline__ uint32_t nibbles(uint32_t w) {
-  constexpr uint32_t kMask = 0x00780078u, kSixteen = 0x41804180u;
-  const uint32_t x = I == 0 ? w << 3 : w >> (4 * I - 3);
-  return (x & kMask) | kSixteen;
+__device__ __forceinline__ uint32_t nibbles(uint32_t w, const Masks& k) {
+  return and_or(I == 0 ? w << 3 : w >> (4 * I - 3), k.nib, k.sixteen);
 }
 
 // Nibbles 0 and 4 of V words: of bf16 caches as 128 + n, which takes no shift
 // (the eightfold of the other channels' offset is taken out in the end)
 template <int TERMS>
-__device__ __forceinline__ uint32_t nibble0(uint32_t w) {
-  return TERMS == 1 ? (w & 0x000f000fu) | 0x43004300u : nibbles<0>(w);
+__device__ __forceinline__ uint32_t nibble0(uint32_t w, const Masks& k) {
+  return TERMS == 1 ? and_or(w, k.low, k.big) : nibbles<0>(w, k);
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -145,27 +159,28 @@ __device__ __forceinline__ float half_at(const uint32_t (&w)[N], int i) {
   return (i & 1) ? bf_hi(w[i >> 1]) : bf_lo(w[i >> 1]);
 }
 
+// N packed words of shared memory (aligned to the widest load that N allows)
 template <int N>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
   if constexpr (N % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < N; i += 4)
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                   : "r"(addr + 4 * i));
+    for (int i = 0; i < N; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    }
   } else if constexpr (N % 2 == 0) {
 #pragma unroll
-    for (int i = 0; i < N; i += 2)
-      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[i]), "=r"(w[i + 1]) : "r"(addr + 4 * i));
+    for (int i = 0; i < N; i += 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p + 4 * i);
+      w[i] = v.x, w[i + 1] = v.y;
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i]) : "r"(addr + 4 * i));
+    for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint32_t*>(p + 4 * i);
   }
 }
-__device__ __forceinline__ float lds_bf16(uint32_t addr) {
-  uint16_t x;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(addr));
-  return __uint_as_float(uint32_t(x) << 16);
+__device__ __forceinline__ float load_bf16(const uint8_t* p) {
+  return __uint_as_float(uint32_t(*reinterpret_cast<const uint16_t*>(p)) << 16);
 }
 
 // x as TERMS bf16 terms, the first the nearest
@@ -224,18 +239,20 @@ __device__ __forceinline__ int64_t row_index(const Kv4AttnArgs& a, int b, int h,
 
 // Walks units: sub-block i of run `run` of sequence b.
 struct UnitCursor {
-  int b, run, i, per_run;
-  __device__ void seek(const int32_t* base, int n, int per, int u) {
+  int b, run, i, per_run, h;  // h: the run's kv head
+  __device__ void seek(const int32_t* base, int n, int per, int row_tiles, int u) {
     b = seq_of_unit(base, n, 0, u);
     per_run = (base[b + 1] - base[b]) / per;
     run = (u - base[b]) / per_run;
     i = u - base[b] - run * per_run;
+    h = run / row_tiles;
   }
-  __device__ void next(const int32_t* base, int n, int per) {
+  __device__ void next(const int32_t* base, int n, int per, int row_tiles) {
     if (++i < per_run) return;
     i = 0;
-    if (++run < per) return;
-    run = 0;
+    h = ++run / row_tiles;
+    if (run < per) return;
+    run = h = 0;
     do ++b;
     while (b < n && base[b + 1] == base[b]);
     per_run = b < n ? (base[b + 1] - base[b]) / per : 1;
@@ -261,6 +278,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
   const int r = lane >> 2, c = lane & 3;
   const int row_tiles = a.row_tiles, per = a.c.hkv * row_tiles;
   const uint32_t ring = sbase + gr.off_ring + uint32_t(warp * gr.stages) * f.sub();
+  const uint8_t* ring_p = smem + gr.off_ring + (warp * gr.stages) * f.sub();
   const uint32_t bar0 = ptx::smem_u32(&bars[warp * 4]);
   if (lane == 0) {
     for (int s = 0; s < gr.stages; ++s) ptx::mbar_init(bar0 + 8 * s, 1);
@@ -298,7 +316,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
       if (page >= 0) {
         ptx::mbar_arrive_expect_tx(bar0 + 8 * s, uint32_t(f.sub()));
         ptx::bulk_load(ring + uint32_t(s) * f.sub(),
-                       a.c.pages + (int64_t(page) * a.c.hkv + ahead.run / row_tiles) * f.block() +
+                       a.c.pages + (int64_t(page) * a.c.hkv + ahead.h) * f.block() +
                            ahead.i % (CP_KV4_PAGE / kKv4Sub) * f.sub(),
                        uint32_t(f.sub()), bar0 + 8 * s);
       } else {
@@ -306,39 +324,42 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
       }
     }
     ++loaded;
-    ahead.next(base, a.c.num_seqs, per);
+    ahead.next(base, a.c.num_seqs, per, row_tiles);
     look_up();
   };
   if (w0 < w1) {
-    cur.seek(base, a.c.num_seqs, per, w0);
+    cur.seek(base, a.c.num_seqs, per, row_tiles, w0);
     ahead = cur;
     look_up();
     for (int s = 0; s < gr.stages; ++s) load_next();
   }
   ptx::grid_launch_dependents();
 
-  const int frag_rows = gr.rows_per_tile;
-  const uint32_t frag0 = sbase + gr.off_frag + uint32_t(warp) * (DQK / 16 * TERMS * 32) * frag_rows;
-  float O[GV][4][NT][4], osix[GV][NT][4], ooff[GV][NT][2], ref[NT][2], sum[NT][2];
+  constexpr int kFragStride = C::COLS * 32;
+  uint8_t* frag0 = smem + gr.off_frag + warp * (DQK / 16 * TERMS) * kFragStride;
+  float O[GV][4][NT][4], osix[GV][NT][4], ref[NT][2];
+  uint64_t ooff2[GV][NT], sum2[NT];  // pairs: columns 2c and 2c + 1
+  const Masks masks;
   int done = 0, stage = 0;
   uint32_t phase = 0;
   bool ok = true, last = false;  // last: the registers hold a partial that the next warp's units continue
   for (int u = w0; u < w1 && ok && !last;) {
     // ---- a run, as far as this warp's units go
-    const int b = cur.b, run = cur.run, run0 = u - cur.i, per_run = cur.per_run;
+    const int b = cur.b, run = cur.run, h = cur.h, run0 = u - cur.i, per_run = cur.per_run;
     const int seg1 = min(w1, run0 + per_run);
-    const int h = run / row_tiles, n0 = (run - h * row_tiles) * gr.rows_per_tile;
+    const int n0 = (run - h * row_tiles) * gr.rows_per_tile;
     const int rows = min(gr.rows_per_tile, a.rows - n0);
     const int len = min(kv4_length(a.c, a.lengths, b), per_run * kKv4Sub);
     // ---- its queries as B fragments (kstep 2j + p: channels 8w + 2p, 8w + 2p + 4 and the next two, w = 4j + c), and
     // the sums of their groups.  Columns past the rows repeat rows; nothing of them is written out.
-    float qsum[GK][NT][2], sl2[NT][2];
+    uint64_t qsum2[GK][NT];
+    float sl2[NT][2];
     int lim[NT][2];
-    uint32_t frag[NT];
+    uint8_t* frag[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int n = (nt * 8 + r) % rows;
-      frag[nt] = frag0 + uint32_t(n * 4 + c) * 8;
+      frag[nt] = frag0 + (n * 4 + c) * 8;
       int t, head;
       const E* q = static_cast<const E*>(a.q) + row_index(a, b, h, n0 + n, &t, &head) * DQK + 8 * c;
       float gs[GK], x[DQK / 32][8];
@@ -375,8 +396,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
               f0 |= even << (4 * i);
               f1 |= odd << (4 * i);
             }
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(frag[nt] + (2 * j + m) * (frag_rows * 32)), "r"(f0), "r"(f1)
-                         : "memory");
+            *reinterpret_cast<uint2*>(frag[nt] + (2 * j + m) * kFragStride) = make_uint2(f0, f1);
           }
       } else {
 #pragma unroll
@@ -388,9 +408,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
             split_pair<TERMS>(x[j][2 * p + 1], x[j][2 * p + 5], f1[p]);
 #pragma unroll
             for (int m = 0; m < TERMS; ++m)
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(frag[nt] + ((2 * j + p) * TERMS + m) * (frag_rows * 32)),
-                           "r"(f0[p][m]), "r"(f1[p][m])
-                           : "memory");
+              *reinterpret_cast<uint2*>(frag[nt] + ((2 * j + p) * TERMS + m) * kFragStride) = make_uint2(f0[p][m], f1[p][m]);
           }
         }
       }
@@ -399,8 +417,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
         gs[g] += __shfl_xor_sync(0xffffffffu, gs[g], 1);
         gs[g] += __shfl_xor_sync(0xffffffffu, gs[g], 2);
         if (TERMS == 1) gs[g] *= unit * (1.f / 512.f);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) qsum[g][nt][e] = __shfl_sync(0xffffffffu, gs[g], (2 * c + e) * 4);
+        const float q0 = __shfl_sync(0xffffffffu, gs[g], 2 * c * 4), q1 = __shfl_sync(0xffffffffu, gs[g], (2 * c + 1) * 4);
+        qsum2[g][nt] = ptx::f32x2(q0, q1);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) sl2[nt][e] = __shfl_sync(0xffffffffu, factor, (2 * c + e) * 4);
@@ -423,22 +441,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
           for (int e = 0; e < 4; ++e) O[g][i][nt][e] = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) osix[g][nt][e] = 0.f;
-        ooff[g][nt][0] = ooff[g][nt][1] = 0.f;
+        ooff2[g][nt] = 0;
       }
       ref[nt][0] = ref[nt][1] = kNoRef;
-      sum[nt][0] = sum[nt][1] = 0.f;
+      sum2[nt] = 0;
     }
 
     for (; u < seg1; ++u) {
       const int s = stage;
       ok = ptx::mbar_wait_w(bar0 + 8 * s, phase, kKv4Wait, wctx);
       if (!ok) break;
-      const uint32_t st = ring + uint32_t(s) * f.sub();
+      const uint8_t* st = ring_p + s * f.sub();
       const bool gone = (absent >> s) & 1;
       const int j0 = (u - run0) * kKv4Sub;
 
       // ---- S^T = K Q^T
-      float S[2][NT][4];
+      uint64_t S2[2][NT][2];  // pairs of columns: row r, row r + 8
       {
         uint32_t kw[2][2][C::KW], kp[2][2][GK];
 #pragma unroll
@@ -446,22 +464,26 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const uint32_t tok = mt * 16 + x * 8 + r;
-            lds_words<C::KW>(st + f.kc() + tok * (DQK / 2) + c * (C::KW * 4), kw[mt][x]);
-            lds_words<GK>(st + f.kp() + tok * (GK * 4), kp[mt][x]);
+            load_words<C::KW>(st + f.kc() + tok * (DQK / 2) + c * (C::KW * 4), kw[mt][x]);
+            load_words<GK>(st + f.kp() + tok * (GK * 4), kp[mt][x]);
           }
 #pragma unroll
         for (int g = 0; g < GK; ++g) {
-          float acc[2][NT][4];
+          uint64_t ks[2][2];
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int x = 0; x < 2; ++x) {
+              const float s1 = half_at(kp[mt][x], g), l1 = half_at(kp[mt][x], GK + g);
+              ks[mt][x] = ptx::f32x2(s1, s1);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[mt][nt][e] = TERMS == 1 ? 0.f : -16.f * qsum[g][nt][e & 1];
+              for (int nt = 0; nt < NT; ++nt)
+                S2[mt][nt][x] = g == 0 ? ptx::mul_f32x2(ptx::f32x2(l1, l1), qsum2[0][nt])
+                                       : ptx::fma_f32x2(ptx::f32x2(l1, l1), qsum2[g][nt], S2[mt][nt][x]);
+            }
+          if constexpr (TERMS == 1) {
 #pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
-            const int j = 2 * g + jj;
-            if constexpr (TERMS == 1) {
+            for (int j = 2 * g; j < 2 * g + 2; ++j) {
               uint32_t A[2][4];
 #pragma unroll
               for (int mt = 0; mt < 2; ++mt)
@@ -475,47 +497,56 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                   uint32_t q2[2];
-                  lds_words<2>(frag[nt] + (2 * j + m) * (frag_rows * 32), q2);
+                  load_words<2>(frag[nt] + (2 * j + m) * kFragStride, q2);
 #pragma unroll
-                  for (int mt = 0; mt < 2; ++mt) ptx::mma_16832(acc[mt][nt], A[mt], q2[0], q2[1]);
+                  for (int mt = 0; mt < 2; ++mt) {
+                    float d[4];
+                    ptx::mma_16832(d, A[mt], q2[0], q2[1]);
+                    S2[mt][nt][0] = ptx::fma_f32x2(ptx::f32x2(d[0], d[1]), ks[mt][0], S2[mt][nt][0]);
+                    S2[mt][nt][1] = ptx::fma_f32x2(ptx::f32x2(d[2], d[3]), ks[mt][1], S2[mt][nt][1]);
+                  }
                 }
-            } else {
-#pragma unroll
-              for (int p = 0; p < 2; ++p) {
-                uint32_t A[2][4];
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                  for (int x = 0; x < 2; ++x) {
-                    A[mt][x] = p == 0 ? nibbles<0>(kw[mt][x][j]) : nibbles<2>(kw[mt][x][j]);
-                    A[mt][2 + x] = p == 0 ? nibbles<1>(kw[mt][x][j]) : nibbles<3>(kw[mt][x][j]);
-                  }
-#pragma unroll
-                for (int m = 0; m < TERMS; ++m)
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) {
-                    uint32_t q2[2];
-                    lds_words<2>(frag[nt] + ((2 * j + p) * TERMS + m) * (frag_rows * 32), q2);
-#pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) ptx::mma_16816(acc[mt][nt], A[mt], q2[0], q2[1]);
-                  }
-              }
             }
-          }
+          } else {
+            float acc[2][NT][4];
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
+            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float ks = half_at(kp[mt][x], g), kl = half_at(kp[mt][x], GK + g);
+              for (int nt = 0; nt < NT; ++nt) {
+                ptx::f32x2_split(ptx::mul_f32x2(qsum2[g][nt], ptx::f32x2(-16.f, -16.f)), acc[mt][nt][0], acc[mt][nt][1]);
+                acc[mt][nt][2] = acc[mt][nt][0];
+                acc[mt][nt][3] = acc[mt][nt][1];
+              }
+#pragma unroll
+            for (int jp = 4 * g; jp < 4 * g + 4; ++jp) {
+              const int j = jp >> 1;
+              uint32_t A[2][4];
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  A[mt][x] = jp & 1 ? nibbles<2>(kw[mt][x][j], masks) : nibbles<0>(kw[mt][x][j], masks);
+                  A[mt][2 + x] = jp & 1 ? nibbles<3>(kw[mt][x][j], masks) : nibbles<1>(kw[mt][x][j], masks);
+                }
+#pragma unroll
+              for (int m = 0; m < TERMS; ++m)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  uint32_t q2[2];
+                  load_words<2>(frag[nt] + (jp * TERMS + m) * kFragStride, q2);
+#pragma unroll
+                  for (int mt = 0; mt < 2; ++mt) ptx::mma_16816(acc[mt][nt], A[mt], q2[0], q2[1]);
+                }
+            }
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float& sc = S[mt][nt][2 * x + e];
-                  sc = g == 0 ? kl * qsum[0][nt][e] : fmaf(kl, qsum[g][nt][e], sc);
-                  sc = fmaf(ks, acc[mt][nt][2 * x + e], sc);
-                }
-            }
+                for (int x = 0; x < 2; ++x)
+                  S2[mt][nt][x] = ptx::fma_f32x2(ptx::f32x2(acc[mt][nt][2 * x], acc[mt][nt][2 * x + 1]), ks[mt][x],
+                                                 S2[mt][nt][x]);
+          }
         }
       }
       // ---- P = 2^(S - ref)
@@ -527,24 +558,32 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (gone || j0 + mt * 16 + (e >> 1) * 8 + r >= lim[nt][e & 1]) {
-                S[mt][nt][e] = -INFINITY;
-                vis &= ~(1u << ((mt * NT + nt) * 4 + e));
-              }
+            for (int x = 0; x < 2; ++x) {
+              float v[2];
+              ptx::f32x2_split(S2[mt][nt][x], v[0], v[1]);
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (gone || j0 + mt * 16 + x * 8 + r >= lim[nt][e]) {
+                  v[e] = -INFINITY;
+                  vis &= ~(1u << ((mt * NT + nt) * 4 + 2 * x + e));
+                }
+              S2[mt][nt][x] = ptx::f32x2(v[0], v[1]);
+            }
       }
       if (a.accumulate) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int n = nt * 8 + 2 * c + (e & 1);
-            if (n < rows) {
-              float* to = gr.score + (int64_t(u) * gr.rows_per_tile + n) * kKv4Sub + (e >> 1) * 8 + r;
-              to[0] = S[0][nt][e] * sl2[nt][e & 1];
-              to[16] = S[1][nt][e] * sl2[nt][e & 1];
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              float v[2];
+              ptx::f32x2_split(ptx::mul_f32x2(S2[mt][nt][x], ptx::f32x2(sl2[nt][0], sl2[nt][1])), v[0], v[1]);
+              const int n = nt * 8 + 2 * c;
+              float* to = gr.score + (int64_t(u) * gr.rows_per_tile + n) * kKv4Sub + mt * 16 + x * 8 + r;
+              if (n < rows) to[0] = v[0];
+              if (n + 1 < rows) to[kKv4Sub] = v[1];
             }
-          }
       }
       float P[2][NT][4];
       float top = -INFINITY;
@@ -553,48 +592,64 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            P[mt][nt][e] = fmaf(S[mt][nt][e], sl2[nt][e & 1], -ref[nt][e & 1]);
-            top = fmaxf(top, P[mt][nt][e]);
+          for (int x = 0; x < 2; ++x) {
+            float* v = P[mt][nt] + 2 * x;
+            ptx::f32x2_split(ptx::fma_f32x2(S2[mt][nt][x], ptx::f32x2(sl2[nt][0], sl2[nt][1]),
+                                            ptx::f32x2(-ref[nt][0], -ref[nt][1])), v[0], v[1]);
+            top = fmaxf(top, fmaxf(v[0], v[1]));
           }
       if (__any_sync(0xffffffffu, top > kSlack)) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          float keep[2], most[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float v[2];
+              ptx::f32x2_split(ptx::mul_f32x2(S2[mt][nt][x], ptx::f32x2(sl2[nt][0], sl2[nt][1])), v[0], v[1]);
+              most[0] = fmaxf(most[0], v[0]);
+              most[1] = fmaxf(most[1], v[1]);
+            }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float m = fmaxf(fmaxf(S[0][nt][e], S[0][nt][e + 2]), fmaxf(S[1][nt][e], S[1][nt][e + 2])) * sl2[nt][e];
+            float m = most[e];
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
             m = fmaxf(m, ref[nt][e]);
-            const float keep = ptx::ex2(ref[nt][e] - m);
+            keep[e] = ptx::ex2(ref[nt][e] - m);
             ref[nt][e] = m;
-            sum[nt][e] *= keep;
-#pragma unroll
-            for (int g = 0; g < GV; ++g) {
-              ooff[g][nt][e] *= keep;
-              osix[g][nt][e] *= keep;
-              osix[g][nt][e + 2] *= keep;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                O[g][i][nt][e] *= keep;
-                O[g][i][nt][e + 2] *= keep;
-              }
-            }
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-              for (int x = 0; x < 4; x += 2) P[mt][nt][e + x] = fmaf(S[mt][nt][e + x], sl2[nt][e], -m);
           }
+          const uint64_t keep2 = ptx::f32x2(keep[0], keep[1]);
+          sum2[nt] = ptx::mul_f32x2(sum2[nt], keep2);
+#pragma unroll
+          for (int g = 0; g < GV; ++g) {
+            ooff2[g][nt] = ptx::mul_f32x2(ooff2[g][nt], keep2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              osix[g][nt][e] *= keep[e & 1];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) O[g][i][nt][e] *= keep[e & 1];
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              ptx::f32x2_split(ptx::fma_f32x2(S2[mt][nt][x], ptx::f32x2(sl2[nt][0], sl2[nt][1]),
+                                              ptx::f32x2(-ref[nt][0], -ref[nt][1])), P[mt][nt][2 * x], P[mt][nt][2 * x + 1]);
+        }
       }
+      uint64_t P2[2][NT][2];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            P[mt][nt][e] = ptx::ex2(P[mt][nt][e]);
-            sum[nt][e & 1] += P[mt][nt][e];
+          for (int x = 0; x < 2; ++x) {
+            P2[mt][nt][x] = ptx::f32x2(ptx::ex2(P[mt][nt][2 * x]), ptx::ex2(P[mt][nt][2 * x + 1]));
+            sum2[nt] = ptx::add_f32x2(sum2[nt], P2[mt][nt][x]);
           }
       // ---- O^T += V^T P^T, 16 tokens at a time
 #pragma unroll
@@ -603,15 +658,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t tok = mt * 16 + 2 * c + (i & 1) + (i >> 1) * 8;
-          lds_words<GV>(st + f.vc() + tok * (DV / 2) + r * (GV * 4), vw[i]);
+          load_words<GV>(st + f.vc() + tok * (DV / 2) + r * (GV * 4), vw[i]);
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const uint32_t tok = mt * 16 + x * 8 + r;
           if constexpr (GV == 2) {
-            lds_words<1>(st + f.vs() + tok * 4, vs[x]);
+            load_words<1>(st + f.vs() + tok * 4, vs[x]);
           } else {
-            vs[x][0] = __float_as_uint(lds_bf16(st + f.vs() + tok * 2)) >> 16;
+            vs[x][0] = __float_as_uint(load_bf16(st + f.vs() + tok * 2)) >> 16;
           }
         }
 #pragma unroll
@@ -619,22 +674,24 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
           // P s of this group as B fragments, and P low on the side
           uint32_t B0[NT][TERMS], B1[NT][TERMS];
           const float s0 = half_at(vs[0], g), s1 = half_at(vs[1], g);
-          const float l0 = lds_bf16(st + f.vl() + (g * kKv4Sub + mt * 16 + r) * 2);
-          const float l1 = lds_bf16(st + f.vl() + (g * kKv4Sub + mt * 16 + 8 + r) * 2);
+          const float l0 = load_bf16(st + f.vl() + (g * kKv4Sub + mt * 16 + r) * 2);
+          const float l1 = load_bf16(st + f.vl() + (g * kKv4Sub + mt * 16 + 8 + r) * 2);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const float* p = P[mt][nt];
-            float ps[4] = {p[0] * s0, p[1] * s0, p[2] * s1, p[3] * s1};
+            float ps[4];
+            ptx::f32x2_split(ptx::mul_f32x2(P2[mt][nt][0], ptx::f32x2(s0, s0)), ps[0], ps[1]);
+            ptx::f32x2_split(ptx::mul_f32x2(P2[mt][nt][1], ptx::f32x2(s1, s1)), ps[2], ps[3]);
             if (masked) {  // what an unseen slot holds (NaN, in the worst case) reaches nothing
+              float pl[4];
+              ptx::f32x2_split(ptx::mul_f32x2(P2[mt][nt][0], ptx::f32x2(l0, l0)), pl[0], pl[1]);
+              ptx::f32x2_split(ptx::mul_f32x2(P2[mt][nt][1], ptx::f32x2(l1, l1)), pl[2], pl[3]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const bool see = (vis >> ((mt * NT + nt) * 4 + e)) & 1;
-                if (!see) ps[e] = 0.f;
-                if (see) ooff[g][nt][e & 1] = fmaf(p[e], e < 2 ? l0 : l1, ooff[g][nt][e & 1]);
-              }
+              for (int e = 0; e < 4; ++e)
+                if (!((vis >> ((mt * NT + nt) * 4 + e)) & 1)) ps[e] = pl[e] = 0.f;
+              ooff2[g][nt] = ptx::add_f32x2(ooff2[g][nt], ptx::f32x2(pl[0] + pl[2], pl[1] + pl[3]));
             } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) ooff[g][nt][e & 1] = fmaf(p[e], e < 2 ? l0 : l1, ooff[g][nt][e & 1]);
+              ooff2[g][nt] = ptx::fma_f32x2(P2[mt][nt][0], ptx::f32x2(l0, l0), ooff2[g][nt]);
+              ooff2[g][nt] = ptx::fma_f32x2(P2[mt][nt][1], ptx::f32x2(l1, l1), ooff2[g][nt]);
             }
             split_pair<TERMS>(ps[0], ps[1], B0[nt]);
             split_pair<TERMS>(ps[2], ps[3], B1[nt]);
@@ -646,10 +703,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
           }
           const uint32_t lo0 = __byte_perm(vw[0][g], vw[1][g], 0x5410), hi0 = __byte_perm(vw[0][g], vw[1][g], 0x7632);
           const uint32_t lo1 = __byte_perm(vw[2][g], vw[3][g], 0x5410), hi1 = __byte_perm(vw[2][g], vw[3][g], 0x7632);
-          const uint32_t A[5][4] = {{nibble0<TERMS>(lo0), nibble0<TERMS>(hi0), nibble0<TERMS>(lo1), nibble0<TERMS>(hi1)},
-                                    {nibbles<1>(lo0), nibbles<1>(hi0), nibbles<1>(lo1), nibbles<1>(hi1)},
-                                    {nibbles<2>(lo0), nibbles<2>(hi0), nibbles<2>(lo1), nibbles<2>(hi1)},
-                                    {nibbles<3>(lo0), nibbles<3>(hi0), nibbles<3>(lo1), nibbles<3>(hi1)},
+          const uint32_t A[5][4] = {{nibble0<TERMS>(lo0, masks), nibble0<TERMS>(hi0, masks), nibble0<TERMS>(lo1, masks), nibble0<TERMS>(hi1, masks)},
+                                    {nibbles<1>(lo0, masks), nibbles<1>(hi0, masks), nibbles<1>(lo1, masks), nibbles<1>(hi1, masks)},
+                                    {nibbles<2>(lo0, masks), nibbles<2>(hi0, masks), nibbles<2>(lo1, masks), nibbles<2>(hi1, masks)},
+                                    {nibbles<3>(lo0, masks), nibbles<3>(hi0, masks), nibbles<3>(lo1, masks), nibbles<3>(hi1, masks)},
                                     {0xC180C180u, 0xC180C180u, 0xC180C180u, 0xC180C180u}};  // -16
 #pragma unroll
           for (int m = 0; m < TERMS; ++m)
@@ -665,12 +722,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
       ++done;
       if (++stage == gr.stages) stage = 0, phase ^= 1;
       load_next();
-      cur.next(base, a.c.num_seqs, per);
+      cur.next(base, a.c.num_seqs, per, row_tiles);
     }
 
     // ---- the warp's sums
+    float sum[NT][2], ooff[GV][NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      ptx::f32x2_split(sum2[nt], sum[nt][0], sum[nt][1]);
+#pragma unroll
+      for (int g = 0; g < GV; ++g) ptx::f32x2_split(ooff2[g][nt], ooff[g][nt][0], ooff[g][nt][1]);
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -679,6 +740,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
 #pragma unroll
           for (int g = 0; g < GV; ++g) ooff[g][nt][e] += __shfl_xor_sync(0xffffffffu, ooff[g][nt][e], o);
         }
+    }
     const bool starts = run0 >= w0, ends = run0 + per_run <= w1;
     if (starts && ends) {  // whole: done
 #pragma unroll
@@ -957,7 +1019,7 @@ cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
   gr.off_base = off;
   off = up(off + 4 * (a.c.num_seqs + 1), 128);
   gr.off_frag = off;
-  off += C::NW * (C::DQK / 16 * C::TERMS * 32) * gr.rows_per_tile;
+  off += C::NW * (C::DQK / 16 * C::TERMS * 32) * C::COLS;
   gr.off_stat = off;
   off += 2 * C::NW * 3 * C::COLS * 4;
   gr.off_stash = off;
