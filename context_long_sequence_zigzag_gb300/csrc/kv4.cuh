@@ -41,7 +41,7 @@ struct Kv4Cache {
 };
 
 // Sites of the device error word (0x300 | site).
-enum : int32_t { kKv4Page = 1, kKv4Length = 2, kKv4Slot = 3, kKv4Row = 4, kKv4Wait = 5 };
+enum : int32_t { kKv4Page = 1, kKv4Length = 2, kKv4Slot = 3, kKv4Row = 4 };
 
 __device__ __forceinline__ void kv4_error(const Kv4Cache& c, int32_t site) {
   if (c.err) atomicCAS(c.err, 0, 0x300 | site);

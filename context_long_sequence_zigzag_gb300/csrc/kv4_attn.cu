@@ -48,7 +48,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoRef = -1e30f;   // a row that has seen nothing
 constexpr float kSlack = 10.f;     // how far (log2) an element may exceed the reference
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 template <int DQK_, int DV_, int NT_, int TERMS_, int NW_>
 struct Cfg {
@@ -57,11 +56,15 @@ struct Cfg {
   static constexpr int KW = DQK / 32;  // words of a K row a lane unpacks
   static constexpr int COLS = 8 * NT;
   static constexpr int THREADS = 32 * NW;
+  static constexpr int SUB = Kv4Format(DQK, DV).sub();
+  static constexpr int STAGES = SUB <= 2400 ? 4 : (SUB <= 3500 ? 3 : 2);  // sub-blocks on their way to a warp
 };
 
-// The shares: sub-blocks ("units") of all runs end to end, cut over n CTAs, a
-// unit a warp at least (a CTA with fewer takes as long, and every CTA that a
-// run is cut over leaves a partial to join).  No share is empty.
+// The shares: all runs end to end, a run being one unit for its start (its
+// queries are made operands, which takes about as long as a sub-block) and
+// one a sub-block, cut over n CTAs; a unit a warp at least (a CTA with fewer
+// takes as long, and every CTA that a run is cut over leaves a partial to
+// join).  No share is empty.
 __device__ __forceinline__ int share_count(int units, int ctas, int warps) { return min(ctas, (units + warps - 1) / warps); }
 __host__ __device__ __forceinline__ int64_t share_begin(int64_t units, int n, int c) { return int64_t(c) * units / n; }
 __device__ __forceinline__ int share_of(int64_t units, int n, int64_t u) { return int(((u + 1) * n - 1) / units); }
@@ -73,7 +76,6 @@ struct Grid {
   int ctas;           // shares at most
   int warps;          // of a CTA of the first kernel
   int rows_per_tile;  // rows of a row tile (at most COLS)
-  int stages;
   uint32_t off_base, off_frag, off_stat, off_stash, off_ring;
   uint32_t off_join;  // the join's weights behind its scan
   float* part;   // [ctas][2][part_floats]
@@ -88,7 +90,8 @@ __device__ void scan_lengths(const Kv4AttnArgs& a, int per, int32_t* base, int32
   int carry = 0;
   for (int b0 = 0; b0 < a.c.num_seqs; b0 += THREADS) {
     const int b = b0 + tid;
-    int x = b < a.c.num_seqs ? (kv4_length(a.c, a.lengths, b) + kKv4Sub - 1) / kKv4Sub * per : 0;
+    const int subs = b < a.c.num_seqs ? (kv4_length(a.c, a.lengths, b) + kKv4Sub - 1) / kKv4Sub : 0;
+    int x = subs > 0 ? (subs + 1) * per : 0;
     const int own = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -196,15 +199,14 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t (&t)[TERMS
   }
 }
 
-// x and y, times `unit`, as two e4m3 bytes (x low); x and y become what is left over
-__device__ __forceinline__ uint32_t e4m3_pair(float& x, float& y, float unit) {
-  x *= unit;
-  y *= unit;
-  const __nv_fp8x2_storage_t t = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
-  const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(t, __NV_E4M3)));
-  x -= back.x;
-  y -= back.y;
-  return t;
+__device__ __forceinline__ uint32_t e4m3_pair(float x, float y) {  // x in the low byte
+  return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+}
+// x to four significant bits, and what is left (Dekker's splitting: both exact)
+__device__ __forceinline__ void split4(float x, float& high, float& rest) {
+  const float t = __fmul_rn(x, 1048577.f);  // 2^20 + 1
+  high = __fsub_rn(t, __fsub_rn(t, x));
+  rest = __fsub_rn(x, high);
 }
 
 __device__ __forceinline__ void load_q8(const float* p, float (&x)[8]) {
@@ -237,7 +239,7 @@ __device__ __forceinline__ int64_t row_index(const Kv4AttnArgs& a, int b, int h,
   return (int64_t(b) * a.n_q + *t) * a.c.hq + *head;
 }
 
-// Walks units: sub-block i of run `run` of sequence b.
+// Walks units: unit i of run `run` of sequence b, its start (i = 0) or sub-block i - 1.
 struct UnitCursor {
   int b, run, i, per_run, h;  // h: the run's kv head
   __device__ void seek(const int32_t* base, int n, int per, int row_tiles, int u) {
@@ -261,14 +263,13 @@ struct UnitCursor {
 
 template <typename C, typename E>
 __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnArgs a, const Grid gr) {
-  constexpr int NT = C::NT, GK = C::GK, GV = C::GV, NW = C::NW, DQK = C::DQK, DV = C::DV, TERMS = C::TERMS;
+  constexpr int NT = C::NT, GK = C::GK, GV = C::GV, NW = C::NW, DQK = C::DQK, DV = C::DV, TERMS = C::TERMS, STAGES = C::STAGES;
   constexpr Kv4Format f(DQK, DV);
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[NW * 4];
-  __shared__ int s_abort;
   __shared__ int32_t s_scan[NW];
-  __shared__ int32_t s_run[2 * NW];  // run of warp w's first partial (2w) and of its last (2w + 1), or -1
-  const uint32_t sbase = ptx::smem_u32(smem);
+  // partials of runs cut over warps: the run of warp w's first (slot 2w) and of its last (2w + 1), or -1; then the slots
+  // that hold one, in order, and where in that list a run's begin
+  __shared__ int32_t s_run[2 * NW], s_slot[2 * NW], s_group[2 * NW + 1], s_groups;
   int32_t* base = reinterpret_cast<int32_t*>(smem + gr.off_base);
   float* stat_s = reinterpret_cast<float*>(smem + gr.off_stat);    // [2 NW][2][COLS]: the partials' references and sums
   float* top_s = stat_s + 2 * NW * 2 * C::COLS;                    // [2 NW][COLS]: the largest of a run's references
@@ -277,15 +278,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
   const int row_tiles = a.row_tiles, per = a.c.hkv * row_tiles;
-  const uint32_t ring = sbase + gr.off_ring + uint32_t(warp * gr.stages) * f.sub();
-  const uint8_t* ring_p = smem + gr.off_ring + (warp * gr.stages) * f.sub();
-  const uint32_t bar0 = ptx::smem_u32(&bars[warp * 4]);
-  if (lane == 0) {
-    for (int s = 0; s < gr.stages; ++s) ptx::mbar_init(bar0 + 8 * s, 1);
-    ptx::fence_barrier_init();
-    s_run[2 * warp] = s_run[2 * warp + 1] = -1;
-  }
-  if (tid == 0) s_abort = 0;
+  const uint8_t* ring_p = smem + gr.off_ring + warp * (STAGES * f.sub());
+  const uint32_t ring = ptx::smem_u32(ring_p);
+  if (lane == 0) s_run[2 * warp] = s_run[2 * warp + 1] = -1;
   scan_lengths<C::THREADS>(a, per, base, s_scan);
   const int units = base[a.c.num_seqs];
   const int shares = share_count(units, gr.ctas, NW);
@@ -293,45 +288,49 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
   const int u0 = int(share_begin(units, shares, blockIdx.x)), u1 = int(share_begin(units, shares, blockIdx.x + 1));
   // this warp's units
   const int w0 = u0 + (u1 - u0) * warp / NW, w1 = u0 + (u1 - u0) * (warp + 1) / NW;
-  const ptx::WaitCtx wctx{&s_abort, a.c.err, kWaitLimitNs};
 
-  // ---- its copies, `stages` ahead
+  // ---- its copies, STAGES ahead, 16 bytes a lane at a time
   UnitCursor cur, ahead;
-  int loaded = 0, load_stage = 0;
-  uint32_t absent = 0;  // bit s: the page of stage s's unit is not in the pool
+  int load_unit = w0, load_stage = 0;
+  uint32_t absent = 0;  // bit s: the page of stage s's sub-block is not in the pool
   int next_page = 0;
-  auto look_up = [&]() {
-    if (w0 + loaded >= w1) return;
-    const int page = __ldg(a.c.table + int64_t(ahead.b) * a.c.max_pages + ahead.i / (CP_KV4_PAGE / kKv4Sub));
-    next_page = page < a.c.num_pages ? page : -1;
+  auto look_up = [&]() {  // the next sub-block, past starts of runs
+    if (load_unit < w1 && ahead.i == 0) {
+      ++load_unit;
+      ahead.next(base, a.c.num_seqs, per, row_tiles);
+    }
+    if (load_unit < w1)
+      next_page = __ldg(a.c.table + int64_t(ahead.b) * a.c.max_pages + (ahead.i - 1) / (CP_KV4_PAGE / kKv4Sub));
   };
   auto load_next = [&]() {
-    if (w0 + loaded >= w1) return;
-    const int page = next_page;  // looked up while the unit before was on its way
-    if (page < 0) kv4_error(a.c, kKv4Page);
-    const int s = load_stage;
-    if (++load_stage == gr.stages) load_stage = 0;
-    absent = page < 0 ? absent | (1u << s) : absent & ~(1u << s);
-    if (lane == 0) {
+    if (load_unit < w1) {
+      // looked up a unit ago; judged only now, so that nothing waited for it
+      const int page = next_page < a.c.num_pages ? next_page : -1;
       if (page >= 0) {
-        ptx::mbar_arrive_expect_tx(bar0 + 8 * s, uint32_t(f.sub()));
-        ptx::bulk_load(ring + uint32_t(s) * f.sub(),
-                       a.c.pages + (int64_t(page) * a.c.hkv + ahead.h) * f.block() +
-                           ahead.i % (CP_KV4_PAGE / kKv4Sub) * f.sub(),
-                       uint32_t(f.sub()), bar0 + 8 * s);
+        const uint8_t* src = a.c.pages + (int64_t(page) * a.c.hkv + ahead.h) * f.block() +
+                             (ahead.i - 1) % (CP_KV4_PAGE / kKv4Sub) * f.sub() + lane * 16;
+        const uint32_t dst = ring + load_stage * f.sub() + lane * 16;
+#pragma unroll
+        for (int o = 0; o < f.sub(); o += 512)
+          if (o + 512 <= f.sub() || lane * 16 < f.sub() - o) ptx::cp_async16(dst + o, src + o);
+        absent &= ~(1u << load_stage);
       } else {
-        ptx::mbar_arrive(bar0 + 8 * s);
+        kv4_error(a.c, kKv4Page);
+        absent |= 1u << load_stage;
       }
+      if (++load_stage == STAGES) load_stage = 0;
+      ++load_unit;
+      ahead.next(base, a.c.num_seqs, per, row_tiles);
+      look_up();
     }
-    ++loaded;
-    ahead.next(base, a.c.num_seqs, per, row_tiles);
-    look_up();
+    ptx::cp_async_commit();  // a group a call, empty or not: the waits count them
   };
   if (w0 < w1) {
     cur.seek(base, a.c.num_seqs, per, row_tiles, w0);
     ahead = cur;
     look_up();
-    for (int s = 0; s < gr.stages; ++s) load_next();
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) load_next();
   }
   ptx::grid_launch_dependents();
 
@@ -340,16 +339,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
   float O[GV][4][NT][4], osix[GV][NT][4], ref[NT][2];
   uint64_t ooff2[GV][NT], sum2[NT];  // pairs: columns 2c and 2c + 1
   const Masks masks;
-  int done = 0, stage = 0;
-  uint32_t phase = 0;
-  bool ok = true, last = false;  // last: the registers hold a partial that the next warp's units continue
-  for (int u = w0; u < w1 && ok && !last;) {
+  int stage = 0;
+  bool last = false;  // last: the registers hold a partial that the next warp's units continue
+  for (int u = w0; u < w1 && !last;) {
     // ---- a run, as far as this warp's units go
     const int b = cur.b, run = cur.run, h = cur.h, run0 = u - cur.i, per_run = cur.per_run;
-    const int seg1 = min(w1, run0 + per_run);
+    const int seg1 = min(w1, run0 + per_run), real0 = run0 + 1;  // sub-blocks from unit real0 on
+    if (cur.i == 0) {
+      ++u;
+      cur.next(base, a.c.num_seqs, per, row_tiles);
+      if (u >= w1) break;  // the next warp has all of its sub-blocks
+    }
     const int n0 = (run - h * row_tiles) * gr.rows_per_tile;
     const int rows = min(gr.rows_per_tile, a.rows - n0);
-    const int len = min(kv4_length(a.c, a.lengths, b), per_run * kKv4Sub);
+    const int len = min(kv4_length(a.c, a.lengths, b), (per_run - 1) * kKv4Sub);
     // ---- its queries as B fragments (kstep 2j + p: channels 8w + 2p, 8w + 2p + 4 and the next two, w = 4j + c), and
     // the sums of their groups.  Columns past the rows repeat rows; nothing of them is written out.
     uint64_t qsum2[GK][NT];
@@ -384,20 +387,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
         // codes are n 2^-9 as e4m3 bytes: scores come out times unit / 512
         factor = big >= 0x7f800000u ? NAN : factor * (512.f / unit);
 #pragma unroll
-        for (int j = 0; j < DQK / 32; ++j)
+        for (int j = 0; j < DQK / 32; ++j) {
+          float hi[8], lo[8];
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            // bytes: channels 8w, 8w + 2, .. and 8w + 1, 8w + 3, ..
-            uint32_t f0 = 0, f1 = 0;
-#pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-              const uint32_t even = e4m3_pair(x[j][i], x[j][i + 2], m == 0 ? unit : 1.f);
-              const uint32_t odd = e4m3_pair(x[j][i + 1], x[j][i + 3], m == 0 ? unit : 1.f);
-              f0 |= even << (4 * i);
-              f1 |= odd << (4 * i);
-            }
-            *reinterpret_cast<uint2*>(frag[nt] + (2 * j + m) * kFragStride) = make_uint2(f0, f1);
-          }
+          for (int i = 0; i < 8; ++i) split4(x[j][i] * unit, hi[i], lo[i]);
+          // bytes: channels 8w, 8w + 2, .. and 8w + 1, 8w + 3, ..
+          uint8_t* to = frag[nt] + 2 * j * kFragStride;
+          *reinterpret_cast<uint2*>(to) = make_uint2(e4m3_pair(hi[0], hi[2]) | e4m3_pair(hi[4], hi[6]) << 16,
+                                                     e4m3_pair(hi[1], hi[3]) | e4m3_pair(hi[5], hi[7]) << 16);
+          *reinterpret_cast<uint2*>(to + kFragStride) = make_uint2(e4m3_pair(lo[0], lo[2]) | e4m3_pair(lo[4], lo[6]) << 16,
+                                                                   e4m3_pair(lo[1], lo[3]) | e4m3_pair(lo[5], lo[7]) << 16);
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < DQK / 32; ++j) {
@@ -449,11 +449,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
 
     for (; u < seg1; ++u) {
       const int s = stage;
-      ok = ptx::mbar_wait_w(bar0 + 8 * s, phase, kKv4Wait, wctx);
-      if (!ok) break;
+      ptx::cp_async_wait<STAGES - 1>();
+      __syncwarp();
       const uint8_t* st = ring_p + s * f.sub();
       const bool gone = (absent >> s) & 1;
-      const int j0 = (u - run0) * kKv4Sub;
+      const int j0 = (u - real0) * kKv4Sub;
 
       // ---- S^T = K Q^T
       uint64_t S2[2][NT][2];  // pairs of columns: row r, row r + 8
@@ -719,8 +719,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
         }
       }
       __syncwarp();  // the stage has been read
-      ++done;
-      if (++stage == gr.stages) stage = 0, phase ^= 1;
+      if (++stage == STAGES) stage = 0;
       load_next();
       cur.next(base, a.c.num_seqs, per, row_tiles);
     }
@@ -741,7 +740,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
           for (int g = 0; g < GV; ++g) ooff[g][nt][e] += __shfl_xor_sync(0xffffffffu, ooff[g][nt][e], o);
         }
     }
-    const bool starts = run0 >= w0, ends = run0 + per_run <= w1;
+    const bool starts = real0 >= w0, ends = run0 + per_run <= w1;
     if (starts && ends) {  // whole: done
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -795,20 +794,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
         }
     }
   }
-  if (!ok) {  // copies still in flight land before the rings are used for anything else
-    volatile int no_abort = 0;
-    const ptx::WaitCtx drain{&no_abort, nullptr, kWaitLimitNs};
-    for (int i = max(done, loaded - gr.stages); i < loaded; ++i)
-      ptx::mbar_wait_w(bar0 + 8 * (i % gr.stages), (i / gr.stages) & 1, kKv4Wait, drain);
-  }
   if (!last) __syncthreads();
   __syncthreads();
 
   // ---- runs cut over warps: their partials, in order, joined by the whole CTA.  First what every partial weighs:
   // lane = partial, a warp a row; partials of one run find their largest reference among them.
   constexpr int kSlots = 2 * NW;
+  const int id = lane < kSlots ? s_run[lane] : -1;
+  const uint32_t held = __ballot_sync(0xffffffffu, id >= 0), under = (1u << lane) - 1u;
   for (int n = warp; n < gr.rows_per_tile; n += NW) {
-    const int id = lane < kSlots ? s_run[lane] : -1;
     float* st = stat_s + (lane < kSlots ? lane : 0) * 2 * C::COLS + n;
     const float m = id < 0 ? kNoRef : st[0], l = id < 0 ? 0.f : st[C::COLS];
     const uint32_t mask = __match_any_sync(0xffffffffu, id);
@@ -817,55 +811,59 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
     const int top = __reduce_max_sync(mask, order);
     const float mm = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
     const float k = l == 0.f ? 0.f : ptx::ex2(m - mm);  // 0: saw nothing
-    __syncwarp();
-    if (lane < kSlots) {
+    if (id >= 0) {
       st[0] = k;
       st[C::COLS] = l == 0.f ? 0.f : k * l;
       top_s[lane * C::COLS + n] = mm;
     }
   }
+  if (warp == NW - 1) {
+    const int before = held & under ? 31 - __clz(held & under) : -1;
+    const int id_before = __shfl_sync(0xffffffffu, id, max(before, 0));
+    const bool first = id >= 0 && (before < 0 || id_before != id);
+    const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+    if (id >= 0) s_slot[__popc(held & under)] = lane;
+    if (first) s_group[__popc(firsts & under)] = __popc(held & under);
+    if (lane == 0) {
+      s_groups = __popc(firsts);
+      s_group[__popc(firsts)] = __popc(held);
+    }
+  }
   __syncthreads();
-  for (int s0 = 0; s0 < kSlots;) {
-    const int id = s_run[s0];
-    int s1 = s0 + 1;
-    if (id >= 0) {
-      while (s1 < kSlots && (s_run[s1] < 0 || s_run[s1] == id)) ++s1;
-      const int b = id / per, run = id - b * per;
-      const int per_run = (base[b + 1] - base[b]) / per, run0 = base[b] + run * per_run;
-      const int h = run / row_tiles, n0 = (run - h * row_tiles) * gr.rows_per_tile;
-      const int rows = min(gr.rows_per_tile, a.rows - n0);
-      const bool whole = run0 >= u0 && run0 + per_run <= u1;
-      float* part = gr.part + (int64_t(blockIdx.x) * 2 + (run0 >= u0)) * part_floats(C::COLS, DV);
-      for (int e = tid; e < rows * DV; e += C::THREADS) {
-        const int n = e / DV, d = e - n * DV;
-        float l = 0.f, x = 0.f;
+  for (int g = 0; g < s_groups; ++g) {
+    const int i0 = s_group[g], i1 = s_group[g + 1], rid = s_run[s_slot[i0]];
+    const int b = rid / per, run = rid - b * per;
+    const int per_run = (base[b + 1] - base[b]) / per, run0 = base[b] + run * per_run;
+    const int h = run / row_tiles, n0 = (run - h * row_tiles) * gr.rows_per_tile;
+    const int rows = min(gr.rows_per_tile, a.rows - n0);
+    const bool whole = run0 + 1 >= u0 && run0 + per_run <= u1;
+    float* part = gr.part + (int64_t(blockIdx.x) * 2 + (run0 + 1 >= u0)) * part_floats(C::COLS, DV);
+    for (int e = tid; e < rows * DV; e += C::THREADS) {
+      const int n = e / DV, d = e - n * DV;
+      float l = 0.f, x = 0.f;
 #pragma unroll 4
-        for (int s = s0; s < s1; ++s) {
-          const float* st = stat_s + s * 2 * C::COLS + n;
-          const float k = s_run[s] < 0 ? 0.f : st[0];
-          if (k != 0.f) {
-            l += st[C::COLS];
-            x += k * ((s & 1) ? last_s : stash_s)[(s >> 1) * gr.rows_per_tile * DV + e];
-          }
-        }
-        const float m = top_s[s0 * C::COLS + n];
-        if (whole) {
-          int t, head;
-          const int64_t row = row_index(a, b, h, n0 + n, &t, &head);
-          store_o(a, row * DV + d, l == 0.f ? 0.f : x / l);
-          if (d == 0)
-            a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] =
-                l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        } else {
-          part[2 * C::COLS + e] = x;
-          if (d == 0) {
-            part[n] = m;
-            part[C::COLS + n] = l;
-          }
+      for (int i = i0; i < i1; ++i) {
+        const int s = s_slot[i];
+        const float* st = stat_s + s * 2 * C::COLS + n;
+        l += st[C::COLS];
+        x = fmaf(st[0], ((s & 1) ? last_s : stash_s)[(s >> 1) * gr.rows_per_tile * DV + e], x);
+      }
+      const float m = top_s[s_slot[i0] * C::COLS + n];
+      if (whole) {
+        int t, head;
+        const int64_t row = row_index(a, b, h, n0 + n, &t, &head);
+        store_o(a, row * DV + d, l == 0.f ? 0.f : x / l);
+        if (d == 0)
+          a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] =
+              l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      } else {
+        part[2 * C::COLS + e] = x;
+        if (d == 0) {
+          part[n] = m;
+          part[C::COLS + n] = l;
         }
       }
     }
-    s0 = s1;
   }
 }
 
@@ -895,7 +893,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnArg
     if (n0 + n >= a.rows) return;
     int c0 = 0, parts = 0;
     if (per_run > 0) {
-      c0 = share_of(units, shares, run0);
+      c0 = share_of(units, shares, run0 + 1);
       parts = share_of(units, shares, run0 + per_run - 1) - c0 + 1;
       if (parts == 1) return;
     }
@@ -942,14 +940,15 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnArg
   const int lane = threadIdx.x & 31;
   const int warps = (int(gridDim.x) - joins) * (kJoinThreads / 32);
   const int w = (int(blockIdx.x) - joins) * (kJoinThreads / 32) + int(threadIdx.x >> 5);
-  const int64_t all = units / row_tiles;  // sub-blocks of the cache
+  const int64_t all = units / row_tiles;  // units of the cache: row tile by row tile the same
   const int64_t v0 = all * w / warps, v1 = all * (w + 1) / warps;
   int b = 0, last_h = -1, last_b = -1;
   float lse2[8];  // row lane of row tile i (at most 8 tiles are kept)
   for (int64_t v = v0; v < v1; ++v) {
     b = seq_of_unit(base, a.c.num_seqs, b, int(v * row_tiles));
     const int per_run = (base[b + 1] - base[b]) / per;
-    const int at = int(v) - base[b] / row_tiles, h = at / per_run, i = at - h * per_run;
+    const int at = int(v) - base[b] / row_tiles, h = at / per_run, i = at - h * per_run - 1;
+    if (i < 0) continue;  // a run's start
     float add = 0.f;
     for (int rt = 0; rt < row_tiles; ++rt) {
       const int run0 = base[b] + (h * row_tiles + rt) * per_run, n0 = rt * gr.rows_per_tile;
@@ -962,7 +961,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnArg
       } else {
         ls = INFINITY;
         if (lane < rows) {
-          const int c0 = share_of(units, shares, run0), c1 = share_of(units, shares, run0 + per_run - 1);
+          const int c0 = share_of(units, shares, run0 + 1), c1 = share_of(units, shares, run0 + per_run - 1);
           if (c0 == c1) {
             int t, head;
             row_index(a, b, h, n0 + lane, &t, &head);
@@ -981,7 +980,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnArg
 #pragma unroll
         for (int k = 0; k < 8; ++k) lse2[k] = rt == k ? ls : lse2[k];
       }
-      const float* sc = gr.score + int64_t(run0 + i) * gr.rows_per_tile * kKv4Sub + lane;
+      const float* sc = gr.score + int64_t(run0 + 1 + i) * gr.rows_per_tile * kKv4Sub + lane;
       for (int n = 0; n < rows; ++n) add += ptx::ex2(sc[n * kKv4Sub] - __shfl_sync(0xffffffffu, ls, n));
     }
     last_b = b;
@@ -1014,7 +1013,6 @@ uint32_t up(uint32_t x, uint32_t n) { return (x + n - 1) / n * n; }
 
 template <typename C, typename E>
 cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
-  constexpr Kv4Format f(C::DQK, C::DV);
   uint32_t off = 0;
   gr.off_base = off;
   off = up(off + 4 * (a.c.num_seqs + 1), 128);
@@ -1027,11 +1025,9 @@ cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
   off = up(off + partials, 128);
   gr.off_ring = off;
   constexpr uint32_t kMost = 230000;  // 227 KB less the static arrays
-  if (off > kMost) return cudaErrorInvalidValue;
-  gr.stages = int(std::min<uint32_t>(4, (kMost - off) / (C::NW * f.sub())));
-  off += gr.stages * C::NW * f.sub();
   // the rings hold the last partials in the end
-  if (gr.stages < 1 || gr.stages * C::NW * f.sub() < partials) return cudaErrorInvalidValue;
+  off += std::max<uint32_t>(C::STAGES * C::NW * C::SUB, partials);
+  if (off > kMost) return cudaErrorInvalidValue;
   gr.warps = C::NW;
   auto kernel = kv4_attn_kernel<C, E>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(off));
@@ -1062,8 +1058,6 @@ template <int DQK, int DV>
 cudaError_t launch_dims(const Kv4AttnArgs& a, const Grid& gr, int dtype, cudaStream_t st) {
   if (dtype == CP_DT_F32) return launch<Cfg<DQK, DV, 1, 3, 8>, float>(a, gr, st);
   if (cols_of(a.rows, dtype) == 16) return launch<Cfg<DQK, DV, 2, 1, 8>, __nv_bfloat16>(a, gr, st);
-  // sixteen warps where registers and shared memory (partials of few rows) allow
-  if (DQK < 192 && gr.rows_per_tile <= 4) return launch<Cfg<DQK, DV, 1, 1, DQK < 192 ? 16 : 12>, __nv_bfloat16>(a, gr, st);
   return launch<Cfg<DQK, DV, 1, 1, 12>, __nv_bfloat16>(a, gr, st);
 }
 
@@ -1080,7 +1074,7 @@ Layout layout_of(int num_seqs, int hq, int hkv, int dv, int max_pages, int dtype
   L.row_tiles = (L.rows + L.rows_per_tile - 1) / L.rows_per_tile;
   L.part = 0;
   L.score = (size_t(sm_count()) * 2 * part_floats(L.cols, dv) * 4 + 255) / 256 * 256;
-  const size_t units = size_t(num_seqs) * hkv * L.row_tiles * max_pages * (CP_KV4_PAGE / kKv4Sub);
+  const size_t units = size_t(num_seqs) * hkv * L.row_tiles * (size_t(max_pages) * (CP_KV4_PAGE / kKv4Sub) + 1);
   L.total = L.score + (accumulate ? units * L.rows_per_tile * kKv4Sub * 4 : 0);
   L.total = (L.total + 255) / 256 * 256;
   return L;
@@ -1093,7 +1087,7 @@ size_t kv4_attn_workspace(const cp_kv4_t* c, int32_t n_q, int32_t accumulate) {
 }
 
 int64_t kv4_attn_units(const cp_kv4_t* c, int32_t n_q) {
-  return int64_t(c->num_seqs) * c->hkv * c->max_pages * (CP_KV4_PAGE / kKv4Sub) *
+  return int64_t(c->num_seqs) * c->hkv * (int64_t(c->max_pages) * (CP_KV4_PAGE / kKv4Sub) + 1) *
          layout_of(c->num_seqs, c->hq, c->hkv, c->d_v, c->max_pages, c->dtype, n_q, 0).row_tiles;
 }
 
