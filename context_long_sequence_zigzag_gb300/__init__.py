@@ -182,6 +182,7 @@ class Problem:
             scale=float(scale if scale is not None else 1.0 / math.sqrt(d_qk)),
             gqa={"blocked": CP_GQA_BLOCKED, "interleaved": CP_GQA_INTERLEAVED}[gqa],
             dtype={torch.float32: CP_DT_F32, torch.bfloat16: CP_DT_BF16}[dtype])
+        self._key_weights_bytes = None
 
     @classmethod
     def from_workload(cls, w, cu_seqlens=None) -> "Problem":
@@ -446,63 +447,85 @@ def cp_attn_fwd_noalloc(prob: Problem, q, k, v, o, lse, stream=None):
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
-def _launch(t: torch.Tensor, stream, temps, name: str, *args) -> None:
-    """Calls a library function with the stream appended, on t's device.
+_raw_stream = torch._C._cuda_getCurrentRawStream  # (torch.cuda.current_stream builds an object on every call)
+_current_device = torch.cuda.current_device
+
+
+def _launch(dev: torch.device, stream, temps, name: str, *args) -> None:
+    """Calls a library function with the stream appended, on device dev.
     ``temps`` (buffers allocated here) are kept until that stream is done."""
-    dev = t.device
-    current = torch.cuda.current_stream(dev)
+    index = dev.index
+    handle = _raw_stream(index)
     if stream is not None:
-        handle = _stream(stream)
-        if handle != current.cuda_stream:
-            on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=dev)
+        other = _stream(stream)
+        if other != handle:
+            on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(other, device=dev)
             for x in temps:
                 x.record_stream(on)
-    else:
-        handle = current.cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        status = getattr(_lib, name)(*args, handle)
+            handle = other
+    if _current_device() == index:
+        status = _kv4_calls[name](*args, handle)
     else:
         with torch.cuda.device(dev):
-            status = getattr(_lib, name)(*args, handle)
+            status = _kv4_calls[name](*args, handle)
     if status != CP_OK:
         raise CpError(status, name)
+
+
+_kv4_calls = {n: getattr(_lib, n) for n in ("cp_attn_key_weights", "cp_kv4_append", "cp_kv4_read", "cp_kv4_attn",
+                                            "cp_kv4_evict")}
 
 
 def _need(t, name: str, dtype, shape, device=None) -> int:
     """Data pointer of a contiguous CUDA tensor of this type and shape (None
     in the shape: any size); ValueError otherwise."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda or (device is not None and t.device != device):
         raise ValueError(f"{name}: a tensor on {device or 'a CUDA device'} is needed")
     if t.dtype != dtype:
         raise ValueError(f"{name}: {dtype} is needed, got {t.dtype}")
-    if t.shape != shape and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
         raise ValueError(f"{name}: shape {tuple(shape)} is needed, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensors must be contiguous")
     return t.data_ptr()
 
 
+def _need_workspace(ws, device) -> int:
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws: a contiguous tensor on {device} is needed")
+    return ws.data_ptr()
+
+
 def cp_attn_key_weights(prob: Problem, q, k, lse, last: Optional[int] = None, w=None, ws=None, stream=None):
     """Accumulated attention weight of every key, float32 [hkv, T] in sharded
     order: the attention probabilities summed over the query heads of the
     key's head and over the queries, or over the last ``last`` of every
-    sequence.  lse: the forward's."""
+    sequence.  lse: the forward's.  Not for capture into a graph (as the other
+    calls with tile plans)."""
     d = prob.desc
-    T, dev = d.total_tokens, q.device
+    T, hkv, dev, dtype = d.total_tokens, d.hkv, q.device, prob.torch_dtype
     if last is not None and last < 1:
         raise ValueError("last: a positive number of queries, or None for all")
-    pq = _need(q, "q", prob.torch_dtype, (T, d.hq, d.d_qk))
-    pk = _need(k, "k", prob.torch_dtype, (T, d.hkv, d.d_qk), dev)
+    pq = _need(q, "q", dtype, (T, d.hq, d.d_qk), dev)
+    pk = _need(k, "k", dtype, (T, hkv, d.d_qk), dev)
     pl = _need(lse, "lse", torch.float32, (d.hq, T), dev)
     temps = []
     if w is None:
-        w = torch.empty(d.hkv, T, dtype=torch.float32, device=dev)
+        w = torch.empty((hkv, T), dtype=torch.float32, device=dev)
         temps.append(w)
-    pw = _need(w, "w", torch.float32, (d.hkv, T), dev)
+        pw = w.data_ptr()
+    else:
+        pw = _need(w, "w", torch.float32, (hkv, T), dev)
     if ws is None:
-        ws = workspace(prob, CP_OP_KEY_WEIGHTS, dev)
+        if prob._key_weights_bytes is None:
+            prob._key_weights_bytes = cp_workspace_size(prob, CP_OP_KEY_WEIGHTS)
+        ws = torch.empty(max(prob._key_weights_bytes, 1), dtype=torch.uint8, device=dev)
         temps.append(ws)
-    _launch(q, stream, temps, "cp_attn_key_weights", prob.ptr, last or 0, pq, pk, pl, pw, ws.data_ptr(), ws.numel())
+    _launch(dev, stream, temps, "cp_attn_key_weights", prob.ptr, last or 0, pq, pk, pl, pw, _need_workspace(ws, dev),
+            ws.numel() * ws.element_size())
     return w
 
 
@@ -536,6 +559,7 @@ class Kv4Cache:
             w = _need(weights, "weights", torch.float32, (pages.shape[0], hkv, CP_KV4_PAGE), pages.device)
         self.pages, self.page_table, self.weights = pages, page_table, weights
         self.torch_dtype, self.device = dtype, pages.device
+        self.num_seqs, self.hq, self.hkv, self.d_qk, self.d_v = page_table.shape[0], hq, hkv, d_qk, d_v
         self.desc = cp_kv4_t(
             num_seqs=page_table.shape[0], hq=hq, hkv=hkv, d_qk=d_qk, d_v=d_v,
             gqa={"blocked": CP_GQA_BLOCKED, "interleaved": CP_GQA_INTERLEAVED}[gqa],
@@ -545,12 +569,6 @@ class Kv4Cache:
         self.ptr = ctypes.byref(self.desc)
         self._ws_bytes = {}
         _check(_lib.cp_kv4_validate(self.ptr), "cp_kv4_validate")
-
-    def workspace_bytes(self, n_q: int, accumulate: bool) -> int:
-        key = (n_q, accumulate)
-        if key not in self._ws_bytes:
-            self._ws_bytes[key] = cp_kv4_workspace_size(self, n_q, accumulate)
-        return self._ws_bytes[key]
 
 
 def cp_kv4_validate(cache: Kv4Cache) -> int:
@@ -568,33 +586,38 @@ def cp_kv4_append(cache: Kv4Cache, k, v, cu, start, w=None, rows=None, stream=No
     slot start[b] + t - cu[b] of sequence b, from row rows[t] (or t) of k
     [n, hkv, d_qk], v [n, hkv, d_v] and w [hkv, n] (their first weights; None: 0).
     cu int32 [B + 1], start int32 [B], rows int32 [tokens], on the device."""
-    d, dev = cache.desc, cache.device
-    pk = _need(k, "k", cache.torch_dtype, (None, d.hkv, d.d_qk), dev)
+    dev, hkv, dtype, B = cache.device, cache.hkv, cache.torch_dtype, cache.num_seqs
     n = k.shape[0]
-    pv = _need(v, "v", cache.torch_dtype, (n, d.hkv, d.d_v), dev)
-    pw = None if w is None else _need(w, "w", torch.float32, (d.hkv, n), dev)
-    pr = None if rows is None else _need(rows, "rows", torch.int32, (None,), dev)
+    pk = _need(k, "k", dtype, (n, hkv, cache.d_qk), dev)
+    pv = _need(v, "v", dtype, (n, hkv, cache.d_v), dev)
+    pw = None if w is None else _need(w, "w", torch.float32, (hkv, n), dev)
     tokens = n if rows is None else rows.shape[0]
-    _launch(k, stream, (), "cp_kv4_append", cache.ptr, pk, pv, pw, n, pr,
-            _need(cu, "cu", torch.int32, (d.num_seqs + 1,), dev), _need(start, "start", torch.int32, (d.num_seqs,), dev),
-            tokens)
+    pr = None if rows is None else _need(rows, "rows", torch.int32, (tokens,), dev)
+    _launch(dev, stream, (), "cp_kv4_append", cache.ptr, pk, pv, pw, n, pr, _need(cu, "cu", torch.int32, (B + 1,), dev),
+            _need(start, "start", torch.int32, (B,), dev), tokens)
 
 
 def cp_kv4_read(cache: Kv4Cache, cu, start, tokens: int, k=None, v=None, stream=None):
     """Slots start[b], start[b] + 1, ... of every sequence b as rows cu[b] .. cu[b + 1] - 1 of
     k [tokens, hkv, d_qk] and v [tokens, hkv, d_v]."""
-    d, dev = cache.desc, cache.device
+    dev, dtype, B = cache.device, cache.torch_dtype, cache.num_seqs
     temps = []
+    shape = (tokens, cache.hkv, cache.d_qk)
     if k is None:
-        k = torch.empty(tokens, d.hkv, d.d_qk, dtype=cache.torch_dtype, device=dev)
+        k = torch.empty(shape, dtype=dtype, device=dev)
         temps.append(k)
+        pk = k.data_ptr()
+    else:
+        pk = _need(k, "k", dtype, shape, dev)
+    shape = (tokens, cache.hkv, cache.d_v)
     if v is None:
-        v = torch.empty(tokens, d.hkv, d.d_v, dtype=cache.torch_dtype, device=dev)
+        v = torch.empty(shape, dtype=dtype, device=dev)
         temps.append(v)
-    _launch(cache.pages, stream, temps, "cp_kv4_read", cache.ptr,
-            _need(cu, "cu", torch.int32, (d.num_seqs + 1,), dev), _need(start, "start", torch.int32, (d.num_seqs,), dev),
-            tokens, _need(k, "k", cache.torch_dtype, (tokens, d.hkv, d.d_qk), dev),
-            _need(v, "v", cache.torch_dtype, (tokens, d.hkv, d.d_v), dev))
+        pv = v.data_ptr()
+    else:
+        pv = _need(v, "v", dtype, shape, dev)
+    _launch(dev, stream, temps, "cp_kv4_read", cache.ptr, _need(cu, "cu", torch.int32, (B + 1,), dev),
+            _need(start, "start", torch.int32, (B,), dev), tokens, pk, pv)
     return k, v
 
 
@@ -604,25 +627,37 @@ def cp_kv4_attn(cache: Kv4Cache, q, lengths, accumulate: bool = False, part: boo
     (lengths int32 [B]: tokens held, the new ones among them).  Returns o [B, n_q, hq, d_v] and
     lse [hq, B * n_q].  accumulate: the attention probabilities are added to cache.weights.
     part: o in float32, for cp_lse_merge."""
-    d, dev = cache.desc, cache.device
-    pq = _need(q, "q", cache.torch_dtype, (d.num_seqs, None, d.hq, d.d_qk), dev)
+    dev, dtype, B, hq = cache.device, cache.torch_dtype, cache.num_seqs, cache.hq
     n_q = q.shape[1]
-    o_dtype = torch.float32 if part else cache.torch_dtype
-    temps = []
-    if o is None:
-        o = torch.empty(d.num_seqs, n_q, d.hq, d.d_v, dtype=o_dtype, device=dev)
-        temps.append(o)
-    if lse is None:
-        lse = torch.empty(d.hq, d.num_seqs * n_q, dtype=torch.float32, device=dev)
-        temps.append(lse)
+    pq = _need(q, "q", dtype, (B, n_q, hq, cache.d_qk), dev)
+    o_dtype = torch.float32 if part else dtype
     accumulate = bool(accumulate)
+    temps = []
+    shape = (B, n_q, hq, cache.d_v)
+    if o is None:
+        o = torch.empty(shape, dtype=o_dtype, device=dev)
+        temps.append(o)
+        po = o.data_ptr()
+    else:
+        po = _need(o, "o", o_dtype, shape, dev)
+    shape = (hq, B * n_q)
+    if lse is None:
+        lse = torch.empty(shape, dtype=torch.float32, device=dev)
+        temps.append(lse)
+        pl = lse.data_ptr()
+    else:
+        pl = _need(lse, "lse", torch.float32, shape, dev)
     if ws is None:
-        ws = torch.empty(max(cache.workspace_bytes(n_q, accumulate), 1), dtype=torch.uint8, device=dev)
+        size = cache._ws_bytes.get((n_q, accumulate))
+        if size is None:
+            size = cache._ws_bytes[n_q, accumulate] = max(cp_kv4_workspace_size(cache, n_q, accumulate), 1)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
         temps.append(ws)
-    _launch(q, stream, temps, "cp_kv4_attn", cache.ptr, n_q, pq,
-            _need(lengths, "lengths", torch.int32, (d.num_seqs,), dev),
-            _need(o, "o", o_dtype, (d.num_seqs, n_q, d.hq, d.d_v), dev), int(part),
-            _need(lse, "lse", torch.float32, (d.hq, d.num_seqs * n_q), dev), int(accumulate), ws.data_ptr(), ws.numel())
+        pw = ws.data_ptr()
+    else:
+        pw, size = _need_workspace(ws, dev), ws.numel() * ws.element_size()
+    _launch(dev, stream, temps, "cp_kv4_attn", cache.ptr, n_q, pq, _need(lengths, "lengths", torch.int32, (B,), dev), po,
+            1 if part else 0, pl, 1 if accumulate else 0, pw, size)
     return o, lse
 
 
@@ -631,20 +666,20 @@ def cp_kv4_evict(cache: Kv4Cache, lengths, budget: int, recent: int, to: Kv4Cach
     """Keeps, for every sequence and head, the last ``recent`` slots and the budget - recent others of
     largest weight, copied in slot order into the pages of ``to`` (no page may be read and written).
     Returns new_lengths int32 [B] and kept int32 [B, hkv, budget], the slots kept (-1 behind the last)."""
-    d, dev = cache.desc, cache.device
+    dev, B = cache.device, cache.num_seqs
     temps = []
     if new_lengths is None:
-        new_lengths = torch.empty(d.num_seqs, dtype=torch.int32, device=dev)
+        new_lengths = torch.empty(B, dtype=torch.int32, device=dev)
         temps.append(new_lengths)
+    shape = (B, cache.hkv, max(budget, 0))
     if kept is None:
-        kept = torch.empty(d.num_seqs, d.hkv, max(budget, 0), dtype=torch.int32, device=dev)
+        kept = torch.empty(shape, dtype=torch.int32, device=dev)
         temps.append(kept)
     if to.device != dev:
         raise ValueError(f"to: a cache on {dev} is needed")
-    _launch(cache.pages, stream, temps, "cp_kv4_evict", cache.ptr,
-            _need(lengths, "lengths", torch.int32, (d.num_seqs,), dev), budget, recent, to.ptr,
-            _need(new_lengths, "new_lengths", torch.int32, (d.num_seqs,), dev),
-            _need(kept, "kept", torch.int32, (d.num_seqs, d.hkv, max(budget, 0)), dev))
+    _launch(dev, stream, temps, "cp_kv4_evict", cache.ptr, _need(lengths, "lengths", torch.int32, (B,), dev), budget,
+            recent, to.ptr, _need(new_lengths, "new_lengths", torch.int32, (B,), dev),
+            _need(kept, "kept", torch.int32, shape, dev))
     return new_lengths, kept
 
 

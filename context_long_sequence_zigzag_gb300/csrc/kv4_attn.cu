@@ -35,6 +35,7 @@
 // second kernel joins.  Weights need the final lse, so the raw scores wait in
 // the workspace (they stay in L2) and the second kernel adds them up.
 #include <algorithm>
+#include <atomic>
 
 #include <cuda_fp8.h>
 
@@ -1030,8 +1031,15 @@ cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
   if (off > kMost) return cudaErrorInvalidValue;
   gr.warps = C::NW;
   auto kernel = kv4_attn_kernel<C, E>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(off));
+  static std::atomic<uint64_t> ready{0};  // devices whose kernel may use that much shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  }
   kernel<<<unsigned(gr.ctas), C::THREADS, off, st>>>(a, gr);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
