@@ -96,6 +96,7 @@ cudaError_t launch_kv4_read(const Kv4Cache& c, int dqk, int dv, int dtype, const
 cudaError_t launch_kv4_evict(const Kv4Cache& c, int dqk, int dv, const int32_t* lengths, int32_t budget,
                              int32_t recent, const Kv4Cache& to, int32_t* new_lengths, int32_t* kept,
                              cudaStream_t st);
+int kv4_sm_count();  // of the current device
 size_t kv4_attn_workspace(const cp_kv4_t* c, int32_t n_q, int32_t accumulate);
 // units of work of the longest sequences that the table can hold
 int64_t kv4_attn_units(const cp_kv4_t* c, int32_t n_q);

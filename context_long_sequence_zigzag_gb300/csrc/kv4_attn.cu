@@ -993,19 +993,6 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnArg
   }
 }
 
-int sm_count() {
-  static int n = 0;
-  if (n == 0) {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) == cudaSuccess &&
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0)
-      n = v;
-    else
-      return 152;
-  }
-  return n;
-}
-
 // Rows of one pass: up to 8 in one column tile of the MMAs, else up to 16 in
 // two (fp32 caches: 8, their three terms take the registers).
 int cols_of(int rows, int dtype) { return dtype == CP_DT_BF16 && rows > 8 ? 16 : 8; }
@@ -1081,7 +1068,7 @@ Layout layout_of(int num_seqs, int hq, int hkv, int dv, int max_pages, int dtype
   L.rows_per_tile = (L.rows + L.row_tiles - 1) / L.row_tiles;
   L.row_tiles = (L.rows + L.rows_per_tile - 1) / L.rows_per_tile;
   L.part = 0;
-  L.score = (size_t(sm_count()) * 2 * part_floats(L.cols, dv) * 4 + 255) / 256 * 256;
+  L.score = (size_t(kv4_sm_count()) * 2 * part_floats(L.cols, dv) * 4 + 255) / 256 * 256;
   const size_t units = size_t(num_seqs) * hkv * L.row_tiles * (size_t(max_pages) * (CP_KV4_PAGE / kKv4Sub) + 1);
   L.total = L.score + (accumulate ? units * L.rows_per_tile * kKv4Sub * 4 : 0);
   L.total = (L.total + 255) / 256 * 256;
@@ -1089,6 +1076,18 @@ Layout layout_of(int num_seqs, int hq, int hkv, int dv, int max_pages, int dtype
 }
 
 }  // namespace
+
+int kv4_sm_count() {
+  static std::atomic<int> counts[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  n = counts[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
+    counts[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
 
 size_t kv4_attn_workspace(const cp_kv4_t* c, int32_t n_q, int32_t accumulate) {
   return layout_of(c->num_seqs, c->hq, c->hkv, c->d_v, c->max_pages, c->dtype, n_q, accumulate).total;
@@ -1104,7 +1103,7 @@ cudaError_t launch_kv4_attn(Kv4AttnArgs a, int dqk, int dv, int dtype, cudaStrea
   a.rows = L.rows;
   a.row_tiles = L.row_tiles;
   Grid gr{};
-  gr.ctas = sm_count();
+  gr.ctas = kv4_sm_count();
   gr.rows_per_tile = L.rows_per_tile;
   gr.part = reinterpret_cast<float*>(a.ws + L.part);
   gr.score = reinterpret_cast<float*>(a.ws + L.score);

@@ -6,6 +6,11 @@
 // groups are aligned runs of 8 lanes, and both the tensor side (16 or 32
 // bytes a lane) and the cache side (whole 64-byte rows) are contiguous
 // across a warp.
+#include <algorithm>
+#include <atomic>
+
+#include <cooperative_groups.h>
+
 #include "kv4.cuh"
 
 namespace cpattn {
@@ -41,83 +46,145 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
 }
 
 // The integer nearest to (x - low) / s, halves to even, of the exact
-// quotient.  The quotient in fp32 is off by a few units of 2^-23: only where
-// it falls that close to a half is the exact sign of (x - low) - (f + 1/2) s
-// needed (f + 1/2 and s have 13 bits together, so the product inside the FMA
-// is exact; e is the rounding error of x - low).
-__device__ __forceinline__ float code_of(float x, float low, float s) {
+// quotient, in 0 .. 15.  The sign of (x - low) - (f + 1/2) s decides between f
+// and f + 1: f + 1/2 and s have 13 bits together, so the product inside the
+// FMA is exact, and e is the rounding error of x - low.
+__device__ __noinline__ float exact_code(float x, float low, float s) {
   const float d = x - low;
-  float q = __fdiv_rn(d, s);
-  if (isinf(d)) q = __fdiv_rn(0.5f * x - 0.5f * low, 0.5f * s);
-  const float f = floorf(q);
-  if (fabsf(q - f - 0.5f) < 1e-5f && f < 16.f) {
-    const float bb = d - x;
-    const float e = (x - (d - bb)) + (-low - bb);
+  const float f = fminf(floorf(isinf(d) ? __fdiv_rn(0.5f * x - 0.5f * low, 0.5f * s) : __fdiv_rn(d, s)), 15.f);
+  const float bb = d - x;
+  const float e = (x - (d - bb)) + (-low - bb);
+  float n = f;
+  if (isfinite(d)) {
     const float t = fmaf(-(f + 0.5f), s, d) + e;
-    q = t > 0.f ? f + 1.f : (t < 0.f ? f : rintf(f + 0.5f));
+    n = t > 0.f ? f + 1.f : (t < 0.f ? f : rintf(f + 0.5f));
   } else {
-    q = rintf(q);
+    n = rintf(__fdiv_rn(0.5f * x - 0.5f * low, 0.5f * s));
   }
-  return fminf(fmaxf(q, 0.f), 15.f);
+  return fminf(fmaxf(n, 0.f), 15.f);
 }
 
-// One token's place in the cache.
+// Codes of 8 channels, channel j in bits 4j.  (x - low) times 1 / s in fp32 is
+// off by less than 1e-5 (its value is below 16), so it rounds as the exact
+// quotient does wherever it is not that close to a half; those, and scales
+// whose reciprocal or range leaves fp32, take the long way.
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float low, float s, bool plain) {
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: the sum's last bits are the integer
+  const float inv = __fdiv_rn(1.f, s);
+  uint32_t codes = 0;
+  float near = plain ? 0.f : 1.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float q = (x[j] - low) * inv, r = q + kMagic;
+    near = fmaxf(near, fabsf(q - (r - kMagic)));
+    codes |= (__float_as_uint(r) & 15u) << (4 * j);
+  }
+  if (near > 0.5f - 1e-5f) {
+    codes = 0;
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) codes |= uint32_t(exact_code(x[j], low, s)) << (4 * j);
+  }
+  return codes;
+}
+
+// A token's place in the cache and its row outside it.
 struct Place {
-  uint8_t* sub;      // sub-block of head 0's block; heads are block() bytes apart
-  int32_t page, row;  // row 0 .. 63 of the page
+  uint8_t* sub;  // sub-block of head 0's block (heads are block() bytes apart), or null
+  float* weight;  // of head 0 (heads are 64 apart), or null
+  int64_t src;
+  int32_t row;  // row of the sub-block
 };
 
-// Slot of token t; false where there is none (padding, or recorded as an error).
-__device__ __forceinline__ bool find_place(const Kv4Cache& c, const Kv4Format& f, const int32_t* cu,
-                                           const int32_t* start, int64_t t, Place* at) {
+// Null where token t has no slot (padding, or recorded as an error).
+__device__ __forceinline__ Place place_of(const Kv4Cache& c, const Kv4Format& f, const int32_t* cu, const int32_t* start,
+                                          const int32_t* rows, int64_t src_rows, int64_t t) {
+  Place at{nullptr, nullptr, t, 0};
   const int b = kv4_seq_of(cu, c.num_seqs, t);
-  if (b < 0) return false;
+  if (b < 0) return at;
   const int64_t slot = int64_t(__ldg(start + b)) + t - __ldg(cu + b);
   if (slot < 0 || slot >= int64_t(c.max_pages) * CP_KV4_PAGE) {
     kv4_error(c, kKv4Slot);
-    return false;
+    return at;
   }
-  at->page = kv4_page(c, b, int32_t(slot / CP_KV4_PAGE));
-  if (at->page < 0) return false;
-  at->row = int32_t(slot % CP_KV4_PAGE);
-  at->sub = c.pages + int64_t(at->page) * c.hkv * f.block() + (at->row / kKv4Sub) * f.sub();
-  return true;
+  if (rows) at.src = __ldg(rows + t);
+  if (at.src < 0 || at.src >= src_rows) {
+    kv4_error(c, kKv4Row);
+    return at;
+  }
+  const int page = kv4_page(c, b, int32_t(slot / CP_KV4_PAGE)), row = int32_t(slot % CP_KV4_PAGE);
+  if (page < 0) return at;
+  at.sub = c.pages + int64_t(page) * c.hkv * f.block() + (row / kKv4Sub) * f.sub();
+  if (c.weights) at.weight = c.weights + int64_t(page) * c.hkv * CP_KV4_PAGE + row;
+  at.row = row % kKv4Sub;
+  return at;
 }
 
+// What word i of a CTA's tokens is: of which token, k or v, head, word.  The
+// divisions are products with rounded-up reciprocals (exact while i times the
+// divisor stays below 2^32, which the launch sees to).
+struct Words {
+  int nk, nv, words, all_k;  // words of a head's k, of its v, of a token, of all its k
+  uint32_t by_words, by_nk, by_nv;
+};
+struct Word {
+  int token, r, head, word;  // r: word of all heads' k, or of all their v
+  bool is_v;
+};
+__device__ __forceinline__ Word word_of(const Words& n, int i) {
+  Word x;
+  x.token = int(n.words == 1 ? uint32_t(i) : __umulhi(uint32_t(i), n.by_words));
+  x.r = i - x.token * n.words;
+  x.is_v = x.r >= n.all_k;
+  if (x.is_v) x.r -= n.all_k;
+  x.head = int(__umulhi(uint32_t(x.r), x.is_v ? n.by_nv : n.by_nk));
+  x.word = x.r - x.head * (x.is_v ? n.nv : n.nk);
+  return x;
+}
+
+constexpr int kMostTokens = 32;  // of a CTA
+
 template <typename E>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Cache c, const Kv4Format f, const E* k, const E* v,
-                                                              const float* w, int64_t src_rows, const int32_t* rows,
-                                                              const int32_t* cu, const int32_t* start, int64_t tokens,
-                                                              int per_block) {
-  const int nk = f.dqk / 8, nv = f.dv / 8, words = c.hkv * (nk + nv);
+__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Cache c, const Kv4Format f, const Words n, const E* k,
+                                                              const E* v, const float* w, int64_t src_rows,
+                                                              const int32_t* rows, const int32_t* cu,
+                                                              const int32_t* start, int64_t tokens, int per_block) {
+  __shared__ Place places[kMostTokens];
   const int64_t t0 = int64_t(blockIdx.x) * per_block;
-  const int n = int(min(int64_t(per_block), tokens - t0)) * words;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int64_t t = t0 + i / words;
-    int r = i % words;
-    Place at;
-    if (!find_place(c, f, cu, start, t, &at)) continue;
-    const int64_t src = rows ? int64_t(__ldg(rows + t)) : t;
-    if (src < 0 || src >= src_rows) {
-      kv4_error(c, kKv4Row);
-      continue;
+  const int here = int(min(int64_t(per_block), tokens - t0));
+  if (threadIdx.x < here) places[threadIdx.x] = place_of(c, f, cu, start, rows, src_rows, t0 + threadIdx.x);
+  __syncthreads();
+  const int all = here * n.words;
+  auto load = [&](int i, float (&x)[8]) {  // the groups of 8 lanes stay whole: all is a multiple of 8
+    const Word o = word_of(n, i);
+    const Place& at = places[o.token];
+    if (at.sub) {
+      load8(o.is_v ? v + (at.src * c.hkv * n.nv + o.r) * 8 : k + (at.src * n.all_k + o.r) * 8, x);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = 0.f;
     }
-    const bool is_v = r >= c.hkv * nk;
-    if (is_v) r -= c.hkv * nk;
-    const int per = is_v ? nv : nk, head = r / per, word = r % per, group = word / 8;
+  };
+  float next[8];
+  if (threadIdx.x < all) load(threadIdx.x, next);
+  for (int i = threadIdx.x; i < all; i += kThreads) {
     float x[8];
-    load8(is_v ? v + (src * c.hkv * nv + r) * 8 : k + (src * c.hkv * nk + r) * 8, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = next[j];
+    if (i + kThreads < all) load(i + kThreads, next);
+    const Word o = word_of(n, i);
+    const Place& at = places[o.token];
     // the group's minimum and maximum over its 8 lanes; x - x is NaN for NaN and infinities
     float lo = x[0], hi = x[0], bad = x[0] - x[0];
 #pragma unroll
     for (int j = 1; j < 8; ++j) lo = fminf(lo, x[j]), hi = fmaxf(hi, x[j]), bad += x[j] - x[j];
     const uint32_t lanes = 0xffu << (threadIdx.x & 24);
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(lanes, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(lanes, hi, o));
-      bad += __shfl_xor_sync(lanes, bad, o);
+    for (int s = 1; s < 8; s <<= 1) {
+      lo = fminf(lo, __shfl_xor_sync(lanes, lo, s));
+      hi = fmaxf(hi, __shfl_xor_sync(lanes, hi, s));
+      bad += __shfl_xor_sync(lanes, bad, s);
     }
+    if (!at.sub) continue;
     __nv_bfloat16 low = __float2bfloat16_rd(lo);
     const float lowf = __bfloat162float(low);
     // (max - low) / 15; halved first, so that no finite range overflows
@@ -127,64 +194,61 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Cache c, 
     if (bad != 0.f || isinf(lowf)) {  // bad is 0 or NaN
       low = scale = __ushort_as_bfloat16(0x7fff);
     } else if (s > 0.f) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) codes |= uint32_t(code_of(x[j], lowf, s)) << (4 * j);
+      codes = codes_of(x, lowf, s, s >= 1.2e-38f && hi - lowf < INFINITY);
     }
-    uint8_t* sub = at.sub + int64_t(head) * f.block();
-    const int row = at.row % kKv4Sub;
-    if (is_v) {
-      reinterpret_cast<uint32_t*>(sub + f.vc() + row * (f.dv / 2))[f.vword(word)] = codes;
-      if (word % 8 == 0) {
-        reinterpret_cast<__nv_bfloat16*>(sub + f.vs())[row * f.gv() + group] = scale;
-        reinterpret_cast<__nv_bfloat16*>(sub + f.vl())[group * kKv4Sub + row] = low;
+    uint8_t* sub = at.sub + int64_t(o.head) * f.block();
+    const int group = o.word / 8;
+    if (o.is_v) {
+      reinterpret_cast<uint32_t*>(sub + f.vc() + at.row * (f.dv / 2))[f.vword(o.word)] = codes;
+      if (o.word % 8 == 0) {
+        reinterpret_cast<__nv_bfloat16*>(sub + f.vs())[at.row * f.gv() + group] = scale;
+        reinterpret_cast<__nv_bfloat16*>(sub + f.vl())[group * kKv4Sub + at.row] = low;
       }
     } else {
-      reinterpret_cast<uint32_t*>(sub + f.kc() + row * (f.dqk / 2))[f.kword(word)] = codes;
-      if (word % 8 == 0) {
-        __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(sub + f.kp()) + row * 2 * f.gk() + group;
+      reinterpret_cast<uint32_t*>(sub + f.kc() + at.row * (f.dqk / 2))[f.kword(o.word)] = codes;
+      if (o.word % 8 == 0) {
+        __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(sub + f.kp()) + at.row * 2 * f.gk() + group;
         p[0] = scale;
         p[f.gk()] = low;
       }
-      if (word == 0 && c.weights)
-        c.weights[(int64_t(at.page) * c.hkv + head) * CP_KV4_PAGE + at.row] =
-            w ? __ldg(w + int64_t(head) * src_rows + src) : 0.f;
+      if (o.word == 0 && at.weight)
+        at.weight[int64_t(o.head) * CP_KV4_PAGE] = w ? __ldg(w + int64_t(o.head) * src_rows + at.src) : 0.f;
     }
   }
 }
 
 template <typename E>
-__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Cache c, const Kv4Format f, const int32_t* cu,
-                                                            const int32_t* start, int64_t tokens, E* k, E* v,
-                                                            int per_block) {
-  const int nk = f.dqk / 8, nv = f.dv / 8, words = c.hkv * (nk + nv);
+__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Cache c, const Kv4Format f, const Words n,
+                                                            const int32_t* cu, const int32_t* start, int64_t tokens,
+                                                            E* k, E* v, int per_block) {
+  __shared__ Place places[kMostTokens];
   const int64_t t0 = int64_t(blockIdx.x) * per_block;
-  const int n = int(min(int64_t(per_block), tokens - t0)) * words;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int64_t t = t0 + i / words;
-    int r = i % words;
-    Place at;
-    if (!find_place(c, f, cu, start, t, &at)) continue;
-    const bool is_v = r >= c.hkv * nk;
-    if (is_v) r -= c.hkv * nk;
-    const int per = is_v ? nv : nk, head = r / per, word = r % per, group = word / 8;
-    const uint8_t* sub = at.sub + int64_t(head) * f.block();
-    const int row = at.row % kKv4Sub;
+  const int here = int(min(int64_t(per_block), tokens - t0));
+  if (threadIdx.x < here) places[threadIdx.x] = place_of(c, f, cu, start, nullptr, tokens, t0 + threadIdx.x);
+  __syncthreads();
+#pragma unroll 4
+  for (int i = threadIdx.x; i < here * n.words; i += kThreads) {
+    const Word o = word_of(n, i);
+    const Place& at = places[o.token];
+    if (!at.sub) continue;
+    const uint8_t* sub = at.sub + int64_t(o.head) * f.block();
+    const int group = o.word / 8;
     uint32_t codes;
     float s, low;
-    if (is_v) {
-      codes = reinterpret_cast<const uint32_t*>(sub + f.vc() + row * (f.dv / 2))[f.vword(word)];
-      s = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sub + f.vs())[row * f.gv() + group]);
-      low = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sub + f.vl())[group * kKv4Sub + row]);
+    if (o.is_v) {
+      codes = reinterpret_cast<const uint32_t*>(sub + f.vc() + at.row * (f.dv / 2))[f.vword(o.word)];
+      s = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sub + f.vs())[at.row * f.gv() + group]);
+      low = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sub + f.vl())[group * kKv4Sub + at.row]);
     } else {
-      codes = reinterpret_cast<const uint32_t*>(sub + f.kc() + row * (f.dqk / 2))[f.kword(word)];
-      const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(sub + f.kp()) + row * 2 * f.gk() + group;
+      codes = reinterpret_cast<const uint32_t*>(sub + f.kc() + at.row * (f.dqk / 2))[f.kword(o.word)];
+      const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(sub + f.kp()) + at.row * 2 * f.gk() + group;
       s = __bfloat162float(p[0]);
       low = __bfloat162float(p[f.gk()]);
     }
     float x[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = fmaf(s, float((codes >> (4 * j)) & 15u), low);
-    store8(is_v ? v + (t * c.hkv * nv + r) * 8 : k + (t * c.hkv * nk + r) * 8, x);
+    store8(o.is_v ? v + (at.src * c.hkv * n.nv + o.r) * 8 : k + (at.src * n.all_k + o.r) * 8, x);
   }
 }
 
@@ -198,84 +262,141 @@ __device__ __forceinline__ uint32_t rank_key(float x) {
 }
 
 constexpr int kSelThreads = 1024;
+constexpr int kDigits = 2048;      // bins of an 11-bit digit
+constexpr int kSelKeys = 49152;    // keys that a CTA keeps in shared memory
+constexpr int kSelSlice = 8192;    // slots a CTA takes at least where a row gets several
 
-// One CTA per (sequence, kv head): the slots to keep, in order.  The key of
-// the last slot that is kept is found digit by digit (8 bits a pass, counted
-// in shared memory); a second walk writes the slots out in order.
+// Sum of x over the threads before this one; *all gets the sum over all.
+__device__ __forceinline__ int block_before(int x, int* scratch, int* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int y = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
+  }
+  if (lane == 31) scratch[warp] = y;
+  __syncthreads();
+  int z = scratch[lane];  // kSelThreads / 32 = 32 warps
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, z, o);
+    if (lane >= o) z += u;
+  }
+  *all = __shfl_sync(0xffffffffu, z, 31);
+  const int warps_before = __shfl_sync(0xffffffffu, z, max(warp - 1, 0));
+  __syncthreads();
+  return y - x + (warp > 0 ? warps_before : 0);
+}
+
+// A cluster of CTAs per (sequence, kv head): the slots to keep, in order.
+// Each CTA holds the keys of its slice of the row in shared memory (rows too
+// long for that are read again).  The key of the last slot that is kept is
+// found digit by digit, 11 bits a pass: the CTAs count their slices, and every
+// one of them sums the counts over the cluster through distributed shared
+// memory.  The slots above the key, and the first `need` of those that equal
+// it, then get their places from counts in slot order.
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4Cache c, const int32_t* lengths,
                                                                  int32_t budget, int32_t recent, int32_t* new_lengths,
-                                                                 int32_t* kept) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t s_prefix, s_need;
-  __shared__ uint32_t warp_sum[kSelThreads / 32];
-  const int b = blockIdx.x / c.hkv, h = blockIdx.x - b * c.hkv;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = kv4_length(c, lengths, b);
-  const int keep = min(n, budget);
-  int32_t* out = kept + (int64_t(b) * c.hkv + h) * budget;
-  if (h == 0 && tid == 0) new_lengths[b] = keep;
-  for (int i = keep + tid; i < budget; i += kSelThreads) out[i] = -1;
+                                                                 int32_t* kept, int most_keys) {
+  extern __shared__ uint32_t keys[];
+  __shared__ int32_t hist[kDigits], scratch[32], s_count[2];
+  __shared__ int32_t s_digit, s_left;
+  cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+  const int parts = int(cluster.num_blocks()), part = int(cluster.block_rank());
+  const int64_t row = blockIdx.x / parts;
+  const int b = int(row / c.hkv), h = int(row - int64_t(b) * c.hkv);
+  const int tid = threadIdx.x;
+  const int n = kv4_length(c, lengths, b), keep = min(n, budget);
+  int32_t* out = kept + row * budget;
+  const int first = part * kSelThreads + tid, step = parts * kSelThreads;
+  if (h == 0 && first == 0) new_lengths[b] = keep;
+  for (int i = keep + first; i < budget; i += step) out[i] = -1;
   if (n <= budget) {
-    for (int i = tid; i < n; i += kSelThreads) out[i] = i;
+    for (int i = first; i < n; i += step) out[i] = i;
     return;
   }
-  const int m = n - recent;        // slots ranked by weight
-  int need = budget - recent;      // of which this many stay (need < m)
-  auto key_at = [&](int j) -> uint32_t {
+  const int m = n - recent;    // slots ranked by weight
+  int need = budget - recent;  // of which this many stay (need < m); behind them the recent ones
+  for (int i = first; i < recent; i += step) out[need + i] = m + i;
+  if (need == 0) return;
+  const int slice = (m + parts - 1) / parts, lo = min(part * slice, m), count = min(m, lo + slice) - lo;
+  auto weight_key = [&](int j) -> uint32_t {
     const int page = kv4_page(c, b, j / CP_KV4_PAGE);
     return page < 0 ? 0u : rank_key(__ldg(c.weights + (int64_t(page) * c.hkv + h) * CP_KV4_PAGE + j % CP_KV4_PAGE));
   };
-  uint32_t prefix = 0;
-  if (need > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      for (int j = tid; j < m; j += kSelThreads) {
-        const uint32_t key = key_at(j);
-        if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255u], 1u);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        uint32_t left = uint32_t(need);
-        int d = 255;
-        while (d > 0 && hist[d] < left) left -= hist[d--];
-        s_prefix = prefix | (uint32_t(d) << shift);
-        s_need = left;
-      }
-      __syncthreads();
-      prefix = s_prefix;
-      need = int(s_need);
-      __syncthreads();
-    }
+  const bool held = count <= most_keys;
+  if (held) {
+#pragma unroll 4
+    for (int j = tid; j < count; j += kSelThreads) keys[j] = weight_key(lo + j);
   }
-  // slots above the key stay, and the first `need` of those that equal it
-  int written = 0, equal = 0;
-  const bool none = budget == recent;
-  for (int j0 = 0; j0 < n; j0 += kSelThreads) {
+  auto key_at = [&](int j) -> uint32_t { return held ? keys[j] : weight_key(lo + j); };
+  uint32_t prefix = 0, known = 0;  // known: the bits of it that are found
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+    const uint32_t digits = pass == 2 ? 1023u : 2047u;
+    for (int i = tid; i < kDigits; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    for (int j = tid; j < count; j += kSelThreads) {
+      const uint32_t key = key_at(j);
+      if ((key & known) == prefix) atomicAdd(&hist[(key >> shift) & digits], 1);
+    }
+    cluster.sync();
+    // thread t sums digits 2047 - 2t and 2046 - 2t
+    int have[2] = {0, 0};
+    for (int q = 0; q < parts; ++q) {
+      const int32_t* other = cluster.map_shared_rank(hist, q);
+      have[0] += other[kDigits - 1 - 2 * tid];
+      have[1] += other[kDigits - 2 - 2 * tid];
+    }
+    int all;
+    const int above = block_before(have[0] + have[1], scratch, &all);
+    if (above < need && need <= above + have[0] + have[1]) {
+      const int low = need > above + have[0];
+      s_digit = kDigits - 1 - 2 * tid - low;
+      s_left = need - above - (low ? have[0] : 0);
+    }
+    cluster.sync();  // (the counts have been read)
+    prefix |= uint32_t(s_digit) << shift;
+    known |= digits << shift;
+    need = s_left;
+    __syncthreads();
+  }
+  // ---- this slice's share of them
+  int above = 0, same = 0;
+  for (int j = tid; j < count; j += kSelThreads) {
+    const uint32_t key = key_at(j);
+    above += key > prefix;
+    same += key == prefix;
+  }
+  int all_above, all_same;
+  block_before(above, scratch, &all_above);
+  block_before(same, scratch, &all_same);
+  if (tid == 0) {
+    s_count[0] = all_above;
+    s_count[1] = all_same;
+  }
+  cluster.sync();
+  int written = 0, equal = 0;  // above and equal in the slices before
+  for (int q = 0; q < part; ++q) {
+    const int32_t* other = cluster.map_shared_rank(s_count, q);
+    written += other[0];
+    equal += other[1];
+  }
+  cluster.sync();  // (no CTA leaves while its counts are read)
+  written += min(equal, need);
+  for (int j0 = 0; j0 < count; j0 += kSelThreads) {
     const int j = j0 + tid;
-    uint32_t key = 0;
-    const bool ranked = j < m;
-    if (ranked && !none) key = key_at(j);
-    const bool above = j < n && (!ranked || (!none && key > prefix)), same = ranked && !none && key == prefix;
-    const uint32_t ma = __ballot_sync(0xffffffffu, above), ms = __ballot_sync(0xffffffffu, same);
-    if (lane == 0) warp_sum[warp] = uint32_t(__popc(ma)) | (uint32_t(__popc(ms)) << 16);
-    __syncthreads();
-    int ba = 0, bs = 0, ta = 0, ts = 0;
-    for (int i = 0; i < kSelThreads / 32; ++i) {
-      const int a = int(warp_sum[i] & 0xffffu), s = int(warp_sum[i] >> 16);
-      if (i < warp) ba += a, bs += s;
-      ta += a;
-      ts += s;
-    }
-    const uint32_t below = (1u << lane) - 1u;
-    const int a_before = ba + __popc(ma & below), s_before = equal + bs + __popc(ms & below);
-    if (above || (same && s_before < need)) {
-      const int at = written + a_before + max(0, min(s_before, need) - min(equal, need));
-      out[at] = j;
-    }
-    written += ta + max(0, min(equal + ts, need) - min(equal, need));
-    equal += ts;
-    __syncthreads();
+    const uint32_t key = j < count ? key_at(j) : 0u;
+    const bool is_above = j < count && key > prefix, is_same = j < count && key == prefix;
+    int all;
+    const int before = block_before(int(is_above) | int(is_same) << 16, scratch, &all);
+    const int same_before = equal + (before >> 16);
+    if (is_above || (is_same && same_before < need))
+      out[written + (before & 0xffff) + min(same_before, need) - min(equal, need)] = lo + j;
+    written += (all & 0xffff) + min(equal + (all >> 16), need) - min(equal, need);
+    equal += all >> 16;
   }
 }
 
@@ -337,23 +458,39 @@ __global__ void __launch_bounds__(kThreads) kv4_move_kernel(const Kv4Cache c, co
 
 }  // namespace
 
-// Tokens a CTA of append or read takes: about one word a thread, whole tokens.
-static int tokens_per_block(const Kv4Cache& c, int dqk, int dv) {
-  const int words = c.hkv * (dqk + dv) / 8;
-  return words >= kThreads ? 1 : kThreads / words;
+// Tokens a CTA of append or read takes: several words a thread once every SM
+// has CTAs enough, whole tokens in any case.
+static int tokens_per_block(int words, int64_t tokens) {
+  const int64_t fill = (kThreads + words - 1) / words;                 // a word a thread
+  const int64_t many = tokens / (int64_t(kv4_sm_count()) * 8);          // 8 CTAs an SM
+  return int(std::min<int64_t>(kMostTokens, std::max<int64_t>(std::max<int64_t>(1, kThreads / words), std::min(many, fill * 16))));
+}
+
+static Words words_of(const Kv4Cache& c, int dqk, int dv) {
+  Words n;
+  n.nk = dqk / 8;
+  n.nv = dv / 8;
+  n.all_k = c.hkv * n.nk;
+  n.words = c.hkv * (n.nk + n.nv);
+  auto inverse = [](int d) { return uint32_t(((uint64_t(1) << 32) + d - 1) / d); };
+  n.by_words = inverse(n.words);
+  n.by_nk = inverse(n.nk);
+  n.by_nv = inverse(n.nv);
+  return n;
 }
 
 cudaError_t launch_kv4_append(const Kv4Cache& c, int dqk, int dv, int dtype, const void* k, const void* v,
                               const float* w, int64_t src_rows, const int32_t* rows, const int32_t* cu,
                               const int32_t* start, int64_t tokens, cudaStream_t st) {
-  const int per = tokens_per_block(c, dqk, dv);
+  const Words n = words_of(c, dqk, dv);
+  const int per = tokens_per_block(n.words, tokens);
   const unsigned grid = unsigned((tokens + per - 1) / per);
   if (dtype == CP_DT_BF16)
-    kv4_append_kernel<<<grid, kThreads, 0, st>>>(c, Kv4Format(dqk, dv), static_cast<const __nv_bfloat16*>(k),
+    kv4_append_kernel<<<grid, kThreads, 0, st>>>(c, Kv4Format(dqk, dv), n, static_cast<const __nv_bfloat16*>(k),
                                                  static_cast<const __nv_bfloat16*>(v), w, src_rows, rows, cu, start,
                                                  tokens, per);
   else
-    kv4_append_kernel<<<grid, kThreads, 0, st>>>(c, Kv4Format(dqk, dv), static_cast<const float*>(k),
+    kv4_append_kernel<<<grid, kThreads, 0, st>>>(c, Kv4Format(dqk, dv), n, static_cast<const float*>(k),
                                                  static_cast<const float*>(v), w, src_rows, rows, cu, start, tokens,
                                                  per);
   return cudaGetLastError();
@@ -361,13 +498,14 @@ cudaError_t launch_kv4_append(const Kv4Cache& c, int dqk, int dv, int dtype, con
 
 cudaError_t launch_kv4_read(const Kv4Cache& c, int dqk, int dv, int dtype, const int32_t* cu, const int32_t* start,
                             int64_t tokens, void* k, void* v, cudaStream_t st) {
-  const int per = tokens_per_block(c, dqk, dv);
+  const Words n = words_of(c, dqk, dv);
+  const int per = tokens_per_block(n.words, tokens);
   const unsigned grid = unsigned((tokens + per - 1) / per);
   if (dtype == CP_DT_BF16)
-    kv4_read_kernel<<<grid, kThreads, 0, st>>>(c, Kv4Format(dqk, dv), cu, start, tokens,
+    kv4_read_kernel<<<grid, kThreads, 0, st>>>(c, Kv4Format(dqk, dv), n, cu, start, tokens,
                                                static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v), per);
   else
-    kv4_read_kernel<<<grid, kThreads, 0, st>>>(c, Kv4Format(dqk, dv), cu, start, tokens, static_cast<float*>(k),
+    kv4_read_kernel<<<grid, kThreads, 0, st>>>(c, Kv4Format(dqk, dv), n, cu, start, tokens, static_cast<float*>(k),
                                                static_cast<float*>(v), per);
   return cudaGetLastError();
 }
@@ -375,9 +513,32 @@ cudaError_t launch_kv4_read(const Kv4Cache& c, int dqk, int dv, int dtype, const
 cudaError_t launch_kv4_evict(const Kv4Cache& c, int dqk, int dv, const int32_t* lengths, int32_t budget,
                              int32_t recent, const Kv4Cache& to, int32_t* new_lengths, int32_t* kept,
                              cudaStream_t st) {
-  kv4_select_kernel<<<unsigned(c.num_seqs) * unsigned(c.hkv), kSelThreads, 0, st>>>(c, lengths, budget, recent,
-                                                                                    new_lengths, kept);
-  cudaError_t e = cudaGetLastError();
+  // CTAs a row by the longest sequence that the table can hold
+  const int64_t most = int64_t(c.max_pages) * CP_KV4_PAGE;
+  int parts = 1;
+  while (parts < 8 && int64_t(parts) * kSelSlice < most) parts *= 2;
+  const int keys = int(std::min<int64_t>(kSelKeys, (most + parts - 1) / parts));
+  static std::atomic<uint64_t> ready{0};  // devices whose kernel may use that much shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kv4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  }
+  cudaLaunchAttribute shape{};
+  shape.id = cudaLaunchAttributeClusterDimension;
+  shape.val.clusterDim.x = unsigned(parts);
+  shape.val.clusterDim.y = shape.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(c.num_seqs) * unsigned(c.hkv) * unsigned(parts));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = size_t(keys) * 4;
+  cfg.stream = st;
+  cfg.attrs = &shape;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kv4_select_kernel, c, lengths, budget, recent, new_lengths, kept, keys);
   if (e != cudaSuccess) return e;
   const int64_t units = int64_t((budget + kKv4Sub - 1) / kKv4Sub) * c.num_seqs * c.hkv;
   const int64_t grid = (units + kThreads / 32 - 1) / (kThreads / 32);
