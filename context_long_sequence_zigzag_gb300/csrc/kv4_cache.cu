@@ -12,6 +12,7 @@
 #include <cooperative_groups.h>
 
 #include "kv4.cuh"
+#include "sm103_ptx.cuh"
 
 namespace cpattn {
 namespace {
@@ -67,24 +68,44 @@ __device__ __noinline__ float exact_code(float x, float low, float s) {
 // Codes of 8 channels, channel j in bits 4j.  (x - low) times 1 / s in fp32 is
 // off by less than 1e-5 (its value is below 16), so it rounds as the exact
 // quotient does wherever it is not that close to a half; those, and scales
-// whose reciprocal or range leaves fp32, take the long way.
+// whose reciprocal or range leaves fp32, take the long way.  Channels j and
+// j + 4 go in pairs; four codes are put together as a number in base 16.
 __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float low, float s, bool plain) {
   constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: the sum's last bits are the integer
-  const float inv = __fdiv_rn(1.f, s);
-  uint32_t codes = 0;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  const uint64_t inv2 = ptx::f32x2(inv, inv), low2 = ptx::f32x2(-low, -low), magic2 = ptx::f32x2(kMagic, kMagic);
+  const uint64_t back2 = ptx::f32x2(-kMagic, -kMagic), minus2 = ptx::f32x2(-1.f, -1.f), base2 = ptx::f32x2(16.f, 16.f);
   float near = plain ? 0.f : 1.f;
+  uint64_t number = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float q = (x[j] - low) * inv, r = q + kMagic;
-    near = fmaxf(near, fabsf(q - (r - kMagic)));
-    codes |= (__float_as_uint(r) & 15u) << (4 * j);
+  for (int j = 3; j >= 0; --j) {
+    const uint64_t d = ptx::add_f32x2(ptx::f32x2(x[j], x[j + 4]), low2);
+    const uint64_t n = ptx::add_f32x2(ptx::fma_f32x2(d, inv2, magic2), back2);
+    float a, b;
+    ptx::f32x2_split(ptx::fma_f32x2(d, inv2, ptx::mul_f32x2(n, minus2)), a, b);
+    near = fmaxf(near, fmaxf(fabsf(a), fabsf(b)));
+    number = j == 3 ? n : ptx::fma_f32x2(number, base2, n);
   }
+  float a, b;
+  ptx::f32x2_split(ptx::add_f32x2(number, magic2), a, b);
+  uint32_t codes = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
   if (near > 0.5f - 1e-5f) {
     codes = 0;
 #pragma unroll 1
     for (int j = 0; j < 8; ++j) codes |= uint32_t(exact_code(x[j], low, s)) << (4 * j);
   }
   return codes;
+}
+
+// Minimum and maximum of 8 channels; NaN where one is NaN.
+__device__ __forceinline__ void range_of(const float (&x)[8], float& lo, float& hi) {
+  lo = hi = x[0];
+#pragma unroll
+  for (int j = 1; j < 8; ++j) {
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(x[j]));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(x[j]));
+  }
 }
 
 // A token's place in the cache and its row outside it.
@@ -154,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Cache c, 
   if (threadIdx.x < here) places[threadIdx.x] = place_of(c, f, cu, start, rows, src_rows, t0 + threadIdx.x);
   __syncthreads();
   const int all = here * n.words;
-  auto load = [&](int i, float (&x)[8]) {  // the groups of 8 lanes stay whole: all is a multiple of 8
+  auto load = [&](int i, float (&x)[8]) -> Word {  // the groups of 8 lanes stay whole: all is a multiple of 8
     const Word o = word_of(n, i);
     const Place& at = places[o.token];
     if (at.sub) {
@@ -163,26 +184,27 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Cache c, 
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = 0.f;
     }
+    return o;
   };
   float next[8];
-  if (threadIdx.x < all) load(threadIdx.x, next);
+  Word o_next{};
+  if (threadIdx.x < all) o_next = load(threadIdx.x, next);
   for (int i = threadIdx.x; i < all; i += kThreads) {
     float x[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = next[j];
-    if (i + kThreads < all) load(i + kThreads, next);
-    const Word o = word_of(n, i);
+    const Word o = o_next;
+    if (i + kThreads < all) o_next = load(i + kThreads, next);
     const Place& at = places[o.token];
-    // the group's minimum and maximum over its 8 lanes; x - x is NaN for NaN and infinities
-    float lo = x[0], hi = x[0], bad = x[0] - x[0];
-#pragma unroll
-    for (int j = 1; j < 8; ++j) lo = fminf(lo, x[j]), hi = fmaxf(hi, x[j]), bad += x[j] - x[j];
+    // the group's minimum and maximum over its 8 lanes
+    float lo, hi;
+    range_of(x, lo, hi);
     const uint32_t lanes = 0xffu << (threadIdx.x & 24);
 #pragma unroll
     for (int s = 1; s < 8; s <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(lanes, lo, s));
-      hi = fmaxf(hi, __shfl_xor_sync(lanes, hi, s));
-      bad += __shfl_xor_sync(lanes, bad, s);
+      const float l = __shfl_xor_sync(lanes, lo, s), h = __shfl_xor_sync(lanes, hi, s);
+      asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(l));
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(h));
     }
     if (!at.sub) continue;
     __nv_bfloat16 low = __float2bfloat16_rd(lo);
@@ -191,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Cache c, 
     __nv_bfloat16 scale = __float2bfloat16_rn((0.5f * hi - 0.5f * lowf) * (1.f / 7.5f));
     const float s = __bfloat162float(scale);
     uint32_t codes = 0;
-    if (bad != 0.f || isinf(lowf)) {  // bad is 0 or NaN
+    if (!isfinite(lowf) || !isfinite(hi)) {
       low = scale = __ushort_as_bfloat16(0x7fff);
     } else if (s > 0.f) {
       codes = codes_of(x, lowf, s, s >= 1.2e-38f && hi - lowf < INFINITY);
@@ -247,7 +269,8 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Cache c, co
     }
     float x[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = fmaf(s, float((codes >> (4 * j)) & 15u), low);
+    for (int j = 0; j < 8; ++j)  // (a code in the last bits of 2^23 is 2^23 + n)
+      x[j] = fmaf(s, __uint_as_float(((codes >> (4 * j)) & 15u) | 0x4b000000u) - 8388608.f, low);
     store8(o.is_v ? v + (at.src * c.hkv * n.nv + o.r) * 8 : k + (at.src * n.all_k + o.r) * 8, x);
   }
 }
