@@ -46,56 +46,58 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// The integer nearest to (x - low) / s, halves to even, of the exact
-// quotient, in 0 .. 15.  The sign of (x - low) - (f + 1/2) s decides between f
-// and f + 1: f + 1/2 and s have 13 bits together, so the product inside the
-// FMA is exact, and e is the rounding error of x - low.
-__device__ __noinline__ float exact_code(float x, float low, float s) {
+// The code of x where (x - low) or 1 / s leaves fp32's normal range.
+__device__ __noinline__ float far_code(float x, float low, float s) {
   const float d = x - low;
-  const float f = fminf(floorf(isinf(d) ? __fdiv_rn(0.5f * x - 0.5f * low, 0.5f * s) : __fdiv_rn(d, s)), 15.f);
-  const float bb = d - x;
-  const float e = (x - (d - bb)) + (-low - bb);
-  float n = f;
-  if (isfinite(d)) {
-    const float t = fmaf(-(f + 0.5f), s, d) + e;
-    n = t > 0.f ? f + 1.f : (t < 0.f ? f : rintf(f + 0.5f));
-  } else {
-    n = rintf(__fdiv_rn(0.5f * x - 0.5f * low, 0.5f * s));
-  }
-  return fminf(fmaxf(n, 0.f), 15.f);
+  const float q = isinf(d) ? __fdiv_rn(0.5f * x - 0.5f * low, 0.5f * s) : __fdiv_rn(d, s);
+  return fminf(fmaxf(rintf(q), 0.f), 15.f);
 }
 
-// Codes of 8 channels, channel j in bits 4j.  (x - low) times 1 / s in fp32 is
-// off by less than 1e-5 (its value is below 16), so it rounds as the exact
-// quotient does wherever it is not that close to a half; those, and scales
-// whose reciprocal or range leaves fp32, take the long way.  Channels j and
-// j + 4 go in pairs; four codes are put together as a number in base 16.
+// Codes of 8 channels, channel j in bits 4j: the integers nearest to (x - low)
+// / s, halves to even, of the exact quotient.  (x - low) times an approximate
+// 1 / s gives n; what it leaves, r = (x - low) - n s, is exact (n s has 12
+// bits, and r is below s), so |r| < s / 2 proves n.  Otherwise n is a step off
+// or halfway, which happens (bf16 values over a bf16 scale: one in some
+// hundreds); there the rounding error e of x - low and n's last bit decide.
+// Channels j and j + 4 go in pairs; four codes are put together as a number in
+// base 16.
 __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float low, float s, bool plain) {
   constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: the sum's last bits are the integer
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
   const uint64_t inv2 = ptx::f32x2(inv, inv), low2 = ptx::f32x2(-low, -low), magic2 = ptx::f32x2(kMagic, kMagic);
-  const uint64_t back2 = ptx::f32x2(-kMagic, -kMagic), minus2 = ptx::f32x2(-1.f, -1.f), base2 = ptx::f32x2(16.f, 16.f);
-  float near = plain ? 0.f : 1.f;
-  uint64_t number = 0;
+  const uint64_t back2 = ptx::f32x2(-kMagic, -kMagic), minus2 = ptx::f32x2(-s, -s), base2 = ptx::f32x2(16.f, 16.f);
+  const float half = 0.5f * s;
+  float n[8], r[8], most = 0.f;
 #pragma unroll
-  for (int j = 3; j >= 0; --j) {
+  for (int j = 0; j < 4; ++j) {
     const uint64_t d = ptx::add_f32x2(ptx::f32x2(x[j], x[j + 4]), low2);
-    const uint64_t n = ptx::add_f32x2(ptx::fma_f32x2(d, inv2, magic2), back2);
-    float a, b;
-    ptx::f32x2_split(ptx::fma_f32x2(d, inv2, ptx::mul_f32x2(n, minus2)), a, b);
-    near = fmaxf(near, fmaxf(fabsf(a), fabsf(b)));
-    number = j == 3 ? n : ptx::fma_f32x2(number, base2, n);
+    const uint64_t k = ptx::add_f32x2(ptx::fma_f32x2(d, inv2, magic2), back2);
+    ptx::f32x2_split(k, n[j], n[j + 4]);
+    ptx::f32x2_split(ptx::fma_f32x2(k, minus2, d), r[j], r[j + 4]);
+    most = fmaxf(most, fmaxf(fabsf(r[j]), fabsf(r[j + 4])));
   }
+  if (!plain) {
+#pragma unroll  // (an index that is not a constant would put x into local memory)
+    for (int j = 0; j < 8; ++j) n[j] = far_code(x[j], low, s);
+  } else if (most >= half) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float a = fabsf(r[j]), step = copysignf(1.f, r[j]);
+      if (a >= half) {
+        const float d = x[j] - low, b = d - x[j];
+        const float e = ((x[j] - (d - b)) + (-low - b)) * step;  // the exact residual's |r| is a + e
+        const bool odd = __float_as_uint(n[j] + kMagic) & 1u;
+        if (a > half || e > 0.f || (e == 0.f && odd)) n[j] += step;
+      }
+    }
+  }
+  uint64_t number = ptx::f32x2(n[3], n[7]);
+#pragma unroll
+  for (int j = 2; j >= 0; --j) number = ptx::fma_f32x2(number, base2, ptx::f32x2(n[j], n[j + 4]));
   float a, b;
   ptx::f32x2_split(ptx::add_f32x2(number, magic2), a, b);
-  uint32_t codes = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
-  if (near > 0.5f - 1e-5f) {
-    codes = 0;
-#pragma unroll 1
-    for (int j = 0; j < 8; ++j) codes |= uint32_t(exact_code(x[j], low, s)) << (4 * j);
-  }
-  return codes;
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
 }
 
 // Minimum and maximum of 8 channels; NaN where one is NaN.
