@@ -1,11 +1,12 @@
 // kv4_cache.cu — the kernels that write, read back and evict from the 4-bit
 // key/value cache (format: include/cp_attn.h; attention over it: kv4_attn.cu).
 //
-// All three move bytes: a thread handles one 32-bit word of codes (8
-// channels), so a token's head of 128 channels is 16 lanes, its 64-channel
-// groups are aligned runs of 8 lanes, and both the tensor side (16 or 32
-// bytes a lane) and the cache side (whole 64-byte rows) are contiguous
-// across a warp.
+// All three move bytes.  In append and read a thread handles 16 channels, two
+// 32-bit words of codes: a token's head of 128 channels is 8 lanes, its
+// 64-channel groups are aligned runs of 4, and both the tensor side (32 or 64
+// bytes a lane) and the cache side (whole 64-byte rows) are contiguous across
+// a warp.  (With one word a thread, the places, addresses and reductions took
+// as many instructions as the quantising.)
 #include <algorithm>
 #include <atomic>
 
@@ -100,13 +101,13 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float low, flo
   return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
 }
 
-// Minimum and maximum of 8 channels; NaN where one is NaN.
-__device__ __forceinline__ void range_of(const float (&x)[8], float& lo, float& hi) {
-  lo = hi = x[0];
+// Minimum and maximum of 16 channels; NaN where one is NaN.
+__device__ __forceinline__ void range_of(const float (&x)[2][8], float& lo, float& hi) {
+  lo = hi = x[0][0];
 #pragma unroll
-  for (int j = 1; j < 8; ++j) {
-    asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(x[j]));
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(x[j]));
+  for (int j = 1; j < 16; ++j) {
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(x[j / 8][j % 8]));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(x[j / 8][j % 8]));
   }
 }
 
@@ -142,15 +143,15 @@ __device__ __forceinline__ Place place_of(const Kv4Cache& c, const Kv4Format& f,
   return at;
 }
 
-// What word i of a CTA's tokens is: of which token, k or v, head, word.  The
+// What piece i (16 channels, two words) of a CTA's tokens is: of which token, k or v, head, piece.  The
 // divisions are products with rounded-up reciprocals (exact while i times the
 // divisor stays below 2^32, which the launch sees to).
 struct Words {
-  int nk, nv, words, all_k;  // words of a head's k, of its v, of a token, of all its k
+  int nk, nv, words, all_k;  // pieces of a head's k, of its v, of a token, of all its k
   uint32_t by_words, by_nk, by_nv;
 };
 struct Word {
-  int token, r, head, word;  // r: word of all heads' k, or of all their v
+  int token, r, head, word;  // r: piece of all heads' k, or of all their v
   bool is_v;
 };
 __device__ __forceinline__ Word word_of(const Words& n, int i) {
@@ -177,33 +178,35 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Cache c, 
   if (threadIdx.x < here) places[threadIdx.x] = place_of(c, f, cu, start, rows, src_rows, t0 + threadIdx.x);
   __syncthreads();
   const int all = here * n.words;
-  auto load = [&](int i, float (&x)[8]) -> Word {  // the groups of 8 lanes stay whole: all is a multiple of 8
+  auto load = [&](int i, float (&x)[2][8]) -> Word {  // the groups of 4 lanes stay whole: all is a multiple of 4
     const Word o = word_of(n, i);
     const Place& at = places[o.token];
     if (at.sub) {
-      load8(o.is_v ? v + (at.src * c.hkv * n.nv + o.r) * 8 : k + (at.src * n.all_k + o.r) * 8, x);
+      const E* p = o.is_v ? v + (at.src * c.hkv * n.nv + o.r) * 16 : k + (at.src * n.all_k + o.r) * 16;
+      load8(p, x[0]);
+      load8(p + 8, x[1]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = 0.f;
+      for (int j = 0; j < 8; ++j) x[0][j] = x[1][j] = 0.f;
     }
     return o;
   };
-  float next[8];
+  float next[2][8];
   Word o_next{};
   if (threadIdx.x < all) o_next = load(threadIdx.x, next);
   for (int i = threadIdx.x; i < all; i += kThreads) {
-    float x[8];
+    float x[2][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = next[j];
+    for (int j = 0; j < 8; ++j) x[0][j] = next[0][j], x[1][j] = next[1][j];
     const Word o = o_next;
     if (i + kThreads < all) o_next = load(i + kThreads, next);
     const Place& at = places[o.token];
-    // the group's minimum and maximum over its 8 lanes
+    // the group's minimum and maximum over its 4 lanes
     float lo, hi;
     range_of(x, lo, hi);
-    const uint32_t lanes = 0xffu << (threadIdx.x & 24);
+    const uint32_t lanes = 0xfu << (threadIdx.x & 28);
 #pragma unroll
-    for (int s = 1; s < 8; s <<= 1) {
+    for (int s = 1; s < 4; s <<= 1) {
       const float l = __shfl_xor_sync(lanes, lo, s), h = __shfl_xor_sync(lanes, hi, s);
       asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(l));
       asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(h));
@@ -214,23 +217,29 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Cache c, 
     // (max - low) / 15; halved first, so that no finite range overflows
     __nv_bfloat16 scale = __float2bfloat16_rn((0.5f * hi - 0.5f * lowf) * (1.f / 7.5f));
     const float s = __bfloat162float(scale);
-    uint32_t codes = 0;
+    uint32_t codes[2] = {0, 0};
     if (!isfinite(lowf) || !isfinite(hi)) {
       low = scale = __ushort_as_bfloat16(0x7fff);
     } else if (s > 0.f) {
-      codes = codes_of(x, lowf, s, s >= 1.2e-38f && hi - lowf < INFINITY);
+      const bool plain = s >= 1.2e-38f && hi - lowf < INFINITY;
+      codes[0] = codes_of(x[0], lowf, s, plain);
+      codes[1] = codes_of(x[1], lowf, s, plain);
     }
     uint8_t* sub = at.sub + int64_t(o.head) * f.block();
-    const int group = o.word / 8;
+    const int w0 = 2 * o.word, group = o.word / 4;
     if (o.is_v) {
-      reinterpret_cast<uint32_t*>(sub + f.vc() + at.row * (f.dv / 2))[f.vword(o.word)] = codes;
-      if (o.word % 8 == 0) {
+      uint32_t* to = reinterpret_cast<uint32_t*>(sub + f.vc() + at.row * (f.dv / 2));
+      to[f.vword(w0)] = codes[0];
+      to[f.vword(w0 + 1)] = codes[1];
+      if (o.word % 4 == 0) {
         reinterpret_cast<__nv_bfloat16*>(sub + f.vs())[at.row * f.gv() + group] = scale;
         reinterpret_cast<__nv_bfloat16*>(sub + f.vl())[group * kKv4Sub + at.row] = low;
       }
     } else {
-      reinterpret_cast<uint32_t*>(sub + f.kc() + at.row * (f.dqk / 2))[f.kword(o.word)] = codes;
-      if (o.word % 8 == 0) {
+      uint32_t* to = reinterpret_cast<uint32_t*>(sub + f.kc() + at.row * (f.dqk / 2));
+      to[f.kword(w0)] = codes[0];
+      to[f.kword(w0 + 1)] = codes[1];
+      if (o.word % 4 == 0) {
         __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(sub + f.kp()) + at.row * 2 * f.gk() + group;
         p[0] = scale;
         p[f.gk()] = low;
@@ -256,24 +265,34 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Cache c, co
     const Place& at = places[o.token];
     if (!at.sub) continue;
     const uint8_t* sub = at.sub + int64_t(o.head) * f.block();
-    const int group = o.word / 8;
-    uint32_t codes;
+    const int w0 = 2 * o.word, group = o.word / 4;
+    uint32_t codes[2];
     float s, low;
+    E* to;
     if (o.is_v) {
-      codes = reinterpret_cast<const uint32_t*>(sub + f.vc() + at.row * (f.dv / 2))[f.vword(o.word)];
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(sub + f.vc() + at.row * (f.dv / 2));
+      codes[0] = from[f.vword(w0)];
+      codes[1] = from[f.vword(w0 + 1)];
       s = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sub + f.vs())[at.row * f.gv() + group]);
       low = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sub + f.vl())[group * kKv4Sub + at.row]);
+      to = v + (at.src * c.hkv * n.nv + o.r) * 16;
     } else {
-      codes = reinterpret_cast<const uint32_t*>(sub + f.kc() + at.row * (f.dqk / 2))[f.kword(o.word)];
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(sub + f.kc() + at.row * (f.dqk / 2));
+      codes[0] = from[f.kword(w0)];
+      codes[1] = from[f.kword(w0 + 1)];
       const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(sub + f.kp()) + at.row * 2 * f.gk() + group;
       s = __bfloat162float(p[0]);
       low = __bfloat162float(p[f.gk()]);
+      to = k + (at.src * n.all_k + o.r) * 16;
     }
-    float x[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)  // (a code in the last bits of 2^23 is 2^23 + n)
-      x[j] = fmaf(s, __uint_as_float(((codes >> (4 * j)) & 15u) | 0x4b000000u) - 8388608.f, low);
-    store8(o.is_v ? v + (at.src * c.hkv * n.nv + o.r) * 8 : k + (at.src * n.all_k + o.r) * 8, x);
+    for (int w = 0; w < 2; ++w) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)  // (a code in the last bits of 2^23 is 2^23 + n)
+        x[j] = fmaf(s, __uint_as_float(((codes[w] >> (4 * j)) & 15u) | 0x4b000000u) - 8388608.f, low);
+      store8(to + 8 * w, x);
+    }
   }
 }
 
@@ -493,8 +512,8 @@ static int tokens_per_block(int words, int64_t tokens) {
 
 static Words words_of(const Kv4Cache& c, int dqk, int dv) {
   Words n;
-  n.nk = dqk / 8;
-  n.nv = dv / 8;
+  n.nk = dqk / 16;
+  n.nv = dv / 16;
   n.all_k = c.hkv * n.nk;
   n.words = c.hkv * (n.nk + n.nv);
   auto inverse = [](int d) { return uint32_t(((uint64_t(1) << 32) + d - 1) / d); };
