@@ -22,6 +22,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "internal.h"
+#include "kv4.cuh"
 #include "plan_check.cuh"
 
 namespace cpattn {
@@ -680,6 +681,68 @@ PlanKind dkdv_plan_kind(const cp_desc_t* d) {
 // The key-weight kernel's: 128-row query steps for both of its head dims.
 PlanKind key_weights_plan_kind(const cp_desc_t* d) { return use_tc_key_weights(d) ? kPlanKeyMajorPacked : kPlanKeyMajor; }
 
+// Few counted queries a sequence: the last `last` of each, at most this many
+// columns (queries times the heads that share a key).
+bool use_window(const cp_desc_t* d, int64_t last) {
+  return use_tc_key_weights(d) && last > 0 && last * (d->hq / d->hkv) <= 256 &&
+         key_weights_window_supported(d->d_qk, int32_t(last * (d->hq / d->hkv)));
+}
+
+// Key tiles, sequences and counted queries of a window, one after the other
+// as the kernel reads them.  Cached like the plans.
+struct Window {
+  std::vector<char> bytes;
+  int32_t num_tiles = 0;
+  size_t seqs = 0, rows = 0;  // offsets
+};
+std::shared_ptr<const Window> get_window(const cp_desc_t* d, const ShardMap& m, int64_t last) {
+  static std::mutex mu;
+  static std::list<std::pair<std::vector<int64_t>, std::shared_ptr<const Window>>> cache;  // most recent first
+  constexpr size_t kMost = 16;
+  std::vector<int64_t> key = {last, d->total_tokens, d->cp_size, d->layout, d->num_seqs};
+  if (d->cu_seqlens) key.insert(key.end(), d->cu_seqlens, d->cu_seqlens + d->num_seqs + 1);
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    for (auto it = cache.begin(); it != cache.end(); ++it)
+      if (it->first == key) {
+        cache.splice(cache.begin(), cache, it);
+        return it->second;
+      }
+  }
+  const std::vector<int32_t> cu = seqlens_of(d);
+  std::vector<WinTile> tiles;
+  std::vector<WinSeq> seqs(size_t(m.S));
+  std::vector<int32_t> rows;
+  for (int s = 0; s < m.S; ++s) {
+    const int32_t len = cu[s + 1] - cu[s], count = int32_t(std::min<int64_t>(last, len));
+    WinSeq& q = seqs[size_t(s)];
+    q = WinSeq{int32_t(tiles.size()), 0, int32_t(rows.size()), count, len - count, {}};
+    rows.resize(rows.size() + size_t(count));
+    for (int r = 0; r < m.C; ++r)
+      for (int k = 0; k < m.per; ++k) {
+        const Chunk& c = m.at(r, s, k);
+        const int32_t pos0 = int32_t(c.grow0 - cu[s]);
+        for (int32_t t = 0; t < c.len; t += kTile)
+          tiles.push_back(WinTile{int32_t(c.srow0 + t), std::min(kTile, c.len - t), pos0 + t * c.stride, c.stride, s, {}});
+        for (int32_t t = tokens_before_window(c, cu[s], len, last); t < c.len; ++t)
+          rows[size_t(q.row0 + pos0 + t * c.stride - q.pos0)] = int32_t(c.srow0 + t);
+      }
+    q.tiles = int32_t(tiles.size()) - q.tile0;
+  }
+  auto w = std::make_shared<Window>();
+  w->num_tiles = int32_t(tiles.size());
+  w->seqs = align256(tiles.size() * sizeof(WinTile));
+  w->rows = w->seqs + align256(seqs.size() * sizeof(WinSeq));
+  w->bytes.resize(w->rows + align256(rows.size() * 4));
+  std::memcpy(w->bytes.data(), tiles.data(), tiles.size() * sizeof(WinTile));
+  std::memcpy(w->bytes.data() + w->seqs, seqs.data(), seqs.size() * sizeof(WinSeq));
+  std::memcpy(w->bytes.data() + w->rows, rows.data(), rows.size() * 4);
+  std::lock_guard<std::mutex> lock(mu);
+  cache.emplace_front(std::move(key), w);
+  if (cache.size() > kMost) cache.pop_back();
+  return w;
+}
+
 // Bytes that hold the key-major plan of any observation window: a window only
 // takes query runs away or shortens them, runs that are not merged are at
 // most the (key tile, query chunk) pairs, and gathering turns a run into at
@@ -695,8 +758,12 @@ size_t key_weights_bytes(const cp_desc_t* d, const ShardMap& m) {
           runs += A.len > 0 && (d->causal == 0 || query_pos0(m, A, B) + A.len - 1 >= B.pos0 + t0);
         }
     }
-  return align256(size_t(tiles) * sizeof(TileDesc)) + align256(size_t(runs) * 2 * sizeof(RangeDesc)) +
-         align256(size_t(runs) * sizeof(PackMask)) + align256(size_t(runs) * 2 * sizeof(PackPiece));
+  const size_t plan = align256(size_t(tiles) * sizeof(TileDesc)) + align256(size_t(runs) * 2 * sizeof(RangeDesc)) +
+                      align256(size_t(runs) * sizeof(PackMask)) + align256(size_t(runs) * 2 * sizeof(PackPiece));
+  // and what the kernel for few queries reads, at most 256 a sequence
+  const size_t rows = size_t(std::min<int64_t>(d->total_tokens, int64_t(m.S) * 256));
+  return std::max(plan, align256(size_t(tiles) * sizeof(WinTile)) + align256(size_t(m.S) * sizeof(WinSeq)) +
+                            align256(rows * 4));
 }
 
 AttnArgs base_args(const cp_desc_t* d) {
@@ -1558,15 +1625,26 @@ cp_status_t cp_attn_key_weights(const cp_desc_t* d, int64_t last, const void* q,
     if (p == nullptr || !aligned16(p)) return CP_ERR_INVALID_ARG;
   if (last >= d->total_tokens) last = 0;
   const ShardMap m = build_map(d);
-  const auto pp = get_plan(d, m, key_weights_plan_kind(d), -1, -1, -1, 0, last);
-  const Plan& p = *pp;
-  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < plan_bytes(p)) return CP_ERR_WORKSPACE;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   AttnArgs a = base_args(d);
   a.q = q;
   a.k = k;
   a.lse_in = lse;
   a.out = w;
+  if (use_window(d, last)) {
+    const auto win = get_window(d, m, last);
+    if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < win->bytes.size()) return CP_ERR_WORKSPACE;
+    if (h2d_async(ws, win->bytes.data(), win->bytes.size(), cs) != cudaSuccess) return CP_ERR_CUDA;
+    const char* base = static_cast<const char*>(ws);
+    return launch_key_weights_window(a, reinterpret_cast<const WinTile*>(base), win->num_tiles,
+                                     reinterpret_cast<const WinSeq*>(base + win->seqs),
+                                     reinterpret_cast<const int32_t*>(base + win->rows), kv4_sm_count(), cs) == cudaSuccess
+               ? CP_OK
+               : CP_ERR_CUDA;
+  }
+  const auto pp = get_plan(d, m, key_weights_plan_kind(d), -1, -1, -1, 0, last);
+  const Plan& p = *pp;
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < plan_bytes(p)) return CP_ERR_WORKSPACE;
   st = stage_plan(p, static_cast<char*>(ws), cs, a, d->total_tokens, d->total_tokens);
   if (st != CP_OK) return st;
   const cudaError_t e = use_tc_key_weights(d) ? launch_tc_key_weights(a, cs) : launch_simt_key_weights(a, d->dtype, cs);

@@ -170,6 +170,22 @@ cudaError_t launch_tc_bwd_dq(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_simt_key_weights(const AttnArgs& a, int32_t dtype, cudaStream_t st);
 cudaError_t launch_tc_key_weights(const AttnArgs& a, cudaStream_t st);
 bool tc_key_weights_supported(int32_t d_qk);
+// The same for a few counted queries a sequence, which stay on chip while the key tiles stream past them.
+struct WinTile {  // up to kTile sharded rows of one chunk
+  int32_t row0, nrows;
+  int32_t pos0, stride;  // positions pos0, pos0 + stride, ...
+  int32_t seq, pad[3];
+};
+static_assert(sizeof(WinTile) == 32, "WinTile layout");
+struct WinSeq {
+  int32_t tile0, tiles;  // its key tiles
+  int32_t row0, count;   // its counted queries' entries in the row list
+  int32_t pos0, pad[3];  // position of the first of them (the others follow)
+};
+static_assert(sizeof(WinSeq) == 32, "WinSeq layout");
+bool key_weights_window_supported(int32_t d_qk, int32_t columns);
+cudaError_t launch_key_weights_window(const AttnArgs& a, const WinTile* tiles, int32_t num_tiles, const WinSeq* seqs,
+                                      const int32_t* rows, int32_t sms, cudaStream_t st);
 bool tc_fwd_supported(int32_t d_qk, int32_t d_v);
 bool tc_bwd_supported(int32_t d_qk, int32_t d_v);
 cudaError_t read_and_clear_device_status(int32_t* code, cudaStream_t st);

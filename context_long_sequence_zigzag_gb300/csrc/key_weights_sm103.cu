@@ -22,6 +22,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "internal.h"
@@ -355,7 +356,280 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// ===========================================================================
+// Few queries: the last ones of a prompt (an observation window)
+// ===========================================================================
+// With G * queries <= 256 all of a kv head's columns are one B operand: it is
+// gathered into shared memory once and stays, and the key tiles stream past it
+// (the key-major kernel above would start a CTA for every key tile to visit a
+// few steps).  The keys are read once and nothing else is: 64K tokens, 8 kv
+// heads of 128 are 134 MB, 20 us of HBM; per tile of 128 keys that is 1400
+// cycles an SM, the MMA (N = 256) and the exponentials take 1024 each.
+// Persistent: the (kv head, key tile) items are cut evenly over the SMs, in
+// order, so a CTA gathers queries once or twice.  S has two TMEM buffers, each
+// read by eight compute warps, four a half of the columns (with four warps a
+// buffer a tile took 4500 cycles: too few warps to hide their latencies).
+
+constexpr int kWinCols = 256;
+constexpr int kWinThreads = 4 * kGroupThreads + 64;
+constexpr int kWinProducer = 16, kWinIssuer = 17;  // warps
+
+struct WinParams {
+  CUtensorMap tk;
+  AttnArgs a;
+  const WinTile* tiles;
+  const WinSeq* seqs;
+  const int32_t* rows;  // sharded rows of the counted queries
+  int32_t num_tiles;
+  int32_t* err;
+};
+
+template <int DQK>
+struct WinCfg {
+  static constexpr int kPanels = DQK / 64;
+  static constexpr int NS = DQK == 128 ? 4 : 2;  // stages of K
+  static constexpr uint32_t kTileBytes = kPanels * kPanel;
+  static constexpr uint32_t kQPanel = kWinCols * 128;  // kWinCols rows x 64 bf16 columns
+  static constexpr uint32_t offQ = 0;
+  static constexpr uint32_t offK = kPanels * kQPanel;
+  static constexpr uint32_t offStat = offK + NS * kTileBytes;  // -lse log2e of every column
+  static constexpr uint32_t offPos = offStat + kWinCols * 4;   // and its query's position
+  static constexpr uint32_t offPart = offPos + kWinCols * 4;   // [parity][2][BT]: sums of the second half's columns
+  static constexpr uint32_t offBar = offPart + 4 * BT * 4;
+  static constexpr int kNumBars = 2 * NS + 4;
+  static constexpr uint32_t kSmem = offBar + kNumBars * 8 + 16;
+  static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+template <int DQK>
+__global__ void __launch_bounds__(kWinThreads, 1) key_weights_window_kernel(const __grid_constant__ WinParams p) {
+  using C = WinCfg<DQK>;
+  constexpr int NS = C::NS;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = ptx::smem_u32(smem);
+  const AttnArgs& a = p.a;
+  if (sbase & 1023u) {
+    if (threadIdx.x == 0 && p.err) atomicCAS(p.err, 0, 0x100 | kSiteAlign);
+    return;
+  }
+  const int64_t items = int64_t(a.hkv) * p.num_tiles;
+  const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
+  if (i0 == i1) return;
+  const int G = a.hq / a.hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar_full = [&](int s) { return sbase + C::offBar + 8u * s; };
+  auto bar_empty = [&](int s) { return sbase + C::offBar + 8u * (NS + s); };
+  auto bar_s_full = [&](int b) { return sbase + C::offBar + 8u * (2 * NS + b); };
+  auto bar_s_free = [&](int b) { return sbase + C::offBar + 8u * (2 * NS + 2 + b); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::offBar + C::kNumBars * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::offBar + C::kNumBars * 8 + 4);
+  float* stat = reinterpret_cast<float*>(smem + C::offStat);
+  int32_t* qpos = reinterpret_cast<int32_t*>(smem + C::offPos);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      ptx::mbar_init(bar_full(s), 2);
+      ptx::mbar_init(bar_empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(bar_s_full(b), 1);
+      ptx::mbar_init(bar_s_free(b), 8);
+    }
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == kWinIssuer) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish();
+  }
+  if (warp == kWinProducer && lane == 0) ptx::prefetch_tmap(&p.tk);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const ptx::WaitCtx wctx{abort_flag, p.err, kWaitLimitNs};
+  const uint64_t sl2x2 = ptx::f32x2(a.scale * kLog2e, a.scale * kLog2e);
+  bool ok = true;
+
+  for (int64_t seg = i0; seg < i1;) {
+    // ---- a kv head and a sequence: its counted queries become the B operand
+    const int kvh = int(seg / p.num_tiles);
+    const WinSeq q = p.seqs[p.tiles[seg - int64_t(kvh) * p.num_tiles].seq];
+    const int64_t end = min(i1, int64_t(kvh) * p.num_tiles + q.tile0 + q.tiles);
+    const int cols = G * q.count, N = (cols + 15) & ~15;
+    for (int e = threadIdx.x; e < N * (DQK / 8); e += kWinThreads) {
+      const int n = e / (DQK / 8), chunk = e - n * (DQK / 8), g = n / q.count;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (n < cols) {
+        const int h = a.gqa_interleaved ? g * a.hkv + kvh : kvh * G + g;
+        v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                 (int64_t(p.rows[q.row0 + n - g * q.count]) * a.hq + h) * DQK) + chunk);
+      }
+      *reinterpret_cast<uint4*>(smem + C::offQ + (chunk >> 3) * C::kQPanel + n * 128 + (((chunk & 7) ^ (n & 7)) << 4)) = v;
+    }
+    for (int n = threadIdx.x; n < kWinCols; n += kWinThreads) {
+      const int g = n / q.count, j = n - g * q.count;
+      const int h = a.gqa_interleaved ? g * a.hkv + kvh : kvh * G + g;
+      stat[n] = n < cols ? -(a.lse_in[int64_t(h) * a.T + p.rows[q.row0 + j]] * kLog2e) : -INFINITY;
+      qpos[n] = a.causal ? q.pos0 + j : INT32_MAX;
+    }
+    ptx::fence_proxy_async_smem();
+    __syncthreads();
+
+    if (warp == kWinProducer) {
+      // ---------------------------------------------------------- producers: lanes 0 and 1 split the panels
+      if (lane < 2) {
+        const uint32_t bytes = uint32_t((C::kPanels + 1 - lane) / 2) * kPanel;
+        for (int64_t i = seg; ok && i < end; ++i) {
+          const int64_t k = i - i0;
+          const int st = int(k % NS);
+          if (k >= NS) ok = ptx::mbar_wait(bar_empty(st), uint32_t((k / NS) - 1) & 1, kSiteQEmpty, wctx);
+          if (!ok) break;
+          const WinTile t = p.tiles[i - int64_t(kvh) * p.num_tiles];
+          ptx::mbar_arrive_expect_tx(bar_full(st), bytes);
+          for (int c = lane; c < C::kPanels; c += 2)
+            ptx::tma_load_3d(sbase + C::offK + st * C::kTileBytes + c * kPanel, &p.tk, bar_full(st), c * 64, kvh, t.row0);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kWinIssuer) {
+      // ---------------------------------------------------------- MMA issuer (whole warp)
+      const uint32_t idS = ptx::idesc_bf16_f32(BT, 16, false, false) - (2u << 17) + (uint32_t(N >> 3) << 17);
+      for (int64_t i = seg; ok && i < end; ++i) {
+        const int64_t k = i - i0;
+        const int st = int(k % NS), b = int(k & 1);
+        ok = ptx::mbar_wait_w(bar_full(st), uint32_t(k / NS) & 1, kSiteQFull, wctx) &&
+             (k < 2 || ptx::mbar_wait_w(bar_s_free(b), uint32_t((k >> 1) - 1) & 1, kSiteSFree, wctx));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint64_t dk = ptx::sdesc_sw128(sbase + C::offK + st * C::kTileBytes, 16, 1024);
+        const uint64_t dq = ptx::sdesc_sw128(sbase + C::offQ, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < DQK / 16; ++kk)
+          ptx::mma_ss_w(tmem + b * kWinCols, dk + (((kk >> 2) * kPanel + (kk & 3) * 32) >> 4),
+                        dq + (((kk >> 2) * C::kQPanel + (kk & 3) * 32) >> 4), idS, kk > 0);
+        ptx::mma_commit_w(bar_s_full(b));
+        ptx::mma_commit_w(bar_empty(st));
+      }
+    } else {
+      // ---------------------------------------------------------- column sums: groups of parity 0 and 1, two halves each
+      const int par = warp >> 3, half = (warp >> 2) & 1, t = threadIdx.x & (kGroupThreads - 1);
+      const uint32_t tS = tmem + (uint32_t((warp & 3) * 32) << 16) + par * kWinCols;
+      float* part = reinterpret_cast<float*>(smem + C::offPart) + par * 2 * BT;
+      const int chunks = (N + 31) / 32, ch0 = half ? (chunks + 1) / 2 : 0, ch1 = half ? chunks : (chunks + 1) / 2;
+      for (int64_t i = seg + (((seg - i0) & 1) != par); i < end; i += 2) {
+        const int64_t k = i - i0;
+        const WinTile tile = p.tiles[i - int64_t(kvh) * p.num_tiles];
+        const int kpos = tile.pos0 + t * tile.stride;
+        const bool need_mask = a.causal && tile.pos0 + (tile.nrows - 1) * tile.stride > q.pos0;
+        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_poll(bar_s_full(par), uint32_t(k >> 1) & 1, kSiteSFull, wctx));
+        float w = 0.f;
+        if (ok) {
+          ptx::tc_fence_after();
+          auto sums = [&](auto mask_) {
+            constexpr bool MASK = decltype(mask_)::value;
+#pragma unroll 1
+            for (int ch = ch0; ch < ch1; ++ch) {  // 32 columns
+              uint32_t x[32];
+              ptx::tmem_ld32(tS + 32 * ch, x);
+              ptx::tmem_ld_wait();
+              ptx::reg_fence32(x);
+              uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 nl = *reinterpret_cast<const float4*>(stat + 32 * ch + j);
+                uint64_t e0 = exp2_pair(ptx::fma_f32x2(ptx::f32x2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), sl2x2,
+                                                       ptx::f32x2(nl.x, nl.y)));
+                uint64_t e1 = exp2_pair(ptx::fma_f32x2(ptx::f32x2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])),
+                                                       sl2x2, ptx::f32x2(nl.z, nl.w)));
+                if (MASK) {
+                  float v[4];
+                  ptx::f32x2_split(e0, v[0], v[1]);
+                  ptx::f32x2_split(e1, v[2], v[3]);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    if (kpos > qpos[32 * ch + j + e] || 32 * ch + j + e >= cols) v[e] = 0.f;
+                  e0 = ptx::f32x2(v[0], v[1]);
+                  e1 = ptx::f32x2(v[2], v[3]);
+                }
+                s0 = ptx::add_f32x2(s0, e0);
+                s1 = ptx::add_f32x2(s1, e1);
+              }
+              float a0, a1;
+              ptx::f32x2_split(ptx::add_f32x2(s0, s1), a0, a1);
+              w += a0 + a1;
+            }
+          };
+          // (columns from cols on in the last 32 are stale numbers where N is no multiple of 32: masked too)
+          if (need_mask || N % 32) sums(std::true_type{});
+          else sums(std::false_type{});
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar_s_free(par));
+        }
+        // the halves meet; the place is used again two of this parity's items on, past the barrier between
+        float* p2 = part + (uint32_t(k >> 1) & 1) * BT;
+        if (half) p2[t] = w;
+        ptx::named_barrier(1 + par, 2 * kGroupThreads);
+        if (!half && t < tile.nrows)
+          static_cast<float*>(a.out)[int64_t(kvh) * a.T + tile.row0 + t] = w + p2[t];
+      }
+    }
+    __syncthreads();  // the operand and the statistics have been read
+    seg = end;
+  }
+  // what was issued ends before the CTA goes: after a wait that gave up, the copies and the MMAs still in flight
+  if (*abort_flag && warp == kWinProducer && lane == 0) {
+    volatile int no_abort = 0;
+    const ptx::WaitCtx drain{&no_abort, nullptr, kWaitLimitNs / 4};
+    for (int s = 0; s < NS; ++s) {
+      ptx::mbar_wait(bar_full(s), 0, kSiteDrain, drain);
+      ptx::mbar_wait(bar_full(s), 1, kSiteDrain, drain);
+    }
+    for (int b = 0; b < 2; ++b) ptx::mbar_wait(bar_s_full(b), 0, kSiteDrain, drain);
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kWinIssuer) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int DQK>
+cudaError_t launch_window(const AttnArgs& a, const WinTile* tiles, int32_t num_tiles, const WinSeq* seqs,
+                          const int32_t* rows, int sms, cudaStream_t st) {
+  using C = WinCfg<DQK>;
+  WinParams p;
+  p.a = a;
+  p.tiles = tiles;
+  p.seqs = seqs;
+  p.rows = rows;
+  p.num_tiles = num_tiles;
+  p.err = device_error_word();
+  if (!make_map_3d(&p.tk, a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, DQK, a.hkv, a.T, 64, BT, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(key_weights_window_kernel<DQK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       int(C::kSmem));
+  if (e != cudaSuccess) return e;
+  const int64_t items = int64_t(num_tiles) * a.hkv;
+  if (items == 0) return cudaSuccess;
+  key_weights_window_kernel<DQK><<<unsigned(std::min<int64_t>(items, sms)), kWinThreads, C::kSmem, st>>>(p);
+  return cudaGetLastError();
+}
+
 }  // namespace
+
+bool key_weights_window_supported(int32_t d_qk, int32_t columns) {
+  return tc_key_weights_supported(d_qk) && columns <= kWinCols;
+}
+
+cudaError_t launch_key_weights_window(const AttnArgs& a, const WinTile* tiles, int32_t num_tiles, const WinSeq* seqs,
+                                      const int32_t* rows, int32_t sms, cudaStream_t st) {
+  if (a.d_qk == 128) return launch_window<128>(a, tiles, num_tiles, seqs, rows, sms, st);
+  if (a.d_qk == 192) return launch_window<192>(a, tiles, num_tiles, seqs, rows, sms, st);
+  return cudaErrorInvalidValue;
+}
 
 bool tc_key_weights_supported(int32_t d_qk) { return d_qk == 128 || d_qk == 192; }
 
