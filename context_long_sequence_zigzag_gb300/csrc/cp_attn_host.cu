@@ -339,16 +339,18 @@ int32_t tokens_before_window(const Chunk& A, int64_t seq_row0, int64_t len, int6
 
 // Key-major plan for the backward: every key tile with the query runs that
 // see it, visiting ranks r, r+1, ... (the direction dK/dV travel in a ring).
-// last > 0 keeps only the last `last` queries of every sequence.
-Plan build_bwd_plan(const cp_desc_t* d, const ShardMap& m, bool pack = false, int64_t last = 0) {
+// last > 0 keeps only the last `last` queries of every sequence; tile_rows:
+// rows of a key tile.
+Plan build_bwd_plan(const cp_desc_t* d, const ShardMap& m, bool pack = false, int64_t last = 0,
+                    int32_t tile_rows = kTile) {
   Plan p;
   const bool causal = d->causal != 0;
   const std::vector<int32_t> cu = seqlens_of(d);
   for (const Chunk& B : m.chunks) {
-    for (int32_t t0 = 0; t0 < B.len; t0 += kTile) {
+    for (int32_t t0 = 0; t0 < B.len; t0 += tile_rows) {
       TileDesc t{};
       t.row0 = int32_t(B.srow0 + t0);
-      t.nrows = std::min(kTile, B.len - t0);
+      t.nrows = std::min(tile_rows, B.len - t0);
       t.pos0 = B.pos0 + t0;
       t.rank = B.rank;
       t.out_row0 = t.row0;
@@ -459,8 +461,15 @@ size_t plan_bytes(const Plan& p) {
 // gathered into shared key tiles (the tensor-core forward and dQ kernels
 // read those); kPlanKeyMajorPacked: the key-major plan with the tails of
 // the query runs that see a whole key tile gathered into shared query tiles
-// (the tensor-core dK/dV kernel with 128-row query steps).
-enum PlanKind : int64_t { kPlanQueryMajor = 0, kPlanKeyMajor = 1, kPlanQueryMajorPacked = 2, kPlanKeyMajorPacked = 3 };
+// (the tensor-core dK/dV kernel with 128-row query steps);
+// kPlanKeyMajorWide: the same over key tiles of 256 rows (the key-weight kernel).
+enum PlanKind : int64_t {
+  kPlanQueryMajor = 0,
+  kPlanKeyMajor = 1,
+  kPlanQueryMajorPacked = 2,
+  kPlanKeyMajorPacked = 3,
+  kPlanKeyMajorWide = 4
+};
 // last: the observation window of a key-major plan (build_bwd_plan).
 std::shared_ptr<const Plan> get_plan(const cp_desc_t* d, const ShardMap& m, PlanKind kind, int q_rank = -1,
                                      int kv_rank = -1, int ring_step = -1, int64_t slot_rows = 0, int64_t last = 0) {
@@ -480,8 +489,9 @@ std::shared_ptr<const Plan> get_plan(const cp_desc_t* d, const ShardMap& m, Plan
         return it->second;
       }
   }
-  const bool key_major = kind == kPlanKeyMajor || kind == kPlanKeyMajorPacked;
-  auto plan = std::make_shared<Plan>(key_major ? build_bwd_plan(d, m, kind == kPlanKeyMajorPacked, last)
+  const bool key_major = kind == kPlanKeyMajor || kind == kPlanKeyMajorPacked || kind == kPlanKeyMajorWide;
+  auto plan = std::make_shared<Plan>(key_major ? build_bwd_plan(d, m, kind != kPlanKeyMajor, last,
+                                                                kind == kPlanKeyMajorWide ? 2 * kTile : kTile)
                                                : build_fwd_plan(d, m, q_rank, kv_rank, ring_step, slot_rows,
                                                                 kind == kPlanQueryMajorPacked));
   order_by_work(*plan);
@@ -641,12 +651,12 @@ std::atomic<int32_t> g_debug_checks{0};
 // range_rows for the runs); an inconsistent plan is refused before any GPU
 // work of the call.
 cp_status_t stage_plan(const Plan& p, char* base, cudaStream_t st, AttnArgs& a, int64_t tile_rows,
-                       int64_t range_rows, bool pinned = true) {
+                       int64_t range_rows, bool pinned = true, int32_t most_rows = kTile) {
   if (a.debug) {
     for (int32_t i = 0; i < int32_t(p.tiles.size()); ++i)
       if (plan_entry_check(p.tiles.data(), int32_t(p.tiles.size()), p.ranges.data(), int32_t(p.ranges.size()),
                            p.packs.data(), int32_t(p.packs.size()), p.pieces.data(), int32_t(p.pieces.size()), i,
-                           0, 1, 0, 1, tile_rows, range_rows, a.block_mode, a.lse_stride) != 0)
+                           0, 1, 0, 1, tile_rows, range_rows, a.block_mode, a.lse_stride, most_rows) != 0)
         return CP_ERR_INVALID_ARG;
   }
   if (upload_plan(p, base, st, a, pinned) != cudaSuccess) return CP_ERR_CUDA;
@@ -679,7 +689,7 @@ PlanKind dkdv_plan_kind(const cp_desc_t* d) {
 }
 
 // The key-weight kernel's: 128-row query steps for both of its head dims.
-PlanKind key_weights_plan_kind(const cp_desc_t* d) { return use_tc_key_weights(d) ? kPlanKeyMajorPacked : kPlanKeyMajor; }
+PlanKind key_weights_plan_kind(const cp_desc_t* d) { return use_tc_key_weights(d) ? kPlanKeyMajorWide : kPlanKeyMajor; }
 
 // Few counted queries a sequence: the last `last` of each, at most this many
 // columns (queries times the heads that share a key).
@@ -1645,7 +1655,7 @@ cp_status_t cp_attn_key_weights(const cp_desc_t* d, int64_t last, const void* q,
   const auto pp = get_plan(d, m, key_weights_plan_kind(d), -1, -1, -1, 0, last);
   const Plan& p = *pp;
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < plan_bytes(p)) return CP_ERR_WORKSPACE;
-  st = stage_plan(p, static_cast<char*>(ws), cs, a, d->total_tokens, d->total_tokens);
+  st = stage_plan(p, static_cast<char*>(ws), cs, a, d->total_tokens, d->total_tokens, true, 2 * kTile);
   if (st != CP_OK) return st;
   const cudaError_t e = use_tc_key_weights(d) ? launch_tc_key_weights(a, cs) : launch_simt_key_weights(a, d->dtype, cs);
   return e == cudaSuccess ? CP_OK : CP_ERR_CUDA;

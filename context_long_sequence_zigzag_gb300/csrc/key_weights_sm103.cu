@@ -11,14 +11,18 @@
 // (TMEM lane = key), so its column sum is a sum over its own registers: no
 // exchange between threads, nothing written but one float a key.
 //
-// Per 128 x 128 step the tensor cores need 512 cycles (128-wide heads), and
-// as much at 32 exponentials a cycle.  K lives in TMEM (a TS MMA): as an SS MMA
-// both operands and the Q copies together asked shared memory for 96 KB a
+// A CTA's key tile has 256 rows, two M = 128 halves, so that a Q tile brought
+// in from L2 serves two MMAs.  With 128 rows the copies (32 KB a step of 512
+// tensor cycles) ran at some 36 bytes a cycle and SM, and the kernel with them.
+// Per 128 x 128 half step the tensor cores need 512 cycles (128-wide heads),
+// and as much at 32 exponentials a cycle.  K lives in TMEM (a TS MMA): as an SS
+// MMA both operands and the Q copies together asked shared memory for 96 KB a
 // step, 768 cycles (16K tokens, 32 heads: 1.64 ms, against 0.98 ms).  S^T has
-// three TMEM buffers; three groups of four warps take the steps in turn, so
-// that one group's loads and waits overlap the others' exponentials (two
-// groups: 1.10 ms; a part of the exponentials as polynomials on the FMA pipes
-// instead: 1.09 ms and up, the issue slots are needed elsewhere).
+// three TMEM buffers (two with 192-wide heads), each read by a group of four
+// warps that takes its tiles in turn, so that one group's loads and waits overlap the others'
+// exponentials (two groups: 1.10 ms; a part of the exponentials as polynomials
+// on the FMA pipes instead: 1.09 ms and up, the issue slots are needed
+// elsewhere).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -37,15 +41,12 @@ bool make_map_3d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int
 
 namespace {
 
-constexpr int BT = 128;                 // keys of a tile, queries of a step
+constexpr int BT = 128;                 // keys of a half tile, queries of a step
 constexpr uint32_t kPanel = 128 * 128;  // 128 rows x 64 bf16 columns, 128-byte swizzled: 16 KiB
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr int kGroupThreads = 128;
-constexpr int kGroups = 3;      // group g takes steps g, g + kGroups, ...
-constexpr int kThreads = kGroups * kGroupThreads + 64;
-constexpr int kProducer = 4 * kGroups, kIssuer = kProducer + 1;  // warps
-constexpr int kBufs = 3;        // S^T buffers of 128 TMEM columns; K behind them
+constexpr unsigned kPhases = 8;
 constexpr int kPieceMaps = 15;  // boxes of 8, 16, ..., 120 rows for the pieces of gathered tiles
 
 enum WaitSite : int { kSiteK = 0x61, kSiteQEmpty, kSiteQFull, kSiteSFull, kSiteSFree, kSiteDrain, kSiteAlign };
@@ -60,7 +61,13 @@ struct Params {
 template <int DQK>
 struct Cfg {
   static constexpr int kPanels = DQK / 64;
-  static constexpr int NS = DQK == 128 ? 6 : 4;  // stages of Q
+  static constexpr int NS = DQK == 128 ? 6 : 4;     // stages of Q
+  static constexpr int kBufs = DQK == 128 ? 3 : 2;  // S^T buffers of 128 TMEM columns; K's halves behind them
+  // Compute groups: one a buffer, so that a group waits only for the phase after the one it freed (a barrier's parity
+  // tells a phase from the next one only).
+  static constexpr int kGroups = kBufs;
+  static constexpr int kThreads = kGroups * kGroupThreads + 64;
+  static constexpr int kProducer = 4 * kGroups, kIssuer = kProducer + 1;  // warps
   static constexpr uint32_t kTileBytes = kPanels * kPanel;
   static constexpr uint32_t offQ = 0;
   static constexpr uint32_t offStat = offQ + NS * kTileBytes;  // [group][2][BT] floats
@@ -69,7 +76,7 @@ struct Cfg {
   static constexpr uint32_t kSmem = offBar + kNumBars * 8 + 16;
   static_assert(kSmem <= 232448, "shared memory budget");
   static constexpr uint32_t tK = kBufs * BT;  // TMEM column of K (packed bf16 pairs)
-  static_assert(tK + DQK / 2 <= 512, "TMEM budget");
+  static_assert(tK + DQK <= 512, "TMEM budget");
 };
 
 // -lse * log2e of query column `col` of the step the cursor points at, -inf
@@ -96,9 +103,9 @@ __device__ __forceinline__ uint64_t exp2_pair(uint64_t y) {
 }
 
 template <int DQK, bool PACKED>
-__global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Cfg<DQK>::kThreads, 1) key_weights_kernel(const __grid_constant__ Params p) {
   using C = Cfg<DQK>;
-  constexpr int NS = C::NS;
+  constexpr int NS = C::NS, kBufs = C::kBufs, kGroups = C::kGroups, kProducer = C::kProducer, kIssuer = C::kIssuer;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = ptx::smem_u32(smem);
   const AttnArgs& a = p.a;
@@ -106,14 +113,17 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
     if (threadIdx.x == 0 && p.err) atomicCAS(p.err, 0, 0x100 | kSiteAlign);
     return;
   }
-  // kv heads outermost, then the tiles (heaviest first): the CTAs resident at
-  // one time read one head's Q
-  const int kvh = int(blockIdx.x / unsigned(a.num_tiles));
-  const int tile_idx = int(blockIdx.x - unsigned(kvh) * unsigned(a.num_tiles));
-  if (a.debug && !debug_plan_ok(a, tile_idx, kvh, kvh, true, p.err)) return;
+  // The tiles (heaviest first) in kPhases parts, inside a part kv heads
+  // outermost: the CTAs resident at one time read one head's Q, and the last
+  // ones to run are light.
+  const unsigned part_tiles = unsigned(a.num_tiles + kPhases - 1) / kPhases, per_part = part_tiles * unsigned(a.hkv);
+  const unsigned phase = blockIdx.x / per_part, rest = blockIdx.x - phase * per_part;
+  const unsigned here = min(part_tiles, unsigned(a.num_tiles) - phase * part_tiles);  // (the last part may be smaller)
+  const int kvh = int(rest / here), tile_idx = int(phase * part_tiles + rest - unsigned(kvh) * here);
+  if (a.debug && !debug_plan_ok(a, tile_idx, kvh, kvh, true, p.err, 2 * BT)) return;
   const TileDesc tile = a.tiles[tile_idx];
   const int G = a.hq / a.hkv;
-  const int n_steps = tile.work * G;
+  const int n_steps = tile.work * G, halves = tile.nrows > BT ? 2 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   const uint32_t bar_k = sbase + C::offBar;
@@ -125,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::offBar + C::kNumBars * 8 + 4);
 
   if (threadIdx.x == 0) {
-    ptx::mbar_init(bar_k, 4);
+    ptx::mbar_init(bar_k, 4 * halves);
     for (int s = 0; s < NS; ++s) {
       ptx::mbar_init(bar_q_full(s), 2);
       ptx::mbar_init(bar_q_empty(s), 1);
@@ -191,26 +201,28 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
     if (n_steps > 0) {
       constexpr uint32_t idS = ptx::idesc_bf16_f32(BT, BT, false, false);
       bool ok = ptx::mbar_wait_w(bar_k, 0, kSiteK, wctx);
-      int i = 0;
-      for (; ok && i < n_steps; ++i) {
-        const int st = i % NS, b = i % kBufs;
-        ok = ptx::mbar_wait_w(bar_q_full(st), (i / NS) & 1, kSiteQFull, wctx) &&
-             (i < kBufs || ptx::mbar_wait_w(bar_s_free(b), ((i / kBufs) - 1) & 1, kSiteSFree, wctx));
-        if (!ok) break;
-        ptx::tc_fence_after();
-        const uint64_t dq = ptx::sdesc_sw128(sbase + C::offQ + st * C::kTileBytes, 16, 1024);
+      int j = 0;  // S^T tiles issued
+      for (int i = 0; ok && i < n_steps; ++i) {
+        const int st = i % NS;
+        ok = ptx::mbar_wait_w(bar_q_full(st), (i / NS) & 1, kSiteQFull, wctx);
+        for (int half = 0; ok && half < halves; ++half, ++j) {
+          const int b = j % kBufs;
+          ok = j < kBufs || ptx::mbar_wait_w(bar_s_free(b), ((j / kBufs) - 1) & 1, kSiteSFree, wctx);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint64_t dq = ptx::sdesc_sw128(sbase + C::offQ + st * C::kTileBytes, 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < DQK / 16; ++kk) {
-          const uint32_t o = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
-          ptx::mma_ts_w(tmem + b * BT, tmem + C::tK + kk * 8, dq + o, idS, kk > 0);
+          for (int kk = 0; kk < DQK / 16; ++kk)
+            ptx::mma_ts_w(tmem + b * BT, tmem + C::tK + half * (DQK / 2) + kk * 8,
+                          dq + (((kk >> 2) * kPanel + (kk & 3) * 32) >> 4), idS, kk > 0);
+          ptx::mma_commit_w(bar_s_full(b));
         }
-        ptx::mma_commit_w(bar_s_full(b));
-        ptx::mma_commit_w(bar_q_empty(st));
+        if (ok) ptx::mma_commit_w(bar_q_empty(st));
       }
-      if (!ok && i > 0) {  // the MMAs issued so far end before the CTA frees its TMEM
+      if (!ok && j > 0) {  // the MMAs issued so far end before the CTA frees its TMEM
         volatile int no_abort = 0;
         const ptx::WaitCtx drain{&no_abort, nullptr, kWaitLimitNs};
-        ptx::mbar_wait_w(bar_s_full((i - 1) % kBufs), ((i - 1) / kBufs) & 1, kSiteDrain, drain);
+        ptx::mbar_wait_w(bar_s_full((j - 1) % kBufs), ((j - 1) / kBufs) & 1, kSiteDrain, drain);
       }
     }
   } else {
@@ -221,11 +233,10 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
     float* stat = reinterpret_cast<float*>(smem + C::offStat) + grp * 2 * BT;
     const float sl2 = a.scale * kLog2e;
     const uint64_t sl2x2 = ptx::f32x2(sl2, sl2);
-    const int kpos = tile.pos0 + t, nk = tile.nrows;
-    if (grp == 0 && n_steps > 0) {
+    if (grp < halves && n_steps > 0) {
       // K row -> TMEM (bf16 pairs are the A-operand packing).  Rows past the
       // tile are the following ones, or zeros past the end: not written out.
-      const int64_t krow = int64_t(tile.row0) + t;
+      const int64_t krow = int64_t(tile.row0) + grp * BT + t;
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k) + (krow * a.hkv + kvh) * DQK);
 #pragma unroll
       for (int c = 0; c < DQK / 64; ++c) {
@@ -235,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
           const uint4 v = krow < a.T ? __ldg(src + 8 * c + i) : make_uint4(0, 0, 0, 0);
           kr[4 * i] = v.x, kr[4 * i + 1] = v.y, kr[4 * i + 2] = v.z, kr[4 * i + 3] = v.w;
         }
-        ptx::tmem_st32(tS + C::tK + 32 * c, kr);
+        ptx::tmem_st32(tS + C::tK + grp * (DQK / 2) + 32 * c, kr);
       }
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
@@ -244,26 +255,38 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
     }
     StepCursor<BT> cur;
     cur.init(a.ranges, tile.range_begin, tile.range_count, G, kvh, a.hkv, a.gqa_interleaved);
-    for (int i = 0; i < grp && i < n_steps; ++i) cur.next();
-    float next = grp < n_steps ? load_stat<PACKED>(a, cur, t) : 0.f;
-    float w = 0.f;
+    // group g takes S^T tiles g, g + kGroups, ...: half j % halves of step j / halves
+    const int n_tiles = n_steps * halves;
+    int step = 0;
+    auto go_to = [&](int j) {
+      for (const int to = j / halves; step < to; ++step) cur.next();
+    };
+    float next = 0.f;
+    if (grp < n_tiles) {
+      go_to(grp);
+      next = load_stat<PACKED>(a, cur, t);
+    }
+    float w[2] = {0.f, 0.f};
     bool ok = true;
-    for (int i = grp, k = 0; i < n_steps; i += kGroups, ++k) {
-      const int nq = cur.n(), qpos0 = cur.pos(), b = i % kBufs;
+    for (int j = grp, k = 0; j < n_tiles; j += kGroups, ++k) {
+      const int nq = cur.n(), qpos0 = cur.pos(), b = j % kBufs, half = j % halves;
       const bool packed = PACKED && cur.packed();
       float* st = stat + (k & 1) * BT;
-      // (the buffer was last read two of this group's steps ago, before the barrier of the step between)
+      // (the buffer was last read two of this group's tiles ago, before the barrier of the tile between)
       st[t] = next;
       ptx::named_barrier(1 + grp, kGroupThreads);
-      for (int x = 0; x < kGroups && i + x + 1 < n_steps; ++x) cur.next();
-      if (i + kGroups < n_steps) next = load_stat<PACKED>(a, cur, t);
-      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_poll(bar_s_full(b), (i / kBufs) & 1, kSiteSFull, wctx));
+      if (j + kGroups < n_tiles) {
+        go_to(j + kGroups);
+        next = load_stat<PACKED>(a, cur, t);
+      }
+      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_poll(bar_s_full(b), (j / kBufs) & 1, kSiteSFull, wctx));
       if (!ok) continue;  // keep to the group's barriers
       ptx::tc_fence_after();
       const bool causal = a.causal && !packed;
+      const int first = tile.pos0 + half * BT;
       // columns from cmin on are visible; columns without a query have the statistic -inf
-      const bool need_mask = packed || nq < BT || (causal && qpos0 < tile.pos0 + BT - 1);
-      const int cmin = causal ? kpos - qpos0 : 0;
+      const bool need_mask = packed || nq < BT || (causal && qpos0 < first + BT - 1);
+      const int cmin = causal ? first + t - qpos0 : 0;
       uint64_t s0 = 0, s1 = 0;  // a step's own sums: a long sum's roundings stay small
       auto sums = [&](auto mask_) {
         constexpr bool MASK = decltype(mask_)::value;
@@ -312,16 +335,20 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
       else sums(std::false_type{});
       float a0, a1;
       ptx::f32x2_split(ptx::add_f32x2(s0, s1), a0, a1);
-      w += a0 + a1;
+      if (half) w[1] += a0 + a1;
+      else w[0] += a0 + a1;
     }
-    // the other groups' sums through shared memory, in their statistics' places once all of a group's threads have read them
+    // the groups' sums through shared memory, in their statistics' places once all of a group's threads have read them
     ptx::named_barrier(1 + grp, kGroupThreads);
-    if (grp > 0) stat[t] = w;
+    stat[t] = w[0];
+    stat[BT + t] = w[1];
     ptx::named_barrier(1 + kGroups, kGroups * kGroupThreads);
-    if (grp == 0 && t < nk) {
+    if (grp < halves && grp * BT + t < tile.nrows) {
+      const float* all = reinterpret_cast<const float*>(smem + C::offStat) + grp * BT + t;
+      float sum = all[0];
 #pragma unroll
-      for (int g = 1; g < kGroups; ++g) w += stat[g * 2 * BT + t];
-      static_cast<float*>(a.out)[int64_t(kvh) * a.T + tile.row0 + t] = w;
+      for (int g = 1; g < kGroups; ++g) sum += all[g * 2 * BT];
+      static_cast<float*>(a.out)[int64_t(kvh) * a.T + tile.row0 + grp * BT + t] = sum;
     }
   }
 
@@ -352,7 +379,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t grid = int64_t(a.num_tiles) * a.hkv;
   if (grid == 0) return cudaSuccess;
-  kernel<<<unsigned(grid), kThreads, C::kSmem, st>>>(p);
+  kernel<<<unsigned(grid), C::kThreads, C::kSmem, st>>>(p);
   return cudaGetLastError();
 }
 

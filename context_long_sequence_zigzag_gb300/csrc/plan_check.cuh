@@ -57,16 +57,18 @@ __host__ __device__ inline bool pack_entry_ok(const PackMask* packs, int32_t num
 //   tile_rows  : rows of the tensors the tile indexes (q for query-major
 //                plans, k / v for key-major ones)
 //   range_rows : rows of the tensors the runs index
+//   most_rows  : rows a tile may have
 //   packs, pieces : the gathered key tiles (null / 0 for plans without them)
 __host__ __device__ inline int plan_entry_check(const TileDesc* tiles, int32_t num_tiles, const RangeDesc* ranges,
                                                 int32_t num_ranges, const PackMask* packs, int32_t num_packs,
                                                 const PackPiece* pieces, int32_t num_pieces, int tile_idx, int head,
                                                 int heads, int kv_head, int kv_heads, int64_t tile_rows,
-                                                int64_t range_rows, int32_t block_mode, int64_t out_rows) {
+                                                int64_t range_rows, int32_t block_mode, int64_t out_rows,
+                                                int32_t most_rows = kTile) {
   if (tile_idx < 0 || tile_idx >= num_tiles) return kPlanTileIndex;
   if (head < 0 || head >= heads || kv_head < 0 || kv_head >= kv_heads) return kPlanHead;
   const TileDesc t = tiles[tile_idx];
-  if (t.nrows < 1 || t.nrows > kTile || t.row0 < 0 || int64_t(t.row0) + t.nrows > tile_rows) return kPlanTileRows;
+  if (t.nrows < 1 || t.nrows > most_rows || t.row0 < 0 || int64_t(t.row0) + t.nrows > tile_rows) return kPlanTileRows;
   if (block_mode && (t.out_row0 < 0 || int64_t(t.out_row0) + t.nrows > out_rows)) return kPlanOutRows;
   if (t.range_begin < 0 || t.range_count < 0 || int64_t(t.range_begin) + t.range_count > num_ranges)
     return kPlanRangeList;
@@ -91,13 +93,13 @@ __host__ __device__ inline int plan_entry_check(const TileDesc* tiles, int32_t n
 // false (after recording the error) when the CTA must not run.  Must be
 // called by all threads of the CTA, before any barrier initialisation.
 __device__ inline bool debug_plan_ok(const AttnArgs& a, int tile_idx, int head, int kv_head, bool key_major,
-                                     int32_t* err) {
+                                     int32_t* err, int32_t most_rows = kTile) {
   int bad = 0;
   if (threadIdx.x == 0) {
     const int64_t tq = a.T, tkv = a.T_kv ? a.T_kv : a.T;
     bad = plan_entry_check(a.tiles, a.num_tiles, a.ranges, a.num_ranges, a.packs, a.num_packs, a.pieces,
                            a.num_pieces, tile_idx, head, key_major ? a.hkv : a.hq,
-                           kv_head, a.hkv, key_major ? tkv : tq, key_major ? tq : tkv, a.block_mode, a.lse_stride);
+                           kv_head, a.hkv, key_major ? tkv : tq, key_major ? tq : tkv, a.block_mode, a.lse_stride, most_rows);
     if (bad && err) atomicCAS(err, 0, kErrPlanBase | bad);
   }
   return __syncthreads_or(bad) == 0;
