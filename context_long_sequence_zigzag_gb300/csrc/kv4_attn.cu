@@ -329,6 +329,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
   if (w0 < w1) {
     cur.seek(base, a.c.num_seqs, per, row_tiles, w0);
     ahead = cur;
+    {  // the first run's queries on their way too
+      int t, head;
+      const int n = (cur.run - cur.h * row_tiles) * gr.rows_per_tile + r % gr.rows_per_tile;
+      const E* q = static_cast<const E*>(a.q) + row_index(a, cur.b, cur.h, min(n, a.rows - 1), &t, &head) * DQK;
+      for (int o = c * 32; o < DQK * int(sizeof(E)); o += 128)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<const char*>(q) + o));
+    }
     look_up();
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) load_next();
@@ -831,165 +838,172 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
     }
   }
   __syncthreads();
-  for (int g = 0; g < s_groups; ++g) {
+  // four channels of a row of a run a thread
+  const int items = gr.rows_per_tile * (DV / 4);
+  for (int e = tid; e < s_groups * items; e += C::THREADS) {
+    const int g = e / items, n = (e - g * items) / (DV / 4), d = (e - g * items) % (DV / 4) * 4;
     const int i0 = s_group[g], i1 = s_group[g + 1], rid = s_run[s_slot[i0]];
     const int b = rid / per, run = rid - b * per;
     const int per_run = (base[b + 1] - base[b]) / per, run0 = base[b] + run * per_run;
     const int h = run / row_tiles, n0 = (run - h * row_tiles) * gr.rows_per_tile;
-    const int rows = min(gr.rows_per_tile, a.rows - n0);
-    const bool whole = run0 + 1 >= u0 && run0 + per_run <= u1;
-    float* part = gr.part + (int64_t(blockIdx.x) * 2 + (run0 + 1 >= u0)) * part_floats(C::COLS, DV);
-    for (int e = tid; e < rows * DV; e += C::THREADS) {
-      const int n = e / DV, d = e - n * DV;
-      float l = 0.f, x = 0.f;
+    if (n0 + n >= a.rows) continue;
+    float l = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (int i = i0; i < i1; ++i) {
-        const int s = s_slot[i];
-        const float* st = stat_s + s * 2 * C::COLS + n;
-        l += st[C::COLS];
-        x = fmaf(st[0], ((s & 1) ? last_s : stash_s)[(s >> 1) * gr.rows_per_tile * DV + e], x);
-      }
-      const float m = top_s[s_slot[i0] * C::COLS + n];
-      if (whole) {
-        int t, head;
-        const int64_t row = row_index(a, b, h, n0 + n, &t, &head);
-        store_o(a, row * DV + d, l == 0.f ? 0.f : x / l);
-        if (d == 0)
-          a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] =
-              l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-      } else {
-        part[2 * C::COLS + e] = x;
-        if (d == 0) {
-          part[n] = m;
-          part[C::COLS + n] = l;
-        }
+    for (int i = i0; i < i1; ++i) {
+      const int s = s_slot[i];
+      const float* st = stat_s + s * 2 * C::COLS + n;
+      const float4 y = *reinterpret_cast<const float4*>(((s & 1) ? last_s : stash_s) +
+                                                        ((s >> 1) * gr.rows_per_tile + n) * DV + d);
+      const float k = st[0];
+      l += st[C::COLS];
+      x = make_float4(fmaf(k, y.x, x.x), fmaf(k, y.y, x.y), fmaf(k, y.z, x.z), fmaf(k, y.w, x.w));
+    }
+    const float m = top_s[s_slot[i0] * C::COLS + n];
+    if (run0 + 1 >= u0 && run0 + per_run <= u1) {  // whole
+      int t, head;
+      const int64_t row = row_index(a, b, h, n0 + n, &t, &head);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      store_o4(a, row * DV + d, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+      if (d == 0)
+        a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] =
+            l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    } else {
+      float* part = gr.part + (int64_t(blockIdx.x) * 2 + (run0 + 1 >= u0)) * part_floats(C::COLS, DV);
+      *reinterpret_cast<float4*>(part + 2 * C::COLS + n * DV + d) = x;
+      if (d == 0) {
+        part[n] = m;
+        part[C::COLS + n] = l;
       }
     }
   }
 }
 
 // Joins the runs that were cut (a CTA a row; whole ones are done, empty ones
-// get o = 0, lse = -inf), and adds up the weights: the other CTAs' warps take
-// sub-blocks, a lane a token.
+// get o = 0, lse = -inf).
 constexpr int kJoinThreads = 256;
 
 template <int COLS, int DV>
-__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnArgs a, const Grid gr, int runs) {
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnArgs a, const Grid gr) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int32_t s_scan[kJoinThreads / 32];
   int32_t* base = reinterpret_cast<int32_t*>(smem);
   const int row_tiles = a.row_tiles, per = a.c.hkv * row_tiles;
   scan_lengths<kJoinThreads>(a, per, base, s_scan);
   const int units = base[a.c.num_seqs], shares = share_count(units, gr.ctas, gr.warps);
+  ptx::grid_launch_dependents();
   ptx::grid_wait_previous();
   constexpr int kPart = part_floats(COLS, DV);
   // partial i of a run cut over shares c0, c0 + 1, ...: slot 1 of the share it starts in, slot 0 of the others
   auto part_of = [&](int c0, int i) { return gr.part + (int64_t(c0 + i) * 2 + (i == 0)) * kPart; };
-  const int joins = runs * gr.rows_per_tile;
-  if (int(blockIdx.x) < joins) {
-    const int id = int(blockIdx.x) / gr.rows_per_tile, n = int(blockIdx.x) - id * gr.rows_per_tile;
-    const int b = id / per, run = id - b * per;
-    const int per_run = (base[b + 1] - base[b]) / per, run0 = base[b] + run * per_run;
-    const int h = run / row_tiles, n0 = (run - h * row_tiles) * gr.rows_per_tile;
-    if (n0 + n >= a.rows) return;
-    int c0 = 0, parts = 0;
-    if (per_run > 0) {
-      c0 = share_of(units, shares, run0 + 1);
-      parts = share_of(units, shares, run0 + per_run - 1) - c0 + 1;
-      if (parts == 1) return;
-    }
-    float* k_s = reinterpret_cast<float*>(smem + gr.off_join);  // [parts]: references, then weights
-    float* l_s = k_s + gr.ctas;                                 // [parts]: sums
-    for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
-      const float* p = part_of(c0, i) + n;
-      k_s[i] = p[0];
-      l_s[i] = p[COLS];
-    }
-    __syncthreads();
-    float m = kNoRef;
-    for (int i = threadIdx.x & 31; i < parts; i += 32) m = fmaxf(m, k_s[i]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    __syncthreads();
-    for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
-      const float k = l_s[i] == 0.f ? 0.f : ptx::ex2(k_s[i] - m);  // 0: saw nothing
-      k_s[i] = k;
-      l_s[i] = l_s[i] == 0.f ? 0.f : k * l_s[i];
-    }
-    __syncthreads();
-    constexpr int kSplit = kJoinThreads / DV;
-    float* x_s = l_s + gr.ctas;  // [kSplit][DV]
-    const int d = threadIdx.x % DV, first = threadIdx.x / DV;
-    float l = 0.f, x = 0.f;
-#pragma unroll 8
-    for (int i = first; i < parts; i += kSplit) x += k_s[i] * part_of(c0, i)[2 * COLS + n * DV + d];
-    x_s[first * DV + d] = x;
-    for (int i = 0; i < parts; ++i) l += l_s[i];
-    __syncthreads();
-    if (first > 0) return;
-#pragma unroll
-    for (int i = 1; i < kSplit; ++i) x += x_s[i * DV + d];
-    int t, head;
-    const int64_t row = row_index(a, b, h, n0 + n, &t, &head);
-    store_o(a, row * DV + d, l == 0.f ? 0.f : x / l);
-    if (d == 0)
-      a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] =
-          l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    return;
+  const int id = int(blockIdx.x) / gr.rows_per_tile, n = int(blockIdx.x) - id * gr.rows_per_tile;
+  const int b = id / per, run = id - b * per;
+  const int per_run = (base[b + 1] - base[b]) / per, run0 = base[b] + run * per_run;
+  const int h = run / row_tiles, n0 = (run - h * row_tiles) * gr.rows_per_tile;
+  if (n0 + n >= a.rows) return;
+  int c0 = 0, parts = 0;
+  if (per_run > 0) {
+    c0 = share_of(units, shares, run0 + 1);
+    parts = share_of(units, shares, run0 + per_run - 1) - c0 + 1;
+    if (parts == 1) return;
   }
-  // ---- weights
+  float* k_s = reinterpret_cast<float*>(smem + gr.off_join);  // [parts]: references, then weights
+  float* l_s = k_s + gr.ctas;                                 // [parts]: sums
+  for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
+    const float* p = part_of(c0, i) + n;
+    k_s[i] = p[0];
+    l_s[i] = p[COLS];
+  }
+  __syncthreads();
+  float m = kNoRef;
+  for (int i = threadIdx.x & 31; i < parts; i += 32) m = fmaxf(m, k_s[i]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  __syncthreads();
+  for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
+    const float k = l_s[i] == 0.f ? 0.f : ptx::ex2(k_s[i] - m);  // 0: saw nothing
+    k_s[i] = k;
+    l_s[i] = l_s[i] == 0.f ? 0.f : k * l_s[i];
+  }
+  __syncthreads();
+  constexpr int kSplit = kJoinThreads / DV;
+  float* x_s = l_s + gr.ctas;  // [kSplit][DV]
+  const int d = threadIdx.x % DV, first = threadIdx.x / DV;
+  float l = 0.f, x = 0.f;
+#pragma unroll 8
+  for (int i = first; i < parts; i += kSplit) x += k_s[i] * part_of(c0, i)[2 * COLS + n * DV + d];
+  x_s[first * DV + d] = x;
+  for (int i = 0; i < parts; ++i) l += l_s[i];
+  __syncthreads();
+  if (first > 0) return;
+#pragma unroll
+  for (int i = 1; i < kSplit; ++i) x += x_s[i * DV + d];
+  int t, head;
+  const int64_t row = row_index(a, b, h, n0 + n, &t, &head);
+  store_o(a, row * DV + d, l == 0.f ? 0.f : x / l);
+  if (d == 0)
+    a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] =
+        l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// Adds up the weights: a warp takes consecutive sub-blocks, of a kv head at a
+// time, a lane a token.  The scores come from L2, the lse from the kernels
+// before; every slot gets one sum a row tile, in order.
+__global__ void __launch_bounds__(kJoinThreads) kv4_weights_kernel(const Kv4AttnArgs a, const Grid gr) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int32_t s_scan[kJoinThreads / 32];
+  int32_t* base = reinterpret_cast<int32_t*>(smem);
+  const int row_tiles = a.row_tiles, per = a.c.hkv * row_tiles;
+  scan_lengths<kJoinThreads>(a, per, base, s_scan);
+  const int units = base[a.c.num_seqs];
+  ptx::grid_wait_previous();
   const int lane = threadIdx.x & 31;
-  const int warps = (int(gridDim.x) - joins) * (kJoinThreads / 32);
-  const int w = (int(blockIdx.x) - joins) * (kJoinThreads / 32) + int(threadIdx.x >> 5);
+  const int warps = int(gridDim.x) * (kJoinThreads / 32);
+  const int w = int(blockIdx.x) * (kJoinThreads / 32) + int(threadIdx.x >> 5);
   const int64_t all = units / row_tiles;  // units of the cache: row tile by row tile the same
   const int64_t v0 = all * w / warps, v1 = all * (w + 1) / warps;
-  int b = 0, last_h = -1, last_b = -1;
-  float lse2[8];  // row lane of row tile i (at most 8 tiles are kept)
-  for (int64_t v = v0; v < v1; ++v) {
+  int b = 0;
+  for (int64_t v = v0; v < v1;) {
     b = seq_of_unit(base, a.c.num_seqs, b, int(v * row_tiles));
     const int per_run = (base[b + 1] - base[b]) / per;
-    const int at = int(v) - base[b] / row_tiles, h = at / per_run, i = at - h * per_run - 1;
-    if (i < 0) continue;  // a run's start
-    float add = 0.f;
+    const int at = int(v) - base[b] / row_tiles, h = at / per_run, first = at - h * per_run;
+    const int i0 = max(first - 1, 0), i1 = int(min(int64_t(per_run), first + v1 - v)) - 1;  // sub-blocks
+    v += per_run - first;
+    const int len = kv4_length(a.c, a.lengths, b);
     for (int rt = 0; rt < row_tiles; ++rt) {
       const int run0 = base[b] + (h * row_tiles + rt) * per_run, n0 = rt * gr.rows_per_tile;
       const int rows = min(gr.rows_per_tile, a.rows - n0);
-      float ls;
-      if (b == last_b && h == last_h && rt < 8) {
-        ls = lse2[0];
+      float ls = INFINITY;  // lane n: the lse of row n (log2)
+      if (lane < rows) {
+        int t, head;
+        row_index(a, b, h, n0 + lane, &t, &head);
+        ls = a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] * kLog2e;
+      }
+      if (ls == -INFINITY) ls = INFINITY;  // a row that sees nothing gives nothing
+      for (int i = i0; i < i1; i += 4) {
+        float add[4] = {0.f, 0.f, 0.f, 0.f};
+        int page[4];
 #pragma unroll
-        for (int k = 1; k < 8; ++k) ls = rt == k ? lse2[k] : ls;
-      } else {
-        ls = INFINITY;
-        if (lane < rows) {
-          const int c0 = share_of(units, shares, run0 + 1), c1 = share_of(units, shares, run0 + per_run - 1);
-          if (c0 == c1) {
-            int t, head;
-            row_index(a, b, h, n0 + lane, &t, &head);
-            ls = a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] * kLog2e;
-          } else {
-            float m = kNoRef, l = 0.f;
-            for (int k = 0; k <= c1 - c0; ++k) m = fmaxf(m, part_of(c0, k)[lane]);
-            for (int k = 0; k <= c1 - c0; ++k) {
-              const float* p = part_of(c0, k);
-              l += ptx::ex2(p[lane] - m) * p[COLS + lane];
-            }
-            ls = l == 0.f ? -INFINITY : m + log2f(l);
-          }
-          if (ls == -INFINITY) ls = INFINITY;  // a row that sees nothing gives nothing
+        for (int k = 0; k < 4; ++k)
+          page[k] = __ldg(a.c.table + int64_t(b) * a.c.max_pages + min(i + k, i1 - 1) / (CP_KV4_PAGE / kKv4Sub));
+        const float* sc = gr.score + int64_t(run0 + 1 + i) * gr.rows_per_tile * kKv4Sub + lane;
+#pragma unroll 2
+        for (int n = 0; n < rows; ++n) {
+          const float lsn = __shfl_sync(0xffffffffu, ls, n);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (i + k < i1) add[k] += ptx::ex2(sc[(k * gr.rows_per_tile + n) * kKv4Sub] - lsn);
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) lse2[k] = rt == k ? ls : lse2[k];
+        for (int k = 0; k < 4; ++k) {
+          const int slot = (i + k) * kKv4Sub + lane;
+          if (i + k >= i1 || slot >= len) continue;
+          const int pg = page[k];
+          if (pg < 0 || pg >= a.c.num_pages) continue;  // (recorded by the first kernel)
+          atomicAdd(a.c.weights + (int64_t(pg) * a.c.hkv + h) * CP_KV4_PAGE + slot % CP_KV4_PAGE, add[k]);
+        }
       }
-      const float* sc = gr.score + int64_t(run0 + 1 + i) * gr.rows_per_tile * kKv4Sub + lane;
-      for (int n = 0; n < rows; ++n) add += ptx::ex2(sc[n * kKv4Sub] - __shfl_sync(0xffffffffu, ls, n));
     }
-    last_b = b;
-    last_h = h;
-    const int page = kv4_page(a.c, b, i / (CP_KV4_PAGE / kKv4Sub));
-    const int slot = i * kKv4Sub + lane;
-    if (page >= 0 && slot < kv4_length(a.c, a.lengths, b))
-      atomicAdd(a.c.weights + (int64_t(page) * a.c.hkv + h) * CP_KV4_PAGE + slot % CP_KV4_PAGE, add);
   }
 }
 
@@ -1033,19 +1047,25 @@ cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
   const int runs = a.c.num_seqs * a.c.hkv * a.row_tiles;
   gr.off_join = up(4 * (a.c.num_seqs + 1), 16);
   const uint32_t join_smem = gr.off_join + (2 * gr.ctas + kJoinThreads) * 4;
-  // the second kernel's launch overlaps the first: it waits on the device
+  // the launches overlap the kernel before: they wait on the device
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(runs * gr.rows_per_tile + (a.accumulate ? 4 * gr.ctas : 0)));
+  cfg.gridDim = dim3(unsigned(runs * gr.rows_per_tile));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = join_smem;
   cfg.stream = st;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kv4_join_kernel<C::COLS, C::DV>, a, gr, runs);
+  e = cudaLaunchKernelEx(&cfg, kv4_join_kernel<C::COLS, C::DV>, a, gr);
   if (e != cudaSuccess) return e;
+  if (a.accumulate) {
+    cfg.gridDim = dim3(unsigned(8 * gr.ctas));
+    cfg.dynamicSmemBytes = gr.off_join;
+    e = cudaLaunchKernelEx(&cfg, kv4_weights_kernel, a, gr);
+    if (e != cudaSuccess) return e;
+  }
   return cudaGetLastError();
 }
 
