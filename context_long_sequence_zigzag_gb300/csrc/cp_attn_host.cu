@@ -1641,9 +1641,17 @@ cp_status_t cp_attn_key_weights(const cp_desc_t* d, int64_t last, const void* q,
   a.k = k;
   a.lse_in = lse;
   a.out = w;
+  // a replayed upload would read what later calls have put into the staging ring
+  auto capturing = [&]() {
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    const cudaError_t e = cudaStreamIsCapturing(cs, &status);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e == cudaErrorStreamCaptureImplicit || status != cudaStreamCaptureStatusNone;
+  };
   if (use_window(d, last)) {
     const auto win = get_window(d, m, last);
     if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < win->bytes.size()) return CP_ERR_WORKSPACE;
+    if (capturing()) return CP_ERR_UNSUPPORTED;
     if (h2d_async(ws, win->bytes.data(), win->bytes.size(), cs) != cudaSuccess) return CP_ERR_CUDA;
     const char* base = static_cast<const char*>(ws);
     return launch_key_weights_window(a, reinterpret_cast<const WinTile*>(base), win->num_tiles,
@@ -1655,6 +1663,7 @@ cp_status_t cp_attn_key_weights(const cp_desc_t* d, int64_t last, const void* q,
   const auto pp = get_plan(d, m, key_weights_plan_kind(d), -1, -1, -1, 0, last);
   const Plan& p = *pp;
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < plan_bytes(p)) return CP_ERR_WORKSPACE;
+  if (capturing()) return CP_ERR_UNSUPPORTED;
   st = stage_plan(p, static_cast<char*>(ws), cs, a, d->total_tokens, d->total_tokens, true, 2 * kTile);
   if (st != CP_OK) return st;
   const cudaError_t e = use_tc_key_weights(d) ? launch_tc_key_weights(a, cs) : launch_simt_key_weights(a, d->dtype, cs);

@@ -1013,11 +1013,14 @@ int cols_of(int rows, int dtype) { return dtype == CP_DT_BF16 && rows > 8 ? 16 :
 
 uint32_t up(uint32_t x, uint32_t n) { return (x + n - 1) / n * n; }
 
-template <typename C, typename E>
-cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
+constexpr uint32_t kMostShared = 230000;  // 227 KB less the static arrays
+
+// Shared memory of the first kernel: fills in the offsets, returns the bytes.
+template <typename C>
+uint32_t shared_layout(int num_seqs, Grid& gr) {
   uint32_t off = 0;
   gr.off_base = off;
-  off = up(off + 4 * (a.c.num_seqs + 1), 128);
+  off = up(off + 4 * (num_seqs + 1), 128);
   gr.off_frag = off;
   off += C::NW * (C::DQK / 16 * C::TERMS * 32) * C::COLS;
   gr.off_stat = off;
@@ -1026,10 +1029,35 @@ cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
   const uint32_t partials = C::NW * gr.rows_per_tile * C::DV * 4;
   off = up(off + partials, 128);
   gr.off_ring = off;
-  constexpr uint32_t kMost = 230000;  // 227 KB less the static arrays
   // the rings hold the last partials in the end
-  off += std::max<uint32_t>(C::STAGES * C::NW * C::SUB, partials);
-  if (off > kMost) return cudaErrorInvalidValue;
+  return off + std::max<uint32_t>(C::STAGES * C::NW * C::SUB, partials);
+}
+
+// Calls f with the configuration for these head dims, columns and type.
+template <int DQK, int DV, typename F>
+auto with_config(int cols, int dtype, F f) {
+  if (dtype == CP_DT_F32) return f(Cfg<DQK, DV, 1, 3, 8>{});
+  if (cols == 16) return f(Cfg<DQK, DV, 2, 1, 8>{});
+  // twelve warps: three a scheduler (sixteen would leave 128 registers a thread, and spill; measured with ten, twelve,
+  // fourteen and sixteen: 400, 345, 401 us and no room at 128K tokens of 64 heads 192 / 128)
+  return f(Cfg<DQK, DV, 1, 1, 12>{});
+}
+template <typename F>
+auto with_dims(int dqk, int dv, int cols, int dtype, F f) {
+  switch (dqk * 1000 + dv) {
+    case 64064: return with_config<64, 64>(cols, dtype, f);
+    case 64128: return with_config<64, 128>(cols, dtype, f);
+    case 128064: return with_config<128, 64>(cols, dtype, f);
+    case 192064: return with_config<192, 64>(cols, dtype, f);
+    case 192128: return with_config<192, 128>(cols, dtype, f);
+    default: return with_config<128, 128>(cols, dtype, f);
+  }
+}
+
+template <typename C, typename E>
+cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
+  const uint32_t bytes = shared_layout<C>(a.c.num_seqs, gr);
+  if (bytes > kMostShared) return cudaErrorInvalidValue;
   gr.warps = C::NW;
   auto kernel = kv4_attn_kernel<C, E>;
   static std::atomic<uint64_t> ready{0};  // devices whose kernel may use that much shared memory
@@ -1037,11 +1065,11 @@ cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared));
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
-  kernel<<<unsigned(gr.ctas), C::THREADS, off, st>>>(a, gr);
+  kernel<<<unsigned(gr.ctas), C::THREADS, bytes, st>>>(a, gr);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int runs = a.c.num_seqs * a.c.hkv * a.row_tiles;
@@ -1061,7 +1089,7 @@ cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
   e = cudaLaunchKernelEx(&cfg, kv4_join_kernel<C::COLS, C::DV>, a, gr);
   if (e != cudaSuccess) return e;
   if (a.accumulate) {
-    cfg.gridDim = dim3(unsigned(8 * gr.ctas));
+    cfg.gridDim = dim3(unsigned(5 * gr.ctas));
     cfg.dynamicSmemBytes = gr.off_join;
     e = cudaLaunchKernelEx(&cfg, kv4_weights_kernel, a, gr);
     if (e != cudaSuccess) return e;
@@ -1069,23 +1097,22 @@ cudaError_t launch(const Kv4AttnArgs& a, Grid gr, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <int DQK, int DV>
-cudaError_t launch_dims(const Kv4AttnArgs& a, const Grid& gr, int dtype, cudaStream_t st) {
-  if (dtype == CP_DT_F32) return launch<Cfg<DQK, DV, 1, 3, 8>, float>(a, gr, st);
-  if (cols_of(a.rows, dtype) == 16) return launch<Cfg<DQK, DV, 2, 1, 8>, __nv_bfloat16>(a, gr, st);
-  return launch<Cfg<DQK, DV, 1, 1, 12>, __nv_bfloat16>(a, gr, st);
-}
-
 struct Layout {
   int rows, cols, row_tiles, rows_per_tile;
   size_t part, score, total;
 };
-Layout layout_of(int num_seqs, int hq, int hkv, int dv, int max_pages, int dtype, int n_q, int accumulate) {
+Layout layout_of(int num_seqs, int hq, int hkv, int dqk, int dv, int max_pages, int dtype, int n_q, int accumulate) {
   Layout L;
   L.rows = hq / hkv * n_q;
   L.cols = cols_of(L.rows, dtype);
   L.row_tiles = (L.rows + L.cols - 1) / L.cols;
-  L.rows_per_tile = (L.rows + L.row_tiles - 1) / L.row_tiles;
+  for (;; ++L.row_tiles) {  // more passes of fewer rows where their partials do not fit (many sequences, wide heads)
+    L.rows_per_tile = (L.rows + L.row_tiles - 1) / L.row_tiles;
+    Grid gr{};
+    gr.rows_per_tile = L.rows_per_tile;
+    const uint32_t bytes = with_dims(dqk, dv, L.cols, dtype, [&](auto c) { return shared_layout<decltype(c)>(num_seqs, gr); });
+    if (bytes <= kMostShared || L.rows_per_tile == 1) break;
+  }
   L.row_tiles = (L.rows + L.rows_per_tile - 1) / L.rows_per_tile;
   L.part = 0;
   L.score = (size_t(kv4_sm_count()) * 2 * part_floats(L.cols, dv) * 4 + 255) / 256 * 256;
@@ -1093,6 +1120,9 @@ Layout layout_of(int num_seqs, int hq, int hkv, int dv, int max_pages, int dtype
   L.total = L.score + (accumulate ? units * L.rows_per_tile * kKv4Sub * 4 : 0);
   L.total = (L.total + 255) / 256 * 256;
   return L;
+}
+Layout layout_of(const cp_kv4_t* c, int n_q, int accumulate) {
+  return layout_of(c->num_seqs, c->hq, c->hkv, c->d_qk, c->d_v, c->max_pages, c->dtype, n_q, accumulate);
 }
 
 }  // namespace
@@ -1110,16 +1140,15 @@ int kv4_sm_count() {
 }
 
 size_t kv4_attn_workspace(const cp_kv4_t* c, int32_t n_q, int32_t accumulate) {
-  return layout_of(c->num_seqs, c->hq, c->hkv, c->d_v, c->max_pages, c->dtype, n_q, accumulate).total;
+  return layout_of(c, n_q, accumulate).total;
 }
 
 int64_t kv4_attn_units(const cp_kv4_t* c, int32_t n_q) {
-  return int64_t(c->num_seqs) * c->hkv * (int64_t(c->max_pages) * (CP_KV4_PAGE / kKv4Sub) + 1) *
-         layout_of(c->num_seqs, c->hq, c->hkv, c->d_v, c->max_pages, c->dtype, n_q, 0).row_tiles;
+  return int64_t(c->num_seqs) * c->hkv * (int64_t(c->max_pages) * (CP_KV4_PAGE / kKv4Sub) + 1) * layout_of(c, n_q, 0).row_tiles;
 }
 
 cudaError_t launch_kv4_attn(Kv4AttnArgs a, int dqk, int dv, int dtype, cudaStream_t st) {
-  const Layout L = layout_of(a.c.num_seqs, a.c.hq, a.c.hkv, dv, a.c.max_pages, dtype, a.n_q, a.accumulate);
+  const Layout L = layout_of(a.c.num_seqs, a.c.hq, a.c.hkv, dqk, dv, a.c.max_pages, dtype, a.n_q, a.accumulate);
   a.rows = L.rows;
   a.row_tiles = L.row_tiles;
   Grid gr{};
@@ -1127,15 +1156,11 @@ cudaError_t launch_kv4_attn(Kv4AttnArgs a, int dqk, int dv, int dtype, cudaStrea
   gr.rows_per_tile = L.rows_per_tile;
   gr.part = reinterpret_cast<float*>(a.ws + L.part);
   gr.score = reinterpret_cast<float*>(a.ws + L.score);
-  switch (dqk * 1000 + dv) {
-    case 64064: return launch_dims<64, 64>(a, gr, dtype, st);
-    case 64128: return launch_dims<64, 128>(a, gr, dtype, st);
-    case 128064: return launch_dims<128, 64>(a, gr, dtype, st);
-    case 128128: return launch_dims<128, 128>(a, gr, dtype, st);
-    case 192064: return launch_dims<192, 64>(a, gr, dtype, st);
-    case 192128: return launch_dims<192, 128>(a, gr, dtype, st);
-  }
-  return cudaErrorInvalidValue;
+  return with_dims(dqk, dv, L.cols, dtype, [&](auto c) {
+    using C = decltype(c);
+    if constexpr (C::TERMS == 3) return launch<C, float>(a, gr, st);
+    else return launch<C, __nv_bfloat16>(a, gr, st);
+  });
 }
 
 }  // namespace cpattn

@@ -351,7 +351,9 @@ cp_status_t cp_lin_attn_fwd(const cp_desc_t* desc, const void* q, const void* k,
  *               query sees get 0
  *   workspace : cp_workspace_size(desc, CP_OP_KEY_WEIGHTS) bytes, for any `last`
  * BF16 with d_qk in {128, 192} runs on the tensor cores; other head dims and
- * FP32 run on the CUDA cores.  d_v is not used. */
+ * FP32 run on the CUDA cores.  d_v is not used.  CP_ERR_UNSUPPORTED while
+ * `stream` is being captured into a graph (the tile plan is uploaded by the
+ * call). */
 cp_status_t cp_attn_key_weights(const cp_desc_t* desc, int64_t last, const void* q, const void* k, const float* lse,
                                 float* w, void* workspace, size_t workspace_bytes, cp_stream_t stream);
 
@@ -457,10 +459,11 @@ cp_status_t cp_kv4_read(const cp_kv4_t* cache, const int32_t* cu, const int32_t*
  *                the query heads of its kv head and the n_q queries, are added
  *                to cache.weights; 0: not
  *   workspace  : cp_kv4_workspace_size bytes
- * Queries, keys and probabilities meet on the tensor cores with FP32
- * accumulation: exactly unpacked codes, the softmax and the scales in FP32;
- * for BF16 caches the scaled probabilities are rounded to BF16 as operands,
- * for FP32 ones queries and probabilities are split into three BF16 terms. */
+ * Queries, codes and probabilities meet on the tensor cores with FP32
+ * accumulation; the codes are exact, the softmax, the scales and the lows act
+ * in FP32.  BF16 caches: a query's channels as two e4m3 terms (exact to 2^-18
+ * of its largest channel), the scaled probabilities rounded to BF16.  FP32
+ * caches: queries and scaled probabilities as three BF16 terms. */
 cp_status_t cp_kv4_attn(const cp_kv4_t* cache, int32_t n_q, const void* q, const int32_t* lengths, void* o,
                         int32_t o_f32, float* lse, int32_t accumulate, void* workspace, size_t workspace_bytes,
                         cp_stream_t stream);

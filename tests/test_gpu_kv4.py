@@ -7,7 +7,11 @@ Tolerances, derived from the arithmetic (u = 2^-24, the half step of fp32):
 * scores: fp32 sums of exact products of magnitude at most (16 + n) s |q|, and
   low |q|; d / 16 tensor-core adds a group and a few FMAs, each off by at most
   2 u of the running magnitude: SCORE = 2^-19 * scale * sum |q| (31 s + |low|)
-  covers 16 such steps.
+  covers 16 such steps.  bf16 queries are taken as two e4m3 terms of a row
+  scaled to a largest channel of 128 .. 256: four bits each, so exact where the
+  second's last bit is at least 2^-9, and off by at most 2^-10 below (channels
+  under 2^-9 of the largest): 2^-17 of the largest at most, with codes up to
+  15.  TINY = scale * 2^-17 max |q| * 15 s * (number of such channels).
 * lse: the scores' error, 2^-22 for the sum and log of it (relative to
   max(1, |lse|)).
 * probabilities: relative error SCORE + 2^-20.  Weights: that of the sum.
@@ -108,7 +112,12 @@ def check_attn(c, n_q=1, seed=1, part=False, q=None, accumulate=True, **kw):
         for h in range(c.hq):
             g = c.kv_of(h)
             mag = (31 * ks[:n, g] + np.abs(kl[:n, g])).max(0) if n else np.zeros(c.d_qk // 64)
-            score = 2.0 ** -19 * c.scale * (np.abs(qn[b, :, h]).reshape(n_q, -1, 64).sum(-1) @ mag)  # [n_q]
+            qa = np.abs(qn[b, :, h])
+            score = 2.0 ** -19 * c.scale * (qa.reshape(n_q, -1, 64).sum(-1) @ mag)  # [n_q]
+            if c.dtype == torch.bfloat16 and n:
+                top = qa.max(-1)
+                tiny = ((qa > 0) & (qa < 2.0 ** -9 * top[:, None])).sum(-1)
+                score = score + c.scale * 2.0 ** -17 * top * 15 * ks[:n, g].max() * tiny
             for t in range(n_q):
                 if n - (n_q - 1 - t) <= 0:
                     assert lse[h, b * n_q + t] == -math.inf and not o[b, t, h].any()
@@ -175,6 +184,45 @@ def test_attn_without_weights_leaves_them_and_a_cache_needs_none():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     with pytest.raises(cpa.CpError):
         cpa.cp_kv4_attn(bare, q, ints(c.lengths), accumulate=True)
+
+
+@pytest.mark.parametrize("spread", [1e-30, 1e-3, 1e25])
+def test_attn_query_magnitudes(spread):
+    """Queries far from 1, rows with one channel far above the others, rows of zeros."""
+    c = Filled([300, 40], 4, 2, 128, 128, seed=19, scale=0.1 / spread)
+    q = torch.randn(2, 2, 4, 128, device="cuda")
+    q[0, 0, :2, 5] = 3000.0
+    q[1, 1, 3] = 0.0
+    q[0, 1, 1, :64] *= 1e-4
+    check_attn(c, n_q=2, q=(q * spread).bfloat16())
+
+
+def test_attn_infinite_query_gives_nan():
+    c = Filled([100], 2, 1, 128, 128, seed=20)
+    q = torch.randn(1, 1, 2, 128, device="cuda").bfloat16()
+    ref = cpa.cp_kv4_attn(c.cache, q, ints([100]))
+    q[0, 0, 1, 3] = math.inf
+    o, lse = cpa.cp_kv4_attn(c.cache, q, ints([100]))
+    assert torch.isnan(o[0, 0, 1]).all() and torch.isnan(lse[1, 0])
+    assert torch.equal(o[0, 0, 0], ref[0][0, 0, 0]) and torch.equal(lse[0], ref[1][0])
+
+
+def test_attn_thousands_of_sequences():
+    """More sequences than leave room for eight rows' partials of the widest heads in shared memory."""
+    rng = np.random.RandomState(21)
+    lengths = [int(x) for x in rng.randint(0, 40, 1500)]
+    c = Filled(lengths, 8, 1, 192, 128, seed=22)
+    q = torch.from_numpy(rng.randn(1500, 1, 8, 192).astype(np.float32)).bfloat16().cuda()
+    o, lse = cpa.cp_kv4_attn(c.cache, q, ints(lengths), accumulate=True)
+    some = [0, 1, 700, 1498, 1499]
+    for b in some:
+        part = Filled.__new__(Filled)
+        part.__dict__.update(c.__dict__, lengths=[lengths[b]], table=c.table[b:b + 1], weights=torch.from_numpy(c.w0).cuda())
+        part.cache = cpa.Kv4Cache(c.pages, ints(part.table.tolist()).reshape(1, -1), 8, 1, 192, 128, part.weights)
+        o1, lse1 = check_attn(part, q=q[b:b + 1].contiguous())
+        ids = c.table[b, :-(-lengths[b] // 64)]
+        assert np.abs(f64(c.weights)[ids] - f64(part.weights)[ids]).max(initial=0) < 1e-4
+        assert np.abs(f64(o[b]) - o1[0]).max() < 0.05
 
 
 def test_attn_large_scores():
@@ -270,6 +318,51 @@ def test_attn_repeats_bit_for_bit_and_in_a_graph():
     graph.replay()
     o2, lse2 = cpa.cp_kv4_attn(c.cache, q, lens)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_two_graphs_and_two_streams_at_once():
+    """Captured calls with workspaces of their own run side by side; a workspace may serve one after the other."""
+    c = Filled([3000, 500], 8, 2, 128, 128, seed=23)
+    q = [torch.randn(2, 1, 8, 128, device="cuda").bfloat16() for _ in range(2)]
+    lens = ints(c.lengths)
+    ref = [cpa.cp_kv4_attn(c.cache, x, lens) for x in q]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for share in (False, True):
+        ws = [torch.empty(cpa.cp_kv4_workspace_size(c.cache), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        if share:
+            ws[1] = ws[0]
+        out, graphs = [], []
+        for i in range(2):
+            o, lse, g = torch.empty_like(ref[i][0]), torch.empty_like(ref[i][1]), torch.cuda.CUDAGraph()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(g, stream=streams[i]):
+                cpa.cp_kv4_attn(c.cache, q[i], lens, o=o, lse=lse, ws=ws[i])
+            out.append((o, lse))
+            graphs.append(g)
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for i in range(2):
+                with torch.cuda.stream(streams[0 if share else i]):
+                    graphs[i].replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, ref):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_key_weights_refuse_capture():
+    T = 256
+    q, k = torch.randn(T, 2, 128, device="cuda").bfloat16(), torch.randn(T, 2, 128, device="cuda").bfloat16()
+    prob = cpa.Problem(T, 2, 2, 128, 64, 1, "contiguous")
+    lse = torch.zeros(2, T, device="cuda")
+    ws = torch.empty(cpa.cp_workspace_size(prob, cpa.CP_OP_KEY_WEIGHTS), dtype=torch.uint8, device="cuda")
+    for last in (None, 16):
+        w = cpa.cp_attn_key_weights(prob, q, k, lse, last=last, ws=ws)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            with pytest.raises(cpa.CpError) as e:
+                cpa.cp_attn_key_weights(prob, q, k, lse, last=last, w=w, ws=ws)
+            torch.empty(1, device="cuda").zero_()  # the capture itself goes on
+        assert e.value.status == cpa.CP_ERR_UNSUPPORTED
 
 
 def test_attn_on_another_stream():
