@@ -142,17 +142,18 @@ __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t a, uint32_t o) {
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(a), "r"(o));
   return y;
 }
-// 16 + n of nibbles i and i + 4 as a bf16 pair
+// n - 8 of nibbles I and I + 4 as a bf16 pair, exact: 16 + n is put together from bits and 24 taken off. Around the
+// middle, because sums over many tokens cancel: with 16 + n or 0 + n the fp32 accumulators (which the tensor cores cut
+// off rather than round) carry 8 to 24 times the sum of P s, and the rounding of P s to bf16 is worth up to 15 steps
+// instead of 8. (128K tokens, d 192/128: error of O 0.047 of its norm with 16 + n.)
 template <int I>
 __device__ __forceinline__ uint32_t nibbles(uint32_t w, const Masks& k) {
-  return and_or(I == 0 ? w << 3 : w >> (4 * I - 3), k.nib, k.sixteen);
+  return ptx::add_bf16x2(and_or(I == 0 ? w << 3 : w >> (4 * I - 3), k.nib, k.sixteen), 0xC1C0C1C0u);
 }
 
-// Nibbles 0 and 4 of V words: of bf16 caches as 128 + n, which takes no shift
-// (the eightfold of the other channels' offset is taken out in the end)
-template <int TERMS>
+// Nibbles 0 and 4, by way of 128 + n, which takes no shift
 __device__ __forceinline__ uint32_t nibble0(uint32_t w, const Masks& k) {
-  return TERMS == 1 ? and_or(w, k.low, k.big) : nibbles<0>(w, k);
+  return ptx::add_bf16x2(and_or(w, k.low, k.big), 0xC308C308u);
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
 
   constexpr int kFragStride = C::COLS * 32;
   uint8_t* frag0 = smem + gr.off_frag + warp * (DQK / 16 * TERMS) * kFragStride;
-  float O[GV][4][NT][4], osix[GV][NT][4], ref[NT][2];
+  float O[GV][4][NT][4], ref[NT][2];
   uint64_t ooff2[GV][NT], sum2[NT];  // pairs: columns 2c and 2c + 1
   const Masks masks;
   int stage = 0;
@@ -447,8 +448,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) O[g][i][nt][e] = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) osix[g][nt][e] = 0.f;
         ooff2[g][nt] = 0;
       }
       ref[nt][0] = ref[nt][1] = kNoRef;
@@ -482,7 +481,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const float s1 = half_at(kp[mt][x], g), l1 = half_at(kp[mt][x], GK + g);
+              const float s1 = half_at(kp[mt][x], g);
+              float l1 = half_at(kp[mt][x], GK + g);
+              if (TERMS == 3) l1 = fmaf(8.f, s1, l1);
               ks[mt][x] = ptx::f32x2(s1, s1);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
@@ -516,15 +517,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
                 }
             }
           } else {
-            float acc[2][NT][4];
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                ptx::f32x2_split(ptx::mul_f32x2(qsum2[g][nt], ptx::f32x2(-16.f, -16.f)), acc[mt][nt][0], acc[mt][nt][1]);
-                acc[mt][nt][2] = acc[mt][nt][0];
-                acc[mt][nt][3] = acc[mt][nt][1];
-              }
+            float acc[2][NT][4] = {};
 #pragma unroll
             for (int jp = 4 * g; jp < 4 * g + 4; ++jp) {
               const int j = jp >> 1;
@@ -533,7 +526,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
               for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                  A[mt][x] = jp & 1 ? nibbles<2>(kw[mt][x][j], masks) : nibbles<0>(kw[mt][x][j], masks);
+                  A[mt][x] = jp & 1 ? nibbles<2>(kw[mt][x][j], masks) : nibble0(kw[mt][x][j], masks);
                   A[mt][2 + x] = jp & 1 ? nibbles<3>(kw[mt][x][j], masks) : nibbles<1>(kw[mt][x][j], masks);
                 }
 #pragma unroll
@@ -635,11 +628,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
           for (int g = 0; g < GV; ++g) {
             ooff2[g][nt] = ptx::mul_f32x2(ooff2[g][nt], keep2);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              osix[g][nt][e] *= keep[e & 1];
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
               for (int i = 0; i < 4; ++i) O[g][i][nt][e] *= keep[e & 1];
-            }
           }
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
@@ -682,8 +673,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
           // P s of this group as B fragments, and P low on the side
           uint32_t B0[NT][TERMS], B1[NT][TERMS];
           const float s0 = half_at(vs[0], g), s1 = half_at(vs[1], g);
-          const float l0 = load_bf16(st + f.vl() + (g * kKv4Sub + mt * 16 + r) * 2);
-          const float l1 = load_bf16(st + f.vl() + (g * kKv4Sub + mt * 16 + 8 + r) * 2);
+          // the middle of the group's range, 8 steps up
+          const float l0 = fmaf(8.f, s0, load_bf16(st + f.vl() + (g * kKv4Sub + mt * 16 + r) * 2));
+          const float l1 = fmaf(8.f, s1, load_bf16(st + f.vl() + (g * kKv4Sub + mt * 16 + 8 + r) * 2));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float ps[4];
@@ -711,19 +703,35 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
           }
           const uint32_t lo0 = __byte_perm(vw[0][g], vw[1][g], 0x5410), hi0 = __byte_perm(vw[0][g], vw[1][g], 0x7632);
           const uint32_t lo1 = __byte_perm(vw[2][g], vw[3][g], 0x5410), hi1 = __byte_perm(vw[2][g], vw[3][g], 0x7632);
-          const uint32_t A[5][4] = {{nibble0<TERMS>(lo0, masks), nibble0<TERMS>(hi0, masks), nibble0<TERMS>(lo1, masks), nibble0<TERMS>(hi1, masks)},
-                                    {nibbles<1>(lo0, masks), nibbles<1>(hi0, masks), nibbles<1>(lo1, masks), nibbles<1>(hi1, masks)},
-                                    {nibbles<2>(lo0, masks), nibbles<2>(hi0, masks), nibbles<2>(lo1, masks), nibbles<2>(hi1, masks)},
-                                    {nibbles<3>(lo0, masks), nibbles<3>(hi0, masks), nibbles<3>(lo1, masks), nibbles<3>(hi1, masks)},
-                                    {0xC180C180u, 0xC180C180u, 0xC180C180u, 0xC180C180u}};  // -16
+          const uint32_t A[4][4] = {
+              {nibble0(lo0, masks), nibble0(hi0, masks), nibble0(lo1, masks), nibble0(hi1, masks)},
+              {nibbles<1>(lo0, masks), nibbles<1>(hi0, masks), nibbles<1>(lo1, masks), nibbles<1>(hi1, masks)},
+              {nibbles<2>(lo0, masks), nibbles<2>(hi0, masks), nibbles<2>(lo1, masks), nibbles<2>(hi1, masks)},
+              {nibbles<3>(lo0, masks), nibbles<3>(hi0, masks), nibbles<3>(lo1, masks), nibbles<3>(hi1, masks)}};
+          // The tensor cores cut a sum off where they add to an accumulator. In fp32 caches each product of 16 tokens is
+          // therefore added outside, rounded (96519 tokens, d 128: error of O 1.9e-7 of its norm, 9.3e-5 otherwise); in
+          // bf16 caches the rounding of P s hides it (0.0024 either way at 128K tokens; 350 us, 354 outside).
+          if constexpr (TERMS == 3) {
 #pragma unroll
-          for (int m = 0; m < TERMS; ++m)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+              for (int i = 0; i < 4; ++i) {
+                float d[4] = {};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) ptx::mma_16816(O[g][i][nt], A[i], B0[nt][m], B1[nt][m]);
-              ptx::mma_16816(osix[g][nt], A[4], B0[nt][m], B1[nt][m]);
-            }
+                for (int m = 0; m < TERMS; ++m) ptx::mma_16816(d, A[i], B0[nt][m], B1[nt][m]);
+#pragma unroll
+                for (int e = 0; e < 4; e += 2)
+                  ptx::f32x2_split(ptx::add_f32x2(ptx::f32x2(O[g][i][nt][e], O[g][i][nt][e + 1]), ptx::f32x2(d[e], d[e + 1])),
+                                   O[g][i][nt][e], O[g][i][nt][e + 1]);
+              }
+          } else {
+#pragma unroll
+            for (int m = 0; m < TERMS; ++m)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ptx::mma_16816(O[g][i][nt], A[i], B0[nt][m], B1[nt][m]);
+          }
         }
       }
       __syncwarp();  // the stage has been read
@@ -761,12 +769,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
           const float l = sum[nt][e], inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
           for (int g = 0; g < GV; ++g) {
-            const float add = osix[g][nt][e] + ooff[g][nt][e];
-            const float add0 = TERMS == 1 ? fmaf(8.f, osix[g][nt][e], ooff[g][nt][e]) : add;
+            const float add = ooff[g][nt][e];
 #pragma unroll
             for (int x = 0; x < 2; ++x)
               store_o4(a, row * DV + 64 * g + 8 * r + 4 * x,
-                       make_float4((O[g][0][nt][e + 2 * x] + add0) * inv, (O[g][1][nt][e + 2 * x] + add) * inv,
+                       make_float4((O[g][0][nt][e + 2 * x] + add) * inv, (O[g][1][nt][e + 2 * x] + add) * inv,
                                    (O[g][2][nt][e + 2 * x] + add) * inv, (O[g][3][nt][e + 2 * x] + add) * inv));
           }
           if (r == 0)
@@ -791,12 +798,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
           }
 #pragma unroll
           for (int g = 0; g < GV; ++g) {
-            const float add = osix[g][nt][e] + ooff[g][nt][e];
-            const float add0 = TERMS == 1 ? fmaf(8.f, osix[g][nt][e], ooff[g][nt][e]) : add;
+            const float add = ooff[g][nt][e];
 #pragma unroll
             for (int x = 0; x < 2; ++x)
               *reinterpret_cast<float4*>(part + n * DV + 64 * g + 8 * r + 4 * x) =
-                  make_float4(O[g][0][nt][e + 2 * x] + add0, O[g][1][nt][e + 2 * x] + add, O[g][2][nt][e + 2 * x] + add,
+                  make_float4(O[g][0][nt][e + 2 * x] + add, O[g][1][nt][e + 2 * x] + add, O[g][2][nt][e + 2 * x] + add,
                               O[g][3][nt][e + 2 * x] + add);
           }
         }

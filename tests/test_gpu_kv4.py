@@ -15,8 +15,9 @@ Tolerances, derived from the arithmetic (u = 2^-24, the half step of fp32):
 * lse: the scores' error, 2^-22 for the sum and log of it (relative to
   max(1, |lse|)).
 * probabilities: relative error SCORE + 2^-20.  Weights: that of the sum.
-* o: sum p (v - low) and sum p low with those probabilities, in bf16 caches
-  with p s rounded to bf16 (2^-8 of sum p (v - low)), and rounded to bf16
+* o: sum p s (n - 8) and sum p (low + 8 s) with those probabilities, in bf16
+  caches with p s rounded to bf16, each by at most 2^-8 of itself: together
+  2^-8 of sum p s |n - 8| = sum p |v - (low + 8 s)|; and rounded to bf16
   (2^-8 of o).
 """
 
@@ -106,9 +107,10 @@ def check_attn(c, n_q=1, seed=1, part=False, q=None, accumulate=True, **kw):
     want_w, tol_w = c.w0.astype(np.float64), 2.0 ** -23 * np.ones_like(c.w0)
     for b, n in enumerate(c.lengths):
         k, kl, ks = c.sequence(b, c.k)
-        v, vl, _ = c.sequence(b, c.v)
+        v, vl, vs = c.sequence(b, c.v)
         ref_o, ref_lse, ref_w = oracle.kv4_attention(qn[b], k, v, n, c.scale, c.kv_of)
         low = oracle.kv4_attention(qn[b], k, np.repeat(vl, 64, -1), n, c.scale, c.kv_of)[0]
+        off = oracle.kv4_attention(qn[b], k, np.abs(v - np.repeat(vl + 8 * vs, 64, -1)), n, c.scale, c.kv_of)[0]
         for h in range(c.hq):
             g = c.kv_of(h)
             mag = (31 * ks[:n, g] + np.abs(kl[:n, g])).max(0) if n else np.zeros(c.d_qk // 64)
@@ -126,7 +128,7 @@ def check_attn(c, n_q=1, seed=1, part=False, q=None, accumulate=True, **kw):
                 above = ref_o[t, h] - low[t, h]  # sum p (v - low) >= 0
                 tol = 2 * (score[t] + 2.0 ** -19) * (above + np.abs(low[t, h]))
                 if c.dtype == torch.bfloat16:
-                    tol = tol + 2.0 ** -8 * above + (0 if part else 2.0 ** -8 * np.abs(ref_o[t, h]))
+                    tol = tol + 2.0 ** -8 * off[t, h] + (0 if part else 2.0 ** -8 * np.abs(ref_o[t, h]))
                 err = np.abs(o[b, t, h] - ref_o[t, h])
                 assert np.all(err <= tol), (b, t, h, (err - tol).max())
         ids = c.table[b, :-(-n // 64)]
