@@ -308,28 +308,30 @@ __device__ __forceinline__ uint32_t rank_key(float x) {
 constexpr int kSelThreads = 1024;
 constexpr int kDigits = 2048;      // bins of an 11-bit digit
 constexpr int kSelKeys = 49152;    // keys that a CTA keeps in shared memory
+constexpr int kSelParts = 8;        // CTAs of a row at most
 constexpr int kSelSlice = 8192;    // slots a CTA takes at least where a row gets several
 
 // Sum of x over the threads before this one; *all gets the sum over all.
-__device__ __forceinline__ int block_before(int x, int* scratch, int* all) {
+// scratch: a word a warp, not used again before the block's next barrier.
+template <typename T>
+__device__ __forceinline__ T block_before(T x, T* scratch, T* all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int y = x;
+  T y = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int z = __shfl_up_sync(0xffffffffu, y, o);
+    const T z = __shfl_up_sync(0xffffffffu, y, o);
     if (lane >= o) y += z;
   }
   if (lane == 31) scratch[warp] = y;
   __syncthreads();
-  int z = scratch[lane];  // kSelThreads / 32 = 32 warps
+  T z = scratch[lane];  // kSelThreads / 32 = 32 warps
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, z, o);
+    const T u = __shfl_up_sync(0xffffffffu, z, o);
     if (lane >= o) z += u;
   }
   *all = __shfl_sync(0xffffffffu, z, 31);
-  const int warps_before = __shfl_sync(0xffffffffu, z, max(warp - 1, 0));
-  __syncthreads();
+  const T warps_before = __shfl_sync(0xffffffffu, z, max(warp - 1, 0));
   return y - x + (warp > 0 ? warps_before : 0);
 }
 
@@ -339,15 +341,26 @@ __device__ __forceinline__ int block_before(int x, int* scratch, int* all) {
 // found digit by digit, 11 bits a pass: the CTAs count their slices, and every
 // one of them sums the counts over the cluster through distributed shared
 // memory.  The slots above the key, and the first `need` of those that equal
-// it, then get their places from counts in slot order.
+// it, then get their places from one scan, a thread having consecutive slots.
+// Bound by the latency of its barriers and loads, so: counts of their own for
+// each pass, the first taken while the keys are loaded, and the block's
+// barrier where a row has one CTA.
 __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4Cache c, const int32_t* lengths,
                                                                  int32_t budget, int32_t recent, int32_t* new_lengths,
                                                                  int32_t* kept, int most_keys) {
   extern __shared__ uint32_t keys[];
-  __shared__ int32_t hist[kDigits], scratch[32], s_count[2];
-  __shared__ int32_t s_digit, s_left;
+  __shared__ __align__(8) int32_t hist[3][kDigits];
+  __shared__ int32_t scratch[3][32], s_digit, s_left;
+  __shared__ uint64_t scratch2[32], s_count;
   cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
   const int parts = int(cluster.num_blocks()), part = int(cluster.block_rank());
+  auto sync_row = [&] {
+    if (parts == 1)
+      __syncthreads();
+    else
+      cluster.sync();
+  };
+  ptx::grid_launch_dependents();
   const int64_t row = blockIdx.x / parts;
   const int b = int(row / c.hkv), h = int(row - int64_t(b) * c.hkv);
   const int tid = threadIdx.x;
@@ -370,77 +383,72 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4Cache 
     return page < 0 ? 0u : rank_key(__ldg(c.weights + (int64_t(page) * c.hkv + h) * CP_KV4_PAGE + j % CP_KV4_PAGE));
   };
   const bool held = count <= most_keys;
-  if (held) {
-#pragma unroll 4
-    for (int j = tid; j < count; j += kSelThreads) keys[j] = weight_key(lo + j);
-  }
   auto key_at = [&](int j) -> uint32_t { return held ? keys[j] : weight_key(lo + j); };
+  for (int i = tid; i < 3 * kDigits; i += kSelThreads) (&hist[0][0])[i] = 0;
+  __syncthreads();
+#pragma unroll 8
+  for (int j = tid; j < count; j += kSelThreads) {
+    const uint32_t key = weight_key(lo + j);
+    if (held) keys[j] = key;
+    atomicAdd(&hist[0][key >> 21], 1);
+  }
   uint32_t prefix = 0, known = 0;  // known: the bits of it that are found
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     const uint32_t digits = pass == 2 ? 1023u : 2047u;
-    for (int i = tid; i < kDigits; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
-    for (int j = tid; j < count; j += kSelThreads) {
-      const uint32_t key = key_at(j);
-      if ((key & known) == prefix) atomicAdd(&hist[(key >> shift) & digits], 1);
-    }
-    cluster.sync();
+    if (pass > 0)
+      for (int j = tid; j < count; j += kSelThreads) {
+        const uint32_t key = key_at(j);
+        if ((key & known) == prefix) atomicAdd(&hist[pass][(key >> shift) & digits], 1);
+      }
+    sync_row();
     // thread t sums digits 2047 - 2t and 2046 - 2t
     int have[2] = {0, 0};
-    for (int q = 0; q < parts; ++q) {
-      const int32_t* other = cluster.map_shared_rank(hist, q);
-      have[0] += other[kDigits - 1 - 2 * tid];
-      have[1] += other[kDigits - 2 - 2 * tid];
+#pragma unroll
+    for (int q = 0; q < kSelParts; ++q) {
+      if (q >= parts) break;
+      const int2 two = *reinterpret_cast<const int2*>(cluster.map_shared_rank(hist[pass], q) + kDigits - 2 - 2 * tid);
+      have[0] += two.y;
+      have[1] += two.x;
     }
     int all;
-    const int above = block_before(have[0] + have[1], scratch, &all);
+    const int above = block_before(have[0] + have[1], scratch[pass], &all);
     if (above < need && need <= above + have[0] + have[1]) {
       const int low = need > above + have[0];
       s_digit = kDigits - 1 - 2 * tid - low;
       s_left = need - above - (low ? have[0] : 0);
     }
-    cluster.sync();  // (the counts have been read)
+    __syncthreads();
     prefix |= uint32_t(s_digit) << shift;
     known |= digits << shift;
     need = s_left;
-    __syncthreads();
   }
-  // ---- this slice's share of them
-  int above = 0, same = 0;
-  for (int j = tid; j < count; j += kSelThreads) {
+  // ---- places: each thread's run of slots (an odd number, so that a warp's reads meet no bank twice)
+  const int run = ((count + kSelThreads - 1) / kSelThreads) | 1;
+  const int j0 = min(tid * run, count), j1 = min(j0 + run, count);
+  uint64_t mine = 0;  // slots above the key, and equal to it in the upper half
+  for (int j = j0; j < j1; ++j) {
     const uint32_t key = key_at(j);
-    above += key > prefix;
-    same += key == prefix;
+    mine += key > prefix ? 1ull : (key == prefix ? 1ull << 32 : 0ull);
   }
-  int all_above, all_same;
-  block_before(above, scratch, &all_above);
-  block_before(same, scratch, &all_same);
-  if (tid == 0) {
-    s_count[0] = all_above;
-    s_count[1] = all_same;
+  uint64_t all, before = block_before(mine, scratch2, &all);
+  if (parts > 1) {
+    if (tid == 0) s_count = all;
+    cluster.sync();
+    for (int q = 0; q < part; ++q) before += *cluster.map_shared_rank(&s_count, q);
+    cluster.sync();  // (no CTA leaves while its counts are read)
   }
-  cluster.sync();
-  int written = 0, equal = 0;  // above and equal in the slices before
-  for (int q = 0; q < part; ++q) {
-    const int32_t* other = cluster.map_shared_rank(s_count, q);
-    written += other[0];
-    equal += other[1];
-  }
-  cluster.sync();  // (no CTA leaves while its counts are read)
-  written += min(equal, need);
-  for (int j0 = 0; j0 < count; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    const uint32_t key = j < count ? key_at(j) : 0u;
-    const bool is_above = j < count && key > prefix, is_same = j < count && key == prefix;
-    int all;
-    const int before = block_before(int(is_above) | int(is_same) << 16, scratch, &all);
-    const int same_before = equal + (before >> 16);
-    if (is_above || (is_same && same_before < need))
-      out[written + (before & 0xffff) + min(same_before, need) - min(equal, need)] = lo + j;
-    written += (all & 0xffff) + min(equal + (all >> 16), need) - min(equal, need);
-    equal += all >> 16;
+  int above = int(uint32_t(before)), same = int(before >> 32);
+  for (int j = j0; j < j1; ++j) {
+    const uint32_t key = key_at(j);
+    if (key > prefix) {
+      out[above + min(same, need)] = lo + j;
+      ++above;
+    } else if (key == prefix) {
+      if (same < need) out[above + same] = lo + j;
+      ++same;
+    }
   }
 }
 
@@ -451,6 +459,7 @@ __global__ void __launch_bounds__(kThreads) kv4_move_kernel(const Kv4Cache c, co
   const int lane = threadIdx.x & 31;
   const int subs = (budget + kKv4Sub - 1) / kKv4Sub;
   const int64_t unit = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  ptx::grid_wait_previous();  // launched while the selection runs
   if (unit >= int64_t(subs) * c.num_seqs * c.hkv) return;
   const int64_t bh = unit / subs;
   const int u = int(unit - bh * subs), b = int(bh / c.hkv), h = int(bh - int64_t(b) * c.hkv);
@@ -560,7 +569,7 @@ cudaError_t launch_kv4_evict(const Kv4Cache& c, int dqk, int dv, const int32_t* 
   // CTAs a row by the longest sequence that the table can hold
   const int64_t most = int64_t(c.max_pages) * CP_KV4_PAGE;
   int parts = 1;
-  while (parts < 8 && int64_t(parts) * kSelSlice < most) parts *= 2;
+  while (parts < kSelParts && int64_t(parts) * kSelSlice < most) parts *= 2;
   const int keys = int(std::min<int64_t>(kSelKeys, (most + parts - 1) / parts));
   static std::atomic<uint64_t> ready{0};  // devices whose kernel may use that much shared memory
   int dev = 0;
@@ -586,8 +595,13 @@ cudaError_t launch_kv4_evict(const Kv4Cache& c, int dqk, int dv, const int32_t* 
   if (e != cudaSuccess) return e;
   const int64_t units = int64_t((budget + kKv4Sub - 1) / kKv4Sub) * c.num_seqs * c.hkv;
   const int64_t grid = (units + kThreads / 32 - 1) / (kThreads / 32);
-  kv4_move_kernel<<<unsigned(grid), kThreads, 0, st>>>(c, to, Kv4Format(dqk, dv), budget, new_lengths, kept);
-  return cudaGetLastError();
+  shape.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  shape.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, kv4_move_kernel, c, to, Kv4Format(dqk, dv), budget, static_cast<const int32_t*>(new_lengths),
+                            static_cast<const int32_t*>(kept));
 }
 
 }  // namespace cpattn
