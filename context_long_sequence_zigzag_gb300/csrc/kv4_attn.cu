@@ -966,14 +966,15 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_weights_kernel(const Kv4Attn
   const int lane = threadIdx.x & 31;
   const int warps = int(gridDim.x) * (kJoinThreads / 32);
   const int w = int(blockIdx.x) * (kJoinThreads / 32) + int(threadIdx.x >> 5);
-  const int64_t all = units / row_tiles;  // units of the cache: row tile by row tile the same
-  const int64_t v0 = all * w / warps, v1 = all * (w + 1) / warps;
+  const int all = units / row_tiles;  // units of the cache: row tile by row tile the same
+  const int each = (all + warps - 1) / warps;
+  const int v1 = int(min(int64_t(all), int64_t(each) * (w + 1)));
   int b = 0;
-  for (int64_t v = v0; v < v1;) {
-    b = seq_of_unit(base, a.c.num_seqs, b, int(v * row_tiles));
+  for (int v = int(min(int64_t(all), int64_t(each) * w)); v < v1;) {
+    b = seq_of_unit(base, a.c.num_seqs, b, v * row_tiles);
     const int per_run = (base[b + 1] - base[b]) / per;
-    const int at = int(v) - base[b] / row_tiles, h = at / per_run, first = at - h * per_run;
-    const int i0 = max(first - 1, 0), i1 = int(min(int64_t(per_run), first + v1 - v)) - 1;  // sub-blocks
+    const int at = v - base[b] / row_tiles, h = at / per_run, first = at - h * per_run;
+    const int i0 = max(first - 1, 0), i1 = min(per_run, first + v1 - v) - 1;  // sub-blocks
     v += per_run - first;
     const int len = kv4_length(a.c, a.lengths, b);
     for (int rt = 0; rt < row_tiles; ++rt) {
@@ -993,7 +994,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_weights_kernel(const Kv4Attn
         for (int k = 0; k < 4; ++k)
           page[k] = __ldg(a.c.table + int64_t(b) * a.c.max_pages + min(i + k, i1 - 1) / (CP_KV4_PAGE / kKv4Sub));
         const float* sc = gr.score + int64_t(run0 + 1 + i) * gr.rows_per_tile * kKv4Sub + lane;
-#pragma unroll 2
+#pragma unroll 4
         for (int n = 0; n < rows; ++n) {
           const float lsn = __shfl_sync(0xffffffffu, ls, n);
 #pragma unroll
