@@ -20,19 +20,68 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+// 16 channels as they lie in memory
+template <typename E>
+struct Raw {
+  static constexpr int N = int(sizeof(E));
+  uint4 u[N];
+  __device__ __forceinline__ void load(const E* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    for (int i = 0; i < N; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
   }
-}
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) u[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ uint32_t word(int i) const {  // i is a constant
+    return i % 4 == 0 ? u[i / 4].x : (i % 4 == 1 ? u[i / 4].y : (i % 4 == 2 ? u[i / 4].z : u[i / 4].w));
+  }
+  // channels 8 w .. 8 w + 7
+  __device__ __forceinline__ void half(int w, float (&x)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (sizeof(E) == 4)
+        x[j] = __uint_as_float(word(8 * w + j));
+      else
+        x[j] = __uint_as_float(j % 2 ? word(4 * w + j / 2) & 0xffff0000u : word(4 * w + j / 2) << 16);
+    }
+  }
+  // Minimum and maximum over 4 lanes' 16 channels each; NaN where one is NaN
+  __device__ __forceinline__ void range(uint32_t lanes, float& lo, float& hi) const {
+    if constexpr (sizeof(E) == 4) {
+      lo = hi = __uint_as_float(word(0));
+#pragma unroll
+      for (int j = 1; j < 16; ++j) {
+        asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(__uint_as_float(word(j))));
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(__uint_as_float(word(j))));
+      }
+#pragma unroll
+      for (int s = 1; s < 4; s <<= 1) {
+        const float l = __shfl_xor_sync(lanes, lo, s), h = __shfl_xor_sync(lanes, hi, s);
+        asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(l));
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(h));
+      }
+    } else {  // pairs of bf16, and across the lanes the minimum beside the negated maximum
+      uint32_t l = word(0), h = l;
+#pragma unroll
+      for (int j = 1; j < 8; ++j) {
+        asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(l) : "r"(word(j)));
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(h) : "r"(word(j)));
+      }
+      h ^= 0x80008000u;
+      const uint32_t other = __byte_perm(l, h, 0x7632);
+      l = __byte_perm(l, h, 0x5410);
+      asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(l) : "r"(other));
+#pragma unroll
+      for (int s = 1; s < 4; s <<= 1) {
+        const uint32_t o = __shfl_xor_sync(lanes, l, s);
+        asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(l) : "r"(o));
+      }
+      lo = __uint_as_float(l << 16);
+      hi = -__uint_as_float(l & 0xffff0000u);
+    }
+  }
+};
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -101,16 +150,6 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float low, flo
   return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
 }
 
-// Minimum and maximum of 16 channels; NaN where one is NaN.
-__device__ __forceinline__ void range_of(const float (&x)[2][8], float& lo, float& hi) {
-  lo = hi = x[0][0];
-#pragma unroll
-  for (int j = 1; j < 16; ++j) {
-    asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(x[j / 8][j % 8]));
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(x[j / 8][j % 8]));
-  }
-}
-
 // A token's place in the cache and its row outside it.
 struct Place {
   uint8_t* sub;  // sub-block of head 0's block (heads are block() bytes apart), or null
@@ -166,9 +205,12 @@ __device__ __forceinline__ Word word_of(const Words& n, int i) {
 }
 
 constexpr int kMostTokens = 32;  // of a CTA
+constexpr int kAhead = 2;        // pieces a thread of read loads before it writes (64K tokens: 65 us; 1: 75, 3: 73)
 
+// CTAs an SM: as many as leave the registers their place (64K tokens of bf16, 8 heads of 128 + 128: 96 us with 4, 135 with
+// 5, whose registers spill; fp32 values take more of them).
 template <typename E>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Cache c, const Kv4Format f, const Words n, const E* k,
+__global__ void __launch_bounds__(kThreads, sizeof(E) == 2 ? 4 : 3) kv4_append_kernel(const Kv4Cache c, const Kv4Format f, const Words n, const E* k,
                                                               const E* v, const float* w, int64_t src_rows,
                                                               const int32_t* rows, const int32_t* cu,
                                                               const int32_t* start, int64_t tokens, int per_block) {
@@ -178,39 +220,27 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Cache c, 
   if (threadIdx.x < here) places[threadIdx.x] = place_of(c, f, cu, start, rows, src_rows, t0 + threadIdx.x);
   __syncthreads();
   const int all = here * n.words;
-  auto load = [&](int i, float (&x)[2][8]) -> Word {  // the groups of 4 lanes stay whole: all is a multiple of 4
+  auto load = [&](int i, Raw<E>& x) -> Word {  // the groups of 4 lanes stay whole: all is a multiple of 4
     const Word o = word_of(n, i);
     const Place& at = places[o.token];
     if (at.sub) {
       const E* p = o.is_v ? v + (at.src * c.hkv * n.nv + o.r) * 16 : k + (at.src * n.all_k + o.r) * 16;
-      load8(p, x[0]);
-      load8(p + 8, x[1]);
+      x.load(p);
     } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[0][j] = x[1][j] = 0.f;
+      x.zero();
     }
     return o;
   };
-  float next[2][8];
+  Raw<E> next;
   Word o_next{};
   if (threadIdx.x < all) o_next = load(threadIdx.x, next);
   for (int i = threadIdx.x; i < all; i += kThreads) {
-    float x[2][8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[0][j] = next[0][j], x[1][j] = next[1][j];
+    const Raw<E> raw = next;
     const Word o = o_next;
     if (i + kThreads < all) o_next = load(i + kThreads, next);
     const Place& at = places[o.token];
-    // the group's minimum and maximum over its 4 lanes
-    float lo, hi;
-    range_of(x, lo, hi);
-    const uint32_t lanes = 0xfu << (threadIdx.x & 28);
-#pragma unroll
-    for (int s = 1; s < 4; s <<= 1) {
-      const float l = __shfl_xor_sync(lanes, lo, s), h = __shfl_xor_sync(lanes, hi, s);
-      asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(l));
-      asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(h));
-    }
+    float lo, hi;  // of the group: 4 lanes
+    raw.range(0xfu << (threadIdx.x & 28), lo, hi);
     if (!at.sub) continue;
     __nv_bfloat16 low = __float2bfloat16_rd(lo);
     const float lowf = __bfloat162float(low);
@@ -222,8 +252,12 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Cache c, 
       low = scale = __ushort_as_bfloat16(0x7fff);
     } else if (s > 0.f) {
       const bool plain = s >= 1.2e-38f && hi - lowf < INFINITY;
-      codes[0] = codes_of(x[0], lowf, s, plain);
-      codes[1] = codes_of(x[1], lowf, s, plain);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        float x[8];
+        raw.half(w, x);
+        codes[w] = codes_of(x, lowf, s, plain);
+      }
     }
     uint8_t* sub = at.sub + int64_t(o.head) * f.block();
     const int w0 = 2 * o.word, group = o.word / 4;
@@ -259,39 +293,53 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Cache c, co
   const int here = int(min(int64_t(per_block), tokens - t0));
   if (threadIdx.x < here) places[threadIdx.x] = place_of(c, f, cu, start, nullptr, tokens, t0 + threadIdx.x);
   __syncthreads();
-#pragma unroll 4
-  for (int i = threadIdx.x; i < here * n.words; i += kThreads) {
-    const Word o = word_of(n, i);
-    const Place& at = places[o.token];
-    if (!at.sub) continue;
-    const uint8_t* sub = at.sub + int64_t(o.head) * f.block();
-    const int w0 = 2 * o.word, group = o.word / 4;
+  struct Piece {
     uint32_t codes[2];
     float s, low;
-    E* to;
+    E* to;  // null: nothing to write
+  };
+  const int all = here * n.words;
+  auto load = [&](int i) {
+    Piece x{};
+    if (i >= all) return x;
+    const Word o = word_of(n, i);
+    const Place& at = places[o.token];
+    if (!at.sub) return x;
+    const uint8_t* sub = at.sub + int64_t(o.head) * f.block();
+    const int w0 = 2 * o.word, group = o.word / 4;
     if (o.is_v) {
       const uint32_t* from = reinterpret_cast<const uint32_t*>(sub + f.vc() + at.row * (f.dv / 2));
-      codes[0] = from[f.vword(w0)];
-      codes[1] = from[f.vword(w0 + 1)];
-      s = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sub + f.vs())[at.row * f.gv() + group]);
-      low = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sub + f.vl())[group * kKv4Sub + at.row]);
-      to = v + (at.src * c.hkv * n.nv + o.r) * 16;
+      x.codes[0] = from[f.vword(w0)];
+      x.codes[1] = from[f.vword(w0 + 1)];
+      x.s = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sub + f.vs())[at.row * f.gv() + group]);
+      x.low = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sub + f.vl())[group * kKv4Sub + at.row]);
+      x.to = v + (at.src * c.hkv * n.nv + o.r) * 16;
     } else {
       const uint32_t* from = reinterpret_cast<const uint32_t*>(sub + f.kc() + at.row * (f.dqk / 2));
-      codes[0] = from[f.kword(w0)];
-      codes[1] = from[f.kword(w0 + 1)];
+      x.codes[0] = from[f.kword(w0)];
+      x.codes[1] = from[f.kword(w0 + 1)];
       const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(sub + f.kp()) + at.row * 2 * f.gk() + group;
-      s = __bfloat162float(p[0]);
-      low = __bfloat162float(p[f.gk()]);
-      to = k + (at.src * n.all_k + o.r) * 16;
+      x.s = __bfloat162float(p[0]);
+      x.low = __bfloat162float(p[f.gk()]);
+      x.to = k + (at.src * n.all_k + o.r) * 16;
     }
+    return x;
+  };
+  for (int i = threadIdx.x; i < all; i += kAhead * kThreads) {
+    Piece x[kAhead];  // loads of several in flight
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      float x[8];
+    for (int u = 0; u < kAhead; ++u) x[u] = load(i + u * kThreads);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)  // (a code in the last bits of 2^23 is 2^23 + n)
-        x[j] = fmaf(s, __uint_as_float(((codes[w] >> (4 * j)) & 15u) | 0x4b000000u) - 8388608.f, low);
-      store8(to + 8 * w, x);
+    for (int u = 0; u < kAhead; ++u) {
+      if (!x[u].to) continue;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)  // (a code in the last bits of 2^23 is 2^23 + n)
+          y[j] = fmaf(x[u].s, __uint_as_float(((x[u].codes[w] >> (4 * j)) & 15u) | 0x4b000000u) - 8388608.f, x[u].low);
+        store8(x[u].to + 8 * w, y);
+      }
     }
   }
 }
