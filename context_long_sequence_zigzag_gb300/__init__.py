@@ -451,6 +451,20 @@ _raw_stream = torch._C._cuda_getCurrentRawStream  # (torch.cuda.current_stream b
 _current_device = torch.cuda.current_device
 
 
+def _order_after(on, dev: torch.device) -> None:
+    """Stream `on` waits for the current one: what the allocator handed out
+    there may still be in use by work queued there before.  (Not across a
+    capture, which would drag the other stream into it.)"""
+    with torch.cuda.device(dev):
+        if torch.cuda.is_current_stream_capturing():
+            return
+        current = torch.cuda.current_stream()
+        with torch.cuda.stream(on):
+            if torch.cuda.is_current_stream_capturing():
+                return
+        on.wait_stream(current)
+
+
 def _launch(dev: torch.device, stream, temps, name: str, *args) -> None:
     """Calls a library function with the stream appended, on device dev.
     ``temps`` (buffers allocated here) are kept until that stream is done."""
@@ -460,6 +474,8 @@ def _launch(dev: torch.device, stream, temps, name: str, *args) -> None:
         other = _stream(stream)
         if other != handle:
             on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(other, device=dev)
+            if temps:
+                _order_after(on, dev)
             for x in temps:
                 x.record_stream(on)
             handle = other

@@ -2,38 +2,49 @@
 //
 // Row (b, t, h) sees slots j < lengths[b] - (n_q - 1 - t):
 //   S_j = scale q.K_j,  lse = log sum_j exp(S_j),  o = sum_j exp(S_j - lse) V_j.
-// The cache is read once (144 bytes a token's head of 128 channels) and every
-// byte of it meets G * n_q rows, so the kernel is bound by HBM as long as
-// unpacking keeps up: at 6.7 TB/s an SM gets about 23 bytes a cycle, 46 codes.
+// The cache is read once (144 bytes a token's head of 128 + 128 channels), and
+// every byte meets G * n_q rows.  At 6.7 TB/s an SM gets about 23 bytes a
+// cycle, 46 codes; unpacking them, the MMAs' operands and the scales take more
+// issue slots than that leaves, so the long cases are bound by instruction
+// issue (8 x up to 64K tokens, d 128: 77 us, 59% of issue slots, ALU pipe 53%,
+// 44% of the measured copy rate; 128K tokens, 64 heads, d 192/128: 347 us,
+// 64% and 64%), the short ones by latency (16K tokens: 15 us, and 7 to join).
 //
 // Warp-level MMAs, not tcgen05: with 1 to 16 rows a tcgen05 tile would be
 // nearly empty, and its operands would have to be unpacked into shared or
 // tensor memory first; here a lane's packed words are unpacked in registers
-// straight into the fragments of mma.m16n8k16 (keys or channels on the 16
-// side, rows on the 8 side), which the format's word order was chosen for.
+// straight into the fragments (keys or channels on the 16 side, rows on the 8
+// side), which the format's word order was chosen for.
 //
-// * A code n becomes bf16(16 + n) with one shift and one LOP3 per pair: 16 is
-//   1.0000000b * 2^4, so a code in mantissa bits 3-6 adds n exactly.  The 16s
-//   are taken out again in fp32: of S by starting the accumulators at -16
-//   sum(q), of O by one MMA a group with a constant -16.
-// * Scales and lows act in fp32: on S per (key, group); on P per (token, group)
-//   before P is rounded to the bf16 operand.
+// * K of bf16 caches: a code's nibble in a byte is the e4m3 number n 2^-9, so
+//   one AND (and a shift) makes four operands of mma.m16n8k32.  A query row is
+//   scaled by a power of two to a largest channel of 128 .. 256 and split into
+//   two e4m3 terms: 8 bits, all that bf16 has.  Each product starts from zero
+//   and is added to S by FMAs with the group's scale.  (bf16 operands would
+//   take twice the MMAs and an instruction more for every two codes.)
+// * V, and K of fp32 caches: a code becomes the bf16 number n - 8 (below) for
+//   mma.m16n8k16.  fp32 caches split q and P s into three bf16 terms (24 bits).
+// * Scales and lows act in fp32: on S per (key, group), the lows on sum(q); on
+//   P per (token, group) before P s is rounded to the bf16 operand, the lows
+//   (with 8 steps added) on a sum of their own.
 // * S^T comes out with keys as rows and goes back in as P^T with tokens as
 //   the contracted index: movmatrix transposes the 8 x 8 quarters.
 // * The softmax keeps a reference per row instead of a running maximum: P =
 //   2^(S - ref), and only when an element exceeds the reference by more than
-//   2^10 does the warp reduce a new maximum and rescale.
-// * fp32 caches split q and P s into three bf16 terms (24 bits), more MMAs on
-//   the same unpacked codes.
+//   2^10 does the warp take a new maximum and rescale.
 //
-// Work: every (sequence, kv head, row tile) is a run of sub-blocks of 32
-// tokens; all runs laid end to end are cut evenly over the CTAs (one an SM),
-// whatever the lengths, on the device: a graph replays with other lengths.
-// Inside its share a CTA's warps take sub-blocks in turn, each through its own
-// ring of bulk copies, so nothing but the end of a run is synchronised.  Runs
-// that lie in one CTA are finished there; the others leave partials, which a
-// second kernel joins.  Weights need the final lse, so the raw scores wait in
-// the workspace (they stay in L2) and the second kernel adds them up.
+// Work: every (sequence, kv head, row tile) is a run of units, one for its
+// start (the queries are made operands) and one a sub-block of 32 tokens; all
+// runs laid end to end are cut evenly over the CTAs (one an SM) and their
+// warps, whatever the lengths, on the device: a graph replays with other
+// lengths.  A warp has a ring of copies of its own and waits for nobody.
+// 12 warps (10, 14 and 16 were slower: registers against latency), 8 where two
+// row tiles or three terms need the registers.  What a warp leaves of a run
+// that goes on elsewhere is joined in the CTA first; runs that lie in one CTA
+// are finished there, the others leave partials for kv4_join_kernel.  Weights
+// need the final lse: the scores wait in the workspace (they stay in L2) and
+// kv4_weights_kernel adds them up.  Both are launched while the kernel before
+// them drains.
 #include <algorithm>
 #include <atomic>
 

@@ -550,7 +550,9 @@ cp_status_t cp_set_debug_checks(int32_t on, int32_t* previous);
 /* Synchronises `stream`, then returns and clears the device error word of
  * the current device: *code = 0 when every bounded wait since the last call
  * completed, otherwise a nonzero code naming the wait that ran out (and the
- * status CP_ERR_DEVICE_TIMEOUT). */
+ * status CP_ERR_DEVICE_TIMEOUT).  The checks above and the 4-bit cache's
+ * (0x300 | site: 1 a page outside the pool, 2 a length and 3 a slot outside the
+ * table, 4 a row outside its tensor) report through the same word. */
 cp_status_t cp_device_status(cp_stream_t stream, int32_t* code);
 
 /* Self-check of the bounded-wait machinery: launches one kernel that waits

@@ -22,6 +22,9 @@ Tolerances, derived from the arithmetic (u = 2^-24, the half step of fp32):
 """
 
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -30,6 +33,8 @@ import torch
 import oracle
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 cpa = pytest.importorskip("context_long_sequence_zigzag_gb300")
 
@@ -380,6 +385,93 @@ def test_attn_on_another_stream():
     assert all(torch.equal(a, b) for g in got for a, b in zip(g, ref))
 
 
+def test_buffers_made_for_another_stream_wait_for_their_last_use():
+    """The outputs made here may take memory that work queued on the current stream still writes."""
+    c = Filled([3000], 8, 2, 128, 128, seed=24)
+    q, lens = torch.randn(1, 1, 8, 128, device="cuda").bfloat16(), ints([3000])
+    ref = cpa.cp_kv4_attn(c.cache, q, lens)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        old = torch.empty_like(ref[0])
+        torch.cuda._sleep(20_000_000)  # cycles: some 10 ms
+        old.fill_(7.0)
+        del old
+        got = cpa.cp_kv4_attn(c.cache, q, lens, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+def test_attn_many_rows():
+    """2048 rows of a kv head: 128 passes (256 in fp32)."""
+    check_attn(Filled([70, 9], 256, 2, 64, 64, seed=25), n_q=16)
+    check_attn(Filled([70, 9], 256, 2, 64, 64, seed=25, dtype=torch.float32), n_q=16)
+
+
+def test_first_calls_are_captured():
+    """Nothing has to run once before a capture: a process whose first calls are captured."""
+    code = """
+import torch, context_long_sequence_zigzag_gb300 as cpa
+n = cpa.cp_kv4_block_bytes(128, 128)
+ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+make = lambda t: cpa.Kv4Cache(torch.zeros(4, 2, n, dtype=torch.uint8, device="cuda"), ints(t), 4, 2, 128, 128,
+                              torch.zeros(4, 2, 64, device="cuda"))
+a, b = make([[2, 0]]), make([[1]])
+k, v, q = (torch.randn(100, 2, 128, device="cuda").bfloat16() for _ in range(3))
+cu, start, lens = ints([0, 100]), ints([0]), ints([100])
+q = q.view(-1)[:512].view(1, 1, 4, 128)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    cpa.cp_kv4_append(a, k, v, cu, start)
+    o, lse = cpa.cp_kv4_attn(a, q, lens, accumulate=True)
+    new, kept = cpa.cp_kv4_evict(a, lens, 64, 8, b)
+g.replay()
+torch.cuda.synchronize()
+assert abs(float(a.weights.sum()) - 4) < 1e-4 and new.tolist() == [64] and int((kept >= 0).sum()) == 128
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=240)
+    assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_decode_step_in_a_graph():
+    """Append, attention with weights, eviction and read in one graph, replayed with other lengths and values."""
+    B, hkv, d = 3, 2, 64
+
+    def caches():
+        c = Filled([150, 64, 20], 4, hkv, d, d, seed=26)
+        ids = torch.arange(B * 2, dtype=torch.int32, device="cuda").view(B, 2)
+        block = cpa.cp_kv4_block_bytes(d, d)
+        return c, cpa.Kv4Cache(torch.zeros(B * 2, hkv, block, dtype=torch.uint8, device="cuda"), ids, 4, hkv, d, d,
+                               torch.zeros(B * 2, hkv, 64, device="cuda"))
+
+    (c1, to1), (c2, to2) = caches(), caches()
+    k, v, q = (torch.randn(B, 1, h, d, device="cuda").bfloat16() for h in (hkv, hkv, 4))
+    cu, start, lens = ints([0, 1, 2, 3]), ints([149, 62, 18]), ints([150, 63, 19])
+    cu_read, zeros = ints([0, 40, 80, 120]), ints([0, 0, 0])
+
+    def step(c, to):
+        cpa.cp_kv4_append(c.cache, k.view(B, hkv, d), v.view(B, hkv, d), cu, start)
+        o, lse = cpa.cp_kv4_attn(c.cache, q, lens, accumulate=True)
+        new, kept = cpa.cp_kv4_evict(c.cache, lens, 100, 10, to)
+        rk, rv = cpa.cp_kv4_read(to, cu_read, zeros, 120)
+        return o, lse, new, kept, rk, rv
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(c1, to1)
+    for n in ([150, 63, 19], [100, 64, 20], [128, 1, 2]):
+        lens.copy_(ints(n))
+        start.copy_(ints([x - 1 for x in n]))
+        k.normal_(), v.normal_(), q.normal_()
+        graph.replay()
+        want = step(c2, to2)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.equal(c1.pages, c2.pages) and torch.equal(c1.weights, c2.weights)
+        assert torch.equal(to1.pages, to2.pages) and torch.equal(to1.weights, to2.weights)
+
+
 def test_attn_shared_prefix_pages():
     """Two sequences over the same page: both add to its weights."""
     c = Filled([64, 64], 4, 2, 128, 128, seed=16)
@@ -588,6 +680,23 @@ def test_evict_ties_and_special_weights(kind):
 
 def test_evict_long():
     check_evict(Filled([50000, 4097, 40], 2, 2, 64, 64, seed=34), 4096, 512)
+
+
+def test_evict_rows_longer_than_shared_memory():
+    """450,000 slots a row: their keys are read again in every pass."""
+    n, budget, recent = 450_000, 1000, 100
+    pages = -(-n // 64)
+    rng = np.random.RandomState(36)
+    table, w = rng.permutation(pages), rng.rand(pages, 1, 64).astype(np.float32)
+    block = cpa.cp_kv4_block_bytes(64, 64)
+    blank = lambda m: torch.zeros(m, 1, block, dtype=torch.uint8, device="cuda")  # noqa: E731
+    c = cpa.Kv4Cache(blank(pages), ints([table.tolist()]), 1, 1, 64, 64, torch.from_numpy(w).cuda())
+    to = cpa.Kv4Cache(blank(16), ints([list(range(16))]), 1, 1, 64, 64, torch.zeros(16, 1, 64, device="cuda"))
+    new, kept = cpa.cp_kv4_evict(c, ints([n]), budget, recent, to)
+    held = w[table].reshape(-1)[:n]
+    want = oracle.kv4_keep(held.tolist(), n, budget, recent)
+    assert new.tolist() == [budget] and kept[0, 0].tolist() == want
+    assert np.array_equal(to.weights.cpu().numpy().reshape(-1)[:budget], held[want])
 
 
 def test_evict_within_one_pool():
