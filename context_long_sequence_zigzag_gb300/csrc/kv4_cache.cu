@@ -357,6 +357,7 @@ constexpr int kSelThreads = 1024;
 constexpr int kDigits = 2048;      // bins of an 11-bit digit
 constexpr int kSelKeys = 49152;    // keys that a CTA keeps in shared memory
 constexpr int kSelParts = 8;        // CTAs of a row at most
+constexpr int kSelAhead = 8;        // weights a thread has on their way
 constexpr int kSelSlice = 8192;    // slots a CTA takes at least where a row gets several
 
 // Sum of x over the threads before this one; *all gets the sum over all.
@@ -393,7 +394,7 @@ __device__ __forceinline__ T block_before(T x, T* scratch, T* all) {
 // Bound by the latency of its barriers and loads, so: counts of their own for
 // each pass, the first taken while the keys are loaded, and the block's
 // barrier where a row has one CTA.
-__global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4Cache c, const int32_t* lengths,
+__global__ void __launch_bounds__(kSelThreads, 2) kv4_select_kernel(const Kv4Cache c, const int32_t* lengths,
                                                                  int32_t budget, int32_t recent, int32_t* new_lengths,
                                                                  int32_t* kept, int most_keys) {
   extern __shared__ uint32_t keys[];
@@ -434,11 +435,34 @@ __global__ void __launch_bounds__(kSelThreads) kv4_select_kernel(const Kv4Cache 
   auto key_at = [&](int j) -> uint32_t { return held ? keys[j] : weight_key(lo + j); };
   for (int i = tid; i < 3 * kDigits; i += kSelThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
-#pragma unroll 8
-  for (int j = tid; j < count; j += kSelThreads) {
-    const uint32_t key = weight_key(lo + j);
-    if (held) keys[j] = key;
-    atomicAdd(&hist[0][key >> 21], 1);
+  for (int j0 = tid; j0 < count; j0 += kSelAhead * kSelThreads) {  // all pages, then all weights: two waits
+    int32_t page[kSelAhead];
+    uint32_t key[kSelAhead];
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < kSelAhead; ++u) {
+      const int j = j0 + u * kSelThreads;
+      page[u] = j < count ? __ldg(c.table + int64_t(b) * c.max_pages + (lo + j) / CP_KV4_PAGE) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kSelAhead; ++u) {
+      const int j = j0 + u * kSelThreads;
+      key[u] = 0;
+      if (j < count) {
+        if (page[u] >= 0 && page[u] < c.num_pages)
+          key[u] = rank_key(__ldg(c.weights + (int64_t(page[u]) * c.hkv + h) * CP_KV4_PAGE + (lo + j) % CP_KV4_PAGE));
+        else
+          bad = true;
+      }
+    }
+    if (bad) kv4_error(c, kKv4Page);
+#pragma unroll
+    for (int u = 0; u < kSelAhead; ++u) {
+      const int j = j0 + u * kSelThreads;
+      if (j >= count) break;
+      if (held) keys[j] = key[u];
+      atomicAdd(&hist[0][key[u] >> 21], 1);
+    }
   }
   uint32_t prefix = 0, known = 0;  // known: the bits of it that are found
 #pragma unroll 1
@@ -540,11 +564,22 @@ __global__ void __launch_bounds__(kThreads) kv4_move_kernel(const Kv4Cache c, co
   auto move_rows = [&](int off, int bytes, auto unit_) {
     using T = decltype(unit_);
     const int per = bytes / int(sizeof(T));
-    for (int i = lane; i < kKv4Sub * per; i += 32) {  // kKv4Sub * per is a multiple of 32: the warp stays whole
-      const int t = i / per, e = i - t * per;
-      int r;
-      const uint8_t* s = from(t, &r);
-      if (s) reinterpret_cast<T*>(dst + off)[i] = __ldg(reinterpret_cast<const T*>(s + off) + r * per + e);
+    constexpr int kAtOnce = 4;
+    for (int i0 = 0; i0 < kKv4Sub * per; i0 += 32 * kAtOnce) {  // kKv4Sub * per is a multiple of 32: the warp stays whole
+      T x[kAtOnce];
+      bool have[kAtOnce] = {};
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (i0 + 32 * u >= kKv4Sub * per) break;
+        const int i = i0 + 32 * u + lane, t = i / per, e = i - t * per;
+        int r;
+        const uint8_t* s = from(t, &r);
+        have[u] = s != nullptr;
+        if (have[u]) x[u] = __ldg(reinterpret_cast<const T*>(s + off) + r * per + e);
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+        if (have[u]) reinterpret_cast<T*>(dst + off)[i0 + 32 * u + lane] = x[u];
     }
   };
   move_rows(f.kc(), f.dqk / 2, uint4{});
