@@ -615,7 +615,8 @@ def cp_kv4_append(cache: Kv4Cache, k, v, cu, start, w=None, rows=None, stream=No
 
 def cp_kv4_read(cache: Kv4Cache, cu, start, tokens: int, k=None, v=None, stream=None):
     """Slots start[b], start[b] + 1, ... of every sequence b as rows cu[b] .. cu[b + 1] - 1 of
-    k [tokens, hkv, d_qk] and v [tokens, hkv, d_v]."""
+    k [tokens, hkv, d_qk] and v [tokens, hkv, d_v].  Other rows (from cu[B] on, or of slots outside the cache) are not
+    written: pass k and v where those should hold something."""
     dev, dtype, B = cache.device, cache.torch_dtype, cache.num_seqs
     temps = []
     shape = (tokens, cache.hkv, cache.d_qk)
