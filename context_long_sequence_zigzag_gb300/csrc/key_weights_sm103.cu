@@ -5,7 +5,7 @@
 //             exp(scale q_i.k_j - lse_i)
 // which is a column sum of the attention probabilities, rebuilt from the
 // forward's lse as the backward rebuilds them ("Ulysses与Ring-Attention详解"
-// §4.3).  The key-major walk is the dK/dV kernel's: one CTA owns a 128-key
+// §4.3).  The key-major walk is the dK/dV kernel's: one CTA owns a key
 // tile of one kv head and visits, for every query head of the group, the
 // query runs that see it.  With S^T = K Q^T a thread holds a whole key row
 // (TMEM lane = key), so its column sum is a sum over its own registers: no
@@ -22,7 +22,8 @@
 // warps that takes its tiles in turn, so that one group's loads and waits overlap the others'
 // exponentials (two groups: 1.10 ms; a part of the exponentials as polynomials
 // on the FMA pipes instead: 1.09 ms and up, the issue slots are needed
-// elsewhere).
+// elsewhere).  As it stands 16K tokens of 32 / 8 heads take 0.89 ms, 1.2
+// PFLOP/s over the visible pairs.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -395,7 +396,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
 // Persistent: the (kv head, key tile) items are cut evenly over the SMs, in
 // order, so a CTA gathers queries once or twice.  S has two TMEM buffers, each
 // read by eight compute warps, four a half of the columns (with four warps a
-// buffer a tile took 4500 cycles: too few warps to hide their latencies).
+// buffer a tile took 4500 cycles: too few warps to hide their latencies).  The
+// case above takes 41 us, 3.3 TB/s.
 
 constexpr int kWinCols = 256;
 constexpr int kWinThreads = 4 * kGroupThreads + 64;
@@ -586,8 +588,8 @@ __global__ void __launch_bounds__(kWinThreads, 1) key_weights_window_kernel(cons
               w += a0 + a1;
             }
           };
-          // (columns from cols on in the last 32 are stale numbers where N is no multiple of 32: masked too)
-          if (need_mask || N % 32) sums(std::true_type{});
+          // (columns from cols on are products with zeros, NaN where a key is infinite, and from N on stale: masked too)
+          if (need_mask || cols % 32) sums(std::true_type{});
           else sums(std::false_type{});
           ptx::tc_fence_before();
           __syncwarp();

@@ -785,6 +785,21 @@ def test_key_weights_excluded_queries_and_debug_checks():
     assert (a.sum() - 100).abs() < 1e-3  # 2 heads, 50 queries
 
 
+@pytest.mark.parametrize("last", [None, 20, 16])
+def test_key_weights_infinite_key(last):
+    """A key of -inf under positive queries has scores of -inf: weight 0, and no other key changes."""
+    T, cu = 300, [0, 300]
+    q, k = torch.rand(T, 2, 128).bfloat16() + 0.5, torch.randn(T, 2, 128).bfloat16()
+    k[37] = -math.inf
+    lse = oracle.attn_forward(f64(q), f64(k), np.zeros((T, 2, 8)), cu, 128 ** -0.5)[1]
+    want = oracle.attn_key_weights(f64(q), f64(k), lse, cu, 128 ** -0.5, True, last)
+    prob = cpa.Problem(T, 2, 2, 128, 64, 1, "contiguous", cu)
+    w = f64(cpa.cp_attn_key_weights(prob, q.cuda(), k.cuda(), torch.from_numpy(lse).float().cuda(), last=last))
+    assert (w[:, 37] == 0).all() and (want[:, 37] == 0).all()
+    # (check_key_weights' bound with |q| <= 1.5, |k| < 5, |lse| < 7: 2^-23 (8 * 85 + 64 + 28) = 9.2e-5)
+    assert np.all(np.abs(w - want) <= 1e-4 * want + 1e-30)
+
+
 # ---------------------------------------------------------------- together
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_prompt_then_decode_with_eviction(dtype):
