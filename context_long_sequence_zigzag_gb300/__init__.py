@@ -473,7 +473,10 @@ def _launch(dev: torch.device, stream, temps, name: str, *args) -> None:
     if stream is not None:
         other = _stream(stream)
         if other != handle:
-            on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(other, device=dev)
+            if isinstance(stream, torch.cuda.Stream):
+                on = stream
+            else:  # (handle 0, the default stream, would make ExternalStream a stream of the pool)
+                on = torch.cuda.ExternalStream(other, device=dev) if other else torch.cuda.default_stream(dev)
             if temps:
                 _order_after(on, dev)
             for x in temps:

@@ -402,6 +402,22 @@ def test_buffers_made_for_another_stream_wait_for_their_last_use():
         assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
 
 
+def test_default_stream_by_its_handle():
+    c = Filled([3000], 8, 2, 128, 128, seed=24)
+    q, lens = torch.randn(1, 1, 8, 128, device="cuda").bfloat16(), ints([3000])
+    ref = cpa.cp_kv4_attn(c.cache, q, lens)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        old = torch.empty_like(ref[0])
+        torch.cuda._sleep(20_000_000)
+        old.fill_(7.0)
+        del old
+        got = cpa.cp_kv4_attn(c.cache, q, lens, stream=0)  # on the default stream, after what this one holds
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
 def test_attn_many_rows():
     """2048 rows of a kv head: 128 passes (256 in fp32)."""
     check_attn(Filled([70, 9], 256, 2, 64, 64, seed=25), n_q=16)
