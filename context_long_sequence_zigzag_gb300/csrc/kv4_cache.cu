@@ -13,12 +13,13 @@
 #include <cooperative_groups.h>
 
 #include "kv4.cuh"
+#include "kv4_words.h"
 #include "sm103_ptx.cuh"
 
 namespace cpattn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kKv4Threads;
 
 // 16 channels as they lie in memory
 template <typename E>
@@ -182,29 +183,6 @@ __device__ __forceinline__ Place place_of(const Kv4Cache& c, const Kv4Format& f,
   return at;
 }
 
-// What piece i (16 channels, two words) of a CTA's tokens is: of which token, k or v, head, piece.  The
-// divisions are products with rounded-up reciprocals (exact while i times the
-// divisor stays below 2^32, which the launch sees to).
-struct Words {
-  int nk, nv, words, all_k;  // pieces of a head's k, of its v, of a token, of all its k
-  uint32_t by_words, by_nk, by_nv;
-};
-struct Word {
-  int token, r, head, word;  // r: piece of all heads' k, or of all their v
-  bool is_v;
-};
-__device__ __forceinline__ Word word_of(const Words& n, int i) {
-  Word x;
-  x.token = int(n.words == 1 ? uint32_t(i) : __umulhi(uint32_t(i), n.by_words));
-  x.r = i - x.token * n.words;
-  x.is_v = x.r >= n.all_k;
-  if (x.is_v) x.r -= n.all_k;
-  x.head = int(__umulhi(uint32_t(x.r), x.is_v ? n.by_nv : n.by_nk));
-  x.word = x.r - x.head * (x.is_v ? n.nv : n.nk);
-  return x;
-}
-
-constexpr int kMostTokens = 32;  // of a CTA
 constexpr int kAhead = 2;        // pieces a thread of read loads before it writes (64K tokens: 65 us; 1: 75, 3: 73)
 
 // CTAs an SM: as many as leave the registers their place (64K tokens of bf16, 8 heads of 128 + 128: 96 us with 4, 135 with
@@ -214,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 ? 4 : 3) kv4_append_k
                                                               const E* v, const float* w, int64_t src_rows,
                                                               const int32_t* rows, const int32_t* cu,
                                                               const int32_t* start, int64_t tokens, int per_block) {
-  __shared__ Place places[kMostTokens];
+  __shared__ Place places[kKv4MostTokens];
   const int64_t t0 = int64_t(blockIdx.x) * per_block;
   const int here = int(min(int64_t(per_block), tokens - t0));
   if (threadIdx.x < here) places[threadIdx.x] = place_of(c, f, cu, start, rows, src_rows, t0 + threadIdx.x);
@@ -288,7 +266,7 @@ template <typename E>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Cache c, const Kv4Format f, const Words n,
                                                             const int32_t* cu, const int32_t* start, int64_t tokens,
                                                             E* k, E* v, int per_block) {
-  __shared__ Place places[kMostTokens];
+  __shared__ Place places[kKv4MostTokens];
   const int64_t t0 = int64_t(blockIdx.x) * per_block;
   const int here = int(min(int64_t(per_block), tokens - t0));
   if (threadIdx.x < here) places[threadIdx.x] = place_of(c, f, cu, start, nullptr, tokens, t0 + threadIdx.x);
@@ -594,32 +572,11 @@ __global__ void __launch_bounds__(kThreads) kv4_move_kernel(const Kv4Cache c, co
 
 }  // namespace
 
-// Tokens a CTA of append or read takes: several words a thread once every SM
-// has CTAs enough, whole tokens in any case.
-static int tokens_per_block(int words, int64_t tokens) {
-  const int64_t fill = (kThreads + words - 1) / words;                 // a word a thread
-  const int64_t many = tokens / (int64_t(kv4_sm_count()) * 8);          // 8 CTAs an SM
-  return int(std::min<int64_t>(kMostTokens, std::max<int64_t>(std::max<int64_t>(1, kThreads / words), std::min(many, fill * 16))));
-}
-
-static Words words_of(const Kv4Cache& c, int dqk, int dv) {
-  Words n;
-  n.nk = dqk / 16;
-  n.nv = dv / 16;
-  n.all_k = c.hkv * n.nk;
-  n.words = c.hkv * (n.nk + n.nv);
-  auto inverse = [](int d) { return uint32_t(((uint64_t(1) << 32) + d - 1) / d); };
-  n.by_words = inverse(n.words);
-  n.by_nk = inverse(n.nk);
-  n.by_nv = inverse(n.nv);
-  return n;
-}
-
 cudaError_t launch_kv4_append(const Kv4Cache& c, int dqk, int dv, int dtype, const void* k, const void* v,
                               const float* w, int64_t src_rows, const int32_t* rows, const int32_t* cu,
                               const int32_t* start, int64_t tokens, cudaStream_t st) {
-  const Words n = words_of(c, dqk, dv);
-  const int per = tokens_per_block(n.words, tokens);
+  const Words n = words_of(c.hkv, dqk, dv);
+  const int per = kv4_tokens_per_block(n.words, tokens, kv4_sm_count());
   const unsigned grid = unsigned((tokens + per - 1) / per);
   if (dtype == CP_DT_BF16)
     kv4_append_kernel<<<grid, kThreads, 0, st>>>(c, Kv4Format(dqk, dv), n, static_cast<const __nv_bfloat16*>(k),
@@ -634,8 +591,8 @@ cudaError_t launch_kv4_append(const Kv4Cache& c, int dqk, int dv, int dtype, con
 
 cudaError_t launch_kv4_read(const Kv4Cache& c, int dqk, int dv, int dtype, const int32_t* cu, const int32_t* start,
                             int64_t tokens, void* k, void* v, cudaStream_t st) {
-  const Words n = words_of(c, dqk, dv);
-  const int per = tokens_per_block(n.words, tokens);
+  const Words n = words_of(c.hkv, dqk, dv);
+  const int per = kv4_tokens_per_block(n.words, tokens, kv4_sm_count());
   const unsigned grid = unsigned((tokens + per - 1) / per);
   if (dtype == CP_DT_BF16)
     kv4_read_kernel<<<grid, kThreads, 0, st>>>(c, Kv4Format(dqk, dv), n, cu, start, tokens,

@@ -1,0 +1,51 @@
+"""The 4-bit cache and the key weights at the limits of what their calls
+accept: the widest caches, queries and keys that are not numbers, rows that see
+nothing, pages that are not there."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+cpa = pytest.importorskip("context_long_sequence_zigzag_gb300")
+
+
+@pytest.fixture(autouse=True)
+def _need_cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    yield
+    assert cpa.cp_device_status() == 0
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def test_append_and_read_of_the_widest_cache():
+    """1024 heads of 192 + 128, more tokens than an SM's CTAs hold one each: one call gives what many short ones give."""
+    hkv, d_qk, d_v, n, chunk = 1024, 192, 128, 12800, 512
+    pages = n // 64
+    torch.manual_seed(60)
+    k, v = (torch.randn(n, hkv, d, device="cuda", dtype=torch.bfloat16) for d in (d_qk, d_v))
+    table = ints([torch.randperm(pages).tolist()])
+    make = lambda: cpa.Kv4Cache(torch.zeros(pages, hkv, cpa.cp_kv4_block_bytes(d_qk, d_v), dtype=torch.uint8,  # noqa: E731
+                                            device="cuda"), table, hkv, hkv, d_qk, d_v)
+    whole, pieces = make(), make()
+    cpa.cp_kv4_append(whole, k, v, ints([0, n]), ints([0]))
+    for i in range(0, n, chunk):
+        cpa.cp_kv4_append(pieces, k[i:i + chunk], v[i:i + chunk], ints([0, chunk]), ints([i]))
+    assert torch.equal(whole.pages, pieces.pages)
+    rk, rv = cpa.cp_kv4_read(whole, ints([0, n]), ints([0]), n)
+    for i in range(0, n, chunk):
+        ck, cv = cpa.cp_kv4_read(pieces, ints([0, chunk]), ints([i]), chunk)
+        assert torch.equal(rk[i:i + chunk], ck) and torch.equal(rv[i:i + chunk], cv)
+    # a group's range is below 14, its step below 0.94: half of it, 15 roundings of the scale (2^-8), the value's own (2^-8
+    # of 7) and the difference's: 0.94 (0.5 + 15 / 256) + 0.03 + 0.01 < 0.6
+    assert (rk - k).abs().max() <= 0.6 and (rv - v).abs().max() <= 0.6
+    torch.cuda.empty_cache()
