@@ -513,7 +513,8 @@ __global__ void __launch_bounds__(kThreads) kv4_move_kernel(const Kv4Cache c, co
   if (unit >= int64_t(subs) * c.num_seqs * c.hkv) return;
   const int64_t bh = unit / subs;
   const int u = int(unit - bh * subs), b = int(bh / c.hkv), h = int(bh - int64_t(b) * c.hkv);
-  const int n = __ldg(new_lengths + b), first = u * kKv4Sub;
+  // plain loads of what the selection writes: __ldg is only for data that nothing writes while the kernel lives
+  const int n = min(new_lengths[b], budget), first = u * kKv4Sub;
   if (first >= n) return;
   const int dst_page = kv4_page(to, b, first / CP_KV4_PAGE);
   if (dst_page < 0) return;
@@ -523,8 +524,10 @@ __global__ void __launch_bounds__(kThreads) kv4_move_kernel(const Kv4Cache c, co
   const uint8_t* src = nullptr;
   int row = 0;
   if (first + lane < n) {
-    const int j = __ldg(kept + bh * budget + first + lane);
-    const int page = kv4_page(c, b, j / CP_KV4_PAGE);
+    const int j = kept[bh * budget + first + lane];
+    const bool held = j >= 0 && j < c.max_pages * CP_KV4_PAGE;  // (a slot of the table)
+    if (!held) kv4_error(c, kKv4Slot);
+    const int page = held ? kv4_page(c, b, j / CP_KV4_PAGE) : -1;
     if (page >= 0) {
       const int64_t block = int64_t(page) * c.hkv + h;
       src = c.pages + block * f.block() + (j % CP_KV4_PAGE) / kKv4Sub * f.sub();

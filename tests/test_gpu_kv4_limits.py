@@ -49,3 +49,47 @@ def test_append_and_read_of_the_widest_cache():
     # of 7) and the difference's: 0.94 (0.5 + 15 / 256) + 0.03 + 0.01 < 0.6
     assert (rk - k).abs().max() <= 0.6 and (rv - v).abs().max() <= 0.6
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_evictions_in_a_row_through_the_same_buffers(graph):
+    """The move starts while the selection runs: it has to see this call's kept slots and lengths, not the last call's,
+    which lie in the same buffers."""
+    B, hkv, d, budget, recent, slots = 8, 4, 64, 200, 16, 1024
+    pages, need = B * slots // 64, -(-budget // 64)
+    torch.manual_seed(61)
+    block = cpa.cp_kv4_block_bytes(d, d)
+    table = torch.randperm(pages, device="cuda").int().view(B, -1)
+    weights = torch.rand(pages, hkv, 64, device="cuda")
+    full = cpa.Kv4Cache(torch.randint(0, 256, (pages, hkv, block), dtype=torch.uint8, device="cuda"), table, hkv, hkv, d, d,
+                        weights)
+    small = cpa.Kv4Cache(torch.zeros(B * need, hkv, block, dtype=torch.uint8, device="cuda"),
+                         torch.arange(B * need, device="cuda").int().view(B, need), hkv, hkv, d, d,
+                         torch.zeros(B * need, hkv, 64, device="cuda"))
+    lens, new, kept = ints([0] * B), ints([0] * B), torch.zeros(B, hkv, budget, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            cpa.cp_kv4_evict(full, lens, budget, recent, small, new_lengths=new, kept=kept)
+    for i in range(30):
+        n = torch.randint(0, slots + 1, (B,)).int()
+        lens.copy_(n)
+        weights.uniform_()
+        small.weights.fill_(-1.0)
+        new.fill_(-1), kept.fill_(-1)
+        if graph:
+            g.replay()
+        else:
+            cpa.cp_kv4_evict(full, lens, budget, recent, small, new_lengths=new, kept=kept)
+        want_n = n.clamp(max=budget)
+        assert torch.equal(new.cpu(), want_n)
+        held = weights[table.long()].transpose(1, 2).flatten(2)  # [B, hkv, slots]
+        moved = small.weights.view(B, need, hkv, 64).transpose(1, 2).flatten(2)[..., :budget]
+        behind = torch.arange(budget, device="cuda").view(1, 1, -1) >= want_n.cuda().view(-1, 1, 1)
+        assert torch.equal(kept < 0, behind.expand_as(kept))
+        assert torch.equal(moved, held.gather(2, kept.clamp(min=0).long()).masked_fill(behind, -1.0))
+        for b in (0, B - 1):
+            for h in range(hkv):
+                keep = oracle.kv4_keep(held[b, h, :int(n[b])].tolist(), int(n[b]), budget, recent)
+                assert kept[b, h, :len(keep)].tolist() == keep
