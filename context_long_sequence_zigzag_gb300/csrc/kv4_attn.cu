@@ -47,6 +47,7 @@
 // them drains.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include <cuda_fp8.h>
 
@@ -405,7 +406,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
         const int k = big < 0x00800000u ? 0 : 134 - int(min(big, 0x7f800000u) >> 23);  // 7 - exponent
         unit = __uint_as_float(uint32_t(127 + max(min(k, 126), -126)) << 23);
         // codes are n 2^-9 as e4m3 bytes: scores come out times unit / 512
-        factor = big >= 0x7f800000u ? NAN : factor * (512.f / unit);
+        // (above 0 and finite, whatever the row holds: an unseen slot's score is -inf times it)
+        factor = fmaxf(factor * 512.f / unit, 1e-45f);
+        if (big >= 0x7f800000u) {  // a row with a NaN or an infinity: NaN in what every key's score adds up
+          factor = 1.f;
+          gs[0] = NAN;
+        }
 #pragma unroll
         for (int j = 0; j < DQK / 32; ++j) {
           float hi[8], lo[8];
@@ -966,7 +972,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4AttnArg
 // Adds up the weights: a warp takes consecutive sub-blocks, of a kv head at a
 // time, a lane a token.  The scores come from L2, the lse from the kernels
 // before; every slot gets one sum a row tile, in order.
-__global__ void __launch_bounds__(kJoinThreads) kv4_weights_kernel(const Kv4AttnArgs a, const Grid gr) {
+__global__ void __launch_bounds__(kJoinThreads, 5) kv4_weights_kernel(const Kv4AttnArgs a, const Grid gr) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int32_t s_scan[kJoinThreads / 32];
   int32_t* base = reinterpret_cast<int32_t*>(smem);
@@ -998,6 +1004,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_weights_kernel(const Kv4Attn
         ls = a.lse[int64_t(head) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] * kLog2e;
       }
       if (ls == -INFINITY) ls = INFINITY;  // a row that sees nothing gives nothing
+      const bool any_nan = __any_sync(0xffffffffu, ls != ls);
       for (int i = i0; i < i1; i += 4) {
         float add[4] = {0.f, 0.f, 0.f, 0.f};
         int page[4];
@@ -1005,13 +1012,21 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_weights_kernel(const Kv4Attn
         for (int k = 0; k < 4; ++k)
           page[k] = __ldg(a.c.table + int64_t(b) * a.c.max_pages + min(i + k, i1 - 1) / (CP_KV4_PAGE / kKv4Sub));
         const float* sc = gr.score + int64_t(run0 + 1 + i) * gr.rows_per_tile * kKv4Sub + lane;
+        auto add_rows = [&](auto nan_) {
 #pragma unroll 4
-        for (int n = 0; n < rows; ++n) {
-          const float lsn = __shfl_sync(0xffffffffu, ls, n);
+          for (int n = 0; n < rows; ++n) {
+            const float lsn = __shfl_sync(0xffffffffu, ls, n);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (i + k < i1) add[k] += ptx::ex2(sc[(k * gr.rows_per_tile + n) * kKv4Sub] - lsn);
-        }
+            for (int k = 0; k < 4; ++k)
+              if (i + k < i1) {
+                const float x = sc[(k * gr.rows_per_tile + n) * kKv4Sub];
+                if (!decltype(nan_)::value || x != -INFINITY) add[k] += ptx::ex2(x - lsn);
+              }
+          }
+        };
+        // a row whose lse is NaN gives the slots that it does not see nothing all the same
+        if (any_nan) add_rows(std::true_type{});
+        else add_rows(std::false_type{});
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int slot = (i + k) * kKv4Sub + lane;

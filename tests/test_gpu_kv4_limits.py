@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import oracle
+from test_gpu_kv4 import Filled, check_attn, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -21,10 +22,6 @@ def _need_cuda():
         pytest.skip("no CUDA device")
     yield
     assert cpa.cp_device_status() == 0
-
-
-def ints(x):
-    return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
 def test_append_and_read_of_the_widest_cache():
@@ -93,3 +90,52 @@ def test_evictions_in_a_row_through_the_same_buffers(graph):
             for h in range(hkv):
                 keep = oracle.kv4_keep(held[b, h, :int(n[b])].tolist(), int(n[b]), budget, recent)
                 assert kept[b, h, :len(keep)].tolist() == keep
+
+
+# (9 to 16 rows of a kv head in bf16 take two column tiles, cuts of the long sequence meet in the second kernel; the
+# scores are small, so that no row's rescaling depends on the others' values)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (4, 2), (6, 2)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_attn_queries_that_are_no_numbers_stay_in_what_they_see(dtype, hq, hkv, bad):
+    """Rows that see nothing give o = 0 and lse = -inf whatever they hold; a row of NaN is NaN, and so are the weights of
+    the slots that it sees; nothing else changes."""
+    n_q, lengths = 5, [3, 70, 20000, 0, 96]
+    rng = np.random.RandomState(70)
+    q = torch.from_numpy(rng.randn(5, n_q, hq, 128).astype(np.float32)).to(dtype).cuda()
+    nan_rows = [(0, 0), (0, 1), (1, 0), (2, 1), (3, 2), (4, 4)]  # (sequence, query)
+    runs = []
+    for value in (0.0, bad):
+        c = Filled(lengths, hq, hkv, 128, 128, dtype, seed=71, scale=0.002)
+        x = q.clone()
+        for b, t in nan_rows:
+            x[b, t, :, 7] = value
+        o, lse = cpa.cp_kv4_attn(c.cache, x, ints(lengths), accumulate=True)
+        plain = cpa.cp_kv4_attn(c.cache, x, ints(lengths))
+        assert torch.equal(o.nan_to_num(9.0), plain[0].nan_to_num(9.0))
+        assert torch.equal(lse.nan_to_num(9.0), plain[1].nan_to_num(9.0))
+        runs.append((o, lse.view(hq, 5, n_q), c.weights.cpu()))
+    (o0, lse0, w0), (o, lse, w) = runs
+    for b, n in enumerate(lengths):
+        seen = [max(0, n - (n_q - 1 - t)) for t in range(n_q)]
+        first = 0  # slots from here on are seen by no row of NaN
+        for t in range(n_q):
+            if seen[t] == 0:
+                assert not o[b, t].any() and torch.isneginf(lse[:, b, t]).all()
+            elif (b, t) in nan_rows:
+                assert torch.isnan(o[b, t]).all() and torch.isnan(lse[:, b, t]).all()
+                first = max(first, seen[t])
+            else:
+                assert torch.equal(o[b, t], o0[b, t]) and torch.equal(lse[:, b, t], lse0[:, b, t])
+        ids = c.table[b, :-(-n // 64)]
+        flat = [x[ids].transpose(0, 1).reshape(hkv, -1) for x in (w, w0)]
+        assert torch.isnan(flat[0][:, :first]).all() and torch.equal(flat[0][:, first:], flat[1][:, first:])
+    assert not torch.isnan(w0).any() and not torch.isnan(o0).any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_attn_scores_of_next_to_nothing(dtype):
+    """Queries near the smallest numbers and a scale near none: uniform weights, and unseen slots stay unseen."""
+    c = Filled([1, 40, 300], 4, 2, 128, 128, dtype, seed=72, scale=1e-12)
+    q = (torch.randn(3, 3, 4, 128, generator=torch.Generator().manual_seed(73)) * 1e-37).to(dtype).cuda()
+    check_attn(c, n_q=3, q=q)
