@@ -216,10 +216,14 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t (&t)[TERMS
 __device__ __forceinline__ uint32_t e4m3_pair(float x, float y) {  // x in the low byte
   return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
 }
-// x to four significant bits, and what is left (Dekker's splitting: both exact)
+// x (|x| < 256) as the e4m3 number next to it, and what is left: four significant bits (Dekker's splitting), then a
+// multiple of 2^-9, e4m3's smallest step, which what has four bits above 2^-6 is already. Both differences are exact, so
+// that the second term makes up for all that the first one's rounding left: off by 2^-10 at most, and only where x has
+// bits below 2^-9.
 __device__ __forceinline__ void split4(float x, float& high, float& rest) {
   const float t = __fmul_rn(x, 1048577.f);  // 2^20 + 1
   high = __fsub_rn(t, __fsub_rn(t, x));
+  high = __fsub_rn(__fadd_rn(high, 24576.f), 24576.f);  // 1.5 2^14: its last bit is 2^-9
   rest = __fsub_rn(x, high);
 }
 

@@ -461,9 +461,10 @@ cp_status_t cp_kv4_read(const cp_kv4_t* cache, const int32_t* cu, const int32_t*
  *   workspace  : cp_kv4_workspace_size bytes
  * Queries, codes and probabilities meet on the tensor cores with FP32
  * accumulation; the codes are exact, the softmax, the scales and the lows act
- * in FP32.  BF16 caches: a query's channels as two e4m3 terms (exact to 2^-18
- * of its largest channel), the scaled probabilities rounded to BF16.  FP32
- * caches: queries and scaled probabilities as three BF16 terms. */
+ * in FP32.  BF16 caches: a query's channels as two e4m3 terms (each off by at
+ * most 2^-17 of the row's largest channel, channels from 2^-9 of it on not at
+ * all), the scaled probabilities rounded to BF16.  FP32 caches: queries and
+ * scaled probabilities as three BF16 terms. */
 cp_status_t cp_kv4_attn(const cp_kv4_t* cache, int32_t n_q, const void* q, const int32_t* lengths, void* o,
                         int32_t o_f32, float* lse, int32_t accumulate, void* workspace, size_t workspace_bytes,
                         cp_stream_t stream);

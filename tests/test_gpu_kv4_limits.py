@@ -139,3 +139,23 @@ def test_attn_scores_of_next_to_nothing(dtype):
     c = Filled([1, 40, 300], 4, 2, 128, 128, dtype, seed=72, scale=1e-12)
     q = (torch.randn(3, 3, 4, 128, generator=torch.Generator().manual_seed(73)) * 1e-37).to(dtype).cuda()
     check_attn(c, n_q=3, q=q)
+
+
+@pytest.mark.parametrize("exponent", [-9, -8, -7, -5, -3, -2])
+def test_attn_small_channels_beside_a_large_one(exponent):
+    """Every significand of a bf16 query channel far below the row's largest (128): off by at most 2^-17 of that, and
+    not at all from 2^-9 of it on.  The large channel's key is 0 and the others' all 15, so that the errors add up."""
+    c = Filled([1], 128, 1, 128, 128, seed=74, scale=0.01)
+    page = c.table[0, 0]
+    c.k[0][page], c.k[1][page], c.k[2][page] = 15, 0.0, 1.0
+    c.k[0][page, :, :, 0] = 0
+    c.pages.copy_(torch.from_numpy(oracle.kv4_pack(c.k, c.v)))
+    x = (1 + torch.arange(128) / 128.0) * 2.0 ** exponent
+    q = x.view(1, 1, 128, 1).repeat(1, 1, 1, 128)
+    q[..., 0] = 128.0
+    assert torch.equal(q.bfloat16().float(), q)
+    _, lse = check_attn(c, q=q.bfloat16().cuda(), accumulate=False)
+    # one slot: lse is the score.  127 channels of x 15 scale; fp32 sums of d / 16 terms
+    exact = x.double().numpy() * 127 * 15 * 0.01
+    most = 127 * 15 * 0.01 * 2.0 ** -10 if exponent < -2 else 0.0
+    assert np.abs(lse[:, 0] - exact).max() <= most + 2.0 ** -19 * 31 * 0.01 * float(q.sum(-1).max())
