@@ -81,7 +81,7 @@ struct Cfg {
 };
 
 // -lse * log2e of query column `col` of the step the cursor points at, -inf
-// where a gathered tile holds no query.
+// where the step holds no query or one that is left out (lse = +inf).
 template <bool PACKED>
 __device__ __forceinline__ float load_stat(const AttnArgs& a, const StepCursor<BT>& c, int col) {
   int64_t row = -1;
@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(Cfg<DQK>::kThreads, 1) key_weights_kernel(cons
       float* st = stat + (k & 1) * BT;
       // (the buffer was last read two of this group's tiles ago, before the barrier of the tile between)
       st[t] = next;
-      ptx::named_barrier(1 + grp, kGroupThreads);
+      // (a query left out may hold what it likes: the step is masked)
+      const bool left_out = ptx::named_barrier_any(1 + grp, kGroupThreads, next == -INFINITY);
       if (j + kGroups < n_tiles) {
         go_to(j + kGroups);
         next = load_stat<PACKED>(a, cur, t);
@@ -285,8 +286,8 @@ __global__ void __launch_bounds__(Cfg<DQK>::kThreads, 1) key_weights_kernel(cons
       ptx::tc_fence_after();
       const bool causal = a.causal && !packed;
       const int first = tile.pos0 + half * BT;
-      // columns from cmin on are visible; columns without a query have the statistic -inf
-      const bool need_mask = packed || nq < BT || (causal && qpos0 < first + BT - 1);
+      // columns from cmin on are visible; columns without a query, and of one left out, have the statistic -inf
+      const bool need_mask = left_out || (causal && qpos0 < first + BT - 1);
       const int cmin = causal ? first + t - qpos0 : 0;
       uint64_t s0 = 0, s1 = 0;  // a step's own sums: a long sum's roundings stay small
       auto sums = [&](auto mask_) {
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(Cfg<DQK>::kThreads, 1) key_weights_kernel(cons
           }
         }
       };
-      // warp-uniform: only tiles on the diagonal, at a ragged edge or gathered pay for the tests
+      // warp-uniform: only steps on the diagonal or with columns that do not count pay for the tests
       if (need_mask) sums(std::true_type{});
       else sums(std::false_type{});
       float a0, a1;
@@ -495,14 +496,16 @@ __global__ void __launch_bounds__(kWinThreads, 1) key_weights_window_kernel(cons
       }
       *reinterpret_cast<uint4*>(smem + C::offQ + (chunk >> 3) * C::kQPanel + n * 128 + (((chunk & 7) ^ (n & 7)) << 4)) = v;
     }
+    bool out = false;  // columns that do not count: no query, or one left out (lse = +inf)
     for (int n = threadIdx.x; n < kWinCols; n += kWinThreads) {
       const int g = n / q.count, j = n - g * q.count;
       const int h = a.gqa_interleaved ? g * a.hkv + kvh : kvh * G + g;
       stat[n] = n < cols ? -(a.lse_in[int64_t(h) * a.T + p.rows[q.row0 + j]] * kLog2e) : -INFINITY;
       qpos[n] = a.causal ? q.pos0 + j : INT32_MAX;
+      out |= stat[n] == -INFINITY && n < ((cols + 31) & ~31);
     }
     ptx::fence_proxy_async_smem();
-    __syncthreads();
+    const bool left_out = __syncthreads_or(out);
 
     if (warp == kWinProducer) {
       // ---------------------------------------------------------- producers: lanes 0 and 1 split the panels
@@ -574,9 +577,10 @@ __global__ void __launch_bounds__(kWinThreads, 1) key_weights_window_kernel(cons
                   float v[4];
                   ptx::f32x2_split(e0, v[0], v[1]);
                   ptx::f32x2_split(e1, v[2], v[3]);
+                  const float n4[4] = {nl.x, nl.y, nl.z, nl.w};
 #pragma unroll
                   for (int e = 0; e < 4; ++e)
-                    if (kpos > qpos[32 * ch + j + e] || 32 * ch + j + e >= cols) v[e] = 0.f;
+                    if (kpos > qpos[32 * ch + j + e] || n4[e] == -INFINITY) v[e] = 0.f;
                   e0 = ptx::f32x2(v[0], v[1]);
                   e1 = ptx::f32x2(v[2], v[3]);
                 }
@@ -588,8 +592,9 @@ __global__ void __launch_bounds__(kWinThreads, 1) key_weights_window_kernel(cons
               w += a0 + a1;
             }
           };
-          // (columns from cols on are products with zeros, NaN where a key is infinite, and from N on stale: masked too)
-          if (need_mask || cols % 32) sums(std::true_type{});
+          // (columns from cols on are products with zeros, NaN where a key is infinite, and from N on stale: masked too,
+          // like those of a query left out, which may hold what it likes)
+          if (need_mask || left_out) sums(std::true_type{});
           else sums(std::false_type{});
           ptx::tc_fence_before();
           __syncwarp();

@@ -481,13 +481,15 @@ __global__ void __launch_bounds__(256) simt_key_weights_kernel(const AttnArgs a)
         float part = 0.f;  // a run's sum on its own: the roundings of a long sum stay small
         for (int i = a.causal ? max(0, kpos - R.pos0) : 0; i < R.nrows; ++i) {
           const int64_t qrow = int64_t(R.row0) + i;
+          const float lse = a.lse_in[int64_t(h) * a.T + qrow];
+          if (lse == INFINITY) continue;  // left out, whatever it holds
           float s = 0.f;
 #pragma unroll
           for (int e = 0; e < kMaxPerLane; ++e) {
             const int c = lane + 32 * e;
             s += c < a.d_qk ? ldf(q + (qrow * a.hq + h) * a.d_qk + c) * kv_[e] : 0.f;
           }
-          part += expf(warp_sum(s) * a.scale - a.lse_in[int64_t(h) * a.T + qrow]);
+          part += expf(warp_sum(s) * a.scale - lse);
         }
         w += part;
       }

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import oracle
-from test_gpu_kv4 import Filled, check_attn, ints
+from test_gpu_kv4 import Filled, check_attn, f64, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -159,3 +159,37 @@ def test_attn_small_channels_beside_a_large_one(exponent):
     exact = x.double().numpy() * 127 * 15 * 0.01
     most = 127 * 15 * 0.01 * 2.0 ** -10 if exponent < -2 else 0.0
     assert np.abs(lse[:, 0] - exact).max() <= most + 2.0 ** -19 * 31 * 0.01 * float(q.sum(-1).max())
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("lengths,last", [([1100, 130, 40], None), ([1100, 130, 40], 30), ([1100, 130, 40], 64),
+                                          ([640], 32), ([640], 400)])
+@pytest.mark.parametrize("d,dtype", [(128, torch.bfloat16), (192, torch.bfloat16), (64, torch.bfloat16),
+                                     (128, torch.float32)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_key_weights_of_queries_left_out(d, dtype, causal, lengths, last, bad):
+    """lse = +inf leaves a query out whatever it holds, wherever its step lies: inside, on the diagonal, gathered."""
+    hq, hkv = 4, 2
+    rng = np.random.RandomState(80)
+    cu = np.concatenate([[0], np.cumsum(lengths)]).tolist()
+    T = cu[-1]
+    q, k = (torch.from_numpy(rng.randn(T, h, d).astype(np.float32)).to(dtype) for h in (hq, hkv))
+    lse = oracle.attn_forward(f64(q), f64(k), np.zeros((T, hkv, 8)), cu, d ** -0.5, causal=causal)[1].astype(np.float32)
+    out = [(T - 1, h) for h in range(hq)] + [(T - 2, 1), (T - 20, 0), (600, 2), (600, 3), (3, 1)]  # (row, head)
+    for i, h in out:
+        lse[h, i] = math.inf
+    perm = torch.from_numpy(oracle.shard_order(cu, 2, "zigzag"))
+    prob = cpa.Problem(T, hq, hkv, d, 64, 2, "zigzag", cu, causal, dtype=dtype)
+    dev = lambda x: x.index_select(0, perm).contiguous().cuda()  # noqa: E731
+    lse_d = torch.from_numpy(lse)[:, perm].contiguous().cuda()
+    want = oracle.attn_key_weights(f64(q), f64(k), lse.astype(np.float64), cu, d ** -0.5, causal, last)
+    w = cpa.cp_attn_key_weights(prob, dev(q), dev(k), lse_d, last=last)
+    got = np.zeros((hkv, T))
+    got[:, perm.numpy()] = f64(w)
+    # check_key_weights' bound
+    big = float(q.abs().max() * k.abs().max()) * d ** 0.5
+    tol = 2.0 ** -23 * (d / 16 * big + 64 + np.abs(lse[np.isfinite(lse)]).max() * 4)
+    assert np.all(np.abs(got - want) <= tol * want + 1e-30)
+    for i, h in out:
+        q[i, h, 5] = bad
+    assert torch.equal(cpa.cp_attn_key_weights(prob, dev(q), dev(k), lse_d, last=last), w)
