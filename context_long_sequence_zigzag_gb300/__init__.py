@@ -447,7 +447,14 @@ def cp_attn_fwd_noalloc(prob: Problem, q, k, v, o, lse, stream=None):
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # (torch.cuda.current_stream builds an object on every call)
+try:  # (torch.cuda.current_stream builds an object on every call)
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:  # a private name, and one that builds without CUDA lack
+
+    def _raw_stream(index: int) -> int:
+        return torch.cuda.current_stream(index).cuda_stream
+
+
 _current_device = torch.cuda.current_device
 
 

@@ -1,0 +1,26 @@
+"""The binding of the 4-bit cache and the key weights, without a GPU."""
+
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+cpa = pytest.importorskip("context_long_sequence_zigzag_gb300")
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def test_import_takes_no_private_name_of_a_cuda_build():
+    """A torch built without CUDA lacks the raw stream's query: the host-side calls still answer."""
+    code = """
+import torch
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    del torch._C._cuda_getCurrentRawStream
+import context_long_sequence_zigzag_gb300 as cpa
+assert cpa.cp_kv4_block_bytes(128, 128) == 9216
+assert cpa.cp_workspace_size(cpa.Problem(1024, 8, 2, 128, 128, 4), cpa.CP_OP_FWD) > 0
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=240)
+    assert done.returncode == 0, done.stderr[-2000:]
