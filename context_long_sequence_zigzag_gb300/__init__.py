@@ -532,6 +532,8 @@ def cp_attn_key_weights(prob: Problem, q, k, lse, last: Optional[int] = None, w=
     sequence.  lse: the forward's.  Not for capture into a graph (as the other
     calls with tile plans)."""
     d = prob.desc
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:  # (the others have to be where q is)
+        raise ValueError("q: a tensor on a CUDA device is needed")
     T, hkv, dev, dtype = d.total_tokens, d.hkv, q.device, prob.torch_dtype
     if last is not None and last < 1:
         raise ValueError("last: a positive number of queries, or None for all")

@@ -24,3 +24,13 @@ assert cpa.cp_workspace_size(cpa.Problem(1024, 8, 2, 128, 128, 4), cpa.CP_OP_FWD
 """
     done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=240)
     assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_key_weights_need_tensors_on_a_gpu():
+    T, prob = 8, cpa.Problem(8, 2, 2, 64, 64, 1)
+    q, k, lse = torch.zeros(T, 2, 64).bfloat16(), torch.zeros(T, 2, 64).bfloat16(), torch.zeros(2, T)
+    for ws in (None, torch.zeros(1 << 20, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            cpa.cp_attn_key_weights(prob, q, k, lse, ws=ws)
+    with pytest.raises(ValueError, match="CUDA device"):
+        cpa.cp_attn_key_weights(prob, None, k, lse)
