@@ -13,6 +13,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <exception>
 #include <list>
 #include <map>
 #include <memory>
@@ -1624,7 +1625,7 @@ cp_status_t cp_lin_attn_fwd(const cp_desc_t* d, const void* q, const void* k, co
 }
 
 cp_status_t cp_attn_key_weights(const cp_desc_t* d, int64_t last, const void* q, const void* k, const float* lse,
-                                float* w, void* ws, size_t ws_bytes, cp_stream_t stream) {
+                                float* w, void* ws, size_t ws_bytes, cp_stream_t stream) try {
   CallRange range_("cp_attn_key_weights");
   cp_status_t st = check_attn_fields(d);
   if (st != CP_OK) return st;
@@ -1668,6 +1669,8 @@ cp_status_t cp_attn_key_weights(const cp_desc_t* d, int64_t last, const void* q,
   if (st != CP_OK) return st;
   const cudaError_t e = use_tc_key_weights(d) ? launch_tc_key_weights(a, cs) : launch_simt_key_weights(a, d->dtype, cs);
   return e == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+} catch (const std::exception&) {  // the host has no memory for the plan (no kernel was launched)
+  return CP_ERR_UNSUPPORTED;
 }
 
 cp_status_t cp_set_debug_checks(int32_t on, int32_t* previous) {

@@ -353,7 +353,7 @@ cp_status_t cp_lin_attn_fwd(const cp_desc_t* desc, const void* q, const void* k,
  * BF16 with d_qk in {128, 192} runs on the tensor cores; other head dims and
  * FP32 run on the CUDA cores.  d_v is not used.  CP_ERR_UNSUPPORTED while
  * `stream` is being captured into a graph (the tile plan is uploaded by the
- * call). */
+ * call), or where the host has no memory for that plan. */
 cp_status_t cp_attn_key_weights(const cp_desc_t* desc, int64_t last, const void* q, const void* k, const float* lse,
                                 float* w, void* workspace, size_t workspace_bytes, cp_stream_t stream);
 

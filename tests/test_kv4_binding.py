@@ -34,3 +34,18 @@ def test_key_weights_need_tensors_on_a_gpu():
             cpa.cp_attn_key_weights(prob, q, k, lse, ws=ws)
     with pytest.raises(ValueError, match="CUDA device"):
         cpa.cp_attn_key_weights(prob, None, k, lse)
+
+
+def test_key_weights_without_memory_for_the_plan():
+    """A host that cannot hold the tile plan: a status, not the end of the process."""
+    code = """
+import resource, context_long_sequence_zigzag_gb300 as cpa
+prob = cpa.Problem(1 << 30, 2, 2, 128, 128, 1, "contiguous")
+size = next(int(x.split()[1]) for x in open("/proc/self/status") if x.startswith("VmSize")) << 10
+resource.setrlimit(resource.RLIMIT_AS, (size + (64 << 20),) * 2)
+for last in (0, 16):
+    status = cpa._lib.cp_attn_key_weights(prob.ptr, last, 256, 256, 256, 256, 256, 0, None)
+    assert status == cpa.CP_ERR_UNSUPPORTED, status
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=240)
+    assert done.returncode == 0, (done.returncode, done.stderr[-2000:])
