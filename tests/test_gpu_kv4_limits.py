@@ -193,3 +193,22 @@ def test_key_weights_of_queries_left_out(d, dtype, causal, lengths, last, bad):
     for i, h in out:
         q[i, h, 5] = bad
     assert torch.equal(cpa.cp_attn_key_weights(prob, dev(q), dev(k), lse_d, last=last), w)
+
+
+def test_append_scales_halfway_between_two():
+    """Ranges of 15 times a number halfway between two bf16 scales: to the even one, as (max - low) / 15 rounds."""
+    half = torch.arange(257, 512, 2, dtype=torch.float64) / 512  # 9 bits, the last one set
+    tokens = half.numel() * 3
+    x = torch.zeros(tokens, 1, 64)
+    x[:, 0, 17] = (15 * torch.cat([half, half * 2.0 ** 9, half * 2.0 ** -11])).float()
+    assert torch.equal(x[:, 0, 17].double() / 15, torch.cat([half, half * 2.0 ** 9, half * 2.0 ** -11]))  # exact
+    pages = -(-tokens // 64)
+    block = cpa.cp_kv4_block_bytes(64, 64)
+    cache = cpa.Kv4Cache(torch.zeros(pages, 1, block, dtype=torch.uint8, device="cuda"), ints([list(range(pages))]), 1, 1, 64,
+                         64, dtype=torch.float32)
+    cpa.cp_kv4_append(cache, x.cuda(), x.cuda(), ints([0, tokens]), ints([0]))
+    held = [oracle.kv4_unpack(cache.pages[p, 0].cpu().numpy(), 64, 64) for p in range(pages)]
+    want = (x[:, 0, 17].double() / 15).float().bfloat16().double().numpy()
+    for which in range(2):
+        step = np.concatenate([h[which][2] for h in held])[:tokens, 0]
+        assert np.array_equal(step, want)
