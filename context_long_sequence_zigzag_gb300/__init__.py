@@ -529,7 +529,8 @@ def cp_attn_key_weights(prob: Problem, q, k, lse, last: Optional[int] = None, w=
     """Accumulated attention weight of every key, float32 [hkv, T] in sharded
     order: the attention probabilities summed over the query heads of the
     key's head and over the queries, or over the last ``last`` of every
-    sequence.  lse: the forward's.  Not for capture into a graph (as the other
+    sequence.  lse: the forward's; +inf leaves a query out.  bfloat16 heads of 128 and 192 run on the
+    tensor cores, others slowly on the CUDA cores.  Not for capture into a graph (as the other
     calls with tile plans)."""
     d = prob.desc
     if not isinstance(q, torch.Tensor) or not q.is_cuda:  # (the others have to be where q is)
@@ -655,7 +656,8 @@ def cp_kv4_attn(cache: Kv4Cache, q, lengths, accumulate: bool = False, part: boo
     """Attention of q [B, n_q, hq, d_qk], the newest n_q tokens of every sequence, over the cache
     (lengths int32 [B]: tokens held, the new ones among them).  Returns o [B, n_q, hq, d_v] and
     lse [hq, B * n_q].  accumulate: the attention probabilities are added to cache.weights.
-    part: o in float32, for cp_lse_merge."""
+    part: o in float32, for cp_lse_merge (in a bfloat16 cache with the probabilities rounded to bfloat16 on the way all the
+    same; a Kv4Cache of dtype float32 over the same pages takes float32 queries and keeps float32)."""
     dev, dtype, B, hq = cache.device, cache.torch_dtype, cache.num_seqs, cache.hq
     n_q = q.shape[1]
     pq = _need(q, "q", dtype, (B, n_q, hq, cache.d_qk), dev)

@@ -7,7 +7,7 @@
 // cycle, 46 codes; unpacking them, the MMAs' operands and the scales take more
 // issue slots than that leaves, so the long cases are bound by instruction
 // issue (8 x up to 64K tokens, d 128: 77 us, 59% of issue slots, ALU pipe 53%,
-// 44% of the measured copy rate; 128K tokens, 64 heads, d 192/128: 347 us,
+// 44% of the measured copy rate; 128K tokens, 64 heads, d 192/128: 351 us,
 // 64% and 64%), the short ones by latency (16K tokens: 15 us, and 7 to join).
 //
 // Warp-level MMAs, not tcgen05: with 1 to 16 rows a tcgen05 tile would be
@@ -21,12 +21,17 @@
 //   scaled by a power of two to a largest channel of 128 .. 256 and split into
 //   two e4m3 terms: 8 bits, all that bf16 has.  Each product starts from zero
 //   and is added to S by FMAs with the group's scale.  (bf16 operands would
-//   take twice the MMAs and an instruction more for every two codes.)
+//   take as many MMAs, one term over twice the steps, but an instruction more
+//   for every two codes to unpack.)
 // * V, and K of fp32 caches: a code becomes the bf16 number n - 8 (below) for
 //   mma.m16n8k16.  fp32 caches split q and P s into three bf16 terms (24 bits).
 // * Scales and lows act in fp32: on S per (key, group), the lows on sum(q); on
-//   P per (token, group) before P s is rounded to the bf16 operand, the lows
-//   (with 8 steps added) on a sum of their own.
+//   P per (token, group), the lows (with 8 steps added) on a sum of their own.
+// * P s of a bf16 cache is rounded to one bf16 operand, as P is in the prompt's
+//   forward; the softmax sum takes it unrounded.  O is then 0.0019 to 0.0024 of
+//   its norm off (fp32 arithmetic rounded to bf16 once: 0.0016), in fp32
+//   partials too.  A second term would double V's MMAs; who needs more opens
+//   the same pages in a descriptor of dtype FP32 (three terms: 2e-7).
 // * S^T comes out with keys as rows and goes back in as P^T with tokens as
 //   the contracted index: movmatrix transposes the 8 x 8 quarters.
 // * The softmax keeps a reference per row instead of a running maximum: P =
@@ -42,8 +47,9 @@
 // row tiles or three terms need the registers.  What a warp leaves of a run
 // that goes on elsewhere is joined in the CTA first; runs that lie in one CTA
 // are finished there, the others leave partials for kv4_join_kernel.  Weights
-// need the final lse: the scores wait in the workspace (they stay in L2) and
-// kv4_weights_kernel adds them up.  Both are launched while the kernel before
+// need the final lse: the scores, 4 bytes a row and slot, wait in the workspace
+// (in L2 as far as they fit: 4 x 64K of 16 / 4 heads are 17 MB, 8 x 64K of 32 / 8
+// with 4 queries 268 MB) and kv4_weights_kernel adds them up.  Both are launched while the kernel before
 // them drains.
 #include <algorithm>
 #include <atomic>

@@ -185,7 +185,7 @@ __device__ __forceinline__ Place place_of(const Kv4Cache& c, const Kv4Format& f,
 
 constexpr int kAhead = 2;        // pieces a thread of read loads before it writes (64K tokens: 65 us; 1: 75, 3: 73)
 
-// CTAs an SM: as many as leave the registers their place (64K tokens of bf16, 8 heads of 128 + 128: 96 us with 4, 135 with
+// CTAs an SM: as many as leave the registers their place (64K tokens of bf16, 8 heads of 128 + 128: 98 us with 4, 135 with
 // 5, whose registers spill; fp32 values take more of them).
 template <typename E>
 __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 ? 4 : 3) kv4_append_kernel(const Kv4Cache c, const Kv4Format f, const Words n, const E* k,

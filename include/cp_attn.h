@@ -350,8 +350,11 @@ cp_status_t cp_lin_attn_fwd(const cp_desc_t* desc, const void* q, const void* k,
  *   w         : device float32 [hkv, T], sharded order; keys that no counted
  *               query sees get 0
  *   workspace : cp_workspace_size(desc, CP_OP_KEY_WEIGHTS) bytes, for any `last`
- * BF16 with d_qk in {128, 192} runs on the tensor cores; other head dims and
- * FP32 run on the CUDA cores.  d_v is not used.  CP_ERR_UNSUPPORTED while
+ * BF16 with d_qk in {128, 192} runs on the tensor cores.  Other head dims and
+ * FP32 run on the CUDA cores, a warp a key: right, and slow (16K tokens, 32 / 8
+ * heads: 0.43 s with BF16 heads of 64, 0.61 s with FP32 heads of 128, four to five
+ * times what matrix products in PyTorch take, where BF16 heads of 128 take
+ * 0.9 ms).  d_v is not used.  CP_ERR_UNSUPPORTED while
  * `stream` is being captured into a graph (the tile plan is uploaded by the
  * call), or where the host has no memory for that plan. */
 cp_status_t cp_attn_key_weights(const cp_desc_t* desc, int64_t last, const void* q, const void* k, const float* lse,
@@ -383,13 +386,16 @@ cp_status_t cp_attn_key_weights(const cp_desc_t* desc, int64_t last, const void*
  * of a V row at (w % 8) * (d / 64) + w / 8.
  * Token (slot) j of sequence b is in page page_table[b][j / 64], row j % 64.
  * Several sequences may share pages (a common prefix) as long as no call
- * writes them.  Table entries past a sequence's last page are not read.
+ * writes them (the weights of such pages get every sequence's sums, in no fixed
+ * order).  Table entries past a sequence's last page are not read.  The pages
+ * do not depend on `dtype`: a second descriptor may open them in the other one.
  *
  * Lengths, offsets and tables are device arrays, read by the kernels: a
  * captured graph can be replayed with new ones.  A length outside 0 ..
  * max_pages * 64 is clamped; a page outside 0 .. num_pages - 1, or a row
- * outside its tensor, is skipped (attention: its keys count as absent).  Both
- * put 0x300 | site into the device error word (cp_device_status). */
+ * outside its tensor, is skipped (attention: its keys count as absent;
+ * eviction: its slots rank below all others, and one that is kept all the same
+ * leaves its place in `to` as it was).  Both put 0x300 | site into the device error word (cp_device_status). */
 #define CP_KV4_PAGE 64
 #define CP_KV4_GROUP 64
 #define CP_KV4_MAX_QUERIES 16
@@ -463,8 +469,11 @@ cp_status_t cp_kv4_read(const cp_kv4_t* cache, const int32_t* cu, const int32_t*
  * accumulation; the codes are exact, the softmax, the scales and the lows act
  * in FP32.  BF16 caches: a query's channels as two e4m3 terms (each off by at
  * most 2^-17 of the row's largest channel, channels from 2^-9 of it on not at
- * all), the scaled probabilities rounded to BF16.  FP32 caches: queries and
- * scaled probabilities as three BF16 terms. */
+ * all), the scaled probabilities rounded to BF16 (with o_f32 = 1 as well).
+ * FP32 caches: queries and scaled probabilities as three BF16 terms.
+ * A query that holds a NaN or an infinity gives NaN in its own row of o and
+ * lse, where it sees a slot at all, and with accumulate = 1 in the weights of
+ * the slots that it sees. */
 cp_status_t cp_kv4_attn(const cp_kv4_t* cache, int32_t n_q, const void* q, const int32_t* lengths, void* o,
                         int32_t o_f32, float* lse, int32_t accumulate, void* workspace, size_t workspace_bytes,
                         cp_stream_t stream);

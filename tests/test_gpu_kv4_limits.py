@@ -212,3 +212,14 @@ def test_append_scales_halfway_between_two():
     for which in range(2):
         step = np.concatenate([h[which][2] for h in held])[:tokens, 0]
         assert np.array_equal(step, want)
+
+
+@pytest.mark.parametrize("n_q", [1, 3])
+def test_attn_of_the_same_pages_in_fp32(n_q):
+    """The pages do not depend on the descriptor's dtype: one of FP32 over pages of a BF16 cache gives FP32 results."""
+    c = Filled([700, 33, 0], 8, 2, 128, 128, torch.bfloat16, seed=75)
+    q = torch.randn(3, n_q, 8, 128, generator=torch.Generator().manual_seed(76)).bfloat16().cuda()
+    check_attn(c, n_q=n_q, q=q, part=True, accumulate=False)
+    c.dtype = torch.float32
+    c.cache = cpa.Kv4Cache(c.pages, c.cache.page_table, 8, 2, 128, 128, c.weights, c.scale, "blocked", torch.float32)
+    check_attn(c, n_q=n_q, q=q.float(), part=True)
