@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_attn_kernel(const Kv4AttnAr
         unit = __uint_as_float(uint32_t(127 + max(min(k, 126), -126)) << 23);
         // codes are n 2^-9 as e4m3 bytes: scores come out times unit / 512
         // (above 0 and finite, whatever the row holds: an unseen slot's score is -inf times it)
-        factor = fmaxf(factor * 512.f / unit, 1e-45f);
+        // (in the order that leaves fp32's range only where the result does)
+        factor = fmaxf(unit < 1.f ? factor / unit * 512.f : factor * (512.f / unit), 1e-45f);
         if (big >= 0x7f800000u) {  // a row with a NaN or an infinity: NaN in what every key's score adds up
           factor = 1.f;
           gs[0] = NAN;

@@ -223,3 +223,11 @@ def test_attn_of_the_same_pages_in_fp32(n_q):
     c.dtype = torch.float32
     c.cache = cpa.Kv4Cache(c.pages, c.cache.page_table, 8, 2, 128, 128, c.weights, c.scale, "blocked", torch.float32)
     check_attn(c, n_q=n_q, q=q.float(), part=True)
+
+
+@pytest.mark.parametrize("spread", [1e-37, 1e-20, 1e20, 1e36])
+def test_attn_scale_against_the_queries_magnitude(spread):
+    """The scale times the queries is what counts, whatever either is."""
+    c = Filled([300, 40], 4, 2, 128, 128, seed=77, scale=0.1 / spread)
+    q = torch.randn(2, 2, 4, 128, generator=torch.Generator().manual_seed(78)) * spread
+    check_attn(c, n_q=2, q=q.bfloat16().cuda())
