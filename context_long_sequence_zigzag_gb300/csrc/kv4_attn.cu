@@ -7,7 +7,7 @@
 // cycle, 46 codes; unpacking them, the MMAs' operands and the scales take more
 // issue slots than that leaves, so the long cases are bound by instruction
 // issue (8 x up to 64K tokens, d 128: 77 us, 59% of issue slots, ALU pipe 53%,
-// 44% of the measured copy rate; 128K tokens, 64 heads, d 192/128: 351 us,
+// 44% of the measured copy rate; 128K tokens, 64 heads, d 192/128: 348 us,
 // 64% and 64%), the short ones by latency (16K tokens: 15 us, and 7 to join).
 //
 // Warp-level MMAs, not tcgen05: with 1 to 16 rows a tcgen05 tile would be
