@@ -16,7 +16,10 @@ Functions carry the C names: ``cp_shard_permute``, ``cp_attn_block_fwd``,
 ``cp_ulysses_attn_fwd``, ``cp_ulysses_attn_bwd``, ``cp_ring_attn_fwd``, ``cp_lin_attn_fwd``,
 ``cp_attn_key_weights``, and for decoding over a 4-bit key/value cache (``Kv4Cache``) ``cp_kv4_append``,
 ``cp_kv4_read``, ``cp_kv4_attn``, ``cp_kv4_evict``, ``cp_kv4_block_bytes``, ``cp_kv4_validate``,
-``cp_kv4_workspace_size``.
+``cp_kv4_workspace_size``.  Over a cache in the model's own type (``KvCache``): ``cp_kv_append``, ``cp_kv_attn``,
+``cp_kv_validate``, ``cp_kv_workspace_size``; rotary positions (``Rope``): ``cp_rope``, ``cp_rope_turns``; pages that
+sequences share (``PagePool``): ``cp_pages_reserve``, ``cp_pages_fork``, ``cp_pages_compact``, ``cp_pages_copy``,
+``cp_pages_validate``, ``cp_pages_workspace_size``.
 """
 
 from __future__ import annotations
@@ -46,6 +49,8 @@ CP_OP_FWD, CP_OP_BWD, CP_OP_BLOCK_FWD, CP_OP_PERMUTE, CP_OP_BWD_DKDV, CP_OP_BWD_
 CP_OP_ULYSSES_A2A, CP_OP_ULYSSES_FWD, CP_OP_ULYSSES_BWD, CP_OP_LIN_FWD, CP_OP_RING_FWD = 6, 7, 8, 9, 10
 CP_OP_KEY_WEIGHTS = 11
 CP_KV4_PAGE, CP_KV4_GROUP, CP_KV4_MAX_QUERIES = 64, 64, 16
+CP_ROPE_HALVES, CP_ROPE_ADJACENT = 0, 1
+CP_ROPE_MAX_AXES, CP_ROPE_MAX_DIMS, CP_PAGES_MAX_BUFFERS = 4, 512, 128
 
 EXPORTED = [
     "cp_status_string", "cp_validate", "cp_workspace_size", "cp_shard_offsets",
@@ -56,6 +61,9 @@ EXPORTED = [
     "cp_set_debug_checks", "cp_attn_key_weights",
     "cp_kv4_block_bytes", "cp_kv4_validate", "cp_kv4_workspace_size", "cp_kv4_append", "cp_kv4_read", "cp_kv4_attn",
     "cp_kv4_evict",
+    "cp_rope_turns", "cp_rope", "cp_kv_validate", "cp_kv_workspace_size", "cp_kv_append", "cp_kv_attn",
+    "cp_pages_validate", "cp_pages_workspace_size", "cp_pages_reserve", "cp_pages_fork", "cp_pages_compact",
+    "cp_pages_copy",
 ]
 
 
@@ -95,9 +103,53 @@ class cp_kv4_t(ctypes.Structure):
     ]
 
 
+class cp_rope_t(ctypes.Structure):
+    _fields_ = [
+        ("first", ctypes.c_int32),
+        ("dims", ctypes.c_int32),
+        ("pairing", ctypes.c_int32),
+        ("axes", ctypes.c_int32),
+        ("factor", ctypes.c_float),
+        ("turns", ctypes.c_void_p),
+        ("axis", ctypes.c_void_p),
+    ]
+
+
+class cp_kv_t(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int32),
+        ("hq", ctypes.c_int32),
+        ("hkv", ctypes.c_int32),
+        ("d_qk", ctypes.c_int32),
+        ("d_v", ctypes.c_int32),
+        ("gqa", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("k_pages", ctypes.c_void_p),
+        ("v_pages", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+    ]
+
+
+class cp_pages_t(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("refs", ctypes.c_void_p),
+        ("num_buffers", ctypes.c_int32),
+        ("base", ctypes.POINTER(ctypes.c_void_p)),
+        ("bytes", ctypes.POINTER(ctypes.c_int64)),
+    ]
+
+
 _P = ctypes.c_void_p
 _DP = ctypes.POINTER(cp_desc_t)
 _KP = ctypes.POINTER(cp_kv4_t)
+_RP, _CP, _GP = ctypes.POINTER(cp_rope_t), ctypes.POINTER(cp_kv_t), ctypes.POINTER(cp_pages_t)
+_I = ctypes.c_int32
 _sigs = {
     "cp_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "cp_validate": (ctypes.c_int, [_DP]),
@@ -133,6 +185,18 @@ _sigs = {
     "cp_kv4_attn": (ctypes.c_int, [_KP, ctypes.c_int32, _P, _P, _P, ctypes.c_int32, _P, ctypes.c_int32, _P,
                                    ctypes.c_size_t, _P]),
     "cp_kv4_evict": (ctypes.c_int, [_KP, _P, ctypes.c_int32, ctypes.c_int32, _KP, _P, _P, _P]),
+    "cp_rope_turns": (ctypes.c_int, [_P, _I, _P]),
+    "cp_rope": (ctypes.c_int, [_RP, ctypes.c_int64, _P, _I, _I, _I, _I, _P, _P, _I, _P, _P, _I, _P]),
+    "cp_kv_validate": (ctypes.c_int, [_CP]),
+    "cp_kv_workspace_size": (ctypes.c_int, [_CP, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "cp_kv_append": (ctypes.c_int, [_CP, _P, _P, ctypes.c_int64, _P, _P, _P, ctypes.c_int64, _RP, _P, _I, _P]),
+    "cp_kv_attn": (ctypes.c_int, [_CP, _I, _P, _P, _P, _I, _P, _P, ctypes.c_size_t, _P]),
+    "cp_pages_validate": (ctypes.c_int, [_GP]),
+    "cp_pages_workspace_size": (ctypes.c_int, [_GP, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "cp_pages_reserve": (ctypes.c_int, [_GP, _I, _I, _P, _P, _P, _P, _P]),
+    "cp_pages_fork": (ctypes.c_int, [_GP, _I, _I, _P, _P, _I, _I, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "cp_pages_compact": (ctypes.c_int, [_GP, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "cp_pages_copy": (ctypes.c_int, [_GP, _GP, _I, _P, _P, _P]),
 }
 for _name, (_res, _args) in _sigs.items():
     _f = getattr(_lib, _name)
@@ -499,7 +563,9 @@ def _launch(dev: torch.device, stream, temps, name: str, *args) -> None:
 
 
 _kv4_calls = {n: getattr(_lib, n) for n in ("cp_attn_key_weights", "cp_kv4_append", "cp_kv4_read", "cp_kv4_attn",
-                                            "cp_kv4_evict")}
+                                            "cp_kv4_evict", "cp_rope", "cp_kv_append", "cp_kv_attn",
+                                            "cp_pages_reserve", "cp_pages_fork", "cp_pages_compact",
+                                            "cp_pages_copy")}
 
 
 def _need(t, name: str, dtype, shape, device=None) -> int:
@@ -714,6 +780,326 @@ def cp_kv4_evict(cache: Kv4Cache, lengths, budget: int, recent: int, to: Kv4Cach
     return new_lengths, kept
 
 
+_DTYPES = {torch.float32: CP_DT_F32, torch.bfloat16: CP_DT_BF16}
+
+
+def cp_rope_turns(inv_freq) -> list:
+    """Frequencies (radians a position) as 64-bit fractions of a turn a position."""
+    f = [float(x) for x in (inv_freq.tolist() if hasattr(inv_freq, "tolist") else inv_freq)]
+    got = (ctypes.c_uint64 * len(f))()
+    _check(_lib.cp_rope_turns((ctypes.c_double * len(f))(*f), len(f), got), "cp_rope_turns")
+    return list(got)
+
+
+class Rope:
+    """Rotary positions: which channels of a head turn, in which pairs and how fast.
+
+    inv_freq : frequency of every pair (radians a position; taken in 64 bits), list or tensor
+    axis     : the position axis that every pair follows (time, height, width, ...), or None: 0
+    first    : first of the 2 * len(inv_freq) turned channels
+    pairing  : "halves": channel i with i + len(inv_freq); "adjacent": 2i with 2i + 1
+    factor   : on every turned channel
+    """
+
+    def __init__(self, inv_freq, axis=None, first: int = 0, pairing: str = "halves", factor: float = 1.0,
+                 device="cuda"):
+        turns = cp_rope_turns(inv_freq)
+        axes = 1
+        if axis is not None:
+            axis = [int(x) for x in (axis.tolist() if hasattr(axis, "tolist") else axis)]
+            if len(axis) != len(turns) or any(x < 0 or x >= CP_ROPE_MAX_AXES for x in axis):
+                raise ValueError(f"axis: one of 0 .. {CP_ROPE_MAX_AXES - 1} for every frequency is needed")
+            axes = max(axis, default=0) + 1
+        if not turns or len(turns) * 2 > CP_ROPE_MAX_DIMS:
+            raise ValueError(f"inv_freq: 1 to {CP_ROPE_MAX_DIMS // 2} frequencies are needed")
+        if first < 0 or not math.isfinite(factor):
+            raise ValueError("first: a channel, and factor: a finite number is needed")
+        self.axes, self.first, self.dims = axes, first, 2 * len(turns)
+        self.turns = torch.tensor([x - (x >> 63 << 64) for x in turns], dtype=torch.int64).to(device)
+        self.axis = None if axis is None else torch.tensor(axis, dtype=torch.int32).to(device)
+        self.device = self.turns.device
+        if not self.turns.is_cuda:
+            raise ValueError("device: a CUDA device is needed")
+        self.desc = cp_rope_t(
+            first=first, dims=self.dims, pairing={"halves": CP_ROPE_HALVES, "adjacent": CP_ROPE_ADJACENT}[pairing],
+            axes=axes, factor=float(factor), turns=self.turns.data_ptr(),
+            axis=None if axis is None else self.axis.data_ptr())
+        self.ptr = ctypes.byref(self.desc)
+
+
+def _positions(rope: Rope, positions, rows: int, dev):
+    """Pointer and row length of positions [rows, axes or more] (or [rows] on one axis)."""
+    if rope.device != dev:
+        raise ValueError(f"rope: a Rope on {dev} is needed")
+    if isinstance(positions, torch.Tensor) and positions.dim() == 1:
+        shape, wide = (rows,), 1
+    else:
+        shape, wide = (rows, None), positions.shape[1] if isinstance(positions, torch.Tensor) and positions.dim() == 2 else 0
+    p = _need(positions, "positions", torch.int32, shape, dev)
+    if wide < rope.axes:
+        raise ValueError(f"positions: {rope.axes} columns are needed, got {wide}")
+    return p, wide
+
+
+def cp_rope(rope: Rope, positions, q, k=None, inverse: bool = False, q_out=None, k_out=None, stream=None):
+    """q [T, hq, d] and k [T, hkv, d] turned by their rows' positions (int32 [T, axes], or more columns, or [T]);
+    inverse: turned back (the gradients of a call's inputs from those of its outputs).  q_out, k_out: q and k
+    themselves for a call in place.  Returns q_out, or (q_out, k_out) with k."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:  # (the others have to be where q is)
+        raise ValueError("q: a tensor on a CUDA device is needed")
+    if q.dim() != 3 or q.dtype not in _DTYPES:
+        raise ValueError("q: float32 or bfloat16 [T, heads, d] is needed")
+    dev, dtype = q.device, q.dtype
+    T, hq, d = q.shape
+    temps = []
+    pq = _need(q, "q", dtype, (T, hq, d), dev)
+    if q_out is None:
+        q_out = torch.empty_like(q)
+        temps.append(q_out)
+        po = q_out.data_ptr()
+    else:
+        po = _need(q_out, "q_out", dtype, (T, hq, d), dev)
+    hkv, pk, pko = 0, None, None
+    if k is not None:
+        pk = _need(k, "k", dtype, (T, None, d), dev)
+        hkv = k.shape[1]
+        if k_out is None:
+            k_out = torch.empty_like(k)
+            temps.append(k_out)
+            pko = k_out.data_ptr()
+        else:
+            pko = _need(k_out, "k_out", dtype, (T, hkv, d), dev)
+    pp, wide = _positions(rope, positions, T, dev)
+    _launch(dev, stream, temps, "cp_rope", rope.ptr, T, pp, wide, d, _DTYPES[dtype], hq, pq, po, hkv, pk, pko,
+            1 if inverse else 0)
+    return q_out if k is None else (q_out, k_out)
+
+
+class KvCache:
+    """A paged key/value cache in float32 or bfloat16, or the part of it that a call deals with: the pools and the
+    page table of the sequences in the batch.
+
+    k_pages    : [num_pages, hkv, page_size, d_qk]
+    v_pages    : [num_pages, hkv, page_size, d_v]
+    page_table : int32 [num_seqs, max_pages], a page of page_size tokens an entry
+
+    Holds the tensors; lengths stay with the caller.
+    """
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, hq: int,
+                 scale: Optional[float] = None, gqa: str = "blocked"):
+        if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4 or k_pages.dtype not in _DTYPES:
+            raise ValueError("k_pages: float32 or bfloat16 [num_pages, hkv, page_size, d_qk] is needed")
+        dtype, (num_pages, hkv, page_size, d_qk) = k_pages.dtype, k_pages.shape
+        pk = _need(k_pages, "k_pages", dtype, (None,) * 4, None if not k_pages.is_cuda else k_pages.device)
+        pv = _need(v_pages, "v_pages", dtype, (num_pages, hkv, page_size, None), k_pages.device)
+        t = _need(page_table, "page_table", torch.int32, (None, None), k_pages.device)
+        self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
+        self.torch_dtype, self.device, self.page_size = dtype, k_pages.device, page_size
+        self.num_seqs, self.hq, self.hkv, self.d_qk, self.d_v = page_table.shape[0], hq, hkv, d_qk, v_pages.shape[3]
+        self.desc = cp_kv_t(
+            num_seqs=page_table.shape[0], hq=hq, hkv=hkv, d_qk=d_qk, d_v=self.d_v,
+            gqa={"blocked": CP_GQA_BLOCKED, "interleaved": CP_GQA_INTERLEAVED}[gqa], dtype=_DTYPES[dtype],
+            scale=float(scale if scale is not None else 1.0 / math.sqrt(d_qk)), page_size=page_size,
+            num_pages=num_pages, max_pages=page_table.shape[1], k_pages=pk, v_pages=pv, page_table=t)
+        self.ptr = ctypes.byref(self.desc)
+        self._ws_bytes = {}
+        _check(_lib.cp_kv_validate(self.ptr), "cp_kv_validate")
+
+
+def cp_kv_validate(cache: KvCache) -> int:
+    return _lib.cp_kv_validate(cache.ptr)
+
+
+def cp_kv_workspace_size(cache: KvCache, n_q: int = 1) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.cp_kv_workspace_size(cache.ptr, n_q, ctypes.byref(n)), "cp_kv_workspace_size")
+    return int(n.value)
+
+
+def cp_kv_append(cache: KvCache, k, v, cu, start, rows=None, rope: Optional[Rope] = None, positions=None,
+                 stream=None) -> None:
+    """Writes tokens into the cache: token t, cu[b] <= t < cu[b + 1], becomes slot start[b] + t - cu[b] of
+    sequence b, from row rows[t] (or t) of k [n, hkv, d_qk] and v [n, hkv, d_v].  rope: keys are turned on the way
+    by positions (int32 [n, axes] or [n], in k's rows; None: by their slots).
+    cu int32 [B + 1], start int32 [B], rows int32 [tokens], on the device."""
+    dev, hkv, dtype, B = cache.device, cache.hkv, cache.torch_dtype, cache.num_seqs
+    pk = _need(k, "k", dtype, (None, hkv, cache.d_qk), dev)
+    n = k.shape[0]
+    pv = _need(v, "v", dtype, (n, hkv, cache.d_v), dev)
+    tokens, pr = n, None
+    if rows is not None:
+        pr = _need(rows, "rows", torch.int32, (None,), dev)
+        tokens = rows.shape[0]
+    ptr, pp, wide = None, None, 0
+    if rope is not None:
+        ptr = rope.ptr
+        if positions is not None:
+            pp, wide = _positions(rope, positions, n, dev)
+        elif rope.device != dev:
+            raise ValueError(f"rope: a Rope on {dev} is needed")
+    elif positions is not None:
+        raise ValueError("positions: they need a rope")
+    _launch(dev, stream, (), "cp_kv_append", cache.ptr, pk, pv, n, pr, _need(cu, "cu", torch.int32, (B + 1,), dev),
+            _need(start, "start", torch.int32, (B,), dev), tokens, ptr, pp, wide)
+
+
+def cp_kv_attn(cache: KvCache, q, lengths, part: bool = False, o=None, lse=None, ws=None, stream=None):
+    """Attention of q [B, n_q, hq, d_qk], the newest n_q tokens of every sequence, over the cache
+    (lengths int32 [B]: tokens held, the new ones among them).  Returns o [B, n_q, hq, d_v] and
+    lse [hq, B * n_q].  part: o in float32, for cp_lse_merge."""
+    dev, dtype, B, hq = cache.device, cache.torch_dtype, cache.num_seqs, cache.hq
+    pq = _need(q, "q", dtype, (B, None, hq, cache.d_qk), dev)
+    n_q = q.shape[1]
+    o_dtype = torch.float32 if part else dtype
+    temps = []
+    shape = (B, n_q, hq, cache.d_v)
+    if o is None:
+        o = torch.empty(shape, dtype=o_dtype, device=dev)
+        temps.append(o)
+        po = o.data_ptr()
+    else:
+        po = _need(o, "o", o_dtype, shape, dev)
+    shape = (hq, B * n_q)
+    if lse is None:
+        lse = torch.empty(shape, dtype=torch.float32, device=dev)
+        temps.append(lse)
+        pl = lse.data_ptr()
+    else:
+        pl = _need(lse, "lse", torch.float32, shape, dev)
+    if ws is None:
+        size = cache._ws_bytes.get(n_q)
+        if size is None:
+            size = cache._ws_bytes[n_q] = max(cp_kv_workspace_size(cache, n_q), 1)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        temps.append(ws)
+        pw = ws.data_ptr()
+    else:
+        pw, size = _need_workspace(ws, dev), ws.numel() * ws.element_size()
+    _launch(dev, stream, temps, "cp_kv_attn", cache.ptr, n_q, pq, _need(lengths, "lengths", torch.int32, (B,), dev), po,
+            1 if part else 0, pl, pw, size)
+    return o, lse
+
+
+class PagePool:
+    """Pages that several sequences may hold, of either cache.
+
+    refs      : int32 [num_pages], the table entries that hold a page (0: it is free)
+    buffers   : tensors [num_pages, ...] that a page consists of (K and V pages of one or all layers, a 4-bit
+                cache's pages and weights)
+    page_size : tokens of a page
+
+    Holds the tensors; tables and lengths stay with the caller.
+    """
+
+    def __init__(self, refs: torch.Tensor, buffers: Sequence[torch.Tensor], page_size: int = CP_KV4_PAGE):
+        r = _need(refs, "refs", torch.int32, (None,), refs.device if isinstance(refs, torch.Tensor) and refs.is_cuda else None)
+        self.refs, self.buffers, self.device, self.num_pages = refs, list(buffers), refs.device, refs.shape[0]
+        self.page_size = page_size
+        base, size = [], []
+        for x in self.buffers:
+            base.append(_need(x, "buffers", x.dtype if isinstance(x, torch.Tensor) else None,
+                              (self.num_pages,) + (None,) * (x.dim() - 1 if isinstance(x, torch.Tensor) else 0), refs.device))
+            size.append(x[0].numel() * x.element_size() if self.num_pages else 16)
+        n = len(base)
+        self._base, self._bytes = (ctypes.c_void_p * n)(*base), (ctypes.c_int64 * n)(*size)
+        self.desc = cp_pages_t(num_pages=self.num_pages, page_size=page_size, refs=r, num_buffers=n,
+                               base=ctypes.cast(self._base, ctypes.POINTER(ctypes.c_void_p)),
+                               bytes=ctypes.cast(self._bytes, ctypes.POINTER(ctypes.c_int64)))
+        self.ptr = ctypes.byref(self.desc)
+        self._ws_bytes = {}
+        _check(_lib.cp_pages_validate(self.ptr), "cp_pages_validate")
+
+    def _workspace(self, num_seqs: int, ws, temps):
+        if ws is not None:
+            return _need_workspace(ws, self.device), ws.numel() * ws.element_size()
+        size = self._ws_bytes.get(num_seqs)
+        if size is None:
+            size = self._ws_bytes[num_seqs] = cp_pages_workspace_size(self, num_seqs)
+        ws = torch.empty(size, dtype=torch.uint8, device=self.device)
+        temps.append(ws)
+        return ws.data_ptr(), size
+
+    def _out(self, t, name, shape, temps):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.int32, device=self.device)
+            temps.append(t)
+            return t, t.data_ptr()
+        return t, _need(t, name, torch.int32, shape, self.device)
+
+
+def cp_pages_validate(pool: PagePool) -> int:
+    return _lib.cp_pages_validate(pool.ptr)
+
+
+def cp_pages_workspace_size(pool: PagePool, num_seqs: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.cp_pages_workspace_size(pool.ptr, num_seqs, ctypes.byref(n)), "cp_pages_workspace_size")
+    return int(n.value)
+
+
+def cp_pages_reserve(pool: PagePool, table, lengths, extra, counts=None, stream=None):
+    """Gives every sequence b of lengths[b] tokens the pages that extra[b] more need, in table [B, max_pages] (in
+    place).  Returns counts int32 [2]: pages in use, and entries that got none (they are -1)."""
+    dev, temps = pool.device, []
+    pt = _need(table, "table", torch.int32, (None, None), dev)
+    B, columns = table.shape
+    counts, pc = pool._out(counts, "counts", (2,), temps)
+    _launch(dev, stream, temps, "cp_pages_reserve", pool.ptr, B, columns, pt,
+            _need(lengths, "lengths", torch.int32, (B,), dev), _need(extra, "extra", torch.int32, (B,), dev), pc)
+    return counts
+
+
+def cp_pages_fork(pool: PagePool, table, lengths, parents, new_table=None, new_lengths=None, counts=None, ws=None,
+                  stream=None):
+    """New sequence b goes on from old sequence parents[b] (below 0: it is empty); the old ones let go of their
+    pages.  Whole pages are shared, a partly filled one is copied for all but the first that takes it.  Returns
+    new_table [len(parents), columns] (-1 behind the last page), new_lengths and counts int32 [2]: pages in use,
+    and entries that got none."""
+    dev, temps = pool.device, []
+    pt = _need(table, "table", torch.int32, (None, None), dev)
+    B, columns = table.shape
+    pp = _need(parents, "parents", torch.int32, (None,), dev)
+    n = parents.shape[0]
+    if new_table is None:
+        new_table, pn = pool._out(None, "", (n, columns), temps)
+    else:
+        pn = _need(new_table, "new_table", torch.int32, (n, None), dev)
+    new_lengths, pl = pool._out(new_lengths, "new_lengths", (n,), temps)
+    counts, pc = pool._out(counts, "counts", (2,), temps)
+    pw, size = pool._workspace(max(B, n), ws, temps)
+    _launch(dev, stream, temps, "cp_pages_fork", pool.ptr, B, columns, pt,
+            _need(lengths, "lengths", torch.int32, (B,), dev), n, new_table.shape[1], pp, pn, pl, pc, pw, size)
+    return new_table, new_lengths, counts
+
+
+def cp_pages_compact(pool: PagePool, table, lengths, new_table=None, moved=None, counts=None, ws=None, stream=None):
+    """Moves the pages in use to the front of the pool.  Returns new_table, the table of the sequences after it (table
+    itself may be given), moved int32 [num_pages], every page's new place (-1: it was free), and counts int32 [2]:
+    pages in use, and 0."""
+    dev, temps = pool.device, []
+    pt = _need(table, "table", torch.int32, (None, None), dev)
+    B, columns = table.shape
+    new_table, pn = pool._out(new_table, "new_table", (B, columns), temps)
+    moved, pm = pool._out(moved, "moved", (pool.num_pages,), temps)
+    counts, pc = pool._out(counts, "counts", (2,), temps)
+    pw, size = pool._workspace(B, ws, temps)
+    _launch(dev, stream, temps, "cp_pages_compact", pool.ptr, B, columns, pt,
+            _need(lengths, "lengths", torch.int32, (B,), dev), pn, pm, pc, pw, size)
+    return new_table, moved, counts
+
+
+def cp_pages_copy(pool: PagePool, src, dst, to: Optional[PagePool] = None, stream=None) -> None:
+    """Copies page src[i] to page dst[i] of pool ``to`` (None: the same; pairs with a negative page are skipped).  No
+    page may be written twice, or read and written, in one call.  refs are not looked at."""
+    dev = pool.device
+    if to is not None and to.device != dev:
+        raise ValueError(f"to: a pool on {dev} is needed")
+    ps = _need(src, "src", torch.int32, (None,), dev)
+    _launch(dev, stream, (), "cp_pages_copy", pool.ptr, (to or pool).ptr, src.shape[0], ps,
+            _need(dst, "dst", torch.int32, (src.shape[0],), dev))
+
+
 def cp_set_debug_checks(on: bool) -> bool:
     """Turns the plan checks on or off for later calls; returns the former setting."""
     prev = ctypes.c_int32(0)
@@ -736,4 +1122,4 @@ def cp_check_bounded_wait(timeout_ns: int = 20_000_000, stream=None) -> int:
     return int(code.value)
 
 
-__all__ = ["Problem", "Kv4Cache", "CpError", "workspace", "LIB_PATH", "EXPORTED"] + EXPORTED
+__all__ = ["Problem", "Kv4Cache", "KvCache", "PagePool", "Rope", "CpError", "workspace", "LIB_PATH", "EXPORTED"] + EXPORTED

@@ -36,6 +36,10 @@ SOURCES = [
     "kv4_host.cu",
     "kv4_cache.cu",
     "kv4_attn.cu",
+    "kv_host.cu",
+    "rope.cu",
+    "kv_attn.cu",
+    "kv_pages.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

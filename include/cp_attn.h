@@ -494,6 +494,187 @@ cp_status_t cp_kv4_attn(const cp_kv4_t* cache, int32_t n_q, const void* q, const
 cp_status_t cp_kv4_evict(const cp_kv4_t* cache, const int32_t* lengths, int32_t budget, int32_t recent,
                          const cp_kv4_t* to, int32_t* new_lengths, int32_t* kept, cp_stream_t stream);
 
+/* Rotary positions.  The source pages say that the positions follow the shard
+ * map ("位置编码必须跟序列分片一起走") and rotate nothing themselves; these calls
+ * have no counterpart there.
+ *
+ * Of every head of d channels the `dims` channels from `first` on are turned in
+ * pairs; pair i is channels (first + i, first + dims/2 + i) (HALVES) or
+ * (first + 2i, first + 2i + 1) (ADJACENT).  A token at positions p[0 .. axes-1]
+ * turns pair i by the angle t = p[axis[i]] * inv_freq[i]:
+ *   a' = factor (a cos t - b sin t),   b' = factor (b cos t + a sin t).
+ * Angles are kept as a 64-bit fraction of a turn (an integer product modulo
+ * 2^64: no precision goes with far or negative positions); sine and cosine in
+ * FP32, the result rounded once. */
+#define CP_ROPE_MAX_AXES 4
+#define CP_ROPE_MAX_DIMS 512
+typedef enum { CP_ROPE_HALVES = 0, CP_ROPE_ADJACENT = 1 } cp_rope_pairing_t;
+
+typedef struct {
+  int32_t first;          /* first turned channel of a head, >= 0             */
+  int32_t dims;           /* turned channels, even, 2 .. CP_ROPE_MAX_DIMS; first + dims <= d */
+  int32_t pairing;        /* cp_rope_pairing_t                                */
+  int32_t axes;           /* position axes, 1 .. CP_ROPE_MAX_AXES             */
+  float factor;           /* on every turned channel (finite; 1: a rotation)  */
+  const uint64_t* turns;  /* device [dims / 2], inv_freq as cp_rope_turns gives it */
+  const int32_t* axis;    /* device [dims / 2], 0 .. axes - 1 (others: recorded, taken as 0), or NULL: 0 */
+} cp_rope_t;
+
+/* turns[i] = inv_freq[i] / (2 pi) modulo 1, in units of 2^-64 (rounded down).
+ * Both on the host; |inv_freq[i]| < 2^32. */
+cp_status_t cp_rope_turns(const double* inv_freq, int32_t pairs, uint64_t* turns);
+
+/* Turns queries and keys (or gradients back) in one pass.
+ *   positions : device int32 [tokens, pos_stride], a token's position on every
+ *               axis in its first columns (pos_stride >= axes; with 4 columns
+ *               cp_shard_permute takes the rows as they are)
+ *   q, k      : device [tokens, hq, d] and [tokens, hkv, d] of `dtype`; hq or
+ *               hkv may be 0 (its pointers are not read)
+ *   q_out, k_out : the same shapes; q itself and k itself (in place), or
+ *               buffers that overlap none of the inputs
+ *   inverse   : 1: turned by -t (the gradient of the call: the transpose, factor
+ *               included), 0: by t */
+cp_status_t cp_rope(const cp_rope_t* rope, int64_t tokens, const int32_t* positions, int32_t pos_stride, int32_t d,
+                    int32_t dtype, int32_t hq, const void* q, void* q_out, int32_t hkv, const void* k, void* k_out,
+                    int32_t inverse, cp_stream_t stream);
+
+/* A paged key/value cache in the model's own type.  No counterpart in the
+ * pages; (o, lse) of cp_kv_attn are in the form that cp_lse_merge joins.
+ *
+ * k_pages [num_pages][hkv][page_size][d_qk], v_pages [num_pages][hkv][page_size]
+ * [d_v], of `dtype`.  Token (slot) j of sequence b is row j % page_size of page
+ * page_table[b][j / page_size].  The rules of the 4-bit cache above hold: shared
+ * pages, entries past the last page, device lengths and tables, and what a
+ * length outside the table or a page outside the pool does (0x300 | site). */
+typedef struct {
+  int32_t num_seqs;          /* B >= 0 sequences (rows of page_table), at most CP_KV4_MAX_SEQS */
+  int32_t hq, hkv;           /* query heads, key/value heads (hq % hkv == 0)     */
+  int32_t d_qk, d_v;         /* d_qk in {64, 128, 192}, d_v in {64, 128}         */
+  int32_t gqa;               /* cp_gqa_t                                         */
+  int32_t dtype;             /* cp_dtype_t of the pages, k, v, q and o           */
+  float scale;               /* softmax scale applied to q.k (> 0, finite)       */
+  int32_t page_size;         /* tokens of a page: 16, 32, 64 or 128              */
+  int32_t num_pages;         /* pages of the pool                                */
+  int32_t max_pages;         /* columns of page_table                            */
+  void* k_pages;             /* device, 16-byte aligned                          */
+  void* v_pages;             /* device, 16-byte aligned                          */
+  const int32_t* page_table; /* device [B][max_pages]                            */
+} cp_kv_t;
+
+/* Check a cache descriptor on the host (no GPU work). */
+cp_status_t cp_kv_validate(const cp_kv_t* cache);
+
+/* Workspace bytes of cp_kv_attn with n_q queries a sequence.  Host only.  The
+ * rules of cp_workspace_size apply. */
+cp_status_t cp_kv_workspace_size(const cp_kv_t* cache, int32_t n_q, size_t* bytes);
+
+/* Writes tokens into the cache, their keys turned on the way: token t, cu[b] <=
+ * t < cu[b+1], becomes slot start[b] + t - cu[b] of sequence b.  The caller
+ * keeps the lengths.
+ *   k, v      : device [src_rows, hkv, d_qk] and [src_rows, hkv, d_v]
+ *   rows      : device int32 [tokens], the row of k, v and positions that token
+ *               t is in (e.g. its sharded row), or NULL: row t
+ *   cu, start, tokens : as in cp_kv4_append
+ *   rope      : NULL: keys as they are
+ *   positions : device int32 [src_rows, pos_stride] (as in cp_rope), or NULL: a
+ *               token's slot, on every axis.  Not read without rope
+ * Two tokens must not go to the same slot. */
+cp_status_t cp_kv_append(const cp_kv_t* cache, const void* k, const void* v, int64_t src_rows, const int32_t* rows,
+                         const int32_t* cu, const int32_t* start, int64_t tokens, const cp_rope_t* rope,
+                         const int32_t* positions, int32_t pos_stride, cp_stream_t stream);
+
+/* Attention of the newest n_q tokens of every sequence over its cache (their
+ * own keys and values appended before).  Query t of sequence b sees slots j <
+ * lengths[b] - (n_q - 1 - t); one that sees none gets o = 0, lse = -inf.  What a
+ * slot that a query does not see holds (NaN, infinities) does not reach it.
+ *   q         : device [B, n_q, hq, d_qk], 1 <= n_q <= CP_KV4_MAX_QUERIES
+ *   lengths   : device int32 [B], tokens held, the new ones among them
+ *   o         : device [B, n_q, hq, d_v], cache.dtype, or float32 with o_f32 = 1
+ *   lse       : device float32 [hq, B * n_q]
+ *   workspace : cp_kv_workspace_size bytes
+ * Products with FP32 accumulation, the softmax in FP32.  BF16 caches: the
+ * probabilities rounded to BF16 for their product with V.  FP32 caches: every
+ * operand as two TF32 terms (the product of both lower ones, 2^-22, left out). */
+cp_status_t cp_kv_attn(const cp_kv_t* cache, int32_t n_q, const void* q, const int32_t* lengths, void* o,
+                       int32_t o_f32, float* lse, void* workspace, size_t workspace_bytes, cp_stream_t stream);
+
+/* Pages held by several sequences, of either cache.  refs[p] is the number of
+ * table entries that hold page p; 0 is free.  The calls below change refs,
+ * tables and pages on the device, in stream order; free pages are taken lowest
+ * first, for the lowest sequence first, so that results do not depend on timing.
+ *
+ * A sequence of n tokens holds the first ceil(n / page_size) entries of its
+ * table row and writes to its last page only, which no other sequence may hold
+ * while it is partly filled: cp_pages_fork sees to that.  An entry outside the
+ * pool is left out (0x300 | 1), a length outside the table clamped (0x300 | 2).
+ * Where the pool has no free page left, the entry becomes -1 and 0x300 | 5 is
+ * recorded.  counts (device int32 [2]): pages in use afterwards (refs not 0),
+ * and entries that got no page.
+ *
+ * buffers: what a page consists of (K and V pages of one or all layers, a 4-bit
+ * cache's pages and weights): page p of buffer i is bytes[i] bytes at base[i] +
+ * p * bytes[i]. */
+#define CP_PAGES_MAX_BUFFERS 128
+typedef struct {
+  int32_t num_pages;       /* >= 0, at most 2^24                               */
+  int32_t page_size;       /* tokens of a page, >= 1                           */
+  int32_t* refs;           /* device [num_pages]                               */
+  int32_t num_buffers;     /* 0 .. CP_PAGES_MAX_BUFFERS                        */
+  void* const* base;       /* HOST, num_buffers device pointers, 16-byte aligned */
+  const int64_t* bytes;    /* HOST, num_buffers sizes, positive multiples of 16 */
+} cp_pages_t;
+
+/* Check a pool descriptor on the host (no GPU work). */
+cp_status_t cp_pages_validate(const cp_pages_t* pool);
+
+/* Workspace bytes of cp_pages_fork and cp_pages_compact with at most num_seqs
+ * sequences, old or new.  Host only.  The rules of cp_workspace_size apply. */
+cp_status_t cp_pages_workspace_size(const cp_pages_t* pool, int32_t num_seqs, size_t* bytes);
+
+/* Room for new tokens: sequence b of lengths[b] tokens gets the pages that
+ * lengths[b] + extra[b] tokens need besides those it holds.
+ *   table   : device int32 [num_seqs][max_pages], entries written behind a
+ *             sequence's last page only
+ *   lengths : device int32 [num_seqs], not changed
+ *   extra   : device int32 [num_seqs], tokens to come (below 0: 0) */
+cp_status_t cp_pages_reserve(const cp_pages_t* pool, int32_t num_seqs, int32_t max_pages, int32_t* table,
+                             const int32_t* lengths, const int32_t* extra, int32_t* counts, cp_stream_t stream);
+
+/* Sequences go on from others, and end: new sequence b takes over the tokens of
+ * old sequence parents[b] (below 0: it is empty), as the beams of a search or
+ * the samples of one prompt do.  The old sequences' holds are dropped; whole
+ * pages are shared; of those that hold a page in part the first keeps it, where
+ * no other sequence of the pool holds it, and every other one gets a free page
+ * with a copy.
+ *   table, lengths         : device int32 [num_seqs][max_pages], [num_seqs]: the
+ *                            old sequences (an entry at the most once a row)
+ *   parents                : device int32 [new_seqs], < num_seqs (others: 0x300 |
+ *                            3, and empty)
+ *   new_table, new_lengths : device int32 [new_seqs][new_max_pages], [new_seqs];
+ *                            -1 behind the last page.  Not the old ones */
+cp_status_t cp_pages_fork(const cp_pages_t* pool, int32_t num_seqs, int32_t max_pages, const int32_t* table,
+                          const int32_t* lengths, int32_t new_seqs, int32_t new_max_pages, const int32_t* parents,
+                          int32_t* new_table, int32_t* new_lengths, int32_t* counts, void* workspace,
+                          size_t workspace_bytes, cp_stream_t stream);
+
+/* Moves the pages in use to the front of the pool: of n pages in use, those
+ * from page n on go, in order, to the free pages below n.
+ *   moved     : device int32 [num_pages], every page's new place, -1: it was free
+ *   table, lengths, new_table : device int32 [num_seqs][max_pages], [num_seqs],
+ *               [num_seqs][max_pages]: a table follows, -1 behind the last page
+ *               (new_table may be table itself) */
+cp_status_t cp_pages_compact(const cp_pages_t* pool, int32_t num_seqs, int32_t max_pages, const int32_t* table,
+                             const int32_t* lengths, int32_t* new_table, int32_t* moved, int32_t* counts,
+                             void* workspace, size_t workspace_bytes, cp_stream_t stream);
+
+/* Copies page src[i] of a pool to page dst[i] of another one with the same
+ * buffers' sizes (or of the same).  Pairs with a negative page are skipped, one
+ * outside its pool as well (0x300 | 1).  No page may be written twice, or read
+ * and written, in one call.  refs are not looked at.
+ *   src, dst : device int32 [n] */
+cp_status_t cp_pages_copy(const cp_pages_t* pool, const cp_pages_t* to, int32_t n, const int32_t* src,
+                          const int32_t* dst, cp_stream_t stream);
+
 /* Forward without a workspace, for callers that cannot allocate device
  * memory.  The source pages have no counterpart to this entry point.
  *
@@ -560,9 +741,10 @@ cp_status_t cp_set_debug_checks(int32_t on, int32_t* previous);
 /* Synchronises `stream`, then returns and clears the device error word of
  * the current device: *code = 0 when every bounded wait since the last call
  * completed, otherwise a nonzero code naming the wait that ran out (and the
- * status CP_ERR_DEVICE_TIMEOUT).  The checks above and the 4-bit cache's
- * (0x300 | site: 1 a page outside the pool, 2 a length and 3 a slot outside the
- * table, 4 a row outside its tensor) report through the same word. */
+ * status CP_ERR_DEVICE_TIMEOUT).  The checks above and the caches' (0x300 |
+ * site: 1 a page outside the pool, 2 a length and 3 a slot or sequence outside
+ * the table, 4 a row outside its tensor, 5 no free page left, 6 an axis that
+ * positions lack) report through the same word. */
 cp_status_t cp_device_status(cp_stream_t stream, int32_t* code);
 
 /* Self-check of the bounded-wait machinery: launches one kernel that waits

@@ -33,6 +33,8 @@ Contents and the passage each follows:
   are merged through the softmax statistics, not averaged).
 * ``kv4``        — the 4-bit key/value cache, attention over it, eviction and a
   prompt's key weights.
+* ``kv``         — rotary positions, attention over a paged cache, pages held by
+  several sequences.
 
 Parity pins for every function live in ``tests/test_oracle_*.py``.
 """
@@ -81,4 +83,10 @@ from .kv4 import (  # noqa: F401
     kv4_quantise,
     kv4_unpack,
     kv4_values,
+)
+from .kv import (  # noqa: F401
+    Pages,
+    kv_attention,
+    rope,
+    rope_turns,
 )

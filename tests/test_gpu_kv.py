@@ -1,0 +1,743 @@
+"""GPU parity of rotary positions, the paged cache in the model's own type and the pages that sequences share,
+against the float64 oracle.
+
+Tolerances, derived from the arithmetic (half steps: fp32 2^-24, bf16 2^-8 of the value):
+* rope: the angle is cut to 32 bits of a turn and rounded to 24 bits of at most an eighth of one (below 2^-24), sine
+  and cosine are off by at most 2 units in the last place (2^-22), times factor (2^-24); two products and their sum
+  round three times: |error| <= (|a| + |b|) |factor| (2^-22 + 4 * 2^-24) < (|a| + |b|) |factor| 2^-21.  The result is
+  rounded to its type.
+* scores: sums in fp32 of products that are exact (bf16) or off by 2^-22 of themselves (fp32: two terms of 11 bits an
+  operand, the product of the lower ones left out; the terms that are kept are exact); up to 24 tensor-core steps a
+  head, each off by at most 2^-23 of the running magnitude, then scale (2^-24) and the exponent's argument (2^-23 of
+  it): SCORE = 2^-18 * scale * sum |q k| covers 32 such steps.
+* lse: the scores' error and 2^-21 of max(1, |lse|) for the sums, their joins and the logarithm.
+* o: probabilities off by SCORE (relative), in bf16 caches rounded to bf16 (2^-8), in fp32 ones split in two terms
+  (2^-22); sums over the slots of a warp in order, n / 8 adds at the most of 2^-24 each, joined twice:
+  |error| <= sum p |v| (2 SCORE + n 2^-27 + 2^-18 + [bf16] 2^-8) + rounding of o.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+cpa = pytest.importorskip("context_long_sequence_zigzag_gb300")
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def _need_cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    yield
+    assert cpa.cp_device_status() == 0
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def randn(rng, shape, dtype):
+    return torch.from_numpy(rng.randn(*shape).astype(np.float32)).to(dtype).cuda()
+
+
+# ---------------------------------------------------------------- rope
+def check_rope(got, x, angle, first, adjacent, factor, inverse):
+    x, m = f64(x), angle.shape[1]
+    want = oracle.rope(x, angle, first, adjacent, factor, inverse)
+    i = np.arange(m)
+    a, b = (first + 2 * i, first + 2 * i + 1) if adjacent else (first + i, first + m + i)
+    room = np.zeros_like(x)
+    room[..., a] = room[..., b] = (np.abs(x[..., a]) + np.abs(x[..., b])) * abs(factor) * 2.0 ** -21
+    still = np.setdiff1d(np.arange(x.shape[-1]), np.concatenate([a, b]))
+    assert np.array_equal(f64(got)[..., still], x[..., still])
+    # (a result next to a rounding border may fall to either side of it: the step of the value and what it is off by)
+    assert np.all(np.abs(f64(got) - want) <= room * (1 + half_step(got.dtype)) + half_step(got.dtype) * np.abs(want) + 1e-30)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,hq,hkv,d,first,pairs,adjacent,axes", [
+    (1, 1, 0, 128, 0, 64, False, 1), (3, 32, 8, 128, 0, 64, False, 1), (701, 5, 1, 128, 0, 64, True, 3),
+    (33, 4, 4, 192, 128, 32, True, 1), (130, 3, 2, 192, 128, 32, False, 2), (17, 2, 1, 64, 0, 32, False, 4),
+    (9, 3, 1, 64, 5, 13, False, 1), (9, 1, 3, 64, 3, 13, True, 2), (5, 1, 1, 1024, 8, 256, False, 1),
+    (4, 2, 1, 1024, 1, 255, True, 1), (5000, 7, 2, 64, 16, 8, True, 1), (2, 1, 1, 16, 0, 1, False, 1),
+    (2, 1, 1, 8, 0, 4, True, 1)])
+def test_rope(T, hq, hkv, d, first, pairs, adjacent, axes, dtype):
+    rng = np.random.RandomState(T)
+    q, k = randn(rng, (T, hq, d), dtype), randn(rng, (T, hkv, d), dtype)
+    f = 10000.0 ** (-rng.permutation(pairs) / pairs)
+    axis = rng.randint(0, axes, pairs)
+    axis[0] = axes - 1
+    pos = rng.randint(-70000, 1 << 20, (T, axes + T % 2))
+    rope = cpa.Rope(f, axis=axis if axes > 1 else None, first=first, pairing="adjacent" if adjacent else "halves")
+    angle = pos[:, axis].astype(np.float64) * f
+    for inverse in (False, True):
+        if hkv == 0:
+            qo, ko = cpa.cp_rope(rope, ints(pos.tolist()), q, inverse=inverse), k
+        else:
+            qo, ko = cpa.cp_rope(rope, ints(pos.tolist()), q, k, inverse=inverse)
+            check_rope(ko, k, angle, first, adjacent, 1.0, inverse)
+        check_rope(qo, q, angle, first, adjacent, 1.0, inverse)
+        # in place: the same bits
+        q2, k2 = q.clone(), k.clone()
+        cpa.cp_rope(rope, ints(pos.tolist()), q2, k2, inverse=inverse, q_out=q2, k_out=k2)
+        assert torch.equal(q2, qo) and (hkv == 0 or torch.equal(k2, ko))
+
+
+def test_rope_far_positions_and_factor():
+    """Positions at both ends of int32, frequencies over a turn a position; angles in exact arithmetic."""
+    rng = np.random.RandomState(3)
+    f = np.array([1.0, 0.1, 3.7, 100.25, 1e-9, -0.5, 0.0, 2.0 ** -31])
+    pos = np.array([0, 1, -1, 2147483647, -2147483648, 123456789, 1 << 30, -77])
+    turns = oracle.rope_turns(f)
+    angle = np.array([[(int(p) * t) % 2 ** 64 / 2 ** 64 * 2 * math.pi for t in turns] for p in pos])
+    # (a product modulo a turn in integers; the frequency's 64 bits are off by 2^-64, times 2^31: 2^-33 of a turn)
+    x = randn(rng, (8, 3, 16), F32)
+    for inverse in (False, True):
+        got = cpa.cp_rope(cpa.Rope(f, factor=-1.75), ints(pos.tolist()), x, inverse=inverse)
+        check_rope(got, x, angle, 0, False, -1.75, inverse)
+
+
+def test_rope_gradient():
+    """dx of sum(g * rope(x)) by differences of the 64-bit formula, and the transposed pass: <g, R x> = <R' g, x>."""
+    rng = np.random.RandomState(4)
+    f, pos = np.array([1.0, 0.01]), np.array([[3], [50]])
+    rope = cpa.Rope(f, first=2, pairing="adjacent", factor=0.7)
+    x, g = randn(rng, (2, 1, 8), F32), randn(rng, (2, 1, 8), F32)
+    dx = f64(cpa.cp_rope(rope, ints(pos.tolist()), g, inverse=True))
+    loss = lambda y: (f64(g) * oracle.rope(y, pos * f, 2, True, 0.7)).sum()  # noqa: E731
+    for i in np.ndindex(2, 1, 8):
+        e = np.zeros((2, 1, 8))
+        e[i] = 1e-3  # (the loss is linear in x: differences are exact but for 64-bit rounding)
+        slope = (loss(f64(x) + e) - loss(f64(x) - e)) / 2e-3
+        assert abs(slope - dx[i]) <= 2.0 ** -21 * 0.7 * 2 * np.abs(f64(g)).max() + 2.0 ** -24 * abs(slope) + 1e-10
+    y = f64(cpa.cp_rope(rope, ints(pos.tolist()), x))
+    assert abs((f64(g) * y).sum() - (dx * f64(x)).sum()) <= 1e-5
+
+
+def test_rope_positions_follow_the_shard_map():
+    """Rows and their positions through cp_shard_permute, rope in sharded order, and back: the global result."""
+    rng = np.random.RandomState(5)
+    cu, T = [0, 300, 517], 517
+    prob = cpa.Problem(T, 4, 2, 64, 64, 4, "zigzag", cu)
+    q, k = randn(rng, (T, 4, 64), BF), randn(rng, (T, 2, 64), BF)
+    pos = np.zeros((T, 4), np.int64)  # four columns: rows of 16 bytes
+    pos[:, 0] = np.concatenate([np.arange(300), np.arange(217)])
+    pos[:, 1], pos[:, 2] = rng.randint(0, 90, T), rng.randint(0, 90, T)
+    axis = np.repeat([0, 1, 2], [12, 10, 10])
+    rope = cpa.Rope(10000.0 ** (-np.arange(32) / 32), axis=axis)
+    at = ints(pos.tolist())
+    want = cpa.cp_rope(rope, at, q, k)
+    sh = [cpa.cp_shard_permute(prob, x) for x in (at, q, k)]
+    got = [cpa.cp_shard_permute(prob, x, inverse=True) for x in cpa.cp_rope(rope, *sh)]
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_rope_records_an_axis_that_positions_lack():
+    rope = cpa.Rope([1.0, 0.5], axis=[0, 1])
+    rope.axis.copy_(ints([0, 3]))
+    x = torch.ones(2, 1, 8, device="cuda")
+    got = cpa.cp_rope(rope, ints([[1, 2], [3, 4]]), x)
+    assert cpa.cp_device_status() == 0x306
+    check_rope(got, x, np.array([[1.0, 0.5], [3.0, 1.5]]), 0, False, 1.0, False)  # axis 0 in its place
+
+
+# ---------------------------------------------------------------- append
+def pool_of(lengths, page, rng, extra=2, columns=None):
+    need = [-(-n // page) for n in lengths]
+    order = rng.permutation(sum(need) + extra)
+    table = rng.randint(-5, 1 << 20, (len(lengths), max(need + [1]) if columns is None else columns))  # (junk is not read)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    return len(order), table
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("start,counts,hkv,d_qk,d_v,page,rope,given", [
+    ([0], [1], 8, 128, 128, 64, "halves", True), ([5, 0, 63, 100], [1, 1, 1, 1], 2, 64, 64, 16, "adjacent", False),
+    ([0, 15, 16], [33, 0, 130], 1, 192, 128, 32, "halves", False), ([0], [700], 8, 128, 128, 128, None, False),
+    ([3, 7], [0, 1000], 4, 128, 64, 64, "odd", True), ([1], [5000], 3, 192, 64, 16, "tail", True)])
+def test_append(start, counts, hkv, d_qk, d_v, page, rope, given, dtype):
+    rng = np.random.RandomState(6)
+    n = sum(counts)
+    after = [a + m for a, m in zip(start, counts)]
+    pages, table = pool_of(after, page, rng)
+    src = n + 3
+    rows = rng.permutation(src)[:n]
+    k, v = randn(rng, (src, hkv, d_qk), dtype), randn(rng, (src, hkv, d_v), dtype)
+    k_pages, v_pages = (torch.full((pages, hkv, page, d), 7.0, dtype=dtype, device="cuda") for d in (d_qk, d_v))
+    cache = cpa.KvCache(k_pages, v_pages, ints(table.tolist()), hkv)
+    slot = np.concatenate([np.arange(a, b) for a, b in zip(start, after)])
+    seq = np.repeat(np.arange(len(counts)), counts)
+    pairs, first, adjacent = {None: (0, 0, 0), "halves": (d_qk // 2, 0, 0), "adjacent": (d_qk // 2, 0, 1),
+                              "odd": (21, 3, 0), "tail": (32, d_qk - 64, 1)}[rope]
+    f = 1000.0 ** (-np.arange(pairs) / max(pairs, 1))
+    pos = rng.randint(0, 100000, (src, 2))
+    handle = cpa.Rope(f, first=first, pairing="adjacent" if adjacent else "halves", factor=1.25) if rope else None
+    tokens = n + 5  # padding behind the last sequence
+    row_list = np.concatenate([rows, rng.randint(-9, src + 9, 5)])
+    cpa.cp_kv_append(cache, k, v, ints(np.concatenate([[0], np.cumsum(counts)]).tolist()), ints(start),
+                     rows=ints(row_list.tolist())[:tokens], rope=handle,
+                     positions=ints(pos.tolist()) if given and rope else None)
+    got_k, got_v = f64(k_pages).transpose(0, 2, 1, 3), f64(v_pages).transpose(0, 2, 1, 3)
+    page_of = table[seq, slot // page]
+    assert np.array_equal(got_v[page_of, slot % page], f64(v)[rows])
+    if rope:
+        p = pos[rows, 0] if given else slot
+        check_rope(torch.from_numpy(got_k[page_of, slot % page]).to(dtype), k[torch.from_numpy(rows).cuda()],
+                   p[:, None] * f[None], first, bool(adjacent), 1.25, False)
+    else:
+        assert np.array_equal(got_k[page_of, slot % page], f64(k)[rows])
+    mark = np.ones((pages, page), bool)
+    mark[page_of, slot % page] = False
+    assert np.all(got_k[mark] == 7) and np.all(got_v[mark] == 7)
+
+
+def test_append_leaves_out_what_does_not_fit():
+    k = torch.ones(4, 1, 64, device="cuda")
+    for table, start, rows, code in (([[0, 99]], 14, None, 0x301), ([[0, 1]], 30, None, 0x303),
+                                     ([[0, 1]], -2, None, 0x303), ([[0, 1]], 0, [0, 4, 1, 2], 0x304)):
+        k_pages, v_pages = torch.zeros(2, 1, 16, 64, device="cuda"), torch.zeros(2, 1, 16, 64, device="cuda")
+        cache = cpa.KvCache(k_pages, v_pages, ints(table), 1)
+        cpa.cp_kv_append(cache, k, k, ints([0, 4]), ints([start]), rows=None if rows is None else ints(rows),
+                         rope=cpa.Rope([0.0]))
+        assert cpa.cp_device_status() == code
+        fits = [s for s in range(start, start + 4) if 0 <= s < (16 if code == 0x301 else 32)]
+        fits = fits if rows is None else [0, 2, 3]
+        got = v_pages[:, 0, :, 0].flatten().cpu().numpy()
+        assert sorted(np.nonzero(got)[0]) == fits
+        assert torch.equal(k_pages, v_pages)
+
+
+# ---------------------------------------------------------------- attention
+class Held:
+    """A pool that holds random tokens at the slots of some sequences and `fill` everywhere else."""
+
+    def __init__(self, lengths, hq, hkv, d_qk, d_v, dtype, page, n_q=1, gqa="blocked", scale=None, seed=0,
+                 fill=math.nan, columns=None, spread=1.0):
+        rng = np.random.RandomState(seed)
+        self.pages, self.table = pool_of(lengths, page, rng, columns=columns)
+        self.lengths, self.hq, self.hkv, self.page, self.n_q, self.gqa = lengths, hq, hkv, page, n_q, gqa
+        self.scale = d_qk ** -0.5 if scale is None else scale
+        self.k, self.v = ([randn(rng, (n, hkv, d), dtype) for n in lengths] for d in (d_qk, d_v))
+        self.q = randn(rng, (len(lengths), n_q, hq, d_qk), dtype) * spread
+        self.kp, self.vp = (torch.full((self.pages, hkv, page, d), fill, dtype=dtype, device="cuda") for d in (d_qk, d_v))
+        for b in range(len(lengths)):
+            self.put(b)
+        self.cache = cpa.KvCache(self.kp, self.vp, ints(self.table.tolist()).reshape(len(lengths), -1), hq, self.scale, gqa)
+
+    def put(self, b):
+        at = np.arange(self.lengths[b])
+        pg, row = torch.from_numpy(self.table[b, at // self.page].astype(np.int64)).cuda(), torch.from_numpy(at % self.page).cuda()
+        self.kp[pg, :, row], self.vp[pg, :, row] = self.k[b], self.v[b]
+
+    def kv_of(self, h):
+        return h % self.hkv if self.gqa == "interleaved" else h // (self.hq // self.hkv)
+
+    def check(self, o, lse, visible=None, rows=None):
+        """visible(b, t): indexes of the slots that a query sees; default the call's rule."""
+        dtype = self.kp.dtype
+        step = 2.0 ** -8 if dtype == BF else 0.0
+        if visible is None:
+            visible = lambda b, t: np.arange(max(self.lengths[b] - (self.n_q - 1 - t), 0))  # noqa: E731
+        o, lse, B = f64(o), f64(lse), len(self.lengths)
+        for b in range(B):
+            k, v, q = f64(self.k[b]), f64(self.v[b]), f64(self.q[b])
+            seen = [visible(b, t) for t in range(self.n_q)]
+            for h in range(self.hq):
+                c = self.kv_of(h)
+                want, want_lse = oracle.kv_attention(q[:, h], k[:, c], v[:, c], seen, self.scale)
+                for t in range(self.n_q):
+                    if rows is not None and not rows(b, t, h):
+                        continue
+                    got, got_lse = o[b, t, h], lse[h, b * self.n_q + t]
+                    if len(seen[t]) == 0:
+                        assert np.all(got == 0) and got_lse == -np.inf
+                        continue
+                    kk, vv = k[seen[t], c], v[seen[t], c]
+                    score = 2.0 ** -18 * self.scale * (np.abs(kk) @ np.abs(q[t, h])).max()
+                    p = np.exp(kk @ q[t, h] * self.scale - want_lse[t])
+                    room = (p @ np.abs(vv)) * (2 * score + len(kk) * 2.0 ** -27 + 2.0 ** -18 + step)
+                    assert abs(got_lse - want_lse[t]) <= score + 2.0 ** -21 * max(1, abs(want_lse[t])), (b, t, h)
+                    out = half_step(BF if self.out == BF else F32)
+                    assert np.all(np.abs(got - want[t]) <= room * (1 + out) + out * np.abs(want[t])), (b, t, h)
+
+    out = F32
+
+    def run(self, part=False, **kw):
+        o, lse = cpa.cp_kv_attn(self.cache, self.q, ints(self.lengths), part=part, **kw)
+        self.out = o.dtype
+        return o, lse
+
+
+CASES = [  # lengths, hq, hkv, d_qk, d_v, page, n_q, gqa
+    ([1], 1, 1, 64, 64, 16, 1, "blocked"),
+    ([0, 1, 15, 16, 17, 63, 64, 65, 200], 8, 2, 128, 128, 16, 1, "blocked"),
+    ([129, 0, 31, 1000], 6, 2, 128, 128, 32, 1, "interleaved"),
+    ([5000, 3, 70], 32, 8, 128, 128, 64, 1, "blocked"),
+    ([300, 513], 4, 4, 192, 128, 64, 1, "blocked"),
+    ([2, 1, 0, 100, 33], 4, 2, 128, 64, 128, 4, "blocked"),
+    ([64, 129, 5], 8, 1, 64, 128, 64, 3, "blocked"),
+    ([40, 700], 7, 1, 192, 64, 32, 1, "blocked"),
+    ([7, 450], 16, 1, 128, 128, 64, 2, "interleaved"),
+    ([90, 1200], 12, 2, 128, 128, 16, 8, "interleaved"),
+    ([20, 333], 16, 1, 64, 64, 64, 16, "blocked"),
+    ([257], 71, 1, 128, 128, 64, 1, "blocked"),
+    ([77, 0, 600], 24, 1, 192, 128, 128, 5, "blocked"),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_attn(case, dtype):
+    """All that no query sees holds NaN."""
+    lengths, hq, hkv, d_qk, d_v, page, n_q, gqa = case
+    h = Held(lengths, hq, hkv, d_qk, d_v, dtype, page, n_q, gqa)
+    o, lse = h.run()
+    assert o.dtype == dtype
+    h.check(o, lse)
+    o32, lse32 = h.run(part=True)
+    h.check(o32, lse32)
+    assert o32.dtype == F32 and torch.equal(lse, lse32) and torch.equal(o32.to(dtype), o)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attn_long(dtype):
+    """One long sequence among short ones; few heads: every CTA has a part of it."""
+    h = Held([70001, 9, 0, 301], 4, 2, 128, 128, dtype, 64, seed=2)
+    h.check(*h.run())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attn_many_sequences(dtype):
+    rng = np.random.RandomState(7)
+    lengths = [int(x) for x in rng.randint(0, 90, 700)]
+    h = Held(lengths, 2, 1, 64, 64, dtype, 16, seed=3)
+    h.check(*h.run(), rows=lambda b, t, x: b % 7 == 0 or lengths[b] < 2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_attn_slots_that_some_queries_see(dtype, bad):
+    """A value (or key) that the last queries see does not reach the ones before."""
+    n_q = 6
+    h = Held([133, 64, 66, 5], 4, 2, 128, 64, dtype, 64, n_q, seed=4)
+    for b, n in enumerate(h.lengths):
+        h.v[b][n - 2, :, 3] = bad  # seen by the last two queries
+        h.k[b][n - 1, 1, 7] = bad  # seen by the last one
+        h.put(b)
+    o, lse = h.run()
+    h.check(o, lse, rows=lambda b, t, x: t < n_q - 2)
+    o = f64(o)
+    for b in range(4):
+        assert not np.isfinite(o[b, n_q - 2, :, 3]).any()
+        others = [c for c in range(64) if c != 3]
+        assert np.isfinite(o[b, n_q - 2][:, others]).all()
+        assert np.isfinite(o[b, n_q - 1, :2][:, others]).all()  # (heads of the first key head)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attn_queries_that_are_not_finite(dtype):
+    h = Held([100, 40], 8, 2, 64, 64, dtype, 32, 2, seed=5)
+    h.q[0, 1, 2, 5], h.q[1, 0, 7, 0] = math.nan, math.inf
+    o, lse = h.run()
+    h.check(o, lse, rows=lambda b, t, x: (b, t, x) not in ((0, 1, 2), (1, 0, 7)))
+    assert torch.isnan(o[0, 1, 2]).all() and torch.isnan(lse[2, 1]) and torch.isnan(o[1, 0, 7]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attn_magnitudes(dtype):
+    """Scores from -2e4 to 2e4: one slot takes all, whichever comes first; keys of zero: the mean."""
+    h = Held([300, 301], 4, 1, 64, 64, dtype, 64, seed=6, spread=3000.0)
+    o, lse = h.run()
+    for b in range(2):
+        s = f64(h.q[b, 0]) @ f64(h.k[b])[:, 0].T * h.scale
+        gap = np.sort(s, 1)
+        for x in range(4):
+            if gap[x, -1] - gap[x, -2] > 60:  # (the others' probabilities are below 1e-26)
+                assert np.array_equal(f64(o)[b, 0, x], f64(h.v[b])[s[x].argmax(), 0])
+    h = Held([500], 2, 2, 128, 128, dtype, 64, seed=7)
+    h.k[0].zero_()
+    h.put(0)
+    h.check(*h.run())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attn_pages_and_lengths_outside(dtype):
+    """A page outside the pool: its slots are absent.  A length outside the table: clamped.  Both are recorded."""
+    h = Held([200, 90, 130], 4, 2, 128, 128, dtype, 16, seed=8, columns=13)
+    h.table[0, 3], h.table[0, 12], h.table[2, 0] = 1 << 20, -1, h.pages
+    h.cache.page_table.copy_(ints(h.table.tolist()))
+    o, lse = h.run()
+    assert cpa.cp_device_status() == 0x301
+    gone = {0: [3, 12], 1: [], 2: [0]}
+    h.check(o, lse, visible=lambda b, t: np.array([j for j in range(h.lengths[b]) if j // 16 not in gone[b]], int))
+    h = Held([13 * 16, 0], 4, 2, 128, 128, dtype, 16, seed=9)
+    o, lse = cpa.cp_kv_attn(h.cache, h.q, ints([13 * 16 + 5, -3]))
+    assert cpa.cp_device_status() == 0x302
+    h.out = dtype
+    h.check(o, lse)
+    # all of a sequence's pages outside: it sees nothing
+    h.cache.page_table.fill_(-1)
+    o, lse = h.run()
+    assert cpa.cp_device_status() == 0x301
+    assert (o == 0).all() and (lse == -math.inf).all()
+
+
+def test_attn_joins_with_lse_merge():
+    """A cache split over two ranks, read rank by rank and joined: the whole cache's result."""
+    h = Held([400], 4, 2, 128, 128, BF, 64, seed=10)
+    whole, whole_lse = h.run(part=True)
+    prob = cpa.Problem(1, 4, 2, 128, 128, 1)
+    parts = []
+    for lo, n in ((0, 256), (4, 144)):
+        table = ints([h.table[0, lo:].tolist()])
+        parts.append(cpa.cp_kv_attn(cpa.KvCache(h.kp, h.vp, table, 4), h.q, ints([n]), part=True))
+    (o, lse), (o2, lse2) = parts
+    o, lse = o.view(1, 4, 128), lse.view(4, 1)
+    cpa.cp_lse_merge(prob, o, lse, o2.view(1, 4, 128), lse2.view(4, 1))
+    h.out = F32
+    h.check(o.view(1, 1, 4, 128), lse)
+    assert torch.allclose(o.view_as(whole), whole, atol=1e-2) and torch.allclose(lse, whole_lse, atol=1e-4)
+
+
+# ---------------------------------------------------------------- pages
+def random_batch(rng, page, B, most, pages, share=True):
+    """Lengths, table and refs of sequences that share whole pages with the one before, now and then."""
+    free = list(rng.permutation(pages))
+    lengths, rows, refs = [], [], np.zeros(pages, int)
+    for b in range(B):
+        n = int(rng.randint(0, most + 1))
+        row = []
+        if share and b and rng.rand() < 0.6:
+            common = int(rng.randint(0, min(n, lengths[-1]) // page + 1))
+            row = rows[-1][:common]
+        while len(row) < -(-n // page):
+            row.append(int(free.pop()))
+        refs[row] += 1
+        lengths.append(n)
+        rows.append(row)
+    return lengths, rows, refs
+
+
+def as_table(rows, columns, fill=-1):
+    return [list(r) + [fill] * (columns - len(r)) for r in rows]
+
+
+def buffers_of(rng, pages, kinds=((BF, 128), (F32, 36), (torch.uint8, 48 * 1024 + 16))):
+    out = []
+    for dtype, n in kinds:
+        x = rng.randint(0, 200, (pages, n))
+        out.append(torch.from_numpy(x).to(dtype).cuda())
+    return out
+
+
+@pytest.mark.parametrize("B,new,most,page,pages,seed", [
+    (1, 1, 5, 64, 3, 0), (3, 5, 100, 16, 64, 1), (8, 8, 300, 32, 400, 2), (40, 70, 130, 16, 1000, 3),
+    (5, 0, 50, 16, 40, 4), (0, 3, 0, 16, 9, 5), (30, 64, 100, 16, 215, 6), (1500, 2500, 40, 16, 12000, 7)])
+def test_fork_and_reserve(B, new, most, page, pages, seed):
+    rng = np.random.RandomState(seed)
+    lengths, rows, refs = random_batch(rng, page, B, most, pages)
+    columns = -(-most // page) + 1
+    kinds = ((BF, 128), (F32, 36), (torch.uint8, 48 * 1024 + 16)) if pages < 2000 else ((BF, 24),)
+    bufs = buffers_of(rng, pages, kinds)
+    before = [x.clone() for x in bufs]
+    pool = cpa.PagePool(ints(refs.tolist()), bufs, page)
+    parents = [int(x) for x in rng.randint(-1, max(B, 1), new)] if B else [-1] * new
+    table = ints(as_table(rows, columns, 1 << 28)).reshape(B, columns)
+    model = oracle.Pages(refs, page)
+    t, n, counts = cpa.cp_pages_fork(pool, table, ints(lengths), ints(parents))
+    want, want_n, want_counts, pairs = model.fork(as_table(rows, columns), lengths, parents)
+    short = want_counts[1]
+    assert cpa.cp_device_status() == (0x305 if short else 0)
+    assert t.tolist() == as_table(want, columns) and n.tolist() == want_n and counts.tolist() == want_counts
+    assert pool.refs.tolist() == model.refs
+    for x, y in zip(bufs, before):
+        for a, b in pairs:
+            y[b] = y[a]
+        assert torch.equal(x, y)
+    extra = [int(x) for x in rng.randint(-2, 2 * page, new)]
+    extra = [min(x, columns * page - m) for x, m in zip(extra, want_n)]
+    counts = cpa.cp_pages_reserve(pool, t, n, ints(extra))
+    held = as_table(want, columns)
+    want, want_counts = model.reserve(held, want_n, extra)
+    assert cpa.cp_device_status() == (0x305 if want_counts[1] else 0)
+    assert t.tolist() == as_table(want, columns) and counts.tolist() == want_counts and pool.refs.tolist() == model.refs
+    assert n.tolist() == want_n
+
+
+def test_fork_of_pages_held_elsewhere():
+    """A page that is partly filled for one sequence and whole for another, or held outside the batch: not written."""
+    pool = cpa.PagePool(ints([2, 1, 0, 0, 2]), [torch.arange(5.0, device="cuda").repeat(4, 1).t().contiguous()], 4)
+    t, n, counts = cpa.cp_pages_fork(pool, ints([[0, -1], [0, 1], [4, -1]]), ints([2, 7, 3]), ints([0, 1, 2]))
+    assert t.tolist() == [[2, -1], [0, 1], [3, -1]] and n.tolist() == [2, 7, 3] and counts.tolist() == [5, 0]
+    assert pool.refs.tolist() == [1, 1, 1, 1, 1] and pool.buffers[0][:, 0].tolist() == [0, 1, 0, 4, 4]
+
+
+def test_page_calls_record_what_does_not_fit():
+    make = lambda refs: cpa.PagePool(ints(refs), [], 4)  # noqa: E731
+    pool = make([1, 1, 0])
+    t, n, _ = cpa.cp_pages_fork(pool, ints([[0, 9]]), ints([8]), ints([0]))  # a page outside the pool
+    assert cpa.cp_device_status() == 0x301 and t.tolist() == [[0, -1]] and pool.refs.tolist() == [1, 1, 0]
+    pool = make([1, 1, 0])
+    t, n, _ = cpa.cp_pages_fork(pool, ints([[0, 1]]), ints([9]), ints([0]))  # longer than its row
+    assert cpa.cp_device_status() == 0x302 and n.tolist() == [8] and pool.refs.tolist() == [1, 1, 0]
+    t, n, _ = cpa.cp_pages_fork(pool, ints([[0, 1]]), ints([8]), ints([1, -7]))  # no such parent
+    assert cpa.cp_device_status() == 0x303 and n.tolist() == [0, 0] and pool.refs.tolist() == [0, 0, 0]
+    pool = make([1, 1, 0])  # a new row too short for its parent's tokens
+    t, n, _ = cpa.cp_pages_fork(pool, ints([[0, 1]]), ints([7]), ints([0]), new_table=ints([[5]]))
+    assert cpa.cp_device_status() == 0x302 and t.tolist() == [[0]] and n.tolist() == [4] and pool.refs.tolist() == [1, 0, 0]
+    pool = make([1, 0, 0, 0])
+    t = ints([[0, 8]])
+    c = cpa.cp_pages_reserve(pool, t, ints([3]), ints([2147483647]))  # past the row
+    assert cpa.cp_device_status() == 0x302 and t.tolist() == [[0, 1]] and c.tolist() == [2, 0]
+
+
+@pytest.mark.parametrize("B,most,page,pages,seed", [
+    (4, 100, 16, 60, 0), (1, 0, 64, 5, 1), (0, 0, 64, 7, 2), (60, 200, 16, 2000, 3), (9, 64, 64, 9, 4), (0, 0, 16, 0, 5),
+    (300, 500, 16, 70001, 6)])
+def test_compact(B, most, page, pages, seed):
+    rng = np.random.RandomState(seed)
+    lengths, rows, refs = random_batch(rng, page, B, most, pages)
+    columns = -(-most // page) + 1
+    refs[rng.permutation(pages)[:pages // 10]] += 1  # held by others
+    kinds = ((BF, 128), (torch.uint8, 36 * 1024)) if pages < 9000 else ((BF, 24),)
+    bufs = buffers_of(rng, pages, kinds)
+    before = [x.clone() for x in bufs]
+    pool = cpa.PagePool(ints(refs.tolist()).reshape(pages), bufs, page)
+    table = ints(as_table(rows, columns, -9)).reshape(B, columns)
+    model = oracle.Pages(refs, page)
+    new, moved, counts = cpa.cp_pages_compact(pool, table, ints(lengths).reshape(B))
+    goes, pairs = model.compact()
+    assert moved.tolist() == goes and pool.refs.tolist() == model.refs
+    assert counts.tolist() == model.counts(0)
+    assert new.tolist() == as_table([[goes[p] for p in r] for r in rows], columns)
+    for x, y in zip(bufs, before):
+        if pairs:
+            a, b = (torch.tensor(z, device="cuda") for z in zip(*pairs))
+            y[b] = y[a]
+        assert torch.equal(x, y)
+    # once more, in place: nothing moves
+    again, moved, _ = cpa.cp_pages_compact(pool, new, ints(lengths).reshape(B), new_table=new)
+    assert again is new and moved.tolist() == [p if r else -1 for p, r in enumerate(model.refs)]
+    assert new.tolist() == as_table([[goes[p] for p in r] for r in rows], columns)
+
+
+def test_copy():
+    rng = np.random.RandomState(11)
+    a, b = (cpa.PagePool(ints([0] * n), buffers_of(rng, n)) for n in (12, 7))
+    src, dst = [3, 11, -1, 5, 2, 12, 4], [6, 0, 1, -4, 3, 1, 7]
+    want = [y.clone() for y in b.buffers]
+    for y, x in zip(want, a.buffers):
+        for s, d in ((3, 6), (11, 0), (2, 3)):
+            y[d] = x[s]
+    cpa.cp_pages_copy(a, ints(src), ints(dst), to=b)
+    assert cpa.cp_device_status() == 0x301
+    assert all(torch.equal(x, y) for x, y in zip(b.buffers, want))
+    want = [x.clone() for x in a.buffers]
+    for y in want:
+        y[1] = y[0]
+    cpa.cp_pages_copy(a, ints([0]), ints([1]))
+    assert all(torch.equal(x, y) for x, y in zip(a.buffers, want))
+
+
+# ---------------------------------------------------------------- together
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_decoding_with_beams(dtype):
+    """A prompt in zigzag shards into the cache, then steps of a beam search: every beam's attention is that of its own
+    tokens' keys and values, whatever pages it shares."""
+    rng = np.random.RandomState(12)
+    T, hq, hkv, d, page, beams, steps = 150, 4, 2, 64, 16, 3, 20
+    prob = cpa.Problem(T, hq, hkv, d, d, 2, "zigzag", dtype=dtype)
+    k, v = randn(rng, (T, hkv, d), dtype), randn(rng, (T, hkv, d), dtype)
+    at = torch.arange(T, dtype=torch.int32, device="cuda").view(T, 1).repeat(1, 4)
+    rope = cpa.Rope(1000.0 ** (-np.arange(d // 2) / (d // 2)))
+    ks, vs, pos = (cpa.cp_shard_permute(prob, x) for x in (k, v, at))
+    rows = cpa.cp_shard_permute(prob, at, inverse=True)[:, 0].contiguous()
+    pages, columns = 60, 16
+    kp, vp = (torch.full((pages, hkv, page, d), math.nan, dtype=dtype, device="cuda") for _ in range(2))
+    pool = cpa.PagePool(torch.zeros(pages, dtype=torch.int32, device="cuda"), [kp, vp], page)
+    table, lengths = ints([[-1] * columns]), ints([0])
+    cpa.cp_pages_reserve(pool, table, lengths, ints([T]))
+    cpa.cp_kv_append(cpa.KvCache(kp, vp, table, hq), ks, vs, ints([0, T]), lengths, rows=rows, rope=rope, positions=pos)
+    lengths = ints([T])
+    whole = f64(oracle_turn(rope, k, np.arange(T), dtype))
+    story = [(whole, f64(v))]
+    parents = [0] * beams
+    for step in range(steps):
+        table, lengths, _ = cpa.cp_pages_fork(pool, table, lengths, ints(parents))
+        cpa.cp_pages_reserve(pool, table, lengths, ints([1] * beams))
+        cache = cpa.KvCache(kp, vp, table, hq)
+        kn, vn, q = randn(rng, (beams, hkv, d), dtype), randn(rng, (beams, hkv, d), dtype), randn(rng, (beams, hq, d), dtype)
+        cpa.cp_kv_append(cache, kn, vn, ints(list(range(beams + 1))), lengths, rope=rope)
+        turned = f64(oracle_turn(rope, kn, np.full(beams, T + step), dtype))
+        story = [(np.concatenate([story[p][0], turned[b:b + 1]]), np.concatenate([story[p][1], f64(vn)[b:b + 1]]))
+                 for b, p in enumerate(parents)]
+        qt = cpa.cp_rope(rope, lengths, q)
+        lengths = lengths + 1
+        o, lse = cpa.cp_kv_attn(cache, qt.view(beams, 1, hq, d), lengths)
+        for b in range(beams):
+            for h in range(hq):
+                kk, vv = (x[:, h // 2] for x in story[b])
+                want, want_lse = oracle.kv_attention(f64(qt)[b, h:h + 1], kk, vv, [np.arange(len(kk))], d ** -0.5)
+                # keys are off by a rounding where the kernel's and the oracle's fall to two sides of a border
+                off = d ** -0.5 * (np.abs(kk) @ np.abs(f64(qt)[b, h])).max() * (2 * half_step(dtype) + 2.0 ** -18)
+                p = np.exp(kk @ f64(qt)[b, h] * d ** -0.5 - want_lse[0])
+                assert abs(f64(lse)[h, b] - want_lse[0]) <= off + 2.0 ** -20
+                room = p @ np.abs(vv) * (2 * off + 2.0 ** -17 + half_step(dtype)) + half_step(dtype) * np.abs(want[0])
+                assert np.all(np.abs(f64(o)[b, 0, h] - want[0]) <= room * (1 + half_step(dtype)))
+        parents = [int(x) for x in rng.randint(0, beams, beams)]
+    table, lengths, counts = cpa.cp_pages_fork(pool, table, lengths, ints([-1]))
+    assert counts.tolist() == [0, 0] and not pool.refs.any()
+
+
+def oracle_turn(rope, k, pos, dtype):
+    f = 1000.0 ** (-np.arange(rope.dims // 2) / (rope.dims // 2))
+    return torch.from_numpy(oracle.rope(f64(k), pos[:, None] * f[None])).to(dtype)
+
+
+def test_fork_of_a_4bit_cache():
+    """The same calls over the 4-bit cache's pages and weights."""
+    rng = np.random.RandomState(13)
+    hkv, d, pages = 2, 64, 6
+    q4 = torch.zeros(pages, hkv, cpa.cp_kv4_block_bytes(d, d), dtype=torch.uint8, device="cuda")
+    w = torch.zeros(pages, hkv, 64, device="cuda")
+    pool = cpa.PagePool(torch.zeros(pages, dtype=torch.int32, device="cuda"), [q4, w])
+    table, lengths = ints([[-1, -1]]), ints([0])
+    cpa.cp_pages_reserve(pool, table, lengths, ints([80]))
+    k, v = randn(rng, (80, hkv, d), BF), randn(rng, (80, hkv, d), BF)
+    cpa.cp_kv4_append(cpa.Kv4Cache(q4, table, hkv, hkv, d, d, w), k, v, ints([0, 80]), ints([0]))
+    old, _ = cpa.cp_kv4_read(cpa.Kv4Cache(q4, table, hkv, hkv, d, d, w), ints([0, 80]), ints([0]), 80)
+    table, lengths, counts = cpa.cp_pages_fork(pool, table, ints([80]), ints([0, 0]))
+    assert counts.tolist() == [3, 0]
+    cache = cpa.Kv4Cache(q4, table, hkv, hkv, d, d, w)
+    got, _ = cpa.cp_kv4_read(cache, ints([0, 80, 160]), ints([0, 0]), 160)
+    assert torch.equal(got[:80], old) and torch.equal(got[80:], old)
+
+
+# ---------------------------------------------------------------- streams, graphs, refusals
+def test_on_another_stream_and_in_a_graph():
+    rng = np.random.RandomState(14)
+    h = Held([100, 37, 250], 8, 2, 128, 128, BF, 32, seed=15, columns=16)
+    rope = cpa.Rope(10000.0 ** (-np.arange(64) / 64))
+    o, lse = h.run()
+    side = torch.cuda.Stream()
+    n, five = ints(h.lengths), ints([5])
+    side.wait_stream(torch.cuda.current_stream())
+    o2, lse2 = cpa.cp_kv_attn(h.cache, h.q, n, stream=side)
+    x = cpa.cp_rope(rope, five, h.q[0], stream=side)
+    side.synchronize()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(x, cpa.cp_rope(rope, ints([5]), h.q[0]))
+    # a captured step, replayed with new lengths, parents and tokens
+    pool = cpa.PagePool(ints([0] * (h.pages + 40)), [torch.cat([h.kp, h.kp.new_zeros(40, *h.kp.shape[1:])]),
+                                                    torch.cat([h.vp, h.vp.new_zeros(40, *h.vp.shape[1:])])], 32)
+    refs = [0] * (h.pages + 40)
+    for b, n in enumerate(h.lengths):
+        for p in h.table[b, :-(-n // 32)]:
+            refs[p] += 1
+    table, lengths = h.cache.page_table.clone(), ints(h.lengths)
+    parents, extra = ints([0, 1, 2]), ints([1, 1, 1])
+    kn, vn, q = randn(rng, (3, 2, 128), BF), randn(rng, (3, 2, 128), BF), randn(rng, (3, 1, 8, 128), BF)
+    cu = ints([0, 1, 2, 3])
+
+    def step():
+        t, n, _ = cpa.cp_pages_fork(pool, table, lengths, parents)
+        cpa.cp_pages_reserve(pool, t, n, extra)
+        cache = cpa.KvCache(*pool.buffers, t, 8)
+        cpa.cp_kv_append(cache, kn, vn, cu, n, rope=rope)
+        new = n + extra
+        return (t, new) + cpa.cp_kv_attn(cache, q, new)
+
+    fresh = [x.clone() for x in pool.buffers]
+
+    def begin():
+        pool.refs.copy_(ints(refs))
+        for x, y in zip(pool.buffers, fresh):
+            x.copy_(y)
+
+    begin()
+    step()
+    torch.cuda.synchronize()
+    begin()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for new in ([0, 1, 2], [2, 2, 0], [1, -1, 1]):
+        parents.copy_(ints(new))
+        extra.copy_(ints([int(p >= 0) for p in new]))
+        q.copy_(randn(rng, (3, 1, 8, 128), BF))
+        begin()
+        graph.replay()
+        got = [x.clone() for x in out]
+        begin()
+        want = step()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        # (a beam that has ended has no page for the token that it is given)
+        assert cpa.cp_device_status() == (0x301 if -1 in new else 0)
+
+
+def test_two_graphs_over_one_workspace_in_turn():
+    a, b = Held([900, 3], 4, 2, 64, 64, BF, 64, seed=16), Held([17, 2100], 4, 2, 64, 64, BF, 64, seed=17)
+    ws = torch.empty(max(cpa.cp_kv_workspace_size(x.cache) for x in (a, b)), dtype=torch.uint8, device="cuda")
+    lengths = [ints(x.lengths) for x in (a, b)]
+    want = [x.run() for x in (a, b)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x, n in zip((a, b), lengths):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(cpa.cp_kv_attn(x.cache, x.q, n, ws=ws))
+        graphs.append(g)
+    ws.fill_(255)
+    for i in (0, 1, 1, 0):
+        graphs[i].replay()
+        assert torch.equal(outs[i][0], want[i][0]) and torch.equal(outs[i][1], want[i][1])
+
+
+def test_refusals():
+    h = Held([40], 4, 2, 64, 64, BF, 16)
+    n = ints(h.lengths)
+    rope = cpa.Rope([1.0, 0.5], axis=[0, 1])
+    for call in (
+            lambda: cpa.cp_kv_attn(h.cache, h.q.float(), n), lambda: cpa.cp_kv_attn(h.cache, h.q[..., :32], n),
+            lambda: cpa.cp_kv_attn(h.cache, h.q, n.long()), lambda: cpa.cp_kv_attn(h.cache, h.q.cpu(), n),
+            lambda: cpa.cp_kv_attn(h.cache, h.q, n, o=torch.empty(1, 1, 4, 64, device="cuda")),
+            lambda: cpa.cp_kv_append(h.cache, h.k[0], h.v[0][:3], ints([0, 1]), n),
+            lambda: cpa.cp_kv_append(h.cache, h.k[0], h.v[0], ints([0, 1, 2]), n),
+            lambda: cpa.cp_kv_append(h.cache, h.k[0], h.v[0], ints([0, 1]), n, positions=ints([0] * 40)),
+            lambda: cpa.cp_kv_append(h.cache, h.k[0], h.v[0], ints([0, 1]), n, rope=rope, positions=ints([0] * 40)),
+            lambda: cpa.cp_rope(rope, ints([[1, 2]]), h.q[0].half()), lambda: cpa.cp_rope(rope, ints([1]), h.q[0]),
+            lambda: cpa.cp_rope(rope, ints([[1, 2]]), h.q[0].transpose(1, 2)),
+            lambda: cpa.cp_rope(rope, ints([[1, 2], [1, 2]]), h.q[0]),
+            lambda: cpa.KvCache(h.kp, h.vp[:, :1], ints([[0]]), 4), lambda: cpa.KvCache(h.kp, h.vp.float(), ints([[0]]), 4),
+            lambda: cpa.KvCache(h.kp[:, :, ::2], h.vp[:, :, ::2], ints([[0]]), 4),
+            lambda: cpa.PagePool(ints([0, 0]), [torch.zeros(3, 16, device="cuda")]),
+            lambda: cpa.PagePool(ints([0, 0]).long(), [])):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: cpa.KvCache(h.kp, h.vp, ints([[0]]), 3), lambda: cpa.PagePool(ints([0, 0]), [torch.zeros(2, 3, device="cuda")]),
+                 lambda: cpa.cp_kv_attn(h.cache, h.q, n, ws=torch.empty(16, dtype=torch.uint8, device="cuda")),
+                 lambda: cpa.cp_rope(rope, ints([[1, 2]]), torch.zeros(1, 1, 2, device="cuda")),
+                 lambda: cpa.cp_rope(rope, ints([[1, 2]]), h.q[0], q_out=h.q[0], k=h.q[0], k_out=h.q[0])):
+        with pytest.raises(cpa.CpError):
+            call()
+    for x in (h.q[0, :, :0], h.q[0][:0]):
+        assert cpa.cp_rope(rope, ints([[1, 2]])[:x.shape[0]], x).shape == x.shape
+    empty = cpa.KvCache(h.kp, h.vp, torch.empty(0, 3, dtype=torch.int32, device="cuda"), 4)
+    o, lse = cpa.cp_kv_attn(empty, h.q[:0], n[:0])
+    assert o.shape == (0, 1, 4, 64) and lse.shape == (4, 0)
