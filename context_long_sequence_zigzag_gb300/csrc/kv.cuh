@@ -91,6 +91,8 @@ int sm_count();  // of the current device
 cudaError_t launch_rope(const RopeArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_kv_append(const KvAppendArgs& a, int dtype, cudaStream_t st);
 size_t kv_attn_workspace(const cp_kv_t* c, int32_t n_q);
+// units of work of the longest sequences that the table can hold
+int64_t kv_attn_units(const cp_kv_t* c, int32_t n_q);
 cudaError_t launch_kv_attn(const KvAttnArgs& a, int dqk, int dv, int dtype, cudaStream_t st);
 
 // ---- pages ----

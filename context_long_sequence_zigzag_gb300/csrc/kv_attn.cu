@@ -1,73 +1,793 @@
 // kv_attn.cu — attention of the newest tokens over the paged cache in the
-// model's own type: a CTA a query row, a warp a slot at a time, on CUDA cores.
+// model's own type: o = sum_j p_j v_j, p = softmax(scale q.k), one pass over
+// the cache with the running maximum and sum of the softmax.
+//
+// What bounds it: the cache's bytes, read once (d_qk + d_v elements a slot and
+// head for 4 (d_qk + d_v) G n_q FLOPs / 2).  With the 1 to 64 rows that share
+// a head a 128-row tcgen05 tile would be mostly empty and its accumulator a
+// detour through TMEM; warp-level MMAs of 16 rows keep up with the copies.
+//
+// Work.  A run is one sequence's slots for one kv head and up to 16, 32 or 64
+// of its rows (query heads of the group times new tokens); its tiles are TT
+// slots.  All runs' tiles laid end to end (a run's start counts as one more)
+// are cut evenly over the CTAs, on the device, from the lengths: a long
+// sequence keeps every SM busy, and a captured graph replays with new lengths.
+// A cut run's parts go to the workspace and a second kernel joins them, whose
+// launch overlaps the first.
+//
+// A CTA: a producer warp looks the pages up and brings tiles of K and V in by
+// TMA, 128-byte swizzled panels through a ring of stages; queries come two
+// runs ahead.  Four compute warps share every tile: MT of them side by side in
+// rows, the others along the slots, each with its own maximum, sum and O, which
+// meet once a run, in shared memory.
+#include <cuda.h>
+
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "kv.cuh"
+#include "sm103_ptx.cuh"
 
 namespace cpattn {
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn get_encode_tiled();
+
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;  // that compute; one more produces
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kJoinFloats = 2048;
+constexpr int kMostStages = 6;
+constexpr float kLog2e = 1.4426950408889634f;
+// log2 units: a row's reference maximum follows a new one past this (p stays below 2^8 relative to it, so that most
+// tiles leave O as it is)
+constexpr float kRescale = 8.f;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+enum : int { kSiteQFull = 0x60, kSiteQEmpty, kSiteKFull, kSiteVFull, kSiteEmpty, kSiteJoin, kSiteDrain };
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename E_, int DQK_, int DV_, int MT_>
+struct Cfg {
+  using E = E_;
+  static constexpr bool F32 = sizeof(E) == 4;
+  static constexpr int DQK = DQK_, DV = DV_, MT = MT_;
+  static constexpr int NS = kWarps / MT;       // warps along a tile's slots
+  static constexpr int TT = F32 ? 32 : 64;     // slots of a tile
+  static constexpr int TS = TT / NS;           // of a warp
+  static constexpr int ROWS = 16 * MT;
+  static constexpr int KP = DQK * sizeof(E) / 128, VP = DV * sizeof(E) / 128;  // panels of 128 bytes
+  static constexpr uint32_t KBYTES = KP * TT * 128, VBYTES = VP * TT * 128, STAGE = KBYTES + VBYTES;
+  static constexpr uint32_t QPITCH = DQK * sizeof(E) + 16;  // (rows of a fragment in different banks)
+  static constexpr uint32_t QBYTES = (ROWS * QPITCH + 127) / 128 * 128;
+};
 
-template <typename E>
-__global__ void __launch_bounds__(32 * kWarps) kv_attn_kernel(const KvAttnArgs a, const int dqk, const int dv) {
-  __shared__ float om[kWarps][128], ml[kWarps][2];
-  const int row = blockIdx.x, hq = a.c.hq, h = row % hq, t = row / hq % a.n_q, b = row / (hq * a.n_q);
-  const int kvh = a.c.inter ? h % a.c.hkv : h / (hq / a.c.hkv);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = kv_length(__ldg(a.lengths + b), int64_t(a.c.max_pages) << a.c.page_shift, a.c.err) - (a.n_q - 1 - t);
-  const E* q = static_cast<const E*>(a.q) + int64_t(row) * dqk;
-  float qr[6], o[4] = {}, m = -INFINITY, l = 0.f;
-  for (int i = 0; i < 6; ++i) qr[i] = 32 * i < dqk ? to_f(q[32 * i + lane]) * a.c.scale : 0.f;
-  int seen = 0;
-  for (int j = warp; j < n; j += kWarps) {
-    const int32_t pg = kv_page(__ldg(a.c.table + int64_t(b) * a.c.max_pages + (j >> a.c.page_shift)), a.c.num_pages, a.c.err);
-    if (pg < 0) continue;
-    seen = 1;
-    const int64_t r = ((int64_t(pg) * a.c.hkv + kvh) << a.c.page_shift) + (j & ((1 << a.c.page_shift) - 1));
-    float s = 0.f;
-    for (int i = 0; i < 6; ++i)
-      if (32 * i < dqk) s = fmaf(qr[i], to_f(static_cast<const E*>(a.c.k)[r * dqk + 32 * i + lane]), s);
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
-    const float top = fmaxf(m, s), ref = top == -INFINITY ? 0.f : top, f = expf(m - ref), p = expf(s - ref);
-    m = top;
-    l = l * f + p;
-    for (int i = 0; i < 4; ++i)
-      if (32 * i < dv) o[i] = fmaf(p, to_f(static_cast<const E*>(a.c.v)[r * dv + 32 * i + lane]), o[i] * f);
+struct RunDesc {
+  int32_t b, head, row0, len;  // b < 0: no more
+  int32_t lo, hi;              // tiles of this part
+  int32_t whole, slot;         // whole: no parts to join; otherwise the part's slot
+};
+
+struct Tail {  // shared memory behind the stages and queries
+  float join[kJoinFloats];
+  float m[kWarps][16], l[kWarps][16];
+  float2 row[64];  // maximum and sum of a row
+  RunDesc run[2];
+  int32_t absent[kMostStages];  // a stage's pages that are outside the pool, a bit each
+  int32_t warp_units[kWarps + 1];
+  int32_t start_b, start_off, total;
+  int abort, drain_abort;
+  uint64_t q_full[2], q_empty[2], k_full[kMostStages], v_full[kMostStages], empty[kMostStages], joined;
+};
+
+struct Params {
+  KvAttnArgs a;
+  CUtensorMap tk, tv;
+  int32_t group, rows, row_tiles;  // G; rows of a kv head; runs they take
+  int32_t box_shift;               // log2 of the slots a copy brings: a page's, at most a tile's
+  int32_t stages;
+  int4* meta;    // [ctas]: sequence, head and row tile, number of parts of the run that is cut behind this CTA
+  float* parts;  // [ctas][2][ROWS][DV + 2]
+};
+
+// units of a sequence's run: its tiles and its start
+__device__ __forceinline__ int units_of(int len, int tt) { return (len + tt - 1) / tt + 1; }
+
+__device__ __forceinline__ uint32_t round_tf32(float x) { return (__float_as_uint(x) + 0x1000u) & 0xffffe000u; }
+// x as two terms of 11 bits
+__device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
+  hi = round_tf32(x);
+  lo = round_tf32(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+  return reinterpret_cast<const uint32_t&>(p);
+}
+
+// Address of 16-byte piece `c` of a slot's row in a tile of panels.
+template <int PANELS>
+__device__ __forceinline__ uint32_t piece(uint32_t tile, int shift, int slot, int c) {
+  return tile + (((slot >> shift) * PANELS + (c >> 3)) << (7 + shift)) + ((slot & ((1 << shift) - 1)) << 7) +
+         (((c ^ slot) & 7) << 4);
+}
+
+// A row's maximum score (before the scale) and sum: what O is multiplied by, and its lse.  A row that saw nothing (or scores of -inf
+// alone) has -inf and 0; a NaN stays one.
+__device__ __forceinline__ float inverse_of(float2 ml) { return ml.y == 0.f ? 0.f : 1.f / ml.y; }
+__device__ __forceinline__ float lse_of(float2 ml, float scale) {
+  return ml.y == 0.f ? -INFINITY : fmaf(ml.x == -INFINITY ? 0.f : ml.x, scale, logf(ml.y));
+}
+
+template <typename C>
+__global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_constant__ Params p) {
+  using E = typename C::E;
+  constexpr int TT = C::TT, MT = C::MT, NS = C::NS, DV = C::DV;
+  extern __shared__ uint8_t raw[];
+  const uint32_t base = (ptx::smem_u32(raw) + 1023) & ~1023u;
+  const uint32_t queries = base + p.stages * C::STAGE;
+  Tail& sh = *reinterpret_cast<Tail*>(raw + (queries + 2 * C::QBYTES - ptx::smem_u32(raw)));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const KvCache& c = p.a.c;
+  ptx::grid_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(ptx::smem_u32(&sh.q_full[i]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sh.q_empty[i]), kWarps);
+    }
+    for (int i = 0; i < p.stages; ++i) {
+      ptx::mbar_init(ptx::smem_u32(&sh.k_full[i]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sh.v_full[i]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sh.empty[i]), kWarps);
+    }
+    ptx::mbar_init(ptx::smem_u32(&sh.joined), kWarps);
+    ptx::fence_barrier_init();
+    sh.abort = sh.drain_abort = 0;
   }
-  seen = __syncthreads_or(seen);
-  for (int i = 0; i < 4; ++i) om[warp][32 * i + lane] = o[i];
-  if (lane == 0) ml[warp][0] = m, ml[warp][1] = l;
+  // rows past the last of a run stay 0
+  for (uint32_t i = tid * 16; i < 2 * C::QBYTES; i += kThreads * 16)
+    *reinterpret_cast<uint4*>(raw + (queries - ptx::smem_u32(raw)) + i) = make_uint4(0, 0, 0, 0);
+  ptx::fence_proxy_async_smem();
+
+  // where this CTA's share begins: a thread adds up some sequences in a row
+  const int64_t most = int64_t(c.max_pages) << c.page_shift;
+  const int runs = c.hkv * p.row_tiles;
+  const int per = (c.num_seqs + kThreads - 1) / kThreads, b0 = min(tid * per, c.num_seqs), b1 = min(b0 + per, c.num_seqs);
+  int units = 0;
+  for (int b = b0; b < b1; ++b) units += units_of(kv_length(__ldg(p.a.lengths + b), most, c.err), TT) * runs;
+  int before = units;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(~0u, before, d);
+    if (lane >= d) before += x;
+  }
+  if (lane == 31) sh.warp_units[warp] = before;
   __syncthreads();
-  float top = -INFINITY, sum = 0.f, out = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][0]);
-  const float ref = top == -INFINITY ? 0.f : top;
-  for (int w = 0; w < kWarps; ++w) {
-    const float f = expf(ml[w][0] - ref);
-    sum += f * ml[w][1];
-    if (threadIdx.x < dv) out += f * om[w][threadIdx.x];
+  int total = 0;
+  for (int w = 0; w <= kWarps; ++w) {
+    if (w == warp) before += total;
+    total += sh.warp_units[w];
   }
-  if (threadIdx.x < dv) {
-    const float x = seen ? out / sum : 0.f;
-    const int64_t at = int64_t(row) * dv + threadIdx.x;
-    if (a.o_f32) static_cast<float*>(a.o)[at] = x;
-    else static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(x);
+  before -= units;
+  const int n = min(int(gridDim.x), total), cta = blockIdx.x;
+  const int u0 = cta < n ? int(int64_t(total) * cta / n) : total, u1 = cta < n ? int(int64_t(total) * (cta + 1) / n) : total;
+  if (before <= u0 && u0 < before + units) {
+    int off = u0 - before, b = b0;
+    for (;; ++b) {
+      const int x = units_of(kv_length(__ldg(p.a.lengths + b), most, nullptr), TT) * runs;
+      if (off < x) break;
+      off -= x;
+    }
+    sh.start_b = b, sh.start_off = off;
   }
-  if (threadIdx.x == 0) a.lse[int64_t(h) * a.c.num_seqs * a.n_q + b * a.n_q + t] = ref + logf(sum);
+  __syncthreads();
+  const ptx::WaitCtx ctx{&sh.abort, c.err, kWaitLimitNs};
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ producer
+    int stage = 0, phase = 0, tiles_sent = 0, runs_sent = 0;
+    int4 cut = make_int4(0, 0, 0, 0);
+    bool ok = true;
+    int b = u0 < u1 ? sh.start_b : 0, off = u0 < u1 ? sh.start_off : 0;
+    for (int u = u0; u < u1 && ok;) {
+      const int len = kv_length(__ldg(p.a.lengths + b), most, nullptr);
+      const int tiles = (len + TT - 1) / TT, per_run = tiles + 1, r = off / per_run, at = off - r * per_run;
+      const int take = min(per_run - at, u1 - u);
+      const int lo = max(at - 1, 0), hi = at + take - 1;
+      if (hi > lo || tiles == 0) {
+        const int head = r / p.row_tiles, row0 = (r - head * p.row_tiles) * C::ROWS, rows = min(C::ROWS, p.rows - row0);
+        const int slot = runs_sent & 1;
+        if (runs_sent >= 2) ok = ptx::mbar_wait(ptx::smem_u32(&sh.q_empty[slot]), (runs_sent / 2 - 1) & 1, kSiteQEmpty, ctx);
+        if (!__all_sync(~0u, ok)) { ok = false; break; }
+        const bool first = lo == 0, last = hi == tiles;
+        const uint32_t bar = ptx::smem_u32(&sh.q_full[slot]);
+        if (lane == 0) {
+          sh.run[slot] = RunDesc{b, head, row0, len, lo, hi, first && last, cta * 2 + (first ? 1 : 0)};
+          ptx::mbar_arrive_expect_tx(bar, hi > lo ? rows * C::DQK * sizeof(E) : 0);
+        }
+        __syncwarp();
+        if (first && !last)  // the CTA with the run's last unit
+          cut = make_int4(b, r, int((int64_t(u - at + per_run) * n + total - 1) / total) - 1 - cta + 1, 0);
+        if (hi > lo) {
+          for (int i = lane; i < rows; i += 32) {
+            const int t = (row0 + i) / p.group, g = row0 + i - t * p.group;
+            const int h = c.inter ? head + g * c.hkv : head * p.group + g;
+            ptx::bulk_load(queries + slot * C::QBYTES + i * C::QPITCH,
+                           static_cast<const E*>(p.a.q) + ((int64_t(b) * p.a.n_q + t) * c.hq + h) * C::DQK,
+                           C::DQK * sizeof(E), bar);
+          }
+          // pages of the part, 32 at a time, a lane each
+          const int32_t* table = c.table + int64_t(b) * c.max_pages;
+          const int pages = (len + (1 << c.page_shift) - 1) >> c.page_shift;
+          int window = -32;
+          int32_t held = -1;
+          const int boxes = TT >> p.box_shift;
+          for (int tile = lo; tile < hi && ok; ++tile) {
+            const int e0 = (tile * TT) >> c.page_shift;
+            if (e0 + boxes > window + 32 || window < 0) {
+              window = e0;
+              held = window + lane < pages ? kv_page(__ldg(table + window + lane), c.num_pages, c.err) : -1;
+            }
+            if (tiles_sent >= p.stages) ok = ptx::mbar_wait(ptx::smem_u32(&sh.empty[stage]), phase ^ 1, kSiteEmpty, ctx);
+            if (!__all_sync(~0u, ok)) { ok = false; break; }
+            const int slot0 = tile * TT + (lane << p.box_shift);  // of this lane's copy
+            const int32_t page = __shfl_sync(~0u, held, ((slot0 >> c.page_shift) - window) & 31);
+            const bool mine = lane < boxes && slot0 < len;
+            const unsigned copies = __ballot_sync(~0u, mine && page >= 0), gone = __ballot_sync(~0u, mine && page < 0);
+            const uint32_t kbar = ptx::smem_u32(&sh.k_full[stage]), vbar = ptx::smem_u32(&sh.v_full[stage]);
+            if (lane == 0) {
+              sh.absent[stage] = int32_t(gone);
+              ptx::mbar_arrive_expect_tx(kbar, __popc(copies) * (C::KBYTES / TT << p.box_shift));
+              ptx::mbar_arrive_expect_tx(vbar, __popc(copies) * (C::VBYTES / TT << p.box_shift));
+            }
+            __syncwarp();
+            if (mine && page >= 0) {
+              const int row = ((page * c.hkv + head) << c.page_shift) + (slot0 & ((1 << c.page_shift) - 1));
+              const uint32_t to = base + stage * C::STAGE;
+              ptx::tma_load_3d(to + lane * (C::KBYTES / TT << p.box_shift), &p.tk, kbar, 0, row, 0);
+              ptx::tma_load_3d(to + C::KBYTES + lane * (C::VBYTES / TT << p.box_shift), &p.tv, vbar, 0, row, 0);
+            }
+            ++tiles_sent;
+            if (++stage == p.stages) stage = 0, phase ^= 1;
+          }
+        }
+        ++runs_sent;
+      }
+      u += take;
+      off += take;
+      if (off == per_run * runs) ++b, off = 0;
+    }
+    if (lane == 0) {
+      if (ok) {
+        const int slot = runs_sent & 1;
+        if (runs_sent < 2 || ptx::mbar_wait(ptx::smem_u32(&sh.q_empty[slot]), (runs_sent / 2 - 1) & 1, kSiteQEmpty, ctx)) {
+          sh.run[slot].b = -1;
+          ptx::mbar_arrive(ptx::smem_u32(&sh.q_full[slot]));
+        }
+      }
+      p.meta[cta] = cut;
+      // no copy is in flight when the CTA's shared memory goes to the next one (computing warps that gave up did not wait)
+      const ptx::WaitCtx drain{&sh.drain_abort, c.err, kWaitLimitNs};
+      for (int i = max(tiles_sent - p.stages, 0); i < tiles_sent; ++i) {
+        ptx::mbar_wait(ptx::smem_u32(&sh.k_full[i % p.stages]), i / p.stages & 1, kSiteDrain, drain);
+        ptx::mbar_wait(ptx::smem_u32(&sh.v_full[i % p.stages]), i / p.stages & 1, kSiteDrain, drain);
+      }
+      for (int i = max(runs_sent - 2, 0); i < runs_sent; ++i)
+        if (!ok) ptx::mbar_wait(ptx::smem_u32(&sh.q_full[i & 1]), i / 2 & 1, kSiteDrain, drain);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- compute
+  const int mt = warp % MT, slice = warp / MT;
+  const int first_slot = slice * C::TS;  // of this warp in a tile
+  const int r0 = lane >> 2, quad = lane & 3;
+  const float cs = c.scale * kLog2e;
+  int stage = 0, phase = 0, join_phase = 0;
+  bool ok = true;
+  auto meet = [&] {
+    __syncwarp();
+    const uint32_t bar = ptx::smem_u32(&sh.joined);
+    if (lane == 0) ptx::mbar_arrive(bar);
+    ok = __all_sync(~0u, ptx::mbar_wait(bar, join_phase, kSiteJoin, ctx));
+    join_phase ^= 1;
+  };
+  for (int run = 0; ok; ++run) {
+    const int qslot = run & 1;
+    ok = ptx::mbar_wait(ptx::smem_u32(&sh.q_full[qslot]), run / 2 & 1, kSiteQFull, ctx);
+    ok = __all_sync(~0u, ok);
+    if (!ok) break;
+    const RunDesc d = sh.run[qslot];
+    if (d.b < 0) break;
+    const uint32_t q_at = queries + qslot * C::QBYTES + (mt * 16 + (lane & 7) + (lane & 8)) * C::QPITCH + (lane >> 4) * 16;
+    uint32_t qf[C::F32 ? 1 : C::DQK / 16][4];
+    if constexpr (!C::F32) {
+#pragma unroll
+      for (int k = 0; k < C::DQK / 16; ++k) ptx::ldmatrix_x4(qf[k], q_at + k * 32);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.q_empty[qslot]));
+    }
+    // slots that this lane's two rows see
+    int see[2], query[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = d.row0 + mt * 16 + r0 + 8 * i;
+      query[i] = row / p.group;
+      see[i] = row < p.rows ? d.len - (p.a.n_q - 1 - query[i]) : 0;
+    }
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[DV / 8][4];
+#pragma unroll
+    for (int i = 0; i < DV / 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+
+    for (int tile = d.lo; tile < d.hi; ++tile) {
+      const uint32_t kt = base + stage * C::STAGE, vt = kt + C::KBYTES;
+      ok = __all_sync(~0u, ptx::mbar_wait(ptx::smem_u32(&sh.k_full[stage]), phase, kSiteKFull, ctx));
+      if (!ok) break;
+      const int absent = sh.absent[stage];
+      constexpr int NB = C::TS / 8;  // blocks of 8 slots
+      float s[NB][4];
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+      if constexpr (C::F32) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int slot = first_slot + 8 * i + (lane & 7);
+          float low[4] = {0.f, 0.f, 0.f, 0.f};  // the products with lower terms, added in the end
+#pragma unroll 2
+          for (int k = 0; k < C::DQK / 16; ++k) {  // two steps of 8 channels
+            uint32_t kf[4], a[2][4];
+            ptx::ldmatrix_x4(kf, piece<C::KP>(kt, p.box_shift, slot, 4 * k + (lane >> 3)));
+            ptx::ldmatrix_x4(a[0], q_at + k * 64);
+            ptx::ldmatrix_x4(a[1], q_at + k * 64 + 32);
+            float high[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t ah[4], al[4], bh[2], bl[2];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) split(__uint_as_float(a[x][j]), ah[j], al[j]);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) split(__uint_as_float(kf[2 * x + j]), bh[j], bl[j]);
+              ptx::mma_1688(low, ah, bl[0], bl[1]);
+              ptx::mma_1688(low, al, bh[0], bh[1]);
+              ptx::mma_1688(high, ah, bh[0], bh[1]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] += high[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[i][j] += low[j];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NB; i += 2) {
+          const int slot = first_slot + 8 * i + (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+          for (int k = 0; k < C::DQK / 16; ++k) {
+            uint32_t kf[4];
+            ptx::ldmatrix_x4(kf, piece<C::KP>(kt, p.box_shift, slot, 2 * k + ((lane >> 3) & 1)));
+            ptx::mma_16816(s[i], qf[k], kf[0], kf[1]);
+            ptx::mma_16816(s[i + 1], qf[k], kf[2], kf[3]);
+          }
+        }
+      }
+      // what not every row sees
+      const int tile0 = tile * TT + first_slot;
+      const bool masked = (tile + 1) * TT > d.len - (p.a.n_q - 1) || absent;
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int x = first_slot + 8 * i + 2 * quad + (j & 1);
+            if (tile * TT + x >= see[j >> 1] || (absent >> (x >> p.box_shift) & 1)) s[i][j] = -INFINITY;
+          }
+      }
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top[j >> 1] = fmaxf(top[j >> 1], s[i][j]);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], 1));
+        top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], 2));
+      }
+      if (__any_sync(~0u, (top[0] - m[0]) * cs > kRescale || (top[1] - m[1]) * cs > kRescale)) {
+        float f[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float next = fmaxf(m[x], top[x]);
+          f[x] = next == -INFINITY ? 1.f : ptx::ex2((m[x] - next) * cs);
+          m[x] = next;
+          l[x] *= f[x];
+        }
+#pragma unroll
+        for (int i = 0; i < DV / 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[i][j] *= f[j >> 1];
+      }
+      const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = ptx::ex2((s[i][j] - ref[j >> 1]) * cs);  // (the largest: exactly 1, however large)
+          l[j >> 1] += s[i][j];
+        }
+
+      ok = __all_sync(~0u, ptx::mbar_wait(ptx::smem_u32(&sh.v_full[stage]), phase, kSiteVFull, ctx));
+      if (!ok) break;
+      // O += P V.  GUARD: slots from `end` on and absent ones count as 0 whatever they hold.  ONE: rows of one query only.
+      auto product = [&](auto guard, auto one, int end, int only) {
+        constexpr bool GUARD = decltype(guard)::value, ONE = decltype(one)::value;
+        auto seen = [&](int x) { return tile * TT + x < end && !(absent >> (x >> p.box_shift) & 1); };
+        auto add = [&](float (&acc)[4], auto&& f) {
+          if constexpr (ONE) {
+            float t[4] = {acc[0], acc[1], acc[2], acc[3]};
+            f(t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (query[j >> 1] == only) acc[j] = t[j];
+          } else {
+            f(acc);
+          }
+        };
+        auto prob = [&](float x, int j) { return !ONE || query[j >> 1] == only ? x : 0.f; };
+        if constexpr (C::F32) {
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const int x = first_slot + 8 * i + 2 * quad;  // the MMA's k = quad and quad + 4: slots x and x + 1
+            uint32_t ah[4], al[4];
+            split(prob(s[i][0], 0), ah[0], al[0]);
+            split(prob(s[i][2], 2), ah[1], al[1]);
+            split(prob(s[i][1], 1), ah[2], al[2]);
+            split(prob(s[i][3], 3), ah[3], al[3]);
+            const bool in0 = !GUARD || seen(x), in1 = !GUARD || seen(x + 1);
+#pragma unroll
+            for (int nb = 0; nb < DV / 8; ++nb) {
+              const int ch = 8 * nb + r0;
+              const uint32_t off = (ch & 3) * 4;
+              float v[2];
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0]) : "r"(piece<C::VP>(vt, p.box_shift, x, ch >> 2) + off) : "memory");
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[1]) : "r"(piece<C::VP>(vt, p.box_shift, x + 1, ch >> 2) + off) : "memory");
+              if (!in0) v[0] = 0.f;
+              if (!in1) v[1] = 0.f;
+              uint32_t bh[2], bl[2];
+              split(v[0], bh[0], bl[0]);
+              split(v[1], bh[1], bl[1]);
+              add(o[nb], [&](float (&acc)[4]) {
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                ptx::mma_1688(t, ah, bl[0], bl[1]);
+                ptx::mma_1688(t, al, bh[0], bh[1]);
+                ptx::mma_1688(t, ah, bh[0], bh[1]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[j] += t[j];
+              });
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NB; i += 2) {
+            const uint32_t a[4] = {pack_bf16(prob(s[i][0], 0), prob(s[i][1], 1)), pack_bf16(prob(s[i][2], 2), prob(s[i][3], 3)),
+                                   pack_bf16(prob(s[i + 1][0], 0), prob(s[i + 1][1], 1)),
+                                   pack_bf16(prob(s[i + 1][2], 2), prob(s[i + 1][3], 3))};
+            uint32_t mask[2] = {~0u, ~0u};
+            if constexpr (GUARD) {
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int x = first_slot + 8 * (i + y) + 2 * quad;
+                mask[y] = (seen(x) ? 0xffffu : 0u) | (seen(x + 1) ? 0xffff0000u : 0u);
+              }
+            }
+            const int slot = first_slot + 8 * i + (lane & 7) + (lane & 8);
+#pragma unroll
+            for (int nb = 0; nb < DV / 8; nb += 2) {
+              uint32_t vf[4];
+              ptx::ldmatrix_x4_trans(vf, piece<C::VP>(vt, p.box_shift, slot, nb + (lane >> 4)));
+              if constexpr (GUARD) vf[0] &= mask[0], vf[1] &= mask[1], vf[2] &= mask[0], vf[3] &= mask[1];
+              add(o[nb], [&](float (&acc)[4]) { ptx::mma_16816(acc, a, vf[0], vf[1]); });
+              add(o[nb + 1], [&](float (&acc)[4]) { ptx::mma_16816(acc, a, vf[2], vf[3]); });
+            }
+          }
+        }
+      };
+      if (!masked) {
+        product(std::false_type{}, std::false_type{}, 0, 0);
+      } else {
+        // 0 times a value that is not finite is not 0: slots that only later queries see are looked at first
+        bool bad = false;
+        const int from = max(d.len - (p.a.n_q - 1), tile0), to = min(d.len, tile0 + C::TS);
+        for (int x = from; x < to; ++x)
+          for (int i = lane; i < DV * int(sizeof(E)) / 16; i += 32) {
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(piece<C::VP>(vt, p.box_shift, x - tile * TT, i))
+                         : "memory");
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              bad = bad || (w[j] & 0x7f800000u) == 0x7f800000u;
+              if (!C::F32) bad = bad || (w[j] & 0x7f80u) == 0x7f80u;
+            }
+          }
+        if (!__any_sync(~0u, bad)) {
+          product(std::true_type{}, std::false_type{}, d.len, 0);
+        } else {
+          for (int t = 0; t < p.a.n_q; ++t) product(std::true_type{}, std::true_type{}, d.len - (p.a.n_q - 1 - t), t);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.empty[stage]));
+      if (++stage == p.stages) stage = 0, phase ^= 1;
+    }
+    if (!ok) break;
+    if constexpr (C::F32) {
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.q_empty[qslot]));
+    }
+
+    // ---- the warps along the slots meet
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      l[x] += __shfl_xor_sync(~0u, l[x], 1);
+      l[x] += __shfl_xor_sync(~0u, l[x], 2);
+      if (quad == 0) sh.m[warp][r0 + 8 * x] = m[x], sh.l[warp][r0 + 8 * x] = l[x];
+    }
+    meet();
+    if (!ok) break;
+    const int rows = min(C::ROWS, p.rows - d.row0);
+    {
+      float f[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float all = m[x];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) all = fmaxf(all, sh.m[i * MT + mt][r0 + 8 * x]);
+        f[x] = all == -INFINITY ? 1.f : ptx::ex2((m[x] - all) * cs);
+      }
+#pragma unroll
+      for (int i = 0; i < DV / 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] *= f[j >> 1];
+    }
+    if (tid < rows) {
+      const int x = tid / 16, r = tid % 16;
+      float all = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) all = fmaxf(all, sh.m[i * MT + x][r]);
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        sum += all == -INFINITY ? sh.l[i * MT + x][r] : sh.l[i * MT + x][r] * ptx::ex2((sh.m[i * MT + x][r] - all) * cs);
+      sh.row[tid] = make_float2(all, sum);
+    }
+    // O by columns, as many at a time as there is room for
+    const int held = rows <= 4 ? 4 : rows <= 8 ? 8 : 16, cols = min(DV, kJoinFloats / kWarps / held);
+    for (int c0 = 0; c0 < DV; c0 += cols) {
+#pragma unroll
+      for (int i = 0; i < DV / 8; ++i)
+        if (8 * i >= c0 && 8 * i < c0 + cols) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (r0 + 8 * x < held)
+              *reinterpret_cast<float2*>(&sh.join[(warp * held + r0 + 8 * x) * cols + 8 * i - c0 + 2 * quad]) =
+                  make_float2(o[i][2 * x], o[i][2 * x + 1]);
+        }
+      meet();
+      if (!ok) break;
+      for (int i = tid; i < rows * cols / 4; i += 32 * kWarps) {
+        const int row = i / (cols / 4), col = (i - row * (cols / 4)) * 4;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+          const float4 v = *reinterpret_cast<const float4*>(&sh.join[((k * MT + row / 16) * held + row % 16) * cols + col]);
+          sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+        const float2 ml = sh.row[row];
+        if (!d.whole) {
+          float* to = p.parts + (int64_t(d.slot) * C::ROWS + row) * (DV + 4);
+          *reinterpret_cast<float4*>(to + c0 + col) = sum;
+          if (c0 + col == 0) *reinterpret_cast<float2*>(to + DV) = ml;
+          continue;
+        }
+        const int t = (d.row0 + row) / p.group, g = d.row0 + row - t * p.group;
+        const int h = c.inter ? d.head + g * c.hkv : d.head * p.group + g;
+        const int64_t at = ((int64_t(d.b) * p.a.n_q + t) * c.hq + h) * DV + c0 + col;
+        const float inv = inverse_of(ml);
+        sum.x *= inv, sum.y *= inv, sum.z *= inv, sum.w *= inv;
+        if (p.a.o_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.a.o) + at) = sum;
+        else
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.o) + at) =
+              make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
+        if (c0 + col == 0)
+          p.a.lse[int64_t(h) * c.num_seqs * p.a.n_q + int64_t(d.b) * p.a.n_q + t] = lse_of(ml, c.scale);
+      }
+      meet();
+      if (!ok) break;
+    }
+  }
+}
+
+constexpr int kJoinThreads = 128;
+
+// A cut run's parts: one behind the last unit of a CTA, the others at the head of those that follow it.  A CTA a row.
+template <typename C>
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ Params p) {
+  constexpr int DV = C::DV, V = DV / 32;
+  __shared__ float top_of[4], sum_of[4];
+  __shared__ float acc_of[4][DV];
+  ptx::grid_wait_previous();
+  const int cta = blockIdx.x, row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 cut = __ldcg(p.meta + cta);
+  const int head = cut.y / p.row_tiles, r = (cut.y - head * p.row_tiles) * C::ROWS + row;
+  if (cut.z == 0 || r >= p.rows) return;
+  auto part = [&](int i) {
+    return p.parts + (int64_t(i == 0 ? cta * 2 + 1 : (cta + i) * 2) * C::ROWS + row) * (DV + 4);
+  };
+  const float cs = p.a.c.scale * kLog2e;
+  float top = -INFINITY;
+  for (int i = threadIdx.x; i < cut.z; i += kJoinThreads) top = fmaxf(top, __ldcg(part(i) + DV));
+#pragma unroll
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+  if (lane == 0) top_of[warp] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(top_of[0], top_of[1]), fmaxf(top_of[2], top_of[3]));
+  float acc[V] = {}, sum = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < cut.z; i += 4) {
+    const float* from = part(i);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + DV));
+    const float f = top == -INFINITY ? 1.f : ptx::ex2((ml.x - top) * cs);
+    sum = fmaf(f, ml.y, sum);
+    if constexpr (V == 4) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(from) + lane);
+      acc[0] = fmaf(f, x.x, acc[0]), acc[1] = fmaf(f, x.y, acc[1]), acc[2] = fmaf(f, x.z, acc[2]), acc[3] = fmaf(f, x.w, acc[3]);
+    } else {
+      const float2 x = __ldcg(reinterpret_cast<const float2*>(from) + lane);
+      acc[0] = fmaf(f, x.x, acc[0]), acc[1] = fmaf(f, x.y, acc[1]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) acc_of[warp][lane * V + j] = acc[j];
+  if (lane == 0) sum_of[warp] = sum;
+  __syncthreads();
+  const KvCache& c = p.a.c;
+  const int t = r / p.group, g = r - t * p.group, h = c.inter ? head + g * c.hkv : head * p.group + g;
+  const float2 ml = make_float2(top, (sum_of[0] + sum_of[1]) + (sum_of[2] + sum_of[3]));
+  if (threadIdx.x < DV) {
+    const int x = threadIdx.x;
+    const float v = ((acc_of[0][x] + acc_of[1][x]) + (acc_of[2][x] + acc_of[3][x])) * inverse_of(ml);
+    const int64_t at = ((int64_t(cut.x) * p.a.n_q + t) * c.hq + h) * DV + x;
+    if (p.a.o_f32) static_cast<float*>(p.a.o)[at] = v;
+    else static_cast<__nv_bfloat16*>(p.a.o)[at] = __float2bfloat16_rn(v);
+  }
+  if (threadIdx.x == 0) p.a.lse[int64_t(h) * c.num_seqs * p.a.n_q + int64_t(cut.x) * p.a.n_q + t] = lse_of(ml, c.scale);
+}
+
+// Panels of 128 bytes of the rows of a pool.
+bool make_map(CUtensorMap* map, const void* pages, bool f32, int64_t rows, int d, int box) {
+  EncodeTiledFn enc = get_encode_tiled();
+  if (enc == nullptr) return false;
+  const int elt = f32 ? 4 : 2, wide = 128 / elt;
+  const cuuint64_t dim[3] = {cuuint64_t(wide), cuuint64_t(rows), cuuint64_t(d / wide)};
+  const cuuint64_t stride[2] = {cuuint64_t(d * elt), 128};
+  const cuuint32_t size[3] = {cuuint32_t(wide), cuuint32_t(box), cuuint32_t(d / wide)};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pages),
+             dim, stride, size, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Shared memory of a CTA: two on an SM where two stages fit then.
+constexpr uint32_t kSmShared = 227 * 1024;
+template <typename C>
+struct Room {
+  static constexpr uint32_t fixed = 1024 + 2 * C::QBYTES + sizeof(Tail);
+  static constexpr uint32_t half = (kSmShared - 1024) / 2;  // (1 KiB a CTA is the system's)
+  static constexpr bool two = fixed + 2 * C::STAGE <= half;
+  static constexpr uint32_t all = two ? half : kSmShared;
+  static constexpr int stages = std::min<uint32_t>((all - fixed) / C::STAGE, kMostStages);
+  static constexpr uint32_t bytes = fixed + stages * C::STAGE;
+  static_assert(stages >= 2, "a ring");
+};
+
+struct Layout {
+  int rows, row_tiles, rows_a_run, ctas;
+  size_t parts, total;
+};
+// Rows of a run: 16, 32 or 64 (fp32: 32, their queries take twice the room).
+Layout layout_of(int hq, int hkv, int dv, int dtype, int n_q) {
+  Layout x;
+  x.rows = hq / hkv * n_q;
+  x.rows_a_run = x.rows <= 16 ? 16 : x.rows <= 32 || dtype == CP_DT_F32 ? 32 : 64;
+  x.row_tiles = (x.rows + x.rows_a_run - 1) / x.rows_a_run;
+  x.ctas = 2 * sm_count();
+  x.parts = (size_t(x.ctas) * sizeof(int4) + 255) / 256 * 256;
+  x.total = (x.parts + size_t(x.ctas) * 2 * x.rows_a_run * (dv + 4) * 4 + 255) / 256 * 256;
+  return x;
+}
+
+template <typename C>
+cudaError_t launch(const KvAttnArgs& a, const Layout& x, cudaStream_t st) {
+  Params p;
+  p.a = a;
+  p.group = a.c.hq / a.c.hkv;
+  p.rows = x.rows;
+  p.row_tiles = x.row_tiles;
+  p.box_shift = std::min(a.c.page_shift, C::F32 ? 5 : 6);
+  p.stages = Room<C>::stages;
+  p.meta = reinterpret_cast<int4*>(a.ws);
+  p.parts = reinterpret_cast<float*>(a.ws + x.parts);
+  const int64_t rows = (int64_t(a.c.num_pages) * a.c.hkv) << a.c.page_shift;
+  // (a pool without pages is not read: any rows will do for its map)
+  const void* any = a.ws;
+  const bool none = rows == 0;
+  if (!make_map(&p.tk, none ? any : a.c.k, C::F32, none ? 1 : rows, C::DQK, 1 << p.box_shift) ||
+      !make_map(&p.tv, none ? any : a.c.v, C::F32, none ? 1 : rows, C::DV, 1 << p.box_shift))
+    return cudaErrorInvalidValue;
+  auto kernel = kv_attn_kernel<C>;
+  static std::atomic<uint64_t> ready{0};  // devices whose kernel may use that much shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Room<C>::bytes));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  }
+  const int ctas = Room<C>::two ? x.ctas : x.ctas / 2;
+  kernel<<<unsigned(ctas), kThreads, Room<C>::bytes, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the launch overlaps the kernel before: it waits on the device
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(ctas), unsigned(std::min(x.rows, x.rows_a_run)));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<C>, p);
+}
+
+template <typename E, int DQK, int DV>
+cudaError_t with_rows(const KvAttnArgs& a, const Layout& x, cudaStream_t st) {
+  if (x.rows_a_run == 16) return launch<Cfg<E, DQK, DV, 1>>(a, x, st);
+  if (x.rows_a_run == 32) return launch<Cfg<E, DQK, DV, 2>>(a, x, st);
+  if constexpr (sizeof(E) == 2) return launch<Cfg<E, DQK, DV, 4>>(a, x, st);
+  return cudaErrorInvalidValue;
+}
+template <typename E>
+cudaError_t with_dims(const KvAttnArgs& a, const Layout& x, int dqk, int dv, cudaStream_t st) {
+  switch (dqk * 1000 + dv) {
+    case 64064: return with_rows<E, 64, 64>(a, x, st);
+    case 64128: return with_rows<E, 64, 128>(a, x, st);
+    case 128064: return with_rows<E, 128, 64>(a, x, st);
+    case 192064: return with_rows<E, 192, 64>(a, x, st);
+    case 192128: return with_rows<E, 192, 128>(a, x, st);
+    default: return with_rows<E, 128, 128>(a, x, st);
+  }
 }
 
 }  // namespace
 
-size_t kv_attn_workspace(const cp_kv_t*, int32_t) { return 256; }
+size_t kv_attn_workspace(const cp_kv_t* c, int32_t n_q) { return layout_of(c->hq, c->hkv, c->d_v, c->dtype, n_q).total; }
+
+int64_t kv_attn_units(const cp_kv_t* c, int32_t n_q) {
+  const int64_t tiles = (int64_t(c->max_pages) * c->page_size + 31) / 32 + 1;
+  return tiles * c->num_seqs * c->hkv * layout_of(c->hq, c->hkv, c->d_v, c->dtype, n_q).row_tiles;
+}
 
 cudaError_t launch_kv_attn(const KvAttnArgs& a, int dqk, int dv, int dtype, cudaStream_t st) {
-  const unsigned rows = unsigned(a.c.num_seqs) * a.n_q * a.c.hq;
-  if (dtype == CP_DT_BF16) kv_attn_kernel<__nv_bfloat16><<<rows, 32 * kWarps, 0, st>>>(a, dqk, dv);
-  else kv_attn_kernel<float><<<rows, 32 * kWarps, 0, st>>>(a, dqk, dv);
-  return cudaGetLastError();
+  const Layout x = layout_of(a.c.hq, a.c.hkv, dv, dtype, a.n_q);
+  return dtype == CP_DT_BF16 ? with_dims<__nv_bfloat16>(a, x, dqk, dv, st) : with_dims<float>(a, x, dqk, dv, st);
 }
 
 }  // namespace cpattn

@@ -60,10 +60,10 @@ cp_status_t check_cache(const cp_kv_t* c) {
   if (c->num_pages < 0 || c->max_pages < 0 || c->page_size < 1 || c->d_qk < 1 || c->d_v < 1) return CP_ERR_INVALID_ARG;
   if ((c->d_qk != 64 && c->d_qk != 128 && c->d_qk != 192) || (c->d_v != 64 && c->d_v != 128)) return CP_ERR_UNSUPPORTED;
   if (page_shift(c->page_size) < 0) return CP_ERR_UNSUPPORTED;
-  // slots, units of work and rows of a call, and rows of the pool (TMA coordinates), stay below 2^31
+  // slots and rows of a call, and rows of the pool (TMA coordinates), stay below 2^31, the scale times log2(e) in range
+  if (c->scale > 1e38f) return CP_ERR_UNSUPPORTED;
   if (c->num_seqs > CP_KV4_MAX_SEQS || c->hq > 1024) return CP_ERR_UNSUPPORTED;
   if (int64_t(c->max_pages) * c->page_size > (1 << 30)) return CP_ERR_UNSUPPORTED;
-  if (int64_t(c->num_seqs) * c->hkv * c->max_pages * c->page_size > int64_t(1) << 35) return CP_ERR_UNSUPPORTED;
   if (int64_t(c->num_pages) * c->hkv * c->page_size > INT32_MAX) return CP_ERR_UNSUPPORTED;
   if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16) || !aligned(c->page_table, 4)) {
     // an empty cache needs none of them
@@ -89,9 +89,9 @@ KvCache device_cache(const cp_kv_t* c) {
   return d;
 }
 
-cp_status_t check_queries(int32_t n_q) {
+cp_status_t check_queries(const cp_kv_t* c, int32_t n_q) {
   if (n_q < 1) return CP_ERR_INVALID_ARG;
-  return n_q > CP_KV4_MAX_QUERIES ? CP_ERR_UNSUPPORTED : CP_OK;
+  return n_q > CP_KV4_MAX_QUERIES || kv_attn_units(c, n_q) > INT32_MAX ? CP_ERR_UNSUPPORTED : CP_OK;
 }
 
 cp_status_t check_pool(const cp_pages_t* p) {
@@ -217,7 +217,7 @@ cp_status_t cp_kv_validate(const cp_kv_t* c) { return check_cache(c); }
 cp_status_t cp_kv_workspace_size(const cp_kv_t* c, int32_t n_q, size_t* bytes) {
   if (bytes == nullptr) return CP_ERR_INVALID_ARG;
   cp_status_t st = check_cache(c);
-  if (st == CP_OK) st = check_queries(n_q);
+  if (st == CP_OK) st = check_queries(c, n_q);
   if (st == CP_OK) *bytes = kv_attn_workspace(c, n_q);
   return st;
 }
@@ -252,7 +252,7 @@ cp_status_t cp_kv_attn(const cp_kv_t* c, int32_t n_q, const void* q, const int32
                        float* lse, void* ws, size_t ws_bytes, cp_stream_t stream) {
   CallRange range_("cp_kv_attn");
   cp_status_t st = check_cache(c);
-  if (st == CP_OK) st = check_queries(n_q);
+  if (st == CP_OK) st = check_queries(c, n_q);
   if (st != CP_OK) return st;
   if (o_f32 != 0 && o_f32 != 1) return CP_ERR_INVALID_ARG;
   if (c->num_seqs == 0) return CP_OK;

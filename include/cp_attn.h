@@ -552,7 +552,7 @@ typedef struct {
   int32_t d_qk, d_v;         /* d_qk in {64, 128, 192}, d_v in {64, 128}         */
   int32_t gqa;               /* cp_gqa_t                                         */
   int32_t dtype;             /* cp_dtype_t of the pages, k, v, q and o           */
-  float scale;               /* softmax scale applied to q.k (> 0, finite)       */
+  float scale;               /* softmax scale applied to q.k (> 0, at most 1e38) */
   int32_t page_size;         /* tokens of a page: 16, 32, 64 or 128              */
   int32_t num_pages;         /* pages of the pool                                */
   int32_t max_pages;         /* columns of page_table                            */
@@ -585,8 +585,9 @@ cp_status_t cp_kv_append(const cp_kv_t* cache, const void* k, const void* v, int
 
 /* Attention of the newest n_q tokens of every sequence over its cache (their
  * own keys and values appended before).  Query t of sequence b sees slots j <
- * lengths[b] - (n_q - 1 - t); one that sees none gets o = 0, lse = -inf.  What a
- * slot that a query does not see holds (NaN, infinities) does not reach it.
+ * lengths[b] - (n_q - 1 - t); one that sees none (or none with a score above
+ * -inf) gets o = 0, lse = -inf.  What a slot that a query does not see holds
+ * (NaN, infinities) does not reach it.
  *   q         : device [B, n_q, hq, d_qk], 1 <= n_q <= CP_KV4_MAX_QUERIES
  *   lengths   : device int32 [B], tokens held, the new ones among them
  *   o         : device [B, n_q, hq, d_v], cache.dtype, or float32 with o_f32 = 1
@@ -594,7 +595,8 @@ cp_status_t cp_kv_append(const cp_kv_t* cache, const void* k, const void* v, int
  *   workspace : cp_kv_workspace_size bytes
  * Products with FP32 accumulation, the softmax in FP32.  BF16 caches: the
  * probabilities rounded to BF16 for their product with V.  FP32 caches: every
- * operand as two TF32 terms (the product of both lower ones, 2^-22, left out). */
+ * operand as two TF32 terms (the product of both lower ones, 2^-22, left out;
+ * an infinity that a query sees may give NaN in an infinity's place). */
 cp_status_t cp_kv_attn(const cp_kv_t* cache, int32_t n_q, const void* q, const int32_t* lengths, void* o,
                        int32_t o_f32, float* lse, void* workspace, size_t workspace_bytes, cp_stream_t stream);
 
