@@ -38,8 +38,11 @@ EncodeTiledFn get_encode_tiled();
 
 namespace {
 
-constexpr int kWarps = 4;  // that compute; one more produces
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kWarps = 4;  // that compute; the first of four more produces (registers move by four warps)
+constexpr int kThreads = 32 * 2 * kWarps;
+// Registers a thread: two CTAs an SM start with 128; the producers hand theirs to the computing warps.
+constexpr int kLaunchRegs = 128, kComputeRegs = 216, kProducerRegs = 40;
+static_assert(kComputeRegs + kProducerRegs == 2 * kLaunchRegs, "what one half takes the other gives");
 constexpr int kJoinFloats = 2048;
 constexpr int kMostStages = 6;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -47,7 +50,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // tiles leave O as it is)
 constexpr float kRescale = 8.f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-enum : int { kSiteQFull = 0x60, kSiteQEmpty, kSiteKFull, kSiteVFull, kSiteEmpty, kSiteJoin, kSiteDrain };
+enum : int { kSiteQFull = 0x60, kSiteQEmpty, kSiteKFull, kSiteKEmpty, kSiteVFull, kSiteVEmpty, kSiteJoin, kSiteDrain };
 
 template <typename E_, int DQK_, int DV_, int MT_>
 struct Cfg {
@@ -59,7 +62,7 @@ struct Cfg {
   static constexpr int TS = TT / NS;           // of a warp
   static constexpr int ROWS = 16 * MT;
   static constexpr int KP = DQK * sizeof(E) / 128, VP = DV * sizeof(E) / 128;  // panels of 128 bytes
-  static constexpr uint32_t KBYTES = KP * TT * 128, VBYTES = VP * TT * 128, STAGE = KBYTES + VBYTES;
+  static constexpr uint32_t KBYTES = KP * TT * 128, VBYTES = VP * TT * 128;
   static constexpr uint32_t QPITCH = DQK * sizeof(E) + 16;  // (rows of a fragment in different banks)
   static constexpr uint32_t QBYTES = (ROWS * QPITCH + 127) / 128 * 128;
 };
@@ -75,11 +78,28 @@ struct Tail {  // shared memory behind the stages and queries
   float m[kWarps][16], l[kWarps][16];
   float2 row[64];  // maximum and sum of a row
   RunDesc run[2];
-  int32_t absent[kMostStages];  // a stage's pages that are outside the pool, a bit each
-  int32_t warp_units[kWarps + 1];
+  int32_t absent[kMostStages];  // pages of a K slot that are outside the pool, a bit each
+  int32_t warp_units[2 * kWarps];
   int32_t start_b, start_off, total;
   int abort, drain_abort;
-  uint64_t q_full[2], q_empty[2], k_full[kMostStages], v_full[kMostStages], empty[kMostStages], joined;
+  uint64_t q_full[2], q_empty[2], joined;
+  uint64_t k_full[kMostStages], k_empty[kMostStages], v_full[kMostStages], v_empty[kMostStages];
+};
+
+// Shared memory of a CTA: two on an SM where two tiles fit then.  What is left holds as many slots of K as of V, or one
+// more of K (they come first).
+constexpr uint32_t kSmShared = 227 * 1024;
+template <typename C>
+struct Room {
+  static constexpr uint32_t fixed = 1024 + 2 * C::QBYTES + sizeof(Tail);
+  static constexpr uint32_t half = (kSmShared - 1024) / 2;  // (1 KiB a CTA is the system's)
+  static constexpr uint32_t pair = C::KBYTES + C::VBYTES;
+  static constexpr bool two = fixed + 2 * pair <= half;
+  static constexpr uint32_t ring = (two ? half : kSmShared) - fixed;
+  static constexpr int nv = std::min<uint32_t>(ring / pair, kMostStages);
+  static constexpr int nk = nv < kMostStages && nv * pair + C::KBYTES <= ring ? nv + 1 : nv;
+  static constexpr uint32_t bytes = fixed + nk * C::KBYTES + nv * C::VBYTES;
+  static_assert(nv >= 2, "a ring");
 };
 
 struct Params {
@@ -87,7 +107,6 @@ struct Params {
   CUtensorMap tk, tv;
   int32_t group, rows, row_tiles;  // G; rows of a kv head; runs they take
   int32_t box_shift;               // log2 of the slots a copy brings: a page's, at most a tile's
-  int32_t stages;
   int4* meta;    // [ctas]: sequence, head and row tile, number of parts of the run that is cut behind this CTA
   float* parts;  // [ctas][2][ROWS][DV + 2]
 };
@@ -126,7 +145,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
   constexpr int TT = C::TT, MT = C::MT, NS = C::NS, DV = C::DV;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (ptx::smem_u32(raw) + 1023) & ~1023u;
-  const uint32_t queries = base + p.stages * C::STAGE;
+  constexpr int NK = Room<C>::nk, NV = Room<C>::nv;
+  const uint32_t values = base + NK * C::KBYTES, queries = values + NV * C::VBYTES;
   Tail& sh = *reinterpret_cast<Tail*>(raw + (queries + 2 * C::QBYTES - ptx::smem_u32(raw)));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const KvCache& c = p.a.c;
@@ -136,10 +156,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
       ptx::mbar_init(ptx::smem_u32(&sh.q_full[i]), 1);
       ptx::mbar_init(ptx::smem_u32(&sh.q_empty[i]), kWarps);
     }
-    for (int i = 0; i < p.stages; ++i) {
+    for (int i = 0; i < kMostStages; ++i) {
       ptx::mbar_init(ptx::smem_u32(&sh.k_full[i]), 1);
       ptx::mbar_init(ptx::smem_u32(&sh.v_full[i]), 1);
-      ptx::mbar_init(ptx::smem_u32(&sh.empty[i]), kWarps);
+      ptx::mbar_init(ptx::smem_u32(&sh.k_empty[i]), kWarps);
+      ptx::mbar_init(ptx::smem_u32(&sh.v_empty[i]), kWarps);
     }
     ptx::mbar_init(ptx::smem_u32(&sh.joined), kWarps);
     ptx::fence_barrier_init();
@@ -165,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
   if (lane == 31) sh.warp_units[warp] = before;
   __syncthreads();
   int total = 0;
-  for (int w = 0; w <= kWarps; ++w) {
+  for (int w = 0; w < 2 * kWarps; ++w) {
     if (w == warp) before += total;
     total += sh.warp_units[w];
   }
@@ -184,9 +205,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
   __syncthreads();
   const ptx::WaitCtx ctx{&sh.abort, c.err, kWaitLimitNs};
 
-  if (warp == kWarps) {
+  if (warp >= kWarps) {
     // ------------------------------------------------------------ producer
-    int stage = 0, phase = 0, tiles_sent = 0, runs_sent = 0;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    if (warp > kWarps) return;
+    int ks = 0, kphase = 0, vs = 0, vphase = 0, keys_sent = 0, tiles_sent = 0, runs_sent = 0;
     int4 cut = make_int4(0, 0, 0, 0);
     bool ok = true;
     int b = u0 < u1 ? sh.start_b : 0, off = u0 < u1 ? sh.start_off : 0;
@@ -229,27 +252,31 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
               window = e0;
               held = window + lane < pages ? kv_page(__ldg(table + window + lane), c.num_pages, c.err) : -1;
             }
-            if (tiles_sent >= p.stages) ok = ptx::mbar_wait(ptx::smem_u32(&sh.empty[stage]), phase ^ 1, kSiteEmpty, ctx);
-            if (!__all_sync(~0u, ok)) { ok = false; break; }
             const int slot0 = tile * TT + (lane << p.box_shift);  // of this lane's copy
             const int32_t page = __shfl_sync(~0u, held, ((slot0 >> c.page_shift) - window) & 31);
             const bool mine = lane < boxes && slot0 < len;
             const unsigned copies = __ballot_sync(~0u, mine && page >= 0), gone = __ballot_sync(~0u, mine && page < 0);
-            const uint32_t kbar = ptx::smem_u32(&sh.k_full[stage]), vbar = ptx::smem_u32(&sh.v_full[stage]);
+            const int row = ((page * c.hkv + head) << c.page_shift) + (slot0 & ((1 << c.page_shift) - 1));
+            if (tiles_sent >= NK) ok = ptx::mbar_wait(ptx::smem_u32(&sh.k_empty[ks]), kphase ^ 1, kSiteKEmpty, ctx);
+            if (!__all_sync(~0u, ok)) { ok = false; break; }
+            const uint32_t kbar = ptx::smem_u32(&sh.k_full[ks]), vbar = ptx::smem_u32(&sh.v_full[vs]);
             if (lane == 0) {
-              sh.absent[stage] = int32_t(gone);
+              sh.absent[ks] = int32_t(gone);
               ptx::mbar_arrive_expect_tx(kbar, __popc(copies) * (C::KBYTES / TT << p.box_shift));
-              ptx::mbar_arrive_expect_tx(vbar, __popc(copies) * (C::VBYTES / TT << p.box_shift));
             }
             __syncwarp();
-            if (mine && page >= 0) {
-              const int row = ((page * c.hkv + head) << c.page_shift) + (slot0 & ((1 << c.page_shift) - 1));
-              const uint32_t to = base + stage * C::STAGE;
-              ptx::tma_load_3d(to + lane * (C::KBYTES / TT << p.box_shift), &p.tk, kbar, 0, row, 0);
-              ptx::tma_load_3d(to + C::KBYTES + lane * (C::VBYTES / TT << p.box_shift), &p.tv, vbar, 0, row, 0);
-            }
+            if (mine && page >= 0)
+              ptx::tma_load_3d(base + ks * C::KBYTES + lane * (C::KBYTES / TT << p.box_shift), &p.tk, kbar, 0, row, 0);
+            ++keys_sent;
+            if (tiles_sent >= NV) ok = ptx::mbar_wait(ptx::smem_u32(&sh.v_empty[vs]), vphase ^ 1, kSiteVEmpty, ctx);
+            if (!__all_sync(~0u, ok)) { ok = false; break; }
+            if (lane == 0) ptx::mbar_arrive_expect_tx(vbar, __popc(copies) * (C::VBYTES / TT << p.box_shift));
+            __syncwarp();
+            if (mine && page >= 0)
+              ptx::tma_load_3d(values + vs * C::VBYTES + lane * (C::VBYTES / TT << p.box_shift), &p.tv, vbar, 0, row, 0);
             ++tiles_sent;
-            if (++stage == p.stages) stage = 0, phase ^= 1;
+            if (++ks == NK) ks = 0, kphase ^= 1;
+            if (++vs == NV) vs = 0, vphase ^= 1;
           }
         }
         ++runs_sent;
@@ -269,10 +296,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
       p.meta[cta] = cut;
       // no copy is in flight when the CTA's shared memory goes to the next one (computing warps that gave up did not wait)
       const ptx::WaitCtx drain{&sh.drain_abort, c.err, kWaitLimitNs};
-      for (int i = max(tiles_sent - p.stages, 0); i < tiles_sent; ++i) {
-        ptx::mbar_wait(ptx::smem_u32(&sh.k_full[i % p.stages]), i / p.stages & 1, kSiteDrain, drain);
-        ptx::mbar_wait(ptx::smem_u32(&sh.v_full[i % p.stages]), i / p.stages & 1, kSiteDrain, drain);
-      }
+      for (int i = max(keys_sent - NK, 0); i < keys_sent; ++i)
+        ptx::mbar_wait(ptx::smem_u32(&sh.k_full[i % NK]), i / NK & 1, kSiteDrain, drain);
+      for (int i = max(tiles_sent - NV, 0); i < tiles_sent; ++i)
+        ptx::mbar_wait(ptx::smem_u32(&sh.v_full[i % NV]), i / NV & 1, kSiteDrain, drain);
       for (int i = max(runs_sent - 2, 0); i < runs_sent; ++i)
         if (!ok) ptx::mbar_wait(ptx::smem_u32(&sh.q_full[i & 1]), i / 2 & 1, kSiteDrain, drain);
     }
@@ -280,11 +307,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
   }
 
   // -------------------------------------------------------------- compute
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
   const int mt = warp % MT, slice = warp / MT;
   const int first_slot = slice * C::TS;  // of this warp in a tile
   const int r0 = lane >> 2, quad = lane & 3;
   const float cs = c.scale * kLog2e;
-  int stage = 0, phase = 0, join_phase = 0;
+  int ks = 0, kphase = 0, vs = 0, vphase = 0, join_phase = 0;
   bool ok = true;
   auto meet = [&] {
     __syncwarp();
@@ -324,10 +352,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
       for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
 
     for (int tile = d.lo; tile < d.hi; ++tile) {
-      const uint32_t kt = base + stage * C::STAGE, vt = kt + C::KBYTES;
-      ok = __all_sync(~0u, ptx::mbar_wait(ptx::smem_u32(&sh.k_full[stage]), phase, kSiteKFull, ctx));
+      const uint32_t kt = base + ks * C::KBYTES, vt = values + vs * C::VBYTES;
+      ok = __all_sync(~0u, ptx::mbar_wait(ptx::smem_u32(&sh.k_full[ks]), kphase, kSiteKFull, ctx));
       if (!ok) break;
-      const int absent = sh.absent[stage];
+      const int absent = sh.absent[ks];
       constexpr int NB = C::TS / 8;  // blocks of 8 slots
       float s[NB][4];
 #pragma unroll
@@ -338,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
           const int slot = first_slot + 8 * i + (lane & 7);
-          float low[4] = {0.f, 0.f, 0.f, 0.f};  // the products with lower terms, added in the end
+          float low[4][4] = {};  // the products with lower terms, in four chains, added in the end
 #pragma unroll 2
           for (int k = 0; k < C::DQK / 16; ++k) {  // two steps of 8 channels
             uint32_t kf[4], a[2][4];
@@ -353,15 +381,15 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
               for (int j = 0; j < 4; ++j) split(__uint_as_float(a[x][j]), ah[j], al[j]);
 #pragma unroll
               for (int j = 0; j < 2; ++j) split(__uint_as_float(kf[2 * x + j]), bh[j], bl[j]);
-              ptx::mma_1688(low, ah, bl[0], bl[1]);
-              ptx::mma_1688(low, al, bh[0], bh[1]);
+              ptx::mma_1688(low[2 * x], ah, bl[0], bl[1]);
+              ptx::mma_1688(low[2 * x + 1], al, bh[0], bh[1]);
               ptx::mma_1688(high, ah, bh[0], bh[1]);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[i][j] += high[j];
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[i][j] += low[j];
+          for (int j = 0; j < 4; ++j) s[i][j] += (low[0][j] + low[1][j]) + (low[2][j] + low[3][j]);
         }
       } else {
 #pragma unroll
@@ -376,6 +404,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.k_empty[ks]));
+      if (++ks == NK) ks = 0, kphase ^= 1;
       // what not every row sees
       const int tile0 = tile * TT + first_slot;
       const bool masked = (tile + 1) * TT > d.len - (p.a.n_q - 1) || absent;
@@ -421,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
           l[j >> 1] += s[i][j];
         }
 
-      ok = __all_sync(~0u, ptx::mbar_wait(ptx::smem_u32(&sh.v_full[stage]), phase, kSiteVFull, ctx));
+      ok = __all_sync(~0u, ptx::mbar_wait(ptx::smem_u32(&sh.v_full[vs]), vphase, kSiteVFull, ctx));
       if (!ok) break;
       // O += P V.  GUARD: slots from `end` on and absent ones count as 0 whatever they hold.  ONE: rows of one query only.
       auto product = [&](auto guard, auto one, int end, int only) {
@@ -523,8 +554,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
         }
       }
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.empty[stage]));
-      if (++stage == p.stages) stage = 0, phase ^= 1;
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.v_empty[vs]));
+      if (++vs == NV) vs = 0, vphase ^= 1;
     }
     if (!ok) break;
     if constexpr (C::F32) {
@@ -683,19 +714,6 @@ bool make_map(CUtensorMap* map, const void* pages, bool f32, int64_t rows, int d
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Shared memory of a CTA: two on an SM where two stages fit then.
-constexpr uint32_t kSmShared = 227 * 1024;
-template <typename C>
-struct Room {
-  static constexpr uint32_t fixed = 1024 + 2 * C::QBYTES + sizeof(Tail);
-  static constexpr uint32_t half = (kSmShared - 1024) / 2;  // (1 KiB a CTA is the system's)
-  static constexpr bool two = fixed + 2 * C::STAGE <= half;
-  static constexpr uint32_t all = two ? half : kSmShared;
-  static constexpr int stages = std::min<uint32_t>((all - fixed) / C::STAGE, kMostStages);
-  static constexpr uint32_t bytes = fixed + stages * C::STAGE;
-  static_assert(stages >= 2, "a ring");
-};
-
 struct Layout {
   int rows, row_tiles, rows_a_run, ctas;
   size_t parts, total;
@@ -720,7 +738,6 @@ cudaError_t launch(const KvAttnArgs& a, const Layout& x, cudaStream_t st) {
   p.rows = x.rows;
   p.row_tiles = x.row_tiles;
   p.box_shift = std::min(a.c.page_shift, C::F32 ? 5 : 6);
-  p.stages = Room<C>::stages;
   p.meta = reinterpret_cast<int4*>(a.ws);
   p.parts = reinterpret_cast<float*>(a.ws + x.parts);
   const int64_t rows = (int64_t(a.c.num_pages) * a.c.hkv) << a.c.page_shift;
@@ -736,6 +753,11 @@ cudaError_t launch(const KvAttnArgs& a, const Layout& x, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    // the warps' shares of the registers wait for each other if they add up to more than the CTA started with
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kernel);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidDeviceFunction;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Room<C>::bytes));
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
