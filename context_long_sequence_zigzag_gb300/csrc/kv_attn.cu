@@ -43,7 +43,6 @@ constexpr int kThreads = 32 * 2 * kWarps;
 // Registers a thread: two CTAs an SM start with 128; the producers hand theirs to the computing warps.
 constexpr int kLaunchRegs = 128, kComputeRegs = 216, kProducerRegs = 40;
 static_assert(kComputeRegs + kProducerRegs == 2 * kLaunchRegs, "what one half takes the other gives");
-constexpr int kJoinFloats = 2048;
 constexpr int kMostStages = 6;
 constexpr float kLog2e = 1.4426950408889634f;
 // log2 units: a row's reference maximum follows a new one past this (p stays below 2^8 relative to it, so that most
@@ -73,11 +72,10 @@ struct RunDesc {
   int32_t whole, slot;         // whole: no parts to join; otherwise the part's slot
 };
 
-struct Tail {  // shared memory behind the stages and queries
-  float join[kJoinFloats];
+struct alignas(16) Tail {  // shared memory behind the stages and queries; the buffer that O is joined in follows
   float m[kWarps][16], l[kWarps][16];
   float2 row[64];  // maximum and sum of a row
-  RunDesc run[2];
+  alignas(16) RunDesc run[2];
   int32_t absent[kMostStages];  // pages of a K slot that are outside the pool, a bit each
   int32_t warp_units[2 * kWarps];
   int32_t start_b, start_off, total;
@@ -91,9 +89,15 @@ struct Tail {  // shared memory behind the stages and queries
 constexpr uint32_t kSmShared = 227 * 1024;
 template <typename C>
 struct Room {
-  static constexpr uint32_t fixed = 1024 + 2 * C::QBYTES + sizeof(Tail);
   static constexpr uint32_t half = (kSmShared - 1024) / 2;  // (1 KiB a CTA is the system's)
   static constexpr uint32_t pair = C::KBYTES + C::VBYTES;
+  // queries a run ahead and 8 KiB to join in, or less of both
+  static constexpr uint32_t fixed_of(int slots, int floats) {
+    return 1024 + (slots + (C::F32 ? 1 : 0)) * C::QBYTES + uint32_t(sizeof(Tail)) + floats * 4;
+  }
+  static constexpr int q_slots = fixed_of(2, 2048) + 2 * pair <= half ? 2 : 1;
+  static constexpr int join_floats = fixed_of(q_slots, 2048) + 2 * pair <= half ? 2048 : 1024;
+  static constexpr uint32_t fixed = fixed_of(q_slots, join_floats);
   static constexpr bool two = fixed + 2 * pair <= half;
   static constexpr uint32_t ring = (two ? half : kSmShared) - fixed;
   static constexpr int nv = std::min<uint32_t>(ring / pair, kMostStages);
@@ -107,18 +111,21 @@ struct Params {
   CUtensorMap tk, tv;
   int32_t group, rows, row_tiles;  // G; rows of a kv head; runs they take
   int32_t box_shift;               // log2 of the slots a copy brings: a page's, at most a tile's
-  int4* meta;    // [ctas]: sequence, head and row tile, number of parts of the run that is cut behind this CTA
+  // sequence, head and row tile, number of parts (0: not cut) and first CTA of every run; where there are more runs than
+  // CTAs, of the run that is cut behind every CTA
+  int4* meta;
+  int32_t by_run;
   float* parts;  // [ctas][2][ROWS][DV + 2]
 };
 
 // units of a sequence's run: its tiles and its start
 __device__ __forceinline__ int units_of(int len, int tt) { return (len + tt - 1) / tt + 1; }
 
-__device__ __forceinline__ uint32_t round_tf32(float x) { return (__float_as_uint(x) + 0x1000u) & 0xffffe000u; }
-// x as two terms of 11 bits
+// x as two terms of 11 bits: the first rounded, of the rest (at most 2^-11 of x) the MMA cuts what is below 2^-10 of
+// it.  A NaN stays in the second term whatever becomes of it in the first.
 __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
-  hi = round_tf32(x);
-  lo = round_tf32(x - __uint_as_float(hi));
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
@@ -146,13 +153,20 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
   extern __shared__ uint8_t raw[];
   const uint32_t base = (ptx::smem_u32(raw) + 1023) & ~1023u;
   constexpr int NK = Room<C>::nk, NV = Room<C>::nv;
+  constexpr int QS = Room<C>::q_slots, kJoinFloats = Room<C>::join_floats;
   const uint32_t values = base + NK * C::KBYTES, queries = values + NV * C::VBYTES;
-  Tail& sh = *reinterpret_cast<Tail*>(raw + (queries + 2 * C::QBYTES - ptx::smem_u32(raw)));
+  const uint32_t low_at = queries + QS * C::QBYTES;  // fp32: the second terms of the run's queries
+  Tail& sh = *reinterpret_cast<Tail*>(raw + (low_at + (C::F32 ? C::QBYTES : 0) - ptx::smem_u32(raw)));
+  float* const join = reinterpret_cast<float*>(&sh + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const KvCache& c = p.a.c;
   ptx::grid_launch_dependents();
+  if (tid == 32 * kWarps) {
+    ptx::prefetch_tmap(&p.tk);
+    ptx::prefetch_tmap(&p.tv);
+  }
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < QS; ++i) {
       ptx::mbar_init(ptx::smem_u32(&sh.q_full[i]), 1);
       ptx::mbar_init(ptx::smem_u32(&sh.q_empty[i]), kWarps);
     }
@@ -167,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
     sh.abort = sh.drain_abort = 0;
   }
   // rows past the last of a run stay 0
-  for (uint32_t i = tid * 16; i < 2 * C::QBYTES; i += kThreads * 16)
+  for (uint32_t i = tid * 16; i < QS * C::QBYTES; i += kThreads * 16)
     *reinterpret_cast<uint4*>(raw + (queries - ptx::smem_u32(raw)) + i) = make_uint4(0, 0, 0, 0);
   ptx::fence_proxy_async_smem();
 
@@ -220,8 +234,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
       const int lo = max(at - 1, 0), hi = at + take - 1;
       if (hi > lo || tiles == 0) {
         const int head = r / p.row_tiles, row0 = (r - head * p.row_tiles) * C::ROWS, rows = min(C::ROWS, p.rows - row0);
-        const int slot = runs_sent & 1;
-        if (runs_sent >= 2) ok = ptx::mbar_wait(ptx::smem_u32(&sh.q_empty[slot]), (runs_sent / 2 - 1) & 1, kSiteQEmpty, ctx);
+        const int slot = runs_sent % QS;
+        if (runs_sent >= QS) ok = ptx::mbar_wait(ptx::smem_u32(&sh.q_empty[slot]), (runs_sent / QS - 1) & 1, kSiteQEmpty, ctx);
         if (!__all_sync(~0u, ok)) { ok = false; break; }
         const bool first = lo == 0, last = hi == tiles;
         const uint32_t bar = ptx::smem_u32(&sh.q_full[slot]);
@@ -230,8 +244,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
           ptx::mbar_arrive_expect_tx(bar, hi > lo ? rows * C::DQK * sizeof(E) : 0);
         }
         __syncwarp();
-        if (first && !last)  // the CTA with the run's last unit
-          cut = make_int4(b, r, int((int64_t(u - at + per_run) * n + total - 1) / total) - 1 - cta + 1, 0);
+        if (first) {
+          // the last of its CTAs is the one with the run's last unit
+          const int parts = last ? 0 : int((int64_t(u - at + per_run) * n + total - 1) / total) - cta;
+          const int4 x = make_int4(b, r, parts, cta);
+          if (p.by_run && lane == 0) p.meta[b * runs + r] = x;
+          if (parts) cut = x;
+        }
         if (hi > lo) {
           for (int i = lane; i < rows; i += 32) {
             const int t = (row0 + i) / p.group, g = row0 + i - t * p.group;
@@ -287,21 +306,21 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
     }
     if (lane == 0) {
       if (ok) {
-        const int slot = runs_sent & 1;
-        if (runs_sent < 2 || ptx::mbar_wait(ptx::smem_u32(&sh.q_empty[slot]), (runs_sent / 2 - 1) & 1, kSiteQEmpty, ctx)) {
+        const int slot = runs_sent % QS;
+        if (runs_sent < QS || ptx::mbar_wait(ptx::smem_u32(&sh.q_empty[slot]), (runs_sent / QS - 1) & 1, kSiteQEmpty, ctx)) {
           sh.run[slot].b = -1;
           ptx::mbar_arrive(ptx::smem_u32(&sh.q_full[slot]));
         }
       }
-      p.meta[cta] = cut;
+      if (!p.by_run) p.meta[cta] = cut;
       // no copy is in flight when the CTA's shared memory goes to the next one (computing warps that gave up did not wait)
       const ptx::WaitCtx drain{&sh.drain_abort, c.err, kWaitLimitNs};
       for (int i = max(keys_sent - NK, 0); i < keys_sent; ++i)
         ptx::mbar_wait(ptx::smem_u32(&sh.k_full[i % NK]), i / NK & 1, kSiteDrain, drain);
       for (int i = max(tiles_sent - NV, 0); i < tiles_sent; ++i)
         ptx::mbar_wait(ptx::smem_u32(&sh.v_full[i % NV]), i / NV & 1, kSiteDrain, drain);
-      for (int i = max(runs_sent - 2, 0); i < runs_sent; ++i)
-        if (!ok) ptx::mbar_wait(ptx::smem_u32(&sh.q_full[i & 1]), i / 2 & 1, kSiteDrain, drain);
+      for (int i = max(runs_sent - QS, 0); i < runs_sent; ++i)
+        if (!ok) ptx::mbar_wait(ptx::smem_u32(&sh.q_full[i % QS]), i / QS & 1, kSiteDrain, drain);
     }
     return;
   }
@@ -322,15 +341,33 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
     join_phase ^= 1;
   };
   for (int run = 0; ok; ++run) {
-    const int qslot = run & 1;
-    ok = ptx::mbar_wait(ptx::smem_u32(&sh.q_full[qslot]), run / 2 & 1, kSiteQFull, ctx);
+    const int qslot = run % QS;
+    ok = ptx::mbar_wait(ptx::smem_u32(&sh.q_full[qslot]), run / QS & 1, kSiteQFull, ctx);
     ok = __all_sync(~0u, ok);
     if (!ok) break;
     const RunDesc d = sh.run[qslot];
     if (d.b < 0) break;
-    const uint32_t q_at = queries + qslot * C::QBYTES + (mt * 16 + (lane & 7) + (lane & 8)) * C::QPITCH + (lane >> 4) * 16;
+    const uint32_t q_lane = (mt * 16 + (lane & 7) + (lane & 8)) * C::QPITCH + (lane >> 4) * 16;
+    const uint32_t q_at = queries + qslot * C::QBYTES + q_lane;
     uint32_t qf[C::F32 ? 1 : C::DQK / 16][4];
-    if constexpr (!C::F32) {
+    if constexpr (C::F32) {
+      // both terms once a run: the first in place
+      if (d.lo < d.hi) {
+        for (int i = slice * 32 + lane; i < 16 * (C::DQK / 4); i += NS * 32) {
+          const uint32_t off = (mt * 16 + i / (C::DQK / 4)) * C::QPITCH + i % (C::DQK / 4) * 16;
+          uint4* const at = reinterpret_cast<uint4*>(raw + (queries + qslot * C::QBYTES + off - ptx::smem_u32(raw)));
+          uint4 x = *at, y;
+          split(__uint_as_float(x.x), x.x, y.x);
+          split(__uint_as_float(x.y), x.y, y.y);
+          split(__uint_as_float(x.z), x.z, y.z);
+          split(__uint_as_float(x.w), x.w, y.w);
+          *at = x;
+          *reinterpret_cast<uint4*>(raw + (low_at + off - ptx::smem_u32(raw))) = y;
+        }
+        meet();
+        if (!ok) break;
+      }
+    } else {
 #pragma unroll
       for (int k = 0; k < C::DQK / 16; ++k) ptx::ldmatrix_x4(qf[k], q_at + k * 32);
       __syncwarp();
@@ -369,16 +406,14 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
           float low[4][4] = {};  // the products with lower terms, in four chains, added in the end
 #pragma unroll 2
           for (int k = 0; k < C::DQK / 16; ++k) {  // two steps of 8 channels
-            uint32_t kf[4], a[2][4];
+            uint32_t kf[4];
             ptx::ldmatrix_x4(kf, piece<C::KP>(kt, p.box_shift, slot, 4 * k + (lane >> 3)));
-            ptx::ldmatrix_x4(a[0], q_at + k * 64);
-            ptx::ldmatrix_x4(a[1], q_at + k * 64 + 32);
             float high[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               uint32_t ah[4], al[4], bh[2], bl[2];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) split(__uint_as_float(a[x][j]), ah[j], al[j]);
+              ptx::ldmatrix_x4(ah, q_at + k * 64 + x * 32);
+              ptx::ldmatrix_x4(al, low_at + q_lane + k * 64 + x * 32);
 #pragma unroll
               for (int j = 0; j < 2; ++j) split(__uint_as_float(kf[2 * x + j]), bh[j], bl[j]);
               ptx::mma_1688(low[2 * x], ah, bl[0], bl[1]);
@@ -559,6 +594,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
     }
     if (!ok) break;
     if constexpr (C::F32) {
+      ptx::fence_proxy_async_smem();  // (written here, and next by a copy)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.q_empty[qslot]));
     }
@@ -606,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
 #pragma unroll
           for (int x = 0; x < 2; ++x)
             if (r0 + 8 * x < held)
-              *reinterpret_cast<float2*>(&sh.join[(warp * held + r0 + 8 * x) * cols + 8 * i - c0 + 2 * quad]) =
+              *reinterpret_cast<float2*>(&join[(warp * held + r0 + 8 * x) * cols + 8 * i - c0 + 2 * quad]) =
                   make_float2(o[i][2 * x], o[i][2 * x + 1]);
         }
       meet();
@@ -616,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < NS; ++k) {
-          const float4 v = *reinterpret_cast<const float4*>(&sh.join[((k * MT + row / 16) * held + row % 16) * cols + col]);
+          const float4 v = *reinterpret_cast<const float4*>(&join[((k * MT + row / 16) * held + row % 16) * cols + col]);
           sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
         }
         const float2 ml = sh.row[row];
@@ -644,60 +680,74 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
   }
 }
 
-constexpr int kJoinThreads = 128;
+constexpr int kJoinWarps = 8;
 
-// A cut run's parts: one behind the last unit of a CTA, the others at the head of those that follow it.  A CTA a row.
+// A cut run's parts: one at the end of a CTA's share, the others at the heads of those that follow it.  A CTA joins
+// `rows_a_cta` rows of a run, kJoinWarps / rows_a_cta warps a row.
 template <typename C>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_constant__ Params p, const int rows_a_cta) {
   constexpr int DV = C::DV, V = DV / 32;
-  __shared__ float top_of[4], sum_of[4];
-  __shared__ float acc_of[4][DV];
+  __shared__ float2 ml_of[kJoinWarps];
+  __shared__ __align__(16) float acc_of[kJoinWarps][DV];
   ptx::grid_wait_previous();
-  const int cta = blockIdx.x, row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4 cut = __ldcg(p.meta + cta);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 cut = __ldcg(p.meta + blockIdx.x);
+  if (cut.z == 0) return;
+  const int across = kJoinWarps / rows_a_cta, row = blockIdx.y * rows_a_cta + warp / across;
   const int head = cut.y / p.row_tiles, r = (cut.y - head * p.row_tiles) * C::ROWS + row;
-  if (cut.z == 0 || r >= p.rows) return;
-  auto part = [&](int i) {
-    return p.parts + (int64_t(i == 0 ? cta * 2 + 1 : (cta + i) * 2) * C::ROWS + row) * (DV + 4);
-  };
+  const bool mine = row < C::ROWS && r < p.rows;
   const float cs = p.a.c.scale * kLog2e;
-  float top = -INFINITY;
-  for (int i = threadIdx.x; i < cut.z; i += kJoinThreads) top = fmaxf(top, __ldcg(part(i) + DV));
+  float acc[V] = {}, top = -INFINITY, sum = 0.f;
+  auto add = [&](float2 ml, const float (&x)[V]) {
+    const float next = fmaxf(top, ml.x);
+    const float f = next == -INFINITY ? 1.f : ptx::ex2((top - next) * cs), g = next == -INFINITY ? 1.f : ptx::ex2((ml.x - next) * cs);
+    top = next;
+    sum = fmaf(sum, f, g * ml.y);
 #pragma unroll
-  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-  if (lane == 0) top_of[warp] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(top_of[0], top_of[1]), fmaxf(top_of[2], top_of[3]));
-  float acc[V] = {}, sum = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < cut.z; i += 4) {
-    const float* from = part(i);
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + DV));
-    const float f = top == -INFINITY ? 1.f : ptx::ex2((ml.x - top) * cs);
-    sum = fmaf(f, ml.y, sum);
-    if constexpr (V == 4) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(from) + lane);
-      acc[0] = fmaf(f, x.x, acc[0]), acc[1] = fmaf(f, x.y, acc[1]), acc[2] = fmaf(f, x.z, acc[2]), acc[3] = fmaf(f, x.w, acc[3]);
-    } else {
-      const float2 x = __ldcg(reinterpret_cast<const float2*>(from) + lane);
-      acc[0] = fmaf(f, x.x, acc[0]), acc[1] = fmaf(f, x.y, acc[1]);
+    for (int j = 0; j < V; ++j) acc[j] = fmaf(acc[j], f, g * x[j]);
+  };
+  if (mine) {
+    constexpr int U = 4;  // parts in flight
+    for (int i0 = warp % across; i0 < cut.z; i0 += U * across) {
+      float2 ml[U];
+      float x[U][V];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * across;
+        if (i >= cut.z) continue;
+        const float* from = p.parts + (int64_t(i == 0 ? cut.w * 2 + 1 : (cut.w + i) * 2) * C::ROWS + row) * (DV + 4);
+        ml[u] = __ldcg(reinterpret_cast<const float2*>(from + DV));
+        if constexpr (V == 4) *reinterpret_cast<float4*>(x[u]) = __ldcg(reinterpret_cast<const float4*>(from) + lane);
+        else *reinterpret_cast<float2*>(x[u]) = __ldcg(reinterpret_cast<const float2*>(from) + lane);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * across < cut.z) add(ml[u], x[u]);
     }
   }
+  if (lane == 0) ml_of[warp] = make_float2(top, sum);
 #pragma unroll
   for (int j = 0; j < V; ++j) acc_of[warp][lane * V + j] = acc[j];
-  if (lane == 0) sum_of[warp] = sum;
   __syncthreads();
+  if (!mine || warp % across) return;
+  for (int w = 1; w < across; ++w) {
+    float x[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = acc_of[warp + w][lane * V + j];
+    add(ml_of[warp + w], x);
+  }
   const KvCache& c = p.a.c;
   const int t = r / p.group, g = r - t * p.group, h = c.inter ? head + g * c.hkv : head * p.group + g;
-  const float2 ml = make_float2(top, (sum_of[0] + sum_of[1]) + (sum_of[2] + sum_of[3]));
-  if (threadIdx.x < DV) {
-    const int x = threadIdx.x;
-    const float v = ((acc_of[0][x] + acc_of[1][x]) + (acc_of[2][x] + acc_of[3][x])) * inverse_of(ml);
-    const int64_t at = ((int64_t(cut.x) * p.a.n_q + t) * c.hq + h) * DV + x;
-    if (p.a.o_f32) static_cast<float*>(p.a.o)[at] = v;
-    else static_cast<__nv_bfloat16*>(p.a.o)[at] = __float2bfloat16_rn(v);
+  const float inv = inverse_of(make_float2(top, sum));
+  const int64_t at = ((int64_t(cut.x) * p.a.n_q + t) * c.hq + h) * DV + lane * V;
+#pragma unroll
+  for (int j = 0; j < V; j += 2) {
+    if (p.a.o_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.a.o) + at + j) = make_float2(acc[j] * inv, acc[j + 1] * inv);
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.a.o) + at + j) = pack_bf16(acc[j] * inv, acc[j + 1] * inv);
   }
-  if (threadIdx.x == 0) p.a.lse[int64_t(h) * c.num_seqs * p.a.n_q + int64_t(cut.x) * p.a.n_q + t] = lse_of(ml, c.scale);
+  if (lane == 0)
+    p.a.lse[int64_t(h) * c.num_seqs * p.a.n_q + int64_t(cut.x) * p.a.n_q + t] = lse_of(make_float2(top, sum), c.scale);
 }
 
 // Panels of 128 bytes of the rows of a pool.
@@ -740,12 +790,12 @@ cudaError_t launch(const KvAttnArgs& a, const Layout& x, cudaStream_t st) {
   p.box_shift = std::min(a.c.page_shift, C::F32 ? 5 : 6);
   p.meta = reinterpret_cast<int4*>(a.ws);
   p.parts = reinterpret_cast<float*>(a.ws + x.parts);
-  const int64_t rows = (int64_t(a.c.num_pages) * a.c.hkv) << a.c.page_shift;
+  const int64_t pool_rows = (int64_t(a.c.num_pages) * a.c.hkv) << a.c.page_shift;
   // (a pool without pages is not read: any rows will do for its map)
   const void* any = a.ws;
-  const bool none = rows == 0;
-  if (!make_map(&p.tk, none ? any : a.c.k, C::F32, none ? 1 : rows, C::DQK, 1 << p.box_shift) ||
-      !make_map(&p.tv, none ? any : a.c.v, C::F32, none ? 1 : rows, C::DV, 1 << p.box_shift))
+  const bool none = pool_rows == 0;
+  if (!make_map(&p.tk, none ? any : a.c.k, C::F32, none ? 1 : pool_rows, C::DQK, 1 << p.box_shift) ||
+      !make_map(&p.tv, none ? any : a.c.v, C::F32, none ? 1 : pool_rows, C::DV, 1 << p.box_shift))
     return cudaErrorInvalidValue;
   auto kernel = kv_attn_kernel<C>;
   static std::atomic<uint64_t> ready{0};  // devices whose kernel may use that much shared memory
@@ -763,6 +813,8 @@ cudaError_t launch(const KvAttnArgs& a, const Layout& x, cudaStream_t st) {
     if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
   const int ctas = Room<C>::two ? x.ctas : x.ctas / 2;
+  const int64_t runs = int64_t(a.c.num_seqs) * a.c.hkv * x.row_tiles;
+  p.by_run = runs <= x.ctas;
   kernel<<<unsigned(ctas), kThreads, Room<C>::bytes, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -771,12 +823,15 @@ cudaError_t launch(const KvAttnArgs& a, const Layout& x, cudaStream_t st) {
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(ctas), unsigned(std::min(x.rows, x.rows_a_run)));
-  cfg.blockDim = dim3(kJoinThreads);
+  // warps a row: eight for up to 8 rows, one for 64 (a CTA for every row of every run that might be cut takes 10 us)
+  const int rows = std::min(x.rows, x.rows_a_run);
+  const int rows_a_cta = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
+  cfg.gridDim = dim3(unsigned(p.by_run ? runs : ctas), unsigned((rows + rows_a_cta - 1) / rows_a_cta));
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = st;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_join_kernel<C>, p);
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<C>, p, rows_a_cta);
 }
 
 template <typename E, int DQK, int DV>
