@@ -827,15 +827,22 @@ class Rope:
         self.ptr = ctypes.byref(self.desc)
 
 
+def _sizes(t) -> tuple:
+    """Shape of a tensor; () of anything else (which _need then refuses)."""
+    return t.shape if isinstance(t, torch.Tensor) else ()
+
+
 def _positions(rope: Rope, positions, rows: int, dev):
     """Pointer and row length of positions [rows, axes or more] (or [rows] on one axis)."""
     if rope.device != dev:
         raise ValueError(f"rope: a Rope on {dev} is needed")
-    if isinstance(positions, torch.Tensor) and positions.dim() == 1:
-        shape, wide = (rows,), 1
+    shape = _sizes(positions)
+    if len(shape) == 1:
+        wide = 1
+        p = _need(positions, "positions", torch.int32, (rows,), dev)
     else:
-        shape, wide = (rows, None), positions.shape[1] if isinstance(positions, torch.Tensor) and positions.dim() == 2 else 0
-    p = _need(positions, "positions", torch.int32, shape, dev)
+        wide = shape[1] if len(shape) == 2 else rope.axes
+        p = _need(positions, "positions", torch.int32, (rows, wide), dev)
     if wide < rope.axes:
         raise ValueError(f"positions: {rope.axes} columns are needed, got {wide}")
     return p, wide
@@ -847,30 +854,32 @@ def cp_rope(rope: Rope, positions, q, k=None, inverse: bool = False, q_out=None,
     themselves for a call in place.  Returns q_out, or (q_out, k_out) with k."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda:  # (the others have to be where q is)
         raise ValueError("q: a tensor on a CUDA device is needed")
-    if q.dim() != 3 or q.dtype not in _DTYPES:
+    dev, dtype, shape = q.device, q.dtype, q.shape
+    code = _DTYPES.get(dtype)
+    if len(shape) != 3 or code is None:
         raise ValueError("q: float32 or bfloat16 [T, heads, d] is needed")
-    dev, dtype = q.device, q.dtype
-    T, hq, d = q.shape
+    T, hq, d = shape
     temps = []
-    pq = _need(q, "q", dtype, (T, hq, d), dev)
+    pq = _need(q, "q", dtype, shape, dev)
     if q_out is None:
         q_out = torch.empty_like(q)
         temps.append(q_out)
         po = q_out.data_ptr()
     else:
-        po = _need(q_out, "q_out", dtype, (T, hq, d), dev)
+        po = _need(q_out, "q_out", dtype, shape, dev)
     hkv, pk, pko = 0, None, None
     if k is not None:
-        pk = _need(k, "k", dtype, (T, None, d), dev)
-        hkv = k.shape[1]
+        kshape = _sizes(k)
+        hkv = kshape[1] if len(kshape) == 3 else 0
+        pk = _need(k, "k", dtype, (T, hkv, d), dev)
         if k_out is None:
             k_out = torch.empty_like(k)
             temps.append(k_out)
             pko = k_out.data_ptr()
         else:
-            pko = _need(k_out, "k_out", dtype, (T, hkv, d), dev)
+            pko = _need(k_out, "k_out", dtype, kshape, dev)
     pp, wide = _positions(rope, positions, T, dev)
-    _launch(dev, stream, temps, "cp_rope", rope.ptr, T, pp, wide, d, _DTYPES[dtype], hq, pq, po, hkv, pk, pko,
+    _launch(dev, stream, temps, "cp_rope", rope.ptr, T, pp, wide, d, code, hq, pq, po, hkv, pk, pko,
             1 if inverse else 0)
     return q_out if k is None else (q_out, k_out)
 
@@ -924,13 +933,13 @@ def cp_kv_append(cache: KvCache, k, v, cu, start, rows=None, rope: Optional[Rope
     by positions (int32 [n, axes] or [n], in k's rows; None: by their slots).
     cu int32 [B + 1], start int32 [B], rows int32 [tokens], on the device."""
     dev, hkv, dtype, B = cache.device, cache.hkv, cache.torch_dtype, cache.num_seqs
-    pk = _need(k, "k", dtype, (None, hkv, cache.d_qk), dev)
-    n = k.shape[0]
+    n = (_sizes(k) or (0,))[0]
+    pk = _need(k, "k", dtype, (n, hkv, cache.d_qk), dev)
     pv = _need(v, "v", dtype, (n, hkv, cache.d_v), dev)
     tokens, pr = n, None
     if rows is not None:
-        pr = _need(rows, "rows", torch.int32, (None,), dev)
-        tokens = rows.shape[0]
+        tokens = (_sizes(rows) or (0,))[0]
+        pr = _need(rows, "rows", torch.int32, (tokens,), dev)
     ptr, pp, wide = None, None, 0
     if rope is not None:
         ptr = rope.ptr
@@ -949,8 +958,9 @@ def cp_kv_attn(cache: KvCache, q, lengths, part: bool = False, o=None, lse=None,
     (lengths int32 [B]: tokens held, the new ones among them).  Returns o [B, n_q, hq, d_v] and
     lse [hq, B * n_q].  part: o in float32, for cp_lse_merge."""
     dev, dtype, B, hq = cache.device, cache.torch_dtype, cache.num_seqs, cache.hq
-    pq = _need(q, "q", dtype, (B, None, hq, cache.d_qk), dev)
-    n_q = q.shape[1]
+    shape = _sizes(q)
+    n_q = shape[1] if len(shape) == 4 else 1
+    pq = _need(q, "q", dtype, (B, n_q, hq, cache.d_qk), dev)
     o_dtype = torch.float32 if part else dtype
     temps = []
     shape = (B, n_q, hq, cache.d_v)
@@ -1038,12 +1048,17 @@ def cp_pages_workspace_size(pool: PagePool, num_seqs: int) -> int:
     return int(n.value)
 
 
+def _rows_of(table, dev):
+    shape = _sizes(table)
+    B, columns = shape if len(shape) == 2 else (0, 0)
+    return B, columns, _need(table, "table", torch.int32, (B, columns), dev)
+
+
 def cp_pages_reserve(pool: PagePool, table, lengths, extra, counts=None, stream=None):
     """Gives every sequence b of lengths[b] tokens the pages that extra[b] more need, in table [B, max_pages] (in
     place).  Returns counts int32 [2]: pages in use, and entries that got none (they are -1)."""
     dev, temps = pool.device, []
-    pt = _need(table, "table", torch.int32, (None, None), dev)
-    B, columns = table.shape
+    B, columns, pt = _rows_of(table, dev)
     counts, pc = pool._out(counts, "counts", (2,), temps)
     _launch(dev, stream, temps, "cp_pages_reserve", pool.ptr, B, columns, pt,
             _need(lengths, "lengths", torch.int32, (B,), dev), _need(extra, "extra", torch.int32, (B,), dev), pc)
@@ -1057,14 +1072,11 @@ def cp_pages_fork(pool: PagePool, table, lengths, parents, new_table=None, new_l
     new_table [len(parents), columns] (-1 behind the last page), new_lengths and counts int32 [2]: pages in use,
     and entries that got none."""
     dev, temps = pool.device, []
-    pt = _need(table, "table", torch.int32, (None, None), dev)
-    B, columns = table.shape
-    pp = _need(parents, "parents", torch.int32, (None,), dev)
-    n = parents.shape[0]
-    if new_table is None:
-        new_table, pn = pool._out(None, "", (n, columns), temps)
-    else:
-        pn = _need(new_table, "new_table", torch.int32, (n, None), dev)
+    B, columns, pt = _rows_of(table, dev)
+    n = (_sizes(parents) or (0,))[0]
+    pp = _need(parents, "parents", torch.int32, (n,), dev)
+    shape = _sizes(new_table)
+    new_table, pn = pool._out(new_table, "new_table", (n, shape[1] if len(shape) == 2 else columns), temps)
     new_lengths, pl = pool._out(new_lengths, "new_lengths", (n,), temps)
     counts, pc = pool._out(counts, "counts", (2,), temps)
     pw, size = pool._workspace(max(B, n), ws, temps)
@@ -1078,8 +1090,7 @@ def cp_pages_compact(pool: PagePool, table, lengths, new_table=None, moved=None,
     itself may be given), moved int32 [num_pages], every page's new place (-1: it was free), and counts int32 [2]:
     pages in use, and 0."""
     dev, temps = pool.device, []
-    pt = _need(table, "table", torch.int32, (None, None), dev)
-    B, columns = table.shape
+    B, columns, pt = _rows_of(table, dev)
     new_table, pn = pool._out(new_table, "new_table", (B, columns), temps)
     moved, pm = pool._out(moved, "moved", (pool.num_pages,), temps)
     counts, pc = pool._out(counts, "counts", (2,), temps)
@@ -1095,9 +1106,10 @@ def cp_pages_copy(pool: PagePool, src, dst, to: Optional[PagePool] = None, strea
     dev = pool.device
     if to is not None and to.device != dev:
         raise ValueError(f"to: a pool on {dev} is needed")
-    ps = _need(src, "src", torch.int32, (None,), dev)
-    _launch(dev, stream, (), "cp_pages_copy", pool.ptr, (to or pool).ptr, src.shape[0], ps,
-            _need(dst, "dst", torch.int32, (src.shape[0],), dev))
+    n = (_sizes(src) or (0,))[0]
+    ps = _need(src, "src", torch.int32, (n,), dev)
+    _launch(dev, stream, (), "cp_pages_copy", pool.ptr, (to or pool).ptr, n, ps,
+            _need(dst, "dst", torch.int32, (n,), dev))
 
 
 def cp_set_debug_checks(on: bool) -> bool:

@@ -114,7 +114,7 @@ struct Params {
   // sequence, head and row tile, number of parts (0: not cut) and first CTA of every run; where there are more runs than
   // CTAs, of the run that is cut behind every CTA
   int4* meta;
-  int32_t by_run;
+  int32_t by_run, join_ctas;
   float* parts;  // [ctas][2][ROWS][DV + 2]
 };
 
@@ -692,7 +692,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_c
   ptx::grid_wait_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 cut = __ldcg(p.meta + blockIdx.x);
-  if (cut.z == 0) return;
+  // (a CTA that gave up waiting has left no plan)
+  const int ctas = p.join_ctas;
+  if (cut.z <= 0 || cut.w < 0 || cut.z > ctas - cut.w || cut.x < 0 || cut.x >= p.a.c.num_seqs || cut.y < 0 ||
+      cut.y >= p.a.c.hkv * p.row_tiles)
+    return;
   const int across = kJoinWarps / rows_a_cta, row = blockIdx.y * rows_a_cta + warp / across;
   const int head = cut.y / p.row_tiles, r = (cut.y - head * p.row_tiles) * C::ROWS + row;
   const bool mine = row < C::ROWS && r < p.rows;
@@ -815,6 +819,7 @@ cudaError_t launch(const KvAttnArgs& a, const Layout& x, cudaStream_t st) {
   const int ctas = Room<C>::two ? x.ctas : x.ctas / 2;
   const int64_t runs = int64_t(a.c.num_seqs) * a.c.hkv * x.row_tiles;
   p.by_run = runs <= x.ctas;
+  p.join_ctas = ctas;
   kernel<<<unsigned(ctas), kThreads, Room<C>::bytes, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -289,8 +289,6 @@ cp_status_t cp_pages_reserve(const cp_pages_t* p, int32_t num_seqs, int32_t max_
   if (!aligned(counts, 4)) return CP_ERR_INVALID_ARG;
   if (num_seqs > 0 && (!aligned(lengths, 4) || !aligned(extra, 4))) return CP_ERR_INVALID_ARG;
   if (num_seqs > 0 && max_pages > 0 && !aligned(table, 4)) return CP_ERR_INVALID_ARG;
-  // (without sequences `extra` may be NULL, which the kernel takes for a fork: any address will do)
-  if (num_seqs == 0) extra = counts;
   return done(launch_pages_reserve(p->num_pages, p->page_size, p->refs, {num_seqs, max_pages, table, lengths}, table,
                                    extra, counts, device_error_word(), reinterpret_cast<cudaStream_t>(stream)));
 }

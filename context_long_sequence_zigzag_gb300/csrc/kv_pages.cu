@@ -26,6 +26,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kPerWarp = 4;                            // pages a lane of a step
 constexpr int kStep = kThreads * kPerWarp;             // pages of a step of a CTA
 constexpr int kMostSeqs = CP_KV4_MAX_SEQS;
+constexpr int kFewEntries = 8 * kCluster * kThreads;  // of a fork's tables, for the cluster that takes the pages
 
 // Head of the workspace; the lists follow (src, then dst).
 struct PairList {
@@ -135,42 +136,88 @@ struct Demand {
   int32_t* table;
   int32_t num_seqs, max_pages, page_size;
   const int32_t* lengths;
-  const int32_t* extra;  // reserve: tokens to come; nullptr: fork
+  const int32_t* extra;  // reserve: tokens to come
 };
 
-// Shared memory: prefix [num_seqs + 1], first [num_seqs].
+// What a fork starts from and leaves.
+struct Fork {
+  PageTable old;
+  const int32_t* parents;
+  int32_t* new_lengths;
+};
+
+// The old sequences let go of their pages, the new ones (of `d`) take theirs; a page held in part is counted later.
+// Thread i of n.
+__device__ __forceinline__ void fork_rows(int32_t* refs, int32_t num_pages, const Fork& f, const Demand& d, int64_t i0,
+                                          int64_t n, int32_t* err) {
+  const int64_t most = int64_t(f.old.max_pages) * d.page_size, new_most = int64_t(d.max_pages) * d.page_size;
+  for (int64_t i = i0; i < int64_t(f.old.num_seqs) * f.old.max_pages; i += n) {
+    const int b = int(i / f.old.max_pages), e = int(i - int64_t(b) * f.old.max_pages);
+    if (e >= pages_of(kv_length(__ldg(f.old.lengths + b), most, err), d.page_size)) continue;
+    const int32_t p = kv_page(__ldg(f.old.table + i), num_pages, err);
+    if (p >= 0) atomicSub(refs + p, 1);
+  }
+  const int across = max(d.max_pages, 1);  // (a length is written even where no page is)
+  for (int64_t i = i0; i < int64_t(d.num_seqs) * across; i += n) {
+    const int b = int(i / across), e = int(i - int64_t(b) * across);
+    int32_t from = __ldg(f.parents + b);
+    if (from >= f.old.num_seqs) {
+      kv_error(err, kKvSlot);
+      from = -1;
+    }
+    int32_t len = from >= 0 ? kv_length(__ldg(f.old.lengths + from), most, nullptr) : 0;
+    if (len > new_most) {
+      kv_error(err, kKvLength);
+      len = int32_t(new_most);
+    }
+    if (e == 0) f.new_lengths[b] = len;
+    if (e >= d.max_pages) continue;
+    int32_t p = -1;
+    if (e < pages_of(len, d.page_size)) {
+      p = __ldg(f.old.table + int64_t(from) * f.old.max_pages + e);
+      if (p < 0 || p >= num_pages) p = -1;  // (recorded above)
+      else if (e < len / d.page_size) atomicAdd(refs + p, 1);
+    }
+    d.table[int64_t(b) * d.max_pages + e] = p;
+  }
+}
+
+__global__ void __launch_bounds__(256)
+    pages_rows_kernel(int32_t* refs, int32_t num_pages, Fork f, Demand d, int32_t* err) {
+  ptx::grid_launch_dependents();
+  fork_rows(refs, num_pages, f, d, int64_t(blockIdx.x) * 256 + threadIdx.x, int64_t(gridDim.x) * 256, err);
+}
+
+// Shared memory: first [num_seqs] (padded to four), prefix [num_seqs + 1].  FORK, `rows`: the rows are done here, not by
+// a kernel before.
+template <bool FORK>
 __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
-    pages_take_kernel(int32_t* refs, int32_t num_pages, Demand d, int32_t* counts, PairList* list, int32_t* src,
-                      int32_t* dst, int32_t* err) {
-  extern __shared__ int32_t shared[];
+    pages_take_kernel(int32_t* refs, int32_t num_pages, Fork f, int32_t rows, Demand d, int32_t* counts, PairList* list,
+                      int32_t* src, int32_t* dst, int32_t* err) {
+  extern __shared__ __align__(16) int32_t shared[];
   __shared__ int warp_sums[kWarps];
   __shared__ int cta_counts[kCluster][2];
   cg::cluster_group cluster = cg::this_cluster();
   const int cta = int(cluster.block_rank()), tid = threadIdx.x;
-  int32_t* prefix = shared;
-  int32_t* first = shared + d.num_seqs + 1;
-  const bool fork = d.extra == nullptr;
-  cluster.sync();  // all are there before their shared memory is written
-  if (fork) ptx::grid_wait_previous();  // the tables and counts before
+  int32_t* first = shared;
+  int32_t* prefix = shared + (d.num_seqs + 3) / 4 * 4;
+  int lo, hi;
+  part_of(num_pages, cta, &lo, &hi);
 
-  // fork: the page that sequence b holds in part (first[b]), -1: none
-  for (int b = tid; b < d.num_seqs; b += kThreads) {
-    const int64_t most = int64_t(d.max_pages) * d.page_size;
-    if (fork) {
+  if constexpr (FORK) {
+    if (rows) {
+      fork_rows(refs, num_pages, f, d, cta * kThreads + tid, kCluster * kThreads, err);
+      cluster.sync();
+    } else {
+      ptx::grid_wait_previous();
+    }
+    // the page that sequence b holds in part, -1: none
+    for (int b = tid; b < d.num_seqs; b += kThreads) {
       const int32_t n = __ldcg(d.lengths + b);
       first[b] = n % d.page_size ? __ldcg(d.table + int64_t(b) * d.max_pages + n / d.page_size) : -1;
-    } else {
-      const int32_t n = kv_length(__ldg(d.lengths + b), most, err);
-      const int64_t want = int64_t(n) + max(__ldg(d.extra + b), 0);
-      if (want > most) kv_error(err, kKvLength);
-      const int32_t held = pages_of(n, d.page_size);
-      first[b] = held;
-      prefix[b] = pages_of(min(want, most), d.page_size) - held;
     }
-  }
-  __syncthreads();
-  bool keeps[kMostSeqs / kThreads];
-  if (fork) {
+    __syncthreads();
+    bool keeps[kMostSeqs / kThreads];
 #pragma unroll
     for (int k = 0; k < kMostSeqs / kThreads; ++k) {
       const int b = tid + k * kThreads;
@@ -178,18 +225,37 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
       if (b >= d.num_seqs) continue;
       const int32_t p = first[b];
       bool earlier = false;
-      if (p >= 0)
-        for (int i = 0; i < b && !earlier; ++i) earlier = first[i] == p;
-      keeps[k] = p >= 0 && !earlier && __ldcg(refs + p) == 0;
+      if (p >= 0) {
+        keeps[k] = __ldcg(refs + p) == 0;
+        for (int i = 0; i < b / 4; ++i) {
+          const int4 x = reinterpret_cast<const int4*>(first)[i];
+          earlier = earlier || x.x == p || x.y == p || x.z == p || x.w == p;
+        }
+        for (int i = b & ~3; i < b; ++i) earlier = earlier || first[i] == p;
+      }
+      keeps[k] = keeps[k] && !earlier;
       prefix[b] = p >= 0 && !keeps[k];
     }
     cluster.sync();  // every CTA has read refs
-    if (cta == 0) {
+    // (a page is scanned by one CTA, which marks it)
 #pragma unroll
-      for (int k = 0; k < kMostSeqs / kThreads; ++k)
-        if (keeps[k]) __stcg(refs + first[tid + k * kThreads], 1);
+    for (int k = 0; k < kMostSeqs / kThreads; ++k) {
+      const int32_t p = keeps[k] ? first[tid + k * kThreads] : -1;
+      if (p >= lo && p < hi) __stcg(refs + p, 1);
     }
-    cluster.sync();
+    __syncthreads();
+  } else {
+    for (int b = tid; b < d.num_seqs; b += kThreads) {
+      const int64_t most = int64_t(d.max_pages) * d.page_size;
+      const int32_t n = kv_length(__ldg(d.lengths + b), most, err);
+      const int64_t want = int64_t(n) + max(__ldg(d.extra + b), 0);
+      if (want > most) kv_error(err, kKvLength);
+      const int32_t held = pages_of(n, d.page_size);
+      first[b] = held;
+      prefix[b] = pages_of(min(want, most), d.page_size) - held;
+    }
+    __syncthreads();
+    cluster.barrier_arrive();  // all are there before their shared memory is written (the wait is below)
   }
   // demands to a prefix sum
   int wanted = 0;
@@ -204,10 +270,9 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
   if (tid == 0) prefix[d.num_seqs] = wanted;
   __syncthreads();
 
-  int lo, hi;
-  part_of(num_pages, cta, &lo, &hi);
   auto is_free = [](int, int32_t r) { return r == 0; };
   const int free_here = scan_refs(refs, lo, hi, 0, INT32_MAX, warp_sums, is_free, [](int, int32_t, int) {});
+  if constexpr (!FORK) cluster.barrier_wait();
   // (hi - lo less the free ones includes negative counts of a caller's mistake: in use, as they are not free)
   const Sums s = exchange(cluster, cta_counts, cta, free_here, hi - lo - free_here);
   const int given = min(wanted, s.all[0]);
@@ -221,14 +286,14 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     return x;
   };
   auto entry_of = [&](int b, int rank) {
-    const int e = fork ? __ldcg(d.lengths + b) / d.page_size : first[b] + rank - prefix[b];
+    const int e = FORK ? __ldcg(d.lengths + b) / d.page_size : first[b] + rank - prefix[b];
     return d.table + int64_t(b) * d.max_pages + e;
   };
   if (s.below[0] < given)
     scan_refs(refs, lo, hi, s.below[0], given, warp_sums, is_free, [&](int page, int32_t, int rank) {
       if (rank >= given) return;
       const int b = taker(rank);
-      if (fork) src[rank] = first[b], dst[rank] = page;
+      if (FORK) src[rank] = first[b], dst[rank] = page;
       *entry_of(b, rank) = page;
       refs[page] = 1;
     });
@@ -238,50 +303,9 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     kv_error(err, kKvNoPage);
   }
   if (cta == 0 && tid == 0) {
-    if (fork) list->n = given;
+    if (FORK) list->n = given;
     counts[0] = s.all[1] + given;
     counts[1] = wanted - given;
-  }
-  cluster.sync();  // (nobody leaves while its shared memory may still be written)
-}
-
-// Fork: the old sequences let go of their pages, the new ones take theirs; a
-// page held in part is counted by the kernel behind.
-__global__ void __launch_bounds__(256)
-    pages_rows_kernel(int32_t* refs, int32_t num_pages, int32_t page_size, PageTable t, int32_t new_seqs,
-                      int32_t new_max_pages, const int32_t* parents, int32_t* new_table, int32_t* new_lengths,
-                      int32_t* err) {
-  ptx::grid_launch_dependents();
-  const int64_t step = int64_t(gridDim.x) * blockDim.x, i0 = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int64_t most = int64_t(t.max_pages) * page_size, new_most = int64_t(new_max_pages) * page_size;
-  for (int64_t i = i0; i < int64_t(t.num_seqs) * t.max_pages; i += step) {
-    const int b = int(i / t.max_pages), e = int(i - int64_t(b) * t.max_pages);
-    if (e >= pages_of(kv_length(__ldg(t.lengths + b), most, err), page_size)) continue;
-    const int32_t p = kv_page(__ldg(t.table + i), num_pages, err);
-    if (p >= 0) atomicSub(refs + p, 1);
-  }
-  const int across = max(new_max_pages, 1);  // (a length is written even where no page is)
-  for (int64_t i = i0; i < int64_t(new_seqs) * across; i += step) {
-    const int b = int(i / across), e = int(i - int64_t(b) * across);
-    int32_t from = __ldg(parents + b);
-    if (from >= t.num_seqs) {
-      kv_error(err, kKvSlot);
-      from = -1;
-    }
-    int32_t n = from >= 0 ? kv_length(__ldg(t.lengths + from), most, nullptr) : 0;
-    if (n > new_most) {
-      kv_error(err, kKvLength);
-      n = int32_t(new_most);
-    }
-    if (e == 0) new_lengths[b] = n;
-    if (e >= new_max_pages) continue;
-    int32_t p = -1;
-    if (e < pages_of(n, page_size)) {
-      p = __ldg(t.table + int64_t(from) * t.max_pages + e);
-      if (p < 0 || p >= num_pages) p = -1;  // (recorded above)
-      else if (e < n / page_size) atomicAdd(refs + p, 1);
-    }
-    new_table[int64_t(b) * new_max_pages + e] = p;
   }
 }
 
@@ -294,23 +318,30 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
   __shared__ int cta_counts[2][kCluster][2];
   cg::cluster_group cluster = cg::this_cluster();
   const int cta = int(cluster.block_rank());
-  cluster.sync();  // all are there before their shared memory is written
+  cluster.barrier_arrive();  // all are there before their shared memory is written (the wait is below)
   int lo, hi;
   part_of(num_pages, cta, &lo, &hi);
   auto nothing = [](int, int32_t, int) {};
   const int free_here = scan_refs(refs, lo, hi, 0, INT32_MAX, warp_sums, [](int, int32_t r) { return r == 0; }, nothing);
+  cluster.barrier_wait();
   const int used = exchange(cluster, cta_counts[0], cta, free_here, hi - lo - free_here).all[1];
-  auto hole = [&](int p, int32_t r) { return p < used && r == 0; };
-  auto mover = [&](int p, int32_t r) { return p >= used && r != 0; };
-  const int holes = scan_refs(refs, lo, hi, 0, INT32_MAX, warp_sums, hole, nothing);
-  const int movers = scan_refs(refs, lo, hi, 0, INT32_MAX, warp_sums, mover, nothing);
+  // free pages of this part below `used` and used ones behind it; only the part that it lies in has to look
+  int holes = lo < used ? free_here : 0;
+  if (lo < used && used < hi)
+    holes = scan_refs(refs, lo, used, 0, INT32_MAX, warp_sums, [](int, int32_t r) { return r == 0; }, nothing);
+  const int movers = hi - lo - free_here - (min(max(used, lo), hi) - lo - holes);
   const Sums s = exchange(cluster, cta_counts[1], cta, holes, movers);
-  scan_refs(refs, lo, hi, s.below[0], INT32_MAX, warp_sums, hole, [&](int p, int32_t, int rank) { __stcg(dst + rank, p); });
-  scan_refs(refs, lo, hi, s.below[1], INT32_MAX, warp_sums, mover, [&](int p, int32_t, int rank) { __stcg(src + rank, p); });
-  for (int p = lo + threadIdx.x; p < hi; p += kThreads) {
-    const int32_t r = __ldcg(refs + p);
-    if (p < used || r == 0) moved[p] = r ? p : -1;
-  }
+  // in page order the part's holes come before its movers
+  scan_refs(
+      refs, lo, hi, 0, INT32_MAX, warp_sums,
+      [&](int p, int32_t r) {
+        if (p < used || r == 0) moved[p] = r ? p : -1;
+        return p < used ? r == 0 : r != 0;
+      },
+      [&](int p, int32_t, int rank) {
+        if (p < used) __stcg(dst + s.below[0] + rank, p);
+        else __stcg(src + s.below[1] + rank - holes, p);
+      });
   cluster.sync();
   for (int i = cta * kThreads + threadIdx.x; i < s.all[1]; i += kCluster * kThreads) {
     const int32_t from = __ldcg(src + i), to = __ldcg(dst + i);
@@ -323,7 +354,6 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     counts[0] = used;
     counts[1] = 0;
   }
-  cluster.sync();
 }
 
 // A table follows the pages' moves.
@@ -424,6 +454,8 @@ Lists lists_of(char* ws, int32_t num_pages, int32_t num_seqs) {
   return l;
 }
 
+size_t take_smem(int32_t num_seqs) { return (size_t(num_seqs + 3) / 4 * 4 + num_seqs + 1) * 4; }
+
 unsigned copy_grid() { return unsigned(8 * sm_count()); }
 
 }  // namespace
@@ -435,8 +467,8 @@ size_t pages_workspace(int32_t num_pages, int32_t num_seqs) {
 cudaError_t launch_pages_reserve(int32_t num_pages, int32_t page_size, int32_t* refs, PageTable t, int32_t* table,
                                  const int32_t* extra, int32_t* counts, int32_t* err, cudaStream_t st) {
   const Demand d{table, t.num_seqs, t.max_pages, page_size, t.lengths, extra};
-  pages_take_kernel<<<kCluster, kThreads, (2 * size_t(t.num_seqs) + 1) * 4, st>>>(refs, num_pages, d, counts, nullptr,
-                                                                                nullptr, nullptr, err);
+  pages_take_kernel<false><<<kCluster, kThreads, take_smem(t.num_seqs), st>>>(refs, num_pages, Fork{}, 0, d, counts,
+                                                                             nullptr, nullptr, nullptr, err);
   return cudaGetLastError();
 }
 
@@ -445,15 +477,24 @@ cudaError_t launch_pages_fork(const PageBuffers& b, int32_t page_size, int32_t* 
                               int32_t* counts, char* ws, int32_t* err, cudaStream_t st) {
   const int32_t num_pages = b.num_pages[0];
   const Lists l = lists_of(ws, num_pages, std::max(t.num_seqs, new_seqs));
-  const int64_t entries = int64_t(t.num_seqs) * t.max_pages + int64_t(new_seqs) * std::max(new_max_pages, 1);
-  const unsigned grid = unsigned(std::clamp<int64_t>((entries + 255) / 256, 1, 8 * sm_count()));
-  pages_rows_kernel<<<grid, 256, 0, st>>>(refs, num_pages, page_size, t, new_seqs, new_max_pages, parents, new_table,
-                                          new_lengths, err);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  const Fork f{t, parents, new_lengths};
   const Demand d{new_table, new_seqs, new_max_pages, page_size, new_lengths, nullptr};
-  e = launch_behind(pages_take_kernel, kCluster, kThreads, (2 * size_t(new_seqs) + 1) * 4, st, refs, num_pages, d,
-                    counts, l.head, l.src, l.dst, err);
+  // tables of a few entries a thread of the cluster: no launch of their own
+  const int64_t entries = int64_t(t.num_seqs) * t.max_pages + int64_t(new_seqs) * std::max(new_max_pages, 1);
+  const bool few = entries <= kFewEntries;
+  cudaError_t e;
+  if (few) {
+    pages_take_kernel<true><<<kCluster, kThreads, take_smem(new_seqs), st>>>(refs, num_pages, f, 1, d, counts, l.head,
+                                                                            l.src, l.dst, err);
+    e = cudaGetLastError();
+  } else {
+    const unsigned grid = unsigned(std::clamp<int64_t>((entries + 255) / 256, 1, 8 * sm_count()));
+    pages_rows_kernel<<<grid, 256, 0, st>>>(refs, num_pages, f, d, err);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = launch_behind(pages_take_kernel<true>, kCluster, kThreads, take_smem(new_seqs), st, refs, num_pages, f, 0, d,
+                      counts, l.head, l.src, l.dst, err);
+  }
   if (e != cudaSuccess || b.n == 0) return e;
   return launch_behind(pages_copy_kernel, copy_grid(), kCopyThreads, 0, st, b, &l.head->n, 0, l.src, l.dst, Follow{},
                        err);
