@@ -57,7 +57,7 @@ struct Cfg {
   static constexpr bool F32 = sizeof(E) == 4;
   static constexpr int DQK = DQK_, DV = DV_, MT = MT_;
   static constexpr int NS = kWarps / MT;       // warps along a tile's slots
-  static constexpr int TT = F32 ? 32 : 64;     // slots of a tile
+  static constexpr int TT_SHIFT = F32 ? 5 : 6, TT = 1 << TT_SHIFT;  // slots of a tile
   static constexpr int TS = TT / NS;           // of a warp
   static constexpr int ROWS = 16 * MT;
   static constexpr int KP = DQK * sizeof(E) / 128, VP = DV * sizeof(E) / 128;  // panels of 128 bytes
@@ -132,11 +132,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return reinterpret_cast<const uint32_t&>(p);
 }
 
-// Address of 16-byte piece `c` of a slot's row in a tile of panels.
-template <int PANELS>
-__device__ __forceinline__ uint32_t piece(uint32_t tile, int shift, int slot, int c) {
-  return tile + (((slot >> shift) * PANELS + (c >> 3)) << (7 + shift)) + ((slot & ((1 << shift) - 1)) << 7) +
-         (((c ^ slot) & 7) << 4);
+// Tiles lie in panels of 128 bytes a slot, 16-byte pieces swizzled: piece c of slot x is piece (c ^ x) % 8 of its row in
+// panel c / 8.  row_of: a lane's row and the low bits of its pieces; piece_of: with the other bits, which are constants.
+__device__ __forceinline__ uint32_t row_of(int slot, int low) { return (slot << 7) | (((slot ^ low) & 7) << 4); }
+template <int TT>
+__device__ __forceinline__ uint32_t piece_of(uint32_t row, int c) {
+  return (row ^ ((c & 7) << 4)) + (c >> 3) * (TT * 128);
 }
 
 // A row's maximum score (before the scale) and sum: what O is multiplied by, and its lse.  A row that saw nothing (or scores of -inf
@@ -271,28 +272,32 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
               window = e0;
               held = window + lane < pages ? kv_page(__ldg(table + window + lane), c.num_pages, c.err) : -1;
             }
-            const int slot0 = tile * TT + (lane << p.box_shift);  // of this lane's copy
+            // a lane a copy: a page's part of the tile and a panel of it
+            const int box = lane & (boxes - 1), panel = lane >> (C::TT_SHIFT - p.box_shift);
+            const int slot0 = tile * TT + (box << p.box_shift);
             const int32_t page = __shfl_sync(~0u, held, ((slot0 >> c.page_shift) - window) & 31);
-            const bool mine = lane < boxes && slot0 < len;
-            const unsigned copies = __ballot_sync(~0u, mine && page >= 0), gone = __ballot_sync(~0u, mine && page < 0);
+            const bool mine = slot0 < len;
+            const unsigned there = __ballot_sync(~0u, panel == 0 && mine && page >= 0);
+            const unsigned gone = __ballot_sync(~0u, panel == 0 && mine && page < 0);
             const int row = ((page * c.hkv + head) << c.page_shift) + (slot0 & ((1 << c.page_shift) - 1));
             if (tiles_sent >= NK) ok = ptx::mbar_wait(ptx::smem_u32(&sh.k_empty[ks]), kphase ^ 1, kSiteKEmpty, ctx);
             if (!__all_sync(~0u, ok)) { ok = false; break; }
             const uint32_t kbar = ptx::smem_u32(&sh.k_full[ks]), vbar = ptx::smem_u32(&sh.v_full[vs]);
             if (lane == 0) {
               sh.absent[ks] = int32_t(gone);
-              ptx::mbar_arrive_expect_tx(kbar, __popc(copies) * (C::KBYTES / TT << p.box_shift));
+              ptx::mbar_arrive_expect_tx(kbar, __popc(there) * (C::KBYTES / TT << p.box_shift));
             }
             __syncwarp();
-            if (mine && page >= 0)
-              ptx::tma_load_3d(base + ks * C::KBYTES + lane * (C::KBYTES / TT << p.box_shift), &p.tk, kbar, 0, row, 0);
+            const uint32_t in_tile = panel * (TT * 128) + (box << (7 + p.box_shift));
+            if (mine && page >= 0 && panel < C::KP)
+              ptx::tma_load_3d(base + ks * C::KBYTES + in_tile, &p.tk, kbar, 0, row, panel);
             ++keys_sent;
             if (tiles_sent >= NV) ok = ptx::mbar_wait(ptx::smem_u32(&sh.v_empty[vs]), vphase ^ 1, kSiteVEmpty, ctx);
             if (!__all_sync(~0u, ok)) { ok = false; break; }
-            if (lane == 0) ptx::mbar_arrive_expect_tx(vbar, __popc(copies) * (C::VBYTES / TT << p.box_shift));
+            if (lane == 0) ptx::mbar_arrive_expect_tx(vbar, __popc(there) * (C::VBYTES / TT << p.box_shift));
             __syncwarp();
-            if (mine && page >= 0)
-              ptx::tma_load_3d(values + vs * C::VBYTES + lane * (C::VBYTES / TT << p.box_shift), &p.tv, vbar, 0, row, 0);
+            if (mine && page >= 0 && panel < C::VP)
+              ptx::tma_load_3d(values + vs * C::VBYTES + in_tile, &p.tv, vbar, 0, row, panel);
             ++tiles_sent;
             if (++ks == NK) ks = 0, kphase ^= 1;
             if (++vs == NV) vs = 0, vphase ^= 1;
@@ -402,13 +407,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
       if constexpr (C::F32) {
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-          const int slot = first_slot + 8 * i + (lane & 7);
+          const uint32_t keys = kt + row_of(first_slot + 8 * i + (lane & 7), lane >> 3);
           float low[4][4] = {};  // the products with lower terms, in four chains, added in the end
-#pragma unroll 2
+#pragma unroll 4
           for (int k = 0; k < C::DQK / 16; ++k) {  // two steps of 8 channels
             uint32_t kf[4];
-            ptx::ldmatrix_x4(kf, piece<C::KP>(kt, p.box_shift, slot, 4 * k + (lane >> 3)));
-            float high[4] = {0.f, 0.f, 0.f, 0.f};
+            ptx::ldmatrix_x4(kf, piece_of<TT>(keys, 4 * k));
+            float high[4];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               uint32_t ah[4], al[4], bh[2], bl[2];
@@ -418,7 +423,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
               for (int j = 0; j < 2; ++j) split(__uint_as_float(kf[2 * x + j]), bh[j], bl[j]);
               ptx::mma_1688(low[2 * x], ah, bl[0], bl[1]);
               ptx::mma_1688(low[2 * x + 1], al, bh[0], bh[1]);
-              ptx::mma_1688(high, ah, bh[0], bh[1]);
+              if (x == 0) ptx::mma_1688_first(high, ah, bh[0], bh[1]);
+              else ptx::mma_1688(high, ah, bh[0], bh[1]);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[i][j] += high[j];
@@ -429,11 +435,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
       } else {
 #pragma unroll
         for (int i = 0; i < NB; i += 2) {
-          const int slot = first_slot + 8 * i + (lane & 7) + (lane >> 4) * 8;
+          const uint32_t keys = kt + row_of(first_slot + 8 * i + (lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
 #pragma unroll
           for (int k = 0; k < C::DQK / 16; ++k) {
             uint32_t kf[4];
-            ptx::ldmatrix_x4(kf, piece<C::KP>(kt, p.box_shift, slot, 2 * k + ((lane >> 3) & 1)));
+            ptx::ldmatrix_x4(kf, piece_of<TT>(keys, 2 * k));
             ptx::mma_16816(s[i], qf[k], kf[0], kf[1]);
             ptx::mma_16816(s[i + 1], qf[k], kf[2], kf[3]);
           }
@@ -515,21 +521,20 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
             split(prob(s[i][1], 1), ah[2], al[2]);
             split(prob(s[i][3], 3), ah[3], al[3]);
             const bool in0 = !GUARD || seen(x), in1 = !GUARD || seen(x + 1);
+            const uint32_t v0 = vt + row_of(x, r0 >> 2) + (r0 & 3) * 4, v1 = vt + row_of(x + 1, r0 >> 2) + (r0 & 3) * 4;
 #pragma unroll
             for (int nb = 0; nb < DV / 8; ++nb) {
-              const int ch = 8 * nb + r0;
-              const uint32_t off = (ch & 3) * 4;
               float v[2];
-              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0]) : "r"(piece<C::VP>(vt, p.box_shift, x, ch >> 2) + off) : "memory");
-              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[1]) : "r"(piece<C::VP>(vt, p.box_shift, x + 1, ch >> 2) + off) : "memory");
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0]) : "r"(piece_of<TT>(v0, 2 * nb)) : "memory");
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[1]) : "r"(piece_of<TT>(v1, 2 * nb)) : "memory");
               if (!in0) v[0] = 0.f;
               if (!in1) v[1] = 0.f;
               uint32_t bh[2], bl[2];
               split(v[0], bh[0], bl[0]);
               split(v[1], bh[1], bl[1]);
               add(o[nb], [&](float (&acc)[4]) {
-                float t[4] = {0.f, 0.f, 0.f, 0.f};
-                ptx::mma_1688(t, ah, bl[0], bl[1]);
+                float t[4];
+                ptx::mma_1688_first(t, ah, bl[0], bl[1]);
                 ptx::mma_1688(t, al, bh[0], bh[1]);
                 ptx::mma_1688(t, ah, bh[0], bh[1]);
 #pragma unroll
@@ -551,11 +556,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
                 mask[y] = (seen(x) ? 0xffffu : 0u) | (seen(x + 1) ? 0xffff0000u : 0u);
               }
             }
-            const int slot = first_slot + 8 * i + (lane & 7) + (lane & 8);
+            const uint32_t vals = vt + row_of(first_slot + 8 * i + (lane & 7) + (lane & 8), lane >> 4);
 #pragma unroll
             for (int nb = 0; nb < DV / 8; nb += 2) {
               uint32_t vf[4];
-              ptx::ldmatrix_x4_trans(vf, piece<C::VP>(vt, p.box_shift, slot, nb + (lane >> 4)));
+              ptx::ldmatrix_x4_trans(vf, piece_of<TT>(vals, nb));
               if constexpr (GUARD) vf[0] &= mask[0], vf[1] &= mask[1], vf[2] &= mask[0], vf[3] &= mask[1];
               add(o[nb], [&](float (&acc)[4]) { ptx::mma_16816(acc, a, vf[0], vf[1]); });
               add(o[nb + 1], [&](float (&acc)[4]) { ptx::mma_16816(acc, a, vf[2], vf[3]); });
@@ -574,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
             uint32_t w[4];
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(piece<C::VP>(vt, p.box_shift, x - tile * TT, i))
+                         : "r"(piece_of<TT>(vt + row_of(x - tile * TT, 0), i))
                          : "memory");
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -761,7 +766,7 @@ bool make_map(CUtensorMap* map, const void* pages, bool f32, int64_t rows, int d
   const int elt = f32 ? 4 : 2, wide = 128 / elt;
   const cuuint64_t dim[3] = {cuuint64_t(wide), cuuint64_t(rows), cuuint64_t(d / wide)};
   const cuuint64_t stride[2] = {cuuint64_t(d * elt), 128};
-  const cuuint32_t size[3] = {cuuint32_t(wide), cuuint32_t(box), cuuint32_t(d / wide)};
+  const cuuint32_t size[3] = {cuuint32_t(wide), cuuint32_t(box), 1};
   const cuuint32_t step[3] = {1, 1, 1};
   return enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pages),
              dim, stride, size, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
