@@ -41,9 +41,14 @@ namespace {
 constexpr int kWarps = 4;  // that compute; the first of four more produces (registers move by four warps)
 constexpr int kThreads = 32 * 2 * kWarps;
 // Registers a thread: two CTAs an SM start with 128; the producers hand theirs to the computing warps.
-constexpr int kLaunchRegs = 128, kComputeRegs = 216, kProducerRegs = 40;
+constexpr int kLaunchRegs = 128, kComputeRegs = 200, kProducerRegs = 56;
 static_assert(kComputeRegs + kProducerRegs == 2 * kLaunchRegs, "what one half takes the other gives");
 constexpr int kMostStages = 6;
+// A cluster of up to eight CTAs a run, in the place of even shares and a second kernel, where the table holds no more
+// tokens than this and the clusters fit the GPU at once.  One sequence of 4K: 12.5 us on the device (even shares: 12.1),
+// 15 us of a host that calls again and again (20); 8 of 4K: 26.9 us (29.7); but one of 8K: 17.0 (13.2), and 8 ragged ones
+// up to 4K: 16.8 (13.5).  Clusters of sixteen start later: one of 4K 13.1 us.
+constexpr int64_t kClusterTokens = 4096;
 constexpr float kLog2e = 1.4426950408889634f;
 // log2 units: a row's reference maximum follows a new one past this (p stays below 2^8 relative to it, so that most
 // tiles leave O as it is)
@@ -115,6 +120,7 @@ struct Params {
   // CTAs, of the run that is cut behind every CTA
   int4* meta;
   int32_t by_run, join_ctas;
+  int32_t cluster;  // 0: shares of all units; otherwise the CTAs of a cluster, which take a run's tiles among them
   float* parts;  // [ctas][2][ROWS][DV + 2]
 };
 
@@ -145,6 +151,30 @@ __device__ __forceinline__ uint32_t piece_of(uint32_t row, int c) {
 __device__ __forceinline__ float inverse_of(float2 ml) { return ml.y == 0.f ? 0.f : 1.f / ml.y; }
 __device__ __forceinline__ float lse_of(float2 ml, float scale) {
   return ml.y == 0.f ? -INFINITY : fmaf(ml.x == -INFINITY ? 0.f : ml.x, scale, logf(ml.y));
+}
+
+// A row of a kv head (of `head` heads' group) to where its query's results go.
+template <int DV>
+__device__ __forceinline__ void store_row(const KvAttnArgs& a, int group, int b, int head, int r, int col, float4 v, float2 ml) {
+  const int t = r / group, g = r - t * group, h = a.c.inter ? head + g * a.c.hkv : head * group + g;
+  const float inv = inverse_of(ml);
+  const int64_t at = ((int64_t(b) * a.n_q + t) * a.c.hq + h) * DV + col;
+  v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+  if (a.o_f32) *reinterpret_cast<float4*>(static_cast<float*>(a.o) + at) = v;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + at) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+  if (col == 0) a.lse[int64_t(h) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] = lse_of(ml, a.c.scale);
+}
+
+// Every thread of a cluster; what was written before is visible behind it.
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank) {
+  uint32_t x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(x) : "r"(addr), "r"(rank));
+  return x;
 }
 
 template <typename C>
@@ -189,7 +219,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
   // where this CTA's share begins: a thread adds up some sequences in a row
   const int64_t most = int64_t(c.max_pages) << c.page_shift;
   const int runs = c.hkv * p.row_tiles;
-  const int per = (c.num_seqs + kThreads - 1) / kThreads, b0 = min(tid * per, c.num_seqs), b1 = min(b0 + per, c.num_seqs);
+  const int rank = p.cluster ? blockIdx.x % p.cluster : 0;
+  const int per = p.cluster ? 0 : (c.num_seqs + kThreads - 1) / kThreads, b0 = min(tid * per, c.num_seqs), b1 = min(b0 + per, c.num_seqs);
   int units = 0;
   for (int b = b0; b < b1; ++b) units += units_of(kv_length(__ldg(p.a.lengths + b), most, c.err), TT) * runs;
   int before = units;
@@ -207,8 +238,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
   }
   before -= units;
   const int n = min(int(gridDim.x), total), cta = blockIdx.x;
-  const int u0 = cta < n ? int(int64_t(total) * cta / n) : total, u1 = cta < n ? int(int64_t(total) * (cta + 1) / n) : total;
-  if (before <= u0 && u0 < before + units) {
+  // a cluster's CTA: one unit, its part of the run
+  const int u0 = p.cluster ? 0 : cta < n ? int(int64_t(total) * cta / n) : total, u1 = p.cluster ? 1 : cta < n ? int(int64_t(total) * (cta + 1) / n) : total;
+  if (p.cluster) {
+    if (tid == 0) sh.start_b = cta / p.cluster / runs, sh.start_off = cta / p.cluster % runs;
+  } else if (before <= u0 && u0 < before + units) {
     int off = u0 - before, b = b0;
     for (;; ++b) {
       const int x = units_of(kv_length(__ldg(p.a.lengths + b), most, nullptr), TT) * runs;
@@ -223,31 +257,42 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
   if (warp >= kWarps) {
     // ------------------------------------------------------------ producer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-    if (warp > kWarps) return;
+    if (warp > kWarps) {
+      if (p.cluster) cluster_meet(), cluster_meet();
+      return;
+    }
     int ks = 0, kphase = 0, vs = 0, vphase = 0, keys_sent = 0, tiles_sent = 0, runs_sent = 0;
     int4 cut = make_int4(0, 0, 0, 0);
     bool ok = true;
-    int b = u0 < u1 ? sh.start_b : 0, off = u0 < u1 ? sh.start_off : 0;
+    int b = u0 < u1 ? sh.start_b : 0, off = u0 < u1 ? sh.start_off : 0;  // (a cluster: its sequence, and its run of that)
     for (int u = u0; u < u1 && ok;) {
-      const int len = kv_length(__ldg(p.a.lengths + b), most, nullptr);
-      const int tiles = (len + TT - 1) / TT, per_run = tiles + 1, r = off / per_run, at = off - r * per_run;
-      const int take = min(per_run - at, u1 - u);
-      const int lo = max(at - 1, 0), hi = at + take - 1;
-      if (hi > lo || tiles == 0) {
+      const int len = kv_length(__ldg(p.a.lengths + b), most, p.cluster && rank == 0 ? c.err : nullptr);
+      const int tiles = (len + TT - 1) / TT, per_run = tiles + 1;
+      int r = off, lo, hi, take = 1, parts = 0;
+      bool first = false, whole = false;
+      if (p.cluster) {
+        lo = int(int64_t(tiles) * rank / p.cluster), hi = int(int64_t(tiles) * (rank + 1) / p.cluster);
+      } else {
+        r = off / per_run;
+        const int at = off - r * per_run;
+        take = min(per_run - at, u1 - u);
+        lo = max(at - 1, 0), hi = at + take - 1;
+        first = lo == 0, whole = first && hi == tiles;
+        // (the last of a run's CTAs is the one with its last unit)
+        if (first && !whole) parts = int((int64_t(u - at + per_run) * n + total - 1) / total) - cta;
+      }
+      if (p.cluster || hi > lo || tiles == 0) {
         const int head = r / p.row_tiles, row0 = (r - head * p.row_tiles) * C::ROWS, rows = min(C::ROWS, p.rows - row0);
         const int slot = runs_sent % QS;
         if (runs_sent >= QS) ok = ptx::mbar_wait(ptx::smem_u32(&sh.q_empty[slot]), (runs_sent / QS - 1) & 1, kSiteQEmpty, ctx);
         if (!__all_sync(~0u, ok)) { ok = false; break; }
-        const bool first = lo == 0, last = hi == tiles;
         const uint32_t bar = ptx::smem_u32(&sh.q_full[slot]);
         if (lane == 0) {
-          sh.run[slot] = RunDesc{b, head, row0, len, lo, hi, first && last, cta * 2 + (first ? 1 : 0)};
+          sh.run[slot] = RunDesc{b, head, row0, len, lo, hi, whole, cta * 2 + (first ? 1 : 0)};
           ptx::mbar_arrive_expect_tx(bar, hi > lo ? rows * C::DQK * sizeof(E) : 0);
         }
         __syncwarp();
         if (first) {
-          // the last of its CTAs is the one with the run's last unit
-          const int parts = last ? 0 : int((int64_t(u - at + per_run) * n + total - 1) / total) - cta;
           const int4 x = make_int4(b, r, parts, cta);
           if (p.by_run && lane == 0) p.meta[b * runs + r] = x;
           if (parts) cut = x;
@@ -307,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
       }
       u += take;
       off += take;
-      if (off == per_run * runs) ++b, off = 0;
+      if (!p.cluster && off == per_run * runs) ++b, off = 0;
     }
     if (lane == 0) {
       if (ok) {
@@ -317,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
           ptx::mbar_arrive(ptx::smem_u32(&sh.q_full[slot]));
         }
       }
-      if (!p.by_run) p.meta[cta] = cut;
+      if (!p.by_run && !p.cluster) p.meta[cta] = cut;
       // no copy is in flight when the CTA's shared memory goes to the next one (computing warps that gave up did not wait)
       const ptx::WaitCtx drain{&sh.drain_abort, c.err, kWaitLimitNs};
       for (int i = max(keys_sent - NK, 0); i < keys_sent; ++i)
@@ -327,6 +372,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
       for (int i = max(runs_sent - QS, 0); i < runs_sent; ++i)
         if (!ok) ptx::mbar_wait(ptx::smem_u32(&sh.q_full[i % QS]), i / QS & 1, kSiteDrain, drain);
     }
+    __syncwarp();
+    if (p.cluster) cluster_meet(), cluster_meet();
     return;
   }
 
@@ -661,28 +708,52 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
           sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
         }
         const float2 ml = sh.row[row];
-        if (!d.whole) {
-          float* to = p.parts + (int64_t(d.slot) * C::ROWS + row) * (DV + 4);
+        if (d.whole) {
+          store_row<DV>(p.a, p.group, d.b, d.head, d.row0 + row, c0 + col, sum, ml);
+        } else {
+          // (a cluster's parts lie where its tiles were)
+          float* to = p.cluster ? reinterpret_cast<float*>(raw + (base - ptx::smem_u32(raw))) + row * (DV + 4)
+                                : p.parts + (int64_t(d.slot) * C::ROWS + row) * (DV + 4);
           *reinterpret_cast<float4*>(to + c0 + col) = sum;
           if (c0 + col == 0) *reinterpret_cast<float2*>(to + DV) = ml;
-          continue;
         }
-        const int t = (d.row0 + row) / p.group, g = d.row0 + row - t * p.group;
-        const int h = c.inter ? d.head + g * c.hkv : d.head * p.group + g;
-        const int64_t at = ((int64_t(d.b) * p.a.n_q + t) * c.hq + h) * DV + c0 + col;
-        const float inv = inverse_of(ml);
-        sum.x *= inv, sum.y *= inv, sum.z *= inv, sum.w *= inv;
-        if (p.a.o_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.a.o) + at) = sum;
-        else
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.o) + at) =
-              make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
-        if (c0 + col == 0)
-          p.a.lse[int64_t(h) * c.num_seqs * p.a.n_q + int64_t(d.b) * p.a.n_q + t] = lse_of(ml, c.scale);
       }
       meet();
       if (!ok) break;
     }
   }
+  if (!p.cluster) return;
+  // the run's parts, each in its CTA's shared memory: a CTA joins some of the rows' pieces of four channels
+  cluster_meet();
+  const int run = blockIdx.x / p.cluster, b = run / runs, r = run - b * runs, head = r / p.row_tiles;
+  const int row0 = (r - head * p.row_tiles) * C::ROWS, rows = min(C::ROWS, p.rows - row0);
+  for (int i = tid * p.cluster + rank; i < rows * (DV / 4) && ok; i += 32 * kWarps * p.cluster) {
+    const int row = i / (DV / 4), col = (i - row * (DV / 4)) * 4;
+    const uint32_t at = base + row * (DV + 4) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < p.cluster; ++k) {
+      float2 ml;
+      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(ml.x), "=f"(ml.y) : "r"(in_cta(at + DV * 4, k)) : "memory");
+      top = fmaxf(top, ml.x);
+    }
+#pragma unroll 4
+    for (int k = 0; k < p.cluster; ++k) {
+      float2 ml;
+      float4 x;
+      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(ml.x), "=f"(ml.y) : "r"(in_cta(at + DV * 4, k)) : "memory");
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                   : "r"(in_cta(at + col * 4, k))
+                   : "memory");
+      const float f = top == -INFINITY ? 1.f : ptx::ex2((ml.x - top) * cs);
+      sum = fmaf(f, ml.y, sum);
+      v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+    }
+    store_row<DV>(p.a, p.group, b, head, row0 + row, col, v, make_float2(top, sum));
+  }
+  cluster_meet();  // (nobody leaves while its part may still be read)
 }
 
 constexpr int kJoinWarps = 8;
@@ -775,15 +846,24 @@ bool make_map(CUtensorMap* map, const void* pages, bool f32, int64_t rows, int d
 
 struct Layout {
   int rows, row_tiles, rows_a_run, ctas;
+  int cluster;
   size_t parts, total;
 };
 // Rows of a run: 16, 32 or 64 (fp32: 32, their queries take twice the room).
-Layout layout_of(int hq, int hkv, int dv, int dtype, int n_q) {
+// Few runs of few tiles: a cluster a run, joined in shared memory, one launch and no parts in the workspace.
+Layout layout_of(int num_seqs, int hq, int hkv, int dv, int dtype, int n_q, int64_t most) {
   Layout x;
   x.rows = hq / hkv * n_q;
   x.rows_a_run = x.rows <= 16 ? 16 : x.rows <= 32 || dtype == CP_DT_F32 ? 32 : 64;
   x.row_tiles = (x.rows + x.rows_a_run - 1) / x.rows_a_run;
   x.ctas = 2 * sm_count();
+  const int64_t runs = int64_t(num_seqs) * hkv * x.row_tiles;
+  x.cluster = 0;
+  if (most <= kClusterTokens)
+    for (int n = 8; n >= 4 && x.cluster == 0; n /= 2)
+      if (runs * n <= x.ctas) x.cluster = n;
+  x.parts = x.total = 256;
+  if (x.cluster) return x;
   x.parts = (size_t(x.ctas) * sizeof(int4) + 255) / 256 * 256;
   x.total = (x.parts + size_t(x.ctas) * 2 * x.rows_a_run * (dv + 4) * 4 + 255) / 256 * 256;
   return x;
@@ -806,6 +886,7 @@ cudaError_t launch(const KvAttnArgs& a, const Layout& x, cudaStream_t st) {
   if (!make_map(&p.tk, none ? any : a.c.k, C::F32, none ? 1 : pool_rows, C::DQK, 1 << p.box_shift) ||
       !make_map(&p.tv, none ? any : a.c.v, C::F32, none ? 1 : pool_rows, C::DV, 1 << p.box_shift))
     return cudaErrorInvalidValue;
+  p.cluster = x.cluster;
   auto kernel = kv_attn_kernel<C>;
   static std::atomic<uint64_t> ready{0};  // devices whose kernel may use that much shared memory
   int dev = 0;
@@ -825,22 +906,31 @@ cudaError_t launch(const KvAttnArgs& a, const Layout& x, cudaStream_t st) {
   const int64_t runs = int64_t(a.c.num_seqs) * a.c.hkv * x.row_tiles;
   p.by_run = runs <= x.ctas;
   p.join_ctas = ctas;
+  cudaLaunchAttribute attr{};
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (x.cluster) {
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = unsigned(x.cluster);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(unsigned(runs * x.cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Room<C>::bytes;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+  }
   kernel<<<unsigned(ctas), kThreads, Room<C>::bytes, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the launch overlaps the kernel before: it waits on the device
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
   // warps a row: eight for up to 8 rows, one for 64 (a CTA for every row of every run that might be cut takes 10 us)
   const int rows = std::min(x.rows, x.rows_a_run);
   const int rows_a_cta = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
   cfg.gridDim = dim3(unsigned(p.by_run ? runs : ctas), unsigned((rows + rows_a_cta - 1) / rows_a_cta));
   cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kv_join_kernel<C>, p, rows_a_cta);
 }
 
@@ -863,17 +953,21 @@ cudaError_t with_dims(const KvAttnArgs& a, const Layout& x, int dqk, int dv, cud
   }
 }
 
+Layout layout_of(const cp_kv_t* c, int32_t n_q) {
+  return layout_of(c->num_seqs, c->hq, c->hkv, c->d_v, c->dtype, n_q, int64_t(c->max_pages) * c->page_size);
+}
+
 }  // namespace
 
-size_t kv_attn_workspace(const cp_kv_t* c, int32_t n_q) { return layout_of(c->hq, c->hkv, c->d_v, c->dtype, n_q).total; }
+size_t kv_attn_workspace(const cp_kv_t* c, int32_t n_q) { return layout_of(c, n_q).total; }
 
 int64_t kv_attn_units(const cp_kv_t* c, int32_t n_q) {
   const int64_t tiles = (int64_t(c->max_pages) * c->page_size + 31) / 32 + 1;
-  return tiles * c->num_seqs * c->hkv * layout_of(c->hq, c->hkv, c->d_v, c->dtype, n_q).row_tiles;
+  return tiles * c->num_seqs * c->hkv * layout_of(c, n_q).row_tiles;
 }
 
 cudaError_t launch_kv_attn(const KvAttnArgs& a, int dqk, int dv, int dtype, cudaStream_t st) {
-  const Layout x = layout_of(a.c.hq, a.c.hkv, dv, dtype, a.n_q);
+  const Layout x = layout_of(a.c.num_seqs, a.c.hq, a.c.hkv, dv, dtype, a.n_q, int64_t(a.c.max_pages) << a.c.page_shift);
   return dtype == CP_DT_BF16 ? with_dims<__nv_bfloat16>(a, x, dqk, dv, st) : with_dims<float>(a, x, dqk, dv, st);
 }
 

@@ -302,12 +302,16 @@ CASES = [  # lengths, hq, hkv, d_qk, d_v, page, n_q, gqa
 ]
 
 
+WIDE = 16400  # slots of a table for which the work is cut evenly, whatever the number of sequences
+
+
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("case", CASES, ids=str)
-def test_attn(case, dtype):
-    """All that no query sees holds NaN."""
+def test_attn(case, dtype, wide):
+    """All that no query sees holds NaN.  wide: a table for many more slots than the sequences hold."""
     lengths, hq, hkv, d_qk, d_v, page, n_q, gqa = case
-    h = Held(lengths, hq, hkv, d_qk, d_v, dtype, page, n_q, gqa)
+    h = Held(lengths, hq, hkv, d_qk, d_v, dtype, page, n_q, gqa, columns=WIDE // page + 1 if wide else None)
     o, lse = h.run()
     assert o.dtype == dtype
     h.check(o, lse)
@@ -331,12 +335,13 @@ def test_attn_many_sequences(dtype):
     h.check(*h.run(), rows=lambda b, t, x: b % 7 == 0 or lengths[b] < 2)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
-def test_attn_slots_that_some_queries_see(dtype, bad):
+def test_attn_slots_that_some_queries_see(dtype, bad, wide):
     """A value (or key) that the last queries see does not reach the ones before."""
     n_q = 6
-    h = Held([133, 64, 66, 5], 4, 2, 128, 64, dtype, 64, n_q, seed=4)
+    h = Held([133, 64, 66, 5], 4, 2, 128, 64, dtype, 64, n_q, seed=4, columns=WIDE // 64 + 1 if wide else None)
     for b, n in enumerate(h.lengths):
         h.v[b][n - 2, :, 3] = bad  # seen by the last two queries
         h.k[b][n - 1, 1, 7] = bad  # seen by the last one
@@ -351,19 +356,21 @@ def test_attn_slots_that_some_queries_see(dtype, bad):
         assert np.isfinite(o[b, n_q - 1, :2][:, others]).all()  # (heads of the first key head)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_attn_queries_that_are_not_finite(dtype):
-    h = Held([100, 40], 8, 2, 64, 64, dtype, 32, 2, seed=5)
+def test_attn_queries_that_are_not_finite(dtype, wide):
+    h = Held([100, 40], 8, 2, 64, 64, dtype, 32, 2, seed=5, columns=WIDE // 32 + 1 if wide else None)
     h.q[0, 1, 2, 5], h.q[1, 0, 7, 0] = math.nan, math.inf
     o, lse = h.run()
     h.check(o, lse, rows=lambda b, t, x: (b, t, x) not in ((0, 1, 2), (1, 0, 7)))
     assert torch.isnan(o[0, 1, 2]).all() and torch.isnan(lse[2, 1]) and torch.isnan(o[1, 0, 7]).all()
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_attn_magnitudes(dtype):
+def test_attn_magnitudes(dtype, wide):
     """Scores from -2e4 to 2e4: one slot takes all, whichever comes first; keys of zero: the mean."""
-    h = Held([300, 301], 4, 1, 64, 64, dtype, 64, seed=6, spread=3000.0)
+    h = Held([300, 301], 4, 1, 64, 64, dtype, 64, seed=6, spread=3000.0, columns=WIDE // 64 + 1 if wide else None)
     o, lse = h.run()
     for b in range(2):
         s = f64(h.q[b, 0]) @ f64(h.k[b])[:, 0].T * h.scale
@@ -380,10 +387,11 @@ def test_attn_magnitudes(dtype):
     h.check(*h.run())
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_attn_pages_and_lengths_outside(dtype):
+def test_attn_pages_and_lengths_outside(dtype, wide):
     """A page outside the pool: its slots are absent.  A length outside the table: clamped.  Both are recorded."""
-    h = Held([200, 90, 130], 4, 2, 128, 128, dtype, 16, seed=8, columns=13)
+    h = Held([200, 90, 130], 4, 2, 128, 128, dtype, 16, seed=8, columns=WIDE // 16 + 1 if wide else 13)
     h.table[0, 3], h.table[0, 12], h.table[2, 0] = 1 << 20, -1, h.pages
     h.cache.page_table.copy_(ints(h.table.tolist()))
     o, lse = h.run()
