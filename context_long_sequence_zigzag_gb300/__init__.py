@@ -1055,8 +1055,9 @@ def _rows_of(table, dev):
 
 
 def cp_pages_reserve(pool: PagePool, table, lengths, extra, counts=None, stream=None):
-    """Gives every sequence b of lengths[b] tokens the pages that extra[b] more need, in table [B, max_pages] (in
-    place).  Returns counts int32 [2]: pages in use, and entries that got none (they are -1)."""
+    """Gives every sequence b of lengths[b] tokens the pages that extra[b] more need, or takes those back that it needs
+    no more (extra below 0), in table [B, max_pages] (in place).  Returns counts int32 [2]: pages in use, and entries
+    that got none (they are -1)."""
     dev, temps = pool.device, []
     B, columns, pt = _rows_of(table, dev)
     counts, pc = pool._out(counts, "counts", (2,), temps)

@@ -136,7 +136,7 @@ struct Demand {
   int32_t* table;
   int32_t num_seqs, max_pages, page_size;
   const int32_t* lengths;
-  const int32_t* extra;  // reserve: tokens to come
+  const int32_t* extra;  // reserve: tokens to come, or to go
 };
 
 // What a fork starts from and leaves.
@@ -248,14 +248,21 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
     for (int b = tid; b < d.num_seqs; b += kThreads) {
       const int64_t most = int64_t(d.max_pages) * d.page_size;
       const int32_t n = kv_length(__ldg(d.lengths + b), most, err);
-      const int64_t want = int64_t(n) + max(__ldg(d.extra + b), 0);
+      const int64_t want = max(int64_t(n) + __ldg(d.extra + b), int64_t(0));
       if (want > most) kv_error(err, kKvLength);
-      const int32_t held = pages_of(n, d.page_size);
+      const int32_t held = pages_of(n, d.page_size), needs = pages_of(min(want, most), d.page_size);
       first[b] = held;
-      prefix[b] = pages_of(min(want, most), d.page_size) - held;
+      prefix[b] = max(needs - held, 0);
+      // what a shorter sequence lets go of: one CTA a sequence
+      if (b / kThreads % kCluster == cta)
+        for (int32_t e = needs; e < held; ++e) {
+          int32_t* entry = d.table + int64_t(b) * d.max_pages + e;
+          const int32_t p = kv_page(*entry, num_pages, err);
+          if (p >= 0) atomicSub(refs + p, 1);
+          *entry = -1;
+        }
     }
-    __syncthreads();
-    cluster.barrier_arrive();  // all are there before their shared memory is written (the wait is below)
+    cluster.sync();  // before the free pages are counted, and shared memory is written from other CTAs
   }
   // demands to a prefix sum
   int wanted = 0;
@@ -272,7 +279,6 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
 
   auto is_free = [](int, int32_t r) { return r == 0; };
   const int free_here = scan_refs(refs, lo, hi, 0, INT32_MAX, warp_sums, is_free, [](int, int32_t, int) {});
-  if constexpr (!FORK) cluster.barrier_wait();
   // (hi - lo less the free ones includes negative counts of a caller's mistake: in use, as they are not free)
   const Sums s = exchange(cluster, cta_counts, cta, free_here, hi - lo - free_here);
   const int given = min(wanted, s.all[0]);

@@ -634,11 +634,15 @@ cp_status_t cp_pages_validate(const cp_pages_t* pool);
 cp_status_t cp_pages_workspace_size(const cp_pages_t* pool, int32_t num_seqs, size_t* bytes);
 
 /* Room for new tokens: sequence b of lengths[b] tokens gets the pages that
- * lengths[b] + extra[b] tokens need besides those it holds.
- *   table   : device int32 [num_seqs][max_pages], entries written behind a
- *             sequence's last page only
+ * lengths[b] + extra[b] tokens need besides those it holds, or lets go of those
+ * that it needs no more (extra below 0: tokens taken back); the latter first.
+ * It then holds what lengths[b] + extra[b] tokens need, which is the length that
+ * later calls are to be given.  A sequence cut inside a page that others hold has
+ * to go through cp_pages_fork before it is written again.
+ *   table   : device int32 [num_seqs][max_pages], written where pages come or go
+ *             (-1: gone)
  *   lengths : device int32 [num_seqs], not changed
- *   extra   : device int32 [num_seqs], tokens to come (below 0: 0) */
+ *   extra   : device int32 [num_seqs] */
 cp_status_t cp_pages_reserve(const cp_pages_t* pool, int32_t num_seqs, int32_t max_pages, int32_t* table,
                              const int32_t* lengths, const int32_t* extra, int32_t* counts, cp_stream_t stream);
 

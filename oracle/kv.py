@@ -84,7 +84,10 @@ class Pages:
     def reserve(self, table, lengths, extra):
         rows, unmet = self.held(table, lengths), 0
         for row, n, x in zip(rows, lengths, extra):
-            while len(row) < -(-(int(n) + max(int(x), 0)) // self.page_size):
+            while len(row) > -(-max(int(n) + int(x), 0) // self.page_size):
+                self.refs[row.pop()] -= 1
+        for row, n, x in zip(rows, lengths, extra):
+            while len(row) < -(-(int(n) + int(x)) // self.page_size):
                 p = self._lowest()
                 unmet += p < 0
                 if p >= 0:

@@ -17,6 +17,9 @@ Tolerances, derived from the arithmetic (half steps: fp32 2^-24, bf16 2^-8 of th
 """
 
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -28,6 +31,7 @@ pytestmark = pytest.mark.gpu
 
 cpa = pytest.importorskip("context_long_sequence_zigzag_gb300")
 BF, F32 = torch.bfloat16, torch.float32
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(autouse=True)
@@ -299,6 +303,7 @@ CASES = [  # lengths, hq, hkv, d_qk, d_v, page, n_q, gqa
     ([20, 333], 16, 1, 64, 64, 64, 16, "blocked"),
     ([257], 71, 1, 128, 128, 64, 1, "blocked"),
     ([77, 0, 600], 24, 1, 192, 128, 128, 5, "blocked"),
+    ([150], 130, 1, 128, 64, 32, 16, "interleaved"),
 ]
 
 
@@ -482,7 +487,7 @@ def test_fork_and_reserve(B, new, most, page, pages, seed):
         for a, b in pairs:
             y[b] = y[a]
         assert torch.equal(x, y)
-    extra = [int(x) for x in rng.randint(-2, 2 * page, new)]
+    extra = [int(x) for x in rng.randint(-2 * page, 2 * page, new)]
     extra = [min(x, columns * page - m) for x, m in zip(extra, want_n)]
     counts = cpa.cp_pages_reserve(pool, t, n, ints(extra))
     held = as_table(want, columns)
@@ -490,6 +495,75 @@ def test_fork_and_reserve(B, new, most, page, pages, seed):
     assert cpa.cp_device_status() == (0x305 if want_counts[1] else 0)
     assert t.tolist() == as_table(want, columns) and counts.tolist() == want_counts and pool.refs.tolist() == model.refs
     assert n.tolist() == want_n
+
+
+def test_reserve_takes_back():
+    """Speculated tokens that go again, pages that others hold, more than a sequence has; what comes free is given in
+    the same call."""
+    pool = cpa.PagePool(ints([1, 1, 2, 1, 1]), [], 4)
+    table = ints([[0, 1, -1], [2, 3, 9], [2, 4, -1]])
+    counts = cpa.cp_pages_reserve(pool, table, ints([8, 5, 6]), ints([-3, -5, 6]))
+    assert cpa.cp_device_status() == 0 and counts.tolist() == [5, 0]
+    assert table.tolist() == [[0, 1, -1], [-1, -1, 9], [2, 4, 3]] and pool.refs.tolist() == [1, 1, 1, 1, 1]
+    counts = cpa.cp_pages_reserve(pool, table, ints([5, 0, 12]), ints([-1, 0, -(1 << 31)]))
+    assert counts.tolist() == [1, 0] and table.tolist() == [[0, -1, -1], [-1, -1, 9], [-1, -1, -1]]
+
+
+def test_offsets_past_32_bits():
+    """Pools of over 2^32 bytes and 2^31 elements: append, attention, copies and compaction in their last pages."""
+    pages, d = 135000, 128
+    kp, vp = (torch.empty(pages, 2, 64, d, dtype=BF, device="cuda") for _ in range(2))
+    assert kp.numel() > 1 << 31
+    rng = np.random.RandomState(20)
+    last = [pages - 1, pages - 3, 5]
+    table = ints([last])
+    cache = cpa.KvCache(kp, vp, table, 4)
+    k, v = randn(rng, (150, 2, d), BF), randn(rng, (150, 2, d), BF)
+    cpa.cp_kv_append(cache, k, v, ints([0, 150]), ints([0]))
+    q = randn(rng, (1, 1, 4, d), BF)
+    h = Held.__new__(Held)
+    h.lengths, h.hq, h.hkv, h.n_q, h.gqa, h.scale, h.kp, h.k, h.v, h.q = [150], 4, 2, 1, "blocked", d ** -0.5, kp, [k], [v], q
+    h.cache = cache
+    first = h.run()
+    h.check(*first)
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    refs[torch.tensor(last, device="cuda")] = 1
+    pool = cpa.PagePool(refs, [kp, vp], 64)
+    new, moved, counts = cpa.cp_pages_compact(pool, table, ints([150]))
+    assert counts.tolist() == [3, 0] and new.tolist() == [[2, 1, 0]]  # (pages 5, then the two at the end, in order)
+    again = cpa.cp_kv_attn(cpa.KvCache(kp, vp, new, 4), q, ints([150]))
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+    cpa.cp_pages_copy(pool, new[0], ints([pages - 2, pages - 5, pages - 4]))
+    again = cpa.cp_kv_attn(cpa.KvCache(kp, vp, ints([[pages - 2, pages - 5, pages - 4]]), 4), q, ints([150]))
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def test_first_calls_in_a_capture():
+    """A process whose first calls are captured (no kernel loaded, no attribute set before)."""
+    code = """
+import torch, context_long_sequence_zigzag_gb300 as cpa
+ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+bf = dict(dtype=torch.bfloat16, device="cuda")
+kp, vp, q = torch.zeros(8, 2, 64, 128, **bf), torch.ones(8, 2, 64, 128, **bf), torch.ones(2, 1, 4, 128, **bf)
+k = torch.ones(2, 2, 128, **bf)
+table, lengths, parents, extra, cu = ints([[0, 1], [2, 3]]), ints([65, 3]), ints([0, 0]), ints([1, 1]), ints([0, 1, 2])
+pool = cpa.PagePool(ints([1, 1, 1, 0, 0, 0, 0, 0]), [kp, vp])
+rope = cpa.Rope([1.0] * 64)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    t, n, _ = cpa.cp_pages_fork(pool, table, lengths, parents)
+    cpa.cp_pages_reserve(pool, t, n, extra)
+    cache = cpa.KvCache(kp, vp, t, 4)
+    cpa.cp_kv_append(cache, k, k, cu, n, rope=rope)
+    o, lse = cpa.cp_kv_attn(cache, cpa.cp_rope(rope, n, q[:, 0]).view_as(q), n + extra)
+    new, moved, counts = cpa.cp_pages_compact(pool, t, n + extra)
+g.replay()
+torch.cuda.synchronize()
+assert t.tolist() == [[0, 1], [0, 2]] and torch.equal(o, torch.ones_like(o)), (t, o)
+assert counts.tolist() == [3, 0] and cpa.cp_device_status() == 0
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=240)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_fork_of_pages_held_elsewhere():

@@ -50,6 +50,8 @@ def test_oracle_pages_by_hand():
     assert pairs == [(3, 0), (3, 2)] and pool.refs == [1, 1, 1, 1, 0, 4, 0] and counts == [5, 0]
     rows, counts = pool.reserve([r + [-1] * (4 - len(r)) for r in rows], n, [2, 3, 5, 1, 0, 0])
     assert rows == [[5, 3], [5, 0, 4], [6, -1], [5, 1, -1], [5, 2], []] and counts == [7, 2]
+    rows, counts = pool.reserve([r + [-1] * (4 - len(r)) for r in rows], [8, 9, 1, 9, 6, 0], [-5, -9, 0, 3, 4, 0])
+    assert rows == [[5], [], [6], [5, 1, -1], [5, 2, 0], []] and counts == [5, 0]
     pool = oracle.Pages([0, 3, 0, 0, 1, 2], 4)
     assert pool.compact() == ([-1, 1, -1, -1, 0, 2], [(4, 0), (5, 2)]) and pool.refs == [1, 3, 2, 0, 0, 0]
     # a page that another sequence holds whole is not written: both of these get copies
