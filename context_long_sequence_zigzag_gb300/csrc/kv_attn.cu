@@ -44,6 +44,7 @@ constexpr int kThreads = 32 * 2 * kWarps;
 constexpr int kLaunchRegs = 128, kComputeRegs = 200, kProducerRegs = 56;
 static_assert(kComputeRegs + kProducerRegs == 2 * kLaunchRegs, "what one half takes the other gives");
 constexpr int kMostStages = 6;
+constexpr int kFewSeqs = 32;
 // A cluster of up to eight CTAs a run, in the place of even shares and a second kernel, where the table holds no more
 // tokens than this and the clusters fit the GPU at once.  One sequence of 4K: 12.5 us on the device (even shares: 12.1),
 // 15 us of a host that calls again and again (20); 8 of 4K: 26.9 us (29.7); but one of 8K: 17.0 (13.2), and 8 ragged ones
@@ -127,6 +128,27 @@ struct Params {
 // units of a sequence's run: its tiles and its start
 __device__ __forceinline__ int units_of(int len, int tt) { return (len + tt - 1) / tt + 1; }
 
+// All units cut for n CTAs, none without a unit: each gets `least` of them, the first `more` one more.  (One division of
+// 32 bits: the CTA's first copy waits for it.)
+struct Share {
+  int n, least, more;
+  __device__ Share(int total, int ctas) : n(min(ctas, total)), least(n ? total / n : 0), more(total - least * n) {}
+  // first unit of a CTA; that of CTA n and those behind it: past the last
+  __device__ int first(int cta) const { return cta < n ? least * cta + min(cta, more) : least * n + more; }
+  __device__ int cta_of(int unit) const {
+    const int x = unit - more * (least + 1);
+    return x < 0 ? unit / (least + 1) : more + x / least;
+  }
+};
+__device__ __forceinline__ int warp_sum_up_to(int x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(~0u, x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
 // x as two terms of 11 bits: the first rounded, of the rest (at most 2^-11 of x) the MMA cuts what is below 2^-10 of
 // it.  A NaN stays in the second term whatever becomes of it in the first.
 __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
@@ -192,64 +214,64 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const KvCache& c = p.a.c;
   ptx::grid_launch_dependents();
-  if (tid == 32 * kWarps) {
-    ptx::prefetch_tmap(&p.tk);
-    ptx::prefetch_tmap(&p.tv);
-  }
-  if (tid == 0) {
-    for (int i = 0; i < QS; ++i) {
-      ptx::mbar_init(ptx::smem_u32(&sh.q_full[i]), 1);
-      ptx::mbar_init(ptx::smem_u32(&sh.q_empty[i]), kWarps);
-    }
-    for (int i = 0; i < kMostStages; ++i) {
-      ptx::mbar_init(ptx::smem_u32(&sh.k_full[i]), 1);
-      ptx::mbar_init(ptx::smem_u32(&sh.v_full[i]), 1);
-      ptx::mbar_init(ptx::smem_u32(&sh.k_empty[i]), kWarps);
-      ptx::mbar_init(ptx::smem_u32(&sh.v_empty[i]), kWarps);
-    }
-    ptx::mbar_init(ptx::smem_u32(&sh.joined), kWarps);
-    ptx::fence_barrier_init();
-    sh.abort = sh.drain_abort = 0;
-  }
-  // rows past the last of a run stay 0
-  for (uint32_t i = tid * 16; i < QS * C::QBYTES; i += kThreads * 16)
-    *reinterpret_cast<uint4*>(raw + (queries - ptx::smem_u32(raw)) + i) = make_uint4(0, 0, 0, 0);
-  ptx::fence_proxy_async_smem();
-
-  // where this CTA's share begins: a thread adds up some sequences in a row
   const int64_t most = int64_t(c.max_pages) << c.page_shift;
-  const int runs = c.hkv * p.row_tiles;
-  const int rank = p.cluster ? blockIdx.x % p.cluster : 0;
-  const int per = p.cluster ? 0 : (c.num_seqs + kThreads - 1) / kThreads, b0 = min(tid * per, c.num_seqs), b1 = min(b0 + per, c.num_seqs);
-  int units = 0;
-  for (int b = b0; b < b1; ++b) units += units_of(kv_length(__ldg(p.a.lengths + b), most, c.err), TT) * runs;
-  int before = units;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int x = __shfl_up_sync(~0u, before, d);
-    if (lane >= d) before += x;
-  }
-  if (lane == 31) sh.warp_units[warp] = before;
-  __syncthreads();
-  int total = 0;
-  for (int w = 0; w < 2 * kWarps; ++w) {
-    if (w == warp) before += total;
-    total += sh.warp_units[w];
-  }
-  before -= units;
-  const int n = min(int(gridDim.x), total), cta = blockIdx.x;
-  // a cluster's CTA: one unit, its part of the run
-  const int u0 = p.cluster ? 0 : cta < n ? int(int64_t(total) * cta / n) : total, u1 = p.cluster ? 1 : cta < n ? int(int64_t(total) * (cta + 1) / n) : total;
-  if (p.cluster) {
-    if (tid == 0) sh.start_b = cta / p.cluster / runs, sh.start_off = cta / p.cluster % runs;
-  } else if (before <= u0 && u0 < before + units) {
-    int off = u0 - before, b = b0;
-    for (;; ++b) {
-      const int x = units_of(kv_length(__ldg(p.a.lengths + b), most, nullptr), TT) * runs;
-      if (off < x) break;
-      off -= x;
+  const int runs = c.hkv * p.row_tiles, cta = blockIdx.x, rank = p.cluster ? cta % p.cluster : 0;
+  const bool few = c.num_seqs <= kFewSeqs;  // the producer adds their lengths up by itself
+  int32_t few_length = 0;
+  if (warp == kWarps) {
+    if (few && lane < c.num_seqs) few_length = __ldg(p.a.lengths + lane);
+    if (lane == 0) {
+      ptx::prefetch_tmap(&p.tk);
+      ptx::prefetch_tmap(&p.tv);
+      for (int i = 0; i < QS; ++i) {
+        ptx::mbar_init(ptx::smem_u32(&sh.q_full[i]), 1);
+        ptx::mbar_init(ptx::smem_u32(&sh.q_empty[i]), kWarps);
+      }
+      for (int i = 0; i < NK; ++i) {
+        ptx::mbar_init(ptx::smem_u32(&sh.k_full[i]), 1);
+        ptx::mbar_init(ptx::smem_u32(&sh.k_empty[i]), kWarps);
+      }
+      for (int i = 0; i < NV; ++i) {
+        ptx::mbar_init(ptx::smem_u32(&sh.v_full[i]), 1);
+        ptx::mbar_init(ptx::smem_u32(&sh.v_empty[i]), kWarps);
+      }
+      ptx::mbar_init(ptx::smem_u32(&sh.joined), kWarps);
+      ptx::fence_barrier_init();
+      sh.abort = sh.drain_abort = 0;
     }
-    sh.start_b = b, sh.start_off = off;
+  } else if (warp < kWarps) {
+    // rows past the last of a run's stay 0
+    const uint32_t from = min(C::ROWS, p.rows) * C::QPITCH;
+    for (int slot = 0; slot < QS; ++slot)
+      for (uint32_t i = from + tid * 16; i + 16 <= C::ROWS * C::QPITCH; i += 32 * kWarps * 16)
+        *reinterpret_cast<uint4*>(raw + (queries + slot * C::QBYTES - ptx::smem_u32(raw)) + i) = make_uint4(0, 0, 0, 0);
+    ptx::fence_proxy_async_smem();
+  }
+  if (!p.cluster && !few) {
+    // where this CTA's share begins: a thread adds up some sequences in a row
+    const int per = (c.num_seqs + kThreads - 1) / kThreads, b0 = min(tid * per, c.num_seqs), b1 = min(b0 + per, c.num_seqs);
+    int units = 0;
+    for (int b = b0; b < b1; ++b) units += units_of(kv_length(__ldg(p.a.lengths + b), most, c.err), TT) * runs;
+    int before = warp_sum_up_to(units, lane);
+    if (lane == 31) sh.warp_units[warp] = before;
+    __syncthreads();
+    int total = 0;
+    for (int w = 0; w < 2 * kWarps; ++w) {
+      if (w == warp) before += total;
+      total += sh.warp_units[w];
+    }
+    before -= units;
+    const int u0 = Share(total, int(gridDim.x)).first(cta);
+    if (tid == 0) sh.total = total;
+    if (before <= u0 && u0 < before + units) {
+      int off = u0 - before, b = b0;
+      for (;; ++b) {
+        const int y = units_of(kv_length(__ldg(p.a.lengths + b), most, nullptr), TT) * runs;
+        if (off < y) break;
+        off -= y;
+      }
+      sh.start_b = b, sh.start_off = off;
+    }
   }
   __syncthreads();
   const ptx::WaitCtx ctx{&sh.abort, c.err, kWaitLimitNs};
@@ -264,25 +286,44 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
     int ks = 0, kphase = 0, vs = 0, vphase = 0, keys_sent = 0, tiles_sent = 0, runs_sent = 0;
     int4 cut = make_int4(0, 0, 0, 0);
     bool ok = true;
-    int b = u0 < u1 ? sh.start_b : 0, off = u0 < u1 ? sh.start_off : 0;  // (a cluster: its sequence, and its run of that)
+    // this CTA's units u0 .. u1 - 1; the first is unit `off` of sequence b.  (A cluster's CTA: one
+    // unit, its part of run `off` of sequence b.)
+    int b = 0, off = 0, u0 = 0, u1 = 1;
+    Share share(0, 0);
+    if (p.cluster) {
+      b = cta / p.cluster / runs, off = cta / p.cluster - b * runs;
+    } else {
+      if (few) {
+        const int units = lane < c.num_seqs ? units_of(kv_length(few_length, most, c.err), TT) * runs : 0;
+        const int upto = warp_sum_up_to(units, lane);
+        share = Share(__shfl_sync(~0u, upto, 31), int(gridDim.x));
+        off = share.first(cta) - (upto - units);
+        const unsigned here = __ballot_sync(~0u, off >= 0 && off < units);
+        b = here ? __ffs(here) - 1 : 0;
+        off = __shfl_sync(~0u, off, b);
+      } else {
+        share = Share(sh.total, int(gridDim.x));
+        b = sh.start_b, off = sh.start_off;
+      }
+      u0 = share.first(cta), u1 = share.first(cta + 1);
+    }
     for (int u = u0; u < u1 && ok;) {
       const int len = kv_length(__ldg(p.a.lengths + b), most, p.cluster && rank == 0 ? c.err : nullptr);
       const int tiles = (len + TT - 1) / TT, per_run = tiles + 1;
-      int r = off, lo, hi, take = 1, parts = 0;
+      int r = off, lo, hi, take = 1;
       bool first = false, whole = false;
       if (p.cluster) {
-        lo = int(int64_t(tiles) * rank / p.cluster), hi = int(int64_t(tiles) * (rank + 1) / p.cluster);
+        lo = tiles * rank / p.cluster, hi = tiles * (rank + 1) / p.cluster;  // (at most kClusterTokens / 32 tiles)
       } else {
         r = off / per_run;
         const int at = off - r * per_run;
         take = min(per_run - at, u1 - u);
         lo = max(at - 1, 0), hi = at + take - 1;
         first = lo == 0, whole = first && hi == tiles;
-        // (the last of a run's CTAs is the one with its last unit)
-        if (first && !whole) parts = int((int64_t(u - at + per_run) * n + total - 1) / total) - cta;
       }
       if (p.cluster || hi > lo || tiles == 0) {
-        const int head = r / p.row_tiles, row0 = (r - head * p.row_tiles) * C::ROWS, rows = min(C::ROWS, p.rows - row0);
+        const int head = p.row_tiles == 1 ? r : r / p.row_tiles;
+        const int row0 = (r - head * p.row_tiles) * C::ROWS, rows = min(C::ROWS, p.rows - row0);
         const int slot = runs_sent % QS;
         if (runs_sent >= QS) ok = ptx::mbar_wait(ptx::smem_u32(&sh.q_empty[slot]), (runs_sent / QS - 1) & 1, kSiteQEmpty, ctx);
         if (!__all_sync(~0u, ok)) { ok = false; break; }
@@ -292,36 +333,32 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
           ptx::mbar_arrive_expect_tx(bar, hi > lo ? rows * C::DQK * sizeof(E) : 0);
         }
         __syncwarp();
-        if (first) {
-          const int4 x = make_int4(b, r, parts, cta);
-          if (p.by_run && lane == 0) p.meta[b * runs + r] = x;
-          if (parts) cut = x;
-        }
         if (hi > lo) {
+          // pages of the part, 32 at a time, a lane each
+          const int32_t* table = c.table + int64_t(b) * c.max_pages;
+          const int pages = (len + (1 << c.page_shift) - 1) >> c.page_shift;
+          int window = (lo * TT) >> c.page_shift;
+          int32_t held = window + lane < pages ? __ldg(table + window + lane) : -1;
           for (int i = lane; i < rows; i += 32) {
-            const int t = (row0 + i) / p.group, g = row0 + i - t * p.group;
+            const int t = p.a.n_q == 1 ? 0 : (row0 + i) / p.group, g = row0 + i - t * p.group;
             const int h = c.inter ? head + g * c.hkv : head * p.group + g;
             ptx::bulk_load(queries + slot * C::QBYTES + i * C::QPITCH,
                            static_cast<const E*>(p.a.q) + ((int64_t(b) * p.a.n_q + t) * c.hq + h) * C::DQK,
                            C::DQK * sizeof(E), bar);
           }
-          // pages of the part, 32 at a time, a lane each
-          const int32_t* table = c.table + int64_t(b) * c.max_pages;
-          const int pages = (len + (1 << c.page_shift) - 1) >> c.page_shift;
-          int window = -32;
-          int32_t held = -1;
           const int boxes = TT >> p.box_shift;
           for (int tile = lo; tile < hi && ok; ++tile) {
             const int e0 = (tile * TT) >> c.page_shift;
-            if (e0 + boxes > window + 32 || window < 0) {
+            if (e0 + boxes > window + 32) {
               window = e0;
-              held = window + lane < pages ? kv_page(__ldg(table + window + lane), c.num_pages, c.err) : -1;
+              held = window + lane < pages ? __ldg(table + window + lane) : -1;
             }
             // a lane a copy: a page's part of the tile and a panel of it
             const int box = lane & (boxes - 1), panel = lane >> (C::TT_SHIFT - p.box_shift);
             const int slot0 = tile * TT + (box << p.box_shift);
-            const int32_t page = __shfl_sync(~0u, held, ((slot0 >> c.page_shift) - window) & 31);
+            int32_t page = __shfl_sync(~0u, held, ((slot0 >> c.page_shift) - window) & 31);
             const bool mine = slot0 < len;
+            if (mine) page = kv_page(page, c.num_pages, c.err);
             const unsigned there = __ballot_sync(~0u, panel == 0 && mine && page >= 0);
             const unsigned gone = __ballot_sync(~0u, panel == 0 && mine && page < 0);
             const int row = ((page * c.hkv + head) << c.page_shift) + (slot0 & ((1 << c.page_shift) - 1));
@@ -347,6 +384,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
             if (++ks == NK) ks = 0, kphase ^= 1;
             if (++vs == NV) vs = 0, vphase ^= 1;
           }
+        }
+        if (first) {  // (what the second kernel reads; the copies come first)
+          const int parts = whole ? 0 : share.cta_of(u + take - (hi + 1) + tiles) - cta + 1;
+          const int4 x = make_int4(b, r, parts, cta);
+          if (p.by_run && lane == 0) p.meta[b * runs + r] = x;
+          if (parts) cut = x;
         }
         ++runs_sent;
       }
