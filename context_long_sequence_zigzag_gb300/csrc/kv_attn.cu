@@ -3,7 +3,7 @@
 // the cache with the running maximum and sum of the softmax.
 //
 // What bounds it: the cache's bytes, read once (d_qk + d_v elements a slot and
-// head for 4 (d_qk + d_v) G n_q FLOPs / 2).  With the 1 to 64 rows that share
+// head, for 2 (d_qk + d_v) G n_q FLOPs).  With the 1 to 64 rows that share
 // a head a 128-row tcgen05 tile would be mostly empty and its accumulator a
 // detour through TMEM; warp-level MMAs of 16 rows keep up with the copies.
 //
@@ -13,7 +13,7 @@
 // are cut evenly over the CTAs, on the device, from the lengths: a long
 // sequence keeps every SM busy, and a captured graph replays with new lengths.
 // A cut run's parts go to the workspace and a second kernel joins them, whose
-// launch overlaps the first.
+// launch overlaps the first.  Few short sequences take a cluster a run instead.
 //
 // A CTA: a producer warp looks the pages up and brings tiles of K and V in by
 // TMA, 128-byte swizzled panels through a ring of stages; queries come two
@@ -122,7 +122,7 @@ struct Params {
   int4* meta;
   int32_t by_run, join_ctas;
   int32_t cluster;  // 0: shares of all units; otherwise the CTAs of a cluster, which take a run's tiles among them
-  float* parts;  // [ctas][2][ROWS][DV + 2]
+  float* parts;  // [ctas][2][ROWS][DV + 4]: O, its maximum and sum
 };
 
 // units of a sequence's run: its tiles and its start
@@ -168,8 +168,8 @@ __device__ __forceinline__ uint32_t piece_of(uint32_t row, int c) {
   return (row ^ ((c & 7) << 4)) + (c >> 3) * (TT * 128);
 }
 
-// A row's maximum score (before the scale) and sum: what O is multiplied by, and its lse.  A row that saw nothing (or scores of -inf
-// alone) has -inf and 0; a NaN stays one.
+// A row's maximum score (before the scale) and sum: what O is multiplied by, and its lse.  A row that saw nothing (or
+// scores of -inf alone) has -inf and 0; a NaN stays one.
 __device__ __forceinline__ float inverse_of(float2 ml) { return ml.y == 0.f ? 0.f : 1.f / ml.y; }
 __device__ __forceinline__ float lse_of(float2 ml, float scale) {
   return ml.y == 0.f ? -INFINITY : fmaf(ml.x == -INFINITY ? 0.f : ml.x, scale, logf(ml.y));
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
   float* const join = reinterpret_cast<float*>(&sh + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const KvCache& c = p.a.c;
-  ptx::grid_launch_dependents();
+  if (!p.cluster) ptx::grid_launch_dependents();  // (the second kernel, which waits)
   const int64_t most = int64_t(c.max_pages) << c.page_shift;
   const int runs = c.hkv * p.row_tiles, cta = blockIdx.x, rank = p.cluster ? cta % p.cluster : 0;
   const bool few = c.num_seqs <= kFewSeqs;  // the producer adds their lengths up by itself
@@ -286,8 +286,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
     int ks = 0, kphase = 0, vs = 0, vphase = 0, keys_sent = 0, tiles_sent = 0, runs_sent = 0;
     int4 cut = make_int4(0, 0, 0, 0);
     bool ok = true;
-    // this CTA's units u0 .. u1 - 1; the first is unit `off` of sequence b.  (A cluster's CTA: one
-    // unit, its part of run `off` of sequence b.)
+    // this CTA's units u0 .. u1 - 1; the first is unit `off` of sequence b.  (A cluster's CTA: one unit, its part of run
+    // `off` of sequence b.)
     int b = 0, off = 0, u0 = 0, u1 = 1;
     Share share(0, 0);
     if (p.cluster) {
