@@ -136,6 +136,9 @@ template <typename E, Piece P>
 __device__ __forceinline__ void stream_heads(const E* in, int64_t in_stride, E* out, int64_t out_stride, int half,
                                              const float2* cs, int heads) {
   int h = 0;
+  if constexpr (P != kHalves)  // (one load a head)
+    for (; h + 8 <= heads; h += 8, in += 8 * in_stride, out += 8 * out_stride)
+      stream_some<E, P, 8>(in, in_stride, out, out_stride, half, cs);
   for (; h + 4 <= heads; h += 4, in += 4 * in_stride, out += 4 * out_stride)
     stream_some<E, P, 4>(in, in_stride, out, out_stride, half, cs);
   for (; h < heads; ++h, in += in_stride, out += out_stride)
@@ -269,6 +272,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_append_kernel(const K
     to[t] = dst, row[t] = r, slot_of[t] = int32_t(slot);
   }
   __syncthreads();
+  const int hkv = a.c.hkv;
+  auto each = [&](const Split& s, auto f) {
+    share(s, n, [&](int p, int t, int g) {
+      const int h0 = hkv * g / s.groups, h1 = hkv * (g + 1) / s.groups;
+      if (to[t] >= 0 && h0 < h1) f(p, t, h0, h1 - h0);
+    });
+  };
+  // values first: nothing of theirs waits for the angles (a 64K prompt: 89 us; behind the keys 92 us)
+  each(sv, [&](int p, int t, int h0, int heads) {
+    const int ch = p * Vec<E>::N;
+    stream_heads<E, kCopy>(static_cast<const E*>(a.v) + (int64_t(row[t]) * hkv + h0) * a.d_v + ch, a.d_v,
+                           static_cast<E*>(a.c.v) + (to[t] + (int64_t(h0) << a.c.page_shift)) * a.d_v + ch,
+                           int64_t(a.d_v) << a.c.page_shift, 0, nullptr, heads);
+  });
   for (int i = threadIdx.x; i < n * a.r.pairs; i += kThreads) {
     const int t = i / a.r.pairs, pr = i - t * a.r.pairs;
     if (to[t] < 0) continue;
@@ -277,13 +294,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_append_kernel(const K
     cs[i] = turn_of(__ldg(a.r.turns + pr), pos, a.r.factor);
   }
   __syncthreads();
-  const int hkv = a.c.hkv;
-  auto each = [&](const Split& s, auto f) {
-    share(s, n, [&](int p, int t, int g) {
-      const int h0 = hkv * g / s.groups, h1 = hkv * (g + 1) / s.groups;
-      if (to[t] >= 0 && h0 < h1) f(p, t, h0, h1 - h0);
-    });
-  };
   each(sp, [&](int p, int t, int h0, int heads) {
     const E* in = static_cast<const E*>(a.k) + (int64_t(row[t]) * hkv + h0) * a.d_qk;
     E* out = static_cast<E*>(a.c.k) + (to[t] + (int64_t(h0) << a.c.page_shift)) * a.d_qk;
@@ -292,12 +302,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_append_kernel(const K
       token_scalar<E>(a.r, p, in, a.d_qk, out, stride, heads, cs + t * a.r.pairs, false);
     else
       token_piece<E, F == kFormAdjacent>(a.r, p, sp.turned, in, a.d_qk, out, stride, heads, cs + t * a.r.pairs, false);
-  });
-  each(sv, [&](int p, int t, int h0, int heads) {
-    const int ch = p * Vec<E>::N;
-    stream_heads<E, kCopy>(static_cast<const E*>(a.v) + (int64_t(row[t]) * hkv + h0) * a.d_v + ch, a.d_v,
-                           static_cast<E*>(a.c.v) + (to[t] + (int64_t(h0) << a.c.page_shift)) * a.d_v + ch,
-                           int64_t(a.d_v) << a.c.page_shift, 0, nullptr, heads);
   });
 }
 
