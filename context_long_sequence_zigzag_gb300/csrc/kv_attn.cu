@@ -972,13 +972,17 @@ cudaError_t launch(const KvAttnArgs& a, const Layout& x, cudaStream_t st) {
   const int rows = std::min(x.rows, x.rows_a_run);
   const int rows_a_cta = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
   cfg.gridDim = dim3(unsigned(p.by_run ? runs : ctas), unsigned((rows + rows_a_cta - 1) / rows_a_cta));
-  // 32 warps for few rows where a run's parts are many: one run of 64 rows over 32K tokens, in 304 parts, 75 us with eight
-  // warps for eight rows, 35 us with 32
-  if (runs * 8 <= ctas) {
-    const int few = (rows_a_cta + 3) / 4;
-    cfg.gridDim.y = unsigned((rows + few - 1) / few);
-    cfg.blockDim = dim3(32 * 32);
-    return cudaLaunchKernelEx(&cfg, kv_join_kernel<C, 32>, p, few);
+  // 32 warps for few rows where a run's parts are many, as long as all of them are there at once: one run of 64 rows over
+  // 32K tokens, in 304 parts, 75 us with eight warps for eight rows, 35 us with 32 for eight, 20 us with 32 for two; but 32
+  // runs of 32 rows 35 us with eight for four, 53 us with 32 for one
+  if (runs * 12 <= ctas) {
+    int few = (rows_a_cta + 3) / 4;
+    while (runs * ((rows + few - 1) / few) > ctas) few *= 2;
+    if (few <= rows_a_cta) {
+      cfg.gridDim.y = unsigned((rows + few - 1) / few);
+      cfg.blockDim = dim3(32 * 32);
+      return cudaLaunchKernelEx(&cfg, kv_join_kernel<C, 32>, p, few);
+    }
   }
   cfg.blockDim = dim3(32 * 8);
   return cudaLaunchKernelEx(&cfg, kv_join_kernel<C, 8>, p, rows_a_cta);
