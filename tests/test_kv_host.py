@@ -122,7 +122,7 @@ def _cache(**kw):
 @pytest.mark.parametrize("change,status", [
     ({}, OK), ({"hq": 6, "hkv": 4}, BAD), ({"hkv": 0}, BAD), ({"num_seqs": -1}, BAD), ({"d_qk": 96}, UNS),
     ({"d_v": 192}, UNS), ({"d_v": 0}, BAD), ({"gqa": 2}, BAD), ({"dtype": 7}, BAD), ({"scale": math.nan}, BAD),
-    ({"scale": 0.0}, BAD), ({"k_pages": None}, BAD), ({"v_pages": None}, BAD), ({"k_pages": 4104}, BAD),
+    ({"scale": 0.0}, BAD), ({"scale": 2e38}, UNS), ({"k_pages": None}, BAD), ({"v_pages": None}, BAD), ({"k_pages": 4104}, BAD),
     ({"page_table": 66}, BAD), ({"num_pages": -1}, BAD), ({"max_pages": -1}, BAD), ({"page_size": 0}, BAD),
     ({"page_size": 8}, UNS), ({"page_size": 48}, UNS), ({"page_size": 256}, UNS), ({"page_size": 16}, OK),
     ({"max_pages": 1 << 25}, UNS), ({"num_pages": 1 << 25}, UNS), ({"num_seqs": 4097}, UNS), ({"hq": 2048}, UNS),
