@@ -980,10 +980,12 @@ def cp_kv_attn(cache: KvCache, q, lengths, part: bool = False, o=None, lse=None,
     if ws is None:
         size = cache._ws_bytes.get(n_q)
         if size is None:
-            size = cache._ws_bytes[n_q] = max(cp_kv_workspace_size(cache, n_q), 1)
-        ws = torch.empty(size, dtype=torch.uint8, device=dev)
-        temps.append(ws)
-        pw = ws.data_ptr()
+            size = cache._ws_bytes[n_q] = cp_kv_workspace_size(cache, n_q)
+        pw = None
+        if size:
+            ws = torch.empty(size, dtype=torch.uint8, device=dev)
+            temps.append(ws)
+            pw = ws.data_ptr()
     else:
         pw, size = _need_workspace(ws, dev), ws.numel() * ws.element_size()
     _launch(dev, stream, temps, "cp_kv_attn", cache.ptr, n_q, pq, _need(lengths, "lengths", torch.int32, (B,), dev), po,

@@ -895,7 +895,7 @@ struct Layout {
 };
 // Rows of a run: 16, 32 or 64 (fp32: 32, their queries take twice the room); more take several passes over the cache.
 // 8 x 8K, 32/8 heads: 64 rows in one pass 66 us, two of 32 93 us, four of 16 167 us; 20 rows in one of 32 53 us, two of 16 87.
-// Few runs of few tiles: a cluster a run, joined in shared memory, one launch and no parts in the workspace.
+// Few runs of few tiles: a cluster a run, joined in shared memory, one launch and no workspace.
 Layout layout_of(int num_seqs, int hq, int hkv, int dv, int dtype, int n_q, int64_t most) {
   Layout x;
   x.rows = hq / hkv * n_q;
@@ -907,7 +907,7 @@ Layout layout_of(int num_seqs, int hq, int hkv, int dv, int dtype, int n_q, int6
   if (most <= kClusterTokens)
     for (int n = 8; n >= 4 && x.cluster == 0; n /= 2)
       if (runs * n <= x.ctas) x.cluster = n;
-  x.parts = x.total = 256;
+  x.parts = x.total = 0;
   if (x.cluster) return x;
   x.parts = (size_t(x.ctas) * sizeof(int4) + 255) / 256 * 256;
   x.total = (x.parts + size_t(x.ctas) * 2 * x.rows_a_run * (dv + 4) * 4 + 255) / 256 * 256;
@@ -925,8 +925,8 @@ cudaError_t launch(const KvAttnArgs& a, const Layout& x, cudaStream_t st) {
   p.meta = reinterpret_cast<int4*>(a.ws);
   p.parts = reinterpret_cast<float*>(a.ws + x.parts);
   const int64_t pool_rows = (int64_t(a.c.num_pages) * a.c.hkv) << a.c.page_shift;
-  // (a pool without pages is not read: any rows will do for its map)
-  const void* any = a.ws;
+  // (a pool without pages is not read: any aligned address will do for its map)
+  const void* any = a.q;
   const bool none = pool_rows == 0;
   if (!make_map(&p.tk, none ? any : a.c.k, C::F32, none ? 1 : pool_rows, C::DQK, 1 << p.box_shift) ||
       !make_map(&p.tv, none ? any : a.c.v, C::F32, none ? 1 : pool_rows, C::DV, 1 << p.box_shift))

@@ -257,7 +257,8 @@ cp_status_t cp_kv_attn(const cp_kv_t* c, int32_t n_q, const void* q, const int32
   if (o_f32 != 0 && o_f32 != 1) return CP_ERR_INVALID_ARG;
   if (c->num_seqs == 0) return CP_OK;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(lengths, 4)) return CP_ERR_INVALID_ARG;
-  if (!aligned(ws, 256) || ws_bytes < kv_attn_workspace(c, n_q)) return CP_ERR_WORKSPACE;
+  const size_t need = kv_attn_workspace(c, n_q);
+  if (need > 0 && (!aligned(ws, 256) || ws_bytes < need)) return CP_ERR_WORKSPACE;
   KvAttnArgs a{};
   a.c = device_cache(c);
   a.n_q = n_q;

@@ -564,7 +564,8 @@ typedef struct {
 /* Check a cache descriptor on the host (no GPU work). */
 cp_status_t cp_kv_validate(const cp_kv_t* cache);
 
-/* Workspace bytes of cp_kv_attn with n_q queries a sequence.  Host only.  The
+/* Workspace bytes of cp_kv_attn with n_q queries a sequence (0: it may be
+ * NULL).  Grows with num_seqs, max_pages and n_q at the most.  Host only.  The
  * rules of cp_workspace_size apply. */
 cp_status_t cp_kv_workspace_size(const cp_kv_t* cache, int32_t n_q, size_t* bytes);
 

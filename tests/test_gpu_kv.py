@@ -777,7 +777,7 @@ def test_on_another_stream_and_in_a_graph():
 
 
 def test_two_graphs_over_one_workspace_in_turn():
-    a, b = Held([900, 3], 4, 2, 64, 64, BF, 64, seed=16), Held([17, 2100], 4, 2, 64, 64, BF, 64, seed=17)
+    a, b = (Held(n, 4, 2, 64, 64, BF, 64, seed=s, columns=WIDE // 64 + 1) for n, s in (([900, 3], 16), ([17, 2100], 17)))
     ws = torch.empty(max(cpa.cp_kv_workspace_size(x.cache) for x in (a, b)), dtype=torch.uint8, device="cuda")
     lengths = [ints(x.lengths) for x in (a, b)]
     want = [x.run() for x in (a, b)]
@@ -795,7 +795,7 @@ def test_two_graphs_over_one_workspace_in_turn():
 
 
 def test_refusals():
-    h = Held([40], 4, 2, 64, 64, BF, 16)
+    h = Held([40], 4, 2, 64, 64, BF, 16, columns=WIDE // 16 + 1)
     n = ints(h.lengths)
     rope = cpa.Rope([1.0, 0.5], axis=[0, 1])
     for call in (

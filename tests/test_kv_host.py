@@ -152,7 +152,12 @@ def test_cache_calls_refuse_before_gpu_work():
 
     assert attn(n_q=0) == attn(q=None) == attn(o=None) == attn(lse=None) == attn(lens=None) == attn(f=2) == BAD
     assert attn(n_q=17) == UNS and attn(c=_cache(d_qk=80)) == UNS
-    assert attn(ws=None) == attn(ws=128) == attn(b=0) == WSP
+    wide = _cache(max_pages=100)
+    assert attn(wide, ws=None) == attn(wide, ws=128) == attn(wide, b=0) == WSP
+    assert lib.cp_kv_workspace_size(ctypes.byref(wide), 1, ctypes.byref(n)) == OK and n.value > 0
+    small = n.value
+    for more in (_cache(max_pages=1000), _cache(max_pages=100, num_seqs=4000), _cache(max_pages=100, hq=256)):
+        assert lib.cp_kv_workspace_size(ctypes.byref(more), 16, ctypes.byref(n)) == OK and n.value >= small
     assert attn(_cache(num_seqs=0), q=None) == OK
 
 
