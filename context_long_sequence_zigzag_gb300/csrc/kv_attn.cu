@@ -82,7 +82,7 @@ struct RunDesc {
 
 struct alignas(16) Tail {  // shared memory behind the stages and queries; the buffer that O is joined in follows
   float m[kWarps][16], l[kWarps][16];
-  float2 row[64];  // maximum and sum of a row
+  float2 row[16];  // maximum and sum of a row (one row tile)
   alignas(16) RunDesc run[2];
   int32_t absent[kMostStages];  // pages of a K slot that are outside the pool, a bit each
   int32_t warp_units[2 * kWarps];
@@ -177,17 +177,25 @@ __device__ __forceinline__ float lse_of(float2 ml, float scale) {
   return ml.y == 0.f ? -INFINITY : fmaf(ml.x == -INFINITY ? 0.f : ml.x, scale, logf(ml.y));
 }
 
-// A row of a kv head (of `head` heads' group) to where its query's results go.
+// Where the results of row r of a kv head go: row of o, entry of lse.
+struct RowOf {
+  int64_t o, lse;
+  __device__ RowOf(const KvAttnArgs& a, int group, int b, int head, int r) {
+    const int t = r / group, g = r - t * group, h = a.c.inter ? head + g * a.c.hkv : head * group + g;
+    o = (int64_t(b) * a.n_q + t) * a.c.hq + h;
+    lse = int64_t(h) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t;
+  }
+};
 template <int DV>
 __device__ __forceinline__ void store_row(const KvAttnArgs& a, int group, int b, int head, int r, int col, float4 v, float2 ml) {
-  const int t = r / group, g = r - t * group, h = a.c.inter ? head + g * a.c.hkv : head * group + g;
+  const RowOf to(a, group, b, head, r);
   const float inv = inverse_of(ml);
-  const int64_t at = ((int64_t(b) * a.n_q + t) * a.c.hq + h) * DV + col;
+  const int64_t at = to.o * DV + col;
   v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
   if (a.o_f32) *reinterpret_cast<float4*>(static_cast<float*>(a.o) + at) = v;
   else
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + at) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-  if (col == 0) a.lse[int64_t(h) * a.c.num_seqs * a.n_q + int64_t(b) * a.n_q + t] = lse_of(ml, a.c.scale);
+  if (col == 0) a.lse[to.lse] = lse_of(ml, a.c.scale);
 }
 
 // Every thread of a cluster; what was written before is visible behind it.
@@ -697,74 +705,133 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
     }
 
     // ---- the warps along the slots meet
+    const int rows = min(C::ROWS, p.rows - d.row0);
+    // where the parts of a run that is not whole go (a cluster's: where its tiles were)
+    float* const parts = p.cluster ? reinterpret_cast<float*>(raw + (base - ptx::smem_u32(raw)))
+                                   : p.parts + int64_t(d.slot) * C::ROWS * (DV + 4);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       l[x] += __shfl_xor_sync(~0u, l[x], 1);
       l[x] += __shfl_xor_sync(~0u, l[x], 2);
-      if (quad == 0) sh.m[warp][r0 + 8 * x] = m[x], sh.l[warp][r0 + 8 * x] = l[x];
     }
-    meet();
-    if (!ok) break;
-    const int rows = min(C::ROWS, p.rows - d.row0);
-    {
+    if (NS > 1 || p.cluster) {  // (and nobody reads tiles any more)
+      if (quad == 0) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) sh.m[warp][r0 + 8 * x] = m[x], sh.l[warp][r0 + 8 * x] = l[x];
+      }
+      meet();
+      if (!ok) break;
+    }
+    if constexpr (NS > 1) {
       float f[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        float all = m[x];
+        float all = m[x], sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NS; ++i) all = fmaxf(all, sh.m[i * MT + mt][r0 + 8 * x]);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          const float y = sh.l[i * MT + mt][r0 + 8 * x];
+          sum += all == -INFINITY ? y : y * ptx::ex2((sh.m[i * MT + mt][r0 + 8 * x] - all) * cs);
+        }
         f[x] = all == -INFINITY ? 1.f : ptx::ex2((m[x] - all) * cs);
+        m[x] = all, l[x] = sum;
+        if (MT == 1 && warp == 0 && quad == 0) sh.row[r0 + 8 * x] = make_float2(all, sum);
       }
 #pragma unroll
       for (int i = 0; i < DV / 8; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][j] *= f[j >> 1];
     }
-    if (tid < rows) {
-      const int x = tid / 16, r = tid % 16;
-      float all = -INFINITY, sum = 0.f;
+    if constexpr (MT == 1) {
+      // O by columns, as many at a time as there is room for; all threads add
+      const int held = rows <= 4 ? 4 : rows <= 8 ? 8 : 16, cols = min(DV, kJoinFloats / kWarps / held);
+      for (int c0 = 0; c0 < DV; c0 += cols) {
 #pragma unroll
-      for (int i = 0; i < NS; ++i) all = fmaxf(all, sh.m[i * MT + x][r]);
+        for (int i = 0; i < DV / 8; ++i)
+          if (8 * i >= c0 && 8 * i < c0 + cols) {
 #pragma unroll
-      for (int i = 0; i < NS; ++i)
-        sum += all == -INFINITY ? sh.l[i * MT + x][r] : sh.l[i * MT + x][r] * ptx::ex2((sh.m[i * MT + x][r] - all) * cs);
-      sh.row[tid] = make_float2(all, sum);
-    }
-    // O by columns, as many at a time as there is room for
-    const int held = rows <= 4 ? 4 : rows <= 8 ? 8 : 16, cols = min(DV, kJoinFloats / kWarps / held);
-    for (int c0 = 0; c0 < DV; c0 += cols) {
+            for (int x = 0; x < 2; ++x)
+              if (r0 + 8 * x < held)
+                *reinterpret_cast<float2*>(&join[(warp * held + r0 + 8 * x) * cols + 8 * i - c0 + 2 * quad]) =
+                    make_float2(o[i][2 * x], o[i][2 * x + 1]);
+          }
+        meet();
+        if (!ok) break;
+        for (int i = tid; i < rows * cols / 4; i += 32 * kWarps) {
+          const int row = i / (cols / 4), col = (i - row * (cols / 4)) * 4;
+          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < DV / 8; ++i)
-        if (8 * i >= c0 && 8 * i < c0 + cols) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            if (r0 + 8 * x < held)
-              *reinterpret_cast<float2*>(&join[(warp * held + r0 + 8 * x) * cols + 8 * i - c0 + 2 * quad]) =
-                  make_float2(o[i][2 * x], o[i][2 * x + 1]);
+          for (int k = 0; k < NS; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(&join[(k * held + row) * cols + col]);
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+          }
+          const float2 ml = sh.row[row];
+          if (d.whole) {
+            store_row<DV>(p.a, p.group, d.b, d.head, d.row0 + row, c0 + col, sum, ml);
+          } else {
+            float* to = parts + row * (DV + 4);
+            *reinterpret_cast<float4*>(to + c0 + col) = sum;
+            if (c0 + col == 0) *reinterpret_cast<float2*>(to + DV) = ml;
+          }
         }
-      meet();
-      if (!ok) break;
-      for (int i = tid; i < rows * cols / 4; i += 32 * kWarps) {
-        const int row = i / (cols / 4), col = (i - row * (cols / 4)) * 4;
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        meet();
+        if (!ok) break;
+      }
+    } else {
+      // many rows: a row's first warp adds what the other one (if there is one) leaves in shared memory, and stores (all
+      // threads adding, as above: 64 rows of 8 x 8K 66 us instead of 63, of 4 x 8K and d 192 40 us instead of 34)
+      if constexpr (NS == 2) {
+        constexpr int cols = kJoinFloats / (MT * 16) < DV ? kJoinFloats / (MT * 16) : DV;
 #pragma unroll
-        for (int k = 0; k < NS; ++k) {
-          const float4 v = *reinterpret_cast<const float4*>(&join[((k * MT + row / 16) * held + row % 16) * cols + col]);
-          sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        for (int c0 = 0; c0 < DV; c0 += cols) {
+#pragma unroll
+          for (int i = c0 / 8; i < (c0 + cols) / 8; ++i)
+            if (slice == 1) {
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+                *reinterpret_cast<float2*>(&join[(mt * 16 + r0 + 8 * x) * cols + 8 * i - c0 + 2 * quad]) =
+                    make_float2(o[i][2 * x], o[i][2 * x + 1]);
+            }
+          meet();
+          if (slice == 0) {
+#pragma unroll
+            for (int i = c0 / 8; i < (c0 + cols) / 8; ++i)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const float2 v = *reinterpret_cast<const float2*>(&join[(mt * 16 + r0 + 8 * x) * cols + 8 * i - c0 + 2 * quad]);
+                o[i][2 * x] += v.x, o[i][2 * x + 1] += v.y;
+              }
+          }
+          meet();
         }
-        const float2 ml = sh.row[row];
-        if (d.whole) {
-          store_row<DV>(p.a, p.group, d.b, d.head, d.row0 + row, c0 + col, sum, ml);
-        } else {
-          // (a cluster's parts lie where its tiles were)
-          float* to = p.cluster ? reinterpret_cast<float*>(raw + (base - ptx::smem_u32(raw))) + row * (DV + 4)
-                                : p.parts + (int64_t(d.slot) * C::ROWS + row) * (DV + 4);
-          *reinterpret_cast<float4*>(to + c0 + col) = sum;
-          if (c0 + col == 0) *reinterpret_cast<float2*>(to + DV) = ml;
+        if (!ok) break;
+      }
+      if (slice == 0) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int row = mt * 16 + r0 + 8 * x;
+          if (row >= rows) continue;
+          const float2 ml = make_float2(m[x], l[x]);
+          const RowOf at(p.a, p.group, d.b, d.head, d.row0 + row);
+          const float inv = inverse_of(ml);
+          float* const part = parts + row * (DV + 4);
+#pragma unroll
+          for (int i = 0; i < DV / 8; ++i) {
+            const int col = 8 * i + 2 * quad;
+            const float2 v = make_float2(o[i][2 * x], o[i][2 * x + 1]);
+            if (!d.whole) *reinterpret_cast<float2*>(part + col) = v;
+            else if (p.a.o_f32)
+              *reinterpret_cast<float2*>(static_cast<float*>(p.a.o) + at.o * DV + col) = make_float2(v.x * inv, v.y * inv);
+            else
+              *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.a.o) + at.o * DV + col) = pack_bf16(v.x * inv, v.y * inv);
+          }
+          if (quad == 0) {
+            if (d.whole) p.a.lse[at.lse] = lse_of(ml, c.scale);
+            else *reinterpret_cast<float2*>(part + DV) = ml;
+          }
         }
       }
-      meet();
-      if (!ok) break;
     }
   }
   if (!p.cluster) return;
@@ -861,17 +928,16 @@ __global__ void __launch_bounds__(32 * W) kv_join_kernel(const __grid_constant__
     add(ml_of[warp + w], x);
   }
   const KvCache& c = p.a.c;
-  const int t = r / p.group, g = r - t * p.group, h = c.inter ? head + g * c.hkv : head * p.group + g;
+  const RowOf to(p.a, p.group, cut.x, head, r);
   const float inv = inverse_of(make_float2(top, sum));
-  const int64_t at = ((int64_t(cut.x) * p.a.n_q + t) * c.hq + h) * DV + lane * V;
+  const int64_t at = to.o * DV + lane * V;
 #pragma unroll
   for (int j = 0; j < V; j += 2) {
     if (p.a.o_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.a.o) + at + j) = make_float2(acc[j] * inv, acc[j + 1] * inv);
     else
       *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.a.o) + at + j) = pack_bf16(acc[j] * inv, acc[j + 1] * inv);
   }
-  if (lane == 0)
-    p.a.lse[int64_t(h) * c.num_seqs * p.a.n_q + int64_t(cut.x) * p.a.n_q + t] = lse_of(make_float2(top, sum), c.scale);
+  if (lane == 0) p.a.lse[to.lse] = lse_of(make_float2(top, sum), c.scale);
 }
 
 // Panels of 128 bytes of the rows of a pool.
@@ -894,7 +960,7 @@ struct Layout {
   size_t parts, total;
 };
 // Rows of a run: 16, 32 or 64 (fp32: 32, their queries take twice the room); more take several passes over the cache.
-// 8 x 8K, 32/8 heads: 64 rows in one pass 66 us, two of 32 93 us, four of 16 167 us; 20 rows in one of 32 53 us, two of 16 87.
+// 8 x 8K, 32/8 heads: 64 rows in one pass 63 us, two of 32 91 us, four of 16 167 us; 20 rows in one of 32 52 us, two of 16 87.
 // Few runs of few tiles: a cluster a run, joined in shared memory, one launch and no workspace.
 Layout layout_of(int num_seqs, int hq, int hkv, int dv, int dtype, int n_q, int64_t most) {
   Layout x;
