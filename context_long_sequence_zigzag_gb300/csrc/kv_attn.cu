@@ -48,9 +48,9 @@ constexpr int kMostStages = 6;
 // leaves 0.6 us earlier (1 x 16K 18.8 us, by all warps 19.4).
 constexpr int kFewSeqs = 32;
 // A cluster of up to eight CTAs a run, in the place of even shares and a second kernel, where the table holds no more
-// tokens than this and the clusters fit the GPU at once.  One sequence of 4K: 12.5 us on the device (even shares: 12.1),
-// 15 us of a host that calls again and again (20); 8 of 4K: 26.9 us (29.7); but one of 8K: 17.0 (13.2), and 8 ragged ones
-// up to 4K: 16.8 (13.5).  Clusters of sixteen start later: one of 4K 13.1 us.
+// tokens than this and the clusters fit the GPU at once.  32/8 heads, one sequence of 512 tokens: 7.9 us on the device
+// (even shares: 9.1), of 4K: 11.8 us (10.3), but 15 us of a host that calls again and again (20); 8 of 4K: 26.1 us (28.5);
+// one of 8K: 16.4 us (11.8), 8 ragged ones up to 4K: 16.0 us (12.7).  Clusters of sixteen start 1 us later.
 constexpr int64_t kClusterTokens = 4096;
 constexpr float kLog2e = 1.4426950408889634f;
 // log2 units: a row's reference maximum follows a new one past this (p stays below 2^8 relative to it, so that most

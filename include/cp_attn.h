@@ -597,7 +597,8 @@ cp_status_t cp_kv_append(const cp_kv_t* cache, const void* k, const void* v, int
  * Products with FP32 accumulation, the softmax in FP32.  BF16 caches: the
  * probabilities rounded to BF16 for their product with V.  FP32 caches: every
  * operand as two TF32 terms (the product of both lower ones, 2^-22, left out;
- * an infinity that a query sees may give NaN in an infinity's place). */
+ * an infinity that a query sees, or a number within 2^-12 of the largest, may
+ * give NaN in an infinity's place). */
 cp_status_t cp_kv_attn(const cp_kv_t* cache, int32_t n_q, const void* q, const int32_t* lengths, void* o,
                        int32_t o_f32, float* lse, void* workspace, size_t workspace_bytes, cp_stream_t stream);
 
