@@ -150,6 +150,31 @@ def test_rope_positions_follow_the_shard_map():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_rope_in_training():
+    """Forward and backward of a packed prompt in zigzag shards with turned queries and keys: the gradients of the
+    unturned ones.  The attention's gradients are within 2e-2 of their norm (its own tolerance for bf16) of the 64-bit
+    ones for the queries and keys that it got; turning back keeps norms, and rounds (2^-8)."""
+    rng = np.random.RandomState(21)
+    cu, T, hq, hkv, d = [0, 200, 330], 330, 4, 2, 128
+    prob = cpa.Problem(T, hq, hkv, d, d, 2, "zigzag", cu)
+    x = {n: randn(rng, (T, h, d), BF) for n, h in (("q", hq), ("k", hkv), ("v", hkv), ("dout", hq))}
+    f = 10000.0 ** (-np.arange(d // 2) / (d // 2))
+    pos = np.zeros((T, 4), np.int64)
+    pos[:, 0] = np.concatenate([np.arange(200), np.arange(130)])
+    rope = cpa.Rope(f)
+    s = {n: cpa.cp_shard_permute(prob, t) for n, t in x.items()}
+    at = cpa.cp_shard_permute(prob, ints(pos.tolist()))
+    q, k = cpa.cp_rope(rope, at, s["q"], s["k"])
+    o, lse = cpa.cp_attn_fwd(prob, q, k, s["v"])
+    dq, dk, dv = cpa.cp_attn_bwd(prob, q, k, s["v"], o, lse, s["dout"])
+    dq, dk = cpa.cp_rope(rope, at, dq, dk, inverse=True, q_out=dq, k_out=dk)
+    whole = lambda t: f64(cpa.cp_shard_permute(prob, t, inverse=True))  # noqa: E731
+    ref = oracle.attn_backward(whole(q), whole(k), f64(x["v"]), f64(x["dout"]), cu, d ** -0.5)
+    angle = pos[:, :1] * f[None]
+    for got, want in ((dq, oracle.rope(ref["dq"], angle, inverse=True)), (dk, oracle.rope(ref["dk"], angle, inverse=True))):
+        assert np.linalg.norm(whole(got) - want) <= (2e-2 + 2.0 ** -8 + 2.0 ** -20) * np.linalg.norm(want)
+
+
 def test_rope_records_an_axis_that_positions_lack():
     rope = cpa.Rope([1.0, 0.5], axis=[0, 1])
     rope.axis.copy_(ints([0, 3]))
