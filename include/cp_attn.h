@@ -565,8 +565,8 @@ typedef struct {
 cp_status_t cp_kv_validate(const cp_kv_t* cache);
 
 /* Workspace bytes of cp_kv_attn with n_q queries a sequence (0: it may be
- * NULL).  Grows with num_seqs, max_pages and n_q at the most.  Host only.  The
- * rules of cp_workspace_size apply. */
+ * NULL).  Never less for more sequences, longer tables or more queries.  Host
+ * only.  The rules of cp_workspace_size apply. */
 cp_status_t cp_kv_workspace_size(const cp_kv_t* cache, int32_t n_q, size_t* bytes);
 
 /* Writes tokens into the cache, their keys turned on the way: token t, cu[b] <=
