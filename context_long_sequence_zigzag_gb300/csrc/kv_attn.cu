@@ -68,6 +68,11 @@ struct Cfg {
   static constexpr int TT_SHIFT = F32 ? 5 : 6, TT = 1 << TT_SHIFT;  // slots of a tile
   static constexpr int TS = TT / NS;           // of a warp
   static constexpr int ROWS = 16 * MT;
+  // BF16: the product with V takes the probabilities as two terms of BF16, off by 2^-15 of them instead of 2^-8 (8 x 8K,
+  // O in fp32 off by 4.6e-6 of its norm instead of 1.4e-3).  With up to 32 rows the MMAs that this adds lie behind the
+  // copies (46.8 -> 47.1 us, 32 rows 52.8 -> 53.7; 1 x 4K 11.7 -> 12.4, 1000 x 100 57 -> 60); 64 rows are bound by MMAs and
+  // take one term (63.5 us, with two 85.7).
+  static constexpr bool REST = !F32 && MT <= 2;
   static constexpr int KP = DQK * sizeof(E) / 128, VP = DV * sizeof(E) / 128;  // panels of 128 bytes
   static constexpr uint32_t KBYTES = KP * TT * 128, VBYTES = VP * TT * 128;
   static constexpr uint32_t QPITCH = DQK * sizeof(E) + 16;  // (rows of a fragment in different banks)
@@ -160,6 +165,14 @@ __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
   return reinterpret_cast<const uint32_t&>(p);
+}
+
+// Two numbers >= 0 as two terms of BF16 each: cut off, and the rest with 2^-20 of the number, so that neither term of a
+// number above 0 is 0 (whose product with an infinity would be NaN).
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t& high, uint32_t& rest) {
+  high = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  rest = pack_bf16(fmaf(a, 1.f + 0x1p-20f, -__uint_as_float(high << 16)),
+                   fmaf(b, 1.f + 0x1p-20f, -__uint_as_float(high & 0xffff0000u)));
 }
 
 // Tiles lie in panels of 128 bytes a slot, 16-byte pieces swizzled: piece c of slot x is piece (c ^ x) % 8 of its row in
@@ -645,9 +658,14 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
         } else {
 #pragma unroll
           for (int i = 0; i < NB; i += 2) {
-            const uint32_t a[4] = {pack_bf16(prob(s[i][0], 0), prob(s[i][1], 1)), pack_bf16(prob(s[i][2], 2), prob(s[i][3], 3)),
-                                   pack_bf16(prob(s[i + 1][0], 0), prob(s[i + 1][1], 1)),
-                                   pack_bf16(prob(s[i + 1][2], 2), prob(s[i + 1][3], 3))};
+            uint32_t a[4], rest[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int j = 2 * (y & 1);
+              const float x0 = prob(s[i + y / 2][j], j), x1 = prob(s[i + y / 2][j + 1], j + 1);
+              if constexpr (C::REST) split_bf16(x0, x1, a[y], rest[y]);
+              else a[y] = pack_bf16(x0, x1);
+            }
             uint32_t mask[2] = {~0u, ~0u};
             if constexpr (GUARD) {
 #pragma unroll
@@ -662,8 +680,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
               uint32_t vf[4];
               ptx::ldmatrix_x4_trans(vf, piece_of<TT>(vals, nb));
               if constexpr (GUARD) vf[0] &= mask[0], vf[1] &= mask[1], vf[2] &= mask[0], vf[3] &= mask[1];
-              add(o[nb], [&](float (&acc)[4]) { ptx::mma_16816(acc, a, vf[0], vf[1]); });
-              add(o[nb + 1], [&](float (&acc)[4]) { ptx::mma_16816(acc, a, vf[2], vf[3]); });
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                add(o[nb + y], [&](float (&acc)[4]) {
+                  if constexpr (C::REST) ptx::mma_16816(acc, rest, vf[2 * y], vf[2 * y + 1]);
+                  ptx::mma_16816(acc, a, vf[2 * y], vf[2 * y + 1]);
+                });
             }
           }
         }

@@ -595,10 +595,11 @@ cp_status_t cp_kv_append(const cp_kv_t* cache, const void* k, const void* v, int
  *   lse       : device float32 [hq, B * n_q]
  *   workspace : cp_kv_workspace_size bytes
  * Products with FP32 accumulation, the softmax in FP32.  BF16 caches: the
- * probabilities rounded to BF16 for their product with V.  FP32 caches: every
- * operand as two TF32 terms (the product of both lower ones, 2^-22, left out;
- * an infinity that a query sees, or a number within 2^-12 of the largest, may
- * give NaN in an infinity's place). */
+ * probabilities as two BF16 terms (off by 2^-15) for their product with V where
+ * up to 32 rows (hq / hkv * n_q) share a kv head, rounded to BF16 (2^-8) where
+ * more do.  FP32 caches: every operand as two TF32 terms (the product of both
+ * lower ones, 2^-22, left out; an infinity that a query sees, or a number within
+ * 2^-12 of the largest, may give NaN in an infinity's place). */
 cp_status_t cp_kv_attn(const cp_kv_t* cache, int32_t n_q, const void* q, const int32_t* lengths, void* o,
                        int32_t o_f32, float* lse, void* workspace, size_t workspace_bytes, cp_stream_t stream);
 
