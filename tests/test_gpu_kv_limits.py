@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import oracle
-from test_gpu_kv import BF, WIDE, Held, f64
+from test_gpu_kv import BF, WIDE, Held, f64, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +61,65 @@ def test_an_infinite_value_stays_one(n_q):
         sees = [t for t in range(n_q) if 300 - (n_q - 1 - t) > 290]
         assert (o[0, :, :, 5] == math.inf).all() and (o[1, sees, :, 6] == -math.inf).all()
         assert o[0, ..., :5].isfinite().all() and o[1, ..., 7:].isfinite().all()
+
+
+# ---------------------------------------------------------------- pages taken back
+@pytest.mark.parametrize("B,most,shared", [(1, 40000, 0), (7, 9000, 3000), (1500, 60, 20), (4096, 9, 0)])
+def test_reserve_takes_many_pages_back(B, most, shared):
+    """Thousands of entries go at once, of one sequence or of all, some of pages that others hold; others grow."""
+    rng = np.random.RandomState(B)
+    held = rng.randint(shared, most + 1, B)
+    held[0] = most
+    rows, at = [], shared
+    for n in held:
+        rows.append(list(range(shared)) + list(range(at, at + n - shared)))
+        at += n - shared
+    pages, columns, page = at + 50, most + 2, 16
+    order = rng.permutation(pages)
+    rows = [[int(order[p]) for p in r] for r in rows]
+    refs = np.zeros(pages, int)
+    np.add.at(refs, np.concatenate([np.array(r, int) for r in rows]), 1)
+    lengths = [int(n) * page - int(rng.randint(0, page)) if n else 0 for n in held]
+    extra = [int(-rng.randint(0, 2 * n + 2)) if rng.rand() < 0.7 else int(rng.randint(0, page)) for n in lengths]
+    extra[0] = 5 - lengths[0]
+    extra = [min(x, columns * page - n) for x, n in zip(extra, lengths)]
+    table = np.full((B, columns), -7)
+    for b, r in enumerate(rows):
+        table[b, :len(r)] = r
+    pool = cpa.PagePool(ints(refs.tolist()), [], page)
+    t = ints(table.tolist())
+    counts = cpa.cp_pages_reserve(pool, t, ints(lengths), ints(extra))
+    # in arrays: sequences let go first, then the lowest free pages go to the lowest sequence
+    needs = np.array([-(-max(n + x, 0) // page) for n, x in zip(lengths, extra)])
+    for b, r in enumerate(rows):
+        np.subtract.at(refs, np.array(r[needs[b]:], int), 1)
+        table[b, needs[b]:len(r)] = -1
+    free = np.flatnonzero(refs == 0)
+    taken = 0
+    for b, r in enumerate(rows):
+        n = max(needs[b] - len(r), 0)
+        table[b, len(r):len(r) + n] = free[taken:taken + n]
+        taken += n
+    refs[free[:taken]] = 1
+    assert np.array_equal(t.cpu().numpy(), table) and np.array_equal(pool.refs.cpu().numpy(), refs)
+    assert counts.tolist() == [int((refs != 0).sum()), 0]
+
+
+def test_reserve_takes_a_long_sequence_back_in_parallel():
+    """65536 pages of one sequence: one after another in a thread they would take 5 ms; shared among the 8192 threads of
+    the call a few dozen microseconds."""
+    pages = 1 << 16
+    pool = cpa.PagePool(torch.empty(pages, dtype=torch.int32, device="cuda"), [], 16)
+    table = torch.empty(1, pages, dtype=torch.int32, device="cuda")
+    lengths, extra, best = ints([pages * 16]), ints([-pages * 16]), 1e9
+    for _ in range(4):
+        pool.refs.fill_(1)
+        torch.arange(pages, out=table[0])
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        counts = cpa.cp_pages_reserve(pool, table, lengths, extra)
+        b.record()
+        torch.cuda.synchronize()
+        assert counts.tolist() == [0, 0] and (table == -1).all() and not pool.refs.any()
+        best = min(best, a.elapsed_time(b))
+    assert best < 2.0
