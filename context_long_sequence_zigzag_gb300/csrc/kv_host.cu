@@ -287,6 +287,8 @@ cp_status_t cp_pages_reserve(const cp_pages_t* p, int32_t num_seqs, int32_t max_
   cp_status_t st = check_pool(p);
   if (st == CP_OK) st = check_table(p, num_seqs, max_pages);
   if (st != CP_OK) return st;
+  // pages that come and go are summed over the batch in 32 bits, and counted on by the cluster's threads
+  if (int64_t(num_seqs) * max_pages > 1 << 30) return CP_ERR_UNSUPPORTED;
   if (!aligned(counts, 4)) return CP_ERR_INVALID_ARG;
   if (num_seqs > 0 && (!aligned(lengths, 4) || !aligned(extra, 4))) return CP_ERR_INVALID_ARG;
   if (num_seqs > 0 && max_pages > 0 && !aligned(table, 4)) return CP_ERR_INVALID_ARG;

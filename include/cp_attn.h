@@ -641,7 +641,8 @@ cp_status_t cp_pages_workspace_size(const cp_pages_t* pool, int32_t num_seqs, si
  * that it needs no more (extra below 0: tokens taken back); the latter first.
  * It then holds what lengths[b] + extra[b] tokens need, which is the length that
  * later calls are to be given.  A sequence cut inside a page that others hold has
- * to go through cp_pages_fork before it is written again.
+ * to go through cp_pages_fork before it is written again.  num_seqs * max_pages
+ * is at most 2^30.
  *   table   : device int32 [num_seqs][max_pages], written where pages come or go
  *             (-1: gone)
  *   lengths : device int32 [num_seqs], not changed
