@@ -672,7 +672,8 @@ def cp_kv4_validate(cache: Kv4Cache) -> int:
 
 def cp_kv4_workspace_size(cache: Kv4Cache, n_q: int = 1, accumulate: bool = False) -> int:
     n = ctypes.c_size_t(0)
-    _check(_lib.cp_kv4_workspace_size(cache.ptr, n_q, int(bool(accumulate)), ctypes.byref(n)), "cp_kv4_workspace_size")
+    with torch.cuda.device(cache.device):  # (whose SMs it goes by)
+        _check(_lib.cp_kv4_workspace_size(cache.ptr, n_q, int(bool(accumulate)), ctypes.byref(n)), "cp_kv4_workspace_size")
     return int(n.value)
 
 
@@ -922,7 +923,8 @@ def cp_kv_validate(cache: KvCache) -> int:
 
 def cp_kv_workspace_size(cache: KvCache, n_q: int = 1) -> int:
     n = ctypes.c_size_t(0)
-    _check(_lib.cp_kv_workspace_size(cache.ptr, n_q, ctypes.byref(n)), "cp_kv_workspace_size")
+    with torch.cuda.device(cache.device):  # (whose SMs it goes by)
+        _check(_lib.cp_kv_workspace_size(cache.ptr, n_q, ctypes.byref(n)), "cp_kv_workspace_size")
     return int(n.value)
 
 

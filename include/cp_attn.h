@@ -426,7 +426,8 @@ cp_status_t cp_kv4_validate(const cp_kv4_t* cache);
 
 /* Workspace bytes of cp_kv4_attn with n_q queries a sequence, without or with
  * weights.  Grows with num_seqs * max_pages in the second case.  Host only.
- * The rules of cp_workspace_size apply. */
+ * The rules of cp_workspace_size apply, and it is for the current device, which
+ * has to be the cache's: it goes by the number of SMs. */
 cp_status_t cp_kv4_workspace_size(const cp_kv4_t* cache, int32_t n_q, int32_t accumulate, size_t* bytes);
 
 /* Quantise tokens into the cache: token t, cu[b] <= t < cu[b+1], becomes slot
@@ -565,8 +566,9 @@ typedef struct {
 cp_status_t cp_kv_validate(const cp_kv_t* cache);
 
 /* Workspace bytes of cp_kv_attn with n_q queries a sequence (0: it may be
- * NULL).  Never less for more sequences, longer tables or more queries.  Host
- * only.  The rules of cp_workspace_size apply. */
+ * NULL), for the current device, which has to be the cache's: it goes by the
+ * number of SMs.  Never less for more sequences, longer tables or more queries.
+ * Host only.  The rules of cp_workspace_size apply. */
 cp_status_t cp_kv_workspace_size(const cp_kv_t* cache, int32_t n_q, size_t* bytes);
 
 /* Writes tokens into the cache, their keys turned on the way: token t, cu[b] <=
