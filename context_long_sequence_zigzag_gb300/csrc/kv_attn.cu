@@ -50,7 +50,8 @@ constexpr int kFewSeqs = 32;
 // A cluster of up to eight CTAs a run, in the place of even shares and a second kernel, where the table holds no more
 // tokens than this and the clusters fit the GPU at once.  32/8 heads, one sequence of 512 tokens: 7.9 us on the device
 // (even shares: 9.1), of 4K: 11.8 us (10.3), but 15 us of a host that calls again and again (20); 8 of 4K: 26.1 us (28.5);
-// one of 8K: 16.4 us (11.8), 8 ragged ones up to 4K: 16.0 us (12.7).  Clusters of sixteen start 1 us later.
+// one of 8K: 16.4 us (11.8), 8 ragged ones up to 4K: 16.0 us (12.7).  Clusters of sixteen start 1 us later.  Where they
+// do not fit (fp32, 32 rows of 32/8 heads of 192: one CTA an SM), 5 of 512 tokens: 36.8 us (23.7), 5 of 4K: 150 us (83).
 constexpr int64_t kClusterTokens = 4096;
 constexpr float kLog2e = 1.4426950408889634f;
 // log2 units: a row's reference maximum follows a new one past this (p stays below 2^8 relative to it, so that most
@@ -976,6 +977,30 @@ bool make_map(CUtensorMap* map, const void* pages, bool f32, int64_t rows, int d
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// f(Cfg) of a call's kernel.
+template <typename E, int DQK, int DV, typename F>
+auto with_rows(int rows_a_run, F f) {
+  if (rows_a_run == 16) return f(Cfg<E, DQK, DV, 1>{});
+  if constexpr (sizeof(E) == 2)
+    if (rows_a_run == 64) return f(Cfg<E, DQK, DV, 4>{});
+  return f(Cfg<E, DQK, DV, 2>{});
+}
+template <typename E, typename F>
+auto with_dims(int dqk, int dv, int rows_a_run, F f) {
+  switch (dqk * 1000 + dv) {
+    case 64064: return with_rows<E, 64, 64>(rows_a_run, f);
+    case 64128: return with_rows<E, 64, 128>(rows_a_run, f);
+    case 128064: return with_rows<E, 128, 64>(rows_a_run, f);
+    case 192064: return with_rows<E, 192, 64>(rows_a_run, f);
+    case 192128: return with_rows<E, 192, 128>(rows_a_run, f);
+    default: return with_rows<E, 128, 128>(rows_a_run, f);
+  }
+}
+template <typename F>
+auto with_config(int dtype, int dqk, int dv, int rows_a_run, F f) {
+  return dtype == CP_DT_BF16 ? with_dims<__nv_bfloat16>(dqk, dv, rows_a_run, f) : with_dims<float>(dqk, dv, rows_a_run, f);
+}
+
 struct Layout {
   int rows, row_tiles, rows_a_run, ctas;
   int cluster;
@@ -984,7 +1009,7 @@ struct Layout {
 // Rows of a run: 16, 32 or 64 (fp32: 32, their queries take twice the room); more take several passes over the cache.
 // 8 x 8K, 32/8 heads: 64 rows in one pass 63 us, two of 32 91 us, four of 16 167 us; 20 rows in one of 32 52 us, two of 16 87.
 // Few runs of few tiles: a cluster a run, joined in shared memory, one launch and no workspace.
-Layout layout_of(int num_seqs, int hq, int hkv, int dv, int dtype, int n_q, int64_t most) {
+Layout layout_of(int num_seqs, int hq, int hkv, int dqk, int dv, int dtype, int n_q, int64_t most) {
   Layout x;
   x.rows = hq / hkv * n_q;
   x.rows_a_run = x.rows <= 16 ? 16 : x.rows <= 32 || dtype == CP_DT_F32 ? 32 : 64;
@@ -992,9 +1017,11 @@ Layout layout_of(int num_seqs, int hq, int hkv, int dv, int dtype, int n_q, int6
   x.ctas = 2 * sm_count();
   const int64_t runs = int64_t(num_seqs) * hkv * x.row_tiles;
   x.cluster = 0;
+  const bool two = with_config(dtype, dqk, dv, x.rows_a_run, [](auto c) { return Room<decltype(c)>::two; });
+  const int at_once = two ? x.ctas : x.ctas / 2;
   if (most <= kClusterTokens)
     for (int n = 8; n >= 4 && x.cluster == 0; n /= 2)
-      if (runs * n <= x.ctas) x.cluster = n;
+      if (runs * n <= at_once) x.cluster = n;
   x.parts = x.total = 0;
   if (x.cluster) return x;
   x.parts = (size_t(x.ctas) * sizeof(int4) + 255) / 256 * 256;
@@ -1080,27 +1107,8 @@ cudaError_t launch(const KvAttnArgs& a, const Layout& x, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kv_join_kernel<C, 8>, p, rows_a_cta);
 }
 
-template <typename E, int DQK, int DV>
-cudaError_t with_rows(const KvAttnArgs& a, const Layout& x, cudaStream_t st) {
-  if (x.rows_a_run == 16) return launch<Cfg<E, DQK, DV, 1>>(a, x, st);
-  if (x.rows_a_run == 32) return launch<Cfg<E, DQK, DV, 2>>(a, x, st);
-  if constexpr (sizeof(E) == 2) return launch<Cfg<E, DQK, DV, 4>>(a, x, st);
-  return cudaErrorInvalidValue;
-}
-template <typename E>
-cudaError_t with_dims(const KvAttnArgs& a, const Layout& x, int dqk, int dv, cudaStream_t st) {
-  switch (dqk * 1000 + dv) {
-    case 64064: return with_rows<E, 64, 64>(a, x, st);
-    case 64128: return with_rows<E, 64, 128>(a, x, st);
-    case 128064: return with_rows<E, 128, 64>(a, x, st);
-    case 192064: return with_rows<E, 192, 64>(a, x, st);
-    case 192128: return with_rows<E, 192, 128>(a, x, st);
-    default: return with_rows<E, 128, 128>(a, x, st);
-  }
-}
-
 Layout layout_of(const cp_kv_t* c, int32_t n_q) {
-  return layout_of(c->num_seqs, c->hq, c->hkv, c->d_v, c->dtype, n_q, int64_t(c->max_pages) * c->page_size);
+  return layout_of(c->num_seqs, c->hq, c->hkv, c->d_qk, c->d_v, c->dtype, n_q, int64_t(c->max_pages) * c->page_size);
 }
 
 }  // namespace
@@ -1113,8 +1121,8 @@ int64_t kv_attn_units(const cp_kv_t* c, int32_t n_q) {
 }
 
 cudaError_t launch_kv_attn(const KvAttnArgs& a, int dqk, int dv, int dtype, cudaStream_t st) {
-  const Layout x = layout_of(a.c.num_seqs, a.c.hq, a.c.hkv, dv, dtype, a.n_q, int64_t(a.c.max_pages) << a.c.page_shift);
-  return dtype == CP_DT_BF16 ? with_dims<__nv_bfloat16>(a, x, dqk, dv, st) : with_dims<float>(a, x, dqk, dv, st);
+  const Layout x = layout_of(a.c.num_seqs, a.c.hq, a.c.hkv, dqk, dv, dtype, a.n_q, int64_t(a.c.max_pages) << a.c.page_shift);
+  return with_config(dtype, dqk, dv, x.rows_a_run, [&](auto c) { return launch<decltype(c)>(a, x, st); });
 }
 
 }  // namespace cpattn

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import oracle
-from test_gpu_kv import BF, WIDE, Held, f64, ints
+from test_gpu_kv import BF, F32, WIDE, Held, f64, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -61,6 +61,14 @@ def test_an_infinite_value_stays_one(n_q):
         sees = [t for t in range(n_q) if 300 - (n_q - 1 - t) > 290]
         assert (o[0, :, :, 5] == math.inf).all() and (o[1, sees, :, 6] == -math.inf).all()
         assert o[0, ..., :5].isfinite().all() and o[1, ..., 7:].isfinite().all()
+
+
+# ---------------------------------------------------------------- attention: clusters or even shares
+def test_attn_where_clusters_do_not_fit():
+    """fp32 heads of 192 with 32 rows: one CTA an SM, so that 40 clusters of four do not fit and shares are even."""
+    h = Held([70, 0, 200, 31, 129], 32, 8, 192, 128, F32, 64, 8, seed=32)
+    assert cpa.cp_kv_workspace_size(h.cache, 8) > 0
+    h.check(*h.run())
 
 
 # ---------------------------------------------------------------- pages taken back

@@ -6,7 +6,7 @@ from types import SimpleNamespace
 import pytest
 import torch
 
-from test_kv_host import OK, UNS, _pool
+from test_kv_host import OK, UNS, _cache, _pool
 
 cpa = pytest.importorskip("context_long_sequence_zigzag_gb300")
 
@@ -39,3 +39,19 @@ def test_workspace_is_sized_for_the_caches_device(monkeypatch, name):
     monkeypatch.setattr(cpa._lib, name, lambda *_: asked.append(current[-1]) or OK)
     getattr(cpa, name)(SimpleNamespace(ptr=None, device=torch.device("cuda", 1)), 2)
     assert asked == ["cuda:1"]
+
+
+def test_clusters_only_where_they_fit_the_gpu_at_once():
+    """Few short runs take clusters of four to eight CTAs, and no workspace, as long as all CTAs are resident: two an
+    SM, but one of fp32 heads of 192 with more than 16 rows (152 SMs)."""
+    n = ctypes.c_size_t(0)
+
+    def size(dtype, seqs, d_qk, n_q):
+        c = _cache(num_seqs=seqs, hq=32, hkv=8, d_qk=d_qk, dtype=dtype)
+        assert cpa._lib.cp_kv_workspace_size(ctypes.byref(c), n_q, ctypes.byref(n)) == OK
+        return n.value
+
+    f32, bf16 = cpa.CP_DT_F32, cpa.CP_DT_BF16
+    assert size(f32, 5, 192, 8) > 0 and size(f32, 4, 192, 8) == 0  # 32 rows: 160 and 128 CTAs
+    for other in ((f32, 192, 4), (f32, 128, 8), (bf16, 192, 8), (bf16, 192, 16)):
+        assert size(other[0], 9, *other[1:]) == 0 and size(other[0], 10, *other[1:]) > 0  # 288 and 320 CTAs
