@@ -65,9 +65,9 @@ cp_status_t check_cache(const cp_kv_t* c) {
   if (c->num_seqs > CP_KV4_MAX_SEQS || c->hq > 1024) return CP_ERR_UNSUPPORTED;
   if (int64_t(c->max_pages) * c->page_size > (1 << 30)) return CP_ERR_UNSUPPORTED;
   if (int64_t(c->num_pages) * c->hkv * c->page_size > INT32_MAX) return CP_ERR_UNSUPPORTED;
-  if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16) || !aligned(c->page_table, 4)) {
-    // an empty cache needs none of them
-    if (c->num_seqs > 0 && c->max_pages > 0) return CP_ERR_INVALID_ARG;
+  if (c->num_seqs > 0 && c->max_pages > 0) {  // (an empty cache needs none of them)
+    if (!aligned(c->page_table, 4)) return CP_ERR_INVALID_ARG;
+    if (c->num_pages > 0 && (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16))) return CP_ERR_INVALID_ARG;
   }
   return CP_OK;
 }

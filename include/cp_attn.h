@@ -557,9 +557,9 @@ typedef struct {
   int32_t page_size;         /* tokens of a page: 16, 32, 64 or 128              */
   int32_t num_pages;         /* pages of the pool                                */
   int32_t max_pages;         /* columns of page_table                            */
-  void* k_pages;             /* device, 16-byte aligned                          */
-  void* v_pages;             /* device, 16-byte aligned                          */
-  const int32_t* page_table; /* device [B][max_pages]                            */
+  void* k_pages;             /* device, 16-byte aligned; not read without pages  */
+  void* v_pages;             /* device, 16-byte aligned; the same                */
+  const int32_t* page_table; /* device [B][max_pages]; not read without columns  */
 } cp_kv_t;
 
 /* Check a cache descriptor on the host (no GPU work). */

@@ -1,6 +1,7 @@
 """Calls of the paged cache and its pages at sizes and forms where their kernels go other ways: against the float64
 oracle, with the tolerances derived in test_gpu_kv.py unless a test says otherwise."""
 
+import ctypes
 import math
 
 import numpy as np
@@ -69,6 +70,33 @@ def test_attn_where_clusters_do_not_fit():
     h = Held([70, 0, 200, 31, 129], 32, 8, 192, 128, F32, 64, 8, seed=32)
     assert cpa.cp_kv_workspace_size(h.cache, 8) > 0
     h.check(*h.run())
+
+
+def test_a_cache_without_columns_or_pages():
+    """A table of no columns: every sequence is empty, and neither pages nor a table have to be there.  A pool of no
+    pages: every slot is absent."""
+    c = cpa.cp_kv_t(num_seqs=2, hq=4, hkv=2, d_qk=64, d_v=64, gqa=0, dtype=cpa.CP_DT_F32, scale=0.1, page_size=64,
+                    num_pages=4, max_pages=0, k_pages=None, v_pages=None, page_table=None)
+    q, lengths = torch.ones(2, 1, 4, 64, device="cuda"), ints([0, 0])
+    o, lse = torch.ones(2, 1, 4, 64, device="cuda"), torch.ones(4, 2, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    assert cpa._lib.cp_kv_attn(ctypes.byref(c), 1, q.data_ptr(), lengths.data_ptr(), o.data_ptr(), 0, lse.data_ptr(),
+                               None, 0, stream) == cpa.CP_OK
+    assert (o == 0).all() and (lse == -math.inf).all()
+    cache = cpa.KvCache(torch.ones(4, 2, 64, 64, device="cuda"), torch.ones(4, 2, 64, 64, device="cuda"),
+                        torch.empty(2, 0, dtype=torch.int32, device="cuda"), 4)
+    o, lse = cpa.cp_kv_attn(cache, q, ints([0, 3]))  # (a length that the table does not hold)
+    assert cpa.cp_device_status() == 0x302 and (o == 0).all() and (lse == -math.inf).all()
+    for columns in (2, WIDE // 64 + 1):
+        none = torch.empty(0, 2, 64, 64, device="cuda")
+        cache = cpa.KvCache(none, none, torch.zeros(2, columns, dtype=torch.int32, device="cuda"), 4)
+        o, lse = cpa.cp_kv_attn(cache, q, ints([0, 0]))
+        assert cpa.cp_device_status() == 0 and (o == 0).all() and (lse == -math.inf).all()
+        k = torch.ones(2, 2, 64, device="cuda")
+        cpa.cp_kv_append(cache, k, k, ints([0, 1, 2]), ints([0, 70]))
+        assert cpa.cp_device_status() == 0x301
+        o, lse = cpa.cp_kv_attn(cache, q, ints([1, 71]))
+        assert cpa.cp_device_status() == 0x301 and (o == 0).all() and (lse == -math.inf).all()
 
 
 # ---------------------------------------------------------------- pages taken back
