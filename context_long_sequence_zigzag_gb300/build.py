@@ -13,6 +13,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import os
 import platform
+import re
 import shutil
 import subprocess
 import sys
@@ -43,7 +44,10 @@ SOURCES = [
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
-         "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]
+         "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills,-v"]
+# Registers a thread that kernels have to come out with: their warps hand them to one another, and the launcher refuses
+# any other count (kLaunchRegs in kv_attn.cu).
+REGISTERS = {"kv_attn_kernel": 128}
 
 
 def _nvcc() -> str:
@@ -64,6 +68,19 @@ def _stale(obj: str, deps) -> bool:
         return True
     t = os.path.getmtime(obj)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def check_registers(log: str) -> None:
+    """Raises if the assembler's report names a kernel of REGISTERS with another count."""
+    kernel = ""
+    for line in log.splitlines():
+        m = re.search(r"Compiling entry function '(\w+)'", line)
+        if m:
+            kernel = m.group(1)
+        m = re.search(r"Used (\d+) registers", line)
+        for name, want in REGISTERS.items():
+            if m and name in kernel and int(m.group(1)) != want:
+                raise RuntimeError(f"{kernel}: {m.group(1)} registers, {want} are needed")
 
 
 def build(verbose: bool = False, extra_flags=None) -> str:
@@ -91,6 +108,11 @@ def build(verbose: bool = False, extra_flags=None) -> str:
                     sys.stderr.write(r.stdout + r.stderr)
                 if r.returncode != 0:
                     raise RuntimeError("nvcc failed: " + " ".join(cmd))
+                try:
+                    check_registers(r.stderr)
+                except RuntimeError:
+                    os.remove(cmd[-1])  # (or the next build would link it)
+                    raise
     if jobs or _stale(LIB, objs):
         cmd = [nvcc, *ARCH, "-shared", "-o", LIB, *objs, "-Xcompiler", "-fPIC", "-ldl"]
         r = subprocess.run(cmd, capture_output=True, text=True)

@@ -55,3 +55,18 @@ def test_clusters_only_where_they_fit_the_gpu_at_once():
     assert size(f32, 5, 192, 8) > 0 and size(f32, 4, 192, 8) == 0  # 32 rows: 160 and 128 CTAs
     for other in ((f32, 192, 4), (f32, 128, 8), (bf16, 192, 8), (bf16, 192, 16)):
         assert size(other[0], 9, *other[1:]) == 0 and size(other[0], 10, *other[1:]) > 0  # 288 and 320 CTAs
+
+
+def test_build_checks_the_registers_of_kernels_that_hand_them_over():
+    """The attention's launcher refuses a kernel of other than 128 registers a thread: a build with one fails."""
+    build = pytest.importorskip("context_long_sequence_zigzag_gb300.build")
+    log = """ptxas info    : Compiling entry function '_ZN6cpattn14kv_join_kernelILi8EEEvi' for 'sm_103a'
+ptxas info    : Used 48 registers, used 1 barriers
+ptxas info    : Compiling entry function '_ZN6cpattn14kv_attn_kernelILi1EEEvi' for 'sm_103a'
+ptxas info    : Function properties for _ZN6cpattn14kv_attn_kernelILi1EEEvi
+    8 bytes stack frame, 8 bytes spill stores, 8 bytes spill loads
+ptxas info    : Used %d registers, used 1 barriers
+"""
+    build.check_registers(log % 128)
+    with pytest.raises(RuntimeError, match="120 registers"):
+        build.check_registers(log % 120)
