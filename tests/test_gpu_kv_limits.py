@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import oracle
-from test_gpu_kv import BF, F32, WIDE, Held, f64, ints
+from test_gpu_kv import BF, F32, WIDE, Held, check_rope, f64, ints, pool_of, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -97,6 +97,59 @@ def test_a_cache_without_columns_or_pages():
         assert cpa.cp_device_status() == 0x301
         o, lse = cpa.cp_kv_attn(cache, q, ints([1, 71]))
         assert cpa.cp_device_status() == 0x301 and (o == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("hq,n_q,gqa", [(8, 1, "blocked"), (24, 9, "interleaved"), (128, 3, "blocked")])
+def test_attn_in_clusters_of_four(hq, n_q, gqa, dtype):
+    """Six sequences of eight kv heads in a short table: 48 runs (96 of fp32 with 48 rows, in even shares)."""
+    h = Held([1, 64, 290, 0, 131, 33], hq, 8, 64, 64, dtype, 32, n_q, gqa, seed=33)
+    assert (cpa.cp_kv_workspace_size(h.cache, n_q) == 0) == (dtype == BF or hq * n_q <= 8 * 32)
+    h.check(*h.run())
+
+
+# ---------------------------------------------------------------- tiles of several tokens
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,hq,hkv,d,first,pairs,adjacent", [
+    (20011, 2, 1, 64, 0, 32, False), (20011, 1, 2, 64, 16, 16, True), (20011, 3, 1, 32, 3, 11, False),
+    (50003, 1, 0, 16, 0, 1, True), (39001, 5, 3, 128, 64, 32, False)])
+def test_rope_of_many_tokens(T, hq, hkv, d, first, pairs, adjacent, dtype):
+    """Tiles of 8 to 20 tokens, the last one with fewer; with and without channels that only move."""
+    rng = np.random.RandomState(T)
+    q, k = randn(rng, (T, hq, d), dtype), randn(rng, (T, hkv, d), dtype)
+    f = 10000.0 ** (-np.arange(pairs) / pairs)
+    pos = rng.randint(0, 1 << 17, (T, 2))
+    axis = rng.randint(0, 2, pairs)
+    axis[0] = 1
+    rope = cpa.Rope(f, axis=axis, first=first, pairing="adjacent" if adjacent else "halves")
+    angle = pos[:, axis] * f[None]
+    for inverse in (False, True):
+        out = cpa.cp_rope(rope, ints(pos.tolist()), q, k if hkv else None, inverse=inverse)
+        for got, x in zip(out if hkv else (out,), (q, k)):
+            check_rope(got, x, angle, first, adjacent, 1.0, inverse)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("pairs,first,adjacent", [(32, 0, False), (16, 32, True), (21, 3, False)])
+def test_append_of_many_tokens(pairs, first, adjacent, dtype):
+    """Tiles of 16 tokens, the last one with fewer and in part behind the last sequence."""
+    rng = np.random.RandomState(34)
+    start, counts, hkv, d, page = [7, 0, 100], [39000, 0, 1010], 2, 64, 16
+    n, after = sum(counts), [a + m for a, m in zip(start, counts)]
+    pages, table = pool_of(after, page, rng)
+    k, v = randn(rng, (n + 9, hkv, d), dtype), randn(rng, (n + 9, hkv, d), dtype)
+    kp, vp = (torch.full((pages, hkv, page, d), 7.0, dtype=dtype, device="cuda") for _ in range(2))
+    f = 1000.0 ** (-np.arange(pairs) / pairs)
+    rope = cpa.Rope(f, first=first, pairing="adjacent" if adjacent else "halves")
+    cpa.cp_kv_append(cpa.KvCache(kp, vp, ints(table.tolist()), hkv), k, v, ints([0, 39000, 39000, n]), ints(start), rope=rope)
+    slot = np.concatenate([np.arange(a, b) for a, b in zip(start, after)])
+    at = table[np.repeat(np.arange(3), counts), slot // page], slot % page
+    got_k, got_v = f64(kp).transpose(0, 2, 1, 3), f64(vp).transpose(0, 2, 1, 3)
+    assert np.array_equal(got_v[at], f64(v)[:n])
+    check_rope(torch.from_numpy(got_k[at]).to(dtype), k[:n], slot[:, None] * f[None], first, adjacent, 1.0, False)
+    mark = np.ones((pages, page), bool)
+    mark[at] = False
+    assert np.all(got_k[mark] == 7) and np.all(got_v[mark] == 7)
 
 
 # ---------------------------------------------------------------- pages taken back
