@@ -3,9 +3,11 @@
 // the cache with the running maximum and sum of the softmax.
 //
 // What bounds it: the cache's bytes, read once (d_qk + d_v elements a slot and
-// head, for 2 (d_qk + d_v) G n_q FLOPs).  With the 1 to 64 rows that share
-// a head a 128-row tcgen05 tile would be mostly empty and its accumulator a
-// detour through TMEM; warp-level MMAs of 16 rows keep up with the copies.
+// head, for 2 (d_qk + d_v) G n_q FLOPs).  With the 1 to 16 rows that share a
+// head in decoding a tcgen05 tile (64 or 128 rows) would be mostly empty and its
+// accumulator a detour through TMEM; warp-level MMAs of 16 rows keep up with the
+// copies, with up to 32 rows (8 x 8K, 32/8 heads: 47 to 54 us).  64 rows, which
+// they bound (64 us), would fill such a tile; there is no such variant.
 //
 // Work.  A run is one sequence's slots for one kv head and up to 16, 32 or 64
 // of its rows (query heads of the group times new tokens); its tiles are TT
@@ -45,13 +47,15 @@ constexpr int kLaunchRegs = 128, kComputeRegs = 200, kProducerRegs = 56;
 static_assert(kComputeRegs + kProducerRegs == 2 * kLaunchRegs, "what one half takes the other gives");
 constexpr int kMostStages = 6;
 // Sequences whose lengths the producer warp adds up alone, a lane each, without the other warps' barrier: the first copy
-// leaves 0.6 us earlier (1 x 16K 18.8 us, by all warps 19.4).
+// leaves 0.6 us earlier (1 x 16K 19.0 us, by all warps 19.6).
 constexpr int kFewSeqs = 32;
 // A cluster of up to eight CTAs a run, in the place of even shares and a second kernel, where the table holds no more
-// tokens than this and the clusters fit the GPU at once.  32/8 heads, one sequence of 512 tokens: 7.9 us on the device
-// (even shares: 9.1), of 4K: 11.8 us (10.3), but 15 us of a host that calls again and again (20); 8 of 4K: 26.1 us (28.5);
-// one of 8K: 16.4 us (11.8), 8 ragged ones up to 4K: 16.0 us (12.7).  Clusters of sixteen start 1 us later.  Where they
-// do not fit (fp32, 32 rows of 32/8 heads of 192: one CTA an SM), 5 of 512 tokens: 36.8 us (23.7), 5 of 4K: 150 us (83).
+// tokens than this and the clusters fit the GPU at once.  32/8 heads, one sequence of 512 tokens: 8.1 us on the device
+// (even shares: 9.4); 8 of 4K: 26.3 us (28.9); 8 ragged ones up to 4K: 20.4 us (21.4) or, of other lengths, 16.0 (12.7);
+// one of 4K: 12.5 us (10.7), but 15 us of a host that calls again and again (20), which decides here; one of 8K: 18.4 us
+// (13.0).  So a replayed graph pays 2 to 3 us for it near the bound; a table of more columns takes even shares.  Clusters
+// of sixteen start 1 us later.  Where they do not fit (fp32, 32 rows of 32/8 heads of 192: one CTA an SM), 5 of 512
+// tokens: 36.8 us (23.7), 5 of 4K: 150 us (83).
 constexpr int64_t kClusterTokens = 4096;
 constexpr float kLog2e = 1.4426950408889634f;
 // log2 units: a row's reference maximum follows a new one past this (p stays below 2^8 relative to it, so that most
@@ -603,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attn_kernel(const __grid_const
       for (int i = 0; i < NB; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s[i][j] = ptx::ex2((s[i][j] - ref[j >> 1]) * cs);  // (the largest: exactly 1, however large)
+          s[i][j] = ptx::ex2((s[i][j] - ref[j >> 1]) * cs);  // (that of the reference: exactly 1, however large the score)
           l[j >> 1] += s[i][j];
         }
 
@@ -1007,7 +1011,7 @@ struct Layout {
   size_t parts, total;
 };
 // Rows of a run: 16, 32 or 64 (fp32: 32, their queries take twice the room); more take several passes over the cache.
-// 8 x 8K, 32/8 heads: 64 rows in one pass 63 us, two of 32 91 us, four of 16 167 us; 20 rows in one of 32 52 us, two of 16 87.
+// 8 x 8K, 32/8 heads: 64 rows in one pass 64 us, two of 32 94 us, four of 16 167 us; 20 rows in one of 32 52 us, two of 16 87.
 // Few runs of few tiles: a cluster a run, joined in shared memory, one launch and no workspace.
 Layout layout_of(int num_seqs, int hq, int hkv, int dqk, int dv, int dtype, int n_q, int64_t most) {
   Layout x;
@@ -1064,7 +1068,7 @@ cudaError_t launch(const KvAttnArgs& a, const Layout& x, cudaStream_t st) {
   }
   const int ctas = Room<C>::two ? x.ctas : x.ctas / 2;
   const int64_t runs = int64_t(a.c.num_seqs) * a.c.hkv * x.row_tiles;
-  // (an entry a run: a CTA of the second kernel for every CTA of the first takes 1 x 16K from 18.8 to 22.7 us)
+  // (an entry a run: a CTA of the second kernel for every CTA of the first takes 1 x 16K from 19.0 to 23.0 us)
   p.by_run = runs <= x.ctas;
   p.join_ctas = ctas;
   cudaLaunchAttribute attr{};

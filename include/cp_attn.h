@@ -601,7 +601,9 @@ cp_status_t cp_kv_append(const cp_kv_t* cache, const void* k, const void* v, int
  * up to 32 rows (hq / hkv * n_q) share a kv head, rounded to BF16 (2^-8) where
  * more do.  FP32 caches: every operand as two TF32 terms (the product of both
  * lower ones, 2^-22, left out; an infinity that a query sees, or a number within
- * 2^-12 of the largest, may give NaN in an infinity's place). */
+ * 2^-12 of the largest, may give NaN in an infinity's place).  V is summed
+ * before it is divided by the probabilities' sum, of which the largest counts 1
+ * to 2^8: sums past FP32's range are infinite. */
 cp_status_t cp_kv_attn(const cp_kv_t* cache, int32_t n_q, const void* q, const int32_t* lengths, void* o,
                        int32_t o_f32, float* lse, void* workspace, size_t workspace_bytes, cp_stream_t stream);
 
